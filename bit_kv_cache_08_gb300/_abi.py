@@ -25,6 +25,7 @@ DEVERR_BLOCK_ID, DEVERR_POSITION, DEVERR_NONFINITE, DEVERR_WAIT_TIMEOUT = 0x1, 0
 BF16, FP32 = 0, 1
 KIND_K, KIND_V = 0, 1
 FLAG_NO_ROTATION, FLAG_NO_TOKEN_PASS, FLAG_NO_CHANNEL_PASS = 0x1, 0x2, 0x4
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 FLAG_TEST_WAIT_TIMEOUT = 0x100   # test only: the decode kernel's first copy waits give up at once
 
 
@@ -40,6 +41,11 @@ class Config(ctypes.Structure):
                 ("varn_iters", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
                 ("n_kv_heads", ctypes.c_int32), ("sm_scale", ctypes.c_float),
                 ("sign_bits", ctypes.c_uint32 * 4), ("flags", ctypes.c_uint32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("turns", ctypes.c_uint64 * 64)]
 
 
 def make_config(n_q_heads: int, n_kv_heads: int, block_size: int, varn_iters: int,
@@ -69,6 +75,12 @@ _SIGS = {
     "kvarn_prefill_workspace_bytes": (_sz, [_cfgp, _i32, _i32, _i32]),
     "kvarn_quantize_block": (ctypes.c_int, [_cfgp, _i32, _vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
     "kvarn_append": (ctypes.c_int, [_cfgp, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "kvarn_rope_init": (ctypes.c_int, [ctypes.POINTER(Rope), _i32, _i32, ctypes.POINTER(ctypes.c_double),
+                                       ctypes.c_float, ctypes.c_float]),
+    "kvarn_append_rope": (ctypes.c_int, [_cfgp, ctypes.POINTER(Rope), _vp, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _i64,
+                                         _i32, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "kvarn_append_rope_bf16": (ctypes.c_int, [_cfgp, ctypes.POINTER(Rope), _vp, _i64, _vp, _i32, _vp, _vp, _vp, _i64,
+                                              _i32, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i32, _vp, _vp]),
     "kvarn_decode_attn": (ctypes.c_int, [_cfgp, _vp, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _i32, _vp, _vp,
                                          _sz, _vp]),
     "kvarn_prefill_attn": (ctypes.c_int, [_cfgp, _vp, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _i32, _i32, _vp,
@@ -245,6 +257,144 @@ def append(cfg: Config, pool: torch.Tensor, staging: torch.Tensor, block_table: 
     _check(lib().kvarn_append(ctypes.byref(cfg), _ptr(pool), pool.shape[0], _ptr(staging), _ptr(block_table),
                               block_table.shape[1], _ptr(pos), _ptr(k_new), _ptr(v_new), batch,
                               _ptr(workspace), _stream()), "kvarn_append")
+
+
+def make_rope(inv_freq: Sequence[float], layout: int = ROPE_HALF, scale: float = 1.0, eps: float = 1e-6) -> Rope:
+    """Rotary positions over the first 2 * len(inv_freq) channels of a head
+    (radians per position, float64; rope_frequencies gives the usual ones),
+    and the epsilon of the head norms."""
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if f.ndim != 1 or f.size > 64:
+        raise ValueError("inv_freq must be a vector of at most 64 rates")
+    r = Rope()
+    _check(lib().kvarn_rope_init(ctypes.byref(r), 2 * f.size, layout, f.ctypes.data_as(ctypes.POINTER(ctypes.c_double)),
+                                 scale, eps), "kvarn_rope_init")
+    return r
+
+
+def rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_ctx: int = 0, low: float = 1.0, high: float = 32.0):
+    """(inv_freq [rotary_dim / 2] float64, scale of cos and sin) for rates
+    theta^(-2i / rotary_dim), stretched for contexts `factor` times as long:
+
+    "none"    as they are
+    "linear"  every rate divided by factor (positions interpolated)
+    "ntk"     theta raised so that the slowest rate is divided by factor and the fastest is kept
+    "bands"   per pair, by its turns within original_ctx: divided by factor below `low` turns, kept above
+              `high`, a blend linear in the number of turns between
+    "yarn"    the same with cos and sin times 0.1 ln(factor) + 1 (Peng et al. 2023, "YaRN")
+    """
+    if rotary_dim < 2 or rotary_dim % 2 or not theta > 0 or not factor >= 1.0:
+        raise ValueError("rotary_dim must be even and positive, theta positive, factor at least 1")
+    i = np.arange(0, rotary_dim, 2, dtype=np.float64) / rotary_dim
+    if scaling == "ntk":
+        if rotary_dim == 2:
+            raise ValueError("ntk scaling needs two pairs")
+        theta = theta * factor ** (rotary_dim / (rotary_dim - 2))
+    f = theta ** -i
+    if scaling in ("none", "ntk"):
+        return f, 1.0
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling not in ("yarn", "bands"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if original_ctx < 1 or not 0 < low < high:
+        raise ValueError("yarn and bands need original_ctx and 0 < low < high")
+    keep = np.clip((original_ctx * f / (2 * np.pi) - low) / (high - low), 0.0, 1.0)
+    return f * (keep + (1 - keep) / factor), 1.0 if scaling == "bands" else 0.1 * float(np.log(factor)) + 1.0
+
+
+def _need_vec(t, name: str, dtype, n: int):
+    _need_cuda(t, name, dtype)
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
+
+
+def _token_rows(t: torch.Tensor, name: str, heads: int, n_tokens: int) -> int:
+    """Checks a [n_tokens][heads][128] bf16 tensor whose token rows may lie apart; returns the token stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor")
+    if t.dim() != 3 or t.shape[0] != n_tokens or t.shape[1] != heads or t.shape[2] != 128:
+        raise ValueError(f"{name} must be [{n_tokens}][{heads}][128], got {list(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != 128):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s0 if n_tokens > 1 else heads * 128
+
+
+def _append_rope(cfg, rope, pool, staging, block_table, pos, q, k, v, q_out, workspace, cu_tokens, rope_pos, q_weight,
+                 k_weight):
+    _need_cuda(block_table, "block_table", torch.int32)
+    _need_cuda(pos, "pos", torch.int32)
+    _need_cuda(workspace, "workspace", torch.uint8)
+    batch, n = pos.numel(), k.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] < batch:
+        raise ValueError("block_table must be [batch][max_blocks]")
+    if cu_tokens is not None:
+        _need_vec(cu_tokens, "cu_tokens", torch.int32, batch + 1)
+    elif n != batch:
+        raise ValueError("without cu_tokens there is one token per sequence")
+    if rope_pos is not None:
+        _need_vec(rope_pos, "rope_pos", torch.int32, batch)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need_vec(w, name, torch.bfloat16, 128)
+    ks, vs, qs, out_code = _token_rows(k, "k", cfg.n_kv_heads, n), _token_rows(v, "v", cfg.n_kv_heads, n), 0, BF16
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        qs = _token_rows(q, "q", cfg.n_q_heads, n)
+        _need_cuda(q_out, "q_out")
+        out_code = _dtype_code(q_out)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+    if workspace.numel() < 256:
+        raise ValueError("workspace must hold 256 bytes")
+    head = (ctypes.byref(cfg), ctypes.byref(rope), pool.data_ptr(), pool.shape[0])
+    mid = () if staging is None else (staging.data_ptr(),)
+    tail = (block_table.data_ptr(), block_table.shape[1], pos.data_ptr(),
+            None if rope_pos is None else rope_pos.data_ptr(), None if cu_tokens is None else cu_tokens.data_ptr(),
+            n, batch, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+            None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+            None if q_out is None else q_out.data_ptr(), out_code, workspace.data_ptr(), _stream())
+    if staging is None:
+        _check(lib().kvarn_append_rope_bf16(*head, *tail), "kvarn_append_rope_bf16")
+    else:
+        _check(lib().kvarn_append_rope(*head, *mid, *tail), "kvarn_append_rope")
+
+
+def append_rope(cfg: Config, rope: Rope, pool: torch.Tensor, staging: torch.Tensor, block_table: torch.Tensor,
+                pos: torch.Tensor, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                q_out: Optional[torch.Tensor], workspace: torch.Tensor, *, cu_tokens: Optional[torch.Tensor] = None,
+                rope_pos: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                k_weight: Optional[torch.Tensor] = None):
+    """One step's keys and values into the packed cache, normed and rotated on
+    the way, and its queries into q_out. q [tokens][n_q][128], k and v
+    [tokens][n_kv][128]: bf16, token rows at any stride that is a multiple of
+    8 (columns of one projection's output). cu_tokens int32 [batch + 1]: ragged
+    runs of tokens; None: one token per sequence. rope_pos int32 [batch]: the
+    position of each sequence's first new token (default: pos)."""
+    _need_cuda(pool, "pool", torch.uint8)
+    _need_cuda(staging, "staging", torch.bfloat16)
+    if pool.dim() != 2 or pool.shape[1] != block_bytes(cfg):
+        raise ValueError("pool must be [n_blocks][block_bytes]")
+    if staging.numel() < pos.numel() * cfg.n_kv_heads * 2 * cfg.block_size * 128:
+        raise ValueError("staging holds fewer sequences than pos")
+    _append_rope(cfg, rope, pool, staging, block_table, pos, q, k, v, q_out, workspace, cu_tokens, rope_pos, q_weight,
+                 k_weight)
+
+
+def append_rope_bf16(cfg: Config, rope: Rope, kv_pool: torch.Tensor, block_table: torch.Tensor, pos: torch.Tensor,
+                     q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, q_out: Optional[torch.Tensor],
+                     workspace: torch.Tensor, *, cu_tokens: Optional[torch.Tensor] = None,
+                     rope_pos: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None):
+    """append_rope into the bf16 pages [n_blocks][n_kv][2][B][128] of decode_attn_bf16."""
+    _need_cuda(kv_pool, "kv_pool", torch.bfloat16)
+    if tuple(kv_pool.shape[1:]) != (cfg.n_kv_heads, 2, cfg.block_size, 128):
+        raise ValueError("kv_pool must be [n_blocks][n_kv][2][B][128]")
+    _append_rope(cfg, rope, kv_pool, None, block_table, pos, q, k, v, q_out, workspace, cu_tokens, rope_pos, q_weight,
+                 k_weight)
 
 
 def decode_attn(cfg: Config, q: torch.Tensor, pool: torch.Tensor, staging: torch.Tensor,

@@ -217,6 +217,84 @@ int kvarn_append(const kvarn_config* cfg, void* pool, int64_t n_pool_blocks, voi
                  void* stream);
 
 /*
+ * Rotary positions for kvarn_append_rope and kvarn_append_rope_bf16 (library
+ * conveniences, like the head norms: the method's pages start from keys that
+ * a model has rotated already). Filled by kvarn_rope_init; plain host data.
+ *   KVARN_ROPE_HALF         channels i and i + rotary_dim / 2 are pair i
+ *   KVARN_ROPE_INTERLEAVED  channels 2i and 2i + 1 are pair i
+ */
+typedef enum { KVARN_ROPE_HALF = 0, KVARN_ROPE_INTERLEAVED = 1 } kvarn_rope_layout;
+
+typedef struct kvarn_rope {
+    int32_t rotary_dim;   /* channels rotated, from channel 0: a multiple of 16, 0..128; the others pass */
+    int32_t layout;       /* kvarn_rope_layout */
+    float scale;          /* multiplies cos and sin (attention factor of some long-context scalings), else 1 */
+    float eps;            /* epsilon of the head norms */
+    uint64_t turns[64];   /* pair i's turns per position, fraction of one, in units of 2^-64 */
+} kvarn_rope;
+
+/* Fills *rope (host) from the angular rates inv_freq[rotary_dim / 2] (host,
+ * radians per position, |rate| <= 2^20; however scaled for long contexts).
+ * KVARN_ERR_UNSUPPORTED for a rotary_dim that is no multiple of 16. */
+int kvarn_rope_init(kvarn_rope* rope, int32_t rotary_dim, int32_t layout, const double* inv_freq, float scale,
+                    float eps);
+
+/*
+ * kvarn_append_rope -- keys and values of one step appended to the packed
+ * cache with head norms and rotary positions on the way, and the step's
+ * queries normed and rotated in the same launch: one token per sequence
+ * (decode) or a ragged run of tokens per sequence (prompts).
+ *
+ * Token rows: q [n_tokens][n_q][128], k and v [n_tokens][n_kv][128], device
+ * bf16, rows of one token contiguous, q_stride / k_stride / v_stride elements
+ * (multiples of 8) from one token to the next, so columns of one projection's
+ * output serve as they are. With cu_tokens (device int32 [batch + 1],
+ * ascending from 0 or more) rows cu_tokens[b] .. cu_tokens[b+1] - 1 are
+ * sequence b's; a sequence may have none, and rows outside every sequence are
+ * left alone, with their q_out. Without it (NULL) n_tokens is batch and row b
+ * is sequence b's one token.
+ *
+ * Row i of sequence b is its token pos[b] + i (pos: device int32 [batch],
+ * tokens cached before), turned by the angles of position
+ * (rope_pos ? rope_pos[b] : pos[b]) + i (rope_pos: device int32 [batch], for a
+ * cache that does not start at position 0, such as the own tokens behind a
+ * shared prefix):
+ *   q_out = rope(norm(q)), key = rope(norm(k)), value = v,
+ *   norm(x) = x w / sqrt(mean(x^2) + eps) with q_weight / k_weight (device
+ *   bf16 [128]; NULL: no norm).
+ * q_out: [n_tokens][n_q][128], q_out_dtype KVARN_BF16 or KVARN_FP32; it may
+ * be q itself where q's rows are laid out like it. q and q_out may both be
+ * NULL. The key is rounded to bf16.
+ *
+ * Tokens of complete blocks are quantised as kvarn_quantize_block does, from
+ * the staging rows of earlier tokens and the new rows, and written to the
+ * pool; tokens of the incomplete block go to their staging rows (other staging
+ * rows are left as they are): the pool then holds the bytes that kvarn_append
+ * would have written token by token. Device faults: KVARN_DEVERR_POSITION
+ * (pos < 0, a token beyond the block table, cu_tokens not ascending or beyond
+ * n_tokens), KVARN_DEVERR_BLOCK_ID, KVARN_DEVERR_NONFINITE.
+ */
+int kvarn_append_rope(const kvarn_config* cfg, const kvarn_rope* rope, void* pool, int64_t n_pool_blocks,
+                      void* staging, const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* pos,
+                      const int32_t* rope_pos, const int32_t* cu_tokens, int64_t n_tokens, int32_t batch,
+                      const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, const void* q_weight, const void* k_weight, void* q_out,
+                      int32_t q_out_dtype, void* workspace, void* stream);
+
+/*
+ * kvarn_append_rope_bf16 -- the same into the plain bf16 pages of
+ * kvarn_decode_attn_bf16 (kv_pool: bf16 [n_pool_blocks][n_kv][2][B][128]):
+ * every token goes to its row of its page. workspace: >= 256 bytes, for the
+ * error word.
+ */
+int kvarn_append_rope_bf16(const kvarn_config* cfg, const kvarn_rope* rope, void* kv_pool, int64_t n_pool_blocks,
+                           const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* pos,
+                           const int32_t* rope_pos, const int32_t* cu_tokens, int64_t n_tokens, int32_t batch,
+                           const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, const void* q_weight, const void* k_weight, void* q_out,
+                           int32_t q_out_dtype, void* workspace, void* stream);
+
+/*
  * kvarn_decode_attn -- decode attention over the packed cache. Passage:
  * section 三 3.1 of the method page (the query is multiplied by the same
  * Hadamard matrix, so q.k is unchanged).
