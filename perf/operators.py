@@ -230,8 +230,7 @@ def _own(s):
             s["rope"] = kv.make_rope(s["inv_freq"], layout=layout, eps=1e-6)
             s["workspace"] = kv.alloc_workspace(s["cfg"], 0, 0)
         else:
-            s["workspace"] = kv.alloc_prefix_workspace(s["cfg"], c["batch"], s["prefix_table"].shape[0],
-                                                       s["block_table"].shape[1])
+            s["workspace"] = kv.alloc_prefix_workspace(s["cfg"], c["batch"], s["prefix_table"].shape[0])
         if c["op"] == "append" and c["cache"] == "packed":
             s["pool"] = kv.alloc_pool(s["cfg"], s["n_pool"])
     if c["op"] == "append":
