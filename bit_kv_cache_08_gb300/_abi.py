@@ -90,6 +90,11 @@ _SIGS = {
                                               _sz, _vp]),
     "kvarn_decode_attn_noalloc": (ctypes.c_int, [_cfgp, _vp, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _i32, _vp,
                                                  _vp, _vp]),
+    "kvarn_prefix_workspace_bytes": (_sz, [_cfgp, _i32, _i32]),
+    "kvarn_prefix_attn": (ctypes.c_int, [_cfgp, _vp, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp,
+                                         _i32, _vp, _sz, _vp]),
+    "kvarn_prefix_attn_bf16": (ctypes.c_int, [_cfgp, _vp, _i32, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp,
+                                              _i32, _vp, _sz, _vp]),
     "kvarn_error_decomposition": (ctypes.c_int, [_cfgp, _i32, _vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
     "kvarn_read_error": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]),
     "kvarn_clear_error": (ctypes.c_int, [_vp, _vp]),
@@ -176,6 +181,17 @@ def alloc_prefill_workspace(cfg: Config, batch: int, chunk: int, max_blocks_per_
     n = prefill_workspace_bytes(cfg, batch, chunk, max_blocks_per_seq)
     if n == 0:
         raise ValueError("kvarn_prefill_workspace_bytes: invalid config or sizes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def prefix_workspace_bytes(cfg: Config, batch: int, prefix_blocks: int) -> int:
+    return int(lib().kvarn_prefix_workspace_bytes(ctypes.byref(cfg), batch, prefix_blocks))
+
+
+def alloc_prefix_workspace(cfg: Config, batch: int, prefix_blocks: int, device="cuda") -> torch.Tensor:
+    n = prefix_workspace_bytes(cfg, batch, prefix_blocks)
+    if n == 0:
+        raise KVarNError(ERR_CUDA, "kvarn_prefix_workspace_bytes")
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
@@ -446,6 +462,53 @@ def decode_attn_bf16(cfg: Config, q: torch.Tensor, kv_pool: torch.Tensor, block_
                                         kv_pool.shape[0], _ptr(block_table), block_table.shape[1],
                                         _ptr(seq_lens), q.shape[0], _ptr(out), _ptr(workspace),
                                         workspace.numel(), _stream()), "kvarn_decode_attn_bf16")
+
+
+def _prefix_args(cfg, q, prefix_table, prefix_lens, block_table, seq_lens, out, workspace):
+    _need_cuda(q, "q")
+    _need_cuda(out, "out")
+    _need_cuda(prefix_table, "prefix_table", torch.int32)
+    _need_cuda(prefix_lens, "prefix_lens", torch.int32)
+    _need_cuda(block_table, "block_table", torch.int32)
+    _need_cuda(seq_lens, "seq_lens", torch.int32)
+    _need_cuda(workspace, "workspace", torch.uint8)
+    batch = q.shape[0]
+    if q.dim() != 3 or q.shape[1] != cfg.n_q_heads or q.shape[2] != 128 or out.shape != q.shape:
+        raise ValueError("q and out must be [batch][n_q][128]")
+    if prefix_lens.numel() != batch or seq_lens.numel() != batch or block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError("prefix_lens, seq_lens and block_table must have a row for each sequence of q")
+    return ((prefix_table.data_ptr(), prefix_table.numel(), prefix_lens.data_ptr(), block_table.data_ptr(),
+             block_table.shape[1], seq_lens.data_ptr(), batch, out.data_ptr(), _dtype_code(out), workspace.data_ptr(),
+             workspace.numel(), _stream()))
+
+
+def prefix_attn(cfg: Config, q: torch.Tensor, pool: torch.Tensor, staging: torch.Tensor, prefix_table: torch.Tensor,
+                prefix_lens: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, out: torch.Tensor,
+                workspace: torch.Tensor):
+    """decode_attn for a batch that shares a prefix: sequence b sees the first
+    prefix_lens[b] tokens of the blocks prefix_table [prefix_blocks], then its
+    own seq_lens[b] tokens. q (bf16|fp32) and out (bf16|fp32): [batch][n_q][128]."""
+    _need_cuda(pool, "pool", torch.uint8)
+    _need_cuda(staging, "staging", torch.bfloat16)
+    rest = _prefix_args(cfg, q, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
+    if pool.dim() != 2 or pool.shape[1] != block_bytes(cfg):
+        raise ValueError("pool must be [n_blocks][block_bytes]")
+    if staging.numel() < q.shape[0] * cfg.n_kv_heads * 2 * cfg.block_size * 128:
+        raise ValueError("staging holds fewer sequences than q")
+    _check(lib().kvarn_prefix_attn(ctypes.byref(cfg), q.data_ptr(), _dtype_code(q), pool.data_ptr(), pool.shape[0],
+                                   staging.data_ptr(), *rest), "kvarn_prefix_attn")
+
+
+def prefix_attn_bf16(cfg: Config, q: torch.Tensor, kv_pool: torch.Tensor, prefix_table: torch.Tensor,
+                     prefix_lens: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, out: torch.Tensor,
+                     workspace: torch.Tensor):
+    """prefix_attn over the bf16 pages [n_blocks][n_kv][2][B][128] of decode_attn_bf16."""
+    _need_cuda(kv_pool, "kv_pool", torch.bfloat16)
+    rest = _prefix_args(cfg, q, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
+    if tuple(kv_pool.shape[1:]) != (cfg.n_kv_heads, 2, cfg.block_size, 128):
+        raise ValueError("kv_pool must be [n_blocks][n_kv][2][B][128]")
+    _check(lib().kvarn_prefix_attn_bf16(ctypes.byref(cfg), q.data_ptr(), _dtype_code(q), kv_pool.data_ptr(),
+                                        kv_pool.shape[0], *rest), "kvarn_prefix_attn_bf16")
 
 
 def decode_attn_noalloc(cfg: Config, q: torch.Tensor, pool: torch.Tensor, staging: torch.Tensor,

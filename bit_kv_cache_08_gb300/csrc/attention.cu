@@ -741,11 +741,15 @@ int attn_grid_warps(int block_size, int bits, int device) {
     return cache[bi][wi][device];
 }
 
-cudaError_t launch_decode_attn(const kvarn_config& cfg, const void* q, int q_dtype, const void* pool,
+// The arguments of a decode launch, and its split kernel alone (the caller
+// merges: launch_decode_attn, or the shared-prefix attention).
+cudaError_t launch_decode_split(const kvarn_config& cfg, const void* q, int q_dtype, const void* pool,
                                int64_t n_pool_blocks, int64_t block_bytes, const void* staging,
                                const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
-                               int batch, float* out, void* workspace, int nw, cudaStream_t st) {
-    AttnArgs a = {};
+                               int batch, float* out, void* workspace, int nw, AttnArgs* args,
+                                cudaStream_t st) {
+    AttnArgs& a = *args;
+    a = {};
     a.q = q;
     a.q_dtype = q_dtype;
     a.pool = (const uint8_t*)pool;
@@ -778,12 +782,21 @@ cudaError_t launch_decode_attn(const kvarn_config& cfg, const void* q, int q_dty
     for (int i = 0; i < 4; ++i) a.sb[i] = cfg.sign_bits[i];
     return with_attn_kernel(cfg.block_size, cfg.bits, [&](auto k) {
         using K = decltype(k);
-        cudaError_t e = launch_pdl(K::fn, nw, 32, K::smem(), st, a);
-        // up to one wave of wide CTAs (4 per SM), so that 8 warps share each
-        // row's raw tail rows
-        if (e == cudaSuccess) e = launch_merge<K::kB, true>(a, nw, 4, st);
-        return e;
+        return launch_pdl(K::fn, nw, 32, K::smem(), st, a);
     });
+}
+
+cudaError_t launch_decode_attn(const kvarn_config& cfg, const void* q, int q_dtype, const void* pool,
+                               int64_t n_pool_blocks, int64_t block_bytes, const void* staging,
+                               const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
+                               int batch, float* out, void* workspace, int nw, cudaStream_t st) {
+    AttnArgs a;
+    const cudaError_t e = launch_decode_split(cfg, q, q_dtype, pool, n_pool_blocks, block_bytes, staging, block_table,
+                                              max_blocks, seq_lens, batch, out, workspace, nw, &a, st);
+    if (e != cudaSuccess) return e;
+    // up to one wave of wide CTAs (4 per SM), so that 8 warps share each
+    // row's raw tail rows
+    return cfg.block_size == 32 ? launch_merge<32, true>(a, nw, 4, st) : launch_merge<64, true>(a, nw, 4, st);
 }
 
 }  // namespace kvarn

@@ -18,7 +18,6 @@
 
 namespace kvarn {
 
-constexpr int kChunk = 16;
 constexpr int kBfStages = 3;
 constexpr int kRowPitch = kD * 2 + 16;                 // 272 bytes
 constexpr int kStageBytes = 2 * kChunk * kRowPitch;    // K rows then V rows
@@ -271,11 +270,13 @@ int attn_bf16_grid_warps(int block_size, int device) {
     return cache[bi][device];
 }
 
-cudaError_t launch_decode_attn_bf16(const kvarn_config& cfg, const void* q, int q_dtype, const void* kv_pool,
+// The arguments of a launch, and its split kernel alone (the caller merges).
+cudaError_t launch_decode_split_bf16(const kvarn_config& cfg, const void* q, int q_dtype, const void* kv_pool,
                                     int64_t n_pool_blocks, const int32_t* block_table, int max_blocks,
                                     const int32_t* seq_lens, int batch, float* out, void* workspace, int nw,
-                                    cudaStream_t st) {
-    AttnArgs a = {};
+                                     AttnArgs* args, cudaStream_t st) {
+    AttnArgs& a = *args;
+    a = {};
     a.q = q;
     a.q_dtype = q_dtype;
     a.pool = (const uint8_t*)kv_pool;
@@ -298,14 +299,21 @@ cudaError_t launch_decode_attn_bf16(const kvarn_config& cfg, const void* q, int 
     a.sm_scale = cfg.sm_scale;
     a.flags = cfg.flags;
     for (int i = 0; i < 4; ++i) a.sb[i] = cfg.sign_bits[i];
-    cudaError_t e;
     if (cfg.block_size == 32)
-        e = launch_pdl(decode_attn_bf16_kernel<32>, nw, 32, attn_bf16_smem_bytes(), st, a);
-    else
-        e = launch_pdl(decode_attn_bf16_kernel<64>, nw, 32, attn_bf16_smem_bytes(), st, a);
+        return launch_pdl(decode_attn_bf16_kernel<32>, nw, 32, attn_bf16_smem_bytes(), st, a);
+    return launch_pdl(decode_attn_bf16_kernel<64>, nw, 32, attn_bf16_smem_bytes(), st, a);
+}
+
+cudaError_t launch_decode_attn_bf16(const kvarn_config& cfg, const void* q, int q_dtype, const void* kv_pool,
+                                    int64_t n_pool_blocks, const int32_t* block_table, int max_blocks,
+                                    const int32_t* seq_lens, int batch, float* out, void* workspace, int nw,
+                                    cudaStream_t st) {
+    AttnArgs a;
+    const cudaError_t e = launch_decode_split_bf16(cfg, q, q_dtype, kv_pool, n_pool_blocks, block_table, max_blocks,
+                                                   seq_lens, batch, out, workspace, nw, &a, st);
+    if (e != cudaSuccess) return e;
     // (no raw tail rows: the wide kernel only for many partials per unit)
-    if (e == cudaSuccess) e = launch_merge<kChunk, false>(a, nw, 0, st);
-    return e;
+    return launch_merge<kChunk, false>(a, nw, 0, st);
 }
 
 }  // namespace kvarn

@@ -7,6 +7,7 @@
 
 namespace kvarn {
 
+constexpr int kChunk = 16;   // tokens per split unit of the bf16 cache
 constexpr uint32_t kWaitLimit = 1u << 22;
 // Cost of one 2-bit block per token of block size, in units of merging one
 // partial; see split_active_warps. Chosen from batch-1 timings of the

@@ -1,0 +1,401 @@
+// prefix.cu -- decode attention for a batch whose sequences share a prefix:
+// out = softmax(sm_scale q.k) v over the first prefix_lens[b] tokens of the
+// shared prefix, then sequence b's own tokens.
+//
+// The prefix is read once for the whole batch: with R = batch * G query rows
+// per kv head, S = Q K^T and O = P V are matrix products of R rows, which a
+// decode that walks each sequence's own block table reads R times over. Three
+// launches: the prefix kernel (partials of token ranges), the split kernel of
+// the plain decode attention over the own tokens, and a merge of both kinds
+// of partial in the log-sum-exp sense,
+//   m = max m_i,  l = sum l_i 2^(m_i - m),  acc = sum acc_i 2^(m_i - m),
+// which also rotates back and adds the raw tail rows (packed cache).
+#include "attn_common.cuh"
+#include "host_checks.h"
+#include "quantize.cuh"
+
+namespace kvarn {
+
+cudaError_t launch_decode_split(const kvarn_config& cfg, const void* q, int q_dtype, const void* pool,
+                                int64_t n_pool_blocks, int64_t block_bytes, const void* staging,
+                                const int32_t* block_table, int max_blocks, const int32_t* seq_lens, int batch,
+                                float* out, void* workspace, int nw, AttnArgs* args, cudaStream_t st);
+cudaError_t launch_decode_split_bf16(const kvarn_config& cfg, const void* q, int q_dtype, const void* kv_pool,
+                                     int64_t n_pool_blocks, const int32_t* block_table, int max_blocks,
+                                     const int32_t* seq_lens, int batch, float* out, void* workspace, int nw,
+                                     AttnArgs* args, cudaStream_t st);
+
+struct PrefixArgs {
+    const void* q;
+    const uint8_t* pool;
+    const int32_t* table;        // physical blocks of the prefix
+    const int32_t* lens;         // prefix tokens each sequence sees
+    float* partials;             // [splits][batch * n_q][kPartialStride]
+    uint32_t* err;
+    int64_t n_pool_blocks, block_bytes;
+    int q_dtype;
+    int n_blocks;                // of the prefix
+    int batch, n_q, n_kv, G;
+    int splits;
+    float sm_scale;
+    uint32_t flags;
+    uint32_t sb[4];
+};
+
+struct PrefixMerge {
+    const float* partials;
+    const int32_t* lens;
+    int max_len;
+    int splits;
+    void* out;
+    int out_bf16;
+};
+
+// The prefix tokens sequence b sees; a length outside [0, max_len] (flagged by
+// the merge) sees none.
+__device__ __forceinline__ int prefix_len(const int32_t* lens, int b, int max_len) {
+    const int L = lens[b];
+    return L < 0 || L > max_len ? 0 : L;
+}
+
+// ---------------------------------------------------------------- prefix kernel
+constexpr int kRowTile = 16, kTokTile = 32;
+
+// grid (splits, row tiles, n_kv), 128 threads: 16 query rows against the
+// split's token range, 32 tokens at a time in shared memory, all in fp32.
+template <int B, int BITS>   // BITS 0: bf16 pages
+__global__ void __launch_bounds__(128) prefix_kernel(PrefixArgs a) {
+    wait_prior_grids();
+    constexpr int HB = BITS ? head_block_bytes(B, BITS ? BITS : 2) : 16;
+    __shared__ __align__(16) float qs[kRowTile][kD];
+    __shared__ __align__(16) float ks[kTokTile][kD + 4], vs[kTokTile][kD + 4];
+    __shared__ float ps[kRowTile][kTokTile];
+    __shared__ float mrow[kRowTile], lrow[kRowTile], frow[kRowTile];
+    __shared__ int len[kRowTile];
+    __shared__ __align__(16) uint8_t img[2][HB];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.z, R = a.batch * a.G, row0 = blockIdx.y * kRowTile;
+    int most = 0;
+    for (int b = lane; b < a.batch; b += 32) most = max(most, prefix_len(a.lens, b, a.n_blocks * B));
+    most = __reduce_max_sync(kFull, most);
+    const int tiles = (most + kTokTile - 1) / kTokTile;
+    const int t_beg = (int)((int64_t)tiles * blockIdx.x / a.splits), t_end = (int)((int64_t)tiles * (blockIdx.x + 1) / a.splits);
+    for (int r = warp; r < kRowTile; r += 4) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        const int row = row0 + r;
+        if (row < R) {
+            load_q4(a.q, a.q_dtype, (int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G, lane, v);
+            if (BITS && !(a.flags & KVARN_FLAG_NO_ROTATION)) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] *= sign_of4(a.sb[0], a.sb[1], a.sb[2], a.sb[3], 4 * lane + k);
+                fwht128(v, lane);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] *= kInvSqrtD;
+            }
+        }
+        const float s = a.sm_scale * kLog2e;
+        *reinterpret_cast<float4*>(&qs[r][4 * lane]) = make_float4(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
+        if (lane == 0) {
+            len[r] = row < R ? prefix_len(a.lens, row / a.G, a.n_blocks * B) : 0;
+            mrow[r] = -INFINITY;
+            lrow[r] = 0.f;
+        }
+    }
+    float acc[kRowTile];
+#pragma unroll
+    for (int r = 0; r < kRowTile; ++r) acc[r] = 0.f;
+    for (int t = t_beg; t < t_end; ++t) {
+        __syncthreads();
+        const int blk = t * kTokTile / B, sub = t * kTokTile % B;
+        int64_t phys = a.table[blk];
+        const bool ok = phys >= 0 && phys < a.n_pool_blocks;   // (the same for the whole CTA)
+        if (!ok) {
+            if (tid == 0) raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
+            continue;
+        }
+        if constexpr (BITS > 0) {
+            for (int kind = 0; kind < 2; ++kind) {
+                const uint4* s4 = reinterpret_cast<const uint4*>(a.pool + phys * a.block_bytes + (int64_t)(2 * h + kind) * HB);
+                for (int i = tid; i < HB / 16; i += 128) reinterpret_cast<uint4*>(img[kind])[i] = s4[i];
+            }
+            __syncthreads();
+            for (int i = warp; i < kTokTile; i += 4) {
+                float v[4];
+                dequant_row4<B, BITS>(img[0], KVARN_KIND_K, sub + i, lane, v);
+                *reinterpret_cast<float4*>(&ks[i][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+                dequant_row4<B, BITS>(img[1], KVARN_KIND_V, sub + i, lane, v);
+                *reinterpret_cast<float4*>(&vs[i][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+        } else {
+            const uint16_t* k = reinterpret_cast<const uint16_t*>(a.pool + phys * a.block_bytes) + (int64_t)(2 * h) * B * kD;
+            for (int i = warp; i < kTokTile; i += 4) {
+                float v[4];
+                load4(k, KVARN_BF16, (int64_t)(sub + i) * kD + 4 * lane, v);
+                *reinterpret_cast<float4*>(&ks[i][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+                load4(k + B * kD, KVARN_BF16, (int64_t)(sub + i) * kD + 4 * lane, v);
+                // rows behind every sequence may hold anything; 0 x NaN must not reach the sum
+                if (t * kTokTile + i >= most) v[0] = v[1] = v[2] = v[3] = 0.f;
+                *reinterpret_cast<float4*>(&vs[i][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+        }
+        __syncthreads();
+        for (int r = warp; r < kRowTile; r += 4) {   // lane: token
+            float s = 0.f;
+            for (int c = 0; c < kD; c += 4) {
+                const float4 q4 = *reinterpret_cast<const float4*>(&qs[r][c]), k4 = *reinterpret_cast<const float4*>(&ks[lane][c]);
+                s = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s))));
+            }
+            if (t * kTokTile + lane >= len[r]) s = -INFINITY;
+            const float m0 = mrow[r], m1 = fmaxf(m0, warp_max(s));
+            const float f = m0 == -INFINITY ? 0.f : exp2f(m0 - m1);
+            const float p = s == -INFINITY ? 0.f : exp2f(s - m1);
+            const float sum = warp_sum(p);
+            ps[r][lane] = p;
+            __syncwarp();
+            if (lane == 0) {
+                mrow[r] = m1;
+                frow[r] = f;
+                lrow[r] = lrow[r] * f + sum;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kRowTile; ++r) {
+            float s = acc[r] * frow[r];
+            for (int i = 0; i < kTokTile; ++i) s = fmaf(ps[r][i], vs[i][tid], s);
+            acc[r] = s;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRowTile; ++r) {
+        const int row = row0 + r;
+        if (row < R) {
+            const int64_t gw = (int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G;
+            float* p = a.partials + ((int64_t)blockIdx.x * a.batch * a.n_q + gw) * kPartialStride;
+            if (tid == 0) {
+                p[0] = mrow[r];
+                p[1] = lrow[r];
+            }
+            p[4 + tid] = acc[r];
+        }
+    }
+}
+
+// ---------------------------------------------------------------- merge
+// One CTA of kWideWarps warps per (sequence, query head): each warp merges its
+// share of the own tokens' partials, of the prefix's and of the raw tail rows;
+// warp 0 combines the shares and finishes the row.
+template <int B, bool ROT>
+__global__ void __launch_bounds__(32 * kWideWarps) prefix_merge_kernel(AttnArgs a, PrefixMerge pm) {
+    wait_prior_grids();
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    const int64_t gw = blockIdx.x;
+    __shared__ __align__(16) float slices[kWideWarps][kPartialStride];
+    __shared__ __align__(16) float tails[kWideWarps][kPartialStride];
+    const int b = (int)(gw / a.n_q), h = (int)(gw % a.n_q) / a.G;
+    const int L = a.seq_lens[b], PL = pm.lens[b];
+    const bool valid = L >= 0 && L <= a.max_blocks * B && PL >= 0 && PL <= pm.max_len;
+    if (!valid) {   // (the same for the whole CTA)
+        if (threadIdx.x == 0) raise_error(a.err, KVARN_DEVERR_POSITION);
+        if (threadIdx.x < kD) {
+            if (pm.out_bf16) static_cast<uint16_t*>(pm.out)[gw * kD + threadIdx.x] = 0x7fc0;
+            else static_cast<float*>(pm.out)[gw * kD + threadIdx.x] = NAN;
+        }
+        return;
+    }
+    int np;
+    const float* p0;
+    merge_locate<B, ROT>(a, gw, lane, np, p0);
+    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const int i0 = np * wp / kWideWarps, i1 = np * (wp + 1) / kWideWarps;
+    const int64_t pstride = (int64_t)a.G * kPartialStride;
+    if (i1 > i0) lse_stream<4>(p0 + i0 * pstride, i1 - i0, pstride, lane, m, l, acc);
+    const int s0 = pm.splits * wp / kWideWarps, s1 = pm.splits * (wp + 1) / kWideWarps;
+    const int64_t sstride = (int64_t)a.batch * a.n_q * kPartialStride;
+    if (PL > 0 && s1 > s0)
+        lse_stream<4>(pm.partials + gw * kPartialStride + s0 * sstride, s1 - s0, sstride, lane, m, l, acc);
+    float tm = -INFINITY, tl = 0.f, tacc[4] = {0.f, 0.f, 0.f, 0.f};
+    if (ROT && wp < L % B) {
+        float qv[4];
+        load_q4(a.q, a.q_dtype, gw, lane, qv);
+        const float qs = a.sm_scale * kLog2e;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) qv[k] *= qs;
+        tail_slice<B, kWideWarps>(a.staging + ((int64_t)b * a.n_kv + h) * 2 * B * kD, L % B, wp, qv, lane, tm, tl, tacc);
+    }
+    if (lane == 0) {
+        slices[wp][0] = m;
+        slices[wp][1] = l;
+        tails[wp][0] = tm;
+        tails[wp][1] = tl;
+    }
+    *reinterpret_cast<float4*>(&slices[wp][4 + 4 * lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    *reinterpret_cast<float4*>(&tails[wp][4 + 4 * lane]) = make_float4(tacc[0], tacc[1], tacc[2], tacc[3]);
+    __syncthreads();
+    if (wp != 0) return;
+    m = -INFINITY, l = 0.f;
+    acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+    combine_slices(&slices[0][0], kWideWarps, lane, m, l, acc);
+    if (ROT && !(a.flags & KVARN_FLAG_NO_ROTATION)) {
+        fwht128(acc, lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] *= kInvSqrtD * sign_of4(a.sb[0], a.sb[1], a.sb[2], a.sb[3], 4 * lane + k);
+    }
+    if (ROT && L % B > 0) {
+        float mt = -INFINITY, lt = 0.f, at[4] = {0.f, 0.f, 0.f, 0.f};
+        combine_slices(&tails[0][0], kWideWarps, lane, mt, lt, at);
+        if (mt != -INFINITY) {
+            const float mn = fmaxf(m, mt);
+            const float fa = m == -INFINITY ? 0.f : exp2f(m - mn), ft = exp2f(mt - mn);
+            l = l * fa + lt * ft;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[k] = acc[k] * fa + at[k] * ft;
+        }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] *= inv;
+    if (pm.out_bf16) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0], acc[1]), hi = __floats2bfloat162_rn(acc[2], acc[3]);
+        reinterpret_cast<uint2*>(static_cast<uint16_t*>(pm.out) + gw * kD)[lane] =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    } else {
+        reinterpret_cast<float4*>(static_cast<float*>(pm.out) + gw * kD)[lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+namespace {
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Token ranges the prefix is cut into: enough for every SM to have one.
+int prefix_splits(const kvarn_config& c, int64_t batch, int64_t prefix_blocks) {
+    const int64_t sms = current_device_sms();
+    if (sms <= 0) return 0;
+    const int64_t units = c.n_kv_heads * ((batch * (c.n_q_heads / c.n_kv_heads) + 127) / 128);
+    const int64_t tiles = (prefix_blocks * c.block_size + 127) / 128;
+    int64_t s = sms / units;
+    s = s < tiles ? s : tiles;
+    return (int)(s > 1 ? s : 1);
+}
+
+size_t prefix_ws_bytes(const kvarn_config& c, int32_t batch, int64_t prefix_blocks) {
+    if (batch == 0) return kWsHeader;
+    const size_t own = decode_ws_bytes(c, batch);
+    const int s = prefix_splits(c, batch, prefix_blocks);
+    if (own == 0 || s == 0) return 0;
+    return align256(own) + (size_t)s * batch * c.n_q_heads * kPartialStride * sizeof(float);
+}
+
+template <bool PACKED>
+int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* pool, int64_t n_pool_blocks,
+                const void* staging, const int32_t* prefix_table, int32_t prefix_blocks, const int32_t* prefix_lens,
+                const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens, int32_t batch, void* out,
+                int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    kvarn_config c;
+    int r = check_config(cfg, &c);
+    if (r != KVARN_OK) return r;
+    if (out_dtype != KVARN_BF16 && out_dtype != KVARN_FP32) return KVARN_ERR_INVALID_ARG;
+    if (prefix_blocks < 0 || (int64_t)prefix_blocks * c.block_size > 0x7fffffff) return KVARN_ERR_INVALID_ARG;
+    if (max_blocks == 0) block_table = seq_lens;         // tables without columns are never read
+    if (prefix_blocks == 0) prefix_table = prefix_lens;
+    r = check_packed_attn_args(c, q, q_dtype, pool, n_pool_blocks, PACKED ? staging : pool, block_table, max_blocks,
+                               seq_lens, batch, 1, (const float*)out);
+    if (r != KVARN_OK || batch == 0) return r;
+    if (!prefix_table || !prefix_lens || !workspace || !aligned(prefix_table, 4) || !aligned(prefix_lens, 4) ||
+        !aligned(workspace, 16))
+        return KVARN_ERR_INVALID_ARG;
+    const int G = c.n_q_heads / c.n_kv_heads;
+    if (((int64_t)batch * G + kRowTile - 1) / kRowTile > 65535 || c.n_kv_heads > 65535) return KVARN_ERR_INVALID_ARG;
+    const size_t need = prefix_ws_bytes(c, batch, prefix_blocks);
+    if (need == 0) return KVARN_ERR_CUDA;
+    if (workspace_bytes < need) return KVARN_ERR_WORKSPACE;
+    const int d = current_device();
+    const int nw = PACKED ? attn_grid_warps(c.block_size, c.bits, d) : attn_bf16_grid_warps(c.block_size, d);
+    if (nw <= 0) return KVARN_ERR_CUDA;
+    const cudaStream_t st = (cudaStream_t)stream;
+
+    PrefixArgs p = {};
+    p.q = q;
+    p.pool = (const uint8_t*)pool;
+    p.table = prefix_table;
+    p.lens = prefix_lens;
+    p.partials = (float*)((uint8_t*)workspace + align256(decode_ws_bytes(c, batch)));
+    p.err = (uint32_t*)workspace;
+    p.n_pool_blocks = n_pool_blocks;
+    p.block_bytes = PACKED ? block_bytes_of(c) : (int64_t)c.n_kv_heads * 2 * c.block_size * kD * 2;
+    p.q_dtype = q_dtype;
+    p.n_blocks = prefix_blocks;
+    p.batch = batch;
+    p.n_q = c.n_q_heads;
+    p.n_kv = c.n_kv_heads;
+    p.G = G;
+    p.splits = prefix_splits(c, batch, prefix_blocks);
+    p.sm_scale = c.sm_scale;
+    p.flags = c.flags;
+    for (int i = 0; i < 4; ++i) p.sb[i] = c.sign_bits[i];
+    const dim3 grid(p.splits, (batch * G + kRowTile - 1) / kRowTile, c.n_kv_heads);
+    cudaError_t e;
+    AttnArgs a;
+    if constexpr (PACKED) {
+        e = dispatch(c, [&](auto b, auto w) {
+            return launch_pdl(prefix_kernel<decltype(b)::value, decltype(w)::value>, grid, 128, 0, st, p);
+        });
+        if (e == cudaSuccess)
+            e = launch_decode_split(c, q, q_dtype, pool, n_pool_blocks, p.block_bytes, staging, block_table, max_blocks,
+                                    seq_lens, batch, nullptr, workspace, nw, &a, st);
+    } else {
+        e = c.block_size == 32 ? launch_pdl(prefix_kernel<32, 0>, grid, 128, 0, st, p)
+                               : launch_pdl(prefix_kernel<64, 0>, grid, 128, 0, st, p);
+        if (e == cudaSuccess)
+            e = launch_decode_split_bf16(c, q, q_dtype, pool, n_pool_blocks, block_table, max_blocks, seq_lens, batch,
+                                         nullptr, workspace, nw, &a, st);
+    }
+    if (e != cudaSuccess) return KVARN_ERR_CUDA;
+    const PrefixMerge pm{p.partials, prefix_lens, prefix_blocks * c.block_size, p.splits, out, out_dtype == KVARN_BF16};
+    const unsigned rows = (unsigned)((int64_t)batch * c.n_q_heads);
+    const int threads = 32 * kWideWarps;
+    if constexpr (PACKED)
+        e = c.block_size == 32 ? launch_pdl(prefix_merge_kernel<32, true>, rows, threads, 0, st, a, pm)
+                               : launch_pdl(prefix_merge_kernel<64, true>, rows, threads, 0, st, a, pm);
+    else
+        e = launch_pdl(prefix_merge_kernel<kChunk, false>, rows, threads, 0, st, a, pm);
+    return e == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace kvarn
+
+using namespace kvarn;
+
+extern "C" {
+
+size_t kvarn_prefix_workspace_bytes(const kvarn_config* cfg, int32_t batch, int32_t prefix_blocks) {
+    kvarn_config c;
+    if (check_config(cfg, &c) != KVARN_OK || batch < 0 || prefix_blocks < 0) return 0;
+    return prefix_ws_bytes(c, batch, prefix_blocks);
+}
+
+int kvarn_prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* pool, int64_t n_pool_blocks,
+                      const void* staging, const int32_t* prefix_table, int32_t prefix_blocks,
+                      const int32_t* prefix_lens, const int32_t* block_table, int32_t max_blocks_per_seq,
+                      const int32_t* seq_lens, int32_t batch, void* out, int32_t out_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    return prefix_attn<true>(cfg, q, q_dtype, pool, n_pool_blocks, staging, prefix_table, prefix_blocks, prefix_lens,
+                             block_table, max_blocks_per_seq, seq_lens, batch, out, out_dtype, workspace,
+                             workspace_bytes, stream);
+}
+
+int kvarn_prefix_attn_bf16(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* kv_pool,
+                           int64_t n_pool_blocks, const int32_t* prefix_table, int32_t prefix_blocks,
+                           const int32_t* prefix_lens, const int32_t* block_table, int32_t max_blocks_per_seq,
+                           const int32_t* seq_lens, int32_t batch, void* out, int32_t out_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    return prefix_attn<false>(cfg, q, q_dtype, kv_pool, n_pool_blocks, nullptr, prefix_table, prefix_blocks, prefix_lens,
+                              block_table, max_blocks_per_seq, seq_lens, batch, out, out_dtype, workspace,
+                              workspace_bytes, stream);
+}
+
+}  // extern "C"

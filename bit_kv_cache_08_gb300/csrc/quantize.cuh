@@ -389,6 +389,72 @@ __device__ __forceinline__ void load4(const void* src, int dtype, int64_t elem_o
     }
 }
 
+// ---------------------------------------------------------------- dequantise
+// Token row t of a head-block image in shared memory: this lane's 4 channels
+// 4 lane .. 4 lane + 3 of (code*s + z)*R*C (rotated space).
+template <int B, int BITS>
+__device__ __forceinline__ void dequant_row4(const uint8_t* img, int kind, int t, int lane, float (&v)[4]) {
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(img);
+    const uint16_t* s_sec = reinterpret_cast<const uint16_t*>(img + off_s(B, BITS));
+    const uint16_t* z_sec = reinterpret_cast<const uint16_t*>(img + off_z(B, BITS));
+    const uint16_t* R_sec = reinterpret_cast<const uint16_t*>(img + off_R(B, BITS));
+    const uint16_t* C_sec = reinterpret_cast<const uint16_t*>(img + off_C(B, BITS));
+    const int g = lane >> 3, sb = t >> 5;
+    const float s = h2f(s_sec[g * B + t]), z = h2f(z_sec[g * B + t]), R = h2f(R_sec[t]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int c = 4 * lane + k;
+        int word, bit;
+        if (BITS == 3) {   // low two bits in the 2-bit layout, the high bit in the 1-bit plane
+            int rec, w2, j, h;
+            if (kind == KVARN_KIND_K) {
+                const int a = (t & 31) >> 2, ii = t & 3, bq = (c & 31) >> 3, e = c & 7;
+                rec = 32 * sb + 4 * a + bq;
+                w2 = 2 * ii + (g >> 1);
+                j = 4 * (g & 1) + (e >> 1);
+                h = e & 1;
+            } else {
+                const int bq = (t & 31) >> 3, d = t & 7, a = (c & 31) >> 2, f = c & 3;
+                rec = 32 * sb + 4 * a + bq;
+                w2 = 2 * g + (f >> 1);
+                j = 4 * (d >> 2) + 2 * ((d & 3) >> 1) + (f & 1);
+                h = d & 1;
+            }
+            const uint32_t lo = (words[rec * 12 + w2] >> (2 * j + 16 * h)) & 3u;
+            const uint32_t hb = (words[rec * 12 + 8 + (w2 >> 1)] >> (8 * (w2 & 1) + j + 16 * h)) & 1u;
+            v[k] = fmaf((float)(lo | (hb << 2)), s, z) * R * h2f(C_sec[c]);
+            continue;
+        }
+        if (kind == KVARN_KIND_K) {
+            const int a = (t & 31) >> 2, ii = t & 3, bq = (c & 31) >> 3, e = c & 7;
+            if (BITS == 4) {
+                word = (32 * sb + 4 * a + bq) * 16 + 4 * ii + g;
+                bit = 4 * (e >> 1) + 16 * (e & 1);
+            } else {
+                word = (32 * sb + 4 * a + bq) * 8 + 2 * ii + (g >> 1);
+                bit = 2 * (4 * (g & 1) + (e >> 1)) + 16 * (e & 1);
+            }
+        } else {
+            const int bq = (t & 31) >> 3, d = t & 7, a = (c & 31) >> 2, f = c & 3;
+            if (BITS == 4) {
+                word = (32 * sb + 4 * a + bq) * 16 + 4 * g + f;
+                bit = 4 * (d >> 1) + 16 * (d & 1);
+            } else {
+                word = (32 * sb + 4 * a + bq) * 8 + 2 * g + (f >> 1);
+                bit = 2 * (4 * (d >> 2) + 2 * ((d & 3) >> 1) + (f & 1)) + 16 * (d & 1);
+            }
+        }
+        const float code = (float)((words[word] >> bit) & ((1u << BITS) - 1u));
+        v[k] = fmaf(code, s, z) * R * h2f(C_sec[c]);
+    }
+}
+
+template <int B, int BITS>
+__device__ __forceinline__ void load_image(uint8_t* img, const uint8_t* src, int tid) {
+    const uint4* s4 = reinterpret_cast<const uint4*>(src);
+    for (int i = tid; i < head_block_bytes(B, BITS) / 16; i += 256) reinterpret_cast<uint4*>(img)[i] = s4[i];
+}
+
 // ---------------------------------------------------------------- host side
 inline QuantParams make_params(const kvarn_config& cfg, int kind) {
     QuantParams p;

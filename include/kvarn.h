@@ -388,6 +388,47 @@ int kvarn_decode_attn_bf16(const kvarn_config* cfg, const void* q, int32_t q_dty
                            const int32_t* seq_lens, int32_t batch, float* out, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/* Workspace bytes for kvarn_prefix_attn / kvarn_prefix_attn_bf16 with this
+ * batch and prefix_blocks on the CURRENT device: the decode workspace for the
+ * own tokens, then one partial per (token range of the prefix, sequence,
+ * query head). 0 on a bad config. */
+size_t kvarn_prefix_workspace_bytes(const kvarn_config* cfg, int32_t batch, int32_t prefix_blocks);
+
+/*
+ * kvarn_prefix_attn -- decode attention over the packed cache for a batch
+ * whose sequences share a prefix (a system prompt, one document, several
+ * samples of one prompt), read once for all of them. (A serving convenience;
+ * the query is multiplied by the same Hadamard matrix, section 三 3.1.)
+ *
+ * The prefix's blocks are prefix_table (device int32 [prefix_blocks]), every
+ * one complete in the pool; sequence b sees its first prefix_lens[b] tokens
+ * (device int32 [batch], 0 .. prefix_blocks * B: any count, the same for all
+ * or not). Its own tokens follow: block_table, seq_lens and staging as for
+ * kvarn_decode_attn, their indices starting at 0.
+ *   out[b][j][:] = sum_t softmax_t(sm_scale * q.k_t) v_t
+ * over the prefix's tokens and the own ones together; no token at all gives
+ * zeros. out: device [batch][n_q][128], out_dtype KVARN_BF16 or KVARN_FP32.
+ * workspace: at least kvarn_prefix_workspace_bytes(cfg, batch, prefix_blocks)
+ * bytes, 16-byte aligned; calls that may overlap need one each. Device
+ * faults: KVARN_DEVERR_BLOCK_ID, KVARN_DEVERR_POSITION (a length outside its
+ * range), KVARN_DEVERR_WAIT_TIMEOUT.
+ */
+int kvarn_prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* pool,
+                      int64_t n_pool_blocks, const void* staging, const int32_t* prefix_table,
+                      int32_t prefix_blocks, const int32_t* prefix_lens, const int32_t* block_table,
+                      int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch, void* out,
+                      int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kvarn_prefix_attn_bf16 -- the same over the bf16 pages of
+ * kvarn_decode_attn_bf16; the last page of the prefix may be partly filled.
+ */
+int kvarn_prefix_attn_bf16(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* kv_pool,
+                           int64_t n_pool_blocks, const int32_t* prefix_table, int32_t prefix_blocks,
+                           const int32_t* prefix_lens, const int32_t* block_table, int32_t max_blocks_per_seq,
+                           const int32_t* seq_lens, int32_t batch, void* out, int32_t out_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 /*
  * kvarn_decode_attn_noalloc -- kvarn_decode_attn for callers that cannot
  * allocate device memory. (The paper has no counterpart; this is a library
