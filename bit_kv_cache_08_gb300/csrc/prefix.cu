@@ -10,8 +10,8 @@
 // of partial in the log-sum-exp sense,
 //   m = max m_i,  l = sum l_i 2^(m_i - m),  acc = sum acc_i 2^(m_i - m),
 // which also rotates back and adds the raw tail rows (packed cache).
-#include "attn_common.cuh"
 #include "host_checks.h"
+#include "prefix.cuh"
 #include "quantize.cuh"
 
 namespace kvarn {
@@ -25,22 +25,7 @@ cudaError_t launch_decode_split_bf16(const kvarn_config& cfg, const void* q, int
                                      const int32_t* seq_lens, int batch, float* out, void* workspace, int nw,
                                      AttnArgs* args, cudaStream_t st);
 
-struct PrefixArgs {
-    const void* q;
-    const uint8_t* pool;
-    const int32_t* table;        // physical blocks of the prefix
-    const int32_t* lens;         // prefix tokens each sequence sees
-    float* partials;             // [splits][batch * n_q][kPartialStride]
-    uint32_t* err;
-    int64_t n_pool_blocks, block_bytes;
-    int q_dtype;
-    int n_blocks;                // of the prefix
-    int batch, n_q, n_kv, G;
-    int splits;
-    float sm_scale;
-    uint32_t flags;
-    uint32_t sb[4];
-};
+cudaError_t launch_prefix_bf16(const PrefixArgs& p, int block_size, cudaStream_t st);
 
 struct PrefixMerge {
     const float* partials;
@@ -51,22 +36,15 @@ struct PrefixMerge {
     int out_bf16;
 };
 
-// The prefix tokens sequence b sees; a length outside [0, max_len] (flagged by
-// the merge) sees none.
-__device__ __forceinline__ int prefix_len(const int32_t* lens, int b, int max_len) {
-    const int L = lens[b];
-    return L < 0 || L > max_len ? 0 : L;
-}
-
 // ---------------------------------------------------------------- prefix kernel
 constexpr int kRowTile = 16, kTokTile = 32;
 
 // grid (splits, row tiles, n_kv), 128 threads: 16 query rows against the
 // split's token range, 32 tokens at a time in shared memory, all in fp32.
-template <int B, int BITS>   // BITS 0: bf16 pages
+template <int B, int BITS>
 __global__ void __launch_bounds__(128) prefix_kernel(PrefixArgs a) {
     wait_prior_grids();
-    constexpr int HB = BITS ? head_block_bytes(B, BITS ? BITS : 2) : 16;
+    constexpr int HB = head_block_bytes(B, BITS);
     __shared__ __align__(16) float qs[kRowTile][kD];
     __shared__ __align__(16) float ks[kTokTile][kD + 4], vs[kTokTile][kD + 4];
     __shared__ float ps[kRowTile][kTokTile];
@@ -75,9 +53,7 @@ __global__ void __launch_bounds__(128) prefix_kernel(PrefixArgs a) {
     __shared__ __align__(16) uint8_t img[2][HB];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.z, R = a.batch * a.G, row0 = blockIdx.y * kRowTile;
-    int most = 0;
-    for (int b = lane; b < a.batch; b += 32) most = max(most, prefix_len(a.lens, b, a.n_blocks * B));
-    most = __reduce_max_sync(kFull, most);
+    const int most = prefix_most(a, a.n_blocks * B, lane);
     const int tiles = (most + kTokTile - 1) / kTokTile;
     const int t_beg = (int)((int64_t)tiles * blockIdx.x / a.splits), t_end = (int)((int64_t)tiles * (blockIdx.x + 1) / a.splits);
     for (int r = warp; r < kRowTile; r += 4) {
@@ -85,7 +61,7 @@ __global__ void __launch_bounds__(128) prefix_kernel(PrefixArgs a) {
         const int row = row0 + r;
         if (row < R) {
             load_q4(a.q, a.q_dtype, (int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G, lane, v);
-            if (BITS && !(a.flags & KVARN_FLAG_NO_ROTATION)) {
+            if (!(a.flags & KVARN_FLAG_NO_ROTATION)) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] *= sign_of4(a.sb[0], a.sb[1], a.sb[2], a.sb[3], 4 * lane + k);
                 fwht128(v, lane);
@@ -113,30 +89,17 @@ __global__ void __launch_bounds__(128) prefix_kernel(PrefixArgs a) {
             if (tid == 0) raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
             continue;
         }
-        if constexpr (BITS > 0) {
-            for (int kind = 0; kind < 2; ++kind) {
-                const uint4* s4 = reinterpret_cast<const uint4*>(a.pool + phys * a.block_bytes + (int64_t)(2 * h + kind) * HB);
-                for (int i = tid; i < HB / 16; i += 128) reinterpret_cast<uint4*>(img[kind])[i] = s4[i];
-            }
-            __syncthreads();
-            for (int i = warp; i < kTokTile; i += 4) {
-                float v[4];
-                dequant_row4<B, BITS>(img[0], KVARN_KIND_K, sub + i, lane, v);
-                *reinterpret_cast<float4*>(&ks[i][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
-                dequant_row4<B, BITS>(img[1], KVARN_KIND_V, sub + i, lane, v);
-                *reinterpret_cast<float4*>(&vs[i][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
-            }
-        } else {
-            const uint16_t* k = reinterpret_cast<const uint16_t*>(a.pool + phys * a.block_bytes) + (int64_t)(2 * h) * B * kD;
-            for (int i = warp; i < kTokTile; i += 4) {
-                float v[4];
-                load4(k, KVARN_BF16, (int64_t)(sub + i) * kD + 4 * lane, v);
-                *reinterpret_cast<float4*>(&ks[i][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
-                load4(k + B * kD, KVARN_BF16, (int64_t)(sub + i) * kD + 4 * lane, v);
-                // rows behind every sequence may hold anything; 0 x NaN must not reach the sum
-                if (t * kTokTile + i >= most) v[0] = v[1] = v[2] = v[3] = 0.f;
-                *reinterpret_cast<float4*>(&vs[i][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
-            }
+        for (int kind = 0; kind < 2; ++kind) {
+            const uint4* s4 = reinterpret_cast<const uint4*>(a.pool + phys * a.block_bytes + (int64_t)(2 * h + kind) * HB);
+            for (int i = tid; i < HB / 16; i += 128) reinterpret_cast<uint4*>(img[kind])[i] = s4[i];
+        }
+        __syncthreads();
+        for (int i = warp; i < kTokTile; i += 4) {
+            float v[4];
+            dequant_row4<B, BITS>(img[0], KVARN_KIND_K, sub + i, lane, v);
+            *reinterpret_cast<float4*>(&ks[i][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+            dequant_row4<B, BITS>(img[1], KVARN_KIND_V, sub + i, lane, v);
+            *reinterpret_cast<float4*>(&vs[i][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
         }
         __syncthreads();
         for (int r = warp; r < kRowTile; r += 4) {   // lane: token
@@ -270,23 +233,41 @@ namespace {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Token ranges the prefix is cut into: enough for every SM to have one.
-int prefix_splits(const kvarn_config& c, int64_t batch, int64_t prefix_blocks) {
-    const int64_t sms = current_device_sms();
-    if (sms <= 0) return 0;
-    const int64_t units = c.n_kv_heads * ((batch * (c.n_q_heads / c.n_kv_heads) + 127) / 128);
+// How the prefix kernel is cut: query rows of a CTA, token ranges (splits) and
+// partials per range (bf16 pages with one row tile: one each from the even and
+// the odd K/V tiles).
+struct PrefixPlan {
+    int rows, streams, splits;
+};
+
+PrefixPlan prefix_plan(const kvarn_config& c, int64_t batch, int64_t prefix_blocks, bool packed, int q_dtype) {
+    const int64_t sms = current_device_sms(), R = batch * (c.n_q_heads / c.n_kv_heads);
+    PrefixPlan p{kPRows, 1, 0};
+    if (sms <= 0) return p;
+    if (!packed) {
+        if (q_dtype == KVARN_BF16 && R > kPRows) p.rows = 2 * kPRows;
+        else p.streams = 2;
+    }
+    // enough ranges for every SM to have one
+    const int64_t units = c.n_kv_heads * ((R + p.rows - 1) / p.rows);
     const int64_t tiles = (prefix_blocks * c.block_size + 127) / 128;
     int64_t s = sms / units;
     s = s < tiles ? s : tiles;
-    return (int)(s > 1 ? s : 1);
+    p.splits = (int)(s > 1 ? s : 1);
+    return p;
 }
 
 size_t prefix_ws_bytes(const kvarn_config& c, int32_t batch, int64_t prefix_blocks) {
     if (batch == 0) return kWsHeader;
     const size_t own = decode_ws_bytes(c, batch);
-    const int s = prefix_splits(c, batch, prefix_blocks);
-    if (own == 0 || s == 0) return 0;
-    return align256(own) + (size_t)s * batch * c.n_q_heads * kPartialStride * sizeof(float);
+    int slots = 0;   // the most that either cache and query type needs
+    for (int k = 0; k < 3; ++k) {
+        const PrefixPlan p = prefix_plan(c, batch, prefix_blocks, k == 0, k == 1 ? KVARN_BF16 : KVARN_FP32);
+        if (p.splits == 0) return 0;
+        slots = p.splits * p.streams > slots ? p.splits * p.streams : slots;
+    }
+    if (own == 0) return 0;
+    return align256(own) + (size_t)slots * batch * c.n_q_heads * kPartialStride * sizeof(float);
 }
 
 template <bool PACKED>
@@ -308,6 +289,7 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
         !aligned(workspace, 16))
         return KVARN_ERR_INVALID_ARG;
     const int G = c.n_q_heads / c.n_kv_heads;
+    if (!PACKED && n_pool_blocks > 0x7fffffff / ((int64_t)c.n_kv_heads * 2 * c.block_size)) return KVARN_ERR_INVALID_ARG;
     if (((int64_t)batch * G + kRowTile - 1) / kRowTile > 65535 || c.n_kv_heads > 65535) return KVARN_ERR_INVALID_ARG;
     const size_t need = prefix_ws_bytes(c, batch, prefix_blocks);
     if (need == 0) return KVARN_ERR_CUDA;
@@ -332,14 +314,15 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
     p.n_q = c.n_q_heads;
     p.n_kv = c.n_kv_heads;
     p.G = G;
-    p.splits = prefix_splits(c, batch, prefix_blocks);
+    const PrefixPlan plan = prefix_plan(c, batch, prefix_blocks, PACKED, q_dtype);
+    p.splits = plan.splits;
     p.sm_scale = c.sm_scale;
     p.flags = c.flags;
     for (int i = 0; i < 4; ++i) p.sb[i] = c.sign_bits[i];
-    const dim3 grid(p.splits, (batch * G + kRowTile - 1) / kRowTile, c.n_kv_heads);
     cudaError_t e;
     AttnArgs a;
     if constexpr (PACKED) {
+        const dim3 grid(p.splits, (batch * G + kRowTile - 1) / kRowTile, c.n_kv_heads);
         e = dispatch(c, [&](auto b, auto w) {
             return launch_pdl(prefix_kernel<decltype(b)::value, decltype(w)::value>, grid, 128, 0, st, p);
         });
@@ -347,14 +330,13 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
             e = launch_decode_split(c, q, q_dtype, pool, n_pool_blocks, p.block_bytes, staging, block_table, max_blocks,
                                     seq_lens, batch, nullptr, workspace, nw, &a, st);
     } else {
-        e = c.block_size == 32 ? launch_pdl(prefix_kernel<32, 0>, grid, 128, 0, st, p)
-                               : launch_pdl(prefix_kernel<64, 0>, grid, 128, 0, st, p);
+        e = launch_prefix_bf16(p, c.block_size, st);
         if (e == cudaSuccess)
             e = launch_decode_split_bf16(c, q, q_dtype, pool, n_pool_blocks, block_table, max_blocks, seq_lens, batch,
                                          nullptr, workspace, nw, &a, st);
     }
     if (e != cudaSuccess) return KVARN_ERR_CUDA;
-    const PrefixMerge pm{p.partials, prefix_lens, prefix_blocks * c.block_size, p.splits, out, out_dtype == KVARN_BF16};
+    const PrefixMerge pm{p.partials, prefix_lens, prefix_blocks * c.block_size, plan.splits * plan.streams, out, out_dtype == KVARN_BF16};
     const unsigned rows = (unsigned)((int64_t)batch * c.n_q_heads);
     const int threads = 32 * kWideWarps;
     if constexpr (PACKED)

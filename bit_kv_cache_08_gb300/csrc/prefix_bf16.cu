@@ -1,0 +1,385 @@
+// prefix_bf16.cu -- the shared prefix over bf16 pages on the tensor cores.
+//
+// Per kv head, R = batch * G query rows meet every prefix token: S = Q K^T,
+// P = 2^(scale S - m), O += P V with the running row maximum m and sum l of
+// an online softmax. A CTA owns up to 256 rows of one head and a range of
+// 128-token tiles, and writes (m, l, O) partials for the merge.
+//
+// Two streams run through the tensor core in turn, so that one multiplies
+// while the other is in its softmax: with more than 128 rows, two row tiles
+// over the same K/V tiles; with fewer, one row tile over even and odd K/V
+// tiles (their partials are joined at the end). Per stream:
+//   S (128 x 128 fp32)   tensor memory; K and Q tiles from shared memory
+//   softmax              128 threads, a row each: S to registers, P (bf16)
+//                        back over S in tensor memory as the A operand of
+//   O (128 x 128 fp32)   tensor memory; V straight from its page rows
+//                        (contraction across rows, so no transposition)
+// O is rescaled only when a row's maximum has grown by more than 2^8 since
+// the reference it was accumulated with (P stays within 2^8; the result is
+// the same up to rounding).
+//
+// Warps: 0-3 and 4-7 softmax of the two streams, 8 issues the products, 9
+// copies pages (a tile copy per page and 64-channel half, swizzled), two
+// stages each of K and V.
+//
+// Rounding: scores are exact products summed in fp32 (an fp32 query is split
+// into two bf16 halves, two products); P is rounded to bf16, the type of V,
+// which leaves the output within 2^-8 of sum p |v|.
+#include "prefix.cuh"
+
+#include <cuda.h>
+
+namespace kvarn {
+
+constexpr int kTileTok = 128;
+constexpr int kOperand = kPRows * kD * 2;           // bytes of a 128 x 128 16-bit operand
+constexpr int kHalfOperand = kOperand / 2;          // its 64-element column block
+
+struct Bf16Smem {
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], v_clean, drained;
+    uint32_t tmem;
+    int stop;
+};
+constexpr int kBf16Header = 1024;
+static_assert(sizeof(Bf16Smem) <= kBf16Header, "header");
+
+// MODE 0: 256 rows; 1: 128 rows; 2: 128 rows, fp32 query in two halves
+constexpr int bf16_q_tiles(int mode) { return mode == 1 ? 1 : 2; }
+constexpr size_t bf16_prefix_smem(int mode) { return 1024 + kBf16Header + (size_t)(bf16_q_tiles(mode) + 4) * kOperand; }
+
+template <int B, int MODE>
+__global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_constant__ CUtensorMap map, PrefixArgs a) {
+    wait_prior_grids();
+    extern __shared__ uint8_t raw[];
+    // operands on 1024-byte boundaries (the swizzle's period)
+    uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    Bf16Smem& s = *reinterpret_cast<Bf16Smem*>(base);
+    uint8_t* q_op = base + kBf16Header;
+    uint8_t* k_op = q_op + bf16_q_tiles(MODE) * kOperand;
+    uint8_t* v_op = k_op + 2 * kOperand;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kRowsCta = MODE == 0 ? 2 * kPRows : kPRows;
+    const int h = blockIdx.z, R = a.batch * a.G, row0 = blockIdx.y * kRowsCta;
+    const int max_len = a.n_blocks * B;
+
+    const int most = prefix_most(a, max_len, lane);
+    const int tiles = (most + kTileTok - 1) / kTileTok;
+    const int t_beg = (int)((int64_t)tiles * blockIdx.x / a.splits), t_end = (int)((int64_t)tiles * (blockIdx.x + 1) / a.splits);
+    const int n = t_end - t_beg;                       // K/V tiles
+    const int steps = MODE == 0 ? 2 * n : n;           // (stream, tile) items: stream = step % 2
+
+    if (tid == 0) {
+        s.stop = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.k_full[i], 1);
+            mbar_init(&s.k_empty[i], 1);
+            mbar_init(&s.v_full[i], 1);
+            mbar_init(&s.v_empty[i], 1);
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.p_ready[i], 128);
+            mbar_init(&s.o_full[i], 1);
+        }
+        mbar_init(&s.v_clean, 1);
+        mbar_init(&s.drained, 1);
+        fence_mbar_init();
+    }
+    if (warp == 8) tmem_alloc(&s.tmem, 512);
+    // ---- the query rows as swizzled operands (rows behind the batch: zeros)
+    for (int i = tid; i < kRowsCta * 16; i += 320) {
+        const int r = i >> 4, u = i & 15;              // row, 8-channel unit
+        const int row = row0 + r;
+        uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+        if (row < R) {
+            const int64_t at = ((int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G) * kD + 8 * u;
+            if (MODE == 2) {
+                const float* f = static_cast<const float*>(a.q) + at;
+                uint32_t* ph = reinterpret_cast<uint32_t*>(&hi);
+                uint32_t* pl = reinterpret_cast<uint32_t*>(&lo);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+                    const float2 xf = __bfloat1622float2(x);
+                    const __nv_bfloat162 y = __floats2bfloat162_rn(f[2 * k] - xf.x, f[2 * k + 1] - xf.y);
+                    ph[k] = *reinterpret_cast<const uint32_t*>(&x);
+                    pl[k] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+            } else {
+                hi = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
+            }
+        }
+        uint8_t* dst = q_op + (r / kPRows) * kOperand + (u >> 3) * kHalfOperand + swizzled(r % kPRows, u & 7);
+        *reinterpret_cast<uint4*>(dst) = hi;
+        if (MODE == 2) *reinterpret_cast<uint4*>(dst + kOperand) = lo;
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = s.tmem;
+    volatile int* stop = &s.stop;
+    const uint32_t tm_s = tm, tm_o = tm + 256;         // S (and P) of stream w at + 128 w, O likewise
+
+    if (warp == 9) {
+        // ---------------------------------------------------------- page copies
+        constexpr int PPT = kTileTok / B;              // pages per tile
+        const int used = (most + B - 1) / B;           // pages that hold a visible token
+        bool ok = true;
+        int done_k = 0, done_v = 0;                    // tiles issued
+        for (int i = 0; i < n && ok; ++i) {
+            const int t = t_beg + i, st = i & 1;
+            int page = -1;
+            const int p = lane >> 1, half = lane & 1;  // lanes 0 .. 2 PPT - 1 copy
+            if (p < PPT && t * PPT + p < used) {
+                page = a.table[t * PPT + p];
+                if (page < 0 || page >= a.n_pool_blocks) {
+                    raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
+                    page = -1;
+                }
+            }
+            const uint32_t bytes = __popc(__ballot_sync(kFull, page >= 0)) * (B * 128);
+            const int y = (int)(((int64_t)max(page, 0) * a.n_kv + h) * 2 * B);
+            for (int kind = 0; kind < 2; ++kind) {
+                uint64_t* full = kind ? &s.v_full[st] : &s.k_full[st];
+                if (i >= 2) ok = mbar_wait_or_stop(kind ? &s.v_empty[st] : &s.k_empty[st], ((i >> 1) - 1) & 1, stop, kWaitLimit);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                __syncwarp();
+                if (page >= 0)
+                    tile_g2s((kind ? v_op : k_op) + st * kOperand + half * kHalfOperand + p * B * 128, &map, 64 * half,
+                             y + kind * B, full);
+                __syncwarp();
+                (kind ? done_v : done_k) = i + 1;
+            }
+            // value rows behind every sequence's prefix: a weight of 0 times
+            // whatever the page or an earlier tile holds must be 0
+            const int valid = most - t * kTileTok;
+            if (ok && valid < kTileTok) {
+                ok = __all_sync(kFull, mbar_wait_or_stop(&s.v_full[st], (i >> 1) & 1, stop, kWaitLimit));
+                for (int x = valid * 8 + lane; x < kTileTok * 8; x += 32)
+                    for (int c = 0; c < 2; ++c)
+                        *reinterpret_cast<uint4*>(v_op + st * kOperand + c * kHalfOperand + x * 16) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.v_clean);
+            }
+        }
+        // copies in flight land before the CTA ends
+        if (*stop) {
+            for (int i = max(0, done_k - 2); i < done_k; ++i) mbar_wait_bounded(&s.k_full[i & 1], (i >> 1) & 1, kWaitLimit);
+            for (int i = max(0, done_v - 2); i < done_v; ++i) mbar_wait_bounded(&s.v_full[i & 1], (i >> 1) & 1, kWaitLimit);
+        }
+    } else if (warp == 8) {
+        // ---------------------------------------------------------- products
+        if (lane == 0 && steps > 0) {
+            constexpr uint32_t kQk = mma_shape(kMmaBf16, kTileTok, false), kPv = mma_shape(kMmaBf16, kD, true);
+            bool ok = true;
+            auto tile_of = [&](int i) { return MODE == 0 ? i >> 1 : i; };
+            auto last_use = [&](int i) { return MODE == 0 ? (i & 1) == 1 : true; };
+            auto qk = [&](int i) {
+                const int w = i & 1, t = tile_of(i), st = t & 1;
+                if (!mbar_wait_or_stop(&s.k_full[st], (t >> 1) & 1, stop, kWaitLimit)) return false;
+                tc_fence_after();
+                const uint32_t ka = smem_addr(k_op + st * kOperand);
+#pragma unroll
+                for (int part = 0; part < (MODE == 2 ? 2 : 1); ++part) {
+                    const uint32_t qa = smem_addr(q_op + (MODE == 0 ? w : part) * kOperand);
+#pragma unroll
+                    for (int k = 0; k < kD / 16; ++k) {
+                        const uint32_t off = (k >> 2) * kHalfOperand + (k & 3) * 32;
+                        mma_ss(tm_s + 128 * w, smem_operand(qa + off, 16, 1024), smem_operand(ka + off, 16, 1024), kQk,
+                               part > 0 || k > 0);
+                    }
+                }
+                mma_commit(&s.s_full[w]);
+                if (last_use(i)) mma_commit(&s.k_empty[st]);
+                return true;
+            };
+            auto pv = [&](int i) {
+                const int w = i & 1, t = tile_of(i), st = t & 1;
+                if (!mbar_wait_or_stop(&s.p_ready[w], (i >> 1) & 1, stop, kWaitLimit)) return false;
+                if (!mbar_wait_or_stop(&s.v_full[st], (t >> 1) & 1, stop, kWaitLimit)) return false;
+                if (most - (t_beg + t) * kTileTok < kTileTok && !mbar_wait_or_stop(&s.v_clean, 0, stop, kWaitLimit)) return false;
+                tc_fence_after();
+                const uint32_t va = smem_addr(v_op + st * kOperand);
+#pragma unroll
+                for (int k = 0; k < kTileTok / 16; ++k)   // 16 tokens: 8 columns of P, 2048 bytes of V rows
+                    mma_ts(tm_o + 128 * w, tm_s + 128 * w + 8 * k, smem_operand(va + 2048 * k, kHalfOperand, 1024), kPv,
+                           i >= 2 || k > 0);
+                if (last_use(i)) mma_commit(&s.v_empty[st]);
+                if (i + 2 >= steps) mma_commit(&s.o_full[w]);
+                return true;
+            };
+            ok = qk(0);
+            if (ok && steps > 1) ok = qk(1);
+            for (int i = 0; i < steps && ok; ++i) {
+                ok = pv(i);
+                if (ok && i + 2 < steps) ok = qk(i + 2);
+            }
+            // products in flight end before the operands and tensor memory go
+            mma_commit(&s.drained);
+            if (!mbar_wait_bounded(&s.drained, 0, kWaitLimit)) *stop = 1;
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------- softmax
+        const int w = warp >> 2;                                  // stream
+        const int r = (MODE == 0 ? w * kPRows : 0) + (warp & 3) * 32 + lane;
+        const int row = row0 + r;
+        const bool real = row < R;
+        const int len = real ? prefix_len(a.lens, row / a.G, max_len) : 0;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t my_s = tm_s + 128 * w + lanes, my_o = tm_o + 128 * w + lanes;
+        const float scale = a.sm_scale * kLog2e;
+        float m = -INFINITY, l = 0.f;                             // m in units of the raw score
+        const int items = steps > w ? (steps - w + 1) / 2 : 0;
+        bool ok = true;
+        for (int j = 0; j < items; ++j) {
+            const int t = t_beg + (MODE == 0 ? j : 2 * j + w);
+            ok = __all_sync(kFull, mbar_wait_or_stop(&s.s_full[w], j & 1, stop, kWaitLimit));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t x[kTileTok];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(my_s + 32 * c, x + 32 * c);
+            tmem_wait_ld();
+            const int shown = len - t * kTileTok;                 // tokens of the tile this row sees
+            if (__any_sync(kFull, shown < kTileTok)) {
+#pragma unroll
+                for (int i = 0; i < kTileTok; ++i)
+                    if (i >= shown) x[i] = 0xff800000u;           // -inf
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < kTileTok; i += 2)
+                mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // the reference grows only past 2^8 of what is there (from -inf: at once)
+            const bool grow = (top - m) * scale > 8.f || (m == -INFINITY && top > -INFINITY);
+            const float m_new = grow ? top : m;
+            if (j > 0 && __any_sync(kFull, grow)) {
+                const float f = (m == -INFINITY || !grow) ? 1.f : ex2((m - m_new) * scale);
+                l *= f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(my_o + 32 * c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st32(my_o + 32 * c, o);
+                }
+            }
+            m = m_new;
+            const float off = m == -INFINITY ? 0.f : m * scale;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kTileTok; i += 2) {
+                const float p0 = ex2(fmaf(__uint_as_float(x[i]), scale, -off)), p1 = ex2(fmaf(__uint_as_float(x[i + 1]), scale, -off));
+                sum[(i >> 1) & 3] += p0 + p1;
+                const __nv_bfloat162 p = __floats2bfloat162_rn(p0, p1);
+                x[i >> 1] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st32(my_s, x);
+            tmem_st32(my_s + 32, x + 32);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&s.p_ready[w]);
+        }
+        // ---- this stream's (m, l, O)
+        if (items > 0 && ok) {
+            ok = __all_sync(kFull, mbar_wait_or_stop(&s.o_full[w], 0, stop, kWaitLimit));
+            tc_fence_after();
+        }
+        if (ok) {
+            const int slot = MODE == 0 ? blockIdx.x : 2 * blockIdx.x + w;
+            const int64_t gw = (int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G;
+            float* p = a.partials + ((int64_t)slot * a.batch * a.n_q + gw) * kPartialStride;
+            if (real) *reinterpret_cast<float2*>(p) = make_float2(m == -INFINITY ? m : m * scale, l);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                if (items > 0) {
+                    tmem_ld32(my_o + 32 * c, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0u;
+                }
+                if (real) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<uint4*>(p + 4 + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (tid == 0 && *stop) raise_error(a.err, KVARN_DEVERR_WAIT_TIMEOUT);
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_free(tm, 512);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+namespace {
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once (a host function: the same for every device).
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return (EncodeTiled)p;
+    }();
+    return fn;
+}
+
+template <int B, int MODE>
+cudaError_t launch_mode(const CUtensorMap& map, const PrefixArgs& p, cudaStream_t st) {
+    constexpr int rows = MODE == 0 ? 2 * kPRows : kPRows;
+    static bool ready[64];
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess) return e;
+    if (d < 0 || d >= 64) return cudaErrorInvalidDevice;
+    if (!ready[d]) {
+        e = cudaFuncSetAttribute(prefix_bf16_kernel<B, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)bf16_prefix_smem(MODE));
+        if (e != cudaSuccess) return e;
+        ready[d] = true;
+    }
+    const dim3 grid(p.splits, (p.batch * p.G + rows - 1) / rows, p.n_kv);
+    return launch_pdl(prefix_bf16_kernel<B, MODE>, grid, 320, bf16_prefix_smem(MODE), st, map, p);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_bf16(const PrefixArgs& p, int block_size, cudaStream_t st) {
+    const EncodeTiled enc = encode_tiled();
+    if (!enc) return cudaErrorNotSupported;
+    CUtensorMap map;
+    const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)p.n_pool_blocks * p.n_kv * 2 * block_size};
+    const cuuint64_t strides[1] = {kD * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)block_size}, one[2] = {1, 1};
+    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t*>(p.pool), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    const int64_t R = (int64_t)p.batch * p.G;
+    const int mode = p.q_dtype == KVARN_FP32 ? 2 : (R > kPRows ? 0 : 1);
+    if (block_size == 32)
+        return mode == 0 ? launch_mode<32, 0>(map, p, st) : (mode == 1 ? launch_mode<32, 1>(map, p, st) : launch_mode<32, 2>(map, p, st));
+    return mode == 0 ? launch_mode<64, 0>(map, p, st) : (mode == 1 ? launch_mode<64, 1>(map, p, st) : launch_mode<64, 2>(map, p, st));
+}
+
+}  // namespace kvarn
