@@ -12,7 +12,6 @@
 // which also rotates back and adds the raw tail rows (packed cache).
 #include "host_checks.h"
 #include "prefix.cuh"
-#include "quantize.cuh"
 
 namespace kvarn {
 
@@ -26,6 +25,7 @@ cudaError_t launch_decode_split_bf16(const kvarn_config& cfg, const void* q, int
                                      AttnArgs* args, cudaStream_t st);
 
 cudaError_t launch_prefix_bf16(const PrefixArgs& p, int block_size, cudaStream_t st);
+cudaError_t launch_prefix_packed(const kvarn_config& c, const PrefixArgs& p, cudaStream_t st);
 
 struct PrefixMerge {
     const float* partials;
@@ -35,115 +35,6 @@ struct PrefixMerge {
     void* out;
     int out_bf16;
 };
-
-// ---------------------------------------------------------------- prefix kernel
-constexpr int kRowTile = 16, kTokTile = 32;
-
-// grid (splits, row tiles, n_kv), 128 threads: 16 query rows against the
-// split's token range, 32 tokens at a time in shared memory, all in fp32.
-template <int B, int BITS>
-__global__ void __launch_bounds__(128) prefix_kernel(PrefixArgs a) {
-    wait_prior_grids();
-    constexpr int HB = head_block_bytes(B, BITS);
-    __shared__ __align__(16) float qs[kRowTile][kD];
-    __shared__ __align__(16) float ks[kTokTile][kD + 4], vs[kTokTile][kD + 4];
-    __shared__ float ps[kRowTile][kTokTile];
-    __shared__ float mrow[kRowTile], lrow[kRowTile], frow[kRowTile];
-    __shared__ int len[kRowTile];
-    __shared__ __align__(16) uint8_t img[2][HB];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.z, R = a.batch * a.G, row0 = blockIdx.y * kRowTile;
-    const int most = prefix_most(a, a.n_blocks * B, lane);
-    const int tiles = (most + kTokTile - 1) / kTokTile;
-    const int t_beg = (int)((int64_t)tiles * blockIdx.x / a.splits), t_end = (int)((int64_t)tiles * (blockIdx.x + 1) / a.splits);
-    for (int r = warp; r < kRowTile; r += 4) {
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        const int row = row0 + r;
-        if (row < R) {
-            load_q4(a.q, a.q_dtype, (int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G, lane, v);
-            if (!(a.flags & KVARN_FLAG_NO_ROTATION)) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] *= sign_of4(a.sb[0], a.sb[1], a.sb[2], a.sb[3], 4 * lane + k);
-                fwht128(v, lane);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] *= kInvSqrtD;
-            }
-        }
-        const float s = a.sm_scale * kLog2e;
-        *reinterpret_cast<float4*>(&qs[r][4 * lane]) = make_float4(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
-        if (lane == 0) {
-            len[r] = row < R ? prefix_len(a.lens, row / a.G, a.n_blocks * B) : 0;
-            mrow[r] = -INFINITY;
-            lrow[r] = 0.f;
-        }
-    }
-    float acc[kRowTile];
-#pragma unroll
-    for (int r = 0; r < kRowTile; ++r) acc[r] = 0.f;
-    for (int t = t_beg; t < t_end; ++t) {
-        __syncthreads();
-        const int blk = t * kTokTile / B, sub = t * kTokTile % B;
-        int64_t phys = a.table[blk];
-        const bool ok = phys >= 0 && phys < a.n_pool_blocks;   // (the same for the whole CTA)
-        if (!ok) {
-            if (tid == 0) raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
-            continue;
-        }
-        for (int kind = 0; kind < 2; ++kind) {
-            const uint4* s4 = reinterpret_cast<const uint4*>(a.pool + phys * a.block_bytes + (int64_t)(2 * h + kind) * HB);
-            for (int i = tid; i < HB / 16; i += 128) reinterpret_cast<uint4*>(img[kind])[i] = s4[i];
-        }
-        __syncthreads();
-        for (int i = warp; i < kTokTile; i += 4) {
-            float v[4];
-            dequant_row4<B, BITS>(img[0], KVARN_KIND_K, sub + i, lane, v);
-            *reinterpret_cast<float4*>(&ks[i][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
-            dequant_row4<B, BITS>(img[1], KVARN_KIND_V, sub + i, lane, v);
-            *reinterpret_cast<float4*>(&vs[i][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
-        }
-        __syncthreads();
-        for (int r = warp; r < kRowTile; r += 4) {   // lane: token
-            float s = 0.f;
-            for (int c = 0; c < kD; c += 4) {
-                const float4 q4 = *reinterpret_cast<const float4*>(&qs[r][c]), k4 = *reinterpret_cast<const float4*>(&ks[lane][c]);
-                s = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s))));
-            }
-            if (t * kTokTile + lane >= len[r]) s = -INFINITY;
-            const float m0 = mrow[r], m1 = fmaxf(m0, warp_max(s));
-            const float f = m0 == -INFINITY ? 0.f : exp2f(m0 - m1);
-            const float p = s == -INFINITY ? 0.f : exp2f(s - m1);
-            const float sum = warp_sum(p);
-            ps[r][lane] = p;
-            __syncwarp();
-            if (lane == 0) {
-                mrow[r] = m1;
-                frow[r] = f;
-                lrow[r] = lrow[r] * f + sum;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < kRowTile; ++r) {
-            float s = acc[r] * frow[r];
-            for (int i = 0; i < kTokTile; ++i) s = fmaf(ps[r][i], vs[i][tid], s);
-            acc[r] = s;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kRowTile; ++r) {
-        const int row = row0 + r;
-        if (row < R) {
-            const int64_t gw = (int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G;
-            float* p = a.partials + ((int64_t)blockIdx.x * a.batch * a.n_q + gw) * kPartialStride;
-            if (tid == 0) {
-                p[0] = mrow[r];
-                p[1] = lrow[r];
-            }
-            p[4 + tid] = acc[r];
-        }
-    }
-}
 
 // ---------------------------------------------------------------- merge
 // One CTA of kWideWarps warps per (sequence, query head): each warp merges its
@@ -234,8 +125,8 @@ namespace {
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // How the prefix kernel is cut: query rows of a CTA, token ranges (splits) and
-// partials per range (bf16 pages with one row tile: one each from the even and
-// the odd K/V tiles).
+// partials per range (2 for one row tile over bf16 pages, where the even and
+// the odd K/V tiles of a range are summed apart).
 struct PrefixPlan {
     int rows, streams, splits;
 };
@@ -290,7 +181,7 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
         return KVARN_ERR_INVALID_ARG;
     const int G = c.n_q_heads / c.n_kv_heads;
     if (!PACKED && n_pool_blocks > 0x7fffffff / ((int64_t)c.n_kv_heads * 2 * c.block_size)) return KVARN_ERR_INVALID_ARG;
-    if (((int64_t)batch * G + kRowTile - 1) / kRowTile > 65535 || c.n_kv_heads > 65535) return KVARN_ERR_INVALID_ARG;
+    if (((int64_t)batch * G + kPRows - 1) / kPRows > 65535 || c.n_kv_heads > 65535) return KVARN_ERR_INVALID_ARG;
     const size_t need = prefix_ws_bytes(c, batch, prefix_blocks);
     if (need == 0) return KVARN_ERR_CUDA;
     if (workspace_bytes < need) return KVARN_ERR_WORKSPACE;
@@ -322,10 +213,7 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
     cudaError_t e;
     AttnArgs a;
     if constexpr (PACKED) {
-        const dim3 grid(p.splits, (batch * G + kRowTile - 1) / kRowTile, c.n_kv_heads);
-        e = dispatch(c, [&](auto b, auto w) {
-            return launch_pdl(prefix_kernel<decltype(b)::value, decltype(w)::value>, grid, 128, 0, st, p);
-        });
+        e = launch_prefix_packed(c, p, st);
         if (e == cudaSuccess)
             e = launch_decode_split(c, q, q_dtype, pool, n_pool_blocks, p.block_bytes, staging, block_table, max_blocks,
                                     seq_lens, batch, nullptr, workspace, nw, &a, st);

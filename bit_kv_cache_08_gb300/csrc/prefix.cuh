@@ -49,4 +49,97 @@ __device__ __forceinline__ float ex2(float x) {
 // within its 64-element column block.
 __device__ __forceinline__ uint32_t swizzled(int r, int u) { return (uint32_t)(r * 128 + ((u ^ (r & 7)) << 4)); }
 
+// One thread's row of an online softmax (everything in the log2 domain): the
+// reference m that P and O are relative to, and the sum l.
+struct RowState {
+    float m, l;
+};
+
+// The softmax of a TOK-token tile by the 128 threads of a stream, a row each:
+// reads S (fp32) at my_s, writes P (16-bit, HALF: fp16, else bf16) over it,
+// and rescales O at my_o. A weight is 2^(scale s + bias - m + lift): bias is
+// the tile's value exponent (V is stored times 2^-bias), lift a constant that
+// keeps small fp16 weights out of the subnormals. The reference grows only
+// past 2^8 of what is there, so P stays within 2^(8 + lift) and O is seldom
+// touched; o_idle() waits until no product writes O (false: gave up).
+// `shown`: tokens of the tile that this row sees. The caller waits for S
+// before and signals P after.
+template <int TOK, bool HALF, typename Idle>
+__device__ __forceinline__ bool softmax_tile(uint32_t my_s, uint32_t my_o, int shown, float scale, float bias, float unbias,
+                                             float lift, bool first, RowState& st, Idle&& o_idle) {
+    uint32_t x[TOK];
+#pragma unroll
+    for (int c = 0; c < TOK; c += 32) tmem_ld32(my_s + c, x + c);
+    tmem_wait_ld();
+    if (__any_sync(kFull, shown < TOK)) {
+#pragma unroll
+        for (int i = 0; i < TOK; ++i)
+            if (i >= shown) x[i] = 0xff800000u;   // -inf, whatever was there
+    }
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < TOK; i += 2)
+        mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+    const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), scale, bias);
+    const bool grow = top - st.m > 8.f;            // (from -inf at once; false where nothing is shown)
+    if (!first && __any_sync(kFull, grow)) {
+        if (!o_idle()) return false;
+        const float f = grow && st.m != -INFINITY ? ex2(st.m - top) : 1.f;
+        st.l *= f;
+#pragma unroll
+        for (int c = 0; c < kD; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(my_o + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(my_o + c, o);
+        }
+    }
+    if (grow) st.m = top;
+    const float off = st.m == -INFINITY ? 0.f : bias + lift - st.m;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < TOK; i += 2) {
+        const float p0 = ex2(fmaf(__uint_as_float(x[i]), scale, off)), p1 = ex2(fmaf(__uint_as_float(x[i + 1]), scale, off));
+        sum[(i >> 1) & 3] += p0 + p1;
+        if (HALF) {
+            x[i >> 1] = pack_h2(p0, p1);
+        } else {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(p0, p1);
+            x[i >> 1] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+    }
+    st.l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * unbias;
+#pragma unroll
+    for (int c = 0; c < TOK / 2; c += 32) tmem_st32(my_s + c, x + c);
+    tmem_wait_st();
+    return true;
+}
+
+// This thread's row of a stream's result as the merge's partial (slot, row):
+// m (log2 domain), l and O; an empty stream's O is zero.
+__device__ __forceinline__ void store_partial(const PrefixArgs& a, int slot, int row, int h, bool real, bool empty, float m,
+                                              float l, uint32_t my_o) {
+    const int64_t gw = (int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G;
+    float* p = a.partials + ((int64_t)slot * a.batch * a.n_q + gw) * kPartialStride;
+    if (real) *reinterpret_cast<float2*>(p) = make_float2(m, l);
+#pragma unroll
+    for (int c = 0; c < kD; c += 32) {
+        uint32_t o[32];
+        if (empty) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+        } else {
+            tmem_ld32(my_o + c, o);
+            tmem_wait_ld();
+        }
+        if (real) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<uint4*>(p + 4 + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        }
+    }
+}
+
 }  // namespace kvarn

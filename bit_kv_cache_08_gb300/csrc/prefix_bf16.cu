@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t my_s = tm_s + 128 * w + lanes, my_o = tm_o + 128 * w + lanes;
         const float scale = a.sm_scale * kLog2e;
-        float m = -INFINITY, l = 0.f;                             // m in units of the raw score
+        RowState st{-INFINITY, 0.f};
         const int items = steps > w ? (steps - w + 1) / 2 : 0;
         bool ok = true;
         for (int j = 0; j < items; ++j) {
@@ -239,81 +239,16 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
             ok = __all_sync(kFull, mbar_wait_or_stop(&s.s_full[w], j & 1, stop, kWaitLimit));
             if (!ok) break;
             tc_fence_after();
-            uint32_t x[kTileTok];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(my_s + 32 * c, x + 32 * c);
-            tmem_wait_ld();
-            const int shown = len - t * kTileTok;                 // tokens of the tile this row sees
-            if (__any_sync(kFull, shown < kTileTok)) {
-#pragma unroll
-                for (int i = 0; i < kTileTok; ++i)
-                    if (i >= shown) x[i] = 0xff800000u;           // -inf
-            }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < kTileTok; i += 2)
-                mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            // the reference grows only past 2^8 of what is there (from -inf: at once)
-            const bool grow = (top - m) * scale > 8.f || (m == -INFINITY && top > -INFINITY);
-            const float m_new = grow ? top : m;
-            if (j > 0 && __any_sync(kFull, grow)) {
-                const float f = (m == -INFINITY || !grow) ? 1.f : ex2((m - m_new) * scale);
-                l *= f;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(my_o + 32 * c, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                    tmem_st32(my_o + 32 * c, o);
-                }
-            }
-            m = m_new;
-            const float off = m == -INFINITY ? 0.f : m * scale;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < kTileTok; i += 2) {
-                const float p0 = ex2(fmaf(__uint_as_float(x[i]), scale, -off)), p1 = ex2(fmaf(__uint_as_float(x[i + 1]), scale, -off));
-                sum[(i >> 1) & 3] += p0 + p1;
-                const __nv_bfloat162 p = __floats2bfloat162_rn(p0, p1);
-                x[i >> 1] = *reinterpret_cast<const uint32_t*>(&p);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st32(my_s, x);
-            tmem_st32(my_s + 32, x + 32);
-            tmem_wait_st();
+            // (the products that S waited for include the last one into O)
+            softmax_tile<kTileTok, false>(my_s, my_o, len - t * kTileTok, scale, 0.f, 1.f, 0.f, j == 0, st, [] { return true; });
             tc_fence_before();
             mbar_arrive(&s.p_ready[w]);
         }
-        // ---- this stream's (m, l, O)
         if (items > 0 && ok) {
             ok = __all_sync(kFull, mbar_wait_or_stop(&s.o_full[w], 0, stop, kWaitLimit));
             tc_fence_after();
         }
-        if (ok) {
-            const int slot = MODE == 0 ? blockIdx.x : 2 * blockIdx.x + w;
-            const int64_t gw = (int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G;
-            float* p = a.partials + ((int64_t)slot * a.batch * a.n_q + gw) * kPartialStride;
-            if (real) *reinterpret_cast<float2*>(p) = make_float2(m == -INFINITY ? m : m * scale, l);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                if (items > 0) {
-                    tmem_ld32(my_o + 32 * c, o);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0u;
-                }
-                if (real) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<uint4*>(p + 4 + 32 * c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                }
-            }
-        }
+        if (ok) store_partial(a, MODE == 0 ? blockIdx.x : 2 * blockIdx.x + w, row, h, real, items == 0, st.m, st.l, my_o);
         tc_fence_before();
     }
     __syncthreads();

@@ -1,0 +1,455 @@
+// prefix_packed.cu -- the shared prefix over the packed cache on the tensor
+// cores: each 64-token tile of codes is turned into 16-bit operands once and
+// multiplied with 128 query rows.
+//
+// Everything runs in the rotated space (the query rows are rotated here, the
+// merge rotates back). Per kv head and 128 of its batch * G query rows, over
+// the CTA's range of 64-token tiles:
+//   S = Q K'^T (128 x 64, fp32)   K' = (code s + z) R C and Q are each split
+//       into two bf16 halves, and three products (hi hi, hi lo, lo hi) keep
+//       2^-16 of each factor: a score is exponentiated, so its error must not
+//       grow with the size of the scores
+//   P = 2^(S - m), O += P V'      one fp16 product (2^-11 each): V' is
+//       (code s + z) R C 2^-e, the tile's exponent e making its largest value
+//       at most 1; e enters the exponent of P, so P V' needs no other scale
+// Tensor memory: Q as the A operand (hi, lo: 2 x 64 columns), S / P of two
+// tiles in flight (2 x 64), O (128); K' and V' have two stages each, so the
+// products of one tile run while the next is built and the last is weighed.
+//
+// Warps: 0-3 softmax (a row a thread), 4 issues the products, 5-12 build
+// operands (13 warps leave 128 registers a thread; 17 would leave 96): one group's share of a record of the packed format (K: 4
+// tokens x 8 channels, V: 8 tokens x 4 channels) is four whole 16-byte units
+// of the swizzled operand rows, so a lane reads a record's words and writes
+// units.
+#include "prefix.cuh"
+
+#include "host_checks.h"
+#include "quantize.cuh"
+
+namespace kvarn {
+
+constexpr int kPkTok = 64;                       // tokens of a tile
+constexpr int kPkK = kPkTok * kD * 2;            // bytes of one 64 x 128 bf16 operand (two 64-channel blocks)
+constexpr int kPkV = kD * kPkTok * 2;            // 128 channel rows x 64 tokens, fp16
+constexpr int kRawStages = 3;
+constexpr int kBuildWarps = 8, kBuildThreads = 32 * kBuildWarps;
+constexpr int kPackedThreads = 160 + kBuildThreads;
+constexpr float kLift = 7.f;                     // P up to 2^(8 + 7), small weights normal down to 2^-21
+
+struct PackedSmem {
+    uint64_t raw_full[kRawStages], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full, drained;
+    uint32_t tmem;
+    int stop;
+    int vexp[4];                                  // e of the last tiles
+    uint32_t red[2][kBuildWarps], redc[2][kBuildWarps];
+    // per tile parity: (a, b) of every K and V (group, token) so that a value
+    // is (f a + b) C with f = 1 + code 2^-bits; C of the tile's two 32-token halves
+    alignas(16) float2 ab[2][2][4][kPkTok];       // [parity][kind]
+    alignas(16) float c[2][2][2][kD];             // [parity][kind][half]
+};
+
+template <int B, int BITS>
+struct PackedLayout {
+    static constexpr int HB = head_block_bytes(B, BITS);
+    static constexpr int kBlocks = kPkTok / B;                 // blocks per tile
+    static constexpr int kRaw = kBlocks * 2 * HB;              // bytes of a raw tile: (K, V) per block
+    static constexpr int kHeader = (sizeof(PackedSmem) + 1023) / 1024 * 1024;
+    static constexpr size_t bytes = 1024 + kHeader + 4 * kPkK + 2 * kPkV + kRawStages * kRaw;
+};
+
+// 1 + code 2^-BITS: the BITS bits at position p of w in the top of a mantissa.
+template <int BITS>
+__device__ __forceinline__ float unit_code(uint32_t w, int p) {
+    constexpr uint32_t mask = ((1u << BITS) - 1) << (23 - BITS);
+    const int s = 23 - BITS - p;
+    const uint32_t x = s >= 0 ? w << s : w >> -s;
+    return __uint_as_float((x & mask) | 0x3f800000u);
+}
+// The same for 3-bit codes: low two bits at p of w, high bit at ph of hw.
+__device__ __forceinline__ float unit_code3(uint32_t w, int p, uint32_t hw, int ph) {
+    const int s = 20 - p, sh = 22 - ph;
+    const uint32_t x = s >= 0 ? w << s : w >> -s, y = sh >= 0 ? hw << sh : hw >> -sh;
+    return __uint_as_float((x & 0x00300000u) | (y & 0x00400000u) | 0x3f800000u);
+}
+
+// The codes of pair j of a record word (the j-th field of its low and of its
+// high half); for 3-bit codes jh is the pair's place in the high-bit word.
+template <int BITS>
+__device__ __forceinline__ float2 code_pair(uint32_t w, uint32_t hw, int j, int jh) {
+    if constexpr (BITS == 3) return make_float2(unit_code3(w, 2 * j, hw, jh), unit_code3(w, 2 * j + 16, hw, jh + 16));
+    else return make_float2(unit_code<BITS>(w, BITS * j), unit_code<BITS>(w, BITS * j + 16));
+}
+
+template <int B, int BITS>
+__global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(PrefixArgs a) {
+    wait_prior_grids();
+    using Lay = PackedLayout<B, BITS>;
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t* base = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+    PackedSmem& s = *reinterpret_cast<PackedSmem*>(base);
+    uint8_t* k_op = base + Lay::kHeader;          // [stage][hi, lo]
+    uint8_t* v_op = k_op + 4 * kPkK;              // [stage]
+    uint8_t* raw = v_op + 2 * kPkV;               // [raw stage][block][K, V]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.z, R = a.batch * a.G, row0 = blockIdx.y * kPRows;
+    const int max_len = a.n_blocks * B;
+
+    const int most = prefix_most(a, max_len, lane);
+    const int tiles = (most + kPkTok - 1) / kPkTok;
+    const int t_beg = (int)((int64_t)tiles * blockIdx.x / a.splits), t_end = (int)((int64_t)tiles * (blockIdx.x + 1) / a.splits);
+    const int n = t_end - t_beg;
+
+    if (tid == 0) {
+        s.stop = 0;
+        for (int i = 0; i < kRawStages; ++i) mbar_init(&s.raw_full[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.k_full[i], kBuildThreads);
+            mbar_init(&s.k_empty[i], 1);
+            mbar_init(&s.v_full[i], kBuildThreads);
+            mbar_init(&s.v_empty[i], 1);
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.p_ready[i], 128);
+        }
+        mbar_init(&s.o_full, 1);
+        mbar_init(&s.drained, 1);
+        fence_mbar_init();
+    }
+    if (warp == 4) tmem_alloc(&s.tmem, 512);
+    // ---- query rows: rotated, split into two bf16 halves, row by row through
+    // shared memory (pitch 272 bytes) into tensor memory
+    constexpr int kPitch = 272;
+    uint8_t* q_hi = k_op;
+    uint8_t* q_lo = k_op + kPRows * kPitch;
+    static_assert(2 * kPRows * kPitch <= 4 * kPkK + 2 * kPkV, "query staging fits the operand stages");
+    for (int r = warp; r < kPRows; r += kPackedThreads / 32) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        const int row = row0 + r;
+        if (row < R) {
+            load_q4(a.q, a.q_dtype, (int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G, lane, v);
+            if (!(a.flags & KVARN_FLAG_NO_ROTATION)) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] *= sign_of4(a.sb[0], a.sb[1], a.sb[2], a.sb[3], 4 * lane + k);
+                fwht128(v, lane);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] *= kInvSqrtD;
+            }
+        }
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+            const float2 xf = __bfloat1622float2(x);
+            const __nv_bfloat162 y = __floats2bfloat162_rn(v[2 * k] - xf.x, v[2 * k + 1] - xf.y);
+            hi[k] = *reinterpret_cast<const uint32_t*>(&x);
+            lo[k] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        *reinterpret_cast<uint2*>(q_hi + r * kPitch + 8 * lane) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(q_lo + r * kPitch + 8 * lane) = make_uint2(lo[0], lo[1]);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = s.tmem;
+    volatile int* stop = &s.stop;
+    const uint32_t tm_q = tm, tm_s = tm + 128, tm_o = tm + 256;   // S of tile i at + 64 (i % 2)
+    if (warp < 4) {
+        const int r = warp * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const uint8_t* src = (c < 4 ? q_hi : q_lo) + r * kPitch + (c & 3) * 64;
+            uint32_t x[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 u = *reinterpret_cast<const uint4*>(src + 16 * i);
+                x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
+            }
+            tmem_st16(tm_q + 16 * c + lanes, x);
+        }
+        tmem_wait_st();
+    }
+    tc_fence_before();
+    __syncthreads();   // (the staging is free for operands)
+    tc_fence_after();
+
+    if (warp > 4) {
+        // ---------------------------------------------------------- operands from codes
+        const int bt = tid - 160, bw = warp - 5;
+        const int used = (most + B - 1) / B;      // blocks that hold a visible token
+        // thread 0 keeps the raw tiles coming
+        auto fetch = [&](int i) {
+            const int st = i % kRawStages, b0 = (t_beg + i) * Lay::kBlocks;
+            int64_t page[Lay::kBlocks];
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int x = 0; x < Lay::kBlocks; ++x) {
+                page[x] = b0 + x < used ? a.table[b0 + x] : -1;
+                if (b0 + x < used && (page[x] < 0 || page[x] >= a.n_pool_blocks)) {
+                    raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
+                    page[x] = -1;
+                }
+                if (page[x] >= 0) bytes += 2 * Lay::HB;
+            }
+            fence_async_smem();
+            mbar_arrive_expect_tx(&s.raw_full[st], bytes);
+#pragma unroll
+            for (int x = 0; x < Lay::kBlocks; ++x)
+                if (page[x] >= 0)
+                    bulk_g2s(raw + st * Lay::kRaw + x * 2 * Lay::HB, a.pool + page[x] * a.block_bytes + (int64_t)(2 * h) * Lay::HB,
+                             2 * Lay::HB, &s.raw_full[st]);
+        };
+        int fetched = 0;
+        if (bt == 0)
+            for (; fetched < kRawStages && fetched < n; ++fetched) fetch(fetched);
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int st = i % kRawStages, par = i & 1;
+            if (ok) ok = mbar_wait_or_stop(&s.raw_full[st], (i / kRawStages) & 1, stop, kWaitLimit);
+            const uint8_t* tile = raw + st * Lay::kRaw;
+            // ---- (a, b) of thread bt's (group, token), C, and the tile's largest value
+            {
+                const int g = bt >> 6, t = bt & 63, x = t / B, tb = t % B;
+                const bool there = (t_beg + i) * Lay::kBlocks + x < used;
+                float vmax = 0.f, cmax = 0.f;
+#pragma unroll
+                for (int kind = 0; kind < 2; ++kind) {
+                    const uint8_t* hb = tile + x * 2 * Lay::HB + kind * Lay::HB;
+                    const float step = h2f(reinterpret_cast<const uint16_t*>(hb + off_s(B, BITS))[g * B + tb]);
+                    const float zero = h2f(reinterpret_cast<const uint16_t*>(hb + off_z(B, BITS))[g * B + tb]);
+                    const float fac = h2f(reinterpret_cast<const uint16_t*>(hb + off_R(B, BITS))[tb]);
+                    constexpr float kSpan = (float)(1 << BITS);
+                    const float wide = step * kSpan;
+                    s.ab[par][kind][g][t] = there ? make_float2(wide * fac, (zero - wide) * fac) : make_float2(0.f, 0.f);
+                    if (kind == 1 && there) vmax = fmaxf(fabsf(zero), fabsf(fmaf(step, kSpan - 1.f, zero))) * fac;
+                }
+                // C: thread bt takes channel bt % 128 of half bt / 128, K and V
+                const int half = bt >> 7, ch = bt & 127, xc = half * 32 / B;
+                const bool has = (t_beg + i) * Lay::kBlocks + xc < used;
+#pragma unroll
+                for (int kind = 0; kind < 2; ++kind) {
+                    const uint8_t* hb = tile + xc * 2 * Lay::HB + kind * Lay::HB;
+                    const float cf = has ? h2f(reinterpret_cast<const uint16_t*>(hb + off_C(B, BITS))[ch]) : 0.f;
+                    s.c[par][kind][half][ch] = cf;
+                    if (kind == 1) cmax = fabsf(cf);
+                }
+                const uint32_t rv = __reduce_max_sync(kFull, __float_as_uint(fabsf(vmax)));
+                const uint32_t rc = __reduce_max_sync(kFull, __float_as_uint(cmax));
+                if (lane == 0) {
+                    s.red[par][bw] = rv;
+                    s.redc[par][bw] = rc;
+                }
+            }
+            // one barrier a tile: the tables are ready, and every thread is done with tile i - 1
+            asm volatile("bar.sync 1, %0;" ::"n"(kBuildThreads) : "memory");
+            if (bt == 0 && i > 0 && fetched < n && !*stop) fetch(fetched++);
+            uint32_t rv = 0, rc = 0;
+#pragma unroll
+            for (int k = 0; k < kBuildWarps; ++k) {
+                rv = max(rv, s.red[par][k]);
+                rc = max(rc, s.redc[par][k]);
+            }
+            // 2^e >= the largest |value|; the clamp keeps 2^-e and 2^e finite
+            const float bound = __uint_as_float(rv) * __uint_as_float(rc);
+            const int e = bound > 0x1p-60f ? min(ceil_log2(bound), 100) : -60;
+            const float down = exp2i(-e);
+            // warp bw: group g of the 32 records of half sb, a record a lane
+            const int g = bw & 3, sb = bw >> 2, ra = lane >> 2, rb = lane & 3;
+            const uint8_t* codes = tile + (B == 64 ? 0 : sb) * 2 * Lay::HB + ((B == 64 ? 32 * sb : 0) + lane) * 16 * BITS;
+            // ---- K: 4 tokens 4 ra + k of the half, channels 32 g + 8 rb .. + 7
+            if (i >= 2 && ok) ok = mbar_wait_or_stop(&s.k_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
+            if (ok) {
+                if (bt == 0) s.vexp[i & 3] = e;
+                uint32_t w[4], hw[4];              // token k's word with this group's fields at its low end
+                {
+                    const uint4* src = reinterpret_cast<const uint4*>(codes);
+                    if constexpr (BITS == 4) {     // word 4 k + g
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint4 u = src[k];
+                            w[k] = g == 0 ? u.x : g == 1 ? u.y : g == 2 ? u.z : u.w;
+                        }
+                    } else {                       // word 2 k + g / 2, fields 4 (g % 2) ..
+                        const uint4 u = src[0], v = src[1];
+                        w[0] = (g & 2 ? u.y : u.x) >> 8 * (g & 1);
+                        w[1] = (g & 2 ? u.w : u.z) >> 8 * (g & 1);
+                        w[2] = (g & 2 ? v.y : v.x) >> 8 * (g & 1);
+                        w[3] = (g & 2 ? v.w : v.z) >> 8 * (g & 1);
+                        if constexpr (BITS == 3) { // high bits in word 8 + k from bit 4 g
+                            const uint4 x = src[2];
+                            hw[0] = x.x >> 4 * g; hw[1] = x.y >> 4 * g; hw[2] = x.z >> 4 * g; hw[3] = x.w >> 4 * g;
+                        }
+                    }
+                }
+                float2 cc[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) cc[k] = *reinterpret_cast<const float2*>(&s.c[par][0][sb][32 * g + 8 * rb + 2 * k]);
+                uint8_t* dst = k_op + par * 2 * kPkK + (g >> 1) * (kPkK / 2);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int t = 32 * sb + 4 * ra + k;
+                    const float2 ab = s.ab[par][0][g][t];
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const float2 f = code_pair<BITS>(w[k], hw[k], p, p);
+                        const float2 y = __fmul2_rn(__ffma2_rn(f, make_float2(ab.x, ab.x), make_float2(ab.y, ab.y)), cc[p]);
+                        const __nv_bfloat162 yh = __floats2bfloat162_rn(y.x, y.y);
+                        const float2 yf = __bfloat1622float2(yh);
+                        const __nv_bfloat162 yl = __floats2bfloat162_rn(y.x - yf.x, y.y - yf.y);
+                        hi[p] = *reinterpret_cast<const uint32_t*>(&yh);
+                        lo[p] = *reinterpret_cast<const uint32_t*>(&yl);
+                    }
+                    const uint32_t at = swizzled(t, 4 * (g & 1) + rb);
+                    *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(dst + kPkK + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_async_smem();
+                mbar_arrive(&s.k_full[par]);
+            }
+            // ---- V: channels 32 g + 4 ra + k, 8 tokens 8 rb .. + 7 of the half
+            if (i >= 2 && ok) ok = mbar_wait_or_stop(&s.v_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
+            if (ok) {
+                uint32_t w[4], hw = 0;             // 4-bit: word 4 g + k; else 2 g + k / 2, and its high bits in word 8 + g
+                if constexpr (BITS == 4) {
+                    const uint4 u = reinterpret_cast<const uint4*>(codes + Lay::HB)[g];
+                    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+                } else {
+                    const uint2 u = reinterpret_cast<const uint2*>(codes + Lay::HB)[g];
+                    w[0] = w[1] = u.x;
+                    w[2] = w[3] = u.y;
+                    if constexpr (BITS == 3) hw = reinterpret_cast<const uint32_t*>(codes + Lay::HB)[8 + g];
+                }
+                float2 ab[8];
+#pragma unroll
+                for (int d = 0; d < 8; ++d) ab[d] = s.ab[par][1][g][32 * sb + 8 * rb + d];
+                uint8_t* dst = v_op + par * kPkV;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int ch = 32 * g + 4 * ra + k;
+                    const float cf = s.c[par][1][sb][ch] * down;
+                    uint32_t out[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {                 // tokens 2p, 2p + 1
+                        const int j = BITS == 4 ? p : 4 * (p >> 1) + 2 * (p & 1) + (k & 1);
+                        const float2 f = code_pair<BITS>(w[k], hw, j, 8 * (k >> 1) + j);
+                        const float2 y = __fmul2_rn(__ffma2_rn(f, make_float2(ab[2 * p].x, ab[2 * p + 1].x),
+                                                               make_float2(ab[2 * p].y, ab[2 * p + 1].y)),
+                                                    make_float2(cf, cf));
+                        out[p] = pack_h2(y.x, y.y);
+                    }
+                    *reinterpret_cast<uint4*>(dst + swizzled(ch, 4 * sb + rb)) = make_uint4(out[0], out[1], out[2], out[3]);
+                }
+                fence_async_smem();
+                mbar_arrive(&s.v_full[par]);
+            }
+        }
+        // copies in flight land before the CTA ends
+        if (bt == 0 && *stop)
+            for (int i = max(0, fetched - kRawStages); i < fetched; ++i)
+                mbar_wait_bounded(&s.raw_full[i % kRawStages], (i / kRawStages) & 1, kWaitLimit);
+    } else if (warp == 4) {
+        // ---------------------------------------------------------- products
+        if (lane == 0 && n > 0) {
+            constexpr uint32_t kQk = mma_shape(kMmaBf16, kPkTok, false), kPv = mma_shape(kMmaF16, kD, false);
+            auto qk = [&](int i) {
+                const int w = i & 1;
+                if (!mbar_wait_or_stop(&s.k_full[w], (i >> 1) & 1, stop, kWaitLimit)) return false;
+                tc_fence_after();
+                const uint32_t ka = smem_addr(k_op + w * 2 * kPkK);
+#pragma unroll
+                for (int part = 0; part < 3; ++part) {            // hi hi, hi lo, lo hi
+                    const uint32_t qa = tm_q + (part == 2 ? 64 : 0), kb = ka + (part == 1 ? kPkK : 0);
+#pragma unroll
+                    for (int k = 0; k < kD / 16; ++k)
+                        mma_ts(tm_s + 64 * w, qa + 8 * k, smem_operand(kb + (k >> 2) * (kPkK / 2) + (k & 3) * 32, 16, 1024), kQk,
+                               part > 0 || k > 0);
+                }
+                mma_commit(&s.s_full[w]);
+                mma_commit(&s.k_empty[w]);
+                return true;
+            };
+            auto pv = [&](int i) {
+                const int w = i & 1;
+                if (!mbar_wait_or_stop(&s.p_ready[w], (i >> 1) & 1, stop, kWaitLimit)) return false;
+                if (!mbar_wait_or_stop(&s.v_full[w], (i >> 1) & 1, stop, kWaitLimit)) return false;
+                tc_fence_after();
+                const uint32_t va = smem_addr(v_op + w * kPkV);
+#pragma unroll
+                for (int k = 0; k < kPkTok / 16; ++k)
+                    mma_ts(tm_o, tm_s + 64 * w + 8 * k, smem_operand(va + 32 * k, 16, 1024), kPv, i > 0 || k > 0);
+                mma_commit(&s.v_empty[w]);
+                if (i + 1 == n) mma_commit(&s.o_full);
+                return true;
+            };
+            bool ok = qk(0);
+            if (ok && n > 1) ok = qk(1);
+            for (int i = 0; i < n && ok; ++i) {
+                ok = pv(i);
+                if (ok && i + 2 < n) ok = qk(i + 2);
+            }
+            // products in flight end before the operands and tensor memory go
+            mma_commit(&s.drained);
+            if (!mbar_wait_bounded(&s.drained, 0, kWaitLimit)) *stop = 1;
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------- softmax
+        const int row = row0 + warp * 32 + lane;
+        const bool real = row < R;
+        const int len = real ? prefix_len(a.lens, row / a.G, max_len) : 0;
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const uint32_t my_o = tm_o + lanes;
+        const float scale = a.sm_scale * kLog2e;
+        RowState st{-INFINITY, 0.f};
+        bool ok = true;
+        for (int i = 0; i < n && ok; ++i) {
+            ok = __all_sync(kFull, mbar_wait_or_stop(&s.s_full[i & 1], (i >> 1) & 1, stop, kWaitLimit));
+            if (!ok) break;
+            tc_fence_after();
+            const int e = *reinterpret_cast<volatile int*>(&s.vexp[i & 3]);
+            // O is idle once tile i - 1's product into it has freed its V stage
+            ok = softmax_tile<kPkTok, true>(tm_s + 64 * (i & 1) + lanes, my_o, len - (t_beg + i) * kPkTok, scale, (float)e,
+                                            exp2i(-e), kLift, i == 0, st, [&] {
+                const bool idle = __all_sync(kFull, mbar_wait_or_stop(&s.v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, stop, kWaitLimit));
+                tc_fence_after();
+                return idle;
+            });
+            tc_fence_before();
+            if (ok) mbar_arrive(&s.p_ready[i & 1]);
+        }
+        if (n > 0 && ok) {
+            ok = __all_sync(kFull, mbar_wait_or_stop(&s.o_full, 0, stop, kWaitLimit));
+            tc_fence_after();
+        }
+        if (ok) store_partial(a, blockIdx.x, row, h, real, n == 0, st.m - kLift, st.l, my_o);
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (tid == 0 && *stop) raise_error(a.err, KVARN_DEVERR_WAIT_TIMEOUT);
+    if (warp == 4) {
+        tc_fence_after();
+        tmem_free(tm, 512);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+cudaError_t launch_prefix_packed(const kvarn_config& c, const PrefixArgs& p, cudaStream_t st) {
+    return dispatch(c, [&](auto b, auto w) {
+        constexpr int B = decltype(b)::value, BITS = decltype(w)::value;
+        constexpr size_t smem = PackedLayout<B, BITS>::bytes;
+        static bool ready[64];
+        int d = 0;
+        cudaError_t e = cudaGetDevice(&d);
+        if (e != cudaSuccess) return e;
+        if (d < 0 || d >= 64) return cudaErrorInvalidDevice;
+        if (!ready[d]) {
+            e = cudaFuncSetAttribute(prefix_packed_kernel<B, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+            ready[d] = true;
+        }
+        const dim3 grid(p.splits, (p.batch * p.G + kPRows - 1) / kPRows, p.n_kv);
+        return launch_pdl(prefix_packed_kernel<B, BITS>, grid, kPackedThreads, smem, st, p);
+    });
+}
+
+}  // namespace kvarn

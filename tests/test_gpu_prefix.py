@@ -8,8 +8,12 @@ product of the low halves (2^-16) left out, so a score is within
 d = 3 * 2^-16 * scale * sum_c |q_c k_c| (and fp32 sums of 128 terms, 2^-17); a
 weight and a value are rounded to fp16 (2^-11 each) and so is the weight in
 the normaliser: the output in the rotated space is within
-(3 * 2^-11 + 2 d) sum p |v| of itself, and an unrotated channel is a sum of 128
-of those over sqrt(128). bf16 cache: scores are fp32 sums of exact products
+(3 * 2^-11 + 2 d) sum p |v| of itself. A tile's values are scaled by the power
+of two over its bound (largest (zero, top level) R times largest C), so small
+ones keep an absolute half step of 2^-25 of at most twice the bound; weights
+are held times 2^7, so one's absolute half step is 2^-32 of the largest, for
+each of the n tokens. An unrotated channel is a sum of 128 of all that over
+sqrt(128). bf16 cache: scores are fp32 sums of exact products
 (d = 2^-17 scale sum |q k|), a weight is rounded to bf16 (2^-8, twice). The
 2^-20 covers the fp32 merge. A bf16 output adds half a step, 2^-8 of itself.
 """
@@ -92,6 +96,14 @@ class Shared:
             assert kv.read_error(ws) == 0
         return out
 
+    def _bound(self, ids, h):
+        """Largest (|zero|, |top level|) R times largest C of the V head-blocks."""
+        hb = self.kv.head_block_bytes(self.cfg)
+        raw = self.pool[torch.from_numpy(ids.astype(np.int64)).cuda()][:, (2 * h + 1) * hb:(2 * h + 2) * hb].cpu().numpy()
+        top = lambda f: (np.maximum(np.abs(f["z16"]), np.abs(f["z16"] + (2 ** self.bits - 1) * f["s16"]))  # noqa: E731
+                         * f["R16"][:, None]).max() * np.abs(f["C16"]).max()
+        return max([top(oracle.unpack(self.B, 1, np.ascontiguousarray(r), bits=self.bits)) for r in raw] + [0.0])
+
     def _head(self, ids, h):
         if not self.bits:
             t = self.pool[torch.from_numpy(ids.astype(np.int64)).cuda()][:, h].double().cpu().numpy()
@@ -114,6 +126,7 @@ class Shared:
         want, tol = np.zeros((len(seqs), n_q, D)), np.zeros((len(seqs), n_q, D))
         for h in range(n_kv):
             kp, vp = self._head(self.prefix_np, h)
+            bound = self._bound(self.prefix_np, h) if self.bits else 0.0
             for i, b in enumerate(seqs):
                 L, P = self.lens[b], prefix_lens[b]
                 whole = L // B * B if self.bits else L
@@ -137,6 +150,7 @@ class Shared:
                 d = ((3 * 2.0 ** -16 if self.bits else 0) + 2.0 ** -17) * size
                 d = np.minimum(np.expm1(np.minimum(2 * d, 1.0)), 2.0)
                 t = ((3 * 2.0 ** -11 if self.bits else 2 * 2.0 ** -8) + d + 2.0 ** -20) * A
+                t = t + (2.0 ** -24 + P * 2.0 ** -32) * bound
                 if rot:
                     o = o @ H * oracle.sigma(self.sb)
                     t = np.repeat(t.sum(-1, keepdims=True) / math.sqrt(D), D, -1)
