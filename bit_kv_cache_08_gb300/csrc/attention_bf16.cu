@@ -122,6 +122,8 @@ __global__ void __launch_bounds__(32) decode_attn_bf16_kernel(AttnArgs a) {
     float m_run = -INFINITY, l_part = 0.f;
 
     auto unit_setup = [&]() {
+        // the unit map: its first warp here, its last at the flush
+        if (cc.j == 0 && lane == 0) a.unit_map[2 * ((int64_t)cc.b * a.n_kv + cc.h)] = w;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int c = 16 * (i >> 1) + 8 * (i & 1) + 2 * tq;
@@ -146,7 +148,8 @@ __global__ void __launch_bounds__(32) decode_attn_bf16_kernel(AttnArgs a) {
         m_run = -INFINITY;
         l_part = 0.f;
     };
-    auto unit_flush = [&]() {
+    auto unit_flush = [&](bool last) {
+        if (last && lane == 0) a.unit_map[2 * ((int64_t)cc.b * a.n_kv + cc.h) + 1] = w;
         float l = l_part;
         l += __shfl_xor_sync(kFull, l, 4);
         l += __shfl_xor_sync(kFull, l, 8);
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(32) decode_attn_bf16_kernel(AttnArgs a) {
             Cursor nxt = cc;
             cc.b = pb;
             cc.h = ph_;
-            unit_flush();
+            unit_flush(nxt.b != pb || nxt.h != ph_);
             cc = nxt;
             if (x + 1 < s_end) unit_setup();
         }
@@ -285,6 +288,9 @@ cudaError_t launch_decode_split_bf16(const kvarn_config& cfg, const void* q, int
     a.seq_lens = seq_lens;
     a.err = (uint32_t*)workspace;
     a.partials = (float*)((uint8_t*)workspace + kWsHeader);
+    a.unit_map = (int32_t*)((uint8_t*)a.partials + ((size_t)batch * cfg.n_kv_heads + (size_t)nw) *
+                                                       (size_t)(cfg.n_q_heads / cfg.n_kv_heads) * kPartialStride *
+                                                       sizeof(float));
     a.out = out;
     a.n_pool_blocks = n_pool_blocks;
     a.block_bytes = (int64_t)cfg.n_kv_heads * 2 * cfg.block_size * kD * 2;

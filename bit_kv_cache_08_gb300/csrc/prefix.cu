@@ -37,68 +37,121 @@ struct PrefixMerge {
 };
 
 // ---------------------------------------------------------------- merge
-// One CTA of kWideWarps warps per (sequence, query head): each warp merges its
-// share of the own tokens' partials, of the prefix's and of the raw tail rows;
-// warp 0 combines the shares and finishes the row.
+// LSE merge of the partials first .. last - 1 of a row's list (np own ones at
+// p0, pstride apart, then the prefix's at s0, sstride apart), 8 in flight at a
+// time with a running rescale; m, l and acc start at -inf, 0 and 0.
+__device__ __forceinline__ void lse_list(const float* p0, int np, int64_t pstride, const float* s0, int64_t sstride, int first,
+                                         int last, int lane, float& m, float& l, float (&acc)[4]) {
+    constexpr int NB = 8;
+    auto at = [&](int i) { return i < np ? p0 + i * pstride : s0 + (i - np) * sstride; };
+    for (int i0 = first; i0 < last; i0 += NB) {
+        const int cnt = min(NB, last - i0);
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < cnt) ml = __ldcg(reinterpret_cast<const float2*>(at(i0 + lane)));
+        float4 pa[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+            if (i < cnt) pa[i] = __ldcg(reinterpret_cast<const float4*>(at(i0 + i) + 4) + lane);
+        const float bm = warp_max(ml.x);
+        if (bm == -INFINITY) continue;
+        const float mn = fmaxf(m, bm);
+        const float fa = m == -INFINITY ? 0.f : exp2f(m - mn);
+        const float wl = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);
+        l = l * fa + warp_sum(ml.y * wl);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] *= fa;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            if (i < cnt) {
+                const float wgt = __shfl_sync(kFull, wl, i);
+                acc[0] = fmaf(wgt, pa[i].x, acc[0]);
+                acc[1] = fmaf(wgt, pa[i].y, acc[1]);
+                acc[2] = fmaf(wgt, pa[i].z, acc[2]);
+                acc[3] = fmaf(wgt, pa[i].w, acc[3]);
+            }
+        }
+        m = mn;
+    }
+}
+
+// One CTA of 8 warps per (sequence, kv head): 8 / G warps to each of its G
+// query heads (their raw tail rows and tables then meet in L1), each with a
+// share of the row's partials and of the tail rows; the row's first warp
+// combines the shares and finishes the row.
+constexpr int kMergeWarps = 8;
 template <int B, bool ROT>
-__global__ void __launch_bounds__(32 * kWideWarps) prefix_merge_kernel(AttnArgs a, PrefixMerge pm) {
+__global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(AttnArgs a, PrefixMerge pm) {
     wait_prior_grids();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    const int64_t gw = blockIdx.x;
-    __shared__ __align__(16) float slices[kWideWarps][kPartialStride];
-    __shared__ __align__(16) float tails[kWideWarps][kPartialStride];
-    const int b = (int)(gw / a.n_q), h = (int)(gw % a.n_q) / a.G;
+    const int b = blockIdx.x / a.n_kv, h = blockIdx.x % a.n_kv;
+    const int parts = kMergeWarps / a.G, g = wp / parts, part = wp % parts;   // (G = 3: two warps are left over)
+    const bool mine = g < a.G;
+    const int64_t gw = (int64_t)b * a.n_q + h * a.G + (mine ? g : 0);
+    __shared__ __align__(16) float slices[kMergeWarps][kPartialStride];
+    __shared__ __align__(16) float tails[kMergeWarps][kPartialStride];
     const int L = a.seq_lens[b], PL = pm.lens[b];
-    const bool valid = L >= 0 && L <= a.max_blocks * B && PL >= 0 && PL <= pm.max_len;
-    if (!valid) {   // (the same for the whole CTA)
-        if (threadIdx.x == 0) raise_error(a.err, KVARN_DEVERR_POSITION);
-        if (threadIdx.x < kD) {
-            if (pm.out_bf16) static_cast<uint16_t*>(pm.out)[gw * kD + threadIdx.x] = 0x7fc0;
-            else static_cast<float*>(pm.out)[gw * kD + threadIdx.x] = NAN;
-        }
-        return;
-    }
     int np;
     const float* p0;
     merge_locate<B, ROT>(a, gw, lane, np, p0);
-    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const int i0 = np * wp / kWideWarps, i1 = np * (wp + 1) / kWideWarps;
-    const int64_t pstride = (int64_t)a.G * kPartialStride;
-    if (i1 > i0) lse_stream<4>(p0 + i0 * pstride, i1 - i0, pstride, lane, m, l, acc);
-    const int s0 = pm.splits * wp / kWideWarps, s1 = pm.splits * (wp + 1) / kWideWarps;
-    const int64_t sstride = (int64_t)a.batch * a.n_q * kPartialStride;
-    if (PL > 0 && s1 > s0)
-        lse_stream<4>(pm.partials + gw * kPartialStride + s0 * sstride, s1 - s0, sstride, lane, m, l, acc);
-    float tm = -INFINITY, tl = 0.f, tacc[4] = {0.f, 0.f, 0.f, 0.f};
-    if (ROT && wp < L % B) {
-        float qv[4];
-        load_q4(a.q, a.q_dtype, gw, lane, qv);
-        const float qs = a.sm_scale * kLog2e;
+    const bool valid = L >= 0 && L <= a.max_blocks * B && PL >= 0 && PL <= pm.max_len;
+    if (!valid) {   // (the same for the whole CTA)
+        if (threadIdx.x == 0) raise_error(a.err, KVARN_DEVERR_POSITION);
+        for (int i = threadIdx.x; i < a.G * kD; i += 32 * kMergeWarps) {
+            const int64_t at = ((int64_t)b * a.n_q + h * a.G) * kD + i;
+            if (pm.out_bf16) static_cast<uint16_t*>(pm.out)[at] = 0x7fc0;
+            else static_cast<float*>(pm.out)[at] = NAN;
+        }
+        return;
+    }
+    const int ntail = ROT ? L % B : 0;
+    if (mine) {
+        float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+        const int n = np + (PL > 0 ? pm.splits : 0);
+        lse_list(p0, np, (int64_t)a.G * kPartialStride, pm.partials + gw * kPartialStride,
+                 (int64_t)a.batch * a.n_q * kPartialStride, n * part / parts, n * (part + 1) / parts, lane, m, l, acc);
+        if (lane == 0) {
+            slices[wp][0] = m;
+            slices[wp][1] = l;
+        }
+        *reinterpret_cast<float4*>(&slices[wp][4 + 4 * lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        if (ntail > 0) {
+            // this warp's run of the tail rows, 8 at a time, each an LSE slice
+            float qv[4], tm = -INFINITY, tl = 0.f, tacc[4] = {0.f, 0.f, 0.f, 0.f};
+            load_q4(a.q, a.q_dtype, gw, lane, qv);
+            const float qs = a.sm_scale * kLog2e;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) qv[k] *= qs;
-        tail_slice<B, kWideWarps>(a.staging + ((int64_t)b * a.n_kv + h) * 2 * B * kD, L % B, wp, qv, lane, tm, tl, tacc);
+            for (int k = 0; k < 4; ++k) qv[k] *= qs;
+            const uint16_t* kst = a.staging + ((int64_t)b * a.n_kv + h) * 2 * B * kD;
+            const int r1 = ntail * (part + 1) / parts;
+            for (int r0 = ntail * part / parts; r0 < r1; r0 += 8) {
+                float sm = -INFINITY, sl = 0.f, sacc[4] = {0.f, 0.f, 0.f, 0.f};
+                tail_run<B, 8>(kst, r0, min(8, r1 - r0), qv, lane, sm, sl, sacc);
+                const float mn = fmaxf(tm, sm);
+                const float fa = tm == -INFINITY ? 0.f : exp2f(tm - mn), fs = exp2f(sm - mn);
+                tl = tl * fa + sl * fs;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tacc[k] = tacc[k] * fa + sacc[k] * fs;
+                tm = mn;
+            }
+            if (lane == 0) {
+                tails[wp][0] = tm;
+                tails[wp][1] = tl;
+            }
+            *reinterpret_cast<float4*>(&tails[wp][4 + 4 * lane]) = make_float4(tacc[0], tacc[1], tacc[2], tacc[3]);
+        }
     }
-    if (lane == 0) {
-        slices[wp][0] = m;
-        slices[wp][1] = l;
-        tails[wp][0] = tm;
-        tails[wp][1] = tl;
-    }
-    *reinterpret_cast<float4*>(&slices[wp][4 + 4 * lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    *reinterpret_cast<float4*>(&tails[wp][4 + 4 * lane]) = make_float4(tacc[0], tacc[1], tacc[2], tacc[3]);
     __syncthreads();
-    if (wp != 0) return;
-    m = -INFINITY, l = 0.f;
-    acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
-    combine_slices(&slices[0][0], kWideWarps, lane, m, l, acc);
+    if (!mine || part != 0) return;
+    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    combine_slices(&slices[wp][0], parts, lane, m, l, acc);
     if (ROT && !(a.flags & KVARN_FLAG_NO_ROTATION)) {
         fwht128(acc, lane);
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[k] *= kInvSqrtD * sign_of4(a.sb[0], a.sb[1], a.sb[2], a.sb[3], 4 * lane + k);
     }
-    if (ROT && L % B > 0) {
+    if (ntail > 0) {
         float mt = -INFINITY, lt = 0.f, at[4] = {0.f, 0.f, 0.f, 0.f};
-        combine_slices(&tails[0][0], kWideWarps, lane, mt, lt, at);
+        combine_slices(&tails[wp][0], parts, lane, mt, lt, at);
         if (mt != -INFINITY) {
             const float mn = fmaxf(m, mt);
             const float fa = m == -INFINITY ? 0.f : exp2f(m - mn), ft = exp2f(mt - mn);
@@ -225,13 +278,13 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
     }
     if (e != cudaSuccess) return KVARN_ERR_CUDA;
     const PrefixMerge pm{p.partials, prefix_lens, prefix_blocks * c.block_size, plan.splits * plan.streams, out, out_dtype == KVARN_BF16};
-    const unsigned rows = (unsigned)((int64_t)batch * c.n_q_heads);
-    const int threads = 32 * kWideWarps;
+    const unsigned units = (unsigned)((int64_t)batch * c.n_kv_heads);
+    const int threads = 32 * kMergeWarps;
     if constexpr (PACKED)
-        e = c.block_size == 32 ? launch_pdl(prefix_merge_kernel<32, true>, rows, threads, 0, st, a, pm)
-                               : launch_pdl(prefix_merge_kernel<64, true>, rows, threads, 0, st, a, pm);
+        e = c.block_size == 32 ? launch_pdl(prefix_merge_kernel<32, true>, units, threads, 0, st, a, pm)
+                               : launch_pdl(prefix_merge_kernel<64, true>, units, threads, 0, st, a, pm);
     else
-        e = launch_pdl(prefix_merge_kernel<kChunk, false>, rows, threads, 0, st, a, pm);
+        e = launch_pdl(prefix_merge_kernel<kChunk, false>, units, threads, 0, st, a, pm);
     return e == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 

@@ -63,10 +63,10 @@ struct RowState {
 // past 2^8 of what is there, so P stays within 2^(8 + lift) and O is seldom
 // touched; o_idle() waits until no product writes O (false: gave up).
 // `shown`: tokens of the tile that this row sees. The caller waits for S
-// before and signals P after.
+// before; P's arrival is signalled on p_ready.
 template <int TOK, bool HALF, typename Idle>
 __device__ __forceinline__ bool softmax_tile(uint32_t my_s, uint32_t my_o, int shown, float scale, float bias, float unbias,
-                                             float lift, bool first, RowState& st, Idle&& o_idle) {
+                                             float lift, bool first, RowState& st, uint64_t* p_ready, Idle&& o_idle) {
     uint32_t x[TOK];
 #pragma unroll
     for (int c = 0; c < TOK; c += 32) tmem_ld32(my_s + c, x + c);
@@ -78,8 +78,8 @@ __device__ __forceinline__ bool softmax_tile(uint32_t my_s, uint32_t my_o, int s
     }
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < TOK; i += 2)
-        mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+    for (int i = 0; i < TOK; i += 2)   // (three-input maxima)
+        mx[(i >> 1) & 3] = fmaxf(fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), mx[(i >> 1) & 3]);
     const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), scale, bias);
     const bool grow = top - st.m > 8.f;            // (from -inf at once; false where nothing is shown)
     if (!first && __any_sync(kFull, grow)) {
@@ -98,22 +98,26 @@ __device__ __forceinline__ bool softmax_tile(uint32_t my_s, uint32_t my_o, int s
     }
     if (grow) st.m = top;
     const float off = st.m == -INFINITY ? 0.f : bias + lift - st.m;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const float2 scale2 = make_float2(scale, scale), off2 = make_float2(off, off);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int i = 0; i < TOK; i += 2) {
-        const float p0 = ex2(fmaf(__uint_as_float(x[i]), scale, off)), p1 = ex2(fmaf(__uint_as_float(x[i + 1]), scale, off));
-        sum[(i >> 1) & 3] += p0 + p1;
+        const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, off2);
+        const float2 p = make_float2(ex2(y.x), ex2(y.y));
+        sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], p);
         if (HALF) {
-            x[i >> 1] = pack_h2(p0, p1);
+            x[i >> 1] = pack_h2(p.x, p.y);
         } else {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(p0, p1);
-            x[i >> 1] = *reinterpret_cast<const uint32_t*>(&p);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
+            x[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
         }
     }
-    st.l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * unbias;
 #pragma unroll
     for (int c = 0; c < TOK / 2; c += 32) tmem_st32(my_s + c, x + c);
     tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(p_ready);
+    st.l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * unbias;
     return true;
 }
 

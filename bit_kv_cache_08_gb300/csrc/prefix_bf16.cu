@@ -171,56 +171,45 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
         }
     } else if (warp == 8) {
         // ---------------------------------------------------------- products
-        if (lane == 0 && steps > 0) {
+        if (steps > 0) {
             constexpr uint32_t kQk = mma_shape(kMmaBf16, kTileTok, false), kPv = mma_shape(kMmaBf16, kD, true);
+            const uint32_t q_desc = smem_operand(smem_addr(q_op), 16), k_desc = smem_operand(smem_addr(k_op), 16);
+            const uint32_t v_desc = smem_operand(smem_addr(v_op), kHalfOperand);
             bool ok = true;
-            auto tile_of = [&](int i) { return MODE == 0 ? i >> 1 : i; };
-            auto last_use = [&](int i) { return MODE == 0 ? (i & 1) == 1 : true; };
-            auto qk = [&](int i) {
-                const int w = i & 1, t = tile_of(i), st = t & 1;
-                if (!mbar_wait_or_stop(&s.k_full[st], (t >> 1) & 1, stop, kWaitLimit)) return false;
-                tc_fence_after();
-                const uint32_t ka = smem_addr(k_op + st * kOperand);
+            for (int i = 0; i < steps + 2 && ok; ++i) {
+                if (i >= 2) {                                     // O (+)= P V of step i - 2
+                    const int j = i - 2, w = j & 1, t = MODE == 0 ? j >> 1 : j, st = t & 1;
+                    if (MODE != 0 || w == 0) ok = warp_wait_or_stop(&s.v_full[st], (t >> 1) & 1, stop, kWaitLimit);
+                    if (ok && (MODE != 0 || w == 0) && most - (t_beg + t) * kTileTok < kTileTok) ok = warp_wait_or_stop(&s.v_clean, 0, stop, kWaitLimit);
+                    ok = ok && warp_wait_or_stop(&s.p_ready[w], (j >> 1) & 1, stop, kWaitLimit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t p = tm_s + 128 * w, vd = v_desc + st * (kOperand >> 4);
 #pragma unroll
-                for (int part = 0; part < (MODE == 2 ? 2 : 1); ++part) {
-                    const uint32_t qa = smem_addr(q_op + (MODE == 0 ? w : part) * kOperand);
-#pragma unroll
-                    for (int k = 0; k < kD / 16; ++k) {
-                        const uint32_t off = (k >> 2) * kHalfOperand + (k & 3) * 32;
-                        mma_ss(tm_s + 128 * w, smem_operand(qa + off, 16, 1024), smem_operand(ka + off, 16, 1024), kQk,
-                               part > 0 || k > 0);
-                    }
+                    for (int k = 0; k < kTileTok / 16; ++k)       // 16 tokens: 8 columns of P, 2048 bytes of V rows
+                        mma_ts(tm_o + 128 * w, p + 8 * k, vd + k * (2048 >> 4), kPv, j >= 2 || k > 0);
+                    if (MODE != 0 || w == 1) mma_commit(&s.v_empty[st]);
+                    if (j + 2 >= steps) mma_commit(&s.o_full[w]);
                 }
-                mma_commit(&s.s_full[w]);
-                if (last_use(i)) mma_commit(&s.k_empty[st]);
-                return true;
-            };
-            auto pv = [&](int i) {
-                const int w = i & 1, t = tile_of(i), st = t & 1;
-                if (!mbar_wait_or_stop(&s.p_ready[w], (i >> 1) & 1, stop, kWaitLimit)) return false;
-                if (!mbar_wait_or_stop(&s.v_full[st], (t >> 1) & 1, stop, kWaitLimit)) return false;
-                if (most - (t_beg + t) * kTileTok < kTileTok && !mbar_wait_or_stop(&s.v_clean, 0, stop, kWaitLimit)) return false;
-                tc_fence_after();
-                const uint32_t va = smem_addr(v_op + st * kOperand);
+                if (i < steps) {                                  // S = Q K^T of step i
+                    const int w = i & 1, t = MODE == 0 ? i >> 1 : i, st = t & 1;
+                    if (MODE != 0 || w == 0) ok = warp_wait_or_stop(&s.k_full[st], (t >> 1) & 1, stop, kWaitLimit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t qd = q_desc + (MODE == 0 ? w * (kOperand >> 4) : 0), kd = k_desc + st * (kOperand >> 4);
 #pragma unroll
-                for (int k = 0; k < kTileTok / 16; ++k)   // 16 tokens: 8 columns of P, 2048 bytes of V rows
-                    mma_ts(tm_o + 128 * w, tm_s + 128 * w + 8 * k, smem_operand(va + 2048 * k, kHalfOperand, 1024), kPv,
-                           i >= 2 || k > 0);
-                if (last_use(i)) mma_commit(&s.v_empty[st]);
-                if (i + 2 >= steps) mma_commit(&s.o_full[w]);
-                return true;
-            };
-            ok = qk(0);
-            if (ok && steps > 1) ok = qk(1);
-            for (int i = 0; i < steps && ok; ++i) {
-                ok = pv(i);
-                if (ok && i + 2 < steps) ok = qk(i + 2);
+                    for (int k = 0; k < (MODE == 2 ? 16 : 8); ++k) {   // (k >= 8: the query's low halves)
+                        const uint32_t off = ((k >> 2 & 1) * kHalfOperand + (k & 3) * 32) >> 4;
+                        mma_ss(tm_s + 128 * w, qd + (k >> 3) * (kOperand >> 4) + off, kd + off, kQk, k > 0);
+                    }
+                    mma_commit(&s.s_full[w]);
+                    if (MODE != 0 || w == 1) mma_commit(&s.k_empty[st]);
+                }
             }
             // products in flight end before the operands and tensor memory go
             mma_commit(&s.drained);
             if (!mbar_wait_bounded(&s.drained, 0, kWaitLimit)) *stop = 1;
         }
-        __syncwarp();
     } else {
         // ---------------------------------------------------------- softmax
         const int w = warp >> 2;                                  // stream
@@ -240,9 +229,8 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
             if (!ok) break;
             tc_fence_after();
             // (the products that S waited for include the last one into O)
-            softmax_tile<kTileTok, false>(my_s, my_o, len - t * kTileTok, scale, 0.f, 1.f, 0.f, j == 0, st, [] { return true; });
-            tc_fence_before();
-            mbar_arrive(&s.p_ready[w]);
+            softmax_tile<kTileTok, false>(my_s, my_o, len - t * kTileTok, scale, 0.f, 1.f, 0.f, j == 0, st, &s.p_ready[w],
+                                          [] { return true; });
         }
         if (items > 0 && ok) {
             ok = __all_sync(kFull, mbar_wait_or_stop(&s.o_full[w], 0, stop, kWaitLimit));

@@ -349,49 +349,44 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
                 mbar_wait_bounded(&s.raw_full[i % kRawStages], (i / kRawStages) & 1, kWaitLimit);
     } else if (warp == 4) {
         // ---------------------------------------------------------- products
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             constexpr uint32_t kQk = mma_shape(kMmaBf16, kPkTok, false), kPv = mma_shape(kMmaF16, kD, false);
-            auto qk = [&](int i) {
-                const int w = i & 1;
-                if (!mbar_wait_or_stop(&s.k_full[w], (i >> 1) & 1, stop, kWaitLimit)) return false;
-                tc_fence_after();
-                const uint32_t ka = smem_addr(k_op + w * 2 * kPkK);
+            const uint32_t k_desc = smem_operand(smem_addr(k_op), 16), v_desc = smem_operand(smem_addr(v_op), 16);
+            bool ok = true;
+            for (int i = 0; i < n + 2 && ok; ++i) {
+                if (i >= 2) {                                     // O (+)= P V' of tile i - 2
+                    const int j = i - 2, w = j & 1;
+                    ok = warp_wait_or_stop(&s.v_full[w], (j >> 1) & 1, stop, kWaitLimit);
+                    ok = ok && warp_wait_or_stop(&s.p_ready[w], (j >> 1) & 1, stop, kWaitLimit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t p = tm_s + 64 * w, vd = v_desc + w * (kPkV >> 4);
 #pragma unroll
-                for (int part = 0; part < 3; ++part) {            // hi hi, hi lo, lo hi
-                    const uint32_t qa = tm_q + (part == 2 ? 64 : 0), kb = ka + (part == 1 ? kPkK : 0);
-#pragma unroll
-                    for (int k = 0; k < kD / 16; ++k)
-                        mma_ts(tm_s + 64 * w, qa + 8 * k, smem_operand(kb + (k >> 2) * (kPkK / 2) + (k & 3) * 32, 16, 1024), kQk,
-                               part > 0 || k > 0);
+                    for (int k = 0; k < kPkTok / 16; ++k) mma_ts(tm_o, p + 8 * k, vd + 2 * k, kPv, j > 0 || k > 0);
+                    mma_commit(&s.v_empty[w]);
+                    if (j + 1 == n) mma_commit(&s.o_full);
                 }
-                mma_commit(&s.s_full[w]);
-                mma_commit(&s.k_empty[w]);
-                return true;
-            };
-            auto pv = [&](int i) {
-                const int w = i & 1;
-                if (!mbar_wait_or_stop(&s.p_ready[w], (i >> 1) & 1, stop, kWaitLimit)) return false;
-                if (!mbar_wait_or_stop(&s.v_full[w], (i >> 1) & 1, stop, kWaitLimit)) return false;
-                tc_fence_after();
-                const uint32_t va = smem_addr(v_op + w * kPkV);
+                if (i < n) {                                      // S = Q K'^T of tile i
+                    const int w = i & 1;
+                    ok = warp_wait_or_stop(&s.k_full[w], (i >> 1) & 1, stop, kWaitLimit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t kd = k_desc + w * (2 * kPkK >> 4);
 #pragma unroll
-                for (int k = 0; k < kPkTok / 16; ++k)
-                    mma_ts(tm_o, tm_s + 64 * w + 8 * k, smem_operand(va + 32 * k, 16, 1024), kPv, i > 0 || k > 0);
-                mma_commit(&s.v_empty[w]);
-                if (i + 1 == n) mma_commit(&s.o_full);
-                return true;
-            };
-            bool ok = qk(0);
-            if (ok && n > 1) ok = qk(1);
-            for (int i = 0; i < n && ok; ++i) {
-                ok = pv(i);
-                if (ok && i + 2 < n) ok = qk(i + 2);
+                    for (int part = 0; part < 3; ++part)          // hi hi, hi lo, lo hi
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_ts(tm_s + 64 * w, tm_q + (part == 2 ? 64 : 0) + 8 * k,
+                                   kd + (((part == 1 ? kPkK : 0) + (k >> 2) * (kPkK / 2) + (k & 3) * 32) >> 4), kQk,
+                                   part > 0 || k > 0);
+                    mma_commit(&s.s_full[w]);
+                    mma_commit(&s.k_empty[w]);
+                }
             }
             // products in flight end before the operands and tensor memory go
             mma_commit(&s.drained);
             if (!mbar_wait_bounded(&s.drained, 0, kWaitLimit)) *stop = 1;
         }
-        __syncwarp();
     } else {
         // ---------------------------------------------------------- softmax
         const int row = row0 + warp * 32 + lane;
@@ -409,13 +404,11 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
             const int e = *reinterpret_cast<volatile int*>(&s.vexp[i & 3]);
             // O is idle once tile i - 1's product into it has freed its V stage
             ok = softmax_tile<kPkTok, true>(tm_s + 64 * (i & 1) + lanes, my_o, len - (t_beg + i) * kPkTok, scale, (float)e,
-                                            exp2i(-e), kLift, i == 0, st, [&] {
+                                            exp2i(-e), kLift, i == 0, st, &s.p_ready[i & 1], [&] {
                 const bool idle = __all_sync(kFull, mbar_wait_or_stop(&s.v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, stop, kWaitLimit));
                 tc_fence_after();
                 return idle;
             });
-            tc_fence_before();
-            if (ok) mbar_arrive(&s.p_ready[i & 1]);
         }
         if (n > 0 && ok) {
             ok = __all_sync(kFull, mbar_wait_or_stop(&s.o_full, 0, stop, kWaitLimit));

@@ -66,10 +66,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
 //   K-major (contraction along the row): sbo = bytes from 8 rows to the next 8
 //   MN-major (contraction across rows):  sbo the same, lbo = bytes from one
 //   64-element column block to the next
-__device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)((lbo >> 4) & 0x3fff) << 16 | (uint64_t)((sbo >> 4) & 0x3fff) << 32 |
-           1ull << 46 | 2ull << 61;
+// The descriptor's low word for an address (+ bytes / 16 steps through the
+// operand) and its constant high word: the thread that issues products adds
+// one immediate per product, since the tensor core takes one every 32-64 cycles.
+__device__ __forceinline__ uint32_t smem_operand(uint32_t addr, uint32_t lbo) {
+    return ((addr >> 4) & 0x3fff) | ((lbo >> 4) & 0x3fff) << 16;
 }
+constexpr uint32_t kOperandHigh = (1024u >> 4) | 1u << 14 | 2u << 29;   // sbo 1024, version 1, 128-byte swizzle
 
 enum { kMmaF16 = 0, kMmaBf16 = 1 };
 // kind::f16, fp32 accumulators, M = 128; b_mn: B is MN-major
@@ -79,25 +82,31 @@ __host__ __device__ constexpr uint32_t mma_shape(int type, int n, bool b_mn) {
 }
 
 // d (+)= A B, A and B in shared memory / A in tensor memory (two 16-bit
-// values of the contraction axis per column). Issued by one thread.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool acc) {
+// values of the contraction axis per column). Called by a whole warp with the
+// same arguments; one lane, always the same, issues. (Called from a branch of
+// one lane instead, every operand takes a trip from a lane's register to a
+// uniform one: about 80-110 cycles a product, which starves the tensor core.)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(shape), "r"((uint32_t)acc)
+        "{\n .reg .pred p, e;\n .reg .b64 da, db;\n elect.sync _|e, 0xffffffff;\n setp.ne.u32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(shape), "r"((uint32_t)acc), "r"(kOperandHigh)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(shape), "r"((uint32_t)acc)
+        "{\n .reg .pred p, e;\n .reg .b64 db;\n elect.sync _|e, 0xffffffff;\n setp.ne.u32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(shape), "r"((uint32_t)acc), "r"(kOperandHigh)
         : "memory");
 }
-// Arrives on the barrier once every product this thread issued before has completed.
+// Arrives on the barrier once every product issued before has completed (a
+// whole warp calls it, the same lane as above issues).
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar))
+        : "memory");
 }
 
 // ---------------------------------------------------------------- barriers and copies
@@ -114,6 +123,11 @@ __device__ __forceinline__ bool mbar_wait_or_stop(uint64_t* bar, uint32_t parity
     }
     *stop = 1;
     return false;
+}
+
+// The same for a whole warp: true for all lanes or for none.
+__device__ __forceinline__ bool warp_wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* stop, uint32_t limit) {
+    return __all_sync(kFull, mbar_wait_or_stop(bar, parity, stop, limit));
 }
 
 // Tile copy global -> shared of a 2-D tensor map, completion counted on a
