@@ -63,7 +63,7 @@ struct RowState {
 // past 2^8 of what is there, so P stays within 2^(8 + lift) and O is seldom
 // touched; o_idle() waits until no product writes O (false: gave up).
 // `shown`: tokens of the tile that this row sees. The caller waits for S
-// before; P's arrival is signalled on p_ready.
+// before; each of the stream's 4 warps arrives on p_ready.
 template <int TOK, bool HALF, typename Idle>
 __device__ __forceinline__ bool softmax_tile(uint32_t my_s, uint32_t my_o, int shown, float scale, float bias, float unbias,
                                              float lift, bool first, RowState& st, uint64_t* p_ready, Idle&& o_idle) {
@@ -116,7 +116,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t my_s, uint32_t my_o, int s
     for (int c = 0; c < TOK / 2; c += 32) tmem_st32(my_s + c, x + c);
     tmem_wait_st();
     tc_fence_before();
-    mbar_arrive(p_ready);
+    warp_arrive(p_ready);
     st.l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * unbias;
     return true;
 }

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
             mbar_init(&s.v_full[i], 1);
             mbar_init(&s.v_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_ready[i], 128);
+            mbar_init(&s.p_ready[i], 4);
             mbar_init(&s.o_full[i], 1);
         }
         mbar_init(&s.v_clean, 1);
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s.tmem;
-    volatile int* stop = &s.stop;
+    int* stop = &s.stop;
     const uint32_t tm_s = tm, tm_o = tm + 256;         // S (and P) of stream w at + 128 w, O likewise
 
     if (warp == 9) {
@@ -140,8 +140,7 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
             const int y = (int)(((int64_t)max(page, 0) * a.n_kv + h) * 2 * B);
             for (int kind = 0; kind < 2; ++kind) {
                 uint64_t* full = kind ? &s.v_full[st] : &s.k_full[st];
-                if (i >= 2) ok = mbar_wait_or_stop(kind ? &s.v_empty[st] : &s.k_empty[st], ((i >> 1) - 1) & 1, stop, kWaitLimit);
-                ok = __all_sync(kFull, ok);
+                if (i >= 2) ok = warp_wait_or_stop(kind ? &s.v_empty[st] : &s.k_empty[st], ((i >> 1) - 1) & 1, stop, kWaitLimit);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(full, bytes);
                 __syncwarp();
@@ -155,17 +154,16 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
             // whatever the page or an earlier tile holds must be 0
             const int valid = most - t * kTileTok;
             if (ok && valid < kTileTok) {
-                ok = __all_sync(kFull, mbar_wait_or_stop(&s.v_full[st], (i >> 1) & 1, stop, kWaitLimit));
+                ok = warp_wait_or_stop(&s.v_full[st], (i >> 1) & 1, stop, kWaitLimit);
                 for (int x = valid * 8 + lane; x < kTileTok * 8; x += 32)
                     for (int c = 0; c < 2; ++c)
                         *reinterpret_cast<uint4*>(v_op + st * kOperand + c * kHalfOperand + x * 16) = make_uint4(0, 0, 0, 0);
                 fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.v_clean);
+                warp_arrive(&s.v_clean);
             }
         }
         // copies in flight land before the CTA ends
-        if (*stop) {
+        if (*reinterpret_cast<volatile int*>(stop)) {
             for (int i = max(0, done_k - 2); i < done_k; ++i) mbar_wait_bounded(&s.k_full[i & 1], (i >> 1) & 1, kWaitLimit);
             for (int i = max(0, done_v - 2); i < done_v; ++i) mbar_wait_bounded(&s.v_full[i & 1], (i >> 1) & 1, kWaitLimit);
         }
@@ -225,7 +223,7 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
         bool ok = true;
         for (int j = 0; j < items; ++j) {
             const int t = t_beg + (MODE == 0 ? j : 2 * j + w);
-            ok = __all_sync(kFull, mbar_wait_or_stop(&s.s_full[w], j & 1, stop, kWaitLimit));
+            ok = warp_wait_or_stop(&s.s_full[w], j & 1, stop, kWaitLimit);
             if (!ok) break;
             tc_fence_after();
             // (the products that S waited for include the last one into O)
@@ -233,7 +231,7 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
                                           [] { return true; });
         }
         if (items > 0 && ok) {
-            ok = __all_sync(kFull, mbar_wait_or_stop(&s.o_full[w], 0, stop, kWaitLimit));
+            ok = warp_wait_or_stop(&s.o_full[w], 0, stop, kWaitLimit);
             tc_fence_after();
         }
         if (ok) store_partial(a, MODE == 0 ? blockIdx.x : 2 * blockIdx.x + w, row, h, real, items == 0, st.m, st.l, my_o);

@@ -16,8 +16,9 @@
 // tiles in flight (2 x 64), O (128); K' and V' have two stages each, so the
 // products of one tile run while the next is built and the last is weighed.
 //
-// Warps: 0-3 softmax (a row a thread), 4 issues the products, 5-12 build
-// operands (13 warps leave 128 registers a thread; 17 would leave 96): one group's share of a record of the packed format (K: 4
+// Warps: 0-3 softmax (a row a thread), 4 issues the products, 13 copies raw
+// tiles and finds their exponents, 5-12 build operands without meeting at a
+// barrier (14 warps leave 128 registers a thread; 17 would leave 96): one group's share of a record of the packed format (K: 4
 // tokens x 8 channels, V: 8 tokens x 4 channels) is four whole 16-byte units
 // of the swizzled operand rows, so a lane reads a record's words and writes
 // units.
@@ -31,21 +32,18 @@ namespace kvarn {
 constexpr int kPkTok = 64;                       // tokens of a tile
 constexpr int kPkK = kPkTok * kD * 2;            // bytes of one 64 x 128 bf16 operand (two 64-channel blocks)
 constexpr int kPkV = kD * kPkTok * 2;            // 128 channel rows x 64 tokens, fp16
-constexpr int kRawStages = 3;
-constexpr int kBuildWarps = 8, kBuildThreads = 32 * kBuildWarps;
-constexpr int kPackedThreads = 160 + kBuildThreads;
+constexpr int kRawStages = 4;
+constexpr int kBuildWarps = 8;
+constexpr int kPackedThreads = 32 * (6 + kBuildWarps);
 constexpr float kLift = 7.f;                     // P up to 2^(8 + 7), small weights normal down to 2^-21
 
 struct PackedSmem {
-    uint64_t raw_full[kRawStages], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full, drained;
+    // ready: a raw tile's exponent is known; raw_empty: its operands are built
+    uint64_t raw_full[kRawStages], ready[kRawStages], raw_empty[kRawStages];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full, drained;
     uint32_t tmem;
     int stop;
     int vexp[4];                                  // e of the last tiles
-    uint32_t red[2][kBuildWarps], redc[2][kBuildWarps];
-    // per tile parity: (a, b) of every K and V (group, token) so that a value
-    // is (f a + b) C with f = 1 + code 2^-bits; C of the tile's two 32-token halves
-    alignas(16) float2 ab[2][2][4][kPkTok];       // [parity][kind]
-    alignas(16) float c[2][2][2][kD];             // [parity][kind][half]
 };
 
 template <int B, int BITS>
@@ -101,14 +99,18 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
 
     if (tid == 0) {
         s.stop = 0;
-        for (int i = 0; i < kRawStages; ++i) mbar_init(&s.raw_full[i], 1);
+        for (int i = 0; i < kRawStages; ++i) {
+            mbar_init(&s.raw_full[i], 1);
+            mbar_init(&s.ready[i], 1);
+            mbar_init(&s.raw_empty[i], kBuildWarps);
+        }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.k_full[i], kBuildThreads);
+            mbar_init(&s.k_full[i], kBuildWarps);
             mbar_init(&s.k_empty[i], 1);
-            mbar_init(&s.v_full[i], kBuildThreads);
+            mbar_init(&s.v_full[i], kBuildWarps);
             mbar_init(&s.v_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_ready[i], 128);
+            mbar_init(&s.p_ready[i], 4);
         }
         mbar_init(&s.o_full, 1);
         mbar_init(&s.drained, 1);
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s.tmem;
-    volatile int* stop = &s.stop;
+    int* stop = &s.stop;
     const uint32_t tm_q = tm, tm_s = tm + 128, tm_o = tm + 256;   // S of tile i at + 64 (i % 2)
     if (warp < 4) {
         const int r = warp * 32 + lane;
@@ -172,181 +174,202 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
     __syncthreads();   // (the staging is free for operands)
     tc_fence_after();
 
-    if (warp > 4) {
-        // ---------------------------------------------------------- operands from codes
-        const int bt = tid - 160, bw = warp - 5;
-        const int used = (most + B - 1) / B;      // blocks that hold a visible token
-        // thread 0 keeps the raw tiles coming
+    const int used = (most + B - 1) / B;          // blocks that hold a visible token
+    if (warp == 5 + kBuildWarps) {
+        // ---------------------------------------------------------- raw tiles and their exponents
         auto fetch = [&](int i) {
             const int st = i % kRawStages, b0 = (t_beg + i) * Lay::kBlocks;
-            int64_t page[Lay::kBlocks];
-            uint32_t bytes = 0;
-#pragma unroll
-            for (int x = 0; x < Lay::kBlocks; ++x) {
-                page[x] = b0 + x < used ? a.table[b0 + x] : -1;
-                if (b0 + x < used && (page[x] < 0 || page[x] >= a.n_pool_blocks)) {
+            int64_t page = -1;                    // lane x: block x of the tile
+            if (lane < Lay::kBlocks && b0 + lane < used) {
+                page = a.table[b0 + lane];
+                if (page < 0 || page >= a.n_pool_blocks) {
                     raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
-                    page[x] = -1;
+                    page = -1;
                 }
-                if (page[x] >= 0) bytes += 2 * Lay::HB;
             }
-            fence_async_smem();
-            mbar_arrive_expect_tx(&s.raw_full[st], bytes);
-#pragma unroll
-            for (int x = 0; x < Lay::kBlocks; ++x)
-                if (page[x] >= 0)
-                    bulk_g2s(raw + st * Lay::kRaw + x * 2 * Lay::HB, a.pool + page[x] * a.block_bytes + (int64_t)(2 * h) * Lay::HB,
-                             2 * Lay::HB, &s.raw_full[st]);
+            const uint32_t bytes = __popc(__ballot_sync(kFull, page >= 0)) * (2 * Lay::HB);
+            if (lane == 0) mbar_arrive_expect_tx(&s.raw_full[st], bytes);
+            __syncwarp();
+            if (page >= 0)
+                bulk_g2s(raw + st * Lay::kRaw + lane * 2 * Lay::HB, a.pool + page * a.block_bytes + (int64_t)(2 * h) * Lay::HB,
+                         2 * Lay::HB, &s.raw_full[st]);
         };
         int fetched = 0;
-        if (bt == 0)
-            for (; fetched < kRawStages && fetched < n; ++fetched) fetch(fetched);
         bool ok = true;
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; i < n && ok; ++i) {
+            // (one stage less in flight than there are: its wait is for tile i - 2)
+            for (; fetched < n && fetched < i + kRawStages - 1 && ok; ++fetched) {
+                if (fetched >= kRawStages)        // the stage's last tile has been built
+                    ok = warp_wait_or_stop(&s.raw_empty[fetched % kRawStages], (fetched / kRawStages - 1) & 1, stop, kWaitLimit);
+                if (!ok) break;
+                fetch(fetched);
+            }
+            const int st = i % kRawStages;
+            ok = ok && warp_wait_or_stop(&s.raw_full[st], (i / kRawStages) & 1, stop, kWaitLimit);
+            if (!ok) break;
+            // 2^e over the tile's values: the largest (|zero|, |top level|) R
+            // times the largest C (a lane: 8 (group, token) pairs, 4 or 8 channels)
+            constexpr int kPer = 32 / Lay::kBlocks;                // lanes per block
+            const int x = lane / kPer, at = 8 * (lane % kPer);
+            float vmax = 0.f, cmax = 0.f;
+            if ((t_beg + i) * Lay::kBlocks + x < used) {
+                const uint8_t* hb = raw + st * Lay::kRaw + x * 2 * Lay::HB + Lay::HB;
+                const uint4 su = *reinterpret_cast<const uint4*>(hb + off_s(B, BITS) + 2 * at);
+                const uint4 zu = *reinterpret_cast<const uint4*>(hb + off_z(B, BITS) + 2 * at);
+                const uint4 ru = *reinterpret_cast<const uint4*>(hb + off_R(B, BITS) + 2 * (at % B));
+                const uint32_t sw[4] = {su.x, su.y, su.z, su.w}, zw[4] = {zu.x, zu.y, zu.z, zu.w}, rw[4] = {ru.x, ru.y, ru.z, ru.w};
+                constexpr float kTop = (float)((1 << BITS) - 1);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 sf = __half22float2(u32_as_h2(sw[k])), zf = __half22float2(u32_as_h2(zw[k]));
+                    const float2 rf = __half22float2(u32_as_h2(rw[k]));
+                    vmax = fmaxf(vmax, fmaxf(fabsf(zf.x), fabsf(fmaf(sf.x, kTop, zf.x))) * fabsf(rf.x));
+                    vmax = fmaxf(vmax, fmaxf(fabsf(zf.y), fabsf(fmaf(sf.y, kTop, zf.y))) * fabsf(rf.y));
+                }
+                constexpr int kCh = kD / kPer;
+#pragma unroll
+                for (int k = 0; k < kCh; k += 2) {
+                    const float2 cf = __half22float2(
+                        u32_as_h2(*reinterpret_cast<const uint32_t*>(hb + off_C(B, BITS) + 2 * (kCh * (lane % kPer) + k))));
+                    cmax = fmaxf(cmax, fmaxf(fabsf(cf.x), fabsf(cf.y)));
+                }
+            }
+            const float bound = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vmax))) *
+                                __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(cmax)));
+            // the clamps keep 2^-e and 2^e finite
+            if (lane == 0) {
+                s.vexp[i & 3] = bound > 0x1p-60f ? min(ceil_log2(bound), 100) : -60;
+                mbar_arrive(&s.ready[st]);
+            }
+        }
+        // copies in flight land before the CTA ends
+        if (*reinterpret_cast<volatile int*>(stop))
+            for (int i = max(0, fetched - kRawStages); i < fetched; ++i)
+                mbar_wait_bounded(&s.raw_full[i % kRawStages], (i / kRawStages) & 1, kWaitLimit);
+    } else if (warp > 4) {
+        // ---------------------------------------------------------- operands from codes
+        // warp bw: group g of the 32 records of half sb, a record a lane
+        const int bw = warp - 5, g = bw & 3, sb = bw >> 2, ra = lane >> 2, rb = lane & 3;
+        const int half0 = B == 64 ? 32 * sb : 0;          // the half's first token within its block
+        constexpr float kSpan = (float)(1 << BITS);
+        bool ok = true;
+        for (int i = 0; i < n && ok; ++i) {
             const int st = i % kRawStages, par = i & 1;
-            if (ok) ok = mbar_wait_or_stop(&s.raw_full[st], (i / kRawStages) & 1, stop, kWaitLimit);
-            const uint8_t* tile = raw + st * Lay::kRaw;
-            // ---- (a, b) of thread bt's (group, token), C, and the tile's largest value
-            {
-                const int g = bt >> 6, t = bt & 63, x = t / B, tb = t % B;
-                const bool there = (t_beg + i) * Lay::kBlocks + x < used;
-                float vmax = 0.f, cmax = 0.f;
-#pragma unroll
-                for (int kind = 0; kind < 2; ++kind) {
-                    const uint8_t* hb = tile + x * 2 * Lay::HB + kind * Lay::HB;
-                    const float step = h2f(reinterpret_cast<const uint16_t*>(hb + off_s(B, BITS))[g * B + tb]);
-                    const float zero = h2f(reinterpret_cast<const uint16_t*>(hb + off_z(B, BITS))[g * B + tb]);
-                    const float fac = h2f(reinterpret_cast<const uint16_t*>(hb + off_R(B, BITS))[tb]);
-                    constexpr float kSpan = (float)(1 << BITS);
-                    const float wide = step * kSpan;
-                    s.ab[par][kind][g][t] = there ? make_float2(wide * fac, (zero - wide) * fac) : make_float2(0.f, 0.f);
-                    if (kind == 1 && there) vmax = fmaxf(fabsf(zero), fabsf(fmaf(step, kSpan - 1.f, zero))) * fac;
-                }
-                // C: thread bt takes channel bt % 128 of half bt / 128, K and V
-                const int half = bt >> 7, ch = bt & 127, xc = half * 32 / B;
-                const bool has = (t_beg + i) * Lay::kBlocks + xc < used;
-#pragma unroll
-                for (int kind = 0; kind < 2; ++kind) {
-                    const uint8_t* hb = tile + xc * 2 * Lay::HB + kind * Lay::HB;
-                    const float cf = has ? h2f(reinterpret_cast<const uint16_t*>(hb + off_C(B, BITS))[ch]) : 0.f;
-                    s.c[par][kind][half][ch] = cf;
-                    if (kind == 1) cmax = fabsf(cf);
-                }
-                const uint32_t rv = __reduce_max_sync(kFull, __float_as_uint(fabsf(vmax)));
-                const uint32_t rc = __reduce_max_sync(kFull, __float_as_uint(cmax));
-                if (lane == 0) {
-                    s.red[par][bw] = rv;
-                    s.redc[par][bw] = rc;
-                }
-            }
-            // one barrier a tile: the tables are ready, and every thread is done with tile i - 1
-            asm volatile("bar.sync 1, %0;" ::"n"(kBuildThreads) : "memory");
-            if (bt == 0 && i > 0 && fetched < n && !*stop) fetch(fetched++);
-            uint32_t rv = 0, rc = 0;
-#pragma unroll
-            for (int k = 0; k < kBuildWarps; ++k) {
-                rv = max(rv, s.red[par][k]);
-                rc = max(rc, s.redc[par][k]);
-            }
-            // 2^e >= the largest |value|; the clamp keeps 2^-e and 2^e finite
-            const float bound = __uint_as_float(rv) * __uint_as_float(rc);
-            const int e = bound > 0x1p-60f ? min(ceil_log2(bound), 100) : -60;
-            const float down = exp2i(-e);
-            // warp bw: group g of the 32 records of half sb, a record a lane
-            const int g = bw & 3, sb = bw >> 2, ra = lane >> 2, rb = lane & 3;
-            const uint8_t* codes = tile + (B == 64 ? 0 : sb) * 2 * Lay::HB + ((B == 64 ? 32 * sb : 0) + lane) * 16 * BITS;
+            ok = warp_wait_or_stop(&s.ready[st], (i / kRawStages) & 1, stop, kWaitLimit) &&
+                 warp_wait_or_stop(&s.raw_full[st], (i / kRawStages) & 1, stop, kWaitLimit);
+            if (!ok) break;
+            const uint8_t* hb = raw + st * Lay::kRaw + (B == 64 ? 0 : sb) * 2 * Lay::HB;
+            const bool there = (t_beg + i) * Lay::kBlocks + (B == 64 ? 0 : sb) < used;   // else its operands are zero
             // ---- K: 4 tokens 4 ra + k of the half, channels 32 g + 8 rb .. + 7
-            if (i >= 2 && ok) ok = mbar_wait_or_stop(&s.k_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
-            if (ok) {
-                if (bt == 0) s.vexp[i & 3] = e;
+            {
+                const uint8_t* codes = hb + (half0 + lane) * 16 * BITS;
                 uint32_t w[4], hw[4];              // token k's word with this group's fields at its low end
-                {
-                    const uint4* src = reinterpret_cast<const uint4*>(codes);
-                    if constexpr (BITS == 4) {     // word 4 k + g
+                const uint4* src = reinterpret_cast<const uint4*>(codes);
+                if constexpr (BITS == 4) {         // word 4 k + g
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint4 u = src[k];
-                            w[k] = g == 0 ? u.x : g == 1 ? u.y : g == 2 ? u.z : u.w;
-                        }
-                    } else {                       // word 2 k + g / 2, fields 4 (g % 2) ..
-                        const uint4 u = src[0], v = src[1];
-                        w[0] = (g & 2 ? u.y : u.x) >> 8 * (g & 1);
-                        w[1] = (g & 2 ? u.w : u.z) >> 8 * (g & 1);
-                        w[2] = (g & 2 ? v.y : v.x) >> 8 * (g & 1);
-                        w[3] = (g & 2 ? v.w : v.z) >> 8 * (g & 1);
-                        if constexpr (BITS == 3) { // high bits in word 8 + k from bit 4 g
-                            const uint4 x = src[2];
-                            hw[0] = x.x >> 4 * g; hw[1] = x.y >> 4 * g; hw[2] = x.z >> 4 * g; hw[3] = x.w >> 4 * g;
-                        }
+                    for (int k = 0; k < 4; ++k) {
+                        const uint4 u = src[k];
+                        w[k] = g == 0 ? u.x : g == 1 ? u.y : g == 2 ? u.z : u.w;
+                    }
+                } else {                           // word 2 k + g / 2, fields 4 (g % 2) ..
+                    const uint4 u = src[0], v = src[1];
+                    w[0] = (g & 2 ? u.y : u.x) >> 8 * (g & 1);
+                    w[1] = (g & 2 ? u.w : u.z) >> 8 * (g & 1);
+                    w[2] = (g & 2 ? v.y : v.x) >> 8 * (g & 1);
+                    w[3] = (g & 2 ? v.w : v.z) >> 8 * (g & 1);
+                    if constexpr (BITS == 3) {     // high bits in word 8 + k from bit 4 g
+                        const uint4 x = src[2];
+                        hw[0] = x.x >> 4 * g; hw[1] = x.y >> 4 * g; hw[2] = x.z >> 4 * g; hw[3] = x.w >> 4 * g;
                     }
                 }
-                float2 cc[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) cc[k] = *reinterpret_cast<const float2*>(&s.c[par][0][sb][32 * g + 8 * rb + 2 * k]);
+                const int t0 = half0 + 4 * ra;
+                const uint2 su = *reinterpret_cast<const uint2*>(hb + off_s(B, BITS) + 2 * (g * B + t0));
+                const uint2 zu = *reinterpret_cast<const uint2*>(hb + off_z(B, BITS) + 2 * (g * B + t0));
+                const uint2 ru = *reinterpret_cast<const uint2*>(hb + off_R(B, BITS) + 2 * t0);
+                const uint4 cu = *reinterpret_cast<const uint4*>(hb + off_C(B, BITS) + 2 * (32 * g + 8 * rb));
+                float2 cc[4] = {__half22float2(u32_as_h2(cu.x)), __half22float2(u32_as_h2(cu.y)),
+                                __half22float2(u32_as_h2(cu.z)), __half22float2(u32_as_h2(cu.w))};
+                if (!there) cc[0] = cc[1] = cc[2] = cc[3] = make_float2(0.f, 0.f);
+                if (i >= 2) ok = warp_wait_or_stop(&s.k_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
+                if (!ok) break;
                 uint8_t* dst = k_op + par * 2 * kPkK + (g >> 1) * (kPkK / 2);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int t = 32 * sb + 4 * ra + k;
-                    const float2 ab = s.ab[par][0][g][t];
+                    const float2 s2 = __half22float2(u32_as_h2(k < 2 ? su.x : su.y)), z2 = __half22float2(u32_as_h2(k < 2 ? zu.x : zu.y));
+                    const float2 r2 = __half22float2(u32_as_h2(k < 2 ? ru.x : ru.y));
+                    const float step = (k & 1) ? s2.y : s2.x, zero = (k & 1) ? z2.y : z2.x, fac = (k & 1) ? r2.y : r2.x;
+                    // code s + z = (1 + code 2^-bits) (2^bits s) + (z - 2^bits s)
+                    const float fa = there ? step * kSpan * fac : 0.f, fb = there ? fmaf(step, -kSpan, zero) * fac : 0.f;
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
                         const float2 f = code_pair<BITS>(w[k], hw[k], p, p);
-                        const float2 y = __fmul2_rn(__ffma2_rn(f, make_float2(ab.x, ab.x), make_float2(ab.y, ab.y)), cc[p]);
+                        const float2 y = __fmul2_rn(__ffma2_rn(f, make_float2(fa, fa), make_float2(fb, fb)), cc[p]);
                         const __nv_bfloat162 yh = __floats2bfloat162_rn(y.x, y.y);
-                        const float2 yf = __bfloat1622float2(yh);
-                        const __nv_bfloat162 yl = __floats2bfloat162_rn(y.x - yf.x, y.y - yf.y);
                         hi[p] = *reinterpret_cast<const uint32_t*>(&yh);
+                        const float2 d = __fadd2_rn(y, make_float2(-__uint_as_float(hi[p] << 16), -__uint_as_float(hi[p] & 0xffff0000u)));
+                        const __nv_bfloat162 yl = __floats2bfloat162_rn(d.x, d.y);
                         lo[p] = *reinterpret_cast<const uint32_t*>(&yl);
                     }
-                    const uint32_t at = swizzled(t, 4 * (g & 1) + rb);
+                    const uint32_t at = swizzled(32 * sb + 4 * ra + k, 4 * (g & 1) + rb);
                     *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(dst + kPkK + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 fence_async_smem();
-                mbar_arrive(&s.k_full[par]);
+                warp_arrive(&s.k_full[par]);
             }
             // ---- V: channels 32 g + 4 ra + k, 8 tokens 8 rb .. + 7 of the half
-            if (i >= 2 && ok) ok = mbar_wait_or_stop(&s.v_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
-            if (ok) {
+            {
+                const uint8_t* vb = hb + Lay::HB;
+                const uint8_t* codes = vb + (half0 + lane) * 16 * BITS;
                 uint32_t w[4], hw = 0;             // 4-bit: word 4 g + k; else 2 g + k / 2, and its high bits in word 8 + g
                 if constexpr (BITS == 4) {
-                    const uint4 u = reinterpret_cast<const uint4*>(codes + Lay::HB)[g];
+                    const uint4 u = reinterpret_cast<const uint4*>(codes)[g];
                     w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
                 } else {
-                    const uint2 u = reinterpret_cast<const uint2*>(codes + Lay::HB)[g];
+                    const uint2 u = reinterpret_cast<const uint2*>(codes)[g];
                     w[0] = w[1] = u.x;
                     w[2] = w[3] = u.y;
-                    if constexpr (BITS == 3) hw = reinterpret_cast<const uint32_t*>(codes + Lay::HB)[8 + g];
+                    if constexpr (BITS == 3) hw = reinterpret_cast<const uint32_t*>(codes)[8 + g];
                 }
-                float2 ab[8];
+                const int t0 = half0 + 8 * rb;
+                const uint4 su = *reinterpret_cast<const uint4*>(vb + off_s(B, BITS) + 2 * (g * B + t0));
+                const uint4 zu = *reinterpret_cast<const uint4*>(vb + off_z(B, BITS) + 2 * (g * B + t0));
+                const uint4 ru = *reinterpret_cast<const uint4*>(vb + off_R(B, BITS) + 2 * t0);
+                const uint2 cu = *reinterpret_cast<const uint2*>(vb + off_C(B, BITS) + 2 * (32 * g + 4 * ra));
+                const uint32_t sw[4] = {su.x, su.y, su.z, su.w}, zw[4] = {zu.x, zu.y, zu.z, zu.w}, rw[4] = {ru.x, ru.y, ru.z, ru.w};
+                float2 fa[4], fb[4];               // token pairs
 #pragma unroll
-                for (int d = 0; d < 8; ++d) ab[d] = s.ab[par][1][g][32 * sb + 8 * rb + d];
+                for (int p = 0; p < 4; ++p) {
+                    const float2 r2 = __half22float2(u32_as_h2(rw[p])), s2 = __half22float2(u32_as_h2(sw[p]));
+                    fa[p] = __fmul2_rn(__fmul2_rn(s2, make_float2(kSpan, kSpan)), r2);
+                    fb[p] = __fmul2_rn(__ffma2_rn(s2, make_float2(-kSpan, -kSpan), __half22float2(u32_as_h2(zw[p]))), r2);
+                    if (!there) fa[p] = fb[p] = make_float2(0.f, 0.f);
+                }
+                const float down = there ? exp2i(-*reinterpret_cast<volatile int*>(&s.vexp[i & 3])) : 0.f;
+                const float2 c01 = __half22float2(u32_as_h2(cu.x)), c23 = __half22float2(u32_as_h2(cu.y));
+                const float cf[4] = {c01.x * down, c01.y * down, c23.x * down, c23.y * down};
+                if (i >= 2) ok = warp_wait_or_stop(&s.v_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
+                if (!ok) break;
                 uint8_t* dst = v_op + par * kPkV;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int ch = 32 * g + 4 * ra + k;
-                    const float cf = s.c[par][1][sb][ch] * down;
+                    const float c = there ? cf[k] : 0.f;
                     uint32_t out[4];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {                 // tokens 2p, 2p + 1
                         const int j = BITS == 4 ? p : 4 * (p >> 1) + 2 * (p & 1) + (k & 1);
                         const float2 f = code_pair<BITS>(w[k], hw, j, 8 * (k >> 1) + j);
-                        const float2 y = __fmul2_rn(__ffma2_rn(f, make_float2(ab[2 * p].x, ab[2 * p + 1].x),
-                                                               make_float2(ab[2 * p].y, ab[2 * p + 1].y)),
-                                                    make_float2(cf, cf));
+                        const float2 y = __fmul2_rn(__ffma2_rn(f, fa[p], fb[p]), make_float2(c, c));
                         out[p] = pack_h2(y.x, y.y);
                     }
-                    *reinterpret_cast<uint4*>(dst + swizzled(ch, 4 * sb + rb)) = make_uint4(out[0], out[1], out[2], out[3]);
+                    *reinterpret_cast<uint4*>(dst + swizzled(32 * g + 4 * ra + k, 4 * sb + rb)) = make_uint4(out[0], out[1], out[2], out[3]);
                 }
                 fence_async_smem();
-                mbar_arrive(&s.v_full[par]);
+                warp_arrive(&s.v_full[par]);
+                warp_arrive(&s.raw_empty[st]);
             }
         }
-        // copies in flight land before the CTA ends
-        if (bt == 0 && *stop)
-            for (int i = max(0, fetched - kRawStages); i < fetched; ++i)
-                mbar_wait_bounded(&s.raw_full[i % kRawStages], (i / kRawStages) & 1, kWaitLimit);
     } else if (warp == 4) {
         // ---------------------------------------------------------- products
         if (n > 0) {
@@ -398,20 +421,20 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
         RowState st{-INFINITY, 0.f};
         bool ok = true;
         for (int i = 0; i < n && ok; ++i) {
-            ok = __all_sync(kFull, mbar_wait_or_stop(&s.s_full[i & 1], (i >> 1) & 1, stop, kWaitLimit));
+            ok = warp_wait_or_stop(&s.s_full[i & 1], (i >> 1) & 1, stop, kWaitLimit);
             if (!ok) break;
             tc_fence_after();
             const int e = *reinterpret_cast<volatile int*>(&s.vexp[i & 3]);
             // O is idle once tile i - 1's product into it has freed its V stage
             ok = softmax_tile<kPkTok, true>(tm_s + 64 * (i & 1) + lanes, my_o, len - (t_beg + i) * kPkTok, scale, (float)e,
                                             exp2i(-e), kLift, i == 0, st, &s.p_ready[i & 1], [&] {
-                const bool idle = __all_sync(kFull, mbar_wait_or_stop(&s.v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, stop, kWaitLimit));
+                const bool idle = warp_wait_or_stop(&s.v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, stop, kWaitLimit);
                 tc_fence_after();
                 return idle;
             });
         }
         if (n > 0 && ok) {
-            ok = __all_sync(kFull, mbar_wait_or_stop(&s.o_full, 0, stop, kWaitLimit));
+            ok = warp_wait_or_stop(&s.o_full, 0, stop, kWaitLimit);
             tc_fence_after();
         }
         if (ok) store_partial(a, blockIdx.x, row, h, real, n == 0, st.m - kLift, st.l, my_o);

@@ -115,19 +115,38 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Bounded wait that also gives up when another warp of the CTA has.
-__device__ __forceinline__ bool mbar_wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* stop, uint32_t limit) {
-    for (uint32_t i = 0; i < limit; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*stop) return false;
-    }
-    *stop = 1;
-    return false;
+// Bounded wait of a whole warp for a phase, which also gives up when another
+// warp of the CTA has: true for all lanes or for none. Every lane polls (a
+// lane polling for the others takes longer: the branch and the shuffle cost
+// more than the 32 polls), in a loop of a few instructions: these kernels'
+// hot loops overflow the instruction caches, where straight-line waits cost
+// several hundred cycles.
+__device__ __forceinline__ bool warp_wait_or_stop(uint64_t* bar, uint32_t parity, int* stop, uint32_t limit) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .u32 n, s;\n"
+        " mov.u32 n, %4;\n"
+        "POLL:\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " @p bra MET;\n"
+        " ld.volatile.shared.u32 s, [%3];\n"
+        " sub.u32 n, n, 1;\n"
+        " setp.ne.u32 q, s, 0;\n"
+        " setp.eq.or.u32 q, n, 0, q;\n"
+        " @!q bra POLL;\n"
+        "MET:\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(smem_addr(stop)), "r"(limit)
+        : "memory");
+    const bool all = __all_sync(kFull, ok);
+    if (!all) *reinterpret_cast<volatile int*>(stop) = 1;
+    return all;
 }
-
-// The same for a whole warp: true for all lanes or for none.
-__device__ __forceinline__ bool warp_wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* stop, uint32_t limit) {
-    return __all_sync(kFull, mbar_wait_or_stop(bar, parity, stop, limit));
+// One arrival for a warp, behind all its lanes' earlier work.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // Tile copy global -> shared of a 2-D tensor map, completion counted on a
