@@ -55,27 +55,29 @@ struct PackedLayout {
     static constexpr size_t bytes = 1024 + kHeader + 4 * kPkK + 2 * kPkV + kRawStages * kRaw;
 };
 
-// 1 + code 2^-BITS: the BITS bits at position p of w in the top of a mantissa.
-template <int BITS>
-__device__ __forceinline__ float unit_code(uint32_t w, int p) {
-    constexpr uint32_t mask = ((1u << BITS) - 1) << (23 - BITS);
-    const int s = 23 - BITS - p;
-    const uint32_t x = s >= 0 ? w << s : w >> -s;
-    return __uint_as_float((x & mask) | 0x3f800000u);
+// a b + c with 16-bit a and b (the low or the high half of a register) and
+// fp32 c: the product is exact, the sum rounds once.
+__device__ __forceinline__ float fma_half(uint32_t a, uint32_t b, float c, bool high_a, bool high_b) {
+    const uint16_t x = high_a ? (uint16_t)(a >> 16) : (uint16_t)a, y = high_b ? (uint16_t)(b >> 16) : (uint16_t)b;
+    float d;
+    asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"(y), "f"(c));
+    return d;
 }
-// The same for 3-bit codes: low two bits at p of w, high bit at ph of hw.
-__device__ __forceinline__ float unit_code3(uint32_t w, int p, uint32_t hw, int ph) {
-    const int s = 20 - p, sh = 22 - ph;
-    const uint32_t x = s >= 0 ? w << s : w >> -s, y = sh >= 0 ? hw << sh : hw >> -sh;
-    return __uint_as_float((x & 0x00300000u) | (y & 0x00400000u) | 0x3f800000u);
+// c - a for a bf16 a.
+__device__ __forceinline__ float minus_bf16(uint32_t a, float c, bool high) {
+    const uint16_t x = high ? (uint16_t)(a >> 16) : (uint16_t)a;
+    float d;
+    asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"((uint16_t)0xbf80), "f"(c));
+    return d;
 }
 
-// The codes of pair j of a record word (the j-th field of its low and of its
-// high half); for 3-bit codes jh is the pair's place in the high-bit word.
+// Pair j of a record word as fp16 code 2^-9 (attn_common.cuh); for 3-bit
+// codes jh is the pair's place in the high-bit word.
 template <int BITS>
-__device__ __forceinline__ float2 code_pair(uint32_t w, uint32_t hw, int j, int jh) {
-    if constexpr (BITS == 3) return make_float2(unit_code3(w, 2 * j, hw, jh), unit_code3(w, 2 * j + 16, hw, jh + 16));
-    else return make_float2(unit_code<BITS>(w, BITS * j), unit_code<BITS>(w, BITS * j + 16));
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t w8, uint32_t hw, int j, int jh) {
+    if constexpr (BITS == 2) return code2_s(w, w8, j);
+    else if constexpr (BITS == 3) return code3_s(w, w8, hw, j, jh);
+    else return code4_s(w, w8, j);
 }
 
 template <int B, int BITS>
@@ -251,7 +253,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
         // warp bw: group g of the 32 records of half sb, a record a lane
         const int bw = warp - 5, g = bw & 3, sb = bw >> 2, ra = lane >> 2, rb = lane & 3;
         const int half0 = B == 64 ? 32 * sb : 0;          // the half's first token within its block
-        constexpr float kSpan = (float)(1 << BITS);
+        // (code 2^-9) s + z 2^-9, times the rest of the value's factors and 2^9
+        constexpr float kUp = 512.f;
         bool ok = true;
         for (int i = 0; i < n && ok; ++i) {
             const int st = i % kRawStages, par = i & 1;
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
                  warp_wait_or_stop(&s.raw_full[st], (i / kRawStages) & 1, stop, kWaitLimit);
             if (!ok) break;
             const uint8_t* hb = raw + st * Lay::kRaw + (B == 64 ? 0 : sb) * 2 * Lay::HB;
-            const bool there = (t_beg + i) * Lay::kBlocks + (B == 64 ? 0 : sb) < used;   // else its operands are zero
+            const bool there = (t_beg + i) * Lay::kBlocks + (B == 64 ? 0 : sb) < used;   // else its values are zero
             // ---- K: 4 tokens 4 ra + k of the half, channels 32 g + 8 rb .. + 7
             {
                 const uint8_t* codes = hb + (half0 + lane) * 16 * BITS;
@@ -289,29 +292,28 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
                 const uint4 cu = *reinterpret_cast<const uint4*>(hb + off_C(B, BITS) + 2 * (32 * g + 8 * rb));
                 float2 cc[4] = {__half22float2(u32_as_h2(cu.x)), __half22float2(u32_as_h2(cu.y)),
                                 __half22float2(u32_as_h2(cu.z)), __half22float2(u32_as_h2(cu.w))};
-                if (!there) cc[0] = cc[1] = cc[2] = cc[3] = make_float2(0.f, 0.f);
                 if (i >= 2) ok = warp_wait_or_stop(&s.k_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
                 if (!ok) break;
                 uint8_t* dst = k_op + par * 2 * kPkK + (g >> 1) * (kPkK / 2);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float2 s2 = __half22float2(u32_as_h2(k < 2 ? su.x : su.y)), z2 = __half22float2(u32_as_h2(k < 2 ? zu.x : zu.y));
-                    const float2 r2 = __half22float2(u32_as_h2(k < 2 ? ru.x : ru.y));
-                    const float step = (k & 1) ? s2.y : s2.x, zero = (k & 1) ? z2.y : z2.x, fac = (k & 1) ? r2.y : r2.x;
-                    // code s + z = (1 + code 2^-bits) (2^bits s) + (z - 2^bits s)
-                    const float fa = there ? step * kSpan * fac : 0.f, fb = there ? fmaf(step, -kSpan, zero) * fac : 0.f;
+                    const uint32_t step = k < 2 ? su.x : su.y;
+                    const float2 z2 = __half22float2(u32_as_h2(k < 2 ? zu.x : zu.y)), r2 = __half22float2(u32_as_h2(k < 2 ? ru.x : ru.y));
+                    const float zero = ((k & 1) ? z2.y : z2.x) * kCodeScale, fac = ((k & 1) ? r2.y : r2.x) * kUp;
+                    const uint32_t w8 = w[k] >> 8;
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        const float2 f = code_pair<BITS>(w[k], hw[k], p, p);
-                        const float2 y = __fmul2_rn(__ffma2_rn(f, make_float2(fa, fa), make_float2(fb, fb)), cc[p]);
+                        const uint32_t f = code_pair<BITS>(w[k], w8, hw[k], p, p);
+                        float2 y = make_float2(fma_half(f, step, zero, false, k & 1), fma_half(f, step, zero, true, k & 1));
+                        y = __fmul2_rn(__fmul2_rn(y, make_float2(fac, fac)), cc[p]);
                         const __nv_bfloat162 yh = __floats2bfloat162_rn(y.x, y.y);
                         hi[p] = *reinterpret_cast<const uint32_t*>(&yh);
-                        const float2 d = __fadd2_rn(y, make_float2(-__uint_as_float(hi[p] << 16), -__uint_as_float(hi[p] & 0xffff0000u)));
-                        const __nv_bfloat162 yl = __floats2bfloat162_rn(d.x, d.y);
+                        const __nv_bfloat162 yl = __floats2bfloat162_rn(minus_bf16(hi[p], y.x, false), minus_bf16(hi[p], y.y, true));
                         lo[p] = *reinterpret_cast<const uint32_t*>(&yl);
                     }
                     const uint32_t at = swizzled(32 * sb + 4 * ra + k, 4 * (g & 1) + rb);
+                    // (an absent half's scores are masked, whatever its raw bytes were)
                     *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(dst + kPkK + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
@@ -338,30 +340,30 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
                 const uint4 ru = *reinterpret_cast<const uint4*>(vb + off_R(B, BITS) + 2 * t0);
                 const uint2 cu = *reinterpret_cast<const uint2*>(vb + off_C(B, BITS) + 2 * (32 * g + 4 * ra));
                 const uint32_t sw[4] = {su.x, su.y, su.z, su.w}, zw[4] = {zu.x, zu.y, zu.z, zu.w}, rw[4] = {ru.x, ru.y, ru.z, ru.w};
-                float2 fa[4], fb[4];               // token pairs
+                // (warps of an absent half, whose raw bytes may be anything, write zeros)
+                const float up = kUp * exp2i(-*reinterpret_cast<volatile int*>(&s.vexp[i & 3]));
+                float2 zero[4], fac[4];            // token pairs
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    const float2 r2 = __half22float2(u32_as_h2(rw[p])), s2 = __half22float2(u32_as_h2(sw[p]));
-                    fa[p] = __fmul2_rn(__fmul2_rn(s2, make_float2(kSpan, kSpan)), r2);
-                    fb[p] = __fmul2_rn(__ffma2_rn(s2, make_float2(-kSpan, -kSpan), __half22float2(u32_as_h2(zw[p]))), r2);
-                    if (!there) fa[p] = fb[p] = make_float2(0.f, 0.f);
+                    zero[p] = __fmul2_rn(__half22float2(u32_as_h2(zw[p])), make_float2(kCodeScale, kCodeScale));
+                    fac[p] = __fmul2_rn(__half22float2(u32_as_h2(rw[p])), make_float2(up, up));
                 }
-                const float down = there ? exp2i(-*reinterpret_cast<volatile int*>(&s.vexp[i & 3])) : 0.f;
                 const float2 c01 = __half22float2(u32_as_h2(cu.x)), c23 = __half22float2(u32_as_h2(cu.y));
-                const float cf[4] = {c01.x * down, c01.y * down, c23.x * down, c23.y * down};
+                const float cf[4] = {c01.x, c01.y, c23.x, c23.y};
                 if (i >= 2) ok = warp_wait_or_stop(&s.v_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
                 if (!ok) break;
                 uint8_t* dst = v_op + par * kPkV;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float c = there ? cf[k] : 0.f;
+                    const uint32_t w8 = w[k] >> 8;
                     uint32_t out[4];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {                 // tokens 2p, 2p + 1
                         const int j = BITS == 4 ? p : 4 * (p >> 1) + 2 * (p & 1) + (k & 1);
-                        const float2 f = code_pair<BITS>(w[k], hw, j, 8 * (k >> 1) + j);
-                        const float2 y = __fmul2_rn(__ffma2_rn(f, fa[p], fb[p]), make_float2(c, c));
-                        out[p] = pack_h2(y.x, y.y);
+                        const uint32_t f = code_pair<BITS>(w[k], w8, hw, j, 8 * (k >> 1) + j);
+                        float2 y = make_float2(fma_half(f, sw[p], zero[p].x, false, false), fma_half(f, sw[p], zero[p].y, true, true));
+                        y = __fmul2_rn(__fmul2_rn(y, fac[p]), make_float2(cf[k], cf[k]));
+                        out[p] = there ? pack_h2(y.x, y.y) : 0u;
                     }
                     *reinterpret_cast<uint4*>(dst + swizzled(32 * g + 4 * ra + k, 4 * sb + rb)) = make_uint4(out[0], out[1], out[2], out[3]);
                 }
