@@ -188,10 +188,8 @@ PrefixPlan prefix_plan(const kvarn_config& c, int64_t batch, int64_t prefix_bloc
     const int64_t sms = current_device_sms(), R = batch * (c.n_q_heads / c.n_kv_heads);
     PrefixPlan p{kPRows, 1, 0};
     if (sms <= 0) return p;
-    if (!packed) {
-        if (q_dtype == KVARN_BF16 && R > kPRows) p.rows = 2 * kPRows;
-        else p.streams = 2;
-    }
+    if (R > kPRows && (packed || q_dtype == KVARN_BF16)) p.rows = 2 * kPRows;
+    else if (!packed) p.streams = 2;
     // enough ranges for every SM to have one
     const int64_t units = c.n_kv_heads * ((R + p.rows - 1) / p.rows);
     const int64_t tiles = (prefix_blocks * c.block_size + 127) / 128;

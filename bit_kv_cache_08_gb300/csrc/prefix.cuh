@@ -64,22 +64,31 @@ struct RowState {
 // touched; o_idle() waits until no product writes O (false: gave up).
 // `shown`: tokens of the tile that this row sees. The caller waits for S
 // before; each of the stream's 4 warps arrives on p_ready.
-template <int TOK, bool HALF, typename Idle>
+// S stays in registers (CHUNK = TOK) or is read twice, CHUNK columns at a
+// time, where the kernel has too few of them.
+template <int TOK, int CHUNK, bool HALF, typename Idle>
 __device__ __forceinline__ bool softmax_tile(uint32_t my_s, uint32_t my_o, int shown, float scale, float bias, float unbias,
                                              float lift, bool first, RowState& st, uint64_t* p_ready, Idle&& o_idle) {
-    uint32_t x[TOK];
+    uint32_t x[CHUNK];
+    const bool cut = __any_sync(kFull, shown < TOK);
+    auto load = [&](int c0) {
 #pragma unroll
-    for (int c = 0; c < TOK; c += 32) tmem_ld32(my_s + c, x + c);
-    tmem_wait_ld();
-    if (__any_sync(kFull, shown < TOK)) {
+        for (int c = 0; c < CHUNK; c += 32) tmem_ld32(my_s + c0 + c, x + c);
+        tmem_wait_ld();
+        if (cut) {
 #pragma unroll
-        for (int i = 0; i < TOK; ++i)
-            if (i >= shown) x[i] = 0xff800000u;   // -inf, whatever was there
-    }
+            for (int i = 0; i < CHUNK; ++i)
+                if (c0 + i >= shown) x[i] = 0xff800000u;   // -inf, whatever was there
+        }
+    };
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < TOK; i += 2)   // (three-input maxima)
-        mx[(i >> 1) & 3] = fmaxf(fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), mx[(i >> 1) & 3]);
+    for (int c0 = 0; c0 < TOK; c0 += CHUNK) {
+        load(c0);
+#pragma unroll
+        for (int i = 0; i < CHUNK; i += 2)   // (three-input maxima)
+            mx[(i >> 1) & 3] = fmaxf(fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), mx[(i >> 1) & 3]);
+    }
     const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), scale, bias);
     const bool grow = top - st.m > 8.f;            // (from -inf at once; false where nothing is shown)
     if (!first && __any_sync(kFull, grow)) {
@@ -101,19 +110,28 @@ __device__ __forceinline__ bool softmax_tile(uint32_t my_s, uint32_t my_o, int s
     const float2 scale2 = make_float2(scale, scale), off2 = make_float2(off, off);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int i = 0; i < TOK; i += 2) {
-        const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, off2);
-        const float2 p = make_float2(ex2(y.x), ex2(y.y));
-        sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], p);
-        if (HALF) {
-            x[i >> 1] = pack_h2(p.x, p.y);
+    for (int c0 = 0; c0 < TOK; c0 += CHUNK) {
+        if (CHUNK < TOK) load(c0);
+#pragma unroll
+        for (int i = 0; i < CHUNK; i += 2) {
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, off2);
+            const float2 p = make_float2(ex2(y.x), ex2(y.y));
+            sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], p);
+            if (HALF) {
+                x[i >> 1] = pack_h2(p.x, p.y);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
+                x[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        // (over columns of S that have been read)
+        if (CHUNK == 32) {
+            tmem_st16(my_s + c0 / 2, x);
         } else {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
-            x[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+#pragma unroll
+            for (int c = 0; c < CHUNK / 2; c += 32) tmem_st32(my_s + c0 / 2 + c, x + c);
         }
     }
-#pragma unroll
-    for (int c = 0; c < TOK / 2; c += 32) tmem_st32(my_s + c, x + c);
     tmem_wait_st();
     tc_fence_before();
     warp_arrive(p_ready);

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
             if (!ok) break;
             tc_fence_after();
             // (the products that S waited for include the last one into O)
-            softmax_tile<kTileTok, false>(my_s, my_o, len - t * kTileTok, scale, 0.f, 1.f, 0.f, j == 0, st, &s.p_ready[w],
+            softmax_tile<kTileTok, kTileTok, false>(my_s, my_o, len - t * kTileTok, scale, 0.f, 1.f, 0.f, j == 0, st, &s.p_ready[w],
                                           [] { return true; });
         }
         if (items > 0 && ok) {

@@ -3,8 +3,9 @@
 // multiplied with 128 query rows.
 //
 // Everything runs in the rotated space (the query rows are rotated here, the
-// merge rotates back). Per kv head and 128 of its batch * G query rows, over
-// the CTA's range of 64-token tiles:
+// merge rotates back). Per kv head and up to 256 of its batch * G query rows
+// (two tiles of 128, which share the built operands), over the CTA's range of
+// 64-token tiles:
 //   S = Q K'^T (128 x 64, fp32)   K' = (code s + z) R C and Q are each split
 //       into two bf16 halves, and three products (hi hi, hi lo, lo hi) keep
 //       2^-16 of each factor: a score is exponentiated, so its error must not
@@ -12,16 +13,21 @@
 //   P = 2^(S - m), O += P V'      one fp16 product (2^-11 each): V' is
 //       (code s + z) R C 2^-e, the tile's exponent e making its largest value
 //       at most 1; e enters the exponent of P, so P V' needs no other scale
-// Tensor memory: Q as the A operand (hi, lo: 2 x 64 columns), S / P of two
-// tiles in flight (2 x 64), O (128); K' and V' have two stages each, so the
-// products of one tile run while the next is built and the last is weighed.
+// Tensor memory: Q's high half as the A operand (64 columns a row tile; its
+// low half stays in shared memory), S / P of two steps (2 x 64), O (128 a row
+// tile) -- 512 columns with two row tiles. K' and V' have two stages each.
+// With two row tiles a step is one of them and the streams take turns in the
+// tensor core; with one, steps are tiles, and the two S let the products of
+// one run under the softmax of the other.
 //
-// Warps: 0-3 softmax (a row a thread), 4 issues the products, 13 copies raw
-// tiles and finds their exponents, 5-12 build operands without meeting at a
-// barrier (14 warps leave 128 registers a thread; 17 would leave 96): one group's share of a record of the packed format (K: 4
-// tokens x 8 channels, V: 8 tokens x 4 channels) is four whole 16-byte units
-// of the swizzled operand rows, so a lane reads a record's words and writes
-// units.
+// Warps: 4 a row tile for the softmax (a row a thread), one that issues the
+// products, one that copies raw tiles and finds their exponents, 8 that build
+// operands without meeting at a barrier: one group's share of a record of the
+// packed format (K: 4 tokens x 8 channels, V: 8 tokens x 4 channels) is four
+// whole 16-byte units of the swizzled operand rows, so a lane reads a record's
+// words and writes units. Building costs about 3200 warp-instructions a tile,
+// a softmax tile 960: with one row tile the SM issues longer than the tensor
+// core multiplies, with two it does not.
 #include "prefix.cuh"
 
 #include "host_checks.h"
@@ -32,27 +38,30 @@ namespace kvarn {
 constexpr int kPkTok = 64;                       // tokens of a tile
 constexpr int kPkK = kPkTok * kD * 2;            // bytes of one 64 x 128 bf16 operand (two 64-channel blocks)
 constexpr int kPkV = kD * kPkTok * 2;            // 128 channel rows x 64 tokens, fp16
+constexpr int kPkQ = kPRows * kD * 2;            // 128 query rows, bf16
 constexpr int kRawStages = 4;
 constexpr int kBuildWarps = 8;
-constexpr int kPackedThreads = 32 * (6 + kBuildWarps);
+constexpr int kChunkCols = 64;
 constexpr float kLift = 7.f;                     // P up to 2^(8 + 7), small weights normal down to 2^-21
 
 struct PackedSmem {
     // ready: a raw tile's exponent is known; raw_empty: its operands are built
     uint64_t raw_full[kRawStages], ready[kRawStages], raw_empty[kRawStages];
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full, drained;
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], drained;
     uint32_t tmem;
     int stop;
     int vexp[4];                                  // e of the last tiles
 };
 
-template <int B, int BITS>
+template <int B, int BITS, int NT>   // NT: row tiles of a CTA
 struct PackedLayout {
+    static constexpr int kSoft = 4 * NT;                       // softmax warps
+    static constexpr int kThreads = 32 * (kSoft + 2 + kBuildWarps);
     static constexpr int HB = head_block_bytes(B, BITS);
     static constexpr int kBlocks = kPkTok / B;                 // blocks per tile
     static constexpr int kRaw = kBlocks * 2 * HB;              // bytes of a raw tile: (K, V) per block
     static constexpr int kHeader = (sizeof(PackedSmem) + 1023) / 1024 * 1024;
-    static constexpr size_t bytes = 1024 + kHeader + 4 * kPkK + 2 * kPkV + kRawStages * kRaw;
+    static constexpr size_t bytes = 1024 + kHeader + NT * kPkQ + 4 * kPkK + 2 * kPkV + kRawStages * kRaw;
 };
 
 // a b + c with 16-bit a and b (the low or the high half of a register) and
@@ -80,24 +89,27 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t w8, uint32_t 
     else return code4_s(w, w8, j);
 }
 
-template <int B, int BITS>
-__global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(PrefixArgs a) {
+template <int B, int BITS, int NT>
+__global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix_packed_kernel(PrefixArgs a) {
     wait_prior_grids();
-    using Lay = PackedLayout<B, BITS>;
+    using Lay = PackedLayout<B, BITS, NT>;
+    constexpr int kSoft = Lay::kSoft;
     extern __shared__ uint8_t raw_smem[];
     uint8_t* base = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
     PackedSmem& s = *reinterpret_cast<PackedSmem*>(base);
-    uint8_t* k_op = base + Lay::kHeader;          // [stage][hi, lo]
+    uint8_t* q_lo = base + Lay::kHeader;          // [row tile]
+    uint8_t* k_op = q_lo + NT * kPkQ;             // [stage][hi, lo]
     uint8_t* v_op = k_op + 4 * kPkK;              // [stage]
     uint8_t* raw = v_op + 2 * kPkV;               // [raw stage][block][K, V]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.z, R = a.batch * a.G, row0 = blockIdx.y * kPRows;
+    const int h = blockIdx.z, R = a.batch * a.G, row0 = blockIdx.y * NT * kPRows;
     const int max_len = a.n_blocks * B;
 
     const int most = prefix_most(a, max_len, lane);
     const int tiles = (most + kPkTok - 1) / kPkTok;
     const int t_beg = (int)((int64_t)tiles * blockIdx.x / a.splits), t_end = (int)((int64_t)tiles * (blockIdx.x + 1) / a.splits);
-    const int n = t_end - t_beg;
+    const int n = t_end - t_beg;                  // tiles
+    const int steps = NT * n;                     // step i: stream i % 2, tile i / NT
 
     if (tid == 0) {
         s.stop = 0;
@@ -114,18 +126,17 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_ready[i], 4);
         }
-        mbar_init(&s.o_full, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&s.o_full[i], 1);
         mbar_init(&s.drained, 1);
         fence_mbar_init();
     }
-    if (warp == 4) tmem_alloc(&s.tmem, 512);
-    // ---- query rows: rotated, split into two bf16 halves, row by row through
-    // shared memory (pitch 272 bytes) into tensor memory
+    if (warp == kSoft) tmem_alloc(&s.tmem, 512);
+    // ---- query rows: rotated, split into two bf16 halves; the high one row by
+    // row through shared memory (pitch 272 bytes) into tensor memory
     constexpr int kPitch = 272;
     uint8_t* q_hi = k_op;
-    uint8_t* q_lo = k_op + kPRows * kPitch;
-    static_assert(2 * kPRows * kPitch <= 4 * kPkK + 2 * kPkV, "query staging fits the operand stages");
-    for (int r = warp; r < kPRows; r += kPackedThreads / 32) {
+    static_assert(NT * kPRows * kPitch <= 4 * kPkK + 2 * kPkV, "query staging fits the operand stages");
+    for (int r = warp; r < NT * kPRows; r += Lay::kThreads / 32) {
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         const int row = row0 + r;
         if (row < R) {
@@ -148,27 +159,29 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
             lo[k] = *reinterpret_cast<const uint32_t*>(&y);
         }
         *reinterpret_cast<uint2*>(q_hi + r * kPitch + 8 * lane) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(q_lo + r * kPitch + 8 * lane) = make_uint2(lo[0], lo[1]);
+        *reinterpret_cast<uint2*>(q_lo + (r / kPRows) * kPkQ + (lane >> 4) * (kPkQ / 2) + swizzled(r % kPRows, (lane >> 1) & 7) +
+                                  8 * (lane & 1)) = make_uint2(lo[0], lo[1]);
     }
+    fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s.tmem;
     int* stop = &s.stop;
-    const uint32_t tm_q = tm, tm_s = tm + 128, tm_o = tm + 256;   // S of tile i at + 64 (i % 2)
-    if (warp < 4) {
-        const int r = warp * 32 + lane;
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    // Q of row tile w at + 64 w, S of stream w at + 64 w, O at + 128 w
+    const uint32_t tm_q = tm, tm_s = tm + 128, tm_o = tm + 256;
+    if (warp < kSoft) {
+        const uint8_t* src = q_hi + (warp * 32 + lane) * kPitch;
+        const uint32_t dst = tm_q + 64 * (warp >> 2) + ((uint32_t)((warp & 3) * 32) << 16);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const uint8_t* src = (c < 4 ? q_hi : q_lo) + r * kPitch + (c & 3) * 64;
+        for (int c = 0; c < 4; ++c) {
             uint32_t x[16];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint4 u = *reinterpret_cast<const uint4*>(src + 16 * i);
+                const uint4 u = *reinterpret_cast<const uint4*>(src + 64 * c + 16 * i);
                 x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
             }
-            tmem_st16(tm_q + 16 * c + lanes, x);
+            tmem_st16(dst + 16 * c, x);
         }
         tmem_wait_st();
     }
@@ -177,7 +190,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
     tc_fence_after();
 
     const int used = (most + B - 1) / B;          // blocks that hold a visible token
-    if (warp == 5 + kBuildWarps) {
+    if (warp == kSoft + 1) {
         // ---------------------------------------------------------- raw tiles and their exponents
         auto fetch = [&](int i) {
             const int st = i % kRawStages, b0 = (t_beg + i) * Lay::kBlocks;
@@ -248,10 +261,10 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
         if (*reinterpret_cast<volatile int*>(stop))
             for (int i = max(0, fetched - kRawStages); i < fetched; ++i)
                 mbar_wait_bounded(&s.raw_full[i % kRawStages], (i / kRawStages) & 1, kWaitLimit);
-    } else if (warp > 4) {
+    } else if (warp > kSoft) {
         // ---------------------------------------------------------- operands from codes
         // warp bw: group g of the 32 records of half sb, a record a lane
-        const int bw = warp - 5, g = bw & 3, sb = bw >> 2, ra = lane >> 2, rb = lane & 3;
+        const int bw = warp - (kSoft + 2), g = bw & 3, sb = bw >> 2, ra = lane >> 2, rb = lane & 3;
         const int half0 = B == 64 ? 32 * sb : 0;          // the half's first token within its block
         // (code 2^-9) s + z 2^-9, times the rest of the value's factors and 2^9
         constexpr float kUp = 512.f;
@@ -372,40 +385,40 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
                 warp_arrive(&s.raw_empty[st]);
             }
         }
-    } else if (warp == 4) {
+    } else if (warp == kSoft) {
         // ---------------------------------------------------------- products
-        if (n > 0) {
+        if (steps > 0) {
             constexpr uint32_t kQk = mma_shape(kMmaBf16, kPkTok, false), kPv = mma_shape(kMmaF16, kD, false);
-            const uint32_t k_desc = smem_operand(smem_addr(k_op), 16), v_desc = smem_operand(smem_addr(v_op), 16);
+            const uint32_t q_desc = smem_operand(smem_addr(q_lo), 16), k_desc = smem_operand(smem_addr(k_op), 16);
+            const uint32_t v_desc = smem_operand(smem_addr(v_op), 16);
             bool ok = true;
-            for (int i = 0; i < n + 2 && ok; ++i) {
-                if (i >= 2) {                                     // O (+)= P V' of tile i - 2
-                    const int j = i - 2, w = j & 1;
-                    ok = warp_wait_or_stop(&s.v_full[w], (j >> 1) & 1, stop, kWaitLimit);
-                    ok = ok && warp_wait_or_stop(&s.p_ready[w], (j >> 1) & 1, stop, kWaitLimit);
+            for (int i = 0; i < steps + 2 && ok; ++i) {
+                if (i >= 2) {                                     // O (+)= P V' of step i - 2
+                    const int j = i - 2, w = j & 1, t = j / NT, st = t & 1, x = NT == 2 ? w : 0;
+                    ok = warp_wait_or_stop(&s.v_full[st], (t >> 1) & 1, stop, kWaitLimit) &&
+                         warp_wait_or_stop(&s.p_ready[w], (j >> 1) & 1, stop, kWaitLimit);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t p = tm_s + 64 * w, vd = v_desc + w * (kPkV >> 4);
+                    const uint32_t p = tm_s + 64 * w, vd = v_desc + st * (kPkV >> 4);
 #pragma unroll
-                    for (int k = 0; k < kPkTok / 16; ++k) mma_ts(tm_o, p + 8 * k, vd + 2 * k, kPv, j > 0 || k > 0);
-                    mma_commit(&s.v_empty[w]);
-                    if (j + 1 == n) mma_commit(&s.o_full);
+                    for (int k = 0; k < kPkTok / 16; ++k) mma_ts(tm_o + 128 * x, p + 8 * k, vd + 2 * k, kPv, t > 0 || k > 0);
+                    if (NT == 1 || w == 1) mma_commit(&s.v_empty[st]);
+                    if (j + NT >= steps) mma_commit(&s.o_full[x]);
                 }
-                if (i < n) {                                      // S = Q K'^T of tile i
-                    const int w = i & 1;
-                    ok = warp_wait_or_stop(&s.k_full[w], (i >> 1) & 1, stop, kWaitLimit);
+                if (i < steps) {                                  // S = Q K'^T of step i
+                    const int w = i & 1, t = i / NT, st = t & 1, x = NT == 2 ? w : 0;
+                    ok = warp_wait_or_stop(&s.k_full[st], (t >> 1) & 1, stop, kWaitLimit);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t kd = k_desc + w * (2 * kPkK >> 4);
+                    const uint32_t kd = k_desc + st * (2 * kPkK >> 4), qa = tm_q + 64 * x, qd = q_desc + x * (kPkQ >> 4);
 #pragma unroll
-                    for (int part = 0; part < 3; ++part)          // hi hi, hi lo, lo hi
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_ts(tm_s + 64 * w, tm_q + (part == 2 ? 64 : 0) + 8 * k,
-                                   kd + (((part == 1 ? kPkK : 0) + (k >> 2) * (kPkK / 2) + (k & 3) * 32) >> 4), kQk,
-                                   part > 0 || k > 0);
+                    for (int k = 0; k < 24; ++k) {                // hi hi, hi lo, lo hi
+                        const uint32_t kb = kd + (((k >> 3) == 1 ? kPkK >> 4 : 0) + (((k >> 2 & 1) * (kPkK / 2) + (k & 3) * 32) >> 4));
+                        if (k < 16) mma_ts(tm_s + 64 * w, qa + 8 * (k & 7), kb, kQk, k > 0);
+                        else mma_ss(tm_s + 64 * w, qd + (((k >> 2 & 1) * (kPkQ / 2) + (k & 3) * 32) >> 4), kb, kQk, true);
+                    }
                     mma_commit(&s.s_full[w]);
-                    mma_commit(&s.k_empty[w]);
+                    if (NT == 1 || w == 1) mma_commit(&s.k_empty[st]);
                 }
             }
             // products in flight end before the operands and tensor memory go
@@ -414,29 +427,33 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
         }
     } else {
         // ---------------------------------------------------------- softmax
+        const int x = warp >> 2;                                  // row tile
         const int row = row0 + warp * 32 + lane;
         const bool real = row < R;
         const int len = real ? prefix_len(a.lens, row / a.G, max_len) : 0;
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        const uint32_t my_o = tm_o + lanes;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t my_o = tm_o + 128 * x + lanes;
         const float scale = a.sm_scale * kLog2e;
         RowState st{-INFINITY, 0.f};
         bool ok = true;
-        for (int i = 0; i < n && ok; ++i) {
-            ok = warp_wait_or_stop(&s.s_full[i & 1], (i >> 1) & 1, stop, kWaitLimit);
+        for (int i = 0; i < n && ok; ++i) {                       // tile
+            const int w = NT == 2 ? x : i & 1, j = NT == 2 ? i : i >> 1;
+            ok = warp_wait_or_stop(&s.s_full[w], j & 1, stop, kWaitLimit);
             if (!ok) break;
             tc_fence_after();
             const int e = *reinterpret_cast<volatile int*>(&s.vexp[i & 3]);
-            // O is idle once tile i - 1's product into it has freed its V stage
-            ok = softmax_tile<kPkTok, true>(tm_s + 64 * (i & 1) + lanes, my_o, len - (t_beg + i) * kPkTok, scale, (float)e,
-                                            exp2i(-e), kLift, i == 0, st, &s.p_ready[i & 1], [&] {
+            ok = softmax_tile<kPkTok, kChunkCols, true>(tm_s + 64 * w + lanes, my_o, len - (t_beg + i) * kPkTok, scale, (float)e,
+                                                        exp2i(-e), kLift, i == 0, st, &s.p_ready[w], [&] {
+                // O is idle once the last product into it has completed: with two row
+                // tiles S came behind it, with one it has freed tile i - 1's V stage
+                if (NT == 2) return true;
                 const bool idle = warp_wait_or_stop(&s.v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, stop, kWaitLimit);
                 tc_fence_after();
                 return idle;
             });
         }
         if (n > 0 && ok) {
-            ok = warp_wait_or_stop(&s.o_full, 0, stop, kWaitLimit);
+            ok = warp_wait_or_stop(&s.o_full[x], 0, stop, kWaitLimit);
             tc_fence_after();
         }
         if (ok) store_partial(a, blockIdx.x, row, h, real, n == 0, st.m - kLift, st.l, my_o);
@@ -444,29 +461,35 @@ __global__ void __launch_bounds__(kPackedThreads, 1) prefix_packed_kernel(Prefix
     }
     __syncthreads();
     if (tid == 0 && *stop) raise_error(a.err, KVARN_DEVERR_WAIT_TIMEOUT);
-    if (warp == 4) {
+    if (warp == kSoft) {
         tc_fence_after();
         tmem_free(tm, 512);
     }
 }
 
 // ---------------------------------------------------------------- host side
+template <int B, int BITS, int NT>
+cudaError_t launch_packed_tiles(const PrefixArgs& p, cudaStream_t st) {
+    using Lay = PackedLayout<B, BITS, NT>;
+    static_assert(Lay::bytes <= 227 * 1024, "shared memory of one CTA");
+    static bool ready[64];
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess) return e;
+    if (d < 0 || d >= 64) return cudaErrorInvalidDevice;
+    if (!ready[d]) {
+        e = cudaFuncSetAttribute(prefix_packed_kernel<B, BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::bytes);
+        if (e != cudaSuccess) return e;
+        ready[d] = true;
+    }
+    const dim3 grid(p.splits, (p.batch * p.G + NT * kPRows - 1) / (NT * kPRows), p.n_kv);
+    return launch_pdl(prefix_packed_kernel<B, BITS, NT>, grid, Lay::kThreads, Lay::bytes, st, p);
+}
+
 cudaError_t launch_prefix_packed(const kvarn_config& c, const PrefixArgs& p, cudaStream_t st) {
     return dispatch(c, [&](auto b, auto w) {
         constexpr int B = decltype(b)::value, BITS = decltype(w)::value;
-        constexpr size_t smem = PackedLayout<B, BITS>::bytes;
-        static bool ready[64];
-        int d = 0;
-        cudaError_t e = cudaGetDevice(&d);
-        if (e != cudaSuccess) return e;
-        if (d < 0 || d >= 64) return cudaErrorInvalidDevice;
-        if (!ready[d]) {
-            e = cudaFuncSetAttribute(prefix_packed_kernel<B, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-            ready[d] = true;
-        }
-        const dim3 grid(p.splits, (p.batch * p.G + kPRows - 1) / kPRows, p.n_kv);
-        return launch_pdl(prefix_packed_kernel<B, BITS>, grid, kPackedThreads, smem, st, p);
+        return (int64_t)p.batch * p.G > kPRows ? launch_packed_tiles<B, BITS, 2>(p, st) : launch_packed_tiles<B, BITS, 1>(p, st);
     });
 }
 
