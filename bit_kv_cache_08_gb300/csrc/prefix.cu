@@ -107,8 +107,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(AttnArgs
     if (mine) {
         float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
         const int n = np + (PL > 0 ? pm.splits : 0);
-        lse_list(p0, np, (int64_t)a.G * kPartialStride, pm.partials + gw * kPartialStride,
-                 (int64_t)a.batch * a.n_q * kPartialStride, n * part / parts, n * (part + 1) / parts, lane, m, l, acc);
+        const int64_t R = (int64_t)a.batch * a.G;
+        lse_list(p0, np, (int64_t)a.G * kPartialStride, pm.partials + partial_row(0, a.n_kv, h, R, (int64_t)b * a.G + g),
+                 partial_row(1, a.n_kv, 0, R, 0), n * part / parts, n * (part + 1) / parts, lane, m, l, acc);
         if (lane == 0) {
             slices[wp][0] = m;
             slices[wp][1] = l;

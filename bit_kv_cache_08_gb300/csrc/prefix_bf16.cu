@@ -42,6 +42,7 @@ struct Bf16Smem {
 };
 constexpr int kBf16Header = 1024;
 static_assert(sizeof(Bf16Smem) <= kBf16Header, "header");
+static_assert(8 * 32 * kPartialStride * 4 <= 5 * kOperand, "the partials' staging fits the operands' memory");
 
 // MODE 0: 256 rows; 1: 128 rows; 2: 128 rows, fp32 query in two halves
 constexpr int bf16_q_tiles(int mode) { return mode == 1 ? 1 : 2; }
@@ -84,40 +85,60 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
         fence_mbar_init();
     }
     if (warp == 8) tmem_alloc(&s.tmem, 512);
-    // ---- the query rows as swizzled operands (rows behind the batch: zeros)
-    for (int i = tid; i < kRowsCta * 16; i += 320) {
-        const int r = i >> 4, u = i & 15;              // row, 8-channel unit
-        const int row = row0 + r;
-        uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-        if (row < R) {
-            const int64_t at = ((int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G) * kD + 8 * u;
-            if (MODE == 2) {
-                const float* f = static_cast<const float*>(a.q) + at;
-                uint32_t* ph = reinterpret_cast<uint32_t*>(&hi);
-                uint32_t* pl = reinterpret_cast<uint32_t*>(&lo);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const __nv_bfloat162 x = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-                    const float2 xf = __bfloat1622float2(x);
-                    const __nv_bfloat162 y = __floats2bfloat162_rn(f[2 * k] - xf.x, f[2 * k + 1] - xf.y);
-                    ph[k] = *reinterpret_cast<const uint32_t*>(&x);
-                    pl[k] = *reinterpret_cast<const uint32_t*>(&y);
-                }
-            } else {
-                hi = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
-            }
-        }
-        uint8_t* dst = q_op + (r / kPRows) * kOperand + (u >> 3) * kHalfOperand + swizzled(r % kPRows, u & 7);
-        *reinterpret_cast<uint4*>(dst) = hi;
-        if (MODE == 2) *reinterpret_cast<uint4*>(dst + kOperand) = lo;
-    }
-    fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = s.tmem;
     int* stop = &s.stop;
     const uint32_t tm_s = tm, tm_o = tm + 256;         // S (and P) of stream w at + 128 w, O likewise
+
+    if (warp != 9) {
+        // ---- the query rows as swizzled operands (rows behind the batch:
+        // zeros), loads in batches, while warp 9 starts on the pages
+        constexpr int kBatch = MODE == 2 ? 4 : 8;
+        for (int i0 = tid; i0 < kRowsCta * 16; i0 += kBatch * 288) {
+            uint4 x[MODE == 2 ? 2 * kBatch : kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int i = i0 + j * 288, row = row0 + (i >> 4);   // 8-channel unit i % 16 of row i / 16
+                const int64_t at = ((int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G) * kD + 8 * (i & 15);
+                const bool there = i < kRowsCta * 16 && row < R;
+                if (MODE == 2) {
+                    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const float*>(a.q) + at);
+                    x[2 * j] = there ? src[0] : make_uint4(0, 0, 0, 0);
+                    x[2 * j + 1] = there ? src[1] : make_uint4(0, 0, 0, 0);
+                } else {
+                    x[j] = there ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at) : make_uint4(0, 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int i = i0 + j * 288, r = i >> 4, u = i & 15;
+                if (i >= kRowsCta * 16) break;
+                uint8_t* dst = q_op + (r / kPRows) * kOperand + (u >> 3) * kHalfOperand + swizzled(r % kPRows, u & 7);
+                if (MODE == 2) {
+                    const uint4 lo4 = x[2 * j], hi4 = x[2 * j + 1];
+                    const uint32_t f[8] = {lo4.x, lo4.y, lo4.z, lo4.w, hi4.x, hi4.y, hi4.z, hi4.w};
+                    uint32_t ph[4], pl[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 v = make_float2(__uint_as_float(f[2 * k]), __uint_as_float(f[2 * k + 1]));
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+                        const float2 bf = __bfloat1622float2(b);
+                        const __nv_bfloat162 c = __floats2bfloat162_rn(v.x - bf.x, v.y - bf.y);
+                        ph[k] = *reinterpret_cast<const uint32_t*>(&b);
+                        pl[k] = *reinterpret_cast<const uint32_t*>(&c);
+                    }
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+                    *reinterpret_cast<uint4*>(dst + kOperand) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+                } else {
+                    *reinterpret_cast<uint4*>(dst) = x[j];
+                }
+            }
+        }
+        fence_async_smem();
+        asm volatile("bar.sync 1, 288;" ::: "memory");
+    }
 
     if (warp == 9) {
         // ---------------------------------------------------------- page copies
@@ -213,8 +234,7 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
         const int w = warp >> 2;                                  // stream
         const int r = (MODE == 0 ? w * kPRows : 0) + (warp & 3) * 32 + lane;
         const int row = row0 + r;
-        const bool real = row < R;
-        const int len = real ? prefix_len(a.lens, row / a.G, max_len) : 0;
+        const int len = row < R ? prefix_len(a.lens, row / a.G, max_len) : 0;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t my_s = tm_s + 128 * w + lanes, my_o = tm_o + 128 * w + lanes;
         const float scale = a.sm_scale * kLog2e;
@@ -230,11 +250,13 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
             softmax_tile<kTileTok, kTileTok, false>(my_s, my_o, len - t * kTileTok, scale, 0.f, 1.f, 0.f, j == 0, st, &s.p_ready[w],
                                           [] { return true; });
         }
-        if (items > 0 && ok) {
-            ok = warp_wait_or_stop(&s.o_full[w], 0, stop, kWaitLimit);
-            tc_fence_after();
-        }
-        if (ok) store_partial(a, MODE == 0 ? blockIdx.x : 2 * blockIdx.x + w, row, h, real, items == 0, st.m, st.l, my_o);
+        // both streams' products are over before the operands' memory is reused
+        for (int x = 0; x < 2 && ok; ++x)
+            if (steps > x) ok = warp_wait_or_stop(&s.o_full[x], 0, stop, kWaitLimit);
+        tc_fence_after();
+        if (ok)
+            store_partials(a, MODE == 0 ? blockIdx.x : 2 * blockIdx.x + w, row - lane, h, q_op + warp * 32 * kPartialStride * 4,
+                           items == 0, st.m, st.l, my_o, lane);
         tc_fence_before();
     }
     __syncthreads();

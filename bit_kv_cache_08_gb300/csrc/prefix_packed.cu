@@ -41,13 +41,13 @@ constexpr int kPkV = kD * kPkTok * 2;            // 128 channel rows x 64 tokens
 constexpr int kPkQ = kPRows * kD * 2;            // 128 query rows, bf16
 constexpr int kRawStages = 4;
 constexpr int kBuildWarps = 8;
-constexpr int kChunkCols = 64;
+static_assert(2 * kPkV == kD * kD * 2, "the rotation matrix fits V's stages");
 constexpr float kLift = 7.f;                     // P up to 2^(8 + 7), small weights normal down to 2^-21
 
 struct PackedSmem {
     // ready: a raw tile's exponent is known; raw_empty: its operands are built
     uint64_t raw_full[kRawStages], ready[kRawStages], raw_empty[kRawStages];
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], drained;
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], q_done, drained;
     uint32_t tmem;
     int stop;
     int vexp[4];                                  // e of the last tiles
@@ -71,6 +71,9 @@ __device__ __forceinline__ float fma_half(uint32_t a, uint32_t b, float c, bool 
     float d;
     asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"(y), "f"(c));
     return d;
+}
+__device__ __forceinline__ uint32_t sign_word(uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3, int w) {
+    return w == 0 ? s0 : w == 1 ? s1 : w == 2 ? s2 : s3;
 }
 // c - a for a bf16 a.
 __device__ __forceinline__ float minus_bf16(uint32_t a, float c, bool high) {
@@ -99,7 +102,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
     PackedSmem& s = *reinterpret_cast<PackedSmem*>(base);
     uint8_t* q_lo = base + Lay::kHeader;          // [row tile]
     uint8_t* k_op = q_lo + NT * kPkQ;             // [stage][hi, lo]
-    uint8_t* v_op = k_op + 4 * kPkK;              // [stage]
+    uint8_t* v_op = k_op + 4 * kPkK;              // [stage]; first the rotation matrix
     uint8_t* raw = v_op + 2 * kPkV;               // [raw stage][block][K, V]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.z, R = a.batch * a.G, row0 = blockIdx.y * NT * kPRows;
@@ -127,42 +130,11 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
             mbar_init(&s.p_ready[i], 4);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&s.o_full[i], 1);
+        mbar_init(&s.q_done, 1);
         mbar_init(&s.drained, 1);
         fence_mbar_init();
     }
     if (warp == kSoft) tmem_alloc(&s.tmem, 512);
-    // ---- query rows: rotated, split into two bf16 halves; the high one row by
-    // row through shared memory (pitch 272 bytes) into tensor memory
-    constexpr int kPitch = 272;
-    uint8_t* q_hi = k_op;
-    static_assert(NT * kPRows * kPitch <= 4 * kPkK + 2 * kPkV, "query staging fits the operand stages");
-    for (int r = warp; r < NT * kPRows; r += Lay::kThreads / 32) {
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        const int row = row0 + r;
-        if (row < R) {
-            load_q4(a.q, a.q_dtype, (int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G, lane, v);
-            if (!(a.flags & KVARN_FLAG_NO_ROTATION)) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] *= sign_of4(a.sb[0], a.sb[1], a.sb[2], a.sb[3], 4 * lane + k);
-                fwht128(v, lane);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] *= kInvSqrtD;
-            }
-        }
-        uint32_t hi[2], lo[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-            const float2 xf = __bfloat1622float2(x);
-            const __nv_bfloat162 y = __floats2bfloat162_rn(v[2 * k] - xf.x, v[2 * k + 1] - xf.y);
-            hi[k] = *reinterpret_cast<const uint32_t*>(&x);
-            lo[k] = *reinterpret_cast<const uint32_t*>(&y);
-        }
-        *reinterpret_cast<uint2*>(q_hi + r * kPitch + 8 * lane) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(q_lo + (r / kPRows) * kPkQ + (lane >> 4) * (kPkQ / 2) + swizzled(r % kPRows, (lane >> 1) & 7) +
-                                  8 * (lane & 1)) = make_uint2(lo[0], lo[1]);
-    }
-    fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -170,24 +142,116 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
     int* stop = &s.stop;
     // Q of row tile w at + 64 w, S of stream w at + 64 w, O at + 128 w
     const uint32_t tm_q = tm, tm_s = tm + 128, tm_o = tm + 256;
-    if (warp < kSoft) {
-        const uint8_t* src = q_hi + (warp * 32 + lane) * kPitch;
-        const uint32_t dst = tm_q + 64 * (warp >> 2) + ((uint32_t)((warp & 3) * 32) << 16);
+    const int q_parts = a.q_dtype == KVARN_FP32 ? 2 : 1;
+    if (warp <= kSoft) {
+        // ---- the query rows, while the other warps start on the tiles: the
+        // rotation H (sigma q) / sqrt(128) is itself a product on the tensor
+        // core, exact in its operands (signs, and q in bf16 or as two bf16
+        // halves, one after the other); without rotation H is the identity.
+        // Then its rows are split into two bf16 halves: the high one to tensor
+        // memory, the low one to its operand. (A row a warp or a thread through
+        // butterflies took 7-14 us of a call.)
+        constexpr int kQThreads = 32 * (kSoft + 1), kBatch = 4;
+        const bool rotate = !(a.flags & KVARN_FLAG_NO_ROTATION);
+        bool ok = true;
+        for (int i = tid; i < kD * 16; i += kQThreads) {                 // H, in V's first stages
+            const int r = i >> 4, u = i & 15;
+            uint32_t w[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t x[16];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 u = *reinterpret_cast<const uint4*>(src + 64 * c + 16 * i);
-                x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
+            for (int k = 0; k < 4; ++k) {
+                const int c = 8 * u + 2 * k;
+                w[k] = rotate ? 0x3f803f80u ^ (__popc(r & c) & 1) << 15 ^ (uint32_t)(__popc(r & (c + 1)) & 1) << 31
+                              : (r == c ? 0x3f80u : 0u) | (r == c + 1 ? 0x3f800000u : 0u);
             }
-            tmem_st16(dst + 16 * c, x);
+            *reinterpret_cast<uint4*>(v_op + (u >> 3) * (kPkQ / 2) + swizzled(r, u & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        tmem_wait_st();
+        for (int part = 0; part < q_parts && ok; ++part) {
+            for (int i0 = tid; i0 < NT * kPRows * 16; i0 += kBatch * kQThreads) {
+                uint4 x[kBatch], y[kBatch];                              // (y: channels 4 .. 7 of an fp32 unit)
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int i = i0 + j * kQThreads, row = row0 + (i >> 4);
+                    const int64_t at = ((int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G) * kD + 8 * (i & 15);
+                    x[j] = y[j] = make_uint4(0, 0, 0, 0);
+                    if (i < NT * kPRows * 16 && row < R) {
+                        const char* src = static_cast<const char*>(a.q) + at * (q_parts == 2 ? 4 : 2);
+                        x[j] = *reinterpret_cast<const uint4*>(src);
+                        if (q_parts == 2) y[j] = *reinterpret_cast<const uint4*>(src + 16);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int i = i0 + j * kQThreads, r = i >> 4, u = i & 15;
+                    if (i >= NT * kPRows * 16) break;
+                    uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                    if (q_parts == 2) {
+                        const uint32_t f[8] = {x[j].x, x[j].y, x[j].z, x[j].w, y[j].x, y[j].y, y[j].z, y[j].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float f0 = __uint_as_float(f[2 * k]), f1 = __uint_as_float(f[2 * k + 1]);
+                            __nv_bfloat162 b = __floats2bfloat162_rn(f0, f1);
+                            if (part == 1) {
+                                const uint32_t hi = *reinterpret_cast<const uint32_t*>(&b);
+                                b = __floats2bfloat162_rn(minus_bf16(hi, f0, false), minus_bf16(hi, f1, true));
+                            }
+                            w[k] = *reinterpret_cast<const uint32_t*>(&b);
+                        }
+                    }
+                    const uint32_t sg = rotate ? sign_word(a.sb[0], a.sb[1], a.sb[2], a.sb[3], u >> 2) >> (8 * (u & 3)) : 0u;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] ^= (sg >> (2 * k) & 1u) << 15 | (sg >> (2 * k + 1) & 1u) << 31;
+                    *reinterpret_cast<uint4*>(q_lo + (r / kPRows) * kPkQ + (u >> 3) * (kPkQ / 2) + swizzled(r % kPRows, u & 7)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            fence_async_smem();
+            asm volatile("bar.sync 1, %0;" ::"n"(kQThreads) : "memory");
+            if (warp == kSoft) {
+                constexpr uint32_t kRot = mma_shape(kMmaBf16, kD, false);
+                const uint32_t q_desc = smem_operand(smem_addr(q_lo), 16), h_desc = smem_operand(smem_addr(v_op), 16);
+#pragma unroll 1
+                for (int k = 0; k < 8 * NT; ++k) {
+                    const uint32_t off = ((k >> 2 & 1) * (kPkQ / 2) + (k & 3) * 32) >> 4;
+                    mma_ss(tm_o + 128 * (k >> 3), q_desc + (k >> 3) * (kPkQ >> 4) + off, h_desc + off, kRot, part > 0 || (k & 7) > 0);
+                }
+                mma_commit(&s.q_done);
+            }
+            ok = warp_wait_or_stop(&s.q_done, part, stop, kWaitLimit);
+            tc_fence_after();
+        }
+        if (warp < kSoft && ok) {
+            const float norm = rotate ? kInvSqrtD : 1.f;
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            uint8_t* lo_row = q_lo + (warp >> 2) * kPkQ;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {                                // 32 channels
+                uint32_t v[32];
+                tmem_ld32(tm_o + 128 * (warp >> 2) + 32 * c + lanes, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t lo[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float x0 = __uint_as_float(v[8 * u + 2 * k]) * norm, x1 = __uint_as_float(v[8 * u + 2 * k + 1]) * norm;
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(x0, x1);
+                        const uint32_t hi = *reinterpret_cast<const uint32_t*>(&x);
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(minus_bf16(hi, x0, false), minus_bf16(hi, x1, true));
+                        lo[k] = *reinterpret_cast<const uint32_t*>(&y);
+                        v[4 * u + k] = hi;
+                    }
+                    *reinterpret_cast<uint4*>(lo_row + (c >> 1) * (kPkQ / 2) + swizzled((warp & 3) * 32 + lane, 4 * (c & 1) + u)) =
+                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                tmem_st16(tm_q + 64 * (warp >> 2) + 16 * c + lanes, v);
+            }
+            tmem_wait_st();
+            fence_async_smem();
+        }
+        tc_fence_before();
+        asm volatile("bar.sync 1, %0;" ::"n"(kQThreads) : "memory");   // the product warp waits for the rows
+        tc_fence_after();
     }
-    tc_fence_before();
-    __syncthreads();   // (the staging is free for operands)
-    tc_fence_after();
 
     const int used = (most + B - 1) / B;          // blocks that hold a visible token
     if (warp == kSoft + 1) {
@@ -364,6 +428,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                 const float2 c01 = __half22float2(u32_as_h2(cu.x)), c23 = __half22float2(u32_as_h2(cu.y));
                 const float cf[4] = {c01.x, c01.y, c23.x, c23.y};
                 if (i >= 2) ok = warp_wait_or_stop(&s.v_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
+                for (int k = 0; k < q_parts && i == 0 && ok; ++k) ok = warp_wait_or_stop(&s.q_done, k, stop, kWaitLimit);   // (H was here)
                 if (!ok) break;
                 uint8_t* dst = v_op + par * kPkV;
 #pragma unroll
@@ -429,8 +494,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
         // ---------------------------------------------------------- softmax
         const int x = warp >> 2;                                  // row tile
         const int row = row0 + warp * 32 + lane;
-        const bool real = row < R;
-        const int len = real ? prefix_len(a.lens, row / a.G, max_len) : 0;
+        const int len = row < R ? prefix_len(a.lens, row / a.G, max_len) : 0;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t my_o = tm_o + 128 * x + lanes;
         const float scale = a.sm_scale * kLog2e;
@@ -442,7 +506,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
             if (!ok) break;
             tc_fence_after();
             const int e = *reinterpret_cast<volatile int*>(&s.vexp[i & 3]);
-            ok = softmax_tile<kPkTok, kChunkCols, true>(tm_s + 64 * w + lanes, my_o, len - (t_beg + i) * kPkTok, scale, (float)e,
+            ok = softmax_tile<kPkTok, NT == 2 ? 32 : 64, true>(tm_s + 64 * w + lanes, my_o, len - (t_beg + i) * kPkTok, scale, (float)e,
                                                         exp2i(-e), kLift, i == 0, st, &s.p_ready[w], [&] {
                 // O is idle once the last product into it has completed: with two row
                 // tiles S came behind it, with one it has freed tile i - 1's V stage
@@ -452,11 +516,10 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                 return idle;
             });
         }
-        if (n > 0 && ok) {
-            ok = warp_wait_or_stop(&s.o_full[x], 0, stop, kWaitLimit);
-            tc_fence_after();
-        }
-        if (ok) store_partial(a, blockIdx.x, row, h, real, n == 0, st.m - kLift, st.l, my_o);
+        // every stream's products are over before the operands' memory is reused
+        for (int k = 0; k < NT && n > 0 && ok; ++k) ok = warp_wait_or_stop(&s.o_full[k], 0, stop, kWaitLimit);
+        tc_fence_after();
+        if (ok) store_partials(a, blockIdx.x, row - lane, h, q_lo + warp * 32 * kPartialStride * 4, n == 0, st.m - kLift, st.l, my_o, lane);
         tc_fence_before();
     }
     __syncthreads();
@@ -472,6 +535,7 @@ template <int B, int BITS, int NT>
 cudaError_t launch_packed_tiles(const PrefixArgs& p, cudaStream_t st) {
     using Lay = PackedLayout<B, BITS, NT>;
     static_assert(Lay::bytes <= 227 * 1024, "shared memory of one CTA");
+    static_assert(Lay::kSoft * 32 * kPartialStride * 4 <= NT * kPkQ + 4 * kPkK + 2 * kPkV, "the partials' staging fits the operands' memory");
     static bool ready[64];
     int d = 0;
     cudaError_t e = cudaGetDevice(&d);

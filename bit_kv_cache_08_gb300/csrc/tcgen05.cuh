@@ -159,4 +159,14 @@ __device__ __forceinline__ void tile_g2s(void* dst, const void* map, int x, int 
         : "memory");
 }
 
+// Bulk copy shared -> global (16-byte aligned, a multiple of 16 bytes), and
+// the wait until the copies of this thread have been written.
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+    asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 }  // namespace kvarn
