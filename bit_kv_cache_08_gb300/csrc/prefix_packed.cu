@@ -142,83 +142,108 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
     int* stop = &s.stop;
     // Q of row tile w at + 64 w, S of stream w at + 64 w, O at + 128 w
     const uint32_t tm_q = tm, tm_s = tm + 128, tm_o = tm + 256;
-    const int q_parts = a.q_dtype == KVARN_FP32 ? 2 : 1;
+    const int used = (most + B - 1) / B;          // blocks that hold a visible token
+    auto fetch = [&](int i) {                     // (the raw tiles' warp) tile i into its stage
+        const int st = i % kRawStages, b0 = (t_beg + i) * Lay::kBlocks;
+        int64_t page = -1;                        // lane x: block x of the tile
+        if (lane < Lay::kBlocks && b0 + lane < used) {
+            page = a.table[b0 + lane];
+            if (page < 0 || page >= a.n_pool_blocks) {
+                raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
+                page = -1;
+            }
+        }
+        const uint32_t bytes = __popc(__ballot_sync(kFull, page >= 0)) * (2 * Lay::HB);
+        if (lane == 0) mbar_arrive_expect_tx(&s.raw_full[st], bytes);
+        __syncwarp();
+        if (page >= 0)
+            bulk_g2s(raw + st * Lay::kRaw + lane * 2 * Lay::HB, a.pool + page * a.block_bytes + (int64_t)(2 * h) * Lay::HB,
+                     2 * Lay::HB, &s.raw_full[st]);
+    };
+    int fetched = 0;
+    if (warp == kSoft + 1)
+        for (; fetched < kRawStages - 1 && fetched < n; ++fetched) fetch(fetched);
+
+    // ---- the query rows: their rotation H (sigma q) / sqrt(128) is itself a
+    // product on the tensor core, exact in its operands (signs, and q in bf16,
+    // or as two bf16 halves of an fp32 one); without rotation H is the identity.
+    // Then the rows are split into two bf16 halves: the high one to tensor
+    // memory, the low one to its operand. (A row a warp or a thread through
+    // butterflies took 7-14 us of a call.)
+    const bool q32 = a.q_dtype == KVARN_FP32, rotate = !(a.flags & KVARN_FLAG_NO_ROTATION);
+    {
+        constexpr int kBatch = 4;
+        for (int i0 = tid; i0 < NT * kPRows * 16; i0 += kBatch * Lay::kThreads) {
+            uint4 x[kBatch], y[kBatch];                                  // (y: channels 4 .. 7 of an fp32 unit)
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int i = i0 + j * Lay::kThreads, row = row0 + (i >> 4);
+                const int64_t at = ((int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G) * kD + 8 * (i & 15);
+                x[j] = y[j] = make_uint4(0, 0, 0, 0);
+                if (i < NT * kPRows * 16 && row < R) {
+                    const char* src = static_cast<const char*>(a.q) + at * (q32 ? 4 : 2);
+                    x[j] = *reinterpret_cast<const uint4*>(src);
+                    if (q32) y[j] = *reinterpret_cast<const uint4*>(src + 16);
+                }
+            }
+            if (i0 == tid)                                               // H, in V's first stages, under the loads
+                for (int i = tid; i < kD * 16; i += Lay::kThreads) {
+                    const int r = i >> 4, u = i & 15;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = 8 * u + 2 * k;
+                        w[k] = rotate ? 0x3f803f80u ^ (__popc(r & c) & 1) << 15 ^ (uint32_t)(__popc(r & (c + 1)) & 1) << 31
+                                      : (r == c ? 0x3f80u : 0u) | (r == c + 1 ? 0x3f800000u : 0u);
+                    }
+                    *reinterpret_cast<uint4*>(v_op + (u >> 3) * (kPkQ / 2) + swizzled(r, u & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int i = i0 + j * Lay::kThreads, r = i >> 4, u = i & 15;
+                if (i >= NT * kPRows * 16) break;
+                uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w}, lo[4];
+                if (q32) {
+                    const uint32_t f[8] = {x[j].x, x[j].y, x[j].z, x[j].w, y[j].x, y[j].y, y[j].z, y[j].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float f0 = __uint_as_float(f[2 * k]), f1 = __uint_as_float(f[2 * k + 1]);
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(f0, f1);
+                        w[k] = *reinterpret_cast<const uint32_t*>(&b);
+                        const __nv_bfloat162 c = __floats2bfloat162_rn(minus_bf16(w[k], f0, false), minus_bf16(w[k], f1, true));
+                        lo[k] = *reinterpret_cast<const uint32_t*>(&c);
+                    }
+                }
+                const uint32_t sg = rotate ? sign_word(a.sb[0], a.sb[1], a.sb[2], a.sb[3], u >> 2) >> (8 * (u & 3)) : 0u;
+                const uint32_t at = (r / kPRows) * kPkQ + (u >> 3) * (kPkQ / 2) + swizzled(r % kPRows, u & 7);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t flip = (sg >> (2 * k) & 1u) << 15 | (sg >> (2 * k + 1) & 1u) << 31;
+                    w[k] ^= flip;
+                    if (q32) lo[k] ^= flip;
+                }
+                *reinterpret_cast<uint4*>(q_lo + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (q32) *reinterpret_cast<uint4*>(k_op + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);   // in K's stages
+            }
+        }
+    }
+    fence_async_smem();
+    __syncthreads();
     if (warp <= kSoft) {
-        // ---- the query rows, while the other warps start on the tiles: the
-        // rotation H (sigma q) / sqrt(128) is itself a product on the tensor
-        // core, exact in its operands (signs, and q in bf16 or as two bf16
-        // halves, one after the other); without rotation H is the identity.
-        // Then its rows are split into two bf16 halves: the high one to tensor
-        // memory, the low one to its operand. (A row a warp or a thread through
-        // butterflies took 7-14 us of a call.)
-        constexpr int kQThreads = 32 * (kSoft + 1), kBatch = 4;
-        const bool rotate = !(a.flags & KVARN_FLAG_NO_ROTATION);
-        bool ok = true;
-        for (int i = tid; i < kD * 16; i += kQThreads) {                 // H, in V's first stages
-            const int r = i >> 4, u = i & 15;
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int c = 8 * u + 2 * k;
-                w[k] = rotate ? 0x3f803f80u ^ (__popc(r & c) & 1) << 15 ^ (uint32_t)(__popc(r & (c + 1)) & 1) << 31
-                              : (r == c ? 0x3f80u : 0u) | (r == c + 1 ? 0x3f800000u : 0u);
-            }
-            *reinterpret_cast<uint4*>(v_op + (u >> 3) * (kPkQ / 2) + swizzled(r, u & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        for (int part = 0; part < q_parts && ok; ++part) {
-            for (int i0 = tid; i0 < NT * kPRows * 16; i0 += kBatch * kQThreads) {
-                uint4 x[kBatch], y[kBatch];                              // (y: channels 4 .. 7 of an fp32 unit)
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const int i = i0 + j * kQThreads, row = row0 + (i >> 4);
-                    const int64_t at = ((int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G) * kD + 8 * (i & 15);
-                    x[j] = y[j] = make_uint4(0, 0, 0, 0);
-                    if (i < NT * kPRows * 16 && row < R) {
-                        const char* src = static_cast<const char*>(a.q) + at * (q_parts == 2 ? 4 : 2);
-                        x[j] = *reinterpret_cast<const uint4*>(src);
-                        if (q_parts == 2) y[j] = *reinterpret_cast<const uint4*>(src + 16);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const int i = i0 + j * kQThreads, r = i >> 4, u = i & 15;
-                    if (i >= NT * kPRows * 16) break;
-                    uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                    if (q_parts == 2) {
-                        const uint32_t f[8] = {x[j].x, x[j].y, x[j].z, x[j].w, y[j].x, y[j].y, y[j].z, y[j].w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float f0 = __uint_as_float(f[2 * k]), f1 = __uint_as_float(f[2 * k + 1]);
-                            __nv_bfloat162 b = __floats2bfloat162_rn(f0, f1);
-                            if (part == 1) {
-                                const uint32_t hi = *reinterpret_cast<const uint32_t*>(&b);
-                                b = __floats2bfloat162_rn(minus_bf16(hi, f0, false), minus_bf16(hi, f1, true));
-                            }
-                            w[k] = *reinterpret_cast<const uint32_t*>(&b);
-                        }
-                    }
-                    const uint32_t sg = rotate ? sign_word(a.sb[0], a.sb[1], a.sb[2], a.sb[3], u >> 2) >> (8 * (u & 3)) : 0u;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) w[k] ^= (sg >> (2 * k) & 1u) << 15 | (sg >> (2 * k + 1) & 1u) << 31;
-                    *reinterpret_cast<uint4*>(q_lo + (r / kPRows) * kPkQ + (u >> 3) * (kPkQ / 2) + swizzled(r % kPRows, u & 7)) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
-            fence_async_smem();
-            asm volatile("bar.sync 1, %0;" ::"n"(kQThreads) : "memory");
-            if (warp == kSoft) {
-                constexpr uint32_t kRot = mma_shape(kMmaBf16, kD, false);
-                const uint32_t q_desc = smem_operand(smem_addr(q_lo), 16), h_desc = smem_operand(smem_addr(v_op), 16);
+        if (warp == kSoft) {
+            constexpr uint32_t kRot = mma_shape(kMmaBf16, kD, false);
+            const uint32_t q_desc = smem_operand(smem_addr(q_lo), 16), l_desc = smem_operand(smem_addr(k_op), 16);
+            const uint32_t h_desc = smem_operand(smem_addr(v_op), 16);
 #pragma unroll 1
-                for (int k = 0; k < 8 * NT; ++k) {
-                    const uint32_t off = ((k >> 2 & 1) * (kPkQ / 2) + (k & 3) * 32) >> 4;
-                    mma_ss(tm_o + 128 * (k >> 3), q_desc + (k >> 3) * (kPkQ >> 4) + off, h_desc + off, kRot, part > 0 || (k & 7) > 0);
-                }
-                mma_commit(&s.q_done);
+            for (int k = 0; k < (q32 ? 16 : 8) * NT; ++k) {
+                const int part = k / (8 * NT), x = k / 8 % NT;
+                const uint32_t off = ((k >> 2 & 1) * (kPkQ / 2) + (k & 3) * 32) >> 4;
+                mma_ss(tm_o + 128 * x, (part ? l_desc : q_desc) + x * (kPkQ >> 4) + off, h_desc + off, kRot, part > 0 || (k & 7) > 0);
             }
-            ok = warp_wait_or_stop(&s.q_done, part, stop, kWaitLimit);
-            tc_fence_after();
+            mma_commit(&s.q_done);
         }
+        const bool ok = warp_wait_or_stop(&s.q_done, 0, stop, kWaitLimit);
+        tc_fence_after();
         if (warp < kSoft && ok) {
             const float norm = rotate ? kInvSqrtD : 1.f;
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -249,31 +274,12 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
             fence_async_smem();
         }
         tc_fence_before();
-        asm volatile("bar.sync 1, %0;" ::"n"(kQThreads) : "memory");   // the product warp waits for the rows
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * (kSoft + 1)) : "memory");   // the product warp waits for the rows
         tc_fence_after();
     }
 
-    const int used = (most + B - 1) / B;          // blocks that hold a visible token
     if (warp == kSoft + 1) {
         // ---------------------------------------------------------- raw tiles and their exponents
-        auto fetch = [&](int i) {
-            const int st = i % kRawStages, b0 = (t_beg + i) * Lay::kBlocks;
-            int64_t page = -1;                    // lane x: block x of the tile
-            if (lane < Lay::kBlocks && b0 + lane < used) {
-                page = a.table[b0 + lane];
-                if (page < 0 || page >= a.n_pool_blocks) {
-                    raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
-                    page = -1;
-                }
-            }
-            const uint32_t bytes = __popc(__ballot_sync(kFull, page >= 0)) * (2 * Lay::HB);
-            if (lane == 0) mbar_arrive_expect_tx(&s.raw_full[st], bytes);
-            __syncwarp();
-            if (page >= 0)
-                bulk_g2s(raw + st * Lay::kRaw + lane * 2 * Lay::HB, a.pool + page * a.block_bytes + (int64_t)(2 * h) * Lay::HB,
-                         2 * Lay::HB, &s.raw_full[st]);
-        };
-        int fetched = 0;
         bool ok = true;
         for (int i = 0; i < n && ok; ++i) {
             // (one stage less in flight than there are: its wait is for tile i - 2)
@@ -370,6 +376,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                 float2 cc[4] = {__half22float2(u32_as_h2(cu.x)), __half22float2(u32_as_h2(cu.y)),
                                 __half22float2(u32_as_h2(cu.z)), __half22float2(u32_as_h2(cu.w))};
                 if (i >= 2) ok = warp_wait_or_stop(&s.k_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
+                if (i == 0 && q32) ok = warp_wait_or_stop(&s.q_done, 0, stop, kWaitLimit);   // (the query's low half was here)
                 if (!ok) break;
                 uint8_t* dst = k_op + par * 2 * kPkK + (g >> 1) * (kPkK / 2);
 #pragma unroll
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                 const float2 c01 = __half22float2(u32_as_h2(cu.x)), c23 = __half22float2(u32_as_h2(cu.y));
                 const float cf[4] = {c01.x, c01.y, c23.x, c23.y};
                 if (i >= 2) ok = warp_wait_or_stop(&s.v_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
-                for (int k = 0; k < q_parts && i == 0 && ok; ++k) ok = warp_wait_or_stop(&s.q_done, k, stop, kWaitLimit);   // (H was here)
+                if (i == 0) ok = warp_wait_or_stop(&s.q_done, 0, stop, kWaitLimit);   // (H was here)
                 if (!ok) break;
                 uint8_t* dst = v_op + par * kPkV;
 #pragma unroll
