@@ -84,7 +84,6 @@ __host__ __device__ constexpr int pex_rot(int B, int r) { return B == 64 ? 16 * 
 template <int B, int BITS, int S>
 __device__ __forceinline__ void decode_attn_2bit_body(const AttnArgs& a) {
     static_assert(BITS >= 2 && BITS <= 4, "2-, 3- or 4-bit codes");
-    wait_prior_grids();
     constexpr int HB = head_block_bytes(B, BITS);
     constexpr int RW = 4 * BITS;             // 32-bit words per lane record
     constexpr int NSB = B / 32;
@@ -672,13 +671,19 @@ __device__ __forceinline__ void decode_attn_2bit_body(const AttnArgs& a) {
 
 // The split kernel at ptxas's own register target, and with a minimum of
 // MINB resident CTAs per SM (at most 65536 / (32 MINB) registers a thread).
-template <int B, int BITS, int S>
+// LATE: behind a kernel that lets this one start beside it (see
+// let_next_grid_start), the wait comes last.
+template <int B, int BITS, int S, bool LATE>
 __global__ void __launch_bounds__(32) decode_attn_2bit_kernel(AttnArgs a) {
+    if (!LATE) wait_prior_grids();
     decode_attn_2bit_body<B, BITS, S>(a);
+    if (LATE) wait_prior_grids();
 }
-template <int B, int BITS, int S, int MINB>
+template <int B, int BITS, int S, int MINB, bool LATE>
 __global__ void __launch_bounds__(32, MINB) decode_attn_2bit_kernel_minb(AttnArgs a) {
+    if (!LATE) wait_prior_grids();
     decode_attn_2bit_body<B, BITS, S>(a);
+    if (LATE) wait_prior_grids();
 }
 
 // ---------------------------------------------------------------- host side
@@ -696,11 +701,11 @@ constexpr int stages_for() { return 2; }
 template <int B, int BITS>
 constexpr int attn_min_ctas() { return BITS != 3 ? 0 : (B == 64 ? 1 : 16); }
 
-template <int B, int BITS>
+template <int B, int BITS, bool LATE>
 constexpr auto attn_kernel_fn() {
     constexpr int S = stages_for<B, BITS>(), M = attn_min_ctas<B, BITS>();
-    if constexpr (M > 0) return decode_attn_2bit_kernel_minb<B, BITS, S, M>;
-    else return decode_attn_2bit_kernel<B, BITS, S>;
+    if constexpr (M > 0) return decode_attn_2bit_kernel_minb<B, BITS, S, M, LATE>;
+    else return decode_attn_2bit_kernel<B, BITS, S, LATE>;
 }
 
 template <int B, int BITS>
@@ -712,7 +717,8 @@ size_t attn_smem_bytes() {
 template <int B, int BITS>
 struct AttnKernel {
     static constexpr int kB = B;
-    static constexpr auto fn = attn_kernel_fn<B, BITS>();
+    static constexpr auto fn = attn_kernel_fn<B, BITS, false>();
+    static constexpr auto late = attn_kernel_fn<B, BITS, true>();
     static size_t smem() { return attn_smem_bytes<B, BITS>(); }
 };
 
@@ -742,11 +748,12 @@ int attn_grid_warps(int block_size, int bits, int device) {
 }
 
 // The arguments of a decode launch, and its split kernel alone (the caller
-// merges: launch_decode_attn, or the shared-prefix attention).
+// merges: launch_decode_attn, or the shared-prefix attention, behind whose
+// prefix kernel it starts early).
 cudaError_t launch_decode_split(const kvarn_config& cfg, const void* q, int q_dtype, const void* pool,
                                int64_t n_pool_blocks, int64_t block_bytes, const void* staging,
                                const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
-                               int batch, float* out, void* workspace, int nw, AttnArgs* args,
+                               int batch, float* out, void* workspace, int nw, bool late, AttnArgs* args,
                                 cudaStream_t st) {
     AttnArgs& a = *args;
     a = {};
@@ -782,7 +789,7 @@ cudaError_t launch_decode_split(const kvarn_config& cfg, const void* q, int q_dt
     for (int i = 0; i < 4; ++i) a.sb[i] = cfg.sign_bits[i];
     return with_attn_kernel(cfg.block_size, cfg.bits, [&](auto k) {
         using K = decltype(k);
-        return launch_pdl(K::fn, nw, 32, K::smem(), st, a);
+        return launch_pdl(late ? K::late : K::fn, nw, 32, K::smem(), st, a);
     });
 }
 
@@ -792,7 +799,7 @@ cudaError_t launch_decode_attn(const kvarn_config& cfg, const void* q, int q_dty
                                int batch, float* out, void* workspace, int nw, cudaStream_t st) {
     AttnArgs a;
     const cudaError_t e = launch_decode_split(cfg, q, q_dtype, pool, n_pool_blocks, block_bytes, staging, block_table,
-                                              max_blocks, seq_lens, batch, out, workspace, nw, &a, st);
+                                              max_blocks, seq_lens, batch, out, workspace, nw, false, &a, st);
     if (e != cudaSuccess) return e;
     // up to one wave of wide CTAs (4 per SM), so that 8 warps share each
     // row's raw tail rows

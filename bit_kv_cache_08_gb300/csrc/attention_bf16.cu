@@ -52,8 +52,7 @@ __device__ __forceinline__ void split_bf16x2(float v0, float v1, uint32_t& hi, u
 }
 
 template <int B>
-__global__ void __launch_bounds__(32) decode_attn_bf16_kernel(AttnArgs a) {
-    wait_prior_grids();
+__device__ __forceinline__ void decode_attn_bf16_body(const AttnArgs& a) {
     constexpr int CPB = B / kChunk;   // chunks per page
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t* stages = smem;
@@ -254,6 +253,14 @@ __global__ void __launch_bounds__(32) decode_attn_bf16_kernel(AttnArgs a) {
     }
 }
 
+// LATE: behind a kernel that lets this one start beside it, the wait comes last.
+template <int B, bool LATE>
+__global__ void __launch_bounds__(32) decode_attn_bf16_kernel(AttnArgs a) {
+    if (!LATE) wait_prior_grids();
+    decode_attn_bf16_body<B>(a);
+    if (LATE) wait_prior_grids();
+}
+
 size_t attn_bf16_smem_bytes() { return (size_t)kBfStages * kStageBytes + 64; }
 
 int attn_bf16_grid_warps(int block_size, int device) {
@@ -264,9 +271,9 @@ int attn_bf16_grid_warps(int block_size, int device) {
     int sms = 0, per_sm = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 0;
     cudaError_t e = block_size == 32
-                        ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_attn_bf16_kernel<32>, 32,
+                        ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_attn_bf16_kernel<32, false>, 32,
                                                                         attn_bf16_smem_bytes())
-                        : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_attn_bf16_kernel<64>, 32,
+                        : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_attn_bf16_kernel<64, false>, 32,
                                                                         attn_bf16_smem_bytes());
     if (e != cudaSuccess || per_sm <= 0) return 0;
     cache[bi][device] = sms * per_sm;
@@ -277,7 +284,7 @@ int attn_bf16_grid_warps(int block_size, int device) {
 cudaError_t launch_decode_split_bf16(const kvarn_config& cfg, const void* q, int q_dtype, const void* kv_pool,
                                     int64_t n_pool_blocks, const int32_t* block_table, int max_blocks,
                                     const int32_t* seq_lens, int batch, float* out, void* workspace, int nw,
-                                     AttnArgs* args, cudaStream_t st) {
+                                     bool late, AttnArgs* args, cudaStream_t st) {
     AttnArgs& a = *args;
     a = {};
     a.q = q;
@@ -306,8 +313,10 @@ cudaError_t launch_decode_split_bf16(const kvarn_config& cfg, const void* q, int
     a.flags = cfg.flags;
     for (int i = 0; i < 4; ++i) a.sb[i] = cfg.sign_bits[i];
     if (cfg.block_size == 32)
-        return launch_pdl(decode_attn_bf16_kernel<32>, nw, 32, attn_bf16_smem_bytes(), st, a);
-    return launch_pdl(decode_attn_bf16_kernel<64>, nw, 32, attn_bf16_smem_bytes(), st, a);
+        return launch_pdl(late ? decode_attn_bf16_kernel<32, true> : decode_attn_bf16_kernel<32, false>, nw, 32,
+                          attn_bf16_smem_bytes(), st, a);
+    return launch_pdl(late ? decode_attn_bf16_kernel<64, true> : decode_attn_bf16_kernel<64, false>, nw, 32,
+                      attn_bf16_smem_bytes(), st, a);
 }
 
 cudaError_t launch_decode_attn_bf16(const kvarn_config& cfg, const void* q, int q_dtype, const void* kv_pool,
@@ -316,7 +325,7 @@ cudaError_t launch_decode_attn_bf16(const kvarn_config& cfg, const void* q, int 
                                     cudaStream_t st) {
     AttnArgs a;
     const cudaError_t e = launch_decode_split_bf16(cfg, q, q_dtype, kv_pool, n_pool_blocks, block_table, max_blocks,
-                                                   seq_lens, batch, out, workspace, nw, &a, st);
+                                                   seq_lens, batch, out, workspace, nw, false, &a, st);
     if (e != cudaSuccess) return e;
     // (no raw tail rows: the wide kernel only for many partials per unit)
     return launch_merge<kChunk, false>(a, nw, 0, st);

@@ -86,6 +86,12 @@ __device__ __forceinline__ void fwht128(float (&v)[4], int lane) {
 // wrote (the wait returns once those grids have completed and flushed).
 __device__ __forceinline__ void wait_prior_grids() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A kernel whose CTAs all call this (behind their wait) lets the next one in
+// the stream start beside it. That one may read what came before the first
+// but not what the first writes, and waits at its own end instead of its
+// beginning, so that a third kernel finds both complete.
+__device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                        Args... args) {

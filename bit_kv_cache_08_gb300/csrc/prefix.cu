@@ -18,11 +18,11 @@ namespace kvarn {
 cudaError_t launch_decode_split(const kvarn_config& cfg, const void* q, int q_dtype, const void* pool,
                                 int64_t n_pool_blocks, int64_t block_bytes, const void* staging,
                                 const int32_t* block_table, int max_blocks, const int32_t* seq_lens, int batch,
-                                float* out, void* workspace, int nw, AttnArgs* args, cudaStream_t st);
+                                float* out, void* workspace, int nw, bool late, AttnArgs* args, cudaStream_t st);
 cudaError_t launch_decode_split_bf16(const kvarn_config& cfg, const void* q, int q_dtype, const void* kv_pool,
                                      int64_t n_pool_blocks, const int32_t* block_table, int max_blocks,
                                      const int32_t* seq_lens, int batch, float* out, void* workspace, int nw,
-                                     AttnArgs* args, cudaStream_t st);
+                                     bool late, AttnArgs* args, cudaStream_t st);
 
 cudaError_t launch_prefix_bf16(const PrefixArgs& p, int block_size, cudaStream_t st);
 cudaError_t launch_prefix_packed(const kvarn_config& c, const PrefixArgs& p, cudaStream_t st);
@@ -80,7 +80,7 @@ __device__ __forceinline__ void lse_list(const float* p0, int np, int64_t pstrid
 // combines the shares and finishes the row.
 constexpr int kMergeWarps = 8;
 template <int B, bool ROT>
-__global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(AttnArgs a, PrefixMerge pm) {
+__global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnArgs a, PrefixMerge pm) {
     wait_prior_grids();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int b = blockIdx.x / a.n_kv, h = blockIdx.x % a.n_kv;
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(AttnArgs
         }
         *reinterpret_cast<float4*>(&slices[wp][4 + 4 * lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         if (ntail > 0) {
-            // this warp's run of the tail rows, 8 at a time, each an LSE slice
+            // this warp's run of the tail rows, 4 at a time, each an LSE slice
             float qv[4], tm = -INFINITY, tl = 0.f, tacc[4] = {0.f, 0.f, 0.f, 0.f};
             load_q4(a.q, a.q_dtype, gw, lane, qv);
             const float qs = a.sm_scale * kLog2e;
@@ -124,9 +124,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(AttnArgs
             for (int k = 0; k < 4; ++k) qv[k] *= qs;
             const uint16_t* kst = a.staging + ((int64_t)b * a.n_kv + h) * 2 * B * kD;
             const int r1 = ntail * (part + 1) / parts;
-            for (int r0 = ntail * part / parts; r0 < r1; r0 += 8) {
+            for (int r0 = ntail * part / parts; r0 < r1; r0 += 4) {
                 float sm = -INFINITY, sl = 0.f, sacc[4] = {0.f, 0.f, 0.f, 0.f};
-                tail_run<B, 8>(kst, r0, min(8, r1 - r0), qv, lane, sm, sl, sacc);
+                tail_run<B, 4>(kst, r0, min(4, r1 - r0), qv, lane, sm, sl, sacc);
                 const float mn = fmaxf(tm, sm);
                 const float fa = tm == -INFINITY ? 0.f : exp2f(tm - mn), fs = exp2f(sm - mn);
                 tl = tl * fa + sl * fs;
@@ -268,12 +268,12 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
         e = launch_prefix_packed(c, p, st);
         if (e == cudaSuccess)
             e = launch_decode_split(c, q, q_dtype, pool, n_pool_blocks, p.block_bytes, staging, block_table, max_blocks,
-                                    seq_lens, batch, nullptr, workspace, nw, &a, st);
+                                    seq_lens, batch, nullptr, workspace, nw, true, &a, st);
     } else {
         e = launch_prefix_bf16(p, c.block_size, st);
         if (e == cudaSuccess)
             e = launch_decode_split_bf16(c, q, q_dtype, pool, n_pool_blocks, block_table, max_blocks, seq_lens, batch,
-                                         nullptr, workspace, nw, &a, st);
+                                         nullptr, workspace, nw, true, &a, st);
     }
     if (e != cudaSuccess) return KVARN_ERR_CUDA;
     const PrefixMerge pm{p.partials, prefix_lens, prefix_blocks * c.block_size, plan.splits * plan.streams, out, out_dtype == KVARN_BF16};

@@ -51,6 +51,7 @@ constexpr size_t bf16_prefix_smem(int mode) { return 1024 + kBf16Header + (size_
 template <int B, int MODE>
 __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_constant__ CUtensorMap map, PrefixArgs a) {
     wait_prior_grids();
+    let_next_grid_start();   // the own tokens' split kernel
     extern __shared__ uint8_t raw[];
     // operands on 1024-byte boundaries (the swizzle's period)
     uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);

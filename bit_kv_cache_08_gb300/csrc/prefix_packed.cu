@@ -95,6 +95,7 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t w8, uint32_t 
 template <int B, int BITS, int NT>
 __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix_packed_kernel(PrefixArgs a) {
     wait_prior_grids();
+    let_next_grid_start();   // the own tokens' split kernel
     using Lay = PackedLayout<B, BITS, NT>;
     constexpr int kSoft = Lay::kSoft;
     extern __shared__ uint8_t raw_smem[];
