@@ -139,8 +139,15 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    """The current stream of the current device (a Stream object takes 3 us of a 4 us launch to make)."""
+    if _raw_stream is None or _raw_device is None or not torch.cuda.is_initialized():
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_raw_device())
 
 
 def _need_cuda(t: torch.Tensor, name: str, dtype=None):
@@ -326,57 +333,74 @@ def _need_vec(t, name: str, dtype, n: int):
         raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
 
 
-def _token_rows(t: torch.Tensor, name: str, heads: int, n_tokens: int) -> int:
+_bf16, _i32t = torch.bfloat16, torch.int32
+
+
+def _token_rows(t: torch.Tensor, name: str, shape: tuple) -> int:
     """Checks a [n_tokens][heads][128] bf16 tensor whose token rows may lie apart; returns the token stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not _bf16:
         raise ValueError(f"{name} must be a bf16 CUDA tensor")
-    if t.dim() != 3 or t.shape[0] != n_tokens or t.shape[1] != heads or t.shape[2] != 128:
-        raise ValueError(f"{name} must be [{n_tokens}][{heads}][128], got {list(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    n, heads, _ = shape
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (heads > 1 and s1 != 128):
+    if s2 != 1 or (s1 != 128 and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s0 if n_tokens > 1 else heads * 128
+    return s0 if n > 1 else heads * 128
 
 
 def _append_rope(cfg, rope, pool, staging, block_table, pos, q, k, v, q_out, workspace, cu_tokens, rope_pos, q_weight,
                  k_weight):
-    _need_cuda(block_table, "block_table", torch.int32)
-    _need_cuda(pos, "pos", torch.int32)
+    # (a decode step's call is as long as its checks: each attribute is read once)
+    _need_cuda(block_table, "block_table", _i32t)
+    _need_cuda(pos, "pos", _i32t)
     _need_cuda(workspace, "workspace", torch.uint8)
-    batch, n = pos.numel(), k.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] < batch:
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [n_tokens][n_kv][128]")
+    batch, n, n_kv = pos.numel(), k.shape[0], cfg.n_kv_heads
+    rows, max_blocks = block_table.shape if block_table.dim() == 2 else (-1, 0)
+    if rows < batch:
         raise ValueError("block_table must be [batch][max_blocks]")
+    cu_ptr = rope_ptr = qw_ptr = kw_ptr = q_ptr = out_ptr = None
     if cu_tokens is not None:
-        _need_vec(cu_tokens, "cu_tokens", torch.int32, batch + 1)
+        _need_vec(cu_tokens, "cu_tokens", _i32t, batch + 1)
+        cu_ptr = cu_tokens.data_ptr()
     elif n != batch:
         raise ValueError("without cu_tokens there is one token per sequence")
     if rope_pos is not None:
-        _need_vec(rope_pos, "rope_pos", torch.int32, batch)
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need_vec(w, name, torch.bfloat16, 128)
-    ks, vs, qs, out_code = _token_rows(k, "k", cfg.n_kv_heads, n), _token_rows(v, "v", cfg.n_kv_heads, n), 0, BF16
+        _need_vec(rope_pos, "rope_pos", _i32t, batch)
+        rope_ptr = rope_pos.data_ptr()
+    if q_weight is not None:
+        _need_vec(q_weight, "q_weight", _bf16, 128)
+        qw_ptr = q_weight.data_ptr()
+    if k_weight is not None:
+        _need_vec(k_weight, "k_weight", _bf16, 128)
+        kw_ptr = k_weight.data_ptr()
+    shape = (n, n_kv, 128)
+    ks, vs, qs, out_code = _token_rows(k, "k", shape), _token_rows(v, "v", shape), 0, BF16
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
-        qs = _token_rows(q, "q", cfg.n_q_heads, n)
+        shape = (n, cfg.n_q_heads, 128)
+        qs = _token_rows(q, "q", shape)
         _need_cuda(q_out, "q_out")
         out_code = _dtype_code(q_out)
-        if q_out.shape != q.shape:
+        if q_out.shape != shape:
             raise ValueError("q_out must have the shape of q")
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     if workspace.numel() < 256:
         raise ValueError("workspace must hold 256 bytes")
-    head = (ctypes.byref(cfg), ctypes.byref(rope), pool.data_ptr(), pool.shape[0])
-    mid = () if staging is None else (staging.data_ptr(),)
-    tail = (block_table.data_ptr(), block_table.shape[1], pos.data_ptr(),
-            None if rope_pos is None else rope_pos.data_ptr(), None if cu_tokens is None else cu_tokens.data_ptr(),
-            n, batch, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
-            None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
-            None if q_out is None else q_out.data_ptr(), out_code, workspace.data_ptr(), _stream())
+    tail = (block_table.data_ptr(), max_blocks, pos.data_ptr(), rope_ptr, cu_ptr, n, batch, q_ptr, k.data_ptr(),
+            v.data_ptr(), qs, ks, vs, qw_ptr, kw_ptr, out_ptr, out_code, workspace.data_ptr(), _stream())
     if staging is None:
-        _check(lib().kvarn_append_rope_bf16(*head, *tail), "kvarn_append_rope_bf16")
+        r = lib().kvarn_append_rope_bf16(ctypes.byref(cfg), ctypes.byref(rope), pool.data_ptr(), pool.shape[0], *tail)
+        if r:
+            _check(r, "kvarn_append_rope_bf16")
     else:
-        _check(lib().kvarn_append_rope(*head, *mid, *tail), "kvarn_append_rope")
+        r = lib().kvarn_append_rope(ctypes.byref(cfg), ctypes.byref(rope), pool.data_ptr(), pool.shape[0],
+                                    staging.data_ptr(), *tail)
+        if r:
+            _check(r, "kvarn_append_rope")
 
 
 def append_rope(cfg: Config, rope: Rope, pool: torch.Tensor, staging: torch.Tensor, block_table: torch.Tensor,
@@ -407,7 +431,7 @@ def append_rope_bf16(cfg: Config, rope: Rope, kv_pool: torch.Tensor, block_table
                      k_weight: Optional[torch.Tensor] = None):
     """append_rope into the bf16 pages [n_blocks][n_kv][2][B][128] of decode_attn_bf16."""
     _need_cuda(kv_pool, "kv_pool", torch.bfloat16)
-    if tuple(kv_pool.shape[1:]) != (cfg.n_kv_heads, 2, cfg.block_size, 128):
+    if kv_pool.shape[1:] != (cfg.n_kv_heads, 2, cfg.block_size, 128):
         raise ValueError("kv_pool must be [n_blocks][n_kv][2][B][128]")
     _append_rope(cfg, rope, kv_pool, None, block_table, pos, q, k, v, q_out, workspace, cu_tokens, rope_pos, q_weight,
                  k_weight)
@@ -467,19 +491,21 @@ def decode_attn_bf16(cfg: Config, q: torch.Tensor, kv_pool: torch.Tensor, block_
 def _prefix_args(cfg, q, prefix_table, prefix_lens, block_table, seq_lens, out, workspace):
     _need_cuda(q, "q")
     _need_cuda(out, "out")
-    _need_cuda(prefix_table, "prefix_table", torch.int32)
-    _need_cuda(prefix_lens, "prefix_lens", torch.int32)
-    _need_cuda(block_table, "block_table", torch.int32)
-    _need_cuda(seq_lens, "seq_lens", torch.int32)
+    _need_cuda(prefix_table, "prefix_table", _i32t)
+    _need_cuda(prefix_lens, "prefix_lens", _i32t)
+    _need_cuda(block_table, "block_table", _i32t)
+    _need_cuda(seq_lens, "seq_lens", _i32t)
     _need_cuda(workspace, "workspace", torch.uint8)
-    batch = q.shape[0]
-    if q.dim() != 3 or q.shape[1] != cfg.n_q_heads or q.shape[2] != 128 or out.shape != q.shape:
+    shape = q.shape
+    if len(shape) != 3 or shape[1] != cfg.n_q_heads or shape[2] != 128 or out.shape != shape:
         raise ValueError("q and out must be [batch][n_q][128]")
-    if prefix_lens.numel() != batch or seq_lens.numel() != batch or block_table.dim() != 2 or block_table.shape[0] != batch:
+    batch = shape[0]
+    rows, max_blocks = block_table.shape if block_table.dim() == 2 else (-1, 0)
+    if prefix_lens.numel() != batch or seq_lens.numel() != batch or rows != batch:
         raise ValueError("prefix_lens, seq_lens and block_table must have a row for each sequence of q")
-    return ((prefix_table.data_ptr(), prefix_table.numel(), prefix_lens.data_ptr(), block_table.data_ptr(),
-             block_table.shape[1], seq_lens.data_ptr(), batch, out.data_ptr(), _dtype_code(out), workspace.data_ptr(),
-             workspace.numel(), _stream()))
+    return (prefix_table.data_ptr(), prefix_table.numel(), prefix_lens.data_ptr(), block_table.data_ptr(), max_blocks,
+            seq_lens.data_ptr(), batch, out.data_ptr(), _dtype_code(out), workspace.data_ptr(), workspace.numel(),
+            _stream())
 
 
 def prefix_attn(cfg: Config, q: torch.Tensor, pool: torch.Tensor, staging: torch.Tensor, prefix_table: torch.Tensor,
@@ -505,7 +531,7 @@ def prefix_attn_bf16(cfg: Config, q: torch.Tensor, kv_pool: torch.Tensor, prefix
     """prefix_attn over the bf16 pages [n_blocks][n_kv][2][B][128] of decode_attn_bf16."""
     _need_cuda(kv_pool, "kv_pool", torch.bfloat16)
     rest = _prefix_args(cfg, q, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
-    if tuple(kv_pool.shape[1:]) != (cfg.n_kv_heads, 2, cfg.block_size, 128):
+    if kv_pool.shape[1:] != (cfg.n_kv_heads, 2, cfg.block_size, 128):
         raise ValueError("kv_pool must be [n_blocks][n_kv][2][B][128]")
     _check(lib().kvarn_prefix_attn_bf16(ctypes.byref(cfg), q.data_ptr(), _dtype_code(q), kv_pool.data_ptr(),
                                         kv_pool.shape[0], *rest), "kvarn_prefix_attn_bf16")

@@ -13,7 +13,10 @@
 // one whose tokens came one by one through the staging buffer.
 //
 // Bound: every q, k and v row is read and written once (512 bytes a row), so
-// memory for prompts and latency for a decode step.
+// memory for prompts and latency for a decode step. 32 760 prompt tokens of 48
+// rows (805 MB) into bf16 pages take 137 us, 0.87 of the measured copy
+// bandwidth, with 4 rows a half-warp in flight (147 us with 2, 194 us with 1).
+#include "attn_common.cuh"
 #include "host_checks.h"
 #include "quantize.cuh"
 #include "rope.cuh"
@@ -44,15 +47,33 @@ struct RopeAppendArgs {
     uint32_t* err;
 };
 
-__device__ __forceinline__ void load_weight(const uint16_t* w, int lane, float (&v)[4]) {
-    if (w) unpack_bf4(reinterpret_cast<const uint2*>(w)[lane], v);
+__device__ __forceinline__ void load_weight(const uint16_t* w, const RopeLane& p, float (&v)[8]) {
+    if (!w) return;
+    unpack_bf4(*reinterpret_cast<const uint2*>(w + p.c0), v);
+    unpack_bf4(*reinterpret_cast<const uint2*>(w + p.c1), v + 4);
 }
 
-__device__ __forceinline__ void store_q(const RopeAppendArgs& a, int64_t row, int lane, const float (&x)[4]) {
-    if (a.q_out_fp32)
-        reinterpret_cast<float4*>(static_cast<float*>(a.q_out) + row * kD)[lane] = make_float4(x[0], x[1], x[2], x[3]);
-    else
-        reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.q_out) + row * kD)[lane] = pack_bf4(x);
+// A loaded row normed (where there is a weight) and rotated.
+__device__ __forceinline__ void turn_row(const uint2 (&u)[2], const RopeLane& p, bool norm, const float (&w)[8], float eps,
+                                         float (&x)[8]) {
+    unpack_bf4(u[0], x);
+    unpack_bf4(u[1], x + 4);
+    if (norm) head_norm(x, w, eps);
+    rope_apply(p, x);
+}
+
+__device__ __forceinline__ void store_row(uint16_t* row, const RopeLane& p, const float (&x)[8]) {
+    *reinterpret_cast<uint2*>(row + p.c0) = pack_bf4(x);
+    *reinterpret_cast<uint2*>(row + p.c1) = pack_bf4(x + 4);
+}
+__device__ __forceinline__ void store_q(const RopeAppendArgs& a, int64_t row, const RopeLane& p, const float (&x)[8]) {
+    if (a.q_out_fp32) {
+        float* out = static_cast<float*>(a.q_out) + row * kD;
+        *reinterpret_cast<float4*>(out + p.c0) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(out + p.c1) = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        store_row(static_cast<uint16_t*>(a.q_out) + row * kD, p, x);
+    }
 }
 
 // The sequence of token row t: the number of ends cu[1 .. batch] at or before
@@ -77,10 +98,12 @@ __device__ __forceinline__ int sequence_of(const RopeAppendArgs& a, int64_t t, i
 }
 
 // ---------------------------------------------------------------- bf16 pages
-// One warp per (token, run of `rows` of its n_q + 2 n_kv head rows).
+// One warp per (token, run): the run-th part of the token's query, key and
+// value rows.
+constexpr int kRowBatch = 4;
 template <int B>
 __global__ void __launch_bounds__(128) append_rope_bf16_kernel(RopeAppendArgs a, const __grid_constant__ kvarn_rope r,
-                                                               int rows, int runs) {
+                                                               int runs) {
     wait_prior_grids();
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -100,32 +123,44 @@ __global__ void __launch_bounds__(128) append_rope_bf16_kernel(RopeAppendArgs a,
     const int64_t phys = a.block_table[(int64_t)b * a.max_blocks + at / B];
     const bool ok = phys >= 0 && phys < a.n_pool_blocks;
     if (!ok && lane == 0) raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
-    const RopeLane rl = rope_lane(r, (a.rope_pos ? (int64_t)a.rope_pos[b] : (int64_t)a.pos[b]) + i, lane);
-    float qw[4], kw[4];
-    load_weight(a.q_weight, lane, qw);
-    load_weight(a.k_weight, lane, kw);
+    const int half = lane >> 4;
+    const RopeLane rl = rope_lane(r, (a.rope_pos ? (int64_t)a.rope_pos[b] : (int64_t)a.pos[b]) + i, lane & 15);
+    float qw[8], kw[8];
+    load_weight(a.q_weight, rl, qw);
+    load_weight(a.k_weight, rl, kw);
     uint16_t* page = reinterpret_cast<uint16_t*>(a.pool + phys * a.block_bytes) + (at % B) * kD;
-    const int r0 = (int)(item % runs) * rows, r1 = min(r0 + rows, a.n_q + 2 * a.n_kv);
-    for (int j = r0; j < r1; ++j) {
-        float x[4];
-        if (j < a.n_q) {
-            if (!a.q) continue;
-            unpack_bf4(reinterpret_cast<const uint2*>(a.q + t * a.q_stride + (int64_t)j * kD)[lane], x);
-            if (a.q_weight) head_norm(x, qw, r.eps);
-            rope_apply(rl, x);
-            store_q(a, t * a.n_q + j, lane, x);
-        } else if (j < a.n_q + a.n_kv) {
-            const int h = j - a.n_q;
-            unpack_bf4(reinterpret_cast<const uint2*>(a.k + t * a.k_stride + (int64_t)h * kD)[lane], x);
-            if (a.k_weight) head_norm(x, kw, r.eps);
-            rope_apply(rl, x);
-            if (ok) reinterpret_cast<uint2*>(page + (int64_t)(2 * h) * B * kD)[lane] = pack_bf4(x);
-        } else {
-            const int h = j - a.n_q - a.n_kv;
-            const uint2 u = reinterpret_cast<const uint2*>(a.v + t * a.v_stride + (int64_t)h * kD)[lane];
-            if (ok) reinterpret_cast<uint2*>(page + (int64_t)(2 * h + 1) * B * kD)[lane] = u;
+    const int run = (int)(item % runs);
+    // the half-warps take the rows of a kind in turn, kRowBatch each at a time;
+    // all loads of a batch are in flight (and in place they come before its stores)
+    auto rows_of = [&](int heads, const uint16_t* src, auto&& put) {
+        const int h0 = (int)((int64_t)heads * run / runs), h1 = (int)((int64_t)heads * (run + 1) / runs);
+        for (int j0 = h0; j0 < h1; j0 += 2 * kRowBatch) {
+            uint2 u[kRowBatch][2];
+#pragma unroll
+            for (int k = 0; k < kRowBatch; ++k)   // (a half without a row repeats the last: the norm's shuffles need it)
+                load_row(src + (int64_t)min(j0 + 2 * k + half, h1 - 1) * kD, rl, u[k]);
+#pragma unroll
+            for (int k = 0; k < kRowBatch; ++k)
+                if (j0 + 2 * k < h1) put(u[k], j0 + 2 * k + half, j0 + 2 * k + half < h1);
         }
-    }
+    };
+    if (a.q)
+        rows_of(a.n_q, a.q + t * a.q_stride, [&](const uint2 (&u)[2], int j, bool real) {
+            float x[8];
+            turn_row(u, rl, a.q_weight != nullptr, qw, r.eps, x);
+            if (real) store_q(a, t * a.n_q + j, rl, x);
+        });
+    rows_of(a.n_kv, a.k + t * a.k_stride, [&](const uint2 (&u)[2], int j, bool real) {
+        float x[8];
+        turn_row(u, rl, a.k_weight != nullptr, kw, r.eps, x);
+        if (real && ok) store_row(page + (int64_t)(2 * j) * B * kD, rl, x);
+    });
+    rows_of(a.n_kv, a.v + t * a.v_stride, [&](const uint2 (&u)[2], int j, bool real) {
+        if (!real || !ok) return;
+        uint16_t* row = page + (int64_t)(2 * j + 1) * B * kD;
+        *reinterpret_cast<uint2*>(row + rl.c0) = u[0];
+        *reinterpret_cast<uint2*>(row + rl.c1) = u[1];
+    });
 }
 
 // ---------------------------------------------------------------- packed cache
@@ -170,7 +205,7 @@ __device__ __forceinline__ int unit_of(const RopeAppendArgs& a, int64_t u, int l
 }
 
 // grid (units, n_kv, 2 or 3): z = 0 keys, 1 values, 2 the G query heads of kv
-// head y. A unit that completes its block quantises it (rows before `pos`
+// head y (of a decode step: with the keys). A unit that completes its block quantises it (rows before `pos`
 // from staging); another one writes staging rows. Where a sequence's first
 // block takes staged rows and its last block stays incomplete, one CTA does
 // both, the last block's staging rows after the first block has been read.
@@ -180,6 +215,7 @@ __global__ void __launch_bounds__(quant_threads<B>(), B == 64 ? 2 : 3) append_ro
                                                                             QuantParams p) {
     wait_prior_grids();
     __shared__ QuantSmem<B, BITS> q;
+    __shared__ __align__(16) uint16_t tile[B * kD];   // the completed block's rows
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.y, kind = blockIdx.z;
     int j;
@@ -197,43 +233,55 @@ __global__ void __launch_bounds__(quant_threads<B>(), B == 64 ? 2 : 3) append_ro
     const int64_t turn0 = (a.rope_pos ? (int64_t)a.rope_pos[b] : pos) - pos;
     const int64_t blk = pos / B + j;
     const int64_t lo = max(pos, blk * B), hi = min(end, (blk + 1) * B);
-    float w[4];
+    const int hw = tid >> 4, l = tid & 15;                      // half-warp, lane in it
+    constexpr int kHalves = 2 * quant_warps<B>();
+    const RopeLane groups = rope_lane(r, 0, l);                 // (for the channel groups)
+    float w[8];
 
-    if (kind == 2) {
-        const int G = a.n_q / a.n_kv;
-        load_weight(a.q_weight, lane, w);
-        for (int64_t x = lo + warp; x < hi; x += quant_warps<B>()) {
-            const RopeLane rl = rope_lane(r, turn0 + x, lane);
-            const int64_t t = t0 + (x - pos);
-            for (int g = 0; g < G; ++g) {
-                float v[4];
-                unpack_bf4(reinterpret_cast<const uint2*>(a.q + t * a.q_stride + (int64_t)(h * G + g) * kD)[lane], v);
-                if (a.q_weight) head_norm(v, w, r.eps);
-                rope_apply(rl, v);
-                store_q(a, t * a.n_q + h * G + g, lane, v);
-            }
+    if (a.q && (kind == 2 || (kind == 0 && !a.cu))) {           // (a decode step's few query rows ride with the keys)
+        const int G = a.n_q / a.n_kv, rows = (int)(hi - lo) * G;
+        load_weight(a.q_weight, groups, w);
+        for (int x0 = 0; x0 < rows; x0 += kHalves) {
+            if (x0 + (hw & ~1) >= rows) break;                  // (whole warps)
+            const int x = min(x0 + hw, rows - 1), g = x % G;
+            const int64_t at = lo + x / G, t = t0 + (at - pos);
+            const RopeLane rl = rope_lane(r, turn0 + at, l);
+            uint2 u[2];
+            load_row(a.q + t * a.q_stride + (int64_t)(h * G + g) * kD, rl, u);
+            float v[8];
+            turn_row(u, rl, a.q_weight != nullptr, w, r.eps, v);
+            if (x0 + hw < rows) store_q(a, t * a.n_q + h * G + g, rl, v);
         }
-        return;
+        if (kind == 2) return;
     }
 
     uint16_t* stage = a.staging + (((int64_t)b * a.n_kv + h) * 2 + kind) * B * kD;
-    if (kind == 0) load_weight(a.k_weight, lane, w);
-    // the new row of position x (this lane's 4 channels), rounded to bf16
-    auto new_row = [&](int64_t x) -> uint2 {
-        const int64_t t = t0 + (x - pos);
-        if (kind == 1) return reinterpret_cast<const uint2*>(a.v + t * a.v_stride + (int64_t)h * kD)[lane];
-        float v[4];
-        unpack_bf4(reinterpret_cast<const uint2*>(a.k + t * a.k_stride + (int64_t)h * kD)[lane], v);
-        if (a.k_weight) head_norm(v, w, r.eps);
-        rope_apply(rope_lane(r, turn0 + x, lane), v);
-        return pack_bf4(v);
-    };
-    auto stage_rows = [&](int64_t from, int64_t to) {
-        for (int64_t x = from + warp; x < to; x += quant_warps<B>())
-            reinterpret_cast<uint2*>(stage + (x % B) * kD)[lane] = new_row(x);
+    if (kind == 0) load_weight(a.k_weight, groups, w);
+    // new rows of positions from .. to - 1, rounded to bf16, to row (position % B) of dst
+    auto new_rows = [&](int64_t from, int64_t to, uint16_t* dst) {
+        const int rows = (int)(to - from);
+        for (int x0 = 0; x0 < rows; x0 += kHalves) {
+            if (x0 + (hw & ~1) >= rows) break;                  // (whole warps)
+            const int64_t at = from + min(x0 + hw, rows - 1), t = t0 + (at - pos);
+            uint16_t* row = dst + (at % B) * kD;
+            uint2 u[2];
+            if (kind == 1) {
+                load_row(a.v + t * a.v_stride + (int64_t)h * kD, groups, u);
+                if (x0 + hw < rows) {
+                    *reinterpret_cast<uint2*>(row + groups.c0) = u[0];
+                    *reinterpret_cast<uint2*>(row + groups.c1) = u[1];
+                }
+            } else {
+                const RopeLane rl = rope_lane(r, turn0 + at, l);
+                load_row(a.k + t * a.k_stride + (int64_t)h * kD, rl, u);
+                float v[8];
+                turn_row(u, rl, a.k_weight != nullptr, w, r.eps, v);
+                if (x0 + hw < rows) store_row(row, rl, v);
+            }
+        }
     };
     if (hi < (blk + 1) * B) {   // the block stays incomplete
-        if (j == 0 || pos % B == 0) stage_rows(lo, hi);
+        if (j == 0 || pos % B == 0) new_rows(lo, hi, stage);
         return;
     }
     const int64_t phys = a.block_table[(int64_t)b * a.max_blocks + blk];
@@ -241,12 +289,15 @@ __global__ void __launch_bounds__(quant_threads<B>(), B == 64 ? 2 : 3) append_ro
     if (!ok && tid == 0) raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
     p.kind = kind;
     zero_code_words<B, BITS>(q, tid);
+    new_rows(lo, hi, tile);
+    for (int64_t x = blk * B + warp; x < lo; x += quant_warps<B>())
+        reinterpret_cast<uint2*>(tile + (x % B) * kD)[lane] = reinterpret_cast<const uint2*>(stage + (x % B) * kD)[lane];
+    __syncthreads();
     float x[kRowsPerWarp][4];
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < kRowsPerWarp; ++i) {
-        const int64_t at = blk * B + warp * kRowsPerWarp + i;
-        unpack_bf4(at < lo ? reinterpret_cast<const uint2*>(stage + (at % B) * kD)[lane] : new_row(at), x[i]);
+        unpack_bf4(reinterpret_cast<const uint2*>(tile + (warp * kRowsPerWarp + i) * kD)[lane], x[i]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) bad |= !isfinite(x[i][c]);
     }
@@ -255,8 +306,8 @@ __global__ void __launch_bounds__(quant_threads<B>(), B == 64 ? 2 : 3) append_ro
         quantize_tile<B, BITS>(x, p, q, warp, lane);
         store_image<B, BITS>(q, a.pool + phys * a.block_bytes + (int64_t)(2 * h + kind) * head_block_bytes(B, BITS), tid);
     }
-    // the staged rows of this block have been read (the barrier above)
-    if (j == 0 && pos % B != 0 && end % B != 0 && end / B > blk) stage_rows(end / B * B, end);
+    // the staged rows of this block have been read (the barriers above)
+    if (j == 0 && pos % B != 0 && end % B != 0 && end / B > blk) new_rows(end / B * B, end, stage);
 }
 
 // ---------------------------------------------------------------- host side
@@ -365,13 +416,16 @@ int kvarn_append_rope_bf16(const kvarn_config* cfg, const kvarn_rope* rope, void
                                q_out, q_out_dtype, workspace, &c, &a);
     if (s != KVARN_OK || batch == 0 || n_tokens == 0) return s;
     a.block_bytes = (int64_t)c.n_kv_heads * 2 * c.block_size * kD * 2;
-    const int all = c.n_q_heads + 2 * c.n_kv_heads;
-    const int rows = n_tokens >= 1024 ? 16 : 4;
-    const int runs = (all + rows - 1) / rows;
+    // a warp of its own for every 4 rows of a token, fewer where the tokens alone fill the GPU
+    const int most = (c.n_q_heads + 2 * c.n_kv_heads + 3) / 4;
+    const int64_t warps = current_device_sms() * 64;
+    int64_t runs = (warps + n_tokens - 1) / n_tokens;
+    runs = runs < most ? runs : most;
+    runs = runs > 1 ? runs : 1;
     const unsigned grid = (unsigned)((n_tokens * runs + 3) / 4);
     const cudaError_t e = c.block_size == 32
-                              ? launch_pdl(append_rope_bf16_kernel<32>, grid, 128, 0, (cudaStream_t)stream, a, *rope, rows, runs)
-                              : launch_pdl(append_rope_bf16_kernel<64>, grid, 128, 0, (cudaStream_t)stream, a, *rope, rows, runs);
+                              ? launch_pdl(append_rope_bf16_kernel<32>, grid, 128, 0, (cudaStream_t)stream, a, *rope, (int)runs)
+                              : launch_pdl(append_rope_bf16_kernel<64>, grid, 128, 0, (cudaStream_t)stream, a, *rope, (int)runs);
     return e == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 
@@ -394,7 +448,7 @@ int kvarn_append_rope(const kvarn_config* cfg, const kvarn_rope* rope, void* poo
     // units: a sequence of n tokens touches at most (n + 2 B - 2) / B blocks
     const int64_t units = cu_tokens ? n_tokens / c.block_size + 2 * (int64_t)batch : batch;
     if (units > 0x7fffffff) return KVARN_ERR_INVALID_ARG;
-    const dim3 grid((unsigned)units, c.n_kv_heads, q ? 3 : 2);
+    const dim3 grid((unsigned)units, c.n_kv_heads, q && cu_tokens ? 3 : 2);
     const cudaError_t e = dispatch(c, [&](auto b, auto w) {
         constexpr int B = decltype(b)::value, BITS = decltype(w)::value;
         return launch_pdl(append_rope_kernel<B, BITS>, grid, quant_threads<B>(), 0, (cudaStream_t)stream, a, *rope, p);

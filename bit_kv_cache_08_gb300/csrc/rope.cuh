@@ -1,5 +1,9 @@
 // rope.cuh -- RMS norm and rotary position rotation of one head's 128
-// channels held by a warp (lane l: channels 4l .. 4l + 3, fp32).
+// channels held by half a warp, 8 channels a lane in fp32. A lane's two
+// groups of 4 channels are chosen so that both channels of a pair are its
+// own, whatever the layout and the part of the head that is rotated: no
+// shuffle but the norm's, and two rows an instruction (with a row per warp and
+// partners fetched by shuffles, the 32 760-token append took 216 us, now 137).
 //
 // The rotation turns channel pair i by the angle position * inv_freq[i]. In
 // 32 bits that product loses the angle of far positions (a position of 10^6
@@ -14,13 +18,14 @@
 
 namespace kvarn {
 
-// This lane's share of a head at one position. HALF layout: channels c and
-// c + rotary_dim / 2 are pair c, and the partner of a lane's four channels
-// are the four of one other lane (rotary_dim is a multiple of 16).
-// INTERLEAVED: channels 2i and 2i + 1 are pair i, both in this lane.
+// Half-lane l's (0..15) channels at one position: groups c0 .. c0 + 3 and
+// c1 .. c1 + 3. HALF layout: channels c and c + rotary_dim / 2 are a pair, so
+// lanes below rotary_dim / 8 take 4l and rotary_dim / 2 + 4l; the 128 -
+// rotary_dim channels that pass are 8 for each lane that is left
+// (rotary_dim is a multiple of 16). INTERLEAVED: 8l and 8l + 4.
 struct RopeLane {
-    float c[4], s[4];   // cos and +-sin for this lane's channels (the sign of the partner's share in s)
-    int partner;        // lane that holds the partner channels (HALF)
+    float c[4], s[4];   // of the lane's 4 pairs
+    int c0, c1;
     bool interleaved;
 };
 
@@ -32,67 +37,72 @@ __device__ __forceinline__ void turn_cossin(uint64_t rate, int64_t pos, float sc
     s *= scale;
 }
 
-__device__ __forceinline__ RopeLane rope_lane(const kvarn_rope& r, int64_t pos, int lane) {
+__device__ __forceinline__ RopeLane rope_lane(const kvarn_rope& r, int64_t pos, int l) {
     RopeLane p;
     p.interleaved = r.layout == KVARN_ROPE_INTERLEAVED;
-    p.partner = lane;
+    const int turned = r.rotary_dim / 8;   // lanes whose channels are rotated
+    if (p.interleaved) {
+        p.c0 = 8 * l;
+        p.c1 = 8 * l + 4;
+    } else {
+        p.c0 = l < turned ? 4 * l : 8 * l;
+        p.c1 = l < turned ? r.rotary_dim / 2 + 4 * l : 8 * l + 4;
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) { p.c[k] = 1.f; p.s[k] = 0.f; }
-    if (4 * lane >= r.rotary_dim) return p;
-    if (p.interleaved) {
+    if (l < turned) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float c, s;
-            turn_cossin(r.turns[2 * lane + k], pos, r.scale, c, s);
-            p.c[2 * k] = p.c[2 * k + 1] = c;
-            p.s[2 * k] = -s;
-            p.s[2 * k + 1] = s;
-        }
-    } else {
-        const int half = r.rotary_dim / 8;   // lanes of the first half
-        const bool second = lane >= half;
-        p.partner = second ? lane - half : lane + half;
-        const int i0 = 4 * (second ? lane - half : lane);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float c, s;
-            turn_cossin(r.turns[i0 + k], pos, r.scale, c, s);
-            p.c[k] = c;
-            p.s[k] = second ? s : -s;
-        }
+        for (int k = 0; k < 4; ++k) turn_cossin(r.turns[4 * l + k], pos, r.scale, p.c[k], p.s[k]);
     }
     return p;
 }
 
-// x' = x cos + partner (+-sin); the whole warp calls it.
-__device__ __forceinline__ void rope_apply(const RopeLane& p, float (&x)[4]) {
-    float o[4];
+// A row's 8 values of this lane: x[0..3] from channel c0, x[4..7] from c1.
+__device__ __forceinline__ void load_row(const uint16_t* row, const RopeLane& p, uint2 (&u)[2]) {
+    u[0] = *reinterpret_cast<const uint2*>(row + p.c0);
+    u[1] = *reinterpret_cast<const uint2*>(row + p.c1);
+}
+
+// (a, b) -> (a cos - b sin, b cos + a sin) for the lane's 4 pairs
+__device__ __forceinline__ void rope_apply(const RopeLane& p, float (&x)[8]) {
     if (p.interleaved) {
-        o[0] = x[1]; o[1] = x[0]; o[2] = x[3]; o[3] = x[2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float a = x[2 * k], b = x[2 * k + 1];
+            x[2 * k] = fmaf(a, p.c[k], __fmul_rn(b, -p.s[k]));
+            x[2 * k + 1] = fmaf(b, p.c[k], __fmul_rn(a, p.s[k]));
+        }
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = __shfl_sync(kFull, x[k], p.partner);
+        for (int k = 0; k < 4; ++k) {
+            const float a = x[k], b = x[k + 4];
+            x[k] = fmaf(a, p.c[k], __fmul_rn(b, -p.s[k]));
+            x[k + 4] = fmaf(b, p.c[k], __fmul_rn(a, p.s[k]));
+        }
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = fmaf(x[k], p.c[k], __fmul_rn(o[k], p.s[k]));
 }
 
-// x' = x w / sqrt(mean(x^2) + eps) over the head; the whole warp calls it.
-__device__ __forceinline__ void head_norm(float (&x)[4], const float (&w)[4], float eps) {
-    const float ss = warp_sum(fmaf(x[0], x[0], fmaf(x[1], x[1], fmaf(x[2], x[2], __fmul_rn(x[3], x[3])))));
+// x' = x w / sqrt(mean(x^2) + eps) over the head; the whole warp calls it, a
+// row per half.
+__device__ __forceinline__ void head_norm(float (&x)[8], const float (&w)[8], float eps) {
+    float ss = __fmul_rn(x[0], x[0]);
+#pragma unroll
+    for (int k = 1; k < 8; ++k) ss = fmaf(x[k], x[k], ss);
+#pragma unroll
+    for (int m = 8; m >= 1; m >>= 1) ss += __shfl_xor_sync(kFull, ss, m);
     const float r = rsqrtf(fmaf(ss, 1.0f / kD, eps));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = __fmul_rn(x[k], __fmul_rn(r, w[k]));
+    for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(x[k], __fmul_rn(r, w[k]));
 }
 
-// Four bf16 values of a row as floats, and four floats rounded to bf16.
-__device__ __forceinline__ void unpack_bf4(uint2 u, float (&v)[4]) {
+// Four bf16 values as floats, and four floats rounded to bf16.
+__device__ __forceinline__ void unpack_bf4(uint2 u, float* v) {
     v[0] = __uint_as_float(u.x << 16);
     v[1] = __uint_as_float(u.x & 0xffff0000u);
     v[2] = __uint_as_float(u.y << 16);
     v[3] = __uint_as_float(u.y & 0xffff0000u);
 }
-__device__ __forceinline__ uint2 pack_bf4(const float (&v)[4]) {
+__device__ __forceinline__ uint2 pack_bf4(const float* v) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
     return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
