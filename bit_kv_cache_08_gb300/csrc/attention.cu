@@ -675,13 +675,15 @@ __device__ __forceinline__ void decode_attn_2bit_body(const AttnArgs& a) {
 // let_next_grid_start), the wait comes last.
 template <int B, int BITS, int S, bool LATE>
 __global__ void __launch_bounds__(32) decode_attn_2bit_kernel(AttnArgs a) {
-    if (!LATE) wait_prior_grids();
+    if (LATE) let_next_grid_start();   // the merge, which waits for this one at its beginning
+    else wait_prior_grids();
     decode_attn_2bit_body<B, BITS, S>(a);
     if (LATE) wait_prior_grids();
 }
 template <int B, int BITS, int S, int MINB, bool LATE>
 __global__ void __launch_bounds__(32, MINB) decode_attn_2bit_kernel_minb(AttnArgs a) {
-    if (!LATE) wait_prior_grids();
+    if (LATE) let_next_grid_start();   // the merge, which waits for this one at its beginning
+    else wait_prior_grids();
     decode_attn_2bit_body<B, BITS, S>(a);
     if (LATE) wait_prior_grids();
 }

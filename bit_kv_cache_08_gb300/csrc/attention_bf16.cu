@@ -256,7 +256,8 @@ __device__ __forceinline__ void decode_attn_bf16_body(const AttnArgs& a) {
 // LATE: behind a kernel that lets this one start beside it, the wait comes last.
 template <int B, bool LATE>
 __global__ void __launch_bounds__(32) decode_attn_bf16_kernel(AttnArgs a) {
-    if (!LATE) wait_prior_grids();
+    if (LATE) let_next_grid_start();   // the merge, which waits for this one at its beginning
+    else wait_prior_grids();
     decode_attn_bf16_body<B>(a);
     if (LATE) wait_prior_grids();
 }

@@ -326,51 +326,6 @@ __device__ __forceinline__ void tail_slice(const uint16_t* kst, int ntail, int f
     }
 }
 
-// The same for the n <= N consecutive rows from `first`.
-template <int B, int N>
-__device__ __forceinline__ void tail_run(const uint16_t* kst, int first, int n, const float (&qv)[4], int lane, float& m,
-                                         float& l, float (&acc)[4]) {
-    const uint16_t* vst = kst + B * kD;
-    uint2 ku[N], vu[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (i < n) {
-            ku[i] = reinterpret_cast<const uint2*>(kst + (int64_t)(first + i) * kD)[lane];
-            vu[i] = reinterpret_cast<const uint2*>(vst + (int64_t)(first + i) * kD)[lane];
-        }
-    float sc[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float d = 0.f;
-        if (i < n) {
-            d = fmaf(qv[0], __uint_as_float(ku[i].x << 16), d);
-            d = fmaf(qv[1], __uint_as_float(ku[i].x & 0xffff0000u), d);
-            d = fmaf(qv[2], __uint_as_float(ku[i].y << 16), d);
-            d = fmaf(qv[3], __uint_as_float(ku[i].y & 0xffff0000u), d);
-        }
-        sc[i] = d;
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) sc[i] += __shfl_xor_sync(kFull, sc[i], o);
-    m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (i < n) m = fmaxf(m, sc[i]);
-    if (m == -INFINITY) return;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (i < n) {
-            const float p = exp2f(sc[i] - m);
-            l += p;
-            acc[0] = fmaf(p, __uint_as_float(vu[i].x << 16), acc[0]);
-            acc[1] = fmaf(p, __uint_as_float(vu[i].x & 0xffff0000u), acc[1]);
-            acc[2] = fmaf(p, __uint_as_float(vu[i].y << 16), acc[2]);
-            acc[3] = fmaf(p, __uint_as_float(vu[i].y & 0xffff0000u), acc[3]);
-        }
-}
-
 // One (row, query head) output: LSE-merge the np partials of its unit
 // (p0: the first, consecutive partials G * kPartialStride floats apart; np =
 // 0 when the unit has no pool blocks), add the raw tail rows, normalise and

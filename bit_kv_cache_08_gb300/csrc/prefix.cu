@@ -74,9 +74,14 @@ __device__ __forceinline__ void lse_list(const float* p0, int np, int64_t pstrid
     }
 }
 
+__device__ __forceinline__ void async_copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async_copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // One CTA of 8 warps per (sequence, kv head): 8 / G warps to each of its G
-// query heads (their raw tail rows and tables then meet in L1), each with a
-// share of the row's partials and of the tail rows; the row's first warp
+// query heads (their raw tail rows are copied to shared memory once), each
+// with a share of the row's partials and of the tail rows; the row's first warp
 // combines the shares and finishes the row.
 constexpr int kMergeWarps = 8;
 template <int B, bool ROT>
@@ -103,7 +108,18 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnA
         }
         return;
     }
+    // the raw tail rows on their way to shared memory while the partials merge
+    // (K rows 272 bytes apart: a lane scores a row, and 32 rows then differ in bank)
+    constexpr int kKPitch = kD * 2 + 16;
+    __shared__ __align__(16) uint8_t tail_k[ROT ? B * kKPitch : 16], tail_v[ROT ? B * kD * 2 : 16];
     const int ntail = ROT ? L % B : 0;
+    if (ntail > 0) {
+        const uint16_t* kst = a.staging + ((int64_t)b * a.n_kv + h) * 2 * B * kD;
+        for (int i = threadIdx.x; i < ntail * 16; i += 32 * kMergeWarps) {
+            async_copy16(tail_k + (i >> 4) * kKPitch + (i & 15) * 16, kst + i * 8);
+            async_copy16(tail_v + i * 16, kst + B * kD + i * 8);
+        }
+    }
     if (mine) {
         float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
         const int n = np + (PL > 0 ? pm.splits : 0);
@@ -115,25 +131,51 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnA
             slices[wp][1] = l;
         }
         *reinterpret_cast<float4*>(&slices[wp][4 + 4 * lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        if (ntail > 0) {
-            // this warp's run of the tail rows, 4 at a time, each an LSE slice
-            float qv[4], tm = -INFINITY, tl = 0.f, tacc[4] = {0.f, 0.f, 0.f, 0.f};
+    }
+    if (ntail > 0) {
+        async_copy_wait();
+        __syncthreads();
+        // this warp's share of the tail rows (at most 32), a row a lane
+        const int c0 = ntail * part / parts, cnt = ntail * (part + 1) / parts - c0;
+        if (mine) {
+            float qv[4];
             load_q4(a.q, a.q_dtype, gw, lane, qv);
             const float qs = a.sm_scale * kLog2e;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) qv[k] *= qs;
-            const uint16_t* kst = a.staging + ((int64_t)b * a.n_kv + h) * 2 * B * kD;
-            const int r1 = ntail * (part + 1) / parts;
-            for (int r0 = ntail * part / parts; r0 < r1; r0 += 4) {
-                float sm = -INFINITY, sl = 0.f, sacc[4] = {0.f, 0.f, 0.f, 0.f};
-                tail_run<B, 4>(kst, r0, min(4, r1 - r0), qv, lane, sm, sl, sacc);
-                const float mn = fmaxf(tm, sm);
-                const float fa = tm == -INFINITY ? 0.f : exp2f(tm - mn), fs = exp2f(sm - mn);
-                tl = tl * fa + sl * fs;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tacc[k] = tacc[k] * fa + sacc[k] * fs;
-                tm = mn;
+            *reinterpret_cast<float4*>(&tails[wp][4 * lane]) = make_float4(qv[0] * qs, qv[1] * qs, qv[2] * qs, qv[3] * qs);
+            __syncwarp();
+            float s = -INFINITY;
+            if (lane < cnt) {
+                const uint4* kr = reinterpret_cast<const uint4*>(tail_k + (c0 + lane) * kKPitch);
+                s = 0.f;
+#pragma unroll 4
+                for (int c = 0; c < 16; ++c) {
+                    const uint4 k = kr[c];
+                    const float4 qa = *reinterpret_cast<const float4*>(&tails[wp][8 * c]);
+                    const float4 qb = *reinterpret_cast<const float4*>(&tails[wp][8 * c + 4]);
+                    s = fmaf(qa.x, __uint_as_float(k.x << 16), s);
+                    s = fmaf(qa.y, __uint_as_float(k.x & 0xffff0000u), s);
+                    s = fmaf(qa.z, __uint_as_float(k.y << 16), s);
+                    s = fmaf(qa.w, __uint_as_float(k.y & 0xffff0000u), s);
+                    s = fmaf(qb.x, __uint_as_float(k.z << 16), s);
+                    s = fmaf(qb.y, __uint_as_float(k.z & 0xffff0000u), s);
+                    s = fmaf(qb.z, __uint_as_float(k.w << 16), s);
+                    s = fmaf(qb.w, __uint_as_float(k.w & 0xffff0000u), s);
+                }
             }
+            const float tm = warp_max(s);
+            const float p = s == -INFINITY ? 0.f : exp2f(s - tm);
+            const float tl = warp_sum(p);
+            float tacc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (int i = 0; i < cnt; ++i) {
+                const float w = __shfl_sync(kFull, p, i);
+                const uint2 v = reinterpret_cast<const uint2*>(tail_v + (c0 + i) * kD * 2)[lane];
+                tacc[0] = fmaf(w, __uint_as_float(v.x << 16), tacc[0]);
+                tacc[1] = fmaf(w, __uint_as_float(v.x & 0xffff0000u), tacc[1]);
+                tacc[2] = fmaf(w, __uint_as_float(v.y << 16), tacc[2]);
+                tacc[3] = fmaf(w, __uint_as_float(v.y & 0xffff0000u), tacc[3]);
+            }
+            __syncwarp();   // (the query has been read)
             if (lane == 0) {
                 tails[wp][0] = tm;
                 tails[wp][1] = tl;
