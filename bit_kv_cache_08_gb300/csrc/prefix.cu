@@ -88,16 +88,19 @@ template <int B, bool ROT>
 __global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnArgs a, PrefixMerge pm) {
     wait_prior_grids();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    const int b = blockIdx.x / a.n_kv, h = blockIdx.x % a.n_kv;
-    const int parts = kMergeWarps / a.G, g = wp / parts, part = wp % parts;   // (G = 3: two warps are left over)
+    const int b = blockIdx.x, h = blockIdx.y;
+    const int parts = a.G == 1 ? 8 : a.G == 2 ? 4 : 2, g = wp / parts, part = wp % parts;   // (G = 3: two warps are left over)
     const bool mine = g < a.G;
     const int64_t gw = (int64_t)b * a.n_q + h * a.G + (mine ? g : 0);
     __shared__ __align__(16) float slices[kMergeWarps][kPartialStride];
     __shared__ __align__(16) float tails[kMergeWarps][kPartialStride];
     const int L = a.seq_lens[b], PL = pm.lens[b];
-    int np;
-    const float* p0;
-    merge_locate<B, ROT>(a, gw, lane, np, p0);
+    // the own partials: those of the warps that the split kernel's unit map
+    // names (a range outside the grid, left by a warp that gave up, is none)
+    const int64_t u = (int64_t)b * a.n_kv + h;
+    const int2 wm = __ldcg(reinterpret_cast<const int2*>(a.unit_map) + u);
+    const int np = (ROT ? L >= B : L > 0) && wm.x >= 0 && wm.y >= wm.x && wm.y < a.nw ? wm.y - wm.x + 1 : 0;
+    const float* p0 = a.partials + ((u + max(wm.x, 0)) * a.G + (mine ? g : 0)) * kPartialStride;
     const bool valid = L >= 0 && L <= a.max_blocks * B && PL >= 0 && PL <= pm.max_len;
     if (!valid) {   // (the same for the whole CTA)
         if (threadIdx.x == 0) raise_error(a.err, KVARN_DEVERR_POSITION);
@@ -319,7 +322,7 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
     }
     if (e != cudaSuccess) return KVARN_ERR_CUDA;
     const PrefixMerge pm{p.partials, prefix_lens, prefix_blocks * c.block_size, plan.splits * plan.streams, out, out_dtype == KVARN_BF16};
-    const unsigned units = (unsigned)((int64_t)batch * c.n_kv_heads);
+    const dim3 units(batch, c.n_kv_heads);
     const int threads = 32 * kMergeWarps;
     if constexpr (PACKED)
         e = c.block_size == 32 ? launch_pdl(prefix_merge_kernel<32, true>, units, threads, 0, st, a, pm)
