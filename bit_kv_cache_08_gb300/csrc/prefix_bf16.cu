@@ -18,9 +18,8 @@
 // the reference it was accumulated with (P stays within 2^8; the result is
 // the same up to rounding).
 //
-// Warps: 0-3 and 4-7 softmax of the two streams, 8 and 9 issue their products
-// (one warp for both spent its time in waits, in turn for one and the other),
-// 10 copies pages (a tile copy per page and 64-channel half, swizzled), two
+// Warps: 0-3 and 4-7 softmax of the two streams, 8 issues the products, 9
+// copies pages (a tile copy per page and 64-channel half, swizzled), two
 // stages each of K and V.
 //
 // Rounding: scores are exact products summed in fp32 (an fp32 query is split
@@ -37,11 +36,11 @@ constexpr int kOperand = kPRows * kD * 2;           // bytes of a 128 x 128 16-b
 constexpr int kHalfOperand = kOperand / 2;          // its 64-element column block
 
 struct Bf16Smem {
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], v_clean, drained[2];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], v_clean, drained;
     uint32_t tmem;
     int stop;
 };
-constexpr int kBf16Header = 1024, kBf16Threads = 32 * 11;
+constexpr int kBf16Header = 1024;
 static_assert(sizeof(Bf16Smem) <= kBf16Header, "header");
 static_assert(8 * 32 * kPartialStride * 4 <= 5 * kOperand, "the partials' staging fits the operands' memory");
 
@@ -50,7 +49,7 @@ constexpr int bf16_q_tiles(int mode) { return mode == 1 ? 1 : 2; }
 constexpr size_t bf16_prefix_smem(int mode) { return 1024 + kBf16Header + (size_t)(bf16_q_tiles(mode) + 4) * kOperand; }
 
 template <int B, int MODE>
-__global__ void __launch_bounds__(kBf16Threads, 1) prefix_bf16_kernel(const __grid_constant__ CUtensorMap map, PrefixArgs a) {
+__global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_constant__ CUtensorMap map, PrefixArgs a) {
     wait_prior_grids();
     let_next_grid_start();   // the own tokens' split kernel
     extern __shared__ uint8_t raw[];
@@ -75,15 +74,15 @@ __global__ void __launch_bounds__(kBf16Threads, 1) prefix_bf16_kernel(const __gr
         s.stop = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.k_full[i], 1);
-            mbar_init(&s.k_empty[i], MODE == 0 ? 2 : 1);   // both streams' products
+            mbar_init(&s.k_empty[i], 1);
             mbar_init(&s.v_full[i], 1);
-            mbar_init(&s.v_empty[i], MODE == 0 ? 2 : 1);
+            mbar_init(&s.v_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_ready[i], 4);
             mbar_init(&s.o_full[i], 1);
-            mbar_init(&s.drained[i], 1);
         }
         mbar_init(&s.v_clean, 1);
+        mbar_init(&s.drained, 1);
         fence_mbar_init();
     }
     if (warp == 8) tmem_alloc(&s.tmem, 512);
@@ -94,15 +93,15 @@ __global__ void __launch_bounds__(kBf16Threads, 1) prefix_bf16_kernel(const __gr
     int* stop = &s.stop;
     const uint32_t tm_s = tm, tm_o = tm + 256;         // S (and P) of stream w at + 128 w, O likewise
 
-    if (warp != 10) {
+    if (warp != 9) {
         // ---- the query rows as swizzled operands (rows behind the batch:
-        // zeros), loads in batches, while warp 10 starts on the pages
+        // zeros), loads in batches, while warp 9 starts on the pages
         constexpr int kBatch = MODE == 2 ? 4 : 8;
-        for (int i0 = tid; i0 < kRowsCta * 16; i0 += kBatch * 320) {
+        for (int i0 = tid; i0 < kRowsCta * 16; i0 += kBatch * 288) {
             uint4 x[MODE == 2 ? 2 * kBatch : kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const int i = i0 + j * 320, row = row0 + (i >> 4);   // 8-channel unit i % 16 of row i / 16
+                const int i = i0 + j * 288, row = row0 + (i >> 4);   // 8-channel unit i % 16 of row i / 16
                 const int64_t at = ((int64_t)(row / a.G) * a.n_q + h * a.G + row % a.G) * kD + 8 * (i & 15);
                 const bool there = i < kRowsCta * 16 && row < R;
                 if (MODE == 2) {
@@ -115,7 +114,7 @@ __global__ void __launch_bounds__(kBf16Threads, 1) prefix_bf16_kernel(const __gr
             }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                const int i = i0 + j * 320, r = i >> 4, u = i & 15;
+                const int i = i0 + j * 288, r = i >> 4, u = i & 15;
                 if (i >= kRowsCta * 16) break;
                 uint8_t* dst = q_op + (r / kPRows) * kOperand + (u >> 3) * kHalfOperand + swizzled(r % kPRows, u & 7);
                 if (MODE == 2) {
@@ -139,10 +138,10 @@ __global__ void __launch_bounds__(kBf16Threads, 1) prefix_bf16_kernel(const __gr
             }
         }
         fence_async_smem();
-        asm volatile("bar.sync 1, 320;" ::: "memory");
+        asm volatile("bar.sync 1, 288;" ::: "memory");
     }
 
-    if (warp == 10) {
+    if (warp == 9) {
         // ---------------------------------------------------------- page copies
         constexpr int PPT = kTileTok / B;              // pages per tile
         const int used = (most + B - 1) / B;           // pages that hold a visible token
@@ -190,50 +189,48 @@ __global__ void __launch_bounds__(kBf16Threads, 1) prefix_bf16_kernel(const __gr
             for (int i = max(0, done_k - 2); i < done_k; ++i) mbar_wait_bounded(&s.k_full[i & 1], (i >> 1) & 1, kWaitLimit);
             for (int i = max(0, done_v - 2); i < done_v; ++i) mbar_wait_bounded(&s.v_full[i & 1], (i >> 1) & 1, kWaitLimit);
         }
-    } else if (warp >= 8) {
-        // ---------------------------------------------------------- products of stream w
-        const int w = warp - 8, items = steps > w ? (steps - w + 1) / 2 : 0;
-        if (items > 0) {
+    } else if (warp == 8) {
+        // ---------------------------------------------------------- products
+        if (steps > 0) {
             constexpr uint32_t kQk = mma_shape(kMmaBf16, kTileTok, false), kPv = mma_shape(kMmaBf16, kD, true);
-            const uint32_t q_desc = smem_operand(smem_addr(q_op), 16) + (MODE == 0 ? w * (kOperand >> 4) : 0);
-            const uint32_t k_desc = smem_operand(smem_addr(k_op), 16), v_desc = smem_operand(smem_addr(v_op), kHalfOperand);
-            const uint32_t sp = tm_s + 128 * w, o = tm_o + 128 * w;
+            const uint32_t q_desc = smem_operand(smem_addr(q_op), 16), k_desc = smem_operand(smem_addr(k_op), 16);
+            const uint32_t v_desc = smem_operand(smem_addr(v_op), kHalfOperand);
             bool ok = true;
-            for (int j = 0; j <= items && ok; ++j) {
-                if (j > 0) {                                      // O (+)= P V of item j - 1
-                    const int t = MODE == 0 ? j - 1 : 2 * (j - 1) + w, st = t & 1;
-                    ok = warp_wait_or_stop(&s.v_full[st], (t >> 1) & 1, stop, kWaitLimit);
-                    if (ok && most - (t_beg + t) * kTileTok < kTileTok) ok = warp_wait_or_stop(&s.v_clean, 0, stop, kWaitLimit);
-                    ok = ok && warp_wait_or_stop(&s.p_ready[w], (j - 1) & 1, stop, kWaitLimit);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t vd = v_desc + st * (kOperand >> 4);
+            for (int i = 0; i < steps + 2; ++i) {                 // O (+)= P V of step j, then S = Q K^T of step i
+                const int j = i - 2, w = i & 1, tj = MODE == 0 ? j >> 1 : j, ti = MODE == 0 ? i >> 1 : i;
+                if (i < steps && (MODE != 0 || w == 0)) ok = warp_wait_or_stop(&s.k_full[ti & 1], (ti >> 1) & 1, stop, kWaitLimit);
+                if (j >= 0) {
+                    if (MODE != 0 || w == 0) {
+                        ok = ok && warp_wait_or_stop(&s.v_full[tj & 1], (tj >> 1) & 1, stop, kWaitLimit);
+                        if (ok && most - (t_beg + tj) * kTileTok < kTileTok) ok = warp_wait_or_stop(&s.v_clean, 0, stop, kWaitLimit);
+                    }
+                    ok = ok && warp_wait_or_stop(&s.p_ready[w], (j >> 1) & 1, stop, kWaitLimit);
+                }
+                if (!ok) break;
+                tc_fence_after();
+                if (j >= 0) {
+                    const uint32_t p = tm_s + 128 * w, vd = v_desc + (tj & 1) * (kOperand >> 4);
 #pragma unroll
                     for (int k = 0; k < kTileTok / 16; ++k)       // 16 tokens: 8 columns of P, 2048 bytes of V rows
-                        mma_ts(o, sp + 8 * k, vd + k * (2048 >> 4), kPv, j > 1 || k > 0);
-                    mma_commit(&s.v_empty[st]);
+                        mma_ts(tm_o + 128 * w, p + 8 * k, vd + k * (2048 >> 4), kPv, j >= 2 || k > 0);
+                    if (MODE != 0 || w == 1) mma_commit(&s.v_empty[tj & 1]);
+                    if (j + 2 >= steps) mma_commit(&s.o_full[w]);
                 }
-                if (j < items) {                                  // S = Q K^T of item j
-                    const int t = MODE == 0 ? j : 2 * j + w, st = t & 1;
-                    ok = warp_wait_or_stop(&s.k_full[st], (t >> 1) & 1, stop, kWaitLimit);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t kd = k_desc + st * (kOperand >> 4);
+                if (i < steps) {
+                    const uint32_t qd = q_desc + (MODE == 0 ? w * (kOperand >> 4) : 0), kd = k_desc + (ti & 1) * (kOperand >> 4);
 #pragma unroll
                     for (int k = 0; k < (MODE == 2 ? 16 : 8); ++k) {   // (k >= 8: the query's low halves)
                         const uint32_t off = ((k >> 2 & 1) * kHalfOperand + (k & 3) * 32) >> 4;
-                        mma_ss(sp, q_desc + (k >> 3) * (kOperand >> 4) + off, kd + off, kQk, k > 0);
+                        mma_ss(tm_s + 128 * w, qd + (k >> 3) * (kOperand >> 4) + off, kd + off, kQk, k > 0);
                     }
                     mma_commit(&s.s_full[w]);
-                    mma_commit(&s.k_empty[st]);
+                    if (MODE != 0 || w == 1) mma_commit(&s.k_empty[ti & 1]);
                 }
             }
-            if (ok) mma_commit(&s.o_full[w]);
             // products in flight end before the operands and tensor memory go
-            mma_commit(&s.drained[w]);
-            if (!mbar_wait_bounded(&s.drained[w], 0, kWaitLimit)) *stop = 1;
+            mma_commit(&s.drained);
+            if (!mbar_wait_bounded(&s.drained, 0, kWaitLimit)) *stop = 1;
         }
-        __syncwarp();
     } else {
         // ---------------------------------------------------------- softmax
         const int w = warp >> 2;                                  // stream
@@ -307,7 +304,7 @@ cudaError_t launch_mode(const CUtensorMap& map, const PrefixArgs& p, cudaStream_
         ready[d] = true;
     }
     const dim3 grid(p.splits, (p.batch * p.G + rows - 1) / rows, p.n_kv);
-    return launch_pdl(prefix_bf16_kernel<B, MODE>, grid, kBf16Threads, bf16_prefix_smem(MODE), st, map, p);
+    return launch_pdl(prefix_bf16_kernel<B, MODE>, grid, 320, bf16_prefix_smem(MODE), st, map, p);
 }
 
 }  // namespace

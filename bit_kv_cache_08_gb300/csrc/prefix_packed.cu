@@ -20,8 +20,8 @@
 // tensor core; with one, steps are tiles, and the two S let the products of
 // one run under the softmax of the other.
 //
-// Warps: a row tile has 4 for the softmax (a row a thread) and one that issues
-// its products; one copies raw tiles and finds their exponents, 8 that build
+// Warps: 4 a row tile for the softmax (a row a thread), one that issues the
+// products, one that copies raw tiles and finds their exponents, 8 that build
 // operands without meeting at a barrier: one group's share of a record of the
 // packed format (K: 4 tokens x 8 channels, V: 8 tokens x 4 channels) is four
 // whole 16-byte units of the swizzled operand rows, so a lane reads a record's
@@ -47,7 +47,7 @@ constexpr float kLift = 7.f;                     // P up to 2^(8 + 7), small wei
 struct PackedSmem {
     // ready: a raw tile's exponent is known; raw_empty: its operands are built
     uint64_t raw_full[kRawStages], ready[kRawStages], raw_empty[kRawStages];
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], q_done, drained[2];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], q_done, drained;
     uint32_t tmem;
     int stop;
     int vexp[4];                                  // e of the last tiles
@@ -56,8 +56,7 @@ struct PackedSmem {
 template <int B, int BITS, int NT>   // NT: row tiles of a CTA
 struct PackedLayout {
     static constexpr int kSoft = 4 * NT;                       // softmax warps
-    static constexpr int kLoad = kSoft + NT;                   // a warp a row tile issues products, then the raw tiles' warp
-    static constexpr int kThreads = 32 * (kLoad + 1 + kBuildWarps);
+    static constexpr int kThreads = 32 * (kSoft + 2 + kBuildWarps);
     static constexpr int HB = head_block_bytes(B, BITS);
     static constexpr int kBlocks = kPkTok / B;                 // blocks per tile
     static constexpr int kRaw = kBlocks * 2 * HB;              // bytes of a raw tile: (K, V) per block
@@ -98,7 +97,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
     wait_prior_grids();
     let_next_grid_start();   // the own tokens' split kernel
     using Lay = PackedLayout<B, BITS, NT>;
-    constexpr int kSoft = Lay::kSoft, kLoad = Lay::kLoad;
+    constexpr int kSoft = Lay::kSoft;
     extern __shared__ uint8_t raw_smem[];
     uint8_t* base = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
     PackedSmem& s = *reinterpret_cast<PackedSmem*>(base);
@@ -114,6 +113,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
     const int tiles = (most + kPkTok - 1) / kPkTok;
     const int t_beg = (int)((int64_t)tiles * blockIdx.x / a.splits), t_end = (int)((int64_t)tiles * (blockIdx.x + 1) / a.splits);
     const int n = t_end - t_beg;                  // tiles
+    const int steps = NT * n;                     // step i: stream i % 2, tile i / NT
 
     if (tid == 0) {
         s.stop = 0;
@@ -124,15 +124,15 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.k_full[i], kBuildWarps);
-            mbar_init(&s.k_empty[i], NT);   // every row tile's products
+            mbar_init(&s.k_empty[i], 1);
             mbar_init(&s.v_full[i], kBuildWarps);
-            mbar_init(&s.v_empty[i], NT);
+            mbar_init(&s.v_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_ready[i], 4);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&s.o_full[i], 1);
         mbar_init(&s.q_done, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&s.drained[i], 1);
+        mbar_init(&s.drained, 1);
         fence_mbar_init();
     }
     if (warp == kSoft) tmem_alloc(&s.tmem, 512);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                      2 * Lay::HB, &s.raw_full[st]);
     };
     int fetched = 0;
-    if (warp == kLoad)
+    if (warp == kSoft + 1)
         for (; fetched < kRawStages - 1 && fetched < n; ++fetched) fetch(fetched);
 
     // ---- the query rows: their rotation H (sigma q) / sqrt(128) is itself a
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
     }
     fence_async_smem();
     __syncthreads();
-    if (warp < kLoad) {
+    if (warp <= kSoft) {
         if (warp == kSoft) {
             constexpr uint32_t kRot = mma_shape(kMmaBf16, kD, false);
             const uint32_t q_desc = smem_operand(smem_addr(q_lo), 16), l_desc = smem_operand(smem_addr(k_op), 16);
@@ -275,11 +275,11 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
             fence_async_smem();
         }
         tc_fence_before();
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kLoad) : "memory");   // the product warps wait for the rows
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * (kSoft + 1)) : "memory");   // the product warp waits for the rows
         tc_fence_after();
     }
 
-    if (warp == kLoad) {
+    if (warp == kSoft + 1) {
         // ---------------------------------------------------------- raw tiles and their exponents
         bool ok = true;
         for (int i = 0; i < n && ok; ++i) {
@@ -332,10 +332,10 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
         if (*reinterpret_cast<volatile int*>(stop))
             for (int i = max(0, fetched - kRawStages); i < fetched; ++i)
                 mbar_wait_bounded(&s.raw_full[i % kRawStages], (i / kRawStages) & 1, kWaitLimit);
-    } else if (warp > kLoad) {
+    } else if (warp > kSoft) {
         // ---------------------------------------------------------- operands from codes
         // warp bw: group g of the 32 records of half sb, a record a lane
-        const int bw = warp - (kLoad + 1), g = bw & 3, sb = bw >> 2, ra = lane >> 2, rb = lane & 3;
+        const int bw = warp - (kSoft + 2), g = bw & 3, sb = bw >> 2, ra = lane >> 2, rb = lane & 3;
         const int half0 = B == 64 ? 32 * sb : 0;          // the half's first token within its block
         // (code 2^-9) s + z 2^-9, times the rest of the value's factors and 2^9
         constexpr float kUp = 512.f;
@@ -458,51 +458,45 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                 warp_arrive(&s.raw_empty[st]);
             }
         }
-    } else if (warp >= kSoft) {
-        // ---------------------------------------------------------- products of row tile x
-        const int x = warp - kSoft;
-        if (n > 0) {
+    } else if (warp == kSoft) {
+        // ---------------------------------------------------------- products
+        if (steps > 0) {
             constexpr uint32_t kQk = mma_shape(kMmaBf16, kPkTok, false), kPv = mma_shape(kMmaF16, kD, false);
-            const uint32_t q_desc = smem_operand(smem_addr(q_lo), 16) + x * (kPkQ >> 4), k_desc = smem_operand(smem_addr(k_op), 16);
-            const uint32_t v_desc = smem_operand(smem_addr(v_op), 16), qa = tm_q + 64 * x, o = tm_o + 128 * x;
-            // With one row tile S has two buffers: tile i's scores come before
-            // tile i - 1's values, under whose softmax they are computed.
-            constexpr int kBehind = 3 - NT;
+            const uint32_t q_desc = smem_operand(smem_addr(q_lo), 16), k_desc = smem_operand(smem_addr(k_op), 16);
+            const uint32_t v_desc = smem_operand(smem_addr(v_op), 16);
             bool ok = true;
-            for (int i = 0; i < n + kBehind && ok; ++i) {
-                if (i >= kBehind) {                               // O (+)= P V' of tile t
-                    const int t = i - kBehind, st = t & 1, w = NT == 2 ? x : st;
-                    ok = warp_wait_or_stop(&s.v_full[st], (t >> 1) & 1, stop, kWaitLimit) &&
-                         warp_wait_or_stop(&s.p_ready[w], (NT == 2 ? t : t >> 1) & 1, stop, kWaitLimit);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t p = tm_s + 64 * w, vd = v_desc + st * (kPkV >> 4);
-#pragma unroll
-                    for (int k = 0; k < kPkTok / 16; ++k) mma_ts(o, p + 8 * k, vd + 2 * k, kPv, t > 0 || k > 0);
-                    mma_commit(&s.v_empty[st]);
+            for (int i = 0; i < steps + 2; ++i) {                 // O (+)= P V' of step j, then S = Q K'^T of step i
+                const int j = i - 2, w = i & 1, tj = j / NT, ti = i / NT, x = NT == 2 ? w : 0;
+                if (i < steps && (NT == 1 || w == 0)) ok = warp_wait_or_stop(&s.k_full[ti & 1], (ti >> 1) & 1, stop, kWaitLimit);
+                if (j >= 0) {
+                    if (NT == 1 || w == 0) ok = ok && warp_wait_or_stop(&s.v_full[tj & 1], (tj >> 1) & 1, stop, kWaitLimit);
+                    ok = ok && warp_wait_or_stop(&s.p_ready[w], (j >> 1) & 1, stop, kWaitLimit);
                 }
-                if (i < n) {                                      // S = Q K'^T of tile i
-                    const int st = i & 1, w = NT == 2 ? x : st;
-                    ok = warp_wait_or_stop(&s.k_full[st], (i >> 1) & 1, stop, kWaitLimit);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t kd = k_desc + st * (2 * kPkK >> 4);
+                if (!ok) break;
+                tc_fence_after();
+                if (j >= 0) {
+                    const uint32_t p = tm_s + 64 * w, vd = v_desc + (tj & 1) * (kPkV >> 4);
+#pragma unroll
+                    for (int k = 0; k < kPkTok / 16; ++k) mma_ts(tm_o + 128 * x, p + 8 * k, vd + 2 * k, kPv, tj > 0 || k > 0);
+                    if (NT == 1 || w == 1) mma_commit(&s.v_empty[tj & 1]);
+                    if (j + NT >= steps) mma_commit(&s.o_full[x]);
+                }
+                if (i < steps) {
+                    const uint32_t kd = k_desc + (ti & 1) * (2 * kPkK >> 4), qa = tm_q + 64 * x, qd = q_desc + x * (kPkQ >> 4);
 #pragma unroll
                     for (int k = 0; k < 24; ++k) {                // hi hi, hi lo, lo hi
                         const uint32_t kb = kd + (((k >> 3) == 1 ? kPkK >> 4 : 0) + (((k >> 2 & 1) * (kPkK / 2) + (k & 3) * 32) >> 4));
                         if (k < 16) mma_ts(tm_s + 64 * w, qa + 8 * (k & 7), kb, kQk, k > 0);
-                        else mma_ss(tm_s + 64 * w, q_desc + (((k >> 2 & 1) * (kPkQ / 2) + (k & 3) * 32) >> 4), kb, kQk, true);
+                        else mma_ss(tm_s + 64 * w, qd + (((k >> 2 & 1) * (kPkQ / 2) + (k & 3) * 32) >> 4), kb, kQk, true);
                     }
                     mma_commit(&s.s_full[w]);
-                    mma_commit(&s.k_empty[st]);
+                    if (NT == 1 || w == 1) mma_commit(&s.k_empty[ti & 1]);
                 }
             }
-            if (ok) mma_commit(&s.o_full[x]);
             // products in flight end before the operands and tensor memory go
-            mma_commit(&s.drained[x]);
-            if (!mbar_wait_bounded(&s.drained[x], 0, kWaitLimit)) *stop = 1;
+            mma_commit(&s.drained);
+            if (!mbar_wait_bounded(&s.drained, 0, kWaitLimit)) *stop = 1;
         }
-        __syncwarp();
     } else {
         // ---------------------------------------------------------- softmax
         const int x = warp >> 2;                                  // row tile
