@@ -41,6 +41,7 @@ constexpr int kPkV = kD * kPkTok * 2;            // 128 channel rows x 64 tokens
 constexpr int kPkQ = kPRows * kD * 2;            // 128 query rows, bf16
 constexpr int kRawStages = 4;
 constexpr int kBuildWarps = 8;
+static_assert(kRawStages + 2 <= 8, "exponents in flight");
 static_assert(2 * kPkV == kD * kD * 2, "the rotation matrix fits V's stages");
 constexpr float kLift = 7.f;                     // P up to 2^(8 + 7), small weights normal down to 2^-21
 
@@ -50,7 +51,9 @@ struct PackedSmem {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], q_done, drained;
     uint32_t tmem;
     int stop;
-    int vexp[4];                                  // e of the last tiles
+    // e of the last tiles: the raw tiles' warp is at most kRawStages tiles ahead of
+    // the V' that is built, which is at most two ahead of the softmax that reads e
+    int vexp[8];
 };
 
 template <int B, int BITS, int NT>   // NT: row tiles of a CTA
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                                 __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(cmax)));
             // the clamps keep 2^-e and 2^e finite
             if (lane == 0) {
-                s.vexp[i & 3] = bound > 0x1p-60f ? min(ceil_log2(bound), 100) : -60;
+                s.vexp[i & 7] = bound > 0x1p-60f ? min(ceil_log2(bound), 100) : -60;
                 mbar_arrive(&s.ready[st]);
             }
         }
@@ -426,7 +429,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                 const uint2 cu = *reinterpret_cast<const uint2*>(vb + off_C(B, BITS) + 2 * (32 * g + 4 * ra));
                 const uint32_t sw[4] = {su.x, su.y, su.z, su.w}, zw[4] = {zu.x, zu.y, zu.z, zu.w}, rw[4] = {ru.x, ru.y, ru.z, ru.w};
                 // (warps of an absent half, whose raw bytes may be anything, write zeros)
-                const float up = kUp * exp2i(-*reinterpret_cast<volatile int*>(&s.vexp[i & 3]));
+                const float up = kUp * exp2i(-*reinterpret_cast<volatile int*>(&s.vexp[i & 7]));
                 float2 zero[4], fac[4];            // token pairs
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
@@ -512,7 +515,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
             ok = warp_wait_or_stop(&s.s_full[w], j & 1, stop, kWaitLimit);
             if (!ok) break;
             tc_fence_after();
-            const int e = *reinterpret_cast<volatile int*>(&s.vexp[i & 3]);
+            const int e = *reinterpret_cast<volatile int*>(&s.vexp[i & 7]);
             ok = softmax_tile<kPkTok, NT == 2 ? 32 : 64, true>(tm_s + 64 * w + lanes, my_o, len - (t_beg + i) * kPkTok, scale, (float)e,
                                                         exp2i(-e), kLift, i == 0, st, &s.p_ready[w], [&] {
                 // O is idle once the last product into it has completed: with two row

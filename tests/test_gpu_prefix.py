@@ -207,6 +207,22 @@ def test_outlier_keys_and_sharp_softmax(kvlib, bits, B):
     _close(s.run(q, pl), want, tol)
 
 
+@pytest.mark.parametrize("bits", [0, 2, 3, 4])
+@pytest.mark.parametrize("batch,n_q,n_kv,B,P", [(256, 40, 10, 64, 2300), (8, 128, 64, 32, 2600), (70, 96, 48, 64, 3333)])
+def test_many_tiles_for_each_range(kvlib, bits, batch, n_q, n_kv, B, P):
+    """More row tiles and heads than the GPU has SMs: each CTA walks 10 to 50 tiles, whose value exponents differ."""
+    lens = [i % 3 for i in range(batch)]
+    s = Shared(kvlib, 31, P, lens, n_q, n_kv, B, bits, wild=True)
+    q = synth.queries(synth.make_gen(4), batch, n_q).to(torch.bfloat16).cuda()
+    pl = [P - 7 * (i % 5) for i in range(batch)]
+    got = s.run(q, pl)
+    seqs = [0, batch // 2, batch - 1]
+    want, tol = s.reference(q, pl, seqs)
+    _close(got[seqs], want, tol)
+    for _ in range(5):
+        assert torch.equal(got, s.run(q, pl))
+
+
 @pytest.mark.parametrize("bits", [0, 2])
 def test_scale_and_ablation_flags(kvlib, bits):
     for flags, scale in ((kvlib.FLAG_NO_ROTATION, 0.0), (0, 0.5), (kvlib.FLAG_NO_TOKEN_PASS, 0.02)):
