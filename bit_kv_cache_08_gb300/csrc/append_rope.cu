@@ -104,6 +104,9 @@ constexpr int kRowBatch = 4;
 template <int B>
 __global__ void __launch_bounds__(128) append_rope_bf16_kernel(RopeAppendArgs a, const __grid_constant__ kvarn_rope r,
                                                                int runs) {
+    __shared__ uint64_t turns[64];
+    copy_turns(r, turns);
+    __syncthreads();
     wait_prior_grids();
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(128) append_rope_bf16_kernel(RopeAppendArgs a,
     const bool ok = phys >= 0 && phys < a.n_pool_blocks;
     if (!ok && lane == 0) raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
     const int half = lane >> 4;
-    const RopeLane rl = rope_lane(r, (a.rope_pos ? (int64_t)a.rope_pos[b] : (int64_t)a.pos[b]) + i, lane & 15);
+    const RopeLane rl = rope_lane(r, turns, (a.rope_pos ? (int64_t)a.rope_pos[b] : (int64_t)a.pos[b]) + i, lane & 15);
     float qw[8], kw[8];
     load_weight(a.q_weight, rl, qw);
     load_weight(a.k_weight, rl, kw);
@@ -213,6 +216,9 @@ template <int B, int BITS>
 __global__ void __launch_bounds__(quant_threads<B>(), B == 64 ? 2 : 3) append_rope_kernel(RopeAppendArgs a,
                                                                             const __grid_constant__ kvarn_rope r,
                                                                             QuantParams p) {
+    __shared__ uint64_t turns[64];
+    copy_turns(r, turns);
+    __syncthreads();
     wait_prior_grids();
     __shared__ QuantSmem<B, BITS> q;
     __shared__ __align__(16) uint16_t tile[B * kD];   // the completed block's rows
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(quant_threads<B>(), B == 64 ? 2 : 3) append_ro
     const int64_t lo = max(pos, blk * B), hi = min(end, (blk + 1) * B);
     const int hw = tid >> 4, l = tid & 15;                      // half-warp, lane in it
     constexpr int kHalves = 2 * quant_warps<B>();
-    const RopeLane groups = rope_lane(r, 0, l);                 // (for the channel groups)
+    const RopeLane groups = rope_lane(r, turns, 0, l);                 // (for the channel groups)
     float w[8];
 
     if (a.q && (kind == 2 || (kind == 0 && !a.cu))) {           // (a decode step's few query rows ride with the keys)
@@ -245,7 +251,7 @@ __global__ void __launch_bounds__(quant_threads<B>(), B == 64 ? 2 : 3) append_ro
             if (x0 + (hw & ~1) >= rows) break;                  // (whole warps)
             const int x = min(x0 + hw, rows - 1), g = x % G;
             const int64_t at = lo + x / G, t = t0 + (at - pos);
-            const RopeLane rl = rope_lane(r, turn0 + at, l);
+            const RopeLane rl = rope_lane(r, turns, turn0 + at, l);
             uint2 u[2];
             load_row(a.q + t * a.q_stride + (int64_t)(h * G + g) * kD, rl, u);
             float v[8];
@@ -272,7 +278,7 @@ __global__ void __launch_bounds__(quant_threads<B>(), B == 64 ? 2 : 3) append_ro
                     *reinterpret_cast<uint2*>(row + groups.c1) = u[1];
                 }
             } else {
-                const RopeLane rl = rope_lane(r, turn0 + at, l);
+                const RopeLane rl = rope_lane(r, turns, turn0 + at, l);
                 load_row(a.k + t * a.k_stride + (int64_t)h * kD, rl, u);
                 float v[8];
                 turn_row(u, rl, a.k_weight != nullptr, w, r.eps, v);

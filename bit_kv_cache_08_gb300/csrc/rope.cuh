@@ -37,7 +37,12 @@ __device__ __forceinline__ void turn_cossin(uint64_t rate, int64_t pos, float sc
     s *= scale;
 }
 
-__device__ __forceinline__ RopeLane rope_lane(const kvarn_rope& r, int64_t pos, int l) {
+// turns: r.turns in shared memory (indexed as a kernel parameter, the lanes'
+// rates would come from the constant bank one after the other, for each row).
+__device__ __forceinline__ void copy_turns(const kvarn_rope& r, uint64_t* turns) {
+    if (threadIdx.x < 64) turns[threadIdx.x] = r.turns[threadIdx.x];
+}
+__device__ __forceinline__ RopeLane rope_lane(const kvarn_rope& r, const uint64_t* turns, int64_t pos, int l) {
     RopeLane p;
     p.interleaved = r.layout == KVARN_ROPE_INTERLEAVED;
     const int turned = r.rotary_dim / 8;   // lanes whose channels are rotated
@@ -52,7 +57,7 @@ __device__ __forceinline__ RopeLane rope_lane(const kvarn_rope& r, int64_t pos, 
     for (int k = 0; k < 4; ++k) { p.c[k] = 1.f; p.s[k] = 0.f; }
     if (l < turned) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) turn_cossin(r.turns[4 * l + k], pos, r.scale, p.c[k], p.s[k]);
+        for (int k = 0; k < 4; ++k) turn_cossin(turns[4 * l + k], pos, r.scale, p.c[k], p.s[k]);
     }
     return p;
 }
