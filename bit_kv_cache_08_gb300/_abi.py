@@ -327,6 +327,14 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: str = "no
     return f * (keep + (1 - keep) / factor), 1.0 if scaling == "bands" else 0.1 * float(np.log(factor)) + 1.0
 
 
+def _need_device(*tensors):
+    """The library launches on the current device: every buffer must be on it."""
+    dev = torch.cuda.current_device() if _raw_device is None else _raw_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
 def _need_vec(t, name: str, dtype, n: int):
     _need_cuda(t, name, dtype)
     if t.numel() != n:
@@ -390,6 +398,7 @@ def _append_rope(cfg, rope, pool, staging, block_table, pos, q, k, v, q_out, wor
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     if workspace.numel() < 256:
         raise ValueError("workspace must hold 256 bytes")
+    _need_device(pool, staging, block_table, pos, cu_tokens, rope_pos, q, k, v, q_weight, k_weight, q_out, workspace)
     tail = (block_table.data_ptr(), max_blocks, pos.data_ptr(), rope_ptr, cu_ptr, n, batch, q_ptr, k.data_ptr(),
             v.data_ptr(), qs, ks, vs, qw_ptr, kw_ptr, out_ptr, out_code, workspace.data_ptr(), _stream())
     if staging is None:
@@ -488,7 +497,7 @@ def decode_attn_bf16(cfg: Config, q: torch.Tensor, kv_pool: torch.Tensor, block_
                                         workspace.numel(), _stream()), "kvarn_decode_attn_bf16")
 
 
-def _prefix_args(cfg, q, prefix_table, prefix_lens, block_table, seq_lens, out, workspace):
+def _prefix_args(cfg, q, pool, staging, prefix_table, prefix_lens, block_table, seq_lens, out, workspace):
     _need_cuda(q, "q")
     _need_cuda(out, "out")
     _need_cuda(prefix_table, "prefix_table", _i32t)
@@ -503,6 +512,7 @@ def _prefix_args(cfg, q, prefix_table, prefix_lens, block_table, seq_lens, out, 
     rows, max_blocks = block_table.shape if block_table.dim() == 2 else (-1, 0)
     if prefix_lens.numel() != batch or seq_lens.numel() != batch or rows != batch:
         raise ValueError("prefix_lens, seq_lens and block_table must have a row for each sequence of q")
+    _need_device(pool, staging, q, out, prefix_table, prefix_lens, block_table, seq_lens, workspace)
     return (prefix_table.data_ptr(), prefix_table.numel(), prefix_lens.data_ptr(), block_table.data_ptr(), max_blocks,
             seq_lens.data_ptr(), batch, out.data_ptr(), _dtype_code(out), workspace.data_ptr(), workspace.numel(),
             _stream())
@@ -516,7 +526,7 @@ def prefix_attn(cfg: Config, q: torch.Tensor, pool: torch.Tensor, staging: torch
     own seq_lens[b] tokens. q (bf16|fp32) and out (bf16|fp32): [batch][n_q][128]."""
     _need_cuda(pool, "pool", torch.uint8)
     _need_cuda(staging, "staging", torch.bfloat16)
-    rest = _prefix_args(cfg, q, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
+    rest = _prefix_args(cfg, q, pool, staging, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
     if pool.dim() != 2 or pool.shape[1] != block_bytes(cfg):
         raise ValueError("pool must be [n_blocks][block_bytes]")
     if staging.numel() < q.shape[0] * cfg.n_kv_heads * 2 * cfg.block_size * 128:
@@ -530,7 +540,7 @@ def prefix_attn_bf16(cfg: Config, q: torch.Tensor, kv_pool: torch.Tensor, prefix
                      workspace: torch.Tensor):
     """prefix_attn over the bf16 pages [n_blocks][n_kv][2][B][128] of decode_attn_bf16."""
     _need_cuda(kv_pool, "kv_pool", torch.bfloat16)
-    rest = _prefix_args(cfg, q, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
+    rest = _prefix_args(cfg, q, kv_pool, None, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
     if kv_pool.shape[1:] != (cfg.n_kv_heads, 2, cfg.block_size, 128):
         raise ValueError("kv_pool must be [n_blocks][n_kv][2][B][128]")
     _check(lib().kvarn_prefix_attn_bf16(ctypes.byref(cfg), q.data_ptr(), _dtype_code(q), kv_pool.data_ptr(),

@@ -221,6 +221,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnA
 // ---------------------------------------------------------------- host side
 namespace {
 
+constexpr int64_t kMaxPrefix = 1 << 30;   // tokens
+
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // How the prefix kernel is cut: query rows of a CTA, token ranges (splits) and
@@ -267,7 +269,7 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
     int r = check_config(cfg, &c);
     if (r != KVARN_OK) return r;
     if (out_dtype != KVARN_BF16 && out_dtype != KVARN_FP32) return KVARN_ERR_INVALID_ARG;
-    if (prefix_blocks < 0 || (int64_t)prefix_blocks * c.block_size > 0x7fffffff) return KVARN_ERR_INVALID_ARG;
+    if (prefix_blocks < 0 || (int64_t)prefix_blocks * c.block_size > kMaxPrefix) return KVARN_ERR_INVALID_ARG;
     if (max_blocks == 0) block_table = seq_lens;         // tables without columns are never read
     if (prefix_blocks == 0) prefix_table = prefix_lens;
     r = check_packed_attn_args(c, q, q_dtype, pool, n_pool_blocks, PACKED ? staging : pool, block_table, max_blocks,
@@ -341,7 +343,9 @@ extern "C" {
 
 size_t kvarn_prefix_workspace_bytes(const kvarn_config* cfg, int32_t batch, int32_t prefix_blocks) {
     kvarn_config c;
-    if (check_config(cfg, &c) != KVARN_OK || batch < 0 || prefix_blocks < 0) return 0;
+    if (check_config(cfg, &c) != KVARN_OK || batch < 0 || prefix_blocks < 0 ||
+        (int64_t)prefix_blocks * c.block_size > kMaxPrefix || batch > 0x7fffffff / c.n_q_heads)
+        return 0;
     return prefix_ws_bytes(c, batch, prefix_blocks);
 }
 

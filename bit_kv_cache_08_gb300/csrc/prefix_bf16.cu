@@ -141,12 +141,12 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
         asm volatile("bar.sync 1, 288;" ::: "memory");
     }
 
+    int done_k = 0, done_v = 0;                        // tiles whose copies warp 9 has issued
     if (warp == 9) {
         // ---------------------------------------------------------- page copies
         constexpr int PPT = kTileTok / B;              // pages per tile
         const int used = (most + B - 1) / B;           // pages that hold a visible token
         bool ok = true;
-        int done_k = 0, done_v = 0;                    // tiles issued
         for (int i = 0; i < n && ok; ++i) {
             const int t = t_beg + i, st = i & 1;
             int page = -1;
@@ -184,19 +184,15 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
                 warp_arrive(&s.v_clean);
             }
         }
-        // copies in flight land before the CTA ends
-        if (*reinterpret_cast<volatile int*>(stop)) {
-            for (int i = max(0, done_k - 2); i < done_k; ++i) mbar_wait_bounded(&s.k_full[i & 1], (i >> 1) & 1, kWaitLimit);
-            for (int i = max(0, done_v - 2); i < done_v; ++i) mbar_wait_bounded(&s.v_full[i & 1], (i >> 1) & 1, kWaitLimit);
-        }
     } else if (warp == 8) {
         // ---------------------------------------------------------- products
         if (steps > 0) {
             constexpr uint32_t kQk = mma_shape(kMmaBf16, kTileTok, false), kPv = mma_shape(kMmaBf16, kD, true);
             const uint32_t q_desc = smem_operand(smem_addr(q_op), 16), k_desc = smem_operand(smem_addr(k_op), 16);
             const uint32_t v_desc = smem_operand(smem_addr(v_op), kHalfOperand);
-            bool ok = true;
-            for (int i = 0; i < steps + 2; ++i) {                 // O (+)= P V of step j, then S = Q K^T of step i
+            bool ok = !(a.flags & KVARN_FLAG_TEST_WAIT_TIMEOUT);
+            if (!ok && lane == 0) *stop = 1;                      // (test switch: as if the first wait had run out)
+            for (int i = 0; i < steps + 2 && ok; ++i) {           // O (+)= P V of step j, then S = Q K^T of step i
                 const int j = i - 2, w = i & 1, tj = MODE == 0 ? j >> 1 : j, ti = MODE == 0 ? i >> 1 : i;
                 if (i < steps && (MODE != 0 || w == 0)) ok = warp_wait_or_stop(&s.k_full[ti & 1], (ti >> 1) & 1, stop, kWaitLimit);
                 if (j >= 0) {
@@ -262,7 +258,14 @@ __global__ void __launch_bounds__(320, 1) prefix_bf16_kernel(const __grid_consta
         tc_fence_before();
     }
     __syncthreads();
-    if (tid == 0 && *stop) raise_error(a.err, KVARN_DEVERR_WAIT_TIMEOUT);
+    if (*stop) {   // a wait ran out: copies in flight land before the CTA ends
+        if (tid == 0) raise_error(a.err, KVARN_DEVERR_WAIT_TIMEOUT);
+        if (warp == 9) {
+            for (int i = max(0, done_k - 2); i < done_k; ++i) mbar_wait_bounded(&s.k_full[i & 1], (i >> 1) & 1, kWaitLimit);
+            for (int i = max(0, done_v - 2); i < done_v; ++i) mbar_wait_bounded(&s.v_full[i & 1], (i >> 1) & 1, kWaitLimit);
+        }
+        __syncthreads();
+    }
     if (warp == 8) {
         tc_fence_after();
         tmem_free(tm, 512);

@@ -331,10 +331,6 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                 mbar_arrive(&s.ready[st]);
             }
         }
-        // copies in flight land before the CTA ends
-        if (*reinterpret_cast<volatile int*>(stop))
-            for (int i = max(0, fetched - kRawStages); i < fetched; ++i)
-                mbar_wait_bounded(&s.raw_full[i % kRawStages], (i / kRawStages) & 1, kWaitLimit);
     } else if (warp > kSoft) {
         // ---------------------------------------------------------- operands from codes
         // warp bw: group g of the 32 records of half sb, a record a lane
@@ -467,8 +463,9 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
             constexpr uint32_t kQk = mma_shape(kMmaBf16, kPkTok, false), kPv = mma_shape(kMmaF16, kD, false);
             const uint32_t q_desc = smem_operand(smem_addr(q_lo), 16), k_desc = smem_operand(smem_addr(k_op), 16);
             const uint32_t v_desc = smem_operand(smem_addr(v_op), 16);
-            bool ok = true;
-            for (int i = 0; i < steps + 2; ++i) {                 // O (+)= P V' of step j, then S = Q K'^T of step i
+            bool ok = !(a.flags & KVARN_FLAG_TEST_WAIT_TIMEOUT);
+            if (!ok && lane == 0) *stop = 1;                      // (test switch: as if the first wait had run out)
+            for (int i = 0; i < steps + 2 && ok; ++i) {           // O (+)= P V' of step j, then S = Q K'^T of step i
                 const int j = i - 2, w = i & 1, tj = j / NT, ti = i / NT, x = NT == 2 ? w : 0;
                 if (i < steps && (NT == 1 || w == 0)) ok = warp_wait_or_stop(&s.k_full[ti & 1], (ti >> 1) & 1, stop, kWaitLimit);
                 if (j >= 0) {
@@ -533,7 +530,13 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
         tc_fence_before();
     }
     __syncthreads();
-    if (tid == 0 && *stop) raise_error(a.err, KVARN_DEVERR_WAIT_TIMEOUT);
+    if (*stop) {   // a wait ran out: copies in flight land before the CTA ends
+        if (tid == 0) raise_error(a.err, KVARN_DEVERR_WAIT_TIMEOUT);
+        if (warp == kSoft + 1)
+            for (int i = max(0, fetched - kRawStages); i < fetched; ++i)
+                mbar_wait_bounded(&s.raw_full[i % kRawStages], (i / kRawStages) & 1, kWaitLimit);
+        __syncthreads();
+    }
     if (warp == kSoft) {
         tc_fence_after();
         tmem_free(tm, 512);

@@ -129,7 +129,9 @@ typedef struct kvarn_config {
 /*
  * Test switch (no counterpart in the paper): with it, every warp of
  * kvarn_decode_attn's split kernel gives up its first shared-memory copy
- * wait at once, so the wait-timeout path runs without anything hanging:
+ * wait at once (and kvarn_prefix_attn's and kvarn_prefix_attn_bf16's prefix
+ * kernels act as if their first had), so the wait-timeout path runs without
+ * anything hanging:
  * KVARN_DEVERR_WAIT_TIMEOUT is raised, the copies already in flight are
  * waited for, the warp stops, the call's outputs are unspecified and the
  * workspace stays usable (clear the error word and call again). Ignored by
@@ -400,8 +402,8 @@ size_t kvarn_prefix_workspace_bytes(const kvarn_config* cfg, int32_t batch, int3
  * samples of one prompt), read once for all of them. (A serving convenience;
  * the query is multiplied by the same Hadamard matrix, section 三 3.1.)
  *
- * The prefix's blocks are prefix_table (device int32 [prefix_blocks]), every
- * one complete in the pool; sequence b sees its first prefix_lens[b] tokens
+ * The prefix's blocks are prefix_table (device int32 [prefix_blocks], at most
+ * 2^30 tokens), every one complete in the pool; sequence b sees its first prefix_lens[b] tokens
  * (device int32 [batch], 0 .. prefix_blocks * B: any count, the same for all
  * or not). Its own tokens follow: block_table, seq_lens and staging as for
  * kvarn_decode_attn, their indices starting at 0.
@@ -421,7 +423,12 @@ int kvarn_prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, c
 
 /*
  * kvarn_prefix_attn_bf16 -- the same over the bf16 pages of
- * kvarn_decode_attn_bf16; the last page of the prefix may be partly filled.
+ * kvarn_decode_attn_bf16; the last page of the prefix may be partly filled,
+ * and its rows behind the longest prefix_lens may hold anything. The values
+ * before that must be finite even for sequences that do not see them (their
+ * weight of 0 takes part in the product). Softmax weights of the prefix are
+ * rounded to bf16, the type of the values: the output is within 2^-8 of
+ * sum p |v| (kvarn_prefix_attn: fp16 weights and values, 2^-11 each).
  */
 int kvarn_prefix_attn_bf16(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* kv_pool,
                            int64_t n_pool_blocks, const int32_t* prefix_table, int32_t prefix_blocks,

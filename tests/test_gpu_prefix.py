@@ -279,6 +279,24 @@ def test_faults_are_flagged(kvlib, bits):
     assert torch.equal(s.run(q, [200] * 3, ws=ws), good)
 
 
+@pytest.mark.parametrize("bits,batch", [(0, 3), (0, 80), (2, 3), (2, 80), (4, 80)])
+def test_wait_timeout_path(kvlib, bits, batch):
+    """With the test switch the prefix kernels' product warp leaves at once: the other warps follow, the flag is raised,
+    and the workspace serves the next call."""
+    kv = kvlib
+    s = Shared(kv, 33, 1500, [2] * batch, 8, 2, 64, bits)
+    q = synth.queries(synth.make_gen(2), batch, 8).to(torch.bfloat16).cuda()
+    ws = kv.alloc_prefix_workspace(s.cfg, batch, len(s.prefix_np))
+    good = s.run(q, [1500] * batch, ws=ws)
+    s.cfg.flags |= kv.FLAG_TEST_WAIT_TIMEOUT
+    for _ in range(3):
+        s.run(q, [1500] * batch, ws=ws, check=False)
+        assert kv.read_error(ws) == kv.DEVERR_WAIT_TIMEOUT
+        kv.clear_error(ws)
+    s.cfg.flags &= ~kv.FLAG_TEST_WAIT_TIMEOUT
+    assert torch.equal(s.run(q, [1500] * batch, ws=ws), good)
+
+
 @pytest.mark.parametrize("bits", [0, 2])
 def test_pool_beyond_4_gib(kvlib, bits):
     n_kv, B = 2, 64

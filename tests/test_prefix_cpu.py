@@ -27,7 +27,7 @@ def _args(**change):
 
 BAD = [dict(cfg=None), dict(q=None), dict(q=0x10004), dict(q_dtype=2), dict(pool=None), dict(pool=0x10008),
        dict(n_pool=0), dict(n_pool=1 << 31), dict(ptable=None), dict(ptable=0x10002), dict(pblocks=-1),
-       dict(pblocks=1 << 27), dict(plens=None), dict(plens=0x10001), dict(table=None), dict(table=0x10002),
+       dict(pblocks=1 << 27), dict(pblocks=(1 << 25) + 1), dict(plens=None), dict(plens=0x10001), dict(table=None), dict(table=0x10002),
        dict(max_blocks=-1), dict(max_blocks=1 << 27), dict(lens=None), dict(lens=0x10002), dict(batch=-1),
        dict(batch=1 << 30), dict(out=None), dict(out=0x10004), dict(out_dtype=2), dict(ws=None), dict(ws=0x10008)]
 
@@ -40,6 +40,23 @@ def test_refusals(change):
     assert L.kvarn_prefix_attn_bf16(*a) == INV
 
 
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """The binding compares every tensor's device with the current one (two stand-in devices)."""
+    class OnDevice:
+        device = "cuda:1"
+
+        def __init__(self, i):
+            self.i = i
+
+        def get_device(self):
+            return self.i
+
+    monkeypatch.setattr(kv._abi, "_raw_device", lambda: 0)
+    kv._abi._need_device(OnDevice(0), None, OnDevice(0))
+    with pytest.raises(ValueError):
+        kv._abi._need_device(OnDevice(0), OnDevice(1))
+
+
 def test_staging_and_empty_batch():
     L = kv.lib()
     for bad in (None, 0x10008):
@@ -47,4 +64,5 @@ def test_staging_and_empty_batch():
     assert L.kvarn_prefix_attn(*_args(batch=0)) == 0
     cfg = kv.make_config(8, 2, 32, 2, synth.sign_bits(0))
     assert kv.prefix_workspace_bytes(cfg, 0, 10) == 256
+    assert kv.prefix_workspace_bytes(cfg, 1, (1 << 25) + 1) == 0 and kv.prefix_workspace_bytes(cfg, 1 << 29, 1) == 0
     assert kv.prefix_workspace_bytes(cfg, -1, 10) == 0 and kv.prefix_workspace_bytes(cfg, 1, -1) == 0
