@@ -672,20 +672,21 @@ __device__ __forceinline__ void decode_attn_2bit_body(const AttnArgs& a) {
 // The split kernel at ptxas's own register target, and with a minimum of
 // MINB resident CTAs per SM (at most 65536 / (32 MINB) registers a thread).
 // LATE: behind a kernel that lets this one start beside it (see
-// let_next_grid_start), the wait comes last.
+// let_next_grid_start), the wait comes last
+// (the grid has not ended before its last CTA has, so one CTA waits for all).
 template <int B, int BITS, int S, bool LATE>
 __global__ void __launch_bounds__(32) decode_attn_2bit_kernel(AttnArgs a) {
     if (LATE) let_next_grid_start();   // the merge, which waits for this one at its beginning
     else wait_prior_grids();
     decode_attn_2bit_body<B, BITS, S>(a);
-    if (LATE) wait_prior_grids();
+    if (LATE && blockIdx.x == gridDim.x - 1) wait_prior_grids();
 }
 template <int B, int BITS, int S, int MINB, bool LATE>
 __global__ void __launch_bounds__(32, MINB) decode_attn_2bit_kernel_minb(AttnArgs a) {
     if (LATE) let_next_grid_start();   // the merge, which waits for this one at its beginning
     else wait_prior_grids();
     decode_attn_2bit_body<B, BITS, S>(a);
-    if (LATE) wait_prior_grids();
+    if (LATE && blockIdx.x == gridDim.x - 1) wait_prior_grids();
 }
 
 // ---------------------------------------------------------------- host side

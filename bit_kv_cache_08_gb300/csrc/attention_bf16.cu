@@ -253,13 +253,14 @@ __device__ __forceinline__ void decode_attn_bf16_body(const AttnArgs& a) {
     }
 }
 
-// LATE: behind a kernel that lets this one start beside it, the wait comes last.
+// LATE: behind a kernel that lets this one start beside it, the wait comes last
+// (the grid has not ended before its last CTA has, so one CTA waits for all).
 template <int B, bool LATE>
 __global__ void __launch_bounds__(32) decode_attn_bf16_kernel(AttnArgs a) {
     if (LATE) let_next_grid_start();   // the merge, which waits for this one at its beginning
     else wait_prior_grids();
     decode_attn_bf16_body<B>(a);
-    if (LATE) wait_prior_grids();
+    if (LATE && blockIdx.x == gridDim.x - 1) wait_prior_grids();
 }
 
 size_t attn_bf16_smem_bytes() { return (size_t)kBfStages * kStageBytes + 64; }

@@ -88,8 +88,8 @@ __device__ __forceinline__ void wait_prior_grids() { asm volatile("griddepcontro
 
 // A kernel whose CTAs all call this (behind their wait) lets the next one in
 // the stream start beside it. That one may read what came before the first
-// but not what the first writes, and waits at its own end instead of its
-// beginning, so that a third kernel finds both complete.
+// but not what the first writes; it waits behind its own work instead of
+// before it, so that a third kernel finds both complete.
 __device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... KArgs, typename... Args>

@@ -9,7 +9,8 @@
 // the plain decode attention over the own tokens, and a merge of both kinds
 // of partial in the log-sum-exp sense,
 //   m = max m_i,  l = sum l_i 2^(m_i - m),  acc = sum acc_i 2^(m_i - m),
-// which also rotates back and adds the raw tail rows (packed cache).
+// which also rotates back and adds the raw tail rows (packed cache). Over bf16
+// pages with short own tables the last two are one (prefix_join_kernel).
 #include "host_checks.h"
 #include "prefix.cuh"
 
@@ -40,9 +41,9 @@ struct PrefixMerge {
 // LSE merge of the partials first .. last - 1 of a row's list (np own ones at
 // p0, pstride apart, then the prefix's at s0, sstride apart), 8 in flight at a
 // time with a running rescale; m, l and acc start at -inf, 0 and 0.
+template <int NB>
 __device__ __forceinline__ void lse_list(const float* p0, int np, int64_t pstride, const float* s0, int64_t sstride, int first,
                                          int last, int lane, float& m, float& l, float (&acc)[4]) {
-    constexpr int NB = 8;
     auto at = [&](int i) { return i < np ? p0 + i * pstride : s0 + (i - np) * sstride; };
     for (int i0 = first; i0 < last; i0 += NB) {
         const int cnt = min(NB, last - i0);
@@ -79,6 +80,39 @@ __device__ __forceinline__ void async_copy16(void* dst, const void* src) {
 }
 __device__ __forceinline__ void async_copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// (m, l, acc) += (ms, ls, as) in the log-sum-exp sense.
+__device__ __forceinline__ void add_slice(float m, float& l, float (&acc)[4], float ms, float ls, const float (&as)[4]) {
+    if (ms == -INFINITY) return;
+    const float mn = fmaxf(m, ms);
+    const float fa = m == -INFINITY ? 0.f : exp2f(m - mn), fs = exp2f(ms - mn);
+    l = l * fa + ls * fs;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = acc[k] * fa + as[k] * fs;
+}
+
+__device__ __forceinline__ void store_out(const PrefixMerge& pm, int64_t row, int lane, float l, float (&acc)[4]) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] *= inv;
+    if (pm.out_bf16) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0], acc[1]), hi = __floats2bfloat162_rn(acc[2], acc[3]);
+        reinterpret_cast<uint2*>(static_cast<uint16_t*>(pm.out) + row * kD)[lane] =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    } else {
+        reinterpret_cast<float4*>(static_cast<float*>(pm.out) + row * kD)[lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    }
+}
+
+// A sequence with a length outside its range: NaN and the error word.
+__device__ __forceinline__ void refuse_row(const AttnArgs& a, const PrefixMerge& pm, int b, int h) {
+    if (threadIdx.x == 0) raise_error(a.err, KVARN_DEVERR_POSITION);
+    for (int i = threadIdx.x; i < a.G * kD; i += blockDim.x) {
+        const int64_t at = ((int64_t)b * a.n_q + h * a.G) * kD + i;
+        if (pm.out_bf16) static_cast<uint16_t*>(pm.out)[at] = 0x7fc0;
+        else static_cast<float*>(pm.out)[at] = NAN;
+    }
+}
+
 // One CTA of 8 warps per (sequence, kv head): 8 / G warps to each of its G
 // query heads (their raw tail rows are copied to shared memory once), each
 // with a share of the row's partials and of the tail rows; the row's first warp
@@ -102,13 +136,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnA
     const int np = (ROT ? L >= B : L > 0) && wm.x >= 0 && wm.y >= wm.x && wm.y < a.nw ? wm.y - wm.x + 1 : 0;
     const float* p0 = a.partials + ((u + max(wm.x, 0)) * a.G + (mine ? g : 0)) * kPartialStride;
     const bool valid = L >= 0 && L <= a.max_blocks * B && PL >= 0 && PL <= pm.max_len;
-    if (!valid) {   // (the same for the whole CTA)
-        if (threadIdx.x == 0) raise_error(a.err, KVARN_DEVERR_POSITION);
-        for (int i = threadIdx.x; i < a.G * kD; i += 32 * kMergeWarps) {
-            const int64_t at = ((int64_t)b * a.n_q + h * a.G) * kD + i;
-            if (pm.out_bf16) static_cast<uint16_t*>(pm.out)[at] = 0x7fc0;
-            else static_cast<float*>(pm.out)[at] = NAN;
-        }
+    if (!valid) {
+        refuse_row(a, pm, b, h);
         return;
     }
     // the raw tail rows on their way to shared memory while the partials merge
@@ -127,7 +156,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnA
         float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
         const int n = np + (PL > 0 ? pm.splits : 0);
         const int64_t R = (int64_t)a.batch * a.G;
-        lse_list(p0, np, (int64_t)a.G * kPartialStride, pm.partials + partial_row(0, a.n_kv, h, R, (int64_t)b * a.G + g),
+        lse_list<8>(p0, np, (int64_t)a.G * kPartialStride, pm.partials + partial_row(0, a.n_kv, h, R, (int64_t)b * a.G + g),
                  partial_row(1, a.n_kv, 0, R, 0), n * part / parts, n * (part + 1) / parts, lane, m, l, acc);
         if (lane == 0) {
             slices[wp][0] = m;
@@ -198,24 +227,219 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnA
     if (ntail > 0) {
         float mt = -INFINITY, lt = 0.f, at[4] = {0.f, 0.f, 0.f, 0.f};
         combine_slices(&tails[wp][0], parts, lane, mt, lt, at);
-        if (mt != -INFINITY) {
-            const float mn = fmaxf(m, mt);
-            const float fa = m == -INFINITY ? 0.f : exp2f(m - mn), ft = exp2f(mt - mn);
-            l = l * fa + lt * ft;
+        add_slice(m, l, acc, mt, lt, at);
+    }
+    store_out(pm, gw, lane, l, acc);
+}
+
+// ---------------------------------------------------------------- own tokens and merge in one (bf16 pages)
+constexpr int kJoinTokens = 1024;   // columns of an own table it takes
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bf16_pair(float v0, float v1, bool low) {   // RN(v), or RN(v - RN(v))
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
+    if (!low) return *reinterpret_cast<const uint32_t*>(&h);
+    const float2 f = __bfloat1622float2(h);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(v0 - f.x, v1 - f.y);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Warp wp's share of a unit's own tokens (16-token chunks wp, wp + W, ...) as
+// a slice (m, l, acc) for each of its G heads, both products on mma.sync with
+// the columns (head, high | low half of q or of p), as in attention_bf16.cu.
+// The fragments are loaded straight from the pages: the order of the channels
+// in S and of the output rows in O is free, so a lane's 16-byte loads of K
+// (token gq, channels 32 j + 8 tq ..) and V (channels 64 j + 8 gq .. of the
+// four tokens its A fragment holds) are whole fragments, and nothing passes
+// through shared memory but q.
+template <int B, int W>
+__device__ __forceinline__ void own_slice(const AttnArgs& a, int b, int h, int L, int wp, int lane, uint2 (*qf)[32],
+                                          float (*own)[W][kPartialStride]) {
+    constexpr int CPB = B / kChunk;
+    const int gq = lane >> 2, tq = lane & 3;
+    const int head = gq >> 1;          // this lane's column of the products: (head, high | low half)
+    const bool low = gq & 1;
+    const int chunks = (L + kChunk - 1) / kChunk, n = chunks > wp ? (chunks - wp + W - 1) / W : 0;
+    const int64_t head_block = 2 * B * kD * 2;
+    const uint8_t* lane_k = a.pool + h * head_block + gq * (kD * 2) + tq * 16;
+    const uint8_t* lane_v = a.pool + h * head_block + B * kD * 2 + 2 * tq * (kD * 2) + gq * 16;
+    const int32_t* table = a.block_table + (int64_t)b * a.max_blocks;
+    // lane i holds the block of this warp's chunk i (without a look at L, which is on its way too)
+    static_assert(kJoinTokens <= 32 * W * kChunk, "a lane for each chunk of a warp");
+    const int held = (wp + W * lane) / CPB < a.max_blocks ? table[(wp + W * lane) / CPB] : 0;
+    auto good = [&](int phys) { return phys >= 0 && phys < a.n_pool_blocks; };
+    uint4 k[2][4], v[4][2];
+    auto offset_of = [&](int i, int phys) {
+        return phys * a.block_bytes + (wp + W * i) % CPB * (kChunk * kD * 2);
+    };
+    auto load_k = [&](int64_t at, int rows) {
+        const uint8_t* p = lane_k + at;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[k] = acc[k] * fa + at[k] * ft;
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                k[t][j] = 8 * t + gq < rows ? __ldcg(reinterpret_cast<const uint4*>(p + 8 * t * (kD * 2) + 64 * j))
+                                            : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto load_v = [&](int64_t at, int rows) {
+        const uint8_t* p = lane_v + at;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int row = (t & 1) + 8 * (t >> 1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                v[t][j] = 2 * tq + row < rows ? __ldcg(reinterpret_cast<const uint4*>(p + row * (kD * 2) + 128 * j))
+                                              : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    int rows = 0;   // of the chunk; none in a bad block
+    auto start = [&](int i) {
+        const int phys = __shfl_sync(kFull, held, i);
+        rows = good(phys) ? L - (wp + W * i) * kChunk : 0;
+        if (rows == 0 && lane == 0) raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
+        return offset_of(i, rows ? phys : 0);
+    };
+    int64_t at = 0;
+    if (n > 0) {
+        at = start(0);
+        load_k(at, rows);
+        load_v(at, rows);
+    }
+    for (int ks = wp; ks < 8; ks += W) {   // the query as the B operand of each k-step, a column for each (head, high | low half)
+        const int c = 32 * (ks >> 1) + 8 * tq + 4 * (ks & 1);
+        const int64_t at_q = ((int64_t)b * a.n_q + h * a.G + min(head, a.G - 1)) * kD + c;
+        float x[4];
+        if (a.q_dtype == KVARN_FP32) {
+            *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at_q);
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + at_q);
+            x[0] = __uint_as_float(u.x << 16);
+            x[1] = __uint_as_float(u.x & 0xffff0000u);
+            x[2] = __uint_as_float(u.y << 16);
+            x[3] = __uint_as_float(u.y & 0xffff0000u);
+        }
+        qf[ks][lane] = make_uint2(bf16_pair(x[0], x[1], low), bf16_pair(x[2], x[3], low));
+    }
+    __syncthreads();
+    float o[8][4], m = -INFINITY, l = 0.f;   // o[4 i + e]: channels 64 i + 8 gq + 2 e (+ 1), head tq high | low
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    const float qs = a.sm_scale * kLog2e;
+    for (int i = 0; i < n; ++i) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};   // tokens gq and gq + 8, head tq high | low
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint2 q0 = qf[2 * j][lane], q1 = qf[2 * j + 1][lane];
+            mma_bf16(s, k[0][j].x, k[1][j].x, k[0][j].y, k[1][j].y, q0.x, q0.y);
+            mma_bf16(s, k[0][j].z, k[1][j].z, k[0][j].w, k[1][j].w, q1.x, q1.y);
+        }
+        const int here = rows;
+        const float s0 = gq < here ? (s[0] + s[1]) * qs : -INFINITY, s1 = gq + 8 < here ? (s[2] + s[3]) * qs : -INFINITY;
+        float bm = fmaxf(s0, s1);
+        bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 4));
+        bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 8));
+        bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 16));
+        const float mn = fmaxf(m, bm), off = mn == -INFINITY ? 0.f : mn;
+        const float f = mn == -INFINITY ? 1.f : exp2f(m - mn), p0 = exp2f(s0 - off), p1 = exp2f(s1 - off);
+        m = mn;
+        l = l * f + (p0 + p1);
+        if (__any_sync(kFull, f != 1.f)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                o[e][0] *= f;
+                o[e][1] *= f;
+                o[e][2] *= f;
+                o[e][3] *= f;
+            }
+        }
+        // weights of tokens 2 tq, 2 tq + 1 and 2 tq + 8, 2 tq + 9 for this lane's column
+        const int from = 8 * tq + head;
+        const uint32_t b0 = bf16_pair(__shfl_sync(kFull, p0, from), __shfl_sync(kFull, p0, from + 4), low);
+        const uint32_t b1 = bf16_pair(__shfl_sync(kFull, p1, from), __shfl_sync(kFull, p1, from + 4), low);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t* r0 = &v[0][j].x;
+            const uint32_t* r1 = &v[1][j].x;
+            const uint32_t* r2 = &v[2][j].x;
+            const uint32_t* r3 = &v[3][j].x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                mma_bf16(o[4 * j + e], __byte_perm(r0[e], r1[e], 0x5410), __byte_perm(r0[e], r1[e], 0x7632),
+                         __byte_perm(r2[e], r3[e], 0x5410), __byte_perm(r2[e], r3[e], 0x7632), b0, b1);
+        }
+        if (i + 1 < n) {
+            at = start(i + 1);
+            load_k(at, rows);
+            load_v(at, rows);
         }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    l += __shfl_xor_sync(kFull, l, 4);
+    l += __shfl_xor_sync(kFull, l, 8);
+    l += __shfl_xor_sync(kFull, l, 16);
+    if (tq < a.G) {
+        float* sl = own[tq][wp];
+        if (gq == 0) {
+            sl[0] = m;
+            sl[1] = l;
+        }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] *= inv;
-    if (pm.out_bf16) {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0], acc[1]), hi = __floats2bfloat162_rn(acc[2], acc[3]);
-        reinterpret_cast<uint2*>(static_cast<uint16_t*>(pm.out) + gw * kD)[lane] =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    } else {
-        reinterpret_cast<float4*>(static_cast<float*>(pm.out) + gw * kD)[lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        for (int e = 0; e < 8; e += 2)
+            *reinterpret_cast<float4*>(sl + 4 + 64 * (e >> 2) + 8 * gq + 2 * (e & 3)) =
+                make_float4(o[e][0] + o[e][1], o[e][2] + o[e][3], o[e + 1][0] + o[e + 1][1], o[e + 1][2] + o[e + 1][3]);
     }
+}
+
+// One CTA of W warps per (sequence, kv head): its own tokens, then, when the
+// prefix kernel is through, the merge with the prefix's partials. Against the
+// split kernel and a merge this saves a launch and the own tokens' partials,
+// but a unit has only its CTA. Memory bounds it (512 bytes a token and kv
+// head) where the units fill the GPU, the chain of dependent loads where they
+// do not. 16 warps per SM in CTAs of 4 finish 64 x 192 own tokens of 8 kv
+// heads behind 8192 of a prefix in 18 us, the whole call in 35 us (as CTAs of
+// 8: 38; at 8 or 12 warps per SM, with the next chunk's loads in flight
+// during a chunk's products: 45, 37; split and merge: 42); 128 x 384 behind
+// 32 768 in 110 (115; 127, 105; 119).
+template <int B, int W>
+__global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 4) prefix_join_kernel(AttnArgs a, PrefixMerge pm) {
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    const int b = blockIdx.x, h = blockIdx.y;
+    const int parts = a.G == 1 ? W : a.G == 2 ? W / 2 : W / 4, g = wp / parts, part = wp % parts;
+    const int64_t gw = (int64_t)b * a.n_q + h * a.G + g;
+    __shared__ __align__(16) float own[4][W][kPartialStride];
+    __shared__ __align__(16) float slices[W][kPartialStride];
+    __shared__ uint2 qf[8][32];
+    const int L = a.seq_lens[b], PL = pm.lens[b];
+    if (L < 0 || L > a.max_blocks * B || PL < 0 || PL > pm.max_len) {
+        wait_prior_grids();
+        refuse_row(a, pm, b, h);
+        return;
+    }
+    own_slice<B, W>(a, b, h, L, wp, lane, qf, own);
+    wait_prior_grids();   // the prefix kernel, beside which this one may have started
+    if (g < a.G) {
+        float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+        const int n = PL > 0 ? pm.splits : 0;
+        const int64_t R = (int64_t)a.batch * a.G;
+        lse_list<16>(nullptr, 0, 0, pm.partials + partial_row(0, a.n_kv, h, R, (int64_t)b * a.G + g),
+                 partial_row(1, a.n_kv, 0, R, 0), n * part / parts, n * (part + 1) / parts, lane, m, l, acc);
+        if (lane == 0) {
+            slices[wp][0] = m;
+            slices[wp][1] = l;
+        }
+        *reinterpret_cast<float4*>(&slices[wp][4 + 4 * lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    }
+    __syncthreads();
+    if (g >= a.G || part != 0) return;
+    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    combine_slices(&slices[wp][0], parts, lane, m, l, acc);
+    float mo = -INFINITY, lo = 0.f, ao[4] = {0.f, 0.f, 0.f, 0.f};
+    combine_slices(&own[g][0][0], W, lane, mo, lo, ao);
+    add_slice(m, l, acc, mo, lo, ao);
+    store_out(pm, gw, lane, l, acc);
 }
 
 // ---------------------------------------------------------------- host side
@@ -310,7 +534,11 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
     p.flags = c.flags;
     for (int i = 0; i < 4; ++i) p.sb[i] = c.sign_bits[i];
     cudaError_t e;
-    AttnArgs a;
+    AttnArgs a = {};
+    // (an own table of more columns may hold sequences that are long for one CTA:
+    // 4 sequences of up to 1024 / 2048 own tokens, 8 kv heads: 26 / 49 us against
+    // 28 / 30 by the split kernel and a merge; 128: 108 / 183 against 111 / 182)
+    const bool join = !PACKED && (int64_t)max_blocks * c.block_size <= kJoinTokens;
     if constexpr (PACKED) {
         e = launch_prefix_packed(c, p, st);
         if (e == cudaSuccess)
@@ -318,7 +546,7 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
                                     seq_lens, batch, nullptr, workspace, nw, true, &a, st);
     } else {
         e = launch_prefix_bf16(p, c.block_size, st);
-        if (e == cudaSuccess)
+        if (e == cudaSuccess && !join)
             e = launch_decode_split_bf16(c, q, q_dtype, pool, n_pool_blocks, block_table, max_blocks, seq_lens, batch,
                                          nullptr, workspace, nw, true, &a, st);
     }
@@ -329,8 +557,32 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
     if constexpr (PACKED)
         e = c.block_size == 32 ? launch_pdl(prefix_merge_kernel<32, true>, units, threads, 0, st, a, pm)
                                : launch_pdl(prefix_merge_kernel<64, true>, units, threads, 0, st, a, pm);
-    else
+    else if (!join)
         e = launch_pdl(prefix_merge_kernel<kChunk, false>, units, threads, 0, st, a, pm);
+    else {
+        a.q = q;
+        a.pool = p.pool;
+        a.block_table = block_table;
+        a.seq_lens = seq_lens;
+        a.err = p.err;
+        a.n_pool_blocks = n_pool_blocks;
+        a.block_bytes = p.block_bytes;
+        a.q_dtype = q_dtype;
+        a.max_blocks = max_blocks;
+        a.batch = batch;
+        a.n_q = p.n_q;
+        a.n_kv = p.n_kv;
+        a.G = G;
+        a.sm_scale = c.sm_scale;
+        const auto start = [&](auto w) {
+            constexpr int W = decltype(w)::value;
+            return c.block_size == 32 ? launch_pdl(prefix_join_kernel<32, W>, units, 32 * W, 0, st, a, pm)
+                                      : launch_pdl(prefix_join_kernel<64, W>, units, 32 * W, 0, st, a, pm);
+        };
+        // (8 warps share a unit where there is an SM for each)
+        e = (int64_t)batch * c.n_kv_heads <= current_device_sms() ? start(std::integral_constant<int, 8>{})
+                                                                  : start(std::integral_constant<int, 4>{});
+    }
     return e == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 

@@ -344,6 +344,58 @@ def test_two_graphs_with_their_own_workspaces(kvlib, bits):
             assert torch.equal(outs[i], s.run(q[i], lens))
 
 
+OWN = [  # own lengths, batch repeats, n_q, n_kv, B, q dtype
+    ([1024, 1023, 0, 517, 16, 15, 1, 64], 1, 8, 2, 64, torch.bfloat16),
+    ([1024, 33, 992, 0], 1, 3, 1, 32, torch.float32),
+    ([700, 5, 0, 128, 300], 1, 4, 2, 64, torch.float32),
+    ([90, 129, 17, 64, 255, 1], 4, 28, 7, 64, torch.bfloat16),     # more units than the GPU has SMs
+    ([40, 3, 100, 0, 63], 13, 12, 12, 32, torch.float32),          # several waves of them
+]
+
+
+@pytest.mark.parametrize("bits", [0, 2, 3, 4])
+@pytest.mark.parametrize("case", range(len(OWN)))
+def test_own_tokens_in_narrow_and_wide_tables(kvlib, case, bits):
+    """Own tokens up to 1024; the same with table columns that no length reaches, for which other kernels serve."""
+    lens, times, n_q, n_kv, B, qdt = OWN[case]
+    lens, P = lens * times, 150
+    s = Shared(kvlib, 50 + case, P, lens, n_q, n_kv, B, bits)
+    q = (2 * synth.queries(synth.make_gen(30 + case), len(lens), n_q)).to(qdt).cuda()
+    pl = [(P, 0, 149, 1)[b % 4] for b in range(len(lens))]
+    seqs = list(range(len(lens) // times)) + [len(lens) - 1]
+    want, tol = s.reference(q, pl, seqs)
+    table = s.table
+    for columns in (table.shape[1], 1024 // B + 1, 4096 // B):
+        s.table = torch.full((len(lens), columns), -1, dtype=torch.int32, device="cuda")
+        s.table[:, :table.shape[1]] = table
+        got = s.run(q, pl)
+        _close(got[seqs], want, tol)
+        assert torch.equal(got, s.run(q, pl))
+
+
+@pytest.mark.parametrize("bits", [0, 2])
+def test_bad_own_blocks_are_flagged(kvlib, bits):
+    """A bad entry of a sequence's own table touches no other sequence and reads nothing."""
+    kv = kvlib
+    s = Shared(kv, 61, 100, [200, 70, 300], 8, 2, 32, bits)
+    q = synth.queries(synth.make_gen(7), 3, 8).cuda()
+    narrow = s.table
+    for columns in (narrow.shape[1], 40):
+        s.table = torch.full((3, columns), -1, dtype=torch.int32, device="cuda")
+        s.table[:, :narrow.shape[1]] = narrow
+        ws = kv.alloc_prefix_workspace(s.cfg, 3, len(s.prefix_np))
+        good = s.run(q, [100, 3, 0], ws=ws)
+        for bad in (-1, s.n_pool, 2 ** 31 - 1, -2 ** 31):
+            kept = int(s.table[0, 2])
+            s.table[0, 2] = bad
+            got = s.run(q, [100, 3, 0], ws=ws, check=False)
+            assert kv.read_error(ws) == kv.DEVERR_BLOCK_ID
+            assert torch.equal(got[1:], good[1:])
+            s.table[0, 2] = kept
+            kv.clear_error(ws)
+        assert torch.equal(s.run(q, [100, 3, 0], ws=ws), good)
+
+
 def test_no_own_blocks_and_small_tables(kvlib):
     for bits in (0, 2):
         s = Shared(kvlib, 19, 64, [0, 0], 4, 2, 32, bits)           # a block table without columns
