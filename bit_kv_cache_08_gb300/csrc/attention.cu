@@ -54,6 +54,7 @@
 // q's hi | lo halves are read from shared memory per block rather than held
 // in 32 registers per lane.
 #include "attn_common.cuh"
+#include "prefix_merge.cuh"
 
 namespace kvarn {
 
@@ -81,21 +82,33 @@ __host__ __device__ constexpr int attn_q_bytes(int) { return 2 * kQZero + 2 * kD
 // store instruction fall on different banks without padding
 __host__ __device__ constexpr int pex_rot(int B, int r) { return B == 64 ? 16 * r : 16 * (r >> 1); }
 
+// Shared memory of a warp: the stages, their barriers, q and the exchange rows.
 template <int B, int BITS, int S>
-__device__ __forceinline__ void decode_attn_2bit_body(const AttnArgs& a) {
+constexpr int attn_warp_bytes() {
+    return S * 2 * head_block_bytes(B, BITS) + 64 + attn_q_bytes(B) + 2 * 4 * B * (int)sizeof(uint16_t);
+}
+
+// UNIT: instead of its range of all units' blocks, the warp takes its share
+// (one of u.parts) of one unit's blocks and leaves its result where q was, a
+// slice for each of the G heads. Returns whether it left one (without UNIT:
+// nothing of use).
+struct UnitShare {
+    int b, h, part, parts;
+};
+template <int B, int BITS, int S, bool UNIT>
+__device__ __forceinline__ bool decode_attn_2bit_body(const AttnArgs& a, uint8_t* smem, const UnitShare u) {
     static_assert(BITS >= 2 && BITS <= 4, "2-, 3- or 4-bit codes");
     constexpr int HB = head_block_bytes(B, BITS);
     constexpr int RW = 4 * BITS;             // 32-bit words per lane record
     constexpr int NSB = B / 32;
     // kA: the operand scale of a code (2-bit: even fields' raw subnormals)
     constexpr float kA = BITS == 2 ? kRawScale : kCodeScale;
-    extern __shared__ __align__(16) uint8_t smem[];
     uint8_t* stages = smem;                                              // S x (K, V)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * 2 * HB);     // S mbarriers
     float* qsm = reinterpret_cast<float*>(smem + S * 2 * HB + 64);       // [4][128] fp32 q, then the fp16 planes below
     uint16_t* pex = reinterpret_cast<uint16_t*>(smem + S * 2 * HB + 64 + attn_q_bytes(B));   // [hi|lo][4 heads][B]
 
-    const int lane = threadIdx.x;
+    const int lane = UNIT ? threadIdx.x & 31 : threadIdx.x;
     const int gq = lane >> 2, tq = lane & 3;   // mma groupID, thread-in-group
     const int w = blockIdx.x;
 
@@ -116,13 +129,21 @@ __device__ __forceinline__ void decode_attn_2bit_body(const AttnArgs& a) {
     const SplitArgs sp{a.seq_lens, a.batch, n_kv, max_blocks, B, 0, 1};
     Cursor cc;
     cc.b = cc.h = cc.j = 0;
-    const int64_t W = split_locate(sp, 0, lane, cc.b, cc.h, cc.j);
-    const int64_t nwe = split_active_warps(W, a.nw, (int64_t)a.batch * n_kv, kSplitRatio2bit * B);
-    if (w >= nwe) return;
-    const int64_t s_beg = (int64_t)w * W / nwe, s_end = (int64_t)(w + 1) * W / nwe;
-    if (s_beg >= s_end) return;
-    split_locate(sp, s_beg, lane, cc.b, cc.h, cc.j);
-    cc.nb = split_nblocks(sp, cc.b);
+    int64_t s_beg, s_end;
+    if constexpr (UNIT) {
+        cc = Cursor{u.b, u.h, 0, split_nblocks(sp, u.b)};
+        s_beg = (int64_t)cc.nb * u.part / u.parts, s_end = (int64_t)cc.nb * (u.part + 1) / u.parts;
+        if (s_beg >= s_end) return false;
+        cc.j = (int)s_beg;
+    } else {
+        const int64_t W = split_locate(sp, 0, lane, cc.b, cc.h, cc.j);
+        const int64_t nwe = split_active_warps(W, a.nw, (int64_t)a.batch * n_kv, kSplitRatio2bit * B);
+        if (w >= nwe) return false;
+        s_beg = (int64_t)w * W / nwe, s_end = (int64_t)(w + 1) * W / nwe;
+        if (s_beg >= s_end) return false;
+        split_locate(sp, s_beg, lane, cc.b, cc.h, cc.j);
+        cc.nb = split_nblocks(sp, cc.b);
+    }
     Cursor ic = cc;   // issue cursor
     {
         // the first unit's query rows on their way to L1 while the block table
@@ -268,7 +289,7 @@ __device__ __forceinline__ void decode_attn_2bit_body(const AttnArgs& a) {
         l += __shfl_xor_sync(kFull, l, 16);
         if (head_ok) {
             const int64_t slot = (int64_t)cc.b * n_kv + cc.h + w;
-            float* base = partials + (slot * G + tq) * kPartialStride;
+            float* base = UNIT ? qsm + tq * kPartialStride : partials + (slot * G + tq) * kPartialStride;
             if (gq == 0) {
                 base[0] = m_run;
                 base[1] = l;
@@ -278,10 +299,10 @@ __device__ __forceinline__ void decode_attn_2bit_body(const AttnArgs& a) {
                 *reinterpret_cast<float4*>(base + 4 + 32 * g + 4 * gq) =
                     make_float4(O[2 * g].x, O[2 * g].y, O[2 * g + 1].x, O[2 * g + 1].y);
         }
-        if (lane == 0) {
-            const int64_t u = (int64_t)cc.b * n_kv + cc.h;
-            if (u_first) umap[2 * u] = w;
-            if (last) umap[2 * u + 1] = w;
+        if (!UNIT && lane == 0) {
+            const int64_t at = (int64_t)cc.b * n_kv + cc.h;
+            if (u_first) umap[2 * at] = w;
+            if (last) umap[2 * at + 1] = w;
         }
     };
 
@@ -302,12 +323,12 @@ __device__ __forceinline__ void decode_attn_2bit_body(const AttnArgs& a) {
     };
     if (!mbar_wait_bounded(&bars[0], 0, a.first_wait_limit)) {
         give_up(s_beg);
-        return;
+        return false;
     }
     for (int64_t x = s_beg; x < s_end; ++x) {
         if (!mbar_wait_bounded(&bars[stage], phase, kWaitLimit)) {
             give_up(x);
-            return;
+            return false;
         }
         const uint8_t* Kb = stages + stage * 2 * HB;
         const uint8_t* Vb = Kb + HB;
@@ -667,31 +688,89 @@ __device__ __forceinline__ void decode_attn_2bit_body(const AttnArgs& a) {
             if (x + 1 < s_end) unit_setup();
         }
     }
+    return true;
 }
 
 // The split kernel at ptxas's own register target, and with a minimum of
 // MINB resident CTAs per SM (at most 65536 / (32 MINB) registers a thread).
 // LATE: behind a kernel that lets this one start beside it (see
-// let_next_grid_start), the wait comes last
-// (the grid has not ended before its last CTA has, so one CTA waits for all).
+// let_next_grid_start), the wait comes last, and in one CTA (the grid has not
+// ended before that one has).
 template <int B, int BITS, int S, bool LATE>
 __global__ void __launch_bounds__(32) decode_attn_2bit_kernel(AttnArgs a) {
     if (LATE) let_next_grid_start();   // the merge, which waits for this one at its beginning
     else wait_prior_grids();
-    decode_attn_2bit_body<B, BITS, S>(a);
+    extern __shared__ __align__(16) uint8_t smem[];
+    decode_attn_2bit_body<B, BITS, S, false>(a, smem, UnitShare{});
     if (LATE && blockIdx.x == gridDim.x - 1) wait_prior_grids();
 }
 template <int B, int BITS, int S, int MINB, bool LATE>
 __global__ void __launch_bounds__(32, MINB) decode_attn_2bit_kernel_minb(AttnArgs a) {
     if (LATE) let_next_grid_start();   // the merge, which waits for this one at its beginning
     else wait_prior_grids();
-    decode_attn_2bit_body<B, BITS, S>(a);
+    extern __shared__ __align__(16) uint8_t smem[];
+    decode_attn_2bit_body<B, BITS, S, false>(a, smem, UnitShare{});
     if (LATE && blockIdx.x == gridDim.x - 1) wait_prior_grids();
 }
 
-// ---------------------------------------------------------------- host side
 template <int B, int BITS>
 constexpr int stages_for() { return 2; }
+
+// ---------------------------------------------------------------- own tokens and merge behind a shared prefix
+// One CTA of 8 warps per (sequence, kv head): a share of the unit's complete
+// own blocks each, the raw tail rows (copied over the blocks' stages), and,
+// when the prefix kernel is through, the merge with the prefix's partials and
+// the rotation back. Where a CTA per SM holds all units, this saves a launch
+// and the own results' way through memory, and on SMs that the prefix kernel
+// leaves free it runs beside it: 4 sequences of up to 64 / 1024 own tokens
+// behind 4096 of a prefix, 8 kv heads, 2-bit, as a graph: 18.5 / 26.2 us
+// against 22.2 / 29.5 with the split kernel and a merge; bound by the latency
+// of the prefix kernel and then of the partials' loads.
+template <int B, int BITS>
+__global__ void __launch_bounds__(32 * kMergeWarps, 1) prefix_join_packed_kernel(AttnArgs a, PrefixMerge pm) {
+    constexpr int S = stages_for<B, BITS>(), kWarp = attn_warp_bytes<B, BITS, S>(), kResult = S * 2 * head_block_bytes(B, BITS) + 64;
+    static_assert(4 * kPartialStride * 4 <= attn_q_bytes(B), "the slices fit where q was");
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float slices[kMergeWarps][kPartialStride], tails[kMergeWarps][kPartialStride];
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    const int b = blockIdx.x, h = blockIdx.y;
+    const int parts = merge_parts(a.G, kMergeWarps), g = wp / parts, part = wp % parts;
+    const bool mine = g < a.G;
+    const int L = a.seq_lens[b], PL = pm.lens[b];
+    if (!lengths_ok<B>(a, pm, L, PL)) {
+        wait_prior_grids();
+        refuse_row(a, pm, b, h);
+        return;
+    }
+    float* result = reinterpret_cast<float*>(smem + wp * kWarp + kResult);
+    if (!decode_attn_2bit_body<B, BITS, S, true>(a, smem + wp * kWarp, UnitShare{b, h, wp, kMergeWarps}))
+        for (int j = 0; j < a.G; ++j) {
+            const float none[4] = {0.f, 0.f, 0.f, 0.f};
+            put_slice(result + j * kPartialStride, lane, -INFINITY, 0.f, none);
+        }
+    const int ntail = L % B;
+    if (ntail > 0) {
+        __syncthreads();   // the stages have been read
+        const TailRows<B / kMergeWarps, kWarp> rows{smem};
+        static_assert(rows.kBytes <= S * 2 * head_block_bytes(B, BITS), "tail rows fit the stages");
+        copy_tail<B>(a, rows, b, h, ntail);
+        async_copy_wait();
+        __syncthreads();
+        if (mine) tail_share(a, rows, ntail, part, parts, (int64_t)b * a.n_q + h * a.G + g, lane, tails[wp]);
+    }
+    wait_prior_grids();   // the prefix kernel, beside which this one may have started
+    if (mine) prefix_slice(a, pm, b, h, g, part, parts, PL, lane, slices[wp]);
+    __syncthreads();
+    if (!mine || part != 0) return;
+    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    combine_slices(&slices[wp][0], parts, lane, m, l, acc);
+    float mo = -INFINITY, lo = 0.f, ao[4] = {0.f, 0.f, 0.f, 0.f};
+    combine_slices(reinterpret_cast<const float*>(smem + kResult) + g * kPartialStride, kMergeWarps, lane, mo, lo, ao, kWarp / 4);
+    add_slice(m, l, acc, mo, lo, ao);
+    finish_row<true>(a, pm, (int64_t)b * a.n_q + h * a.G + g, ntail > 0 ? &tails[wp][0] : nullptr, parts, lane, m, l, acc);
+}
+
+// ---------------------------------------------------------------- host side
 
 // Minimum resident CTAs per SM that the split kernel is compiled for (0: the
 // plain kernel), chosen by timing each instantiation on the 64 x 8192-token
@@ -713,13 +792,12 @@ constexpr auto attn_kernel_fn() {
 
 template <int B, int BITS>
 size_t attn_smem_bytes() {
-    return (size_t)stages_for<B, BITS>() * 2 * head_block_bytes(B, BITS) + 64 + attn_q_bytes(B) +
-           2 * 4 * B * sizeof(uint16_t);
+    return (size_t)attn_warp_bytes<B, BITS, stages_for<B, BITS>()>();
 }
 
 template <int B, int BITS>
 struct AttnKernel {
-    static constexpr int kB = B;
+    static constexpr int kB = B, kBits = BITS;
     static constexpr auto fn = attn_kernel_fn<B, BITS, false>();
     static constexpr auto late = attn_kernel_fn<B, BITS, true>();
     static size_t smem() { return attn_smem_bytes<B, BITS>(); }
@@ -750,16 +828,11 @@ int attn_grid_warps(int block_size, int bits, int device) {
     return cache[bi][wi][device];
 }
 
-// The arguments of a decode launch, and its split kernel alone (the caller
-// merges: launch_decode_attn, or the shared-prefix attention, behind whose
-// prefix kernel it starts early).
-cudaError_t launch_decode_split(const kvarn_config& cfg, const void* q, int q_dtype, const void* pool,
-                               int64_t n_pool_blocks, int64_t block_bytes, const void* staging,
-                               const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
-                               int batch, float* out, void* workspace, int nw, bool late, AttnArgs* args,
-                                cudaStream_t st) {
-    AttnArgs& a = *args;
-    a = {};
+// The arguments of a decode launch.
+AttnArgs decode_split_args(const kvarn_config& cfg, const void* q, int q_dtype, const void* pool, int64_t n_pool_blocks,
+                           int64_t block_bytes, const void* staging, const int32_t* block_table, int max_blocks,
+                           const int32_t* seq_lens, int batch, float* out, void* workspace, int nw) {
+    AttnArgs a = {};
     a.q = q;
     a.q_dtype = q_dtype;
     a.pool = (const uint8_t*)pool;
@@ -790,9 +863,27 @@ cudaError_t launch_decode_split(const kvarn_config& cfg, const void* q, int q_dt
     // wait-timeout path, run without a hang)
     a.first_wait_limit = (cfg.flags & KVARN_FLAG_TEST_WAIT_TIMEOUT) ? 0u : kWaitLimit;
     for (int i = 0; i < 4; ++i) a.sb[i] = cfg.sign_bits[i];
+    return a;
+}
+
+// The split kernel alone (the caller merges: launch_decode_attn, or the
+// shared-prefix attention, behind whose prefix kernel it starts early).
+cudaError_t launch_decode_split(const kvarn_config& cfg, const AttnArgs& a, bool late, cudaStream_t st) {
     return with_attn_kernel(cfg.block_size, cfg.bits, [&](auto k) {
         using K = decltype(k);
-        return launch_pdl(late ? K::late : K::fn, nw, 32, K::smem(), st, a);
+        return launch_pdl(late ? K::late : K::fn, a.nw, 32, K::smem(), st, a);
+    });
+}
+
+// The own tokens' part of a shared-prefix call and its merge, one CTA per
+// (sequence, kv head); a: as decode_split_args fills it.
+cudaError_t launch_prefix_join_packed(const kvarn_config& cfg, const AttnArgs& a, const PrefixMerge& pm, cudaStream_t st) {
+    return with_attn_kernel(cfg.block_size, cfg.bits, [&](auto k) {
+        using K = decltype(k);
+        const auto fn = prefix_join_packed_kernel<K::kB, K::kBits>;
+        const int bytes = kMergeWarps * (int)K::smem();
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        return e != cudaSuccess ? e : launch_pdl(fn, dim3(a.batch, a.n_kv), 32 * kMergeWarps, bytes, st, a, pm);
     });
 }
 
@@ -800,9 +891,9 @@ cudaError_t launch_decode_attn(const kvarn_config& cfg, const void* q, int q_dty
                                int64_t n_pool_blocks, int64_t block_bytes, const void* staging,
                                const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
                                int batch, float* out, void* workspace, int nw, cudaStream_t st) {
-    AttnArgs a;
-    const cudaError_t e = launch_decode_split(cfg, q, q_dtype, pool, n_pool_blocks, block_bytes, staging, block_table,
-                                              max_blocks, seq_lens, batch, out, workspace, nw, false, &a, st);
+    const AttnArgs a = decode_split_args(cfg, q, q_dtype, pool, n_pool_blocks, block_bytes, staging, block_table, max_blocks,
+                                         seq_lens, batch, out, workspace, nw);
+    const cudaError_t e = launch_decode_split(cfg, a, false, st);
     if (e != cudaSuccess) return e;
     // up to one wave of wide CTAs (4 per SM), so that 8 warps share each
     // row's raw tail rows

@@ -253,8 +253,8 @@ __device__ __forceinline__ void decode_attn_bf16_body(const AttnArgs& a) {
     }
 }
 
-// LATE: behind a kernel that lets this one start beside it, the wait comes last
-// (the grid has not ended before its last CTA has, so one CTA waits for all).
+// LATE: behind a kernel that lets this one start beside it, the wait comes
+// last, and in one CTA (the grid has not ended before that one has).
 template <int B, bool LATE>
 __global__ void __launch_bounds__(32) decode_attn_bf16_kernel(AttnArgs a) {
     if (LATE) let_next_grid_start();   // the merge, which waits for this one at its beginning

@@ -254,17 +254,18 @@ __device__ __forceinline__ void lse_stream(const float* p0, int np, int64_t pstr
 }
 
 // The same merge over the per-warp results (m, l, acc[128], at 0, 1 and 4 of
-// each kPartialStride-float row) of the n <= 32 warps of a wide merge.
-__device__ __forceinline__ void combine_slices(const float* sl, int n, int lane, float& m, float& l, float (&acc)[4]) {
-    const float pm = lane < n ? sl[lane * kPartialStride] : -INFINITY;
-    const float pl = lane < n ? sl[lane * kPartialStride + 1] : 0.f;
+// each of n <= 32 rows, kPartialStride floats apart) of the warps of a wide merge.
+__device__ __forceinline__ void combine_slices(const float* sl, int n, int lane, float& m, float& l, float (&acc)[4],
+                                               int stride = kPartialStride) {
+    const float pm = lane < n ? sl[lane * stride] : -INFINITY;
+    const float pl = lane < n ? sl[lane * stride + 1] : 0.f;
     m = warp_max(pm);
     if (m == -INFINITY) return;
     const float wl = (lane < n && pm != -INFINITY) ? exp2f(pm - m) : 0.f;
     l = warp_sum(pl * wl);
     for (int i = 0; i < n; ++i) {
         const float wgt = __shfl_sync(kFull, wl, i);
-        const float4 pa = *reinterpret_cast<const float4*>(sl + i * kPartialStride + 4 + 4 * lane);
+        const float4 pa = *reinterpret_cast<const float4*>(sl + i * stride + 4 + 4 * lane);
         acc[0] = fmaf(wgt, pa.x, acc[0]);
         acc[1] = fmaf(wgt, pa.y, acc[1]);
         acc[2] = fmaf(wgt, pa.z, acc[2]);

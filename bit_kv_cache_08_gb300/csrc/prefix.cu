@@ -9,17 +9,19 @@
 // the plain decode attention over the own tokens, and a merge of both kinds
 // of partial in the log-sum-exp sense,
 //   m = max m_i,  l = sum l_i 2^(m_i - m),  acc = sum acc_i 2^(m_i - m),
-// which also rotates back and adds the raw tail rows (packed cache). Over bf16
-// pages with short own tables the last two are one (prefix_join_kernel).
+// which also rotates back and adds the raw tail rows (packed cache). Where own
+// tables are short, the last two are one: prefix_join_kernel over bf16 pages,
+// prefix_join_packed_kernel (attention.cu) over the packed cache.
 #include "host_checks.h"
-#include "prefix.cuh"
+#include "prefix_merge.cuh"
 
 namespace kvarn {
 
-cudaError_t launch_decode_split(const kvarn_config& cfg, const void* q, int q_dtype, const void* pool,
-                                int64_t n_pool_blocks, int64_t block_bytes, const void* staging,
-                                const int32_t* block_table, int max_blocks, const int32_t* seq_lens, int batch,
-                                float* out, void* workspace, int nw, bool late, AttnArgs* args, cudaStream_t st);
+AttnArgs decode_split_args(const kvarn_config& cfg, const void* q, int q_dtype, const void* pool, int64_t n_pool_blocks,
+                           int64_t block_bytes, const void* staging, const int32_t* block_table, int max_blocks,
+                           const int32_t* seq_lens, int batch, float* out, void* workspace, int nw);
+cudaError_t launch_decode_split(const kvarn_config& cfg, const AttnArgs& a, bool late, cudaStream_t st);
+cudaError_t launch_prefix_join_packed(const kvarn_config& cfg, const AttnArgs& a, const PrefixMerge& pm, cudaStream_t st);
 cudaError_t launch_decode_split_bf16(const kvarn_config& cfg, const void* q, int q_dtype, const void* kv_pool,
                                      int64_t n_pool_blocks, const int32_t* block_table, int max_blocks,
                                      const int32_t* seq_lens, int batch, float* out, void* workspace, int nw,
@@ -28,102 +30,17 @@ cudaError_t launch_decode_split_bf16(const kvarn_config& cfg, const void* q, int
 cudaError_t launch_prefix_bf16(const PrefixArgs& p, int block_size, cudaStream_t st);
 cudaError_t launch_prefix_packed(const kvarn_config& c, const PrefixArgs& p, cudaStream_t st);
 
-struct PrefixMerge {
-    const float* partials;
-    const int32_t* lens;
-    int max_len;
-    int splits;
-    void* out;
-    int out_bf16;
-};
-
 // ---------------------------------------------------------------- merge
-// LSE merge of the partials first .. last - 1 of a row's list (np own ones at
-// p0, pstride apart, then the prefix's at s0, sstride apart), 8 in flight at a
-// time with a running rescale; m, l and acc start at -inf, 0 and 0.
-template <int NB>
-__device__ __forceinline__ void lse_list(const float* p0, int np, int64_t pstride, const float* s0, int64_t sstride, int first,
-                                         int last, int lane, float& m, float& l, float (&acc)[4]) {
-    auto at = [&](int i) { return i < np ? p0 + i * pstride : s0 + (i - np) * sstride; };
-    for (int i0 = first; i0 < last; i0 += NB) {
-        const int cnt = min(NB, last - i0);
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (lane < cnt) ml = __ldcg(reinterpret_cast<const float2*>(at(i0 + lane)));
-        float4 pa[NB];
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-            if (i < cnt) pa[i] = __ldcg(reinterpret_cast<const float4*>(at(i0 + i) + 4) + lane);
-        const float bm = warp_max(ml.x);
-        if (bm == -INFINITY) continue;
-        const float mn = fmaxf(m, bm);
-        const float fa = m == -INFINITY ? 0.f : exp2f(m - mn);
-        const float wl = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);
-        l = l * fa + warp_sum(ml.y * wl);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] *= fa;
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            if (i < cnt) {
-                const float wgt = __shfl_sync(kFull, wl, i);
-                acc[0] = fmaf(wgt, pa[i].x, acc[0]);
-                acc[1] = fmaf(wgt, pa[i].y, acc[1]);
-                acc[2] = fmaf(wgt, pa[i].z, acc[2]);
-                acc[3] = fmaf(wgt, pa[i].w, acc[3]);
-            }
-        }
-        m = mn;
-    }
-}
-
-__device__ __forceinline__ void async_copy16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void async_copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-// (m, l, acc) += (ms, ls, as) in the log-sum-exp sense.
-__device__ __forceinline__ void add_slice(float m, float& l, float (&acc)[4], float ms, float ls, const float (&as)[4]) {
-    if (ms == -INFINITY) return;
-    const float mn = fmaxf(m, ms);
-    const float fa = m == -INFINITY ? 0.f : exp2f(m - mn), fs = exp2f(ms - mn);
-    l = l * fa + ls * fs;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = acc[k] * fa + as[k] * fs;
-}
-
-__device__ __forceinline__ void store_out(const PrefixMerge& pm, int64_t row, int lane, float l, float (&acc)[4]) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] *= inv;
-    if (pm.out_bf16) {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0], acc[1]), hi = __floats2bfloat162_rn(acc[2], acc[3]);
-        reinterpret_cast<uint2*>(static_cast<uint16_t*>(pm.out) + row * kD)[lane] =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    } else {
-        reinterpret_cast<float4*>(static_cast<float*>(pm.out) + row * kD)[lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    }
-}
-
-// A sequence with a length outside its range: NaN and the error word.
-__device__ __forceinline__ void refuse_row(const AttnArgs& a, const PrefixMerge& pm, int b, int h) {
-    if (threadIdx.x == 0) raise_error(a.err, KVARN_DEVERR_POSITION);
-    for (int i = threadIdx.x; i < a.G * kD; i += blockDim.x) {
-        const int64_t at = ((int64_t)b * a.n_q + h * a.G) * kD + i;
-        if (pm.out_bf16) static_cast<uint16_t*>(pm.out)[at] = 0x7fc0;
-        else static_cast<float*>(pm.out)[at] = NAN;
-    }
-}
-
 // One CTA of 8 warps per (sequence, kv head): 8 / G warps to each of its G
 // query heads (their raw tail rows are copied to shared memory once), each
 // with a share of the row's partials and of the tail rows; the row's first warp
 // combines the shares and finishes the row.
-constexpr int kMergeWarps = 8;
 template <int B, bool ROT>
 __global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnArgs a, PrefixMerge pm) {
     wait_prior_grids();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int b = blockIdx.x, h = blockIdx.y;
-    const int parts = a.G == 1 ? 8 : a.G == 2 ? 4 : 2, g = wp / parts, part = wp % parts;   // (G = 3: two warps are left over)
+    const int parts = merge_parts(a.G, kMergeWarps), g = wp / parts, part = wp % parts;
     const bool mine = g < a.G;
     const int64_t gw = (int64_t)b * a.n_q + h * a.G + (mine ? g : 0);
     __shared__ __align__(16) float slices[kMergeWarps][kPartialStride];
@@ -135,105 +52,38 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnA
     const int2 wm = __ldcg(reinterpret_cast<const int2*>(a.unit_map) + u);
     const int np = (ROT ? L >= B : L > 0) && wm.x >= 0 && wm.y >= wm.x && wm.y < a.nw ? wm.y - wm.x + 1 : 0;
     const float* p0 = a.partials + ((u + max(wm.x, 0)) * a.G + (mine ? g : 0)) * kPartialStride;
-    const bool valid = L >= 0 && L <= a.max_blocks * B && PL >= 0 && PL <= pm.max_len;
-    if (!valid) {
+    if (!lengths_ok<B>(a, pm, L, PL)) {
         refuse_row(a, pm, b, h);
         return;
     }
     // the raw tail rows on their way to shared memory while the partials merge
-    // (K rows 272 bytes apart: a lane scores a row, and 32 rows then differ in bank)
-    constexpr int kKPitch = kD * 2 + 16;
-    __shared__ __align__(16) uint8_t tail_k[ROT ? B * kKPitch : 16], tail_v[ROT ? B * kD * 2 : 16];
     const int ntail = ROT ? L % B : 0;
-    if (ntail > 0) {
-        const uint16_t* kst = a.staging + ((int64_t)b * a.n_kv + h) * 2 * B * kD;
-        for (int i = threadIdx.x; i < ntail * 16; i += 32 * kMergeWarps) {
-            async_copy16(tail_k + (i >> 4) * kKPitch + (i & 15) * 16, kst + i * 8);
-            async_copy16(tail_v + i * 16, kst + B * kD + i * 8);
-        }
-    }
+    using Tail = TailRows<ROT ? B : 1, 0>;
+    __shared__ __align__(16) uint8_t tail_rows[ROT ? Tail::kBytes : 16];
+    const Tail rows{tail_rows};
+    if (ntail > 0) copy_tail<B>(a, rows, b, h, ntail);
     if (mine) {
         float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
         const int n = np + (PL > 0 ? pm.splits : 0);
         const int64_t R = (int64_t)a.batch * a.G;
         lse_list<8>(p0, np, (int64_t)a.G * kPartialStride, pm.partials + partial_row(0, a.n_kv, h, R, (int64_t)b * a.G + g),
-                 partial_row(1, a.n_kv, 0, R, 0), n * part / parts, n * (part + 1) / parts, lane, m, l, acc);
-        if (lane == 0) {
-            slices[wp][0] = m;
-            slices[wp][1] = l;
-        }
-        *reinterpret_cast<float4*>(&slices[wp][4 + 4 * lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                    partial_row(1, a.n_kv, 0, R, 0), n * part / parts, n * (part + 1) / parts, lane, m, l, acc);
+        put_slice(slices[wp], lane, m, l, acc);
     }
     if (ntail > 0) {
         async_copy_wait();
         __syncthreads();
-        // this warp's share of the tail rows (at most 32), a row a lane
-        const int c0 = ntail * part / parts, cnt = ntail * (part + 1) / parts - c0;
-        if (mine) {
-            float qv[4];
-            load_q4(a.q, a.q_dtype, gw, lane, qv);
-            const float qs = a.sm_scale * kLog2e;
-            *reinterpret_cast<float4*>(&tails[wp][4 * lane]) = make_float4(qv[0] * qs, qv[1] * qs, qv[2] * qs, qv[3] * qs);
-            __syncwarp();
-            float s = -INFINITY;
-            if (lane < cnt) {
-                const uint4* kr = reinterpret_cast<const uint4*>(tail_k + (c0 + lane) * kKPitch);
-                s = 0.f;
-#pragma unroll 4
-                for (int c = 0; c < 16; ++c) {
-                    const uint4 k = kr[c];
-                    const float4 qa = *reinterpret_cast<const float4*>(&tails[wp][8 * c]);
-                    const float4 qb = *reinterpret_cast<const float4*>(&tails[wp][8 * c + 4]);
-                    s = fmaf(qa.x, __uint_as_float(k.x << 16), s);
-                    s = fmaf(qa.y, __uint_as_float(k.x & 0xffff0000u), s);
-                    s = fmaf(qa.z, __uint_as_float(k.y << 16), s);
-                    s = fmaf(qa.w, __uint_as_float(k.y & 0xffff0000u), s);
-                    s = fmaf(qb.x, __uint_as_float(k.z << 16), s);
-                    s = fmaf(qb.y, __uint_as_float(k.z & 0xffff0000u), s);
-                    s = fmaf(qb.z, __uint_as_float(k.w << 16), s);
-                    s = fmaf(qb.w, __uint_as_float(k.w & 0xffff0000u), s);
-                }
-            }
-            const float tm = warp_max(s);
-            const float p = s == -INFINITY ? 0.f : exp2f(s - tm);
-            const float tl = warp_sum(p);
-            float tacc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-            for (int i = 0; i < cnt; ++i) {
-                const float w = __shfl_sync(kFull, p, i);
-                const uint2 v = reinterpret_cast<const uint2*>(tail_v + (c0 + i) * kD * 2)[lane];
-                tacc[0] = fmaf(w, __uint_as_float(v.x << 16), tacc[0]);
-                tacc[1] = fmaf(w, __uint_as_float(v.x & 0xffff0000u), tacc[1]);
-                tacc[2] = fmaf(w, __uint_as_float(v.y << 16), tacc[2]);
-                tacc[3] = fmaf(w, __uint_as_float(v.y & 0xffff0000u), tacc[3]);
-            }
-            __syncwarp();   // (the query has been read)
-            if (lane == 0) {
-                tails[wp][0] = tm;
-                tails[wp][1] = tl;
-            }
-            *reinterpret_cast<float4*>(&tails[wp][4 + 4 * lane]) = make_float4(tacc[0], tacc[1], tacc[2], tacc[3]);
-        }
+        if (mine) tail_share(a, rows, ntail, part, parts, gw, lane, tails[wp]);
     }
     __syncthreads();
     if (!mine || part != 0) return;
     float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     combine_slices(&slices[wp][0], parts, lane, m, l, acc);
-    if (ROT && !(a.flags & KVARN_FLAG_NO_ROTATION)) {
-        fwht128(acc, lane);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] *= kInvSqrtD * sign_of4(a.sb[0], a.sb[1], a.sb[2], a.sb[3], 4 * lane + k);
-    }
-    if (ntail > 0) {
-        float mt = -INFINITY, lt = 0.f, at[4] = {0.f, 0.f, 0.f, 0.f};
-        combine_slices(&tails[wp][0], parts, lane, mt, lt, at);
-        add_slice(m, l, acc, mt, lt, at);
-    }
-    store_out(pm, gw, lane, l, acc);
+    finish_row<ROT>(a, pm, gw, ntail > 0 ? &tails[wp][0] : nullptr, parts, lane, m, l, acc);
 }
 
 // ---------------------------------------------------------------- own tokens and merge in one (bf16 pages)
-constexpr int kJoinTokens = 1024;   // columns of an own table it takes
+constexpr int kJoinTokens = 1024;   // of an own table's columns, at most
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -407,31 +257,20 @@ template <int B, int W>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 4) prefix_join_kernel(AttnArgs a, PrefixMerge pm) {
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int b = blockIdx.x, h = blockIdx.y;
-    const int parts = a.G == 1 ? W : a.G == 2 ? W / 2 : W / 4, g = wp / parts, part = wp % parts;
+    const int parts = merge_parts(a.G, W), g = wp / parts, part = wp % parts;
     const int64_t gw = (int64_t)b * a.n_q + h * a.G + g;
     __shared__ __align__(16) float own[4][W][kPartialStride];
     __shared__ __align__(16) float slices[W][kPartialStride];
     __shared__ uint2 qf[8][32];
     const int L = a.seq_lens[b], PL = pm.lens[b];
-    if (L < 0 || L > a.max_blocks * B || PL < 0 || PL > pm.max_len) {
+    if (!lengths_ok<B>(a, pm, L, PL)) {
         wait_prior_grids();
         refuse_row(a, pm, b, h);
         return;
     }
     own_slice<B, W>(a, b, h, L, wp, lane, qf, own);
     wait_prior_grids();   // the prefix kernel, beside which this one may have started
-    if (g < a.G) {
-        float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-        const int n = PL > 0 ? pm.splits : 0;
-        const int64_t R = (int64_t)a.batch * a.G;
-        lse_list<16>(nullptr, 0, 0, pm.partials + partial_row(0, a.n_kv, h, R, (int64_t)b * a.G + g),
-                 partial_row(1, a.n_kv, 0, R, 0), n * part / parts, n * (part + 1) / parts, lane, m, l, acc);
-        if (lane == 0) {
-            slices[wp][0] = m;
-            slices[wp][1] = l;
-        }
-        *reinterpret_cast<float4*>(&slices[wp][4 + 4 * lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    }
+    if (g < a.G) prefix_slice(a, pm, b, h, g, part, parts, PL, lane, slices[wp]);
     __syncthreads();
     if (g >= a.G || part != 0) return;
     float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -439,7 +278,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 4) prefix_join_kernel(Att
     float mo = -INFINITY, lo = 0.f, ao[4] = {0.f, 0.f, 0.f, 0.f};
     combine_slices(&own[g][0][0], W, lane, mo, lo, ao);
     add_slice(m, l, acc, mo, lo, ao);
-    store_out(pm, gw, lane, l, acc);
+    finish_row<false>(a, pm, gw, nullptr, parts, lane, m, l, acc);
 }
 
 // ---------------------------------------------------------------- host side
@@ -535,15 +374,19 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
     for (int i = 0; i < 4; ++i) p.sb[i] = c.sign_bits[i];
     cudaError_t e;
     AttnArgs a = {};
-    // (an own table of more columns may hold sequences that are long for one CTA:
-    // 4 sequences of up to 1024 / 2048 own tokens, 8 kv heads: 26 / 49 us against
-    // 28 / 30 by the split kernel and a merge; 128: 108 / 183 against 111 / 182)
-    const bool join = !PACKED && (int64_t)max_blocks * c.block_size <= kJoinTokens;
+    // An own table of more columns may hold sequences that are long for one CTA:
+    // 4 sequences of up to 1024 / 2048 own tokens in bf16 pages, 8 kv heads, take
+    // 26 / 49 us against 28 / 30 by the split kernel and a merge, 128 sequences
+    // 108 / 183 against 111 / 182. Packed blocks need an SM's shared memory for a
+    // unit: with a CTA per SM 16 sequences take 21.1 .. 28.8 us against 22.7 ..
+    // 37.2 (up to 64 .. 1024 tokens).
+    const bool join = (int64_t)max_blocks * c.block_size <= kJoinTokens &&
+                      (!PACKED || (int64_t)batch * c.n_kv_heads <= current_device_sms());
     if constexpr (PACKED) {
+        a = decode_split_args(c, q, q_dtype, pool, n_pool_blocks, p.block_bytes, staging, block_table, max_blocks, seq_lens,
+                              batch, nullptr, workspace, nw);
         e = launch_prefix_packed(c, p, st);
-        if (e == cudaSuccess)
-            e = launch_decode_split(c, q, q_dtype, pool, n_pool_blocks, p.block_bytes, staging, block_table, max_blocks,
-                                    seq_lens, batch, nullptr, workspace, nw, true, &a, st);
+        if (e == cudaSuccess && !join) e = launch_decode_split(c, a, true, st);
     } else {
         e = launch_prefix_bf16(p, c.block_size, st);
         if (e == cudaSuccess && !join)
@@ -554,10 +397,13 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
     const PrefixMerge pm{p.partials, prefix_lens, prefix_blocks * c.block_size, plan.splits * plan.streams, out, out_dtype == KVARN_BF16};
     const dim3 units(batch, c.n_kv_heads);
     const int threads = 32 * kMergeWarps;
-    if constexpr (PACKED)
-        e = c.block_size == 32 ? launch_pdl(prefix_merge_kernel<32, true>, units, threads, 0, st, a, pm)
-                               : launch_pdl(prefix_merge_kernel<64, true>, units, threads, 0, st, a, pm);
-    else if (!join)
+    if constexpr (PACKED) {
+        if (join)
+            e = launch_prefix_join_packed(c, a, pm, st);
+        else
+            e = c.block_size == 32 ? launch_pdl(prefix_merge_kernel<32, true>, units, threads, 0, st, a, pm)
+                                   : launch_pdl(prefix_merge_kernel<64, true>, units, threads, 0, st, a, pm);
+    } else if (!join)
         e = launch_pdl(prefix_merge_kernel<kChunk, false>, units, threads, 0, st, a, pm);
     else {
         a.q = q;
