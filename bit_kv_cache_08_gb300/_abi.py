@@ -327,9 +327,13 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: str = "no
     return f * (keep + (1 - keep) / factor), 1.0 if scaling == "bands" else 0.1 * float(np.log(factor)) + 1.0
 
 
+def _current_device() -> int:
+    return torch.cuda.current_device() if _raw_device is None else _raw_device()
+
+
 def _need_device(*tensors):
     """The library launches on the current device: every buffer must be on it."""
-    dev = torch.cuda.current_device() if _raw_device is None else _raw_device()
+    dev = _current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
@@ -341,64 +345,118 @@ def _need_vec(t, name: str, dtype, n: int):
         raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
 
 
-_bf16, _i32t = torch.bfloat16, torch.int32
+_bf16, _i32t, _u8, _f32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
 
 
-def _token_rows(t: torch.Tensor, name: str, shape: tuple) -> int:
-    """Checks a [n_tokens][heads][128] bf16 tensor whose token rows may lie apart; returns the token stride."""
+def _need_rows(t: torch.Tensor, name: str, shape: tuple):
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not _bf16:
         raise ValueError(f"{name} must be a bf16 CUDA tensor")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    n, heads, _ = shape
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != 128 and heads > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s0 if n > 1 else heads * 128
+    raise ValueError(f"{name}: the heads of a token must be contiguous")
 
 
-def _append_rope(cfg, rope, pool, staging, block_table, pos, q, k, v, q_out, workspace, cu_tokens, rope_pos, q_weight,
-                 k_weight):
-    # (a decode step's call is as long as its checks: each attribute is read once)
+def _refuse_append(cfg, pool, staging, block_table, pos, q, k, v, q_out, workspace, cu_tokens, rope_pos, q_weight,
+                   k_weight):
+    """Why _append_rope's arguments do not pass: always raises."""
     _need_cuda(block_table, "block_table", _i32t)
     _need_cuda(pos, "pos", _i32t)
-    _need_cuda(workspace, "workspace", torch.uint8)
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("k must be [n_tokens][n_kv][128]")
-    batch, n, n_kv = pos.numel(), k.shape[0], cfg.n_kv_heads
-    rows, max_blocks = block_table.shape if block_table.dim() == 2 else (-1, 0)
-    if rows < batch:
+    _need_cuda(workspace, "workspace", _u8)
+    for t, name in ((k, "k"), (v, "v")) + (((q, "q"),) if q is not None else ()):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{name} must be [n_tokens][heads][128]")
+    batch, n = pos.numel(), k.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] < batch:
         raise ValueError("block_table must be [batch][max_blocks]")
-    cu_ptr = rope_ptr = qw_ptr = kw_ptr = q_ptr = out_ptr = None
     if cu_tokens is not None:
         _need_vec(cu_tokens, "cu_tokens", _i32t, batch + 1)
-        cu_ptr = cu_tokens.data_ptr()
     elif n != batch:
         raise ValueError("without cu_tokens there is one token per sequence")
     if rope_pos is not None:
         _need_vec(rope_pos, "rope_pos", _i32t, batch)
-        rope_ptr = rope_pos.data_ptr()
-    if q_weight is not None:
-        _need_vec(q_weight, "q_weight", _bf16, 128)
-        qw_ptr = q_weight.data_ptr()
-    if k_weight is not None:
-        _need_vec(k_weight, "k_weight", _bf16, 128)
-        kw_ptr = k_weight.data_ptr()
-    shape = (n, n_kv, 128)
-    ks, vs, qs, out_code = _token_rows(k, "k", shape), _token_rows(v, "v", shape), 0, BF16
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need_vec(w, name, _bf16, 128)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    if q is not None:
-        shape = (n, cfg.n_q_heads, 128)
-        qs = _token_rows(q, "q", shape)
+    if q_out is not None:
         _need_cuda(q_out, "q_out")
-        out_code = _dtype_code(q_out)
-        if q_out.shape != shape:
+        _dtype_code(q_out)
+        if q_out.shape != q.shape:
             raise ValueError("q_out must have the shape of q")
-        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     if workspace.numel() < 256:
         raise ValueError("workspace must hold 256 bytes")
     _need_device(pool, staging, block_table, pos, cu_tokens, rope_pos, q, k, v, q_weight, k_weight, q_out, workspace)
+    if q is not None and (q.dtype is not _bf16 or q.shape != (n, cfg.n_q_heads, 128) or not _heads_together(q)):
+        _need_rows(q, "q", (n, cfg.n_q_heads, 128))
+    if k.dtype is not _bf16 or k.shape != (n, cfg.n_kv_heads, 128) or not _heads_together(k):
+        _need_rows(k, "k", (n, cfg.n_kv_heads, 128))
+    _need_rows(v, "v", (n, cfg.n_kv_heads, 128))
+
+
+def _heads_together(t) -> bool:
+    _, s1, s2 = t.stride()
+    return s2 == 1 and (s1 == 128 or t.shape[1] == 1)
+
+
+def _append_rope(cfg, rope, pool, staging, block_table, pos, q, k, v, q_out, workspace, cu_tokens, rope_pos, q_weight,
+                 k_weight):
+    # A decode step's call takes as long as its checks, so each attribute is read
+    # once (a CPU tensor's get_device() is -1) and the words for what does not
+    # pass are found apart.
+    dev, i32, bf16 = _current_device(), _i32t, _bf16
+    args = (cfg, pool, staging, block_table, pos, q, k, v, q_out, workspace, cu_tokens, rope_pos, q_weight, k_weight)
+    cu_ptr = rope_ptr = qw_ptr = kw_ptr = q_ptr = out_ptr = None
+    qs, out_code = 0, BF16
+    try:
+        batch, (n, kh, kd), n_kv = pos.numel(), k.shape, cfg.n_kv_heads
+        rows, max_blocks = block_table.shape
+        ks, k1, k2 = k.stride()
+        vs, v1, v2 = v.stride()
+        good = (dev == pool.get_device() == block_table.get_device() == pos.get_device() == k.get_device()
+                == v.get_device() == workspace.get_device()
+                and block_table.dtype is i32 and pos.dtype is i32 and k.dtype is bf16 and v.dtype is bf16
+                and workspace.dtype is _u8 and kh == n_kv and kd == 128 and v.shape == k.shape and rows >= batch
+                and k2 == 1 and v2 == 1 and (k1 == v1 == 128 or n_kv == 1) and workspace.numel() >= 256
+                and block_table.is_contiguous() and pos.is_contiguous() and workspace.is_contiguous()
+                and (staging is None or staging.get_device() == dev))
+        if cu_tokens is not None:
+            good = (good and cu_tokens.dtype is i32 and cu_tokens.get_device() == dev and cu_tokens.numel() == batch + 1
+                    and cu_tokens.is_contiguous())
+            cu_ptr = cu_tokens.data_ptr()
+        else:
+            good = good and n == batch
+        if rope_pos is not None:
+            good = (good and rope_pos.dtype is i32 and rope_pos.get_device() == dev and rope_pos.numel() == batch
+                    and rope_pos.is_contiguous())
+            rope_ptr = rope_pos.data_ptr()
+        if q_weight is not None:
+            good = (good and q_weight.dtype is bf16 and q_weight.get_device() == dev and q_weight.numel() == 128
+                    and q_weight.is_contiguous())
+            qw_ptr = q_weight.data_ptr()
+        if k_weight is not None:
+            good = (good and k_weight.dtype is bf16 and k_weight.get_device() == dev and k_weight.numel() == 128
+                    and k_weight.is_contiguous())
+            kw_ptr = k_weight.data_ptr()
+        if q is not None and q_out is not None:
+            shape, n_q, out_type = q.shape, cfg.n_q_heads, q_out.dtype
+            qs, q1, q2 = q.stride()
+            good = (good and q.get_device() == dev == q_out.get_device() and q.dtype is bf16
+                    and (out_type is bf16 or out_type is _f32) and shape == (n, n_q, 128) and q_out.shape == shape
+                    and q2 == 1 and (q1 == 128 or n_q == 1) and q_out.is_contiguous())
+            if out_type is _f32:
+                out_code = FP32
+            if n == 1:
+                qs = n_q * 128
+            q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+        else:
+            good = good and q is None and q_out is None
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_append(*args)
+    if n == 1:   # (a single row's stride is not looked at)
+        ks = vs = n_kv * 128
     tail = (block_table.data_ptr(), max_blocks, pos.data_ptr(), rope_ptr, cu_ptr, n, batch, q_ptr, k.data_ptr(),
             v.data_ptr(), qs, ks, vs, qw_ptr, kw_ptr, out_ptr, out_code, workspace.data_ptr(), _stream())
     if staging is None:
@@ -497,25 +555,47 @@ def decode_attn_bf16(cfg: Config, q: torch.Tensor, kv_pool: torch.Tensor, block_
                                         workspace.numel(), _stream()), "kvarn_decode_attn_bf16")
 
 
-def _prefix_args(cfg, q, pool, staging, prefix_table, prefix_lens, block_table, seq_lens, out, workspace):
+def _refuse_prefix(cfg, q, pool, staging, prefix_table, prefix_lens, block_table, seq_lens, out, workspace):
+    """Why _prefix_args does not pass its arguments: always raises."""
     _need_cuda(q, "q")
     _need_cuda(out, "out")
+    _dtype_code(q), _dtype_code(out)
     _need_cuda(prefix_table, "prefix_table", _i32t)
     _need_cuda(prefix_lens, "prefix_lens", _i32t)
     _need_cuda(block_table, "block_table", _i32t)
     _need_cuda(seq_lens, "seq_lens", _i32t)
-    _need_cuda(workspace, "workspace", torch.uint8)
-    shape = q.shape
-    if len(shape) != 3 or shape[1] != cfg.n_q_heads or shape[2] != 128 or out.shape != shape:
-        raise ValueError("q and out must be [batch][n_q][128]")
-    batch = shape[0]
-    rows, max_blocks = block_table.shape if block_table.dim() == 2 else (-1, 0)
-    if prefix_lens.numel() != batch or seq_lens.numel() != batch or rows != batch:
-        raise ValueError("prefix_lens, seq_lens and block_table must have a row for each sequence of q")
+    _need_cuda(workspace, "workspace", _u8)
     _need_device(pool, staging, q, out, prefix_table, prefix_lens, block_table, seq_lens, workspace)
-    return (prefix_table.data_ptr(), prefix_table.numel(), prefix_lens.data_ptr(), block_table.data_ptr(), max_blocks,
-            seq_lens.data_ptr(), batch, out.data_ptr(), _dtype_code(out), workspace.data_ptr(), workspace.numel(),
-            _stream())
+    if q.dim() != 3 or q.shape[1:] != (cfg.n_q_heads, 128) or out.shape != q.shape:
+        raise ValueError("q and out must be [batch][n_q][128]")
+    raise ValueError("prefix_lens, seq_lens and block_table must have a row for each sequence of q")
+
+
+def _prefix_args(cfg, q, pool, staging, prefix_table, prefix_lens, block_table, seq_lens, out, workspace):
+    # (as in _append_rope: each attribute read once)
+    dev, i32 = _current_device(), _i32t
+    try:
+        shape, q_type, out_type = q.shape, q.dtype, out.dtype
+        batch, n_q, d = shape
+        rows, max_blocks = block_table.shape
+        n_prefix, n_workspace = prefix_table.numel(), workspace.numel()
+        good = (dev == pool.get_device() == q.get_device() == out.get_device() == prefix_table.get_device()
+                == prefix_lens.get_device() == block_table.get_device() == seq_lens.get_device()
+                == workspace.get_device() and (staging is None or staging.get_device() == dev)
+                and prefix_table.dtype is i32 and prefix_lens.dtype is i32 and block_table.dtype is i32
+                and seq_lens.dtype is i32 and workspace.dtype is _u8 and (q_type is _bf16 or q_type is _f32)
+                and (out_type is _bf16 or out_type is _f32) and n_q == cfg.n_q_heads and d == 128 and out.shape == shape
+                and prefix_lens.numel() == batch == seq_lens.numel() and rows == batch and q.is_contiguous()
+                and out.is_contiguous() and prefix_table.is_contiguous() and prefix_lens.is_contiguous()
+                and block_table.is_contiguous() and seq_lens.is_contiguous() and workspace.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_prefix(cfg, q, pool, staging, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
+    return (FP32 if q_type is _f32 else BF16,
+            (prefix_table.data_ptr(), n_prefix, prefix_lens.data_ptr(), block_table.data_ptr(), max_blocks,
+             seq_lens.data_ptr(), batch, out.data_ptr(), FP32 if out_type is _f32 else BF16, workspace.data_ptr(),
+             n_workspace, _stream()))
 
 
 def prefix_attn(cfg: Config, q: torch.Tensor, pool: torch.Tensor, staging: torch.Tensor, prefix_table: torch.Tensor,
@@ -526,13 +606,15 @@ def prefix_attn(cfg: Config, q: torch.Tensor, pool: torch.Tensor, staging: torch
     own seq_lens[b] tokens. q (bf16|fp32) and out (bf16|fp32): [batch][n_q][128]."""
     _need_cuda(pool, "pool", torch.uint8)
     _need_cuda(staging, "staging", torch.bfloat16)
-    rest = _prefix_args(cfg, q, pool, staging, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
+    code, rest = _prefix_args(cfg, q, pool, staging, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
     if pool.dim() != 2 or pool.shape[1] != block_bytes(cfg):
         raise ValueError("pool must be [n_blocks][block_bytes]")
     if staging.numel() < q.shape[0] * cfg.n_kv_heads * 2 * cfg.block_size * 128:
         raise ValueError("staging holds fewer sequences than q")
-    _check(lib().kvarn_prefix_attn(ctypes.byref(cfg), q.data_ptr(), _dtype_code(q), pool.data_ptr(), pool.shape[0],
-                                   staging.data_ptr(), *rest), "kvarn_prefix_attn")
+    r = lib().kvarn_prefix_attn(ctypes.byref(cfg), q.data_ptr(), code, pool.data_ptr(), pool.shape[0],
+                                staging.data_ptr(), *rest)
+    if r:
+        _check(r, "kvarn_prefix_attn")
 
 
 def prefix_attn_bf16(cfg: Config, q: torch.Tensor, kv_pool: torch.Tensor, prefix_table: torch.Tensor,
@@ -540,11 +622,12 @@ def prefix_attn_bf16(cfg: Config, q: torch.Tensor, kv_pool: torch.Tensor, prefix
                      workspace: torch.Tensor):
     """prefix_attn over the bf16 pages [n_blocks][n_kv][2][B][128] of decode_attn_bf16."""
     _need_cuda(kv_pool, "kv_pool", torch.bfloat16)
-    rest = _prefix_args(cfg, q, kv_pool, None, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
+    code, rest = _prefix_args(cfg, q, kv_pool, None, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
     if kv_pool.shape[1:] != (cfg.n_kv_heads, 2, cfg.block_size, 128):
         raise ValueError("kv_pool must be [n_blocks][n_kv][2][B][128]")
-    _check(lib().kvarn_prefix_attn_bf16(ctypes.byref(cfg), q.data_ptr(), _dtype_code(q), kv_pool.data_ptr(),
-                                        kv_pool.shape[0], *rest), "kvarn_prefix_attn_bf16")
+    r = lib().kvarn_prefix_attn_bf16(ctypes.byref(cfg), q.data_ptr(), code, kv_pool.data_ptr(), kv_pool.shape[0], *rest)
+    if r:
+        _check(r, "kvarn_prefix_attn_bf16")
 
 
 def decode_attn_noalloc(cfg: Config, q: torch.Tensor, pool: torch.Tensor, staging: torch.Tensor,

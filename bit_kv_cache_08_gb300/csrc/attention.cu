@@ -882,8 +882,17 @@ cudaError_t launch_prefix_join_packed(const kvarn_config& cfg, const AttnArgs& a
         using K = decltype(k);
         const auto fn = prefix_join_packed_kernel<K::kB, K::kBits>;
         const int bytes = kMergeWarps * (int)K::smem();
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        return e != cudaSuccess ? e : launch_pdl(fn, dim3(a.batch, a.n_kv), 32 * kMergeWarps, bytes, st, a, pm);
+        static bool ready[64];
+        int d = 0;
+        cudaError_t e = cudaGetDevice(&d);
+        if (e != cudaSuccess) return e;
+        if (d < 0 || d >= 64) return cudaErrorInvalidDevice;
+        if (!ready[d]) {
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            if (e != cudaSuccess) return e;
+            ready[d] = true;
+        }
+        return launch_pdl(fn, dim3(a.batch, a.n_kv), 32 * kMergeWarps, bytes, st, a, pm);
     });
 }
 

@@ -396,6 +396,50 @@ def test_bad_own_blocks_are_flagged(kvlib, bits):
         assert torch.equal(s.run(q, [100, 3, 0], ws=ws), good)
 
 
+@pytest.mark.parametrize("bits,columns", [(0, 4), (0, 40), (2, 4), (2, 40)])
+def test_inputs_that_the_kernel_before_wrote(kvlib, bits, columns):
+    """Lengths, table entries, queries and own rows written on the stream just before each call, with nothing waited for:
+    the same bits as with the GPU idle between the steps."""
+    s = Shared(kvlib, 71, 640, [120] * 6, 8, 2, 32, bits)
+    gen, steps = synth.make_gen(12), 60
+    qs = torch.stack([synth.queries(gen, 6, 8) for _ in range(steps)]).to(torch.bfloat16).cuda()
+    narrow, pool, staging = s.table, s.pool.clone(), s.staging.clone()
+    rows = torch.randn(steps, *s.staging.shape[:3], D, generator=torch.Generator("cuda").manual_seed(3), device="cuda").to(torch.bfloat16)
+    ws = kvlib.alloc_prefix_workspace(s.cfg, 6, len(s.prefix_np))
+    results = []
+    for wait in (True, False):
+        s.pool.copy_(pool)
+        s.staging.copy_(staging)
+        table = torch.full((6, columns), -1, dtype=torch.int32, device="cuda")
+        q, pl, sl = torch.zeros_like(qs[0]), s.i32([0] * 6), s.i32([0] * 6)
+        outs = torch.zeros(steps, 6, 8, D, device="cuda")
+        for i in range(steps):
+            L = 2 * i + 1
+            q.copy_(qs[i])
+            table[:, (L - 1) // 32] = narrow[:, (L - 1) // 32]
+            sl.add_(L - (2 * i - 1 if i else 0))
+            pl.add_(10)
+            if bits:
+                s.staging[:, :, :, (L - 1) % 32] = rows[i]
+                if L % 32:
+                    s.staging[:, :, :, :L % 32].nan_to_num_(0.25)
+            else:
+                page = s.pool[narrow[:, (L - 1) // 32].long()]
+                page[:, :, :, (L - 1) % 32] = rows[i]
+                s.pool[narrow[:, (L - 1) // 32].long()] = page
+            if wait:
+                torch.cuda.synchronize()
+            if bits:
+                kvlib.prefix_attn(s.cfg, q, s.pool, s.staging, s.prefix_table, pl, table, sl, outs[i], ws)
+            else:
+                kvlib.prefix_attn_bf16(s.cfg, q, s.pool, s.prefix_table, pl, table, sl, outs[i], ws)
+        torch.cuda.synchronize()
+        assert kvlib.read_error(ws) == 0
+        results.append(outs)
+    assert torch.isfinite(results[0]).all()
+    assert torch.equal(results[0], results[1])
+
+
 def test_no_own_blocks_and_small_tables(kvlib):
     for bits in (0, 2):
         s = Shared(kvlib, 19, 64, [0, 0], 4, 2, 32, bits)           # a block table without columns
