@@ -718,7 +718,7 @@ constexpr int stages_for() { return 2; }
 
 // ---------------------------------------------------------------- own tokens and merge behind a shared prefix
 // One CTA of 8 warps per (sequence, kv head): a share of the unit's complete
-// own blocks each, the raw tail rows (copied over the blocks' stages), and,
+// own blocks each, the raw tail rows, and,
 // when the prefix kernel is through, the merge with the prefix's partials and
 // the rotation back. Where a CTA per SM holds all units, this saves a launch
 // and the own results' way through memory, and on SMs that the prefix kernel
@@ -726,15 +726,17 @@ constexpr int stages_for() { return 2; }
 // behind 4096 of a prefix, 8 kv heads, 2-bit, as a graph: 18.5 / 26.2 us
 // against 22.2 / 29.5 with the split kernel and a merge; bound by the latency
 // of the prefix kernel and then of the partials' loads.
+constexpr int kJoinWarps = 8;
 template <int B, int BITS>
-__global__ void __launch_bounds__(32 * kMergeWarps, 1) prefix_join_packed_kernel(AttnArgs a, PrefixMerge pm) {
+__global__ void __launch_bounds__(32 * kJoinWarps, 1) prefix_join_packed_kernel(AttnArgs a, PrefixMerge pm) {
     constexpr int S = stages_for<B, BITS>(), kWarp = attn_warp_bytes<B, BITS, S>(), kResult = S * 2 * head_block_bytes(B, BITS) + 64;
     static_assert(4 * kPartialStride * 4 <= attn_q_bytes(B), "the slices fit where q was");
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ __align__(16) float slices[kMergeWarps][kPartialStride], tails[kMergeWarps][kPartialStride];
+    __shared__ __align__(16) float slices[kJoinWarps][kPartialStride], tails[4][4][kPartialStride];
+    __shared__ uint2 qf[8][32];
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int b = blockIdx.x, h = blockIdx.y;
-    const int parts = merge_parts(a.G, kMergeWarps), g = wp / parts, part = wp % parts;
+    const int parts = merge_parts(a.G, kJoinWarps), g = wp / parts, part = wp % parts;
     const bool mine = g < a.G;
     const int L = a.seq_lens[b], PL = pm.lens[b];
     if (!lengths_ok<B>(a, pm, L, PL)) {
@@ -743,21 +745,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 1) prefix_join_packed_kernel
         return;
     }
     float* result = reinterpret_cast<float*>(smem + wp * kWarp + kResult);
-    if (!decode_attn_2bit_body<B, BITS, S, true>(a, smem + wp * kWarp, UnitShare{b, h, wp, kMergeWarps}))
+    if (!decode_attn_2bit_body<B, BITS, S, true>(a, smem + wp * kWarp, UnitShare{b, h, wp, kJoinWarps}))
         for (int j = 0; j < a.G; ++j) {
             const float none[4] = {0.f, 0.f, 0.f, 0.f};
             put_slice(result + j * kPartialStride, lane, -INFINITY, 0.f, none);
         }
     const int ntail = L % B;
-    if (ntail > 0) {
-        __syncthreads();   // the stages have been read
-        const TailRows<B / kMergeWarps, kWarp> rows{smem};
-        static_assert(rows.kBytes <= S * 2 * head_block_bytes(B, BITS), "tail rows fit the stages");
-        copy_tail<B>(a, rows, b, h, ntail);
-        async_copy_wait();
-        __syncthreads();
-        if (mine) tail_share(a, rows, ntail, part, parts, (int64_t)b * a.n_q + h * a.G + g, lane, tails[wp]);
-    }
+    if (ntail > 0) tail_slice16<B, kJoinWarps>(a, b, h, ntail, wp, lane, qf, tails);
     wait_prior_grids();   // the prefix kernel, beside which this one may have started
     if (mine) prefix_slice(a, pm, b, h, g, part, parts, PL, lane, slices[wp]);
     __syncthreads();
@@ -765,9 +759,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 1) prefix_join_packed_kernel
     float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     combine_slices(&slices[wp][0], parts, lane, m, l, acc);
     float mo = -INFINITY, lo = 0.f, ao[4] = {0.f, 0.f, 0.f, 0.f};
-    combine_slices(reinterpret_cast<const float*>(smem + kResult) + g * kPartialStride, kMergeWarps, lane, mo, lo, ao, kWarp / 4);
+    combine_slices(reinterpret_cast<const float*>(smem + kResult) + g * kPartialStride, kJoinWarps, lane, mo, lo, ao, kWarp / 4);
     add_slice(m, l, acc, mo, lo, ao);
-    finish_row<true>(a, pm, (int64_t)b * a.n_q + h * a.G + g, ntail > 0 ? &tails[wp][0] : nullptr, parts, lane, m, l, acc);
+    finish_row<true>(a, pm, (int64_t)b * a.n_q + h * a.G + g, ntail > 0 ? &tails[g][0][0] : nullptr, lane, m, l, acc);
 }
 
 // ---------------------------------------------------------------- host side
@@ -881,7 +875,7 @@ cudaError_t launch_prefix_join_packed(const kvarn_config& cfg, const AttnArgs& a
     return with_attn_kernel(cfg.block_size, cfg.bits, [&](auto k) {
         using K = decltype(k);
         const auto fn = prefix_join_packed_kernel<K::kB, K::kBits>;
-        const int bytes = kMergeWarps * (int)K::smem();
+        const int bytes = kJoinWarps * (int)K::smem();
         static bool ready[64];
         int d = 0;
         cudaError_t e = cudaGetDevice(&d);
@@ -892,7 +886,7 @@ cudaError_t launch_prefix_join_packed(const kvarn_config& cfg, const AttnArgs& a
             if (e != cudaSuccess) return e;
             ready[d] = true;
         }
-        return launch_pdl(fn, dim3(a.batch, a.n_kv), 32 * kMergeWarps, bytes, st, a, pm);
+        return launch_pdl(fn, dim3(a.batch, a.n_kv), 32 * kJoinWarps, bytes, st, a, pm);
     });
 }
 

@@ -31,228 +31,89 @@ cudaError_t launch_prefix_bf16(const PrefixArgs& p, int block_size, cudaStream_t
 cudaError_t launch_prefix_packed(const kvarn_config& c, const PrefixArgs& p, cudaStream_t st);
 
 // ---------------------------------------------------------------- merge
-// One CTA of 8 warps per (sequence, kv head): 8 / G warps to each of its G
-// query heads (their raw tail rows are copied to shared memory once), each
-// with a share of the row's partials and of the tail rows; the row's first warp
-// combines the shares and finishes the row.
+// One CTA of 4 warps per (sequence, kv head): the raw tail rows (ROT), which
+// wait for nothing, then, when the split kernel is through, 4 / G warps to
+// each of the G query heads with a share of the row's partials; the row's first
+// warp combines the shares and finishes the row. On the tensor cores a tail row
+// costs a quarter of the instructions that it costs scored by a lane: calls
+// of 64 x 8192 at 2 bits and 128 x 32 768 at 4 went from 52 to 46 and from 185
+// to 180 us.
+constexpr int kMergeWarps = 4;
 template <int B, bool ROT>
 __global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnArgs a, PrefixMerge pm) {
-    wait_prior_grids();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int b = blockIdx.x, h = blockIdx.y;
     const int parts = merge_parts(a.G, kMergeWarps), g = wp / parts, part = wp % parts;
-    const bool mine = g < a.G;
-    const int64_t gw = (int64_t)b * a.n_q + h * a.G + (mine ? g : 0);
     __shared__ __align__(16) float slices[kMergeWarps][kPartialStride];
-    __shared__ __align__(16) float tails[kMergeWarps][kPartialStride];
+    __shared__ __align__(16) float tails[ROT ? 4 : 1][4][kPartialStride];
+    __shared__ uint2 qf[8][32];
     const int L = a.seq_lens[b], PL = pm.lens[b];
-    // the own partials: those of the warps that the split kernel's unit map
-    // names (a range outside the grid, left by a warp that gave up, is none)
-    const int64_t u = (int64_t)b * a.n_kv + h;
-    const int2 wm = __ldcg(reinterpret_cast<const int2*>(a.unit_map) + u);
-    const int np = (ROT ? L >= B : L > 0) && wm.x >= 0 && wm.y >= wm.x && wm.y < a.nw ? wm.y - wm.x + 1 : 0;
-    const float* p0 = a.partials + ((u + max(wm.x, 0)) * a.G + (mine ? g : 0)) * kPartialStride;
     if (!lengths_ok<B>(a, pm, L, PL)) {
+        wait_prior_grids();
         refuse_row(a, pm, b, h);
         return;
     }
-    // the raw tail rows on their way to shared memory while the partials merge
     const int ntail = ROT ? L % B : 0;
-    using Tail = TailRows<ROT ? B : 1, 0>;
-    __shared__ __align__(16) uint8_t tail_rows[ROT ? Tail::kBytes : 16];
-    const Tail rows{tail_rows};
-    if (ntail > 0) copy_tail<B>(a, rows, b, h, ntail);
-    if (mine) {
+    if (ROT && ntail > 0) tail_slice16<B, kMergeWarps>(a, b, h, ntail, wp, lane, qf, tails);
+    wait_prior_grids();
+    if (g < a.G) {
+        // the own partials: those of the warps that the split kernel's unit map
+        // names (a range outside the grid, left by a warp that gave up, is none)
+        const int64_t u = (int64_t)b * a.n_kv + h;
+        const int2 wm = __ldcg(reinterpret_cast<const int2*>(a.unit_map) + u);
+        const int np = (ROT ? L >= B : L > 0) && wm.x >= 0 && wm.y >= wm.x && wm.y < a.nw ? wm.y - wm.x + 1 : 0;
+        const float* p0 = a.partials + ((u + max(wm.x, 0)) * a.G + g) * kPartialStride;
         float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
         const int n = np + (PL > 0 ? pm.splits : 0);
         const int64_t R = (int64_t)a.batch * a.G;
-        lse_list<8>(p0, np, (int64_t)a.G * kPartialStride, pm.partials + partial_row(0, a.n_kv, h, R, (int64_t)b * a.G + g),
-                    partial_row(1, a.n_kv, 0, R, 0), n * part / parts, n * (part + 1) / parts, lane, m, l, acc);
+        lse_list<16>(p0, np, (int64_t)a.G * kPartialStride, pm.partials + partial_row(0, a.n_kv, h, R, (int64_t)b * a.G + g),
+                     partial_row(1, a.n_kv, 0, R, 0), n * part / parts, n * (part + 1) / parts, lane, m, l, acc);
         put_slice(slices[wp], lane, m, l, acc);
     }
-    if (ntail > 0) {
-        async_copy_wait();
-        __syncthreads();
-        if (mine) tail_share(a, rows, ntail, part, parts, gw, lane, tails[wp]);
-    }
     __syncthreads();
-    if (!mine || part != 0) return;
+    if (g >= a.G || part != 0) return;
     float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     combine_slices(&slices[wp][0], parts, lane, m, l, acc);
-    finish_row<ROT>(a, pm, gw, ntail > 0 ? &tails[wp][0] : nullptr, parts, lane, m, l, acc);
+    finish_row<ROT>(a, pm, (int64_t)b * a.n_q + h * a.G + g, ntail > 0 ? &tails[g][0][0] : nullptr, lane, m, l, acc);
 }
 
 // ---------------------------------------------------------------- own tokens and merge in one (bf16 pages)
 constexpr int kJoinTokens = 1024;   // of an own table's columns, at most
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t bf16_pair(float v0, float v1, bool low) {   // RN(v), or RN(v - RN(v))
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
-    if (!low) return *reinterpret_cast<const uint32_t*>(&h);
-    const float2 f = __bfloat1622float2(h);
-    const __nv_bfloat162 r = __floats2bfloat162_rn(v0 - f.x, v1 - f.y);
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// Warp wp's share of a unit's own tokens (16-token chunks wp, wp + W, ...) as
-// a slice (m, l, acc) for each of its G heads, both products on mma.sync with
-// the columns (head, high | low half of q or of p), as in attention_bf16.cu.
-// The fragments are loaded straight from the pages: the order of the channels
-// in S and of the output rows in O is free, so a lane's 16-byte loads of K
-// (token gq, channels 32 j + 8 tq ..) and V (channels 64 j + 8 gq .. of the
-// four tokens its A fragment holds) are whole fragments, and nothing passes
-// through shared memory but q.
+// The 16-token chunks wp, wp + W, ... of a unit's own pages, for bf16_slice.
 template <int B, int W>
-__device__ __forceinline__ void own_slice(const AttnArgs& a, int b, int h, int L, int wp, int lane, uint2 (*qf)[32],
-                                          float (*own)[W][kPartialStride]) {
-    constexpr int CPB = B / kChunk;
-    const int gq = lane >> 2, tq = lane & 3;
-    const int head = gq >> 1;          // this lane's column of the products: (head, high | low half)
-    const bool low = gq & 1;
-    const int chunks = (L + kChunk - 1) / kChunk, n = chunks > wp ? (chunks - wp + W - 1) / W : 0;
-    const int64_t head_block = 2 * B * kD * 2;
-    const uint8_t* lane_k = a.pool + h * head_block + gq * (kD * 2) + tq * 16;
-    const uint8_t* lane_v = a.pool + h * head_block + B * kD * 2 + 2 * tq * (kD * 2) + gq * 16;
-    const int32_t* table = a.block_table + (int64_t)b * a.max_blocks;
-    // lane i holds the block of this warp's chunk i (without a look at L, which is on its way too)
-    static_assert(kJoinTokens <= 32 * W * kChunk, "a lane for each chunk of a warp");
-    const int held = (wp + W * lane) / CPB < a.max_blocks ? table[(wp + W * lane) / CPB] : 0;
-    auto good = [&](int phys) { return phys >= 0 && phys < a.n_pool_blocks; };
-    uint4 k[2][4], v[4][2];
-    auto offset_of = [&](int i, int phys) {
-        return phys * a.block_bytes + (wp + W * i) % CPB * (kChunk * kD * 2);
-    };
-    auto load_k = [&](int64_t at, int rows) {
-        const uint8_t* p = lane_k + at;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                k[t][j] = 8 * t + gq < rows ? __ldcg(reinterpret_cast<const uint4*>(p + 8 * t * (kD * 2) + 64 * j))
-                                            : make_uint4(0u, 0u, 0u, 0u);
-    };
-    auto load_v = [&](int64_t at, int rows) {
-        const uint8_t* p = lane_v + at;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int row = (t & 1) + 8 * (t >> 1);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                v[t][j] = 2 * tq + row < rows ? __ldcg(reinterpret_cast<const uint4*>(p + row * (kD * 2) + 128 * j))
-                                              : make_uint4(0u, 0u, 0u, 0u);
-        }
-    };
-    int rows = 0;   // of the chunk; none in a bad block
-    auto start = [&](int i) {
+struct OwnChunks {
+    const AttnArgs& a;
+    int L, wp, held;
+    __device__ __forceinline__ OwnChunks(const AttnArgs& a, int b, int L, int wp, int lane) : a(a), L(L), wp(wp) {
+        // lane i holds the block of chunk i (without a look at L, which is on its way too); -1: a bad one
+        static_assert(kJoinTokens <= 32 * W * kChunk, "a lane for each chunk of a warp");
+        const int c = (wp + W * lane) / (B / kChunk);
+        held = c < a.max_blocks ? a.block_table[(int64_t)b * a.max_blocks + c] : 0;
+        if (held < 0 || held >= a.n_pool_blocks) held = -1;
+        if (held < 0 && lane < count()) raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
+    }
+    __device__ __forceinline__ int count() const {
+        const int chunks = (L + kChunk - 1) / kChunk;
+        return chunks > wp ? (chunks - wp + W - 1) / W : 0;
+    }
+    __device__ __forceinline__ ChunkRows operator()(int i) const {
         const int phys = __shfl_sync(kFull, held, i);
-        rows = good(phys) ? L - (wp + W * i) * kChunk : 0;
-        if (rows == 0 && lane == 0) raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
-        return offset_of(i, rows ? phys : 0);
-    };
-    int64_t at = 0;
-    if (n > 0) {
-        at = start(0);
-        load_k(at, rows);
-        load_v(at, rows);
+        return {max(phys, 0) * a.block_bytes + (wp + W * i) % (B / kChunk) * (kChunk * kD * 2),
+                phys >= 0 ? L - (wp + W * i) * kChunk : 0};
     }
-    for (int ks = wp; ks < 8; ks += W) {   // the query as the B operand of each k-step, a column for each (head, high | low half)
-        const int c = 32 * (ks >> 1) + 8 * tq + 4 * (ks & 1);
-        const int64_t at_q = ((int64_t)b * a.n_q + h * a.G + min(head, a.G - 1)) * kD + c;
-        float x[4];
-        if (a.q_dtype == KVARN_FP32) {
-            *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at_q);
-        } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + at_q);
-            x[0] = __uint_as_float(u.x << 16);
-            x[1] = __uint_as_float(u.x & 0xffff0000u);
-            x[2] = __uint_as_float(u.y << 16);
-            x[3] = __uint_as_float(u.y & 0xffff0000u);
-        }
-        qf[ks][lane] = make_uint2(bf16_pair(x[0], x[1], low), bf16_pair(x[2], x[3], low));
-    }
-    __syncthreads();
-    float o[8][4], m = -INFINITY, l = 0.f;   // o[4 i + e]: channels 64 i + 8 gq + 2 e (+ 1), head tq high | low
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    const float qs = a.sm_scale * kLog2e;
-    for (int i = 0; i < n; ++i) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};   // tokens gq and gq + 8, head tq high | low
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint2 q0 = qf[2 * j][lane], q1 = qf[2 * j + 1][lane];
-            mma_bf16(s, k[0][j].x, k[1][j].x, k[0][j].y, k[1][j].y, q0.x, q0.y);
-            mma_bf16(s, k[0][j].z, k[1][j].z, k[0][j].w, k[1][j].w, q1.x, q1.y);
-        }
-        const int here = rows;
-        const float s0 = gq < here ? (s[0] + s[1]) * qs : -INFINITY, s1 = gq + 8 < here ? (s[2] + s[3]) * qs : -INFINITY;
-        float bm = fmaxf(s0, s1);
-        bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 4));
-        bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 8));
-        bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 16));
-        const float mn = fmaxf(m, bm), off = mn == -INFINITY ? 0.f : mn;
-        const float f = mn == -INFINITY ? 1.f : exp2f(m - mn), p0 = exp2f(s0 - off), p1 = exp2f(s1 - off);
-        m = mn;
-        l = l * f + (p0 + p1);
-        if (__any_sync(kFull, f != 1.f)) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                o[e][0] *= f;
-                o[e][1] *= f;
-                o[e][2] *= f;
-                o[e][3] *= f;
-            }
-        }
-        // weights of tokens 2 tq, 2 tq + 1 and 2 tq + 8, 2 tq + 9 for this lane's column
-        const int from = 8 * tq + head;
-        const uint32_t b0 = bf16_pair(__shfl_sync(kFull, p0, from), __shfl_sync(kFull, p0, from + 4), low);
-        const uint32_t b1 = bf16_pair(__shfl_sync(kFull, p1, from), __shfl_sync(kFull, p1, from + 4), low);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t* r0 = &v[0][j].x;
-            const uint32_t* r1 = &v[1][j].x;
-            const uint32_t* r2 = &v[2][j].x;
-            const uint32_t* r3 = &v[3][j].x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                mma_bf16(o[4 * j + e], __byte_perm(r0[e], r1[e], 0x5410), __byte_perm(r0[e], r1[e], 0x7632),
-                         __byte_perm(r2[e], r3[e], 0x5410), __byte_perm(r2[e], r3[e], 0x7632), b0, b1);
-        }
-        if (i + 1 < n) {
-            at = start(i + 1);
-            load_k(at, rows);
-            load_v(at, rows);
-        }
-    }
-    l += __shfl_xor_sync(kFull, l, 4);
-    l += __shfl_xor_sync(kFull, l, 8);
-    l += __shfl_xor_sync(kFull, l, 16);
-    if (tq < a.G) {
-        float* sl = own[tq][wp];
-        if (gq == 0) {
-            sl[0] = m;
-            sl[1] = l;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; e += 2)
-            *reinterpret_cast<float4*>(sl + 4 + 64 * (e >> 2) + 8 * gq + 2 * (e & 3)) =
-                make_float4(o[e][0] + o[e][1], o[e][2] + o[e][3], o[e + 1][0] + o[e + 1][1], o[e + 1][2] + o[e + 1][3]);
-    }
-}
+};
 
 // One CTA of W warps per (sequence, kv head): its own tokens, then, when the
 // prefix kernel is through, the merge with the prefix's partials. Against the
 // split kernel and a merge this saves a launch and the own tokens' partials,
 // but a unit has only its CTA. Memory bounds it (512 bytes a token and kv
 // head) where the units fill the GPU, the chain of dependent loads where they
-// do not. 16 warps per SM in CTAs of 4 finish 64 x 192 own tokens of 8 kv
-// heads behind 8192 of a prefix in 18 us, the whole call in 35 us (as CTAs of
-// 8: 38; at 8 or 12 warps per SM, with the next chunk's loads in flight
-// during a chunk's products: 45, 37; split and merge: 42); 128 x 384 behind
-// 32 768 in 110 (115; 127, 105; 119).
+// do not. A call of 64 sequences with 192 own tokens of 8 kv heads behind 8192
+// of a prefix takes 33 us with CTAs of 4 at 16 warps per SM (CTAs of 8: 36; 8 or
+// 12 warps per SM with the next chunk's loads in flight during a chunk's
+// products: 45, 37; split kernel and merge: 42), 128 with 384 behind 32 768
+// takes 106 (112; 127, 105; 119).
 template <int B, int W>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 4) prefix_join_kernel(AttnArgs a, PrefixMerge pm) {
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
@@ -268,7 +129,8 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 4) prefix_join_kernel(Att
         refuse_row(a, pm, b, h);
         return;
     }
-    own_slice<B, W>(a, b, h, L, wp, lane, qf, own);
+    const OwnChunks<B, W> chunks(a, b, L, wp, lane);
+    bf16_slice<B, W, W>(a, b, h, chunks.count(), a.pool + (int64_t)h * 2 * B * kD * 2, chunks, wp, lane, qf, own);
     wait_prior_grids();   // the prefix kernel, beside which this one may have started
     if (g < a.G) prefix_slice(a, pm, b, h, g, part, parts, PL, lane, slices[wp]);
     __syncthreads();
@@ -278,7 +140,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 4) prefix_join_kernel(Att
     float mo = -INFINITY, lo = 0.f, ao[4] = {0.f, 0.f, 0.f, 0.f};
     combine_slices(&own[g][0][0], W, lane, mo, lo, ao);
     add_slice(m, l, acc, mo, lo, ao);
-    finish_row<false>(a, pm, gw, nullptr, parts, lane, m, l, acc);
+    finish_row<false>(a, pm, gw, nullptr, lane, m, l, acc);
 }
 
 // ---------------------------------------------------------------- host side

@@ -7,7 +7,6 @@
 
 namespace kvarn {
 
-constexpr int kMergeWarps = 8;
 // Warps to a query head (G = 3: the CTA's last ones are left over).
 __device__ __forceinline__ int merge_parts(int G, int warps) { return G == 1 ? warps : G == 2 ? warps / 2 : warps / 4; }
 
@@ -56,11 +55,6 @@ __device__ __forceinline__ void lse_list(const float* p0, int np, int64_t pstrid
         m = mn;
     }
 }
-
-__device__ __forceinline__ void async_copy16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void async_copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // (m, l, acc) += (ms, ls, as) in the log-sum-exp sense.
 __device__ __forceinline__ void add_slice(float& m, float& l, float (&acc)[4], float ms, float ls, const float (&as)[4]) {
@@ -121,84 +115,169 @@ __device__ __forceinline__ void prefix_slice(const AttnArgs& a, const PrefixMerg
     put_slice(slice, lane, m, l, acc);
 }
 
-// The raw tail rows in shared memory, PER of them in every REGION bytes: K,
-// then V 272 bytes on; rows 528 bytes apart, so that lanes that score a row
-// each read different banks.
-template <int PER, int REGION>
-struct TailRows {
-    static constexpr int kPitch = 2 * kD * 2 + 16, kBytes = PER * kPitch;
-    uint8_t* base;
-    __device__ __forceinline__ uint8_t* k(int i) const { return base + i / PER * REGION + i % PER * kPitch; }
-    __device__ __forceinline__ uint8_t* v(int i) const { return k(i) + kD * 2 + 16; }
-};
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bf16_pair(float v0, float v1, bool low) {   // RN(v), or RN(v - RN(v))
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
+    if (!low) return *reinterpret_cast<const uint32_t*>(&h);
+    const float2 f = __bfloat1622float2(h);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(v0 - f.x, v1 - f.y);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 
-// The whole CTA starts the copies of the first ntail staging rows.
-template <int B, typename Rows>
-__device__ __forceinline__ void copy_tail(const AttnArgs& a, const Rows& rows, int b, int h, int ntail) {
-    const uint16_t* st = a.staging + ((int64_t)b * a.n_kv + h) * 2 * B * kD;
-    for (int i = threadIdx.x; i < ntail * 16; i += 32 * kMergeWarps) {
-        async_copy16(rows.k(i >> 4) + (i & 15) * 16, st + i * 8);
-        async_copy16(rows.v(i >> 4) + (i & 15) * 16, st + B * kD + i * 8);
+struct ChunkRows {
+    int64_t at;   // bytes from the base to K's rows (128 channels, 256 bytes apart); V's are B rows behind
+    int rows;     // that there are (16 and more: all)
+};
+// n chunks of 16 bf16 tokens (chunk(i): the whole warp calls it) against the G
+// queries of (sequence b, kv head h), a slice for each in own[head][wp]. Both
+// products run on mma.sync with the columns (head, high | low half of q or of
+// p), as in attention_bf16.cu. The fragments are loaded straight from memory:
+// the order of the channels in S and of the output rows in O is free, so a
+// lane's 16-byte loads of K (token gq, channels 32 j + 8 tq ..) and V (channels
+// 64 j + 8 gq .. of the four tokens its A fragment holds) are whole fragments,
+// and nothing passes through shared memory but q. K, V and O take 96 registers
+// a lane: with a chunk's loads at the end of the one before, 128 did not hold
+// them (112 instead of 106 us for 128 x 384 own tokens behind 32 768).
+template <int B, int W, int SLICES, typename At>
+__device__ __forceinline__ void bf16_slice(const AttnArgs& a, int b, int h, int n, const uint8_t* base, const At& chunk, int wp, int lane,
+                                           uint2 (*qf)[32], float (*own)[SLICES][kPartialStride]) {
+    const int gq = lane >> 2, tq = lane & 3;
+    const int head = gq >> 1;          // this lane's column of the products: (head, high | low half)
+    const bool low = gq & 1;
+    const uint8_t* lane_k = base + gq * (kD * 2) + tq * 16;
+    const uint8_t* lane_v = base + B * kD * 2 + 2 * tq * (kD * 2) + gq * 16;
+    uint4 k[2][4], v[4][2];
+    auto load_k = [&](const ChunkRows& c) {
+        const uint8_t* p = lane_k + c.at;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                k[t][j] = 8 * t + gq < c.rows ? __ldcg(reinterpret_cast<const uint4*>(p + 8 * t * (kD * 2) + 64 * j))
+                                            : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto load_v = [&](const ChunkRows& c) {
+        const uint8_t* p = lane_v + c.at;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int row = (t & 1) + 8 * (t >> 1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                v[t][j] = 2 * tq + row < c.rows ? __ldcg(reinterpret_cast<const uint4*>(p + row * (kD * 2) + 128 * j))
+                                              : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    ChunkRows now{0, 0};
+    if (n > 0) {   // (the first one's loads go ahead of the query's)
+        now = chunk(0);
+        load_k(now);
+        load_v(now);
+    }
+    for (int ks = wp; ks < 8; ks += W) {   // the query as the B operand of each k-step, a column for each (head, high | low half)
+        const int c = 32 * (ks >> 1) + 8 * tq + 4 * (ks & 1);
+        const int64_t at_q = ((int64_t)b * a.n_q + h * a.G + min(head, a.G - 1)) * kD + c;
+        float x[4];
+        if (a.q_dtype == KVARN_FP32) {
+            *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at_q);
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + at_q);
+            x[0] = __uint_as_float(u.x << 16);
+            x[1] = __uint_as_float(u.x & 0xffff0000u);
+            x[2] = __uint_as_float(u.y << 16);
+            x[3] = __uint_as_float(u.y & 0xffff0000u);
+        }
+        qf[ks][lane] = make_uint2(bf16_pair(x[0], x[1], low), bf16_pair(x[2], x[3], low));
+    }
+    __syncthreads();
+    float o[8][4], m = -INFINITY, l = 0.f;   // o[4 i + e]: channels 64 i + 8 gq + 2 e (+ 1), head tq high | low
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    const float qs = a.sm_scale * kLog2e;
+    for (int i = 0; i < n; ++i) {
+        if (i > 0) {
+            now = chunk(i);
+            load_k(now);
+            load_v(now);
+        }
+        float s[4] = {0.f, 0.f, 0.f, 0.f};   // tokens gq and gq + 8, head tq high | low
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint2 q0 = qf[2 * j][lane], q1 = qf[2 * j + 1][lane];
+            mma_bf16(s, k[0][j].x, k[1][j].x, k[0][j].y, k[1][j].y, q0.x, q0.y);
+            mma_bf16(s, k[0][j].z, k[1][j].z, k[0][j].w, k[1][j].w, q1.x, q1.y);
+        }
+        const int here = now.rows;
+        const float s0 = gq < here ? (s[0] + s[1]) * qs : -INFINITY, s1 = gq + 8 < here ? (s[2] + s[3]) * qs : -INFINITY;
+        float bm = fmaxf(s0, s1);
+        bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 4));
+        bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 8));
+        bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 16));
+        const float mn = fmaxf(m, bm), off = mn == -INFINITY ? 0.f : mn;
+        const float f = mn == -INFINITY ? 1.f : exp2f(m - mn), p0 = exp2f(s0 - off), p1 = exp2f(s1 - off);
+        m = mn;
+        l = l * f + (p0 + p1);
+        if (__any_sync(kFull, f != 1.f)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                o[e][0] *= f;
+                o[e][1] *= f;
+                o[e][2] *= f;
+                o[e][3] *= f;
+            }
+        }
+        // weights of tokens 2 tq, 2 tq + 1 and 2 tq + 8, 2 tq + 9 for this lane's column
+        const int from = 8 * tq + head;
+        const uint32_t b0 = bf16_pair(__shfl_sync(kFull, p0, from), __shfl_sync(kFull, p0, from + 4), low);
+        const uint32_t b1 = bf16_pair(__shfl_sync(kFull, p1, from), __shfl_sync(kFull, p1, from + 4), low);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t* r0 = &v[0][j].x;
+            const uint32_t* r1 = &v[1][j].x;
+            const uint32_t* r2 = &v[2][j].x;
+            const uint32_t* r3 = &v[3][j].x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                mma_bf16(o[4 * j + e], __byte_perm(r0[e], r1[e], 0x5410), __byte_perm(r0[e], r1[e], 0x7632),
+                         __byte_perm(r2[e], r3[e], 0x5410), __byte_perm(r2[e], r3[e], 0x7632), b0, b1);
+        }
+    }
+    l += __shfl_xor_sync(kFull, l, 4);
+    l += __shfl_xor_sync(kFull, l, 8);
+    l += __shfl_xor_sync(kFull, l, 16);
+    if (tq < a.G && (SLICES == W || wp < SLICES)) {
+        float* sl = own[tq][wp];
+        if (gq == 0) {
+            sl[0] = m;
+            sl[1] = l;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e += 2)
+            *reinterpret_cast<float4*>(sl + 4 + 64 * (e >> 2) + 8 * gq + 2 * (e & 3)) =
+                make_float4(o[e][0] + o[e][1], o[e][2] + o[e][3], o[e + 1][0] + o[e + 1][1], o[e + 1][2] + o[e + 1][3]);
     }
 }
 
-// A warp's share (at most 32) of the tail rows against query row `row` as a
-// slice, unrotated: a lane scores a row.
-template <typename Rows>
-__device__ __forceinline__ void tail_share(const AttnArgs& a, const Rows& rows, int ntail, int part, int parts, int64_t row,
-                                           int lane, float* tail) {
-    const int c0 = ntail * part / parts, cnt = ntail * (part + 1) / parts - c0;
-    float qv[4];
-    load_q4(a.q, a.q_dtype, row, lane, qv);
-    const float qs = a.sm_scale * kLog2e;
-    *reinterpret_cast<float4*>(&tail[4 * lane]) = make_float4(qv[0] * qs, qv[1] * qs, qv[2] * qs, qv[3] * qs);
-    __syncwarp();
-    float s = -INFINITY;
-    if (lane < cnt) {
-        const uint4* kr = reinterpret_cast<const uint4*>(rows.k(c0 + lane));
-        s = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < 16; ++c) {
-            const uint4 k = kr[c];
-            const float4 qa = *reinterpret_cast<const float4*>(&tail[8 * c]);
-            const float4 qb = *reinterpret_cast<const float4*>(&tail[8 * c + 4]);
-            s = fmaf(qa.x, __uint_as_float(k.x << 16), s);
-            s = fmaf(qa.y, __uint_as_float(k.x & 0xffff0000u), s);
-            s = fmaf(qa.z, __uint_as_float(k.y << 16), s);
-            s = fmaf(qa.w, __uint_as_float(k.y & 0xffff0000u), s);
-            s = fmaf(qb.x, __uint_as_float(k.z << 16), s);
-            s = fmaf(qb.y, __uint_as_float(k.z & 0xffff0000u), s);
-            s = fmaf(qb.z, __uint_as_float(k.w << 16), s);
-            s = fmaf(qb.w, __uint_as_float(k.w & 0xffff0000u), s);
-        }
-    }
-    const float tm = warp_max(s);
-    const float p = s == -INFINITY ? 0.f : exp2f(s - tm);
-    const float tl = warp_sum(p);
-    float tacc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = 0; i < cnt; ++i) {
-        const float w = __shfl_sync(kFull, p, i);
-        const uint2 v = reinterpret_cast<const uint2*>(rows.v(c0 + i))[lane];
-        tacc[0] = fmaf(w, __uint_as_float(v.x << 16), tacc[0]);
-        tacc[1] = fmaf(w, __uint_as_float(v.x & 0xffff0000u), tacc[1]);
-        tacc[2] = fmaf(w, __uint_as_float(v.y << 16), tacc[2]);
-        tacc[3] = fmaf(w, __uint_as_float(v.y & 0xffff0000u), tacc[3]);
-    }
-    __syncwarp();   // (the query has been read)
-    if (lane == 0) {
-        tail[0] = tm;
-        tail[1] = tl;
-    }
-    *reinterpret_cast<float4*>(&tail[4 + 4 * lane]) = make_float4(tacc[0], tacc[1], tacc[2], tacc[3]);
+// The first ntail raw rows of a unit's staging buffer, one chunk to a warp
+// (the first four have them all), as slices of the unrotated query.
+template <int B, int W>
+__device__ __forceinline__ void tail_slice16(const AttnArgs& a, int b, int h, int ntail, int wp, int lane, uint2 (*qf)[32],
+                                             float (*tails)[4][kPartialStride]) {
+    const uint8_t* st = reinterpret_cast<const uint8_t*>(a.staging) + ((int64_t)b * a.n_kv + h) * 2 * B * kD * 2;
+    const int rows = ntail - wp * kChunk;
+    bf16_slice<B, W, 4>(a, b, h, rows > 0 ? 1 : 0, st, [&](int) { return ChunkRows{wp * kChunk * kD * 2, rows}; }, wp, lane, qf,
+                        tails);
 }
 
 // A row's merged result (own and prefix tokens) rotated back (ROT), joined
-// with its tail slices (tails, one for each of `parts` warps; nullptr: no tail)
+// with its four tail slices (nullptr: no tail)
 // and stored.
 template <bool ROT>
-__device__ __forceinline__ void finish_row(const AttnArgs& a, const PrefixMerge& pm, int64_t row, const float* tails, int parts,
-                                           int lane, float m, float l, float (&acc)[4]) {
+__device__ __forceinline__ void finish_row(const AttnArgs& a, const PrefixMerge& pm, int64_t row, const float* tails, int lane,
+                                           float m, float l, float (&acc)[4]) {
     if (ROT && !(a.flags & KVARN_FLAG_NO_ROTATION)) {
         fwht128(acc, lane);
 #pragma unroll
@@ -206,7 +285,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, const PrefixMerge&
     }
     if (tails) {
         float mt = -INFINITY, lt = 0.f, at[4] = {0.f, 0.f, 0.f, 0.f};
-        combine_slices(tails, parts, lane, mt, lt, at);
+        combine_slices(tails, 4, lane, mt, lt, at);
         add_slice(m, l, acc, mt, lt, at);
     }
     store_out(pm, row, lane, l, acc);
