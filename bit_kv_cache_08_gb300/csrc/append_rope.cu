@@ -14,8 +14,12 @@
 //
 // Bound: every q, k and v row is read and written once (512 bytes a row), so
 // memory for prompts and latency for a decode step. 32 760 prompt tokens of 48
-// rows (805 MB) into bf16 pages take 137 us, 0.87 of the measured copy
-// bandwidth, with 4 rows a half-warp in flight (147 us with 2, 194 us with 1).
+// rows (805 MB) into bf16 pages take 134 us, 0.89 of the measured copy
+// bandwidth, with 4 rows a half-warp in flight (147 us with 2, 194 us with 1);
+// with few rows a token its lookups and angles weigh more (12 rows: 58 us for
+// 201 MB). A decode step of 64 tokens takes 4 us as a graph node, into the
+// packed cache 8 (a CTA per kv head and kind, which quantises where the token
+// completes its block).
 #include "attn_common.cuh"
 #include "host_checks.h"
 #include "quantize.cuh"
@@ -422,9 +426,12 @@ int kvarn_append_rope_bf16(const kvarn_config* cfg, const kvarn_rope* rope, void
                                q_out, q_out_dtype, workspace, &c, &a);
     if (s != KVARN_OK || batch == 0 || n_tokens == 0) return s;
     a.block_bytes = (int64_t)c.n_kv_heads * 2 * c.block_size * kD * 2;
-    // a warp of its own for every 4 rows of a token, fewer where the tokens alone fill the GPU
+    // a warp of its own for every 4 rows of a token, fewer where the tokens alone
+    // give 16 warps to an SM: each looks the token's place up and makes its angles
+    // (as a graph, 1407 tokens of 60 rows: 15.0, 9.3, 8.5, 8.5 and 10.1 us with 64,
+    // 20, 16, 12 and 8)
     const int most = (c.n_q_heads + 2 * c.n_kv_heads + 3) / 4;
-    const int64_t warps = current_device_sms() * 64;
+    const int64_t warps = current_device_sms() * 16;
     int64_t runs = (warps + n_tokens - 1) / n_tokens;
     runs = runs < most ? runs : most;
     runs = runs > 1 ? runs : 1;
