@@ -14,12 +14,12 @@
 //
 // Bound: every q, k and v row is read and written once (512 bytes a row), so
 // memory for prompts and latency for a decode step. 32 760 prompt tokens of 48
-// rows (805 MB) into bf16 pages take 134 us, 0.89 of the measured copy
-// bandwidth, with 4 rows a half-warp in flight (147 us with 2, 194 us with 1);
-// with few rows a token its lookups and angles weigh more (12 rows: 58 us for
-// 201 MB). A decode step of 64 tokens takes 4 us as a graph node, into the
-// packed cache 8 (a CTA per kv head and kind, which quantises where the token
-// completes its block).
+// rows (805 MB) into bf16 pages take 128 us, 0.93 of the measured copy
+// bandwidth, with 4 rows a half-warp in flight (with 2 and 1 it took 10 and 60
+// us more); with few rows a token its lookups and angles weigh more (12 rows:
+// 50 us for 201 MB). A decode step of 64 tokens takes 4 us as a graph node, into
+// the packed cache 8 (a CTA per kv head and kind, which quantises where the
+// token completes its block).
 #include "attn_common.cuh"
 #include "host_checks.h"
 #include "quantize.cuh"
@@ -107,14 +107,15 @@ __device__ __forceinline__ int sequence_of(const RopeAppendArgs& a, int64_t t, i
 constexpr int kRowBatch = 4;
 template <int B>
 __global__ void __launch_bounds__(128) append_rope_bf16_kernel(RopeAppendArgs a, const __grid_constant__ kvarn_rope r,
-                                                               int runs) {
+                                                               uint32_t runs) {
     __shared__ uint64_t turns[64];
     copy_turns(r, turns);
     __syncthreads();
     wait_prior_grids();
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int64_t t = item / runs;
+    // (items and heads * runs stay below 2^32: the host's bounds)
+    const uint32_t item = blockIdx.x * 4 + (threadIdx.x >> 5), run = runs == 1 ? 0u : item % runs;
+    const int64_t t = runs == 1 ? item : item / runs;
     if (t >= a.n_tokens) return;
     const int b = sequence_of(a, t, lane);
     if (b < 0) {
@@ -136,11 +137,10 @@ __global__ void __launch_bounds__(128) append_rope_bf16_kernel(RopeAppendArgs a,
     load_weight(a.q_weight, rl, qw);
     load_weight(a.k_weight, rl, kw);
     uint16_t* page = reinterpret_cast<uint16_t*>(a.pool + phys * a.block_bytes) + (at % B) * kD;
-    const int run = (int)(item % runs);
     // the half-warps take the rows of a kind in turn, kRowBatch each at a time;
     // all loads of a batch are in flight (and in place they come before its stores)
     auto rows_of = [&](int heads, const uint16_t* src, auto&& put) {
-        const int h0 = (int)((int64_t)heads * run / runs), h1 = (int)((int64_t)heads * (run + 1) / runs);
+        const int h0 = runs == 1 ? 0 : heads * run / runs, h1 = runs == 1 ? heads : heads * (run + 1) / runs;
         for (int j0 = h0; j0 < h1; j0 += 2 * kRowBatch) {
             uint2 u[kRowBatch][2];
 #pragma unroll
@@ -430,15 +430,15 @@ int kvarn_append_rope_bf16(const kvarn_config* cfg, const kvarn_rope* rope, void
     // give 16 warps to an SM: each looks the token's place up and makes its angles
     // (as a graph, 1407 tokens of 60 rows: 15.0, 9.3, 8.5, 8.5 and 10.1 us with 64,
     // 20, 16, 12 and 8)
-    const int most = (c.n_q_heads + 2 * c.n_kv_heads + 3) / 4;
-    const int64_t warps = current_device_sms() * 16;
-    int64_t runs = (warps + n_tokens - 1) / n_tokens;
+    const int64_t rows = c.n_q_heads + 2 * (int64_t)c.n_kv_heads, warps = current_device_sms() * 16;
+    int64_t runs = (warps + n_tokens - 1) / n_tokens, most = (rows + 3) / 4;
+    if (most * rows > 0xffffffffll) most = 0xffffffffll / rows;
     runs = runs < most ? runs : most;
     runs = runs > 1 ? runs : 1;
     const unsigned grid = (unsigned)((n_tokens * runs + 3) / 4);
     const cudaError_t e = c.block_size == 32
-                              ? launch_pdl(append_rope_bf16_kernel<32>, grid, 128, 0, (cudaStream_t)stream, a, *rope, (int)runs)
-                              : launch_pdl(append_rope_bf16_kernel<64>, grid, 128, 0, (cudaStream_t)stream, a, *rope, (int)runs);
+                              ? launch_pdl(append_rope_bf16_kernel<32>, grid, 128, 0, (cudaStream_t)stream, a, *rope, (uint32_t)runs)
+                              : launch_pdl(append_rope_bf16_kernel<64>, grid, 128, 0, (cudaStream_t)stream, a, *rope, (uint32_t)runs);
     return e == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 

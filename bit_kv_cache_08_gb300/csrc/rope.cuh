@@ -3,7 +3,7 @@
 // groups of 4 channels are chosen so that both channels of a pair are its
 // own, whatever the layout and the part of the head that is rotated: no
 // shuffle but the norm's, and two rows an instruction (with a row per warp and
-// partners fetched by shuffles, the 32 760-token append took 216 us, now 134).
+// partners fetched by shuffles, the 32 760-token append took 216 us, now 128).
 //
 // The rotation turns channel pair i by the angle position * inv_freq[i]. In
 // 32 bits that product loses the angle of far positions (a position of 10^6
