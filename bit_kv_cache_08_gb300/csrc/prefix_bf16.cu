@@ -25,6 +25,17 @@
 // Rounding: scores are exact products summed in fp32 (an fp32 query is split
 // into two bf16 halves, two products); P is rounded to bf16, the type of V,
 // which leaves the output within 2^-8 of sum p |v|.
+//
+// Measured (32 query heads on 8 kv heads, 128 channels): 512 rows a head
+// behind 32 768 tokens (69 GFLOP, 134 MB) in 66 us, 1.05 PFLOP/s, 0.55 of a
+// library bf16 product; 256 rows behind 8192 (34 MB) in 14 us of a call, 21
+// alone and cold. The tensor pipe is busy 52 % of the time and HBM a third: the
+// bound is a step's chain (product, softmax, product and the waits between),
+// of which two streams hide half. Timing stand-ins of the whole call (119.5 us
+// then): no exponentials 115.6, no softmax 109.5, an eighth of the products
+// 111, no pages after the first two tiles 119.3. A product warp for each stream
+// (124), half a row a thread (129), P in two halves (the same), S read twice in
+// fewer registers (131) and fewer token ranges (132) were slower or no faster.
 #include "prefix.cuh"
 
 #include <cuda.h>
