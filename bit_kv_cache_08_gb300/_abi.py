@@ -8,6 +8,7 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from dataclasses import dataclass
@@ -327,6 +328,41 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: str = "no
     return f * (keep + (1 - keep) / factor), 1.0 if scaling == "bands" else 0.1 * float(np.log(factor)) + 1.0
 
 
+@functools.lru_cache(maxsize=64)
+def _block_bytes_of(n_kv: int, block_size: int, bits: int) -> int:
+    """block_bytes, which depends on these alone (a call into the library each time: 1 us)."""
+    return block_bytes(make_config(n_kv, n_kv, block_size, 1, [0, 0, 0, 0], bits=bits))
+
+
+def _need_packed(cfg, pool, staging, batch: int, of: str):
+    """The packed pool and the staging buffer of `batch` sequences (their device is checked with the others')."""
+    n_kv, B = cfg.n_kv_heads, cfg.block_size
+    try:
+        _, row = pool.shape
+        good = (pool.dtype is _u8 and staging.dtype is _bf16 and pool.is_contiguous() and staging.is_contiguous()
+                and staging.numel() >= batch * n_kv * 256 * B and row == _block_bytes_of(n_kv, B, cfg.bits))
+    except (AttributeError, TypeError, ValueError, KVarNError):
+        good = False
+    if not good:
+        _need_cuda(pool, "pool", _u8)
+        _need_cuda(staging, "staging", _bf16)
+        if pool.dim() != 2 or pool.shape[1] != block_bytes(cfg):
+            raise ValueError("pool must be [n_blocks][block_bytes]")
+        raise ValueError(f"staging holds fewer sequences than {of}")
+
+
+def _need_pages(cfg, kv_pool):
+    if (not isinstance(kv_pool, torch.Tensor) or kv_pool.dtype is not _bf16 or not kv_pool.is_contiguous()
+            or kv_pool.shape[1:] != (cfg.n_kv_heads, 2, cfg.block_size, 128)):
+        _need_cuda(kv_pool, "kv_pool", _bf16)
+        raise ValueError("kv_pool must be [n_blocks][n_kv][2][B][128]")
+
+
+def _stream_of(dev: int) -> int:
+    """The current stream of the current device `dev`, which the caller's tensors are on."""
+    return _stream() if _raw_stream is None else _raw_stream(dev)
+
+
 def _current_device() -> int:
     return torch.cuda.current_device() if _raw_device is None else _raw_device()
 
@@ -458,7 +494,7 @@ def _append_rope(cfg, rope, pool, staging, block_table, pos, q, k, v, q_out, wor
     if n == 1:   # (a single row's stride is not looked at)
         ks = vs = n_kv * 128
     tail = (block_table.data_ptr(), max_blocks, pos.data_ptr(), rope_ptr, cu_ptr, n, batch, q_ptr, k.data_ptr(),
-            v.data_ptr(), qs, ks, vs, qw_ptr, kw_ptr, out_ptr, out_code, workspace.data_ptr(), _stream())
+            v.data_ptr(), qs, ks, vs, qw_ptr, kw_ptr, out_ptr, out_code, workspace.data_ptr(), _stream_of(dev))
     if staging is None:
         r = lib().kvarn_append_rope_bf16(ctypes.byref(cfg), ctypes.byref(rope), pool.data_ptr(), pool.shape[0], *tail)
         if r:
@@ -481,12 +517,7 @@ def append_rope(cfg: Config, rope: Rope, pool: torch.Tensor, staging: torch.Tens
     8 (columns of one projection's output). cu_tokens int32 [batch + 1]: ragged
     runs of tokens; None: one token per sequence. rope_pos int32 [batch]: the
     position of each sequence's first new token (default: pos)."""
-    _need_cuda(pool, "pool", torch.uint8)
-    _need_cuda(staging, "staging", torch.bfloat16)
-    if pool.dim() != 2 or pool.shape[1] != block_bytes(cfg):
-        raise ValueError("pool must be [n_blocks][block_bytes]")
-    if staging.numel() < pos.numel() * cfg.n_kv_heads * 2 * cfg.block_size * 128:
-        raise ValueError("staging holds fewer sequences than pos")
+    _need_packed(cfg, pool, staging, pos.numel(), "pos")
     _append_rope(cfg, rope, pool, staging, block_table, pos, q, k, v, q_out, workspace, cu_tokens, rope_pos, q_weight,
                  k_weight)
 
@@ -497,9 +528,7 @@ def append_rope_bf16(cfg: Config, rope: Rope, kv_pool: torch.Tensor, block_table
                      rope_pos: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
                      k_weight: Optional[torch.Tensor] = None):
     """append_rope into the bf16 pages [n_blocks][n_kv][2][B][128] of decode_attn_bf16."""
-    _need_cuda(kv_pool, "kv_pool", torch.bfloat16)
-    if kv_pool.shape[1:] != (cfg.n_kv_heads, 2, cfg.block_size, 128):
-        raise ValueError("kv_pool must be [n_blocks][n_kv][2][B][128]")
+    _need_pages(cfg, kv_pool)
     _append_rope(cfg, rope, kv_pool, None, block_table, pos, q, k, v, q_out, workspace, cu_tokens, rope_pos, q_weight,
                  k_weight)
 
@@ -595,7 +624,7 @@ def _prefix_args(cfg, q, pool, staging, prefix_table, prefix_lens, block_table, 
     return (FP32 if q_type is _f32 else BF16,
             (prefix_table.data_ptr(), n_prefix, prefix_lens.data_ptr(), block_table.data_ptr(), max_blocks,
              seq_lens.data_ptr(), batch, out.data_ptr(), FP32 if out_type is _f32 else BF16, workspace.data_ptr(),
-             n_workspace, _stream()))
+             n_workspace, _stream_of(dev)))
 
 
 def prefix_attn(cfg: Config, q: torch.Tensor, pool: torch.Tensor, staging: torch.Tensor, prefix_table: torch.Tensor,
@@ -604,13 +633,8 @@ def prefix_attn(cfg: Config, q: torch.Tensor, pool: torch.Tensor, staging: torch
     """decode_attn for a batch that shares a prefix: sequence b sees the first
     prefix_lens[b] tokens of the blocks prefix_table [prefix_blocks], then its
     own seq_lens[b] tokens. q (bf16|fp32) and out (bf16|fp32): [batch][n_q][128]."""
-    _need_cuda(pool, "pool", torch.uint8)
-    _need_cuda(staging, "staging", torch.bfloat16)
+    _need_packed(cfg, pool, staging, seq_lens.numel(), "q")
     code, rest = _prefix_args(cfg, q, pool, staging, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
-    if pool.dim() != 2 or pool.shape[1] != block_bytes(cfg):
-        raise ValueError("pool must be [n_blocks][block_bytes]")
-    if staging.numel() < q.shape[0] * cfg.n_kv_heads * 2 * cfg.block_size * 128:
-        raise ValueError("staging holds fewer sequences than q")
     r = lib().kvarn_prefix_attn(ctypes.byref(cfg), q.data_ptr(), code, pool.data_ptr(), pool.shape[0],
                                 staging.data_ptr(), *rest)
     if r:
@@ -621,10 +645,8 @@ def prefix_attn_bf16(cfg: Config, q: torch.Tensor, kv_pool: torch.Tensor, prefix
                      prefix_lens: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, out: torch.Tensor,
                      workspace: torch.Tensor):
     """prefix_attn over the bf16 pages [n_blocks][n_kv][2][B][128] of decode_attn_bf16."""
-    _need_cuda(kv_pool, "kv_pool", torch.bfloat16)
+    _need_pages(cfg, kv_pool)
     code, rest = _prefix_args(cfg, q, kv_pool, None, prefix_table, prefix_lens, block_table, seq_lens, out, workspace)
-    if kv_pool.shape[1:] != (cfg.n_kv_heads, 2, cfg.block_size, 128):
-        raise ValueError("kv_pool must be [n_blocks][n_kv][2][B][128]")
     r = lib().kvarn_prefix_attn_bf16(ctypes.byref(cfg), q.data_ptr(), code, kv_pool.data_ptr(), kv_pool.shape[0], *rest)
     if r:
         _check(r, "kvarn_prefix_attn_bf16")

@@ -411,9 +411,11 @@ size_t kvarn_prefix_workspace_bytes(const kvarn_config* cfg, int32_t batch, int3
  * over the prefix's tokens and the own ones together; no token at all gives
  * zeros. out: device [batch][n_q][128], out_dtype KVARN_BF16 or KVARN_FP32.
  * workspace: at least kvarn_prefix_workspace_bytes(cfg, batch, prefix_blocks)
- * bytes, 16-byte aligned; calls that may overlap need one each. Device
- * faults: KVARN_DEVERR_BLOCK_ID, KVARN_DEVERR_POSITION (a length outside its
- * range), KVARN_DEVERR_WAIT_TIMEOUT.
+ * bytes, 16-byte aligned; calls that may overlap need one each. A prefix block
+ * quantised from values that were not finite (flagged when it was written)
+ * makes the outputs of every sequence with a prefix undefined.
+ * Device faults: KVARN_DEVERR_BLOCK_ID, KVARN_DEVERR_POSITION (a length outside
+ * its range), KVARN_DEVERR_WAIT_TIMEOUT.
  */
 int kvarn_prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* pool,
                       int64_t n_pool_blocks, const void* staging, const int32_t* prefix_table,
