@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnA
 }
 
 // ---------------------------------------------------------------- own tokens and merge in one (bf16 pages)
-constexpr int kJoinTokens = 1024;   // of an own table's columns, at most
+constexpr int kJoinTokens = 2048;   // of an own table's columns, at most
 
 // The 16-token chunks wp, wp + W, ... of a unit's own pages, for bf16_slice.
 template <int B, int W>
@@ -110,12 +110,11 @@ struct OwnChunks {
 // but a unit has only its CTA. Memory bounds it (512 bytes a token and kv
 // head) where the units fill the GPU, the chain of dependent loads where they
 // do not. A call of 64 sequences with 192 own tokens of 8 kv heads behind 8192
-// of a prefix takes 33 us with CTAs of 4 at 16 warps per SM (CTAs of 8: 36; 8 or
-// 12 warps per SM with the next chunk's loads in flight during a chunk's
-// products: 45, 37; split kernel and merge: 42), 128 with 384 behind 32 768
-// takes 106 (112; 127, 105; 119).
+// of a prefix takes 33 us with CTAs of 4 at 16 warps per SM (8 or 12 warps per SM
+// with the next chunk's loads in flight during a chunk's products: 45, 37; split
+// kernel and merge: 42), 128 with 384 behind 32 768 takes 106 (127, 105; 119).
 template <int B, int W>
-__global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 4) prefix_join_kernel(AttnArgs a, PrefixMerge pm) {
+__global__ void __launch_bounds__(32 * W, 16 / W) prefix_join_kernel(AttnArgs a, PrefixMerge pm) {
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int b = blockIdx.x, h = blockIdx.y;
     const int parts = merge_parts(a.G, W), g = wp / parts, part = wp % parts;
@@ -237,11 +236,11 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
     cudaError_t e;
     AttnArgs a = {};
     // An own table of more columns may hold sequences that are long for one CTA:
-    // 4 sequences of up to 1024 / 2048 own tokens in bf16 pages, 8 kv heads, take
-    // 26 / 49 us against 28 / 30 by the split kernel and a merge, 128 sequences
-    // 108 / 183 against 111 / 182. Packed blocks need an SM's shared memory for a
-    // unit: with a CTA per SM 16 sequences take 21.1 .. 28.8 us against 22.7 ..
-    // 37.2 (up to 64 .. 1024 tokens).
+    // 4 sequences of up to 2048 / 4096 own tokens in bf16 pages, 8 kv heads, take
+    // 28 / 38 us against 29 / 32 by the split kernel and a merge, 128 sequences
+    // 169 / 310 against 181 / 325. Packed blocks need an SM's shared memory for a
+    // unit: with a CTA per SM 16 sequences take 21 .. 32 us against 23 .. 37 (up to
+    // 64 .. 2048 tokens; 4096: 39 against 41).
     const bool join = (int64_t)max_blocks * c.block_size <= kJoinTokens &&
                       (!PACKED || (int64_t)batch * c.n_kv_heads <= current_device_sms());
     if constexpr (PACKED) {
@@ -287,9 +286,15 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
             return c.block_size == 32 ? launch_pdl(prefix_join_kernel<32, W>, units, 32 * W, 0, st, a, pm)
                                       : launch_pdl(prefix_join_kernel<64, W>, units, 32 * W, 0, st, a, pm);
         };
-        // (8 warps share a unit where there is an SM for each)
-        e = (int64_t)batch * c.n_kv_heads <= current_device_sms() ? start(std::integral_constant<int, 8>{})
-                                                                  : start(std::integral_constant<int, 4>{});
+        // 16 warps per SM, and as many of them to a unit as let all units run at
+        // once: 16 sequences of up to 64 / 1024 own tokens, 8 kv heads, take 14.0 /
+        // 22.6 us with 16 to a unit and 15.5 / 30.5 with 8, 28 sequences 17.0 / 36.2
+        // with 8 and 19.6 / 50.4 with 4. Beyond that 4, but 8 for long tables: 64
+        // sequences 21.1 / 64.5 with 4, 23.2 / 63.2 with 8, 40 of 1024 57 and 49.
+        const int64_t n = (int64_t)batch * c.n_kv_heads, sms = current_device_sms();
+        const bool wide = n <= 2 * sms || (int64_t)max_blocks * c.block_size > kJoinTokens / 4;
+        e = n <= sms ? start(std::integral_constant<int, 16>{})
+                     : wide ? start(std::integral_constant<int, 8>{}) : start(std::integral_constant<int, 4>{});
     }
     return e == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }

@@ -350,13 +350,16 @@ OWN = [  # own lengths, batch repeats, n_q, n_kv, B, q dtype
     ([700, 5, 0, 128, 300], 1, 4, 2, 64, torch.float32),
     ([90, 129, 17, 64, 255, 1], 4, 28, 7, 64, torch.bfloat16),     # more units than the GPU has SMs
     ([40, 3, 100, 0, 63], 13, 12, 12, 32, torch.float32),          # several waves of them
+    ([2048, 31, 0, 1999, 1], 1, 12, 4, 64, torch.bfloat16),
+    ([2047, 1100], 1, 2, 2, 32, torch.float32),
+    ([1500, 2048] + [3] * 78, 1, 4, 4, 64, torch.bfloat16),        # long ones among many
 ]
 
 
 @pytest.mark.parametrize("bits", [0, 2, 3, 4])
 @pytest.mark.parametrize("case", range(len(OWN)))
 def test_own_tokens_in_narrow_and_wide_tables(kvlib, case, bits):
-    """Own tokens up to 1024; the same with table columns that no length reaches, for which other kernels serve."""
+    """Own tokens up to 2048; the same with table columns that no length reaches, for which other kernels serve."""
     lens, times, n_q, n_kv, B, qdt = OWN[case]
     lens, P = lens * times, 150
     s = Shared(kvlib, 50 + case, P, lens, n_q, n_kv, B, bits)
@@ -365,7 +368,7 @@ def test_own_tokens_in_narrow_and_wide_tables(kvlib, case, bits):
     seqs = list(range(len(lens) // times)) + [len(lens) - 1]
     want, tol = s.reference(q, pl, seqs)
     table = s.table
-    for columns in (table.shape[1], 1024 // B + 1, 4096 // B):
+    for columns in sorted({max(c, table.shape[1]) for c in (0, 1024 // B + 1, 2048 // B, 2048 // B + 1, 4096 // B)}):
         s.table = torch.full((len(lens), columns), -1, dtype=torch.int32, device="cuda")
         s.table[:, :table.shape[1]] = table
         got = s.run(q, pl)
@@ -380,7 +383,7 @@ def test_bad_own_blocks_are_flagged(kvlib, bits):
     s = Shared(kv, 61, 100, [200, 70, 300], 8, 2, 32, bits)
     q = synth.queries(synth.make_gen(7), 3, 8).cuda()
     narrow = s.table
-    for columns in (narrow.shape[1], 40):
+    for columns in (narrow.shape[1], 80):
         s.table = torch.full((3, columns), -1, dtype=torch.int32, device="cuda")
         s.table[:, :narrow.shape[1]] = narrow
         ws = kv.alloc_prefix_workspace(s.cfg, 3, len(s.prefix_np))
@@ -396,7 +399,7 @@ def test_bad_own_blocks_are_flagged(kvlib, bits):
         assert torch.equal(s.run(q, [100, 3, 0], ws=ws), good)
 
 
-@pytest.mark.parametrize("bits,columns", [(0, 4), (0, 40), (2, 4), (2, 40)])
+@pytest.mark.parametrize("bits,columns", [(0, 4), (0, 80), (2, 4), (2, 80)])
 def test_inputs_that_the_kernel_before_wrote(kvlib, bits, columns):
     """Lengths, table entries, queries and own rows written on the stream just before each call, with nothing waited for:
     the same bits as with the GPU idle between the steps."""
