@@ -154,20 +154,37 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // the odd K/V tiles of a range are summed apart).
 struct PrefixPlan {
     int rows, streams, splits;
+    int most;   // ranges that a shorter prefix may take: the workspace holds them, so that it serves that one too
 };
 
 PrefixPlan prefix_plan(const kvarn_config& c, int64_t batch, int64_t prefix_blocks, bool packed, int q_dtype) {
     const int64_t sms = current_device_sms(), R = batch * (c.n_q_heads / c.n_kv_heads);
-    PrefixPlan p{kPRows, 1, 0};
+    PrefixPlan p{kPRows, 1, 0, 0};
     if (sms <= 0) return p;
     if (R > kPRows && (packed || q_dtype == KVARN_BF16)) p.rows = 2 * kPRows;
     else if (!packed) p.streams = 2;
-    // enough ranges for every SM to have one
+    // The token ranges that make waves of CTAs times a CTA's tiles least: 3 tiles
+    // stand for a CTA's start and end; of the ranges with the same tiles for a CTA
+    // the fewest, for there are as many partials (64 sequences behind 8192 tokens:
+    // 16 ranges 23.3 us, 19 24.2). More than one wave only where one would leave
+    // many SMs idle (1300 sequences behind 8000 tokens, 168 CTAs a range: one range
+    // 321 us, four waves at most 275; packed 654 and 520). Packed CTAs of one tile
+    // lost 3 us to twice the partials.
     const int64_t units = c.n_kv_heads * ((R + p.rows - 1) / p.rows);
-    const int64_t tiles = (prefix_blocks * c.block_size + 127) / 128;
-    int64_t s = sms / units;
-    s = s < tiles ? s : tiles;
-    p.splits = (int)(s > 1 ? s : 1);
+    const int64_t tile = packed ? 64 : 128, tiles = (prefix_blocks * c.block_size + tile - 1) / tile;
+    const int64_t ranges = packed ? (tiles + 1) / 2 : tiles;
+    const int max_waves = 4 * units > sms ? 4 : 1;
+    auto within = [&](int64_t s) { return s > ranges ? (ranges > 1 ? ranges : 1) : s > 1 ? s : 1; };
+    int64_t least = 0;
+    for (int waves = 1; waves <= max_waves; ++waves) {
+        const int64_t s = within(waves * sms / units), per = (tiles + s - 1) / s;
+        const int64_t few = per > 0 ? (tiles + per - 1) / per : 1;
+        const int64_t cost = (units * few + sms - 1) / sms * (per + 3);
+        if (waves > 1 && cost >= least) continue;
+        least = cost;
+        p.splits = (int)few;
+    }
+    p.most = (int)within(max_waves * sms / units);
     return p;
 }
 
@@ -178,7 +195,7 @@ size_t prefix_ws_bytes(const kvarn_config& c, int32_t batch, int64_t prefix_bloc
     for (int k = 0; k < 3; ++k) {
         const PrefixPlan p = prefix_plan(c, batch, prefix_blocks, k == 0, k == 1 ? KVARN_BF16 : KVARN_FP32);
         if (p.splits == 0) return 0;
-        slots = p.splits * p.streams > slots ? p.splits * p.streams : slots;
+        slots = p.most * p.streams > slots ? p.most * p.streams : slots;
     }
     if (own == 0) return 0;
     return align256(own) + (size_t)slots * batch * c.n_q_heads * kPartialStride * sizeof(float);

@@ -393,7 +393,8 @@ int kvarn_decode_attn_bf16(const kvarn_config* cfg, const void* q, int32_t q_dty
 /* Workspace bytes for kvarn_prefix_attn / kvarn_prefix_attn_bf16 with this
  * batch and prefix_blocks on the CURRENT device: the decode workspace for the
  * own tokens, then one partial per (token range of the prefix, sequence,
- * query head). 0 on a bad config. */
+ * query head). It serves shorter prefixes of the same batch too. 0 on a bad
+ * config. */
 size_t kvarn_prefix_workspace_bytes(const kvarn_config* cfg, int32_t batch, int32_t prefix_blocks);
 
 /*

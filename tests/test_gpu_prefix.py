@@ -453,6 +453,14 @@ def test_no_own_blocks_and_small_tables(kvlib):
         assert torch.all(got[1] == 0)
 
 
+@pytest.mark.parametrize("n_q,n_kv,B", [(32, 8, 64), (40, 10, 32), (1, 1, 64), (128, 64, 32)])
+@pytest.mark.parametrize("batch", [1, 5, 64, 700])
+def test_a_workspace_serves_shorter_prefixes(kvlib, n_q, n_kv, B, batch):
+    cfg = kvlib.make_config(n_q, n_kv, B, 2, synth.sign_bits(1))
+    sizes = [kvlib.prefix_workspace_bytes(cfg, batch, b) for b in list(range(0, 400)) + [512, 1000, 4096, 20000]]
+    assert all(0 < x <= y for x, y in zip(sizes, sizes[1:]))
+
+
 def test_workspace_and_binding_refusals(kvlib):
     kv = kvlib
     s = Shared(kv, 19, 64, [40, 3], 4, 2, 32, 2)
