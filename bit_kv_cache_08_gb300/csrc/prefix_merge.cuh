@@ -20,7 +20,7 @@ struct PrefixMerge {
 };
 
 // LSE merge of the partials first .. last - 1 of a row's list (np own ones at
-// p0, pstride apart, then the prefix's at s0, sstride apart), 8 in flight at a
+// p0, pstride apart, then the prefix's at s0, sstride apart), NB in flight at a
 // time with a running rescale; m, l and acc start at -inf, 0 and 0.
 template <int NB>
 __device__ __forceinline__ void lse_list(const float* p0, int np, int64_t pstride, const float* s0, int64_t sstride, int first,
