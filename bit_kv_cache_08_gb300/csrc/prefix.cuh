@@ -49,6 +49,41 @@ __device__ __forceinline__ float ex2(float x) {
 // within its 64-element column block.
 __device__ __forceinline__ uint32_t swizzled(int r, int u) { return (uint32_t)(r * 128 + ((u ^ (r & 7)) << 4)); }
 
+// a b + c with 16-bit a and b (the low or the high half of a register) and
+// fp32 c: the product is exact, the sum rounds once.
+__device__ __forceinline__ float fma_half(uint32_t a, uint32_t b, float c, bool high_a, bool high_b) {
+    const uint16_t x = high_a ? (uint16_t)(a >> 16) : (uint16_t)a, y = high_b ? (uint16_t)(b >> 16) : (uint16_t)b;
+    float d;
+    asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"(y), "f"(c));
+    return d;
+}
+// c - a for a bf16 a.
+__device__ __forceinline__ float minus_bf16(uint32_t a, float c, bool high) {
+    const uint16_t x = high ? (uint16_t)(a >> 16) : (uint16_t)a;
+    float d;
+    asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"((uint16_t)0xbf80), "f"(c));
+    return d;
+}
+
+// Two fp32 values as pairs of 16-bit halves, hi = RN(x) and lo = RN(x - hi):
+// together within 2^-16 (bf16) or 2^-22 (HALF: fp16, normal halves) of x.
+template <bool HALF>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
+    if (HALF) {
+        hi = pack_h2(x, y);
+        lo = pack_h2(fma_half(hi, 0xbc00u, x, false, false), fma_half(hi, 0xbc00u, y, true, false));
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        hi = *reinterpret_cast<const uint32_t*>(&h);
+        const __nv_bfloat162 l = __floats2bfloat162_rn(minus_bf16(hi, x, false), minus_bf16(hi, y, true));
+        lo = *reinterpret_cast<const uint32_t*>(&l);
+    }
+}
+
+// P in the tensor memory of S: a weight's two halves take the place of its
+// score, so 16 columns of S become 8 of high and 8 of low halves.
+constexpr uint32_t kPLow = 8;
+
 // One thread's row of an online softmax (everything in the log2 domain): the
 // reference m that P and O are relative to, and the sum l.
 struct RowState {
@@ -56,12 +91,12 @@ struct RowState {
 };
 
 // The softmax of a TOK-token tile by the 128 threads of a stream, a row each:
-// reads S (fp32) at my_s, writes P (16-bit, HALF: fp16, else bf16) over it,
-// and rescales O at my_o. A weight is 2^(scale s + bias - m + lift): bias is
-// the tile's value exponent (V is stored times 2^-bias), lift a constant that
-// keeps small fp16 weights out of the subnormals. The reference grows only
-// past 2^8 of what is there, so P stays within 2^(8 + lift) and O is seldom
-// touched; o_idle() waits until no product writes O (false: gave up).
+// reads S (fp32) at my_s, writes P (two 16-bit halves, HALF: fp16, else bf16)
+// over it, and rescales O at my_o. A weight is 2^(scale s + bias - m + lift):
+// bias is the tile's value exponent (V is stored times 2^-bias), lift a
+// constant that keeps small fp16 weights out of the subnormals. The reference
+// grows only past 2^8 of what is there, so P stays within 2^(8 + lift) and O is
+// seldom touched; o_idle() waits until no product writes O (false: gave up).
 // `shown`: tokens of the tile that this row sees. The caller waits for S
 // before; each of the stream's 4 warps arrives on p_ready.
 // S stays in registers (CHUNK = TOK) or is read twice, CHUNK columns at a
@@ -113,23 +148,16 @@ __device__ __forceinline__ bool softmax_tile(uint32_t my_s, uint32_t my_o, int s
     for (int c0 = 0; c0 < TOK; c0 += CHUNK) {
         if (CHUNK < TOK) load(c0);
 #pragma unroll
-        for (int i = 0; i < CHUNK; i += 2) {
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, off2);
-            const float2 p = make_float2(ex2(y.x), ex2(y.y));
-            sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], p);
-            if (HALF) {
-                x[i >> 1] = pack_h2(p.x, p.y);
-            } else {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
-                x[i >> 1] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-        }
-        // (over columns of S that have been read)
-        if (CHUNK == 32) {
-            tmem_st16(my_s + c0 / 2, x);
-        } else {
+        for (int c = 0; c < CHUNK; c += 16) {
+            uint32_t y[16];   // high halves, low halves
 #pragma unroll
-            for (int c = 0; c < CHUNK / 2; c += 32) tmem_st32(my_s + c0 / 2 + c, x + c);
+            for (int i = 0; i < 16; i += 2) {
+                const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[c + i]), __uint_as_float(x[c + i + 1])), scale2, off2);
+                const float2 p = make_float2(ex2(e.x), ex2(e.y));
+                sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], p);
+                split_pair<HALF>(p.x, p.y, y[i >> 1], y[8 + (i >> 1)]);
+            }
+            tmem_st16(my_s + c0 + c, y);   // (over columns of S that have been read)
         }
     }
     tmem_wait_st();

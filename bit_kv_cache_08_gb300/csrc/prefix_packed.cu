@@ -10,9 +10,9 @@
 //       into two bf16 halves, and three products (hi hi, hi lo, lo hi) keep
 //       2^-16 of each factor: a score is exponentiated, so its error must not
 //       grow with the size of the scores
-//   P = 2^(S - m), O += P V'      one fp16 product (2^-11 each): V' is
-//       (code s + z) R C 2^-e, the tile's exponent e making its largest value
-//       at most 1; e enters the exponent of P, so P V' needs no other scale
+//   P = 2^(S - m), O += P V'      P is split into two fp16 halves, V' is fp16
+//       (2^-11): (code s + z) R C 2^-e, the tile's exponent e making its largest
+//       value at most 1; e enters the exponent of P, so P V' needs no other scale
 // Tensor memory: Q's high half as the A operand (64 columns a row tile; its
 // low half stays in shared memory), S / P of two steps (2 x 64), O (128 a row
 // tile) -- 512 columns with two row tiles. K' and V' have two stages each.
@@ -76,25 +76,9 @@ struct PackedLayout {
     static constexpr size_t bytes = 1024 + kHeader + NT * kPkQ + 4 * kPkK + 2 * kPkV + kRawStages * kRaw;
 };
 
-// a b + c with 16-bit a and b (the low or the high half of a register) and
-// fp32 c: the product is exact, the sum rounds once.
-__device__ __forceinline__ float fma_half(uint32_t a, uint32_t b, float c, bool high_a, bool high_b) {
-    const uint16_t x = high_a ? (uint16_t)(a >> 16) : (uint16_t)a, y = high_b ? (uint16_t)(b >> 16) : (uint16_t)b;
-    float d;
-    asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"(y), "f"(c));
-    return d;
-}
 __device__ __forceinline__ uint32_t sign_word(uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3, int w) {
     return w == 0 ? s0 : w == 1 ? s1 : w == 2 ? s2 : s3;
 }
-// c - a for a bf16 a.
-__device__ __forceinline__ float minus_bf16(uint32_t a, float c, bool high) {
-    const uint16_t x = high ? (uint16_t)(a >> 16) : (uint16_t)a;
-    float d;
-    asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"((uint16_t)0xbf80), "f"(c));
-    return d;
-}
-
 // Pair j of a record word as fp16 code 2^-9 (attn_common.cuh); for 3-bit
 // codes jh is the pair's place in the high-bit word.
 template <int BITS>
@@ -486,7 +470,10 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                 if (j >= 0) {
                     const uint32_t p = tm_s + 64 * w, vd = v_desc + (tj & 1) * (kPkV >> 4);
 #pragma unroll
-                    for (int k = 0; k < kPkTok / 16; ++k) mma_ts(tm_o + 128 * x, p + 8 * k, vd + 2 * k, kPv, tj > 0 || k > 0);
+                    for (int k = 0; k < kPkTok / 16; ++k) {       // P's high and low halves
+                        mma_ts(tm_o + 128 * x, p + 16 * k, vd + 2 * k, kPv, tj > 0 || k > 0);
+                        mma_ts(tm_o + 128 * x, p + 16 * k + kPLow, vd + 2 * k, kPv, true);
+                    }
                     if (NT == 1 || w == 1) mma_commit(&s.v_empty[tj & 1]);
                     if (j + NT >= steps) mma_commit(&s.o_full[x]);
                 }

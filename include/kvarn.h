@@ -429,9 +429,9 @@ int kvarn_prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, c
  * kvarn_decode_attn_bf16; the last page of the prefix may be partly filled,
  * and its rows behind the longest prefix_lens may hold anything. The values
  * before that must be finite even for sequences that do not see them (their
- * weight of 0 takes part in the product). Softmax weights of the prefix are
- * rounded to bf16, the type of the values: the output is within 2^-8 of
- * sum p |v| (kvarn_prefix_attn: fp16 weights and values, 2^-11 each).
+ * weight of 0 takes part in the product). Softmax weights of the prefix enter
+ * the product as two bf16 halves, as in kvarn_decode_attn_bf16 (within 2^-16;
+ * kvarn_prefix_attn: two fp16 halves, and the values rounded to fp16, 2^-11).
  */
 int kvarn_prefix_attn_bf16(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* kv_pool,
                            int64_t n_pool_blocks, const int32_t* prefix_table, int32_t prefix_blocks,
