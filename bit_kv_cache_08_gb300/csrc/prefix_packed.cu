@@ -10,9 +10,12 @@
 //       into two bf16 halves, and three products (hi hi, hi lo, lo hi) keep
 //       2^-16 of each factor: a score is exponentiated, so its error must not
 //       grow with the size of the scores
-//   P = 2^(S - m), O += P V'      P is split into two fp16 halves, V' is fp16
-//       (2^-11): (code s + z) R C 2^-e, the tile's exponent e making its largest
-//       value at most 1; e enters the exponent of P, so P V' needs no other scale
+//   P = 2^(S - m), O += P V'      P and V' are each split into two fp16 halves,
+//       three products (2^-22): V' is (code s + z) R C 2^-e, the tile's exponent
+//       e making its largest value at most 2^15, so that the low halves of
+//       values down to 2^-18 of it are normal; e enters the exponent of P, so
+//       P V' needs no other scale. (One fp16 value each left errors of 2^-12 of
+//       sum p |v|, for 23 us of 205 at 128 x 32 768, 4 bits.)
 // Tensor memory: Q's high half as the A operand (64 columns a row tile; its
 // low half stays in shared memory), S / P of two steps (2 x 64), O (128 a row
 // tile) -- 512 columns with two row tiles. K' and V' have two stages each.
@@ -48,19 +51,20 @@ constexpr int kPkTok = 64;                       // tokens of a tile
 constexpr int kPkK = kPkTok * kD * 2;            // bytes of one 64 x 128 bf16 operand (two 64-channel blocks)
 constexpr int kPkV = kD * kPkTok * 2;            // 128 channel rows x 64 tokens, fp16
 constexpr int kPkQ = kPRows * kD * 2;            // 128 query rows, bf16
-constexpr int kRawStages = 4;
+constexpr int kMaxRaw = 4;                       // stages of raw tiles, at most
 constexpr int kBuildWarps = 8;
-static_assert(kRawStages + 2 <= 8, "exponents in flight");
-static_assert(2 * kPkV == kD * kD * 2, "the rotation matrix fits V's stages");
+static_assert(kMaxRaw + 2 <= 8, "exponents in flight");
+static_assert(2 * kPkV == kD * kD * 2, "the rotation matrix fits V's first stage");
 constexpr float kLift = 7.f;                     // P up to 2^(8 + 7), small weights normal down to 2^-21
+constexpr int kTopExp = 15;                      // V' up to 2^15: halves of small values stay normal
 
 struct PackedSmem {
     // ready: a raw tile's exponent is known; raw_empty: its operands are built
-    uint64_t raw_full[kRawStages], ready[kRawStages], raw_empty[kRawStages];
+    uint64_t raw_full[kMaxRaw], ready[kMaxRaw], raw_empty[kMaxRaw];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], q_done, drained;
     uint32_t tmem;
     int stop;
-    // e of the last tiles: the raw tiles' warp is at most kRawStages tiles ahead of
+    // e of the last tiles: the raw tiles' warp is at most kMaxRaw tiles ahead of
     // the V' that is built, which is at most two ahead of the softmax that reads e
     int vexp[8];
 };
@@ -73,7 +77,11 @@ struct PackedLayout {
     static constexpr int kBlocks = kPkTok / B;                 // blocks per tile
     static constexpr int kRaw = kBlocks * 2 * HB;              // bytes of a raw tile: (K, V) per block
     static constexpr int kHeader = (sizeof(PackedSmem) + 1023) / 1024 * 1024;
-    static constexpr size_t bytes = 1024 + kHeader + NT * kPkQ + 4 * kPkK + 2 * kPkV + kRawStages * kRaw;
+    static constexpr int kFixed = 1024 + kHeader + NT * kPkQ + 4 * kPkK + 4 * kPkV;
+    static constexpr int kFit = (227 * 1024 - kFixed) / kRaw;  // (2 with two row tiles and 4-bit blocks of 32 tokens)
+    static constexpr int kRawStages = kFit < kMaxRaw ? kFit : kMaxRaw;
+    static_assert(kRawStages >= 2, "a raw tile in flight while another is built");
+    static constexpr size_t bytes = kFixed + kRawStages * kRaw;
 };
 
 __device__ __forceinline__ uint32_t sign_word(uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3, int w) {
@@ -93,14 +101,14 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
     wait_prior_grids();
     let_next_grid_start();   // the own tokens' split kernel
     using Lay = PackedLayout<B, BITS, NT>;
-    constexpr int kSoft = Lay::kSoft;
+    constexpr int kSoft = Lay::kSoft, kRawStages = Lay::kRawStages;
     extern __shared__ uint8_t raw_smem[];
     uint8_t* base = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
     PackedSmem& s = *reinterpret_cast<PackedSmem*>(base);
     uint8_t* q_lo = base + Lay::kHeader;          // [row tile]
     uint8_t* k_op = q_lo + NT * kPkQ;             // [stage][hi, lo]
-    uint8_t* v_op = k_op + 4 * kPkK;              // [stage]; first the rotation matrix
-    uint8_t* raw = v_op + 2 * kPkV;               // [raw stage][block][K, V]
+    uint8_t* v_op = k_op + 4 * kPkK;              // [stage][hi, lo]; first the rotation matrix
+    uint8_t* raw = v_op + 4 * kPkV;               // [raw stage][block][K, V]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.z, R = a.batch * a.G, row0 = blockIdx.y * NT * kPRows;
     const int max_len = a.n_blocks * B;
@@ -183,7 +191,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                     if (q32) y[j] = *reinterpret_cast<const uint4*>(src + 16);
                 }
             }
-            if (i0 == tid)                                               // H, in V's first stages, under the loads
+            if (i0 == tid)                                               // H, in V's first stage, under the loads
                 for (int i = tid; i < kD * 16; i += Lay::kThreads) {
                     const int r = i >> 4, u = i & 15;
                     uint32_t w[4];
@@ -320,7 +328,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                                 __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(cmax)));
             // the clamps keep 2^-e and 2^e finite
             if (lane == 0) {
-                s.vexp[i & 7] = bound > 0x1p-60f ? min(ceil_log2(bound), 100) : -60;
+                s.vexp[i & 7] = (bound > 0x1p-60f ? min(ceil_log2(bound), 100) : -60) - kTopExp;
                 mbar_arrive(&s.ready[st]);
             }
         }
@@ -430,20 +438,23 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                 if (i >= 2) ok = warp_wait_or_stop(&s.v_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
                 if (i == 0) ok = warp_wait_or_stop(&s.q_done, 0, stop, kWaitLimit);   // (H was here)
                 if (!ok) break;
-                uint8_t* dst = v_op + par * kPkV;
+                uint8_t* dst = v_op + par * 2 * kPkV;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t w8 = w[k] >> 8;
-                    uint32_t out[4];
+                    uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {                 // tokens 2p, 2p + 1
                         const int j = BITS == 4 ? p : 4 * (p >> 1) + 2 * (p & 1) + (k & 1);
                         const uint32_t f = code_pair<BITS>(w[k], w8, hw, j, 8 * (k >> 1) + j);
                         float2 y = make_float2(fma_half(f, sw[p], zero[p].x, false, false), fma_half(f, sw[p], zero[p].y, true, true));
                         y = __fmul2_rn(__fmul2_rn(y, fac[p]), make_float2(cf[k], cf[k]));
-                        out[p] = there ? pack_h2(y.x, y.y) : 0u;
+                        split_pair<true>(y.x, y.y, hi[p], lo[p]);
+                        if (!there) hi[p] = lo[p] = 0u;
                     }
-                    *reinterpret_cast<uint4*>(dst + swizzled(32 * g + 4 * ra + k, 4 * sb + rb)) = make_uint4(out[0], out[1], out[2], out[3]);
+                    const uint32_t at = swizzled(32 * g + 4 * ra + k, 4 * sb + rb);
+                    *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(dst + kPkV + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 fence_async_smem();
                 warp_arrive(&s.v_full[par]);
@@ -468,10 +479,11 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                 if (!ok) break;
                 tc_fence_after();
                 if (j >= 0) {
-                    const uint32_t p = tm_s + 64 * w, vd = v_desc + (tj & 1) * (kPkV >> 4);
+                    const uint32_t p = tm_s + 64 * w, vd = v_desc + (tj & 1) * (2 * kPkV >> 4);
 #pragma unroll
-                    for (int k = 0; k < kPkTok / 16; ++k) {       // P's high and low halves
+                    for (int k = 0; k < kPkTok / 16; ++k) {       // hi hi, hi lo, lo hi
                         mma_ts(tm_o + 128 * x, p + 16 * k, vd + 2 * k, kPv, tj > 0 || k > 0);
+                        mma_ts(tm_o + 128 * x, p + 16 * k, vd + (kPkV >> 4) + 2 * k, kPv, true);
                         mma_ts(tm_o + 128 * x, p + 16 * k + kPLow, vd + 2 * k, kPv, true);
                     }
                     if (NT == 1 || w == 1) mma_commit(&s.v_empty[tj & 1]);
@@ -544,7 +556,7 @@ template <int B, int BITS, int NT>
 cudaError_t launch_packed_tiles(const PrefixArgs& p, cudaStream_t st) {
     using Lay = PackedLayout<B, BITS, NT>;
     static_assert(Lay::bytes <= 227 * 1024, "shared memory of one CTA");
-    static_assert(Lay::kSoft * 32 * kPartialStride * 4 <= NT * kPkQ + 4 * kPkK + 2 * kPkV, "the partials' staging fits the operands' memory");
+    static_assert(Lay::kSoft * 32 * kPartialStride * 4 <= NT * kPkQ + 4 * kPkK + 4 * kPkV, "the partials' staging fits the operands' memory");
     static bool ready[64];
     int d = 0;
     cudaError_t e = cudaGetDevice(&d);

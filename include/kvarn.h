@@ -431,7 +431,8 @@ int kvarn_prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, c
  * before that must be finite even for sequences that do not see them (their
  * weight of 0 takes part in the product). Softmax weights of the prefix enter
  * the product as two bf16 halves, as in kvarn_decode_attn_bf16 (within 2^-16;
- * kvarn_prefix_attn: two fp16 halves, and the values rounded to fp16, 2^-11).
+ * kvarn_prefix_attn: weights and values as two fp16 halves, within 2^-22, and
+ * for values below 2^-18 of the largest of their 64 tokens within 2^-40 of it).
  */
 int kvarn_prefix_attn_bf16(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* kv_pool,
                            int64_t n_pool_blocks, const int32_t* prefix_table, int32_t prefix_blocks,

@@ -8,7 +8,8 @@ Tolerance of a row, t_c = e A_c for channel c of the space the products run in,
 A = sum p |v|, and the 2-norm of t plus 2^-20 of the output's (8 fp32 roundings
 of the rotation back and the store), with e the sum of
   what is kept of a weight and a value   2^-16 for a weight in bf16 halves (a
-    bf16 value is exact)
+    bf16 value is exact), 3 * 2^-22 in fp16 halves (a weight, a value, and the
+    product of the low halves, which is left out)
   the scores   2 d: a score is off by d, its weight by that, and the normaliser
     by it again; d = (2^-17 for the fp32 sum of 128 products, 2^-22 for the
     exponent's product and sum, and 2^-16 for an fp32 query in bf16 halves)
@@ -55,7 +56,7 @@ def _check(s, q, pl, kept, score):
     o, A, size = _exact(s, q, pl)
     got = s.run(q, pl).double().cpu().numpy()
     if s.bits and not int(s.cfg.flags) & 1:
-        got = oracle.rotate(got, s.sb)
+        got = oracle.rotate(got, s.sb).reshape(got.shape)
     tol = (kept + 2.0 ** -18 + np.expm1(2 * score * size)) * A
     norm = lambda x: np.linalg.norm(x, axis=-1)  # noqa: E731
     ratio = norm(got - o) / (norm(tol) + 2.0 ** -20 * norm(o))
@@ -81,3 +82,23 @@ def test_weights_over_bf16_pages(kvlib, case):
     q = (0.1 * synth.queries(synth.make_gen(40 + case), batch, n_q)).to(qdt).cuda()
     score = 2.0 ** -17 + 2.0 ** -22 + (2.0 ** -16 if qdt == torch.float32 else 0)
     _check(s, q, [P] * batch, 2.0 ** -16, score)
+
+
+PACKED = [  # prefix tokens, batch, n_q, n_kv, B, q dtype
+    (2, 3, 4, 4, 32, torch.bfloat16),
+    (5, 40, 8, 2, 64, torch.bfloat16),
+    (33, 150, 4, 4, 32, torch.float32),
+    (64, 70, 8, 4, 64, torch.bfloat16),
+    (90, 5, 3, 1, 32, torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4])
+@pytest.mark.parametrize("case", range(len(PACKED)))
+def test_weights_and_values_over_the_packed_cache(kvlib, case, bits):
+    """Flat scores; the queries so small that what the score's halves leave out (3 * 2^-16 of sum |q k|) is nothing."""
+    P, batch, n_q, n_kv, B, qdt = PACKED[case]
+    s = Shared(kvlib, 90 + case, P, [0] * batch, n_q, n_kv, B, bits, small=1)
+    q = (0.01 * synth.queries(synth.make_gen(50 + case), batch, n_q)).to(qdt).cuda()
+    # (a weight and a value as fp16 pairs: 2^-22 each and the product of the low halves)
+    _check(s, q, [P] * batch, 3 * 2.0 ** -22, 3 * 2.0 ** -16 + 2.0 ** -17)
