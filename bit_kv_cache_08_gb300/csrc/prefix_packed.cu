@@ -6,10 +6,12 @@
 // merge rotates back). Per kv head and up to 256 of its batch * G query rows
 // (two tiles of 128, which share the built operands), over the CTA's range of
 // 64-token tiles:
-//   S = Q K'^T (128 x 64, fp32)   K' = (code s + z) R C and Q are each split
-//       into two bf16 halves, and three products (hi hi, hi lo, lo hi) keep
-//       2^-16 of each factor: a score is exponentiated, so its error must not
-//       grow with the size of the scores
+//   S = Q K'^T (128 x 64, fp32)   K' = (code s + z) R C 2^-k, its largest value
+//       at most 2^15, and Q (scaled likewise, a row at a time) are each split
+//       into two fp16 halves, and three products (hi hi, hi lo, lo hi) keep
+//       2^-22 of each factor: a score is exponentiated, so its error must not
+//       grow with the size of the scores (with bf16 halves it was 2^-16 of
+//       sum |q k|). The exponents go into the scale of the scores.
 //   P = 2^(S - m), O += P V'      P and V' are each split into two fp16 halves,
 //       three products (2^-22): V' is (code s + z) R C 2^-e, the tile's exponent
 //       e making its largest value at most 2^15, so that the low halves of
@@ -56,7 +58,8 @@ constexpr int kBuildWarps = 8;
 static_assert(kMaxRaw + 2 <= 8, "exponents in flight");
 static_assert(2 * kPkV == kD * kD * 2, "the rotation matrix fits V's first stage");
 constexpr float kLift = 7.f;                     // P up to 2^(8 + 7), small weights normal down to 2^-21
-constexpr int kTopExp = 15;                      // V' up to 2^15: halves of small values stay normal
+constexpr int kTopExp = 15;                      // K' and V' up to 2^15: halves of small values stay normal
+constexpr int kTopQuery = 11;                    // the query's channels up to 2^11, rotated up to sqrt(128) times that
 
 struct PackedSmem {
     // ready: a raw tile's exponent is known; raw_empty: its operands are built
@@ -64,9 +67,10 @@ struct PackedSmem {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], q_done, drained;
     uint32_t tmem;
     int stop;
-    // e of the last tiles: the raw tiles' warp is at most kMaxRaw tiles ahead of
+    // the exponents of the last tiles: the raw tiles' warp is at most kMaxRaw tiles ahead of
     // the V' that is built, which is at most two ahead of the softmax that reads e
-    int vexp[8];
+    int kexp[8], vexp[8];
+    int16_t qexp[2 * kPRows];   // of the query rows
 };
 
 template <int B, int BITS, int NT>   // NT: row tiles of a CTA
@@ -169,12 +173,13 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
     if (warp == kSoft + 1)
         for (; fetched < kRawStages - 1 && fetched < n; ++fetched) fetch(fetched);
 
-    // ---- the query rows: their rotation H (sigma q) / sqrt(128) is itself a
-    // product on the tensor core, exact in its operands (signs, and q in bf16,
-    // or as two bf16 halves of an fp32 one); without rotation H is the identity.
-    // Then the rows are split into two bf16 halves: the high one to tensor
-    // memory, the low one to its operand. (A row a warp or a thread through
-    // butterflies took 7-14 us of a call.)
+    // ---- the query rows: each is scaled by the power of two that brings its
+    // largest channel to 2^11; their rotation H (sigma q) / sqrt(128) is itself a
+    // product on the tensor core, of signs and of q in fp16 (a bf16 one is exact
+    // down to 2^-25 of the largest) or, for an fp32 one, of its two fp16 halves;
+    // without rotation H is the identity. Then the rows are split into two fp16
+    // halves: the high one to tensor memory, the low one to its operand. (A row a
+    // warp or a thread through butterflies took 7-14 us of a call.)
     const bool q32 = a.q_dtype == KVARN_FP32, rotate = !(a.flags & KVARN_FLAG_NO_ROTATION);
     {
         constexpr int kBatch = 4;
@@ -198,8 +203,8 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int c = 8 * u + 2 * k;
-                        w[k] = rotate ? 0x3f803f80u ^ (__popc(r & c) & 1) << 15 ^ (uint32_t)(__popc(r & (c + 1)) & 1) << 31
-                                      : (r == c ? 0x3f80u : 0u) | (r == c + 1 ? 0x3f800000u : 0u);
+                        w[k] = rotate ? 0x3c003c00u ^ (__popc(r & c) & 1) << 15 ^ (uint32_t)(__popc(r & (c + 1)) & 1) << 31
+                                      : (r == c ? 0x3c00u : 0u) | (r == c + 1 ? 0x3c000000u : 0u);
                     }
                     *reinterpret_cast<uint4*>(v_op + (u >> 3) * (kPkQ / 2) + swizzled(r, u & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
@@ -208,16 +213,30 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                 const int i = i0 + j * Lay::kThreads, r = i >> 4, u = i & 15;
                 if (i >= NT * kPRows * 16) break;
                 uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w}, lo[4];
+                float f[8];
                 if (q32) {
-                    const uint32_t f[8] = {x[j].x, x[j].y, x[j].z, x[j].w, y[j].x, y[j].y, y[j].z, y[j].w};
+                    const uint32_t u8[8] = {w[0], w[1], w[2], w[3], y[j].x, y[j].y, y[j].z, y[j].w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(u8[k]);
+                } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float f0 = __uint_as_float(f[2 * k]), f1 = __uint_as_float(f[2 * k + 1]);
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(f0, f1);
-                        w[k] = *reinterpret_cast<const uint32_t*>(&b);
-                        const __nv_bfloat162 c = __floats2bfloat162_rn(minus_bf16(w[k], f0, false), minus_bf16(w[k], f1, true));
-                        lo[k] = *reinterpret_cast<const uint32_t*>(&c);
+                        f[2 * k] = __uint_as_float(w[k] << 16);
+                        f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
                     }
+                }
+                float big = 0.f;                                         // (a row: 16 lanes next to one another)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(f[k]));
+#pragma unroll
+                for (int m = 8; m >= 1; m >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, m));
+                const int e = big > 0x1p-100f ? ceil_log2(big) : -100;
+                if (u == 0) s.qexp[r] = (int16_t)e;
+                const float up = exp2i(kTopQuery - e);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (q32) split_pair<true>(f[2 * k] * up, f[2 * k + 1] * up, w[k], lo[k]);
+                    else w[k] = pack_h2(f[2 * k] * up, f[2 * k + 1] * up);
                 }
                 const uint32_t sg = rotate ? sign_word(a.sb[0], a.sb[1], a.sb[2], a.sb[3], u >> 2) >> (8 * (u & 3)) : 0u;
                 const uint32_t at = (r / kPRows) * kPkQ + (u >> 3) * (kPkQ / 2) + swizzled(r % kPRows, u & 7);
@@ -236,7 +255,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
     __syncthreads();
     if (warp <= kSoft) {
         if (warp == kSoft) {
-            constexpr uint32_t kRot = mma_shape(kMmaBf16, kD, false);
+            constexpr uint32_t kRot = mma_shape(kMmaF16, kD, false);
             const uint32_t q_desc = smem_operand(smem_addr(q_lo), 16), l_desc = smem_operand(smem_addr(k_op), 16);
             const uint32_t h_desc = smem_operand(smem_addr(v_op), 16);
 #pragma unroll 1
@@ -264,11 +283,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float x0 = __uint_as_float(v[8 * u + 2 * k]) * norm, x1 = __uint_as_float(v[8 * u + 2 * k + 1]) * norm;
-                        const __nv_bfloat162 x = __floats2bfloat162_rn(x0, x1);
-                        const uint32_t hi = *reinterpret_cast<const uint32_t*>(&x);
-                        const __nv_bfloat162 y = __floats2bfloat162_rn(minus_bf16(hi, x0, false), minus_bf16(hi, x1, true));
-                        lo[k] = *reinterpret_cast<const uint32_t*>(&y);
-                        v[4 * u + k] = hi;
+                        split_pair<true>(x0, x1, v[4 * u + k], lo[k]);
                     }
                     *reinterpret_cast<uint4*>(lo_row + (c >> 1) * (kPkQ / 2) + swizzled((warp & 3) * 32 + lane, 4 * (c & 1) + u)) =
                         make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -297,38 +312,44 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
             const int st = i % kRawStages;
             ok = ok && warp_wait_or_stop(&s.raw_full[st], (i / kRawStages) & 1, stop, kWaitLimit);
             if (!ok) break;
-            // 2^e over the tile's values: the largest (|zero|, |top level|) R
-            // times the largest C (a lane: 8 (group, token) pairs, 4 or 8 channels)
+            // 2^e over the tile's keys and over its values: the largest (|zero|, |top
+            // level|) R times the largest C (a lane: 8 (group, token) pairs, 4 or 8 channels)
             constexpr int kPer = 32 / Lay::kBlocks;                // lanes per block
             const int x = lane / kPer, at = 8 * (lane % kPer);
-            float vmax = 0.f, cmax = 0.f;
-            if ((t_beg + i) * Lay::kBlocks + x < used) {
-                const uint8_t* hb = raw + st * Lay::kRaw + x * 2 * Lay::HB + Lay::HB;
-                const uint4 su = *reinterpret_cast<const uint4*>(hb + off_s(B, BITS) + 2 * at);
-                const uint4 zu = *reinterpret_cast<const uint4*>(hb + off_z(B, BITS) + 2 * at);
-                const uint4 ru = *reinterpret_cast<const uint4*>(hb + off_R(B, BITS) + 2 * (at % B));
-                const uint32_t sw[4] = {su.x, su.y, su.z, su.w}, zw[4] = {zu.x, zu.y, zu.z, zu.w}, rw[4] = {ru.x, ru.y, ru.z, ru.w};
-                constexpr float kTop = (float)((1 << BITS) - 1);
+            const bool there = (t_beg + i) * Lay::kBlocks + x < used;
+            auto exponent = [&](const uint8_t* hb) {
+                float vmax = 0.f, cmax = 0.f;
+                if (there) {
+                    const uint4 su = *reinterpret_cast<const uint4*>(hb + off_s(B, BITS) + 2 * at);
+                    const uint4 zu = *reinterpret_cast<const uint4*>(hb + off_z(B, BITS) + 2 * at);
+                    const uint4 ru = *reinterpret_cast<const uint4*>(hb + off_R(B, BITS) + 2 * (at % B));
+                    const uint32_t sw[4] = {su.x, su.y, su.z, su.w}, zw[4] = {zu.x, zu.y, zu.z, zu.w}, rw[4] = {ru.x, ru.y, ru.z, ru.w};
+                    constexpr float kTop = (float)((1 << BITS) - 1);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 sf = __half22float2(u32_as_h2(sw[k])), zf = __half22float2(u32_as_h2(zw[k]));
-                    const float2 rf = __half22float2(u32_as_h2(rw[k]));
-                    vmax = fmaxf(vmax, fmaxf(fabsf(zf.x), fabsf(fmaf(sf.x, kTop, zf.x))) * fabsf(rf.x));
-                    vmax = fmaxf(vmax, fmaxf(fabsf(zf.y), fabsf(fmaf(sf.y, kTop, zf.y))) * fabsf(rf.y));
-                }
-                constexpr int kCh = kD / kPer;
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 sf = __half22float2(u32_as_h2(sw[k])), zf = __half22float2(u32_as_h2(zw[k]));
+                        const float2 rf = __half22float2(u32_as_h2(rw[k]));
+                        vmax = fmaxf(vmax, fmaxf(fabsf(zf.x), fabsf(fmaf(sf.x, kTop, zf.x))) * fabsf(rf.x));
+                        vmax = fmaxf(vmax, fmaxf(fabsf(zf.y), fabsf(fmaf(sf.y, kTop, zf.y))) * fabsf(rf.y));
+                    }
+                    constexpr int kCh = kD / kPer;
 #pragma unroll
-                for (int k = 0; k < kCh; k += 2) {
-                    const float2 cf = __half22float2(
-                        u32_as_h2(*reinterpret_cast<const uint32_t*>(hb + off_C(B, BITS) + 2 * (kCh * (lane % kPer) + k))));
-                    cmax = fmaxf(cmax, fmaxf(fabsf(cf.x), fabsf(cf.y)));
+                    for (int k = 0; k < kCh; k += 2) {
+                        const float2 cf = __half22float2(
+                            u32_as_h2(*reinterpret_cast<const uint32_t*>(hb + off_C(B, BITS) + 2 * (kCh * (lane % kPer) + k))));
+                        cmax = fmaxf(cmax, fmaxf(fabsf(cf.x), fabsf(cf.y)));
+                    }
                 }
-            }
-            const float bound = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vmax))) *
-                                __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(cmax)));
-            // the clamps keep 2^-e and 2^e finite
+                const float bound = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vmax))) *
+                                    __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(cmax)));
+                // (the clamps keep 2^-e and 2^e finite)
+                return (bound > 0x1p-60f ? min(ceil_log2(bound), 100) : -60) - kTopExp;
+            };
+            const uint8_t* hb = raw + st * Lay::kRaw + x * 2 * Lay::HB;
+            const int ke = exponent(hb), ve = exponent(hb + Lay::HB);
             if (lane == 0) {
-                s.vexp[i & 7] = (bound > 0x1p-60f ? min(ceil_log2(bound), 100) : -60) - kTopExp;
+                s.kexp[i & 7] = ke;
+                s.vexp[i & 7] = ve;
                 mbar_arrive(&s.ready[st]);
             }
         }
@@ -380,11 +401,12 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                 if (i == 0 && q32) ok = warp_wait_or_stop(&s.q_done, 0, stop, kWaitLimit);   // (the query's low half was here)
                 if (!ok) break;
                 uint8_t* dst = k_op + par * 2 * kPkK + (g >> 1) * (kPkK / 2);
+                const float up = kUp * exp2i(-*reinterpret_cast<volatile int*>(&s.kexp[i & 7]));
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t step = k < 2 ? su.x : su.y;
                     const float2 z2 = __half22float2(u32_as_h2(k < 2 ? zu.x : zu.y)), r2 = __half22float2(u32_as_h2(k < 2 ? ru.x : ru.y));
-                    const float zero = ((k & 1) ? z2.y : z2.x) * kCodeScale, fac = ((k & 1) ? r2.y : r2.x) * kUp;
+                    const float zero = ((k & 1) ? z2.y : z2.x) * kCodeScale, fac = ((k & 1) ? r2.y : r2.x) * up;
                     const uint32_t w8 = w[k] >> 8;
                     uint32_t hi[4], lo[4];
 #pragma unroll
@@ -392,10 +414,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
                         const uint32_t f = code_pair<BITS>(w[k], w8, hw[k], p, p);
                         float2 y = make_float2(fma_half(f, step, zero, false, k & 1), fma_half(f, step, zero, true, k & 1));
                         y = __fmul2_rn(__fmul2_rn(y, make_float2(fac, fac)), cc[p]);
-                        const __nv_bfloat162 yh = __floats2bfloat162_rn(y.x, y.y);
-                        hi[p] = *reinterpret_cast<const uint32_t*>(&yh);
-                        const __nv_bfloat162 yl = __floats2bfloat162_rn(minus_bf16(hi[p], y.x, false), minus_bf16(hi[p], y.y, true));
-                        lo[p] = *reinterpret_cast<const uint32_t*>(&yl);
+                        split_pair<true>(y.x, y.y, hi[p], lo[p]);
                     }
                     const uint32_t at = swizzled(32 * sb + 4 * ra + k, 4 * (g & 1) + rb);
                     // (an absent half's scores are masked, whatever its raw bytes were)
@@ -464,7 +483,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
     } else if (warp == kSoft) {
         // ---------------------------------------------------------- products
         if (steps > 0) {
-            constexpr uint32_t kQk = mma_shape(kMmaBf16, kPkTok, false), kPv = mma_shape(kMmaF16, kD, false);
+            constexpr uint32_t kQk = mma_shape(kMmaF16, kPkTok, false), kPv = mma_shape(kMmaF16, kD, false);
             const uint32_t q_desc = smem_operand(smem_addr(q_lo), 16), k_desc = smem_operand(smem_addr(k_op), 16);
             const uint32_t v_desc = smem_operand(smem_addr(v_op), 16);
             bool ok = !(a.flags & KVARN_FLAG_TEST_WAIT_TIMEOUT);
@@ -512,7 +531,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
         const int len = row < R ? prefix_len(a.lens, row / a.G, max_len) : 0;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t my_o = tm_o + 128 * x + lanes;
-        const float scale = a.sm_scale * kLog2e;
+        const float scale = a.sm_scale * kLog2e * exp2i(s.qexp[warp * 32 + lane] - kTopQuery);
         RowState st{-INFINITY, 0.f};
         bool ok = true;
         for (int i = 0; i < n && ok; ++i) {                       // tile
@@ -521,7 +540,9 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
             if (!ok) break;
             tc_fence_after();
             const int e = *reinterpret_cast<volatile int*>(&s.vexp[i & 7]);
-            ok = softmax_tile<kPkTok, NT == 2 ? 32 : 64, true>(tm_s + 64 * w + lanes, my_o, len - (t_beg + i) * kPkTok, scale, (float)e,
+            // (finite and not 0, so that what is masked stays masked)
+            const float here = fminf(fmaxf(scale * exp2i(*reinterpret_cast<volatile int*>(&s.kexp[i & 7])), 0x1p-126f), 0x1p127f);
+            ok = softmax_tile<kPkTok, NT == 2 ? 32 : 64, true>(tm_s + 64 * w + lanes, my_o, len - (t_beg + i) * kPkTok, here, (float)e,
                                                         exp2i(-e), kLift, i == 0, st, &s.p_ready[w], [&] {
                 // O is idle once the last product into it has completed: with two row
                 // tiles S came behind it, with one it has freed tile i - 1's V stage

@@ -102,3 +102,17 @@ def test_weights_and_values_over_the_packed_cache(kvlib, case, bits):
     q = (0.01 * synth.queries(synth.make_gen(50 + case), batch, n_q)).to(qdt).cuda()
     # (a weight and a value as fp16 pairs: 2^-22 each and the product of the low halves)
     _check(s, q, [P] * batch, 3 * 2.0 ** -22, 3 * 2.0 ** -16 + 2.0 ** -17)
+
+
+@pytest.mark.parametrize("bits,B,batch", [(2, 32, 6), (3, 64, 40), (4, 32, 40), (4, 64, 6)])
+@pytest.mark.parametrize("qdt", [torch.float32, torch.bfloat16])
+def test_scores_over_the_packed_cache(kvlib, bits, B, batch, qdt):
+    """Scores of one product each (queries of one channel, no rotation) and up to 60: no sum hides what the halves of a
+    key and of a query leave out. As fp16 pairs that is 2^-22 each and the product of the low halves; 2^-22 for the
+    exponent's product and sum."""
+    P = 96
+    s = Shared(kvlib, 100 + bits, P, [0] * batch, 8, 2, B, bits, flags=kvlib.FLAG_NO_ROTATION, small=1)
+    g = torch.Generator().manual_seed(bits)
+    q = torch.zeros(batch, 8, D)
+    q.scatter_(2, torch.randint(0, D, (batch, 8, 1), generator=g), 150 * (1 + torch.rand(batch, 8, 1, generator=g)))
+    _check(s, q.to(qdt).cuda(), [P] * batch, 3 * 2.0 ** -22, 2.0 ** -20)
