@@ -761,7 +761,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 1) prefix_join_packed_kernel(
     float mo = -INFINITY, lo = 0.f, ao[4] = {0.f, 0.f, 0.f, 0.f};
     combine_slices(reinterpret_cast<const float*>(smem + kResult) + g * kPartialStride, kJoinWarps, lane, mo, lo, ao, kWarp / 4);
     add_slice(m, l, acc, mo, lo, ao);
-    finish_row<true>(a, pm, (int64_t)b * a.n_q + h * a.G + g, ntail > 0 ? &tails[g][0][0] : nullptr, lane, m, l, acc);
+    finish_row<true>(a, pm, (int64_t)b * a.n_q + h * a.G + g, L > 0 || PL > 0, ntail > 0 ? &tails[g][0][0] : nullptr, lane, m, l,
+                     acc);
 }
 
 // ---------------------------------------------------------------- host side

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnA
     if (g >= a.G || part != 0) return;
     float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     combine_slices(&slices[wp][0], parts, lane, m, l, acc);
-    finish_row<ROT>(a, pm, (int64_t)b * a.n_q + h * a.G + g, ntail > 0 ? &tails[g][0][0] : nullptr, lane, m, l, acc);
+    finish_row<ROT>(a, pm, (int64_t)b * a.n_q + h * a.G + g, L > 0 || PL > 0, ntail > 0 ? &tails[g][0][0] : nullptr, lane, m, l, acc);
 }
 
 // ---------------------------------------------------------------- own tokens and merge in one (bf16 pages)
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) prefix_join_kernel(AttnArgs a,
     float mo = -INFINITY, lo = 0.f, ao[4] = {0.f, 0.f, 0.f, 0.f};
     combine_slices(&own[g][0][0], W, lane, mo, lo, ao);
     add_slice(m, l, acc, mo, lo, ao);
-    finish_row<false>(a, pm, gw, nullptr, lane, m, l, acc);
+    finish_row<false>(a, pm, gw, L > 0 || PL > 0, nullptr, lane, m, l, acc);
 }
 
 // ---------------------------------------------------------------- host side

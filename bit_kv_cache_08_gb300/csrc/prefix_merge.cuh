@@ -68,7 +68,7 @@ __device__ __forceinline__ void add_slice(float& m, float& l, float (&acc)[4], f
 }
 
 __device__ __forceinline__ void store_out(const PrefixMerge& pm, int64_t row, int lane, float l, float (&acc)[4]) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l > 0.f ? 1.f / l : l;   // (0 for no token at all; NaN stays)
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[k] *= inv;
     if (pm.out_bf16) {
@@ -274,10 +274,11 @@ __device__ __forceinline__ void tail_slice16(const AttnArgs& a, int b, int h, in
 
 // A row's merged result (own and prefix tokens) rotated back (ROT), joined
 // with its four tail slices (nullptr: no tail)
-// and stored.
+// and stored. Maxima drop NaN, so a row of tokens (any) without a score above
+// -inf is one whose scores are NaN, or all -inf: its softmax is NaN.
 template <bool ROT>
-__device__ __forceinline__ void finish_row(const AttnArgs& a, const PrefixMerge& pm, int64_t row, const float* tails, int lane,
-                                           float m, float l, float (&acc)[4]) {
+__device__ __forceinline__ void finish_row(const AttnArgs& a, const PrefixMerge& pm, int64_t row, bool any, const float* tails,
+                                           int lane, float m, float l, float (&acc)[4]) {
     if (ROT && !(a.flags & KVARN_FLAG_NO_ROTATION)) {
         fwht128(acc, lane);
 #pragma unroll
@@ -288,6 +289,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, const PrefixMerge&
         combine_slices(tails, 4, lane, mt, lt, at);
         add_slice(m, l, acc, mt, lt, at);
     }
+    if (any && m == -INFINITY) l = NAN;
     store_out(pm, row, lane, l, acc);
 }
 

@@ -410,7 +410,7 @@ size_t kvarn_prefix_workspace_bytes(const kvarn_config* cfg, int32_t batch, int3
  * kvarn_decode_attn, their indices starting at 0.
  *   out[b][j][:] = sum_t softmax_t(sm_scale * q.k_t) v_t
  * over the prefix's tokens and the own ones together; no token at all gives
- * zeros. out: device [batch][n_q][128], out_dtype KVARN_BF16 or KVARN_FP32.
+ * zeros, and a query that is not finite NaN (the other rows keep theirs). out: device [batch][n_q][128], out_dtype KVARN_BF16 or KVARN_FP32.
  * workspace: at least kvarn_prefix_workspace_bytes(cfg, batch, prefix_blocks)
  * bytes, 16-byte aligned; calls that may overlap need one each. A prefix block
  * quantised from values that were not finite (flagged when it was written)
