@@ -332,6 +332,20 @@ int check_rope(const kvarn_rope* r) {
     return KVARN_OK;
 }
 
+// The fraction of rate / (2 pi) in units of 2^-64, to the nearest: 1 / (2 pi)
+// as the sum of two doubles (a relative 2^-108), its product with the rate as
+// the rounded one with the first, that one's exact remainder and the small one
+// with the second, so that whole turns of a large rate take no bits of the rest.
+uint64_t turns_of(double rate) {
+    // (volatile: the product is rounded before the remainder, on every host)
+    const volatile double turns = rate * 0x1.45f306dc9c883p-3;
+    const double rest = fma(rate, 0x1.45f306dc9c883p-3, -turns) - rate * 0x1.6b01ec5417056p-57;
+    const double f = turns - floor(turns);                                 // exact, in [0, 1)
+    const double hi = floor(f * 0x1p32), lo = (f * 0x1p32 - hi) * 0x1p32;   // exact
+    // (rest is below 2^-35 of a turn; the sum wraps at a whole one)
+    return ((uint64_t)hi << 32) + (uint64_t)(int64_t)floor(lo + rest * 0x1p64 + 0.5);
+}
+
 // Everything but the cache's own buffers; fills the kernels' arguments.
 int check_append(const kvarn_config* cfg, const kvarn_rope* rope, void* pool, int64_t n_pool_blocks,
                  const int32_t* block_table, int32_t max_blocks, const int32_t* pos, const int32_t* rope_pos,
@@ -402,12 +416,8 @@ int kvarn_rope_init(kvarn_rope* rope, int32_t rotary_dim, int32_t layout, const 
     if (rotary_dim > 0 && !inv_freq) return KVARN_ERR_INVALID_ARG;
     for (int i = 0; i < rotary_dim / 2; ++i) {
         if (!(fabs(inv_freq[i]) <= 1048576.0)) return KVARN_ERR_INVALID_ARG;
-        // (volatile: the product is rounded before the difference, on every host)
-        const volatile double turns = inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi): per position
-        const double f = turns - floor(turns);                                // exact, in [0, 1]
-        // high and low halves: each product and difference below is exact
-        const double hi = floor(f * 0x1p32), lo = (f * 0x1p32 - hi) * 0x1p32;
-        r.turns[i] = ((uint64_t)hi << 32) + (uint64_t)floor(lo + 0.5);   // (a whole turn wraps to 0)
+        r.turns[i] = turns_of(fabs(inv_freq[i]));
+        if (inv_freq[i] < 0) r.turns[i] = 0 - r.turns[i];
     }
     *rope = r;
     return KVARN_OK;

@@ -10,9 +10,10 @@
 // leaves an error of 0.06 rad), so a rate is kept as the fraction of a turn
 // per position in units of 2^-64: an integer product then wraps at whole
 // turns by itself and its top 32 bits are the angle to 2^-32 of a turn,
-// whatever the position. The error of the angle is |position| * 2^-54 turns
-// from the rate's own rounding plus 2^-25 turns from the conversion to fp32
-// (at half a turn; relative below), below sincospif's own.
+// whatever the position. The rate is exact to half a unit whatever its size, so
+// the error of the angle is |position| * 2^-65 turns (2^-34 at the ends of 32
+// bits), 2^-32 from the cut, and 2^-25 from the conversion to fp32 (at half a
+// turn; relative below), which is below sincospif's own.
 #pragma once
 #include "common.cuh"
 
