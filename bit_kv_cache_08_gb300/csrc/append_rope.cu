@@ -80,9 +80,16 @@ __device__ __forceinline__ void store_q(const RopeAppendArgs& a, int64_t row, co
     }
 }
 
+// A ragged sequence whose tokens cannot all be placed: offsets that descend or
+// leave the token rows, or tokens beyond the block table. None of them is.
+__device__ __forceinline__ bool bad_sequence(const RopeAppendArgs& a, int b, int64_t capacity) {
+    const int64_t c0 = a.cu[b], c1 = a.cu[b + 1], p = a.pos[b];
+    return c0 < 0 || c1 < c0 || c1 > a.n_tokens || (c1 > c0 && (p < 0 || p + (c1 - c0) > capacity));
+}
+
 // The sequence of token row t: the number of ends cu[1 .. batch] at or before
 // t, counted by the warp (32-way search, then one round over what is left).
-// -1 for a row behind the last sequence; -2 where cu is not ascending around t.
+// -1 for a row outside every sequence (also where offsets around it descend).
 __device__ __forceinline__ int sequence_of(const RopeAppendArgs& a, int64_t t, int lane) {
     if (!a.cu) return (int)t;
     int lo = 0, n = a.batch;   // ends lo + 1 .. lo + n are undecided
@@ -98,7 +105,7 @@ __device__ __forceinline__ int sequence_of(const RopeAppendArgs& a, int64_t t, i
     const int b = lo + __popc(__ballot_sync(kFull, passed));
     if (b >= a.batch) return -1;
     const int c0 = a.cu[b];
-    return c0 >= 0 && c0 <= t && t < a.cu[b + 1] ? b : -2;
+    return c0 >= 0 && c0 <= t && t < a.cu[b + 1] ? b : -1;
 }
 
 // ---------------------------------------------------------------- bf16 pages
@@ -115,16 +122,18 @@ __global__ void __launch_bounds__(128) append_rope_bf16_kernel(RopeAppendArgs a,
     const int lane = threadIdx.x & 31;
     // (items and heads * runs stay below 2^32: the host's bounds)
     const uint32_t item = blockIdx.x * 4 + (threadIdx.x >> 5), run = runs == 1 ? 0u : item % runs;
-    const int64_t t = runs == 1 ? item : item / runs;
+    const int64_t t = runs == 1 ? item : item / runs, capacity = (int64_t)a.max_blocks * B;
+    if (a.cu)   // the grid's threads look at every sequence, with rows here or not
+        for (int64_t x = blockIdx.x * 128ll + threadIdx.x; x < a.batch; x += gridDim.x * 128ll)
+            if (bad_sequence(a, (int)x, capacity)) raise_error(a.err, KVARN_DEVERR_POSITION);
     if (t >= a.n_tokens) return;
     const int b = sequence_of(a, t, lane);
-    if (b < 0) {
-        if (b == -2 && lane == 0) raise_error(a.err, KVARN_DEVERR_POSITION);
-        return;
-    }
+    if (b < 0) return;
     const int64_t i = a.cu ? t - a.cu[b] : 0;
     const int64_t at = (int64_t)a.pos[b] + i;
-    if (a.pos[b] < 0 || at >= (int64_t)a.max_blocks * B) {
+    if (a.cu) {
+        if (bad_sequence(a, b, capacity)) return;
+    } else if (a.pos[b] < 0 || at >= capacity) {
         if (lane == 0) raise_error(a.err, KVARN_DEVERR_POSITION);
         return;
     }
@@ -189,7 +198,7 @@ __device__ __forceinline__ int unit_of(const RopeAppendArgs& a, int64_t u, int l
         bool wrong = false;
         if (b < a.batch) {
             const int64_t c0 = a.cu[b], c1 = a.cu[b + 1], p = a.pos[b];
-            wrong = c0 < 0 || c1 < c0 || c1 > a.n_tokens || (c1 > c0 && (p < 0 || p + (c1 - c0) > (int64_t)a.max_blocks * B));
+            wrong = bad_sequence(a, b, (int64_t)a.max_blocks * B);
             if (!wrong && c1 > c0) n = (p + (c1 - c0) - 1) / B - p / B + 1;
         }
         bad |= __any_sync(kFull, wrong);

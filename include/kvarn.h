@@ -274,7 +274,8 @@ int kvarn_rope_init(kvarn_rope* rope, int32_t rotary_dim, int32_t layout, const 
  * rows are left as they are): the pool then holds the bytes that kvarn_append
  * would have written token by token. Device faults: KVARN_DEVERR_POSITION
  * (pos < 0, a token beyond the block table, cu_tokens not ascending or beyond
- * n_tokens), KVARN_DEVERR_BLOCK_ID, KVARN_DEVERR_NONFINITE.
+ * n_tokens: nothing of that sequence is written, its q_out rows neither),
+ * KVARN_DEVERR_BLOCK_ID, KVARN_DEVERR_NONFINITE.
  */
 int kvarn_append_rope(const kvarn_config* cfg, const kvarn_rope* rope, void* pool, int64_t n_pool_blocks,
                       void* staging, const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* pos,
@@ -286,8 +287,8 @@ int kvarn_append_rope(const kvarn_config* cfg, const kvarn_rope* rope, void* poo
 /*
  * kvarn_append_rope_bf16 -- the same into the plain bf16 pages of
  * kvarn_decode_attn_bf16 (kv_pool: bf16 [n_pool_blocks][n_kv][2][B][128]):
- * every token goes to its row of its page. workspace: >= 256 bytes, for the
- * error word.
+ * every token goes to its row of its page. Device faults as there, without
+ * KVARN_DEVERR_NONFINITE. workspace: >= 256 bytes, for the error word.
  */
 int kvarn_append_rope_bf16(const kvarn_config* cfg, const kvarn_rope* rope, void* kv_pool, int64_t n_pool_blocks,
                            const int32_t* block_table, int32_t max_blocks_per_seq, const int32_t* pos,
