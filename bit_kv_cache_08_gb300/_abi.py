@@ -307,6 +307,9 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: str = "no
     "bands"   per pair, by its turns within original_ctx: divided by factor below `low` turns, kept above
               `high`, a blend linear in the number of turns between
     "yarn"    the same with cos and sin times 0.1 ln(factor) + 1 (Peng et al. 2023, "YaRN")
+
+    "yarn" blends by a pair's turns, as the paper writes it. A model trained with a blend linear in the pair's index
+    (between the pairs of `high` and of `low` turns) has other rates in between: give make_rope that model's own.
     """
     if rotary_dim < 2 or rotary_dim % 2 or not theta > 0 or not factor >= 1.0:
         raise ValueError("rotary_dim must be even and positive, theta positive, factor at least 1")
