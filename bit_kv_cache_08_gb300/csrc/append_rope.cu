@@ -17,9 +17,10 @@
 // rows (805 MB) into bf16 pages take 128 us, 0.93 of the measured copy
 // bandwidth, with 4 rows a half-warp in flight (with 2 and 1 it took 10 and 60
 // us more); with few rows a token its lookups and angles weigh more (12 rows:
-// 50 us for 201 MB). A decode step of 64 tokens takes 4 us as a graph node, into
-// the packed cache 8 (a CTA per kv head and kind, which quantises where the
-// token completes its block).
+// 50 us for 201 MB). A decode step of 64 tokens takes 5 us as a graph node, into
+// the packed cache 8 where no token completes its block, 14 where one does and
+// 36 where all do (2 bits, 1024 head-blocks; a CTA per kv head and kind, which
+// quantises then). 32 760 prompt tokens into the packed cache take 526 us.
 #include "attn_common.cuh"
 #include "host_checks.h"
 #include "quantize.cuh"

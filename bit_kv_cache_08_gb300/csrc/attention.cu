@@ -722,10 +722,12 @@ constexpr int stages_for() { return 2; }
 // when the prefix kernel is through, the merge with the prefix's partials and
 // the rotation back. Where a CTA per SM holds all units, this saves a launch
 // and the own results' way through memory, and on SMs that the prefix kernel
-// leaves free it runs beside it: 4 sequences of up to 64 / 1024 own tokens
-// behind 4096 of a prefix, 8 kv heads, 2-bit, as a graph: 18.5 / 26.2 us
-// against 22.2 / 29.5 with the split kernel and a merge; bound by the latency
-// of the prefix kernel and then of the partials' loads.
+// leaves free it runs beside it. Calls at 2 bits, 8 kv heads, as graph nodes, of
+// up to 64 / 512 / 2048 own tokens against the split kernel and a merge: 4
+// sequences behind 4096 of a prefix 20 / 26 / 33 us against 22 / 23 / 34, behind
+// 16 384 43 / 47 / 54 against 45 / 52 / 56; 16 sequences behind 4096 21 / 27 / 34
+// against 24 / 32 / 39. Bound by the latency of the prefix kernel and then of the
+// partials' loads.
 constexpr int kJoinWarps = 8;
 template <int B, int BITS>
 __global__ void __launch_bounds__(32 * kJoinWarps, 1) prefix_join_packed_kernel(AttnArgs a, PrefixMerge pm) {

@@ -35,9 +35,9 @@ cudaError_t launch_prefix_packed(const kvarn_config& c, const PrefixArgs& p, cud
 // wait for nothing, then, when the split kernel is through, 4 / G warps to
 // each of the G query heads with a share of the row's partials; the row's first
 // warp combines the shares and finishes the row. On the tensor cores a tail row
-// costs a quarter of the instructions that it costs scored by a lane: calls
-// of 64 x 8192 at 2 bits and 128 x 32 768 at 4 went from 52 to 46 and from 185
-// to 180 us.
+// costs a quarter of the instructions that it costs scored by a lane, which
+// took 6 and 5 us off calls of 64 x 8192 at 2 bits and 128 x 32 768 at 4 (55 and
+// 210 us now; the kernel alone and cold 14 and 19).
 constexpr int kMergeWarps = 4;
 template <int B, bool ROT>
 __global__ void __launch_bounds__(32 * kMergeWarps, 4) prefix_merge_kernel(AttnArgs a, PrefixMerge pm) {
@@ -110,9 +110,11 @@ struct OwnChunks {
 // but a unit has only its CTA. Memory bounds it (512 bytes a token and kv
 // head) where the units fill the GPU, the chain of dependent loads where they
 // do not. A call of 64 sequences with 192 own tokens of 8 kv heads behind 8192
-// of a prefix takes 33 us with CTAs of 4 at 16 warps per SM (8 or 12 warps per SM
-// with the next chunk's loads in flight during a chunk's products: 45, 37; split
-// kernel and merge: 42), 128 with 384 behind 32 768 takes 106 (127, 105; 119).
+// of a prefix takes 32.6 us as a graph node with CTAs of 4 at 16 warps per SM and
+// 40.7 with the split kernel and a merge, 128 with 384 behind 32 768 take 118.0
+// and 127.2. (8 or 12 warps per SM with the next chunk's loads in flight during a
+// chunk's products took 12 and 4 us more for the first, 21 more and 1 less for the
+// second.)
 template <int B, int W>
 __global__ void __launch_bounds__(32 * W, 16 / W) prefix_join_kernel(AttnArgs a, PrefixMerge pm) {
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
@@ -165,11 +167,18 @@ PrefixPlan prefix_plan(const kvarn_config& c, int64_t batch, int64_t prefix_bloc
     else if (!packed) p.streams = 2;
     // The token ranges that make waves of CTAs times a CTA's tiles least: 3 tiles
     // stand for a CTA's start and end; of the ranges with the same tiles for a CTA
-    // the fewest, for there are as many partials (64 sequences behind 8192 tokens:
-    // 16 ranges 23.3 us, 19 24.2). More than one wave only where one would leave
-    // many SMs idle (1300 sequences behind 8000 tokens, 168 CTAs a range: one range
-    // 321 us, four waves at most 275; packed 654 and 520). Packed CTAs of one tile
-    // lost 3 us to twice the partials.
+    // the fewest, for there are as many partials. More than one wave only where one
+    // would leave many SMs idle. Calls with a few own tokens as graph nodes, 32
+    // query heads on 8 kv heads, us by ranges (* the plan's):
+    //   64 behind 8192     bf16  10: 28.6  13: 25.1  16*: 23.9  19: 24.8
+    //                      2-bit 13: 47.8  16: 43.5  19*: 41.5
+    //   128 behind 32 768  bf16   7: 97.1   8: 87.9   9*: 81.4  19: 92.9
+    //                      4-bit  7: 212    8: 188    9*: 171   19: 184
+    //   300 behind 8192    bf16   2: 94.0   3*: 73.4  4: 101    5: 90.3   8: 96.3
+    //                      2-bit  2: 195    3*: 145   4: 207    5: 177    8: 182
+    //   1300 behind 8000   bf16   1: 367    2: 314    3*: 306   4: 307
+    //                      2-bit  1: 742    2: 606    3*: 575   4: 568
+    // Packed CTAs of one tile lost 3 us to twice the partials.
     const int64_t units = c.n_kv_heads * ((R + p.rows - 1) / p.rows);
     const int64_t tile = packed ? 64 : 128, tiles = (prefix_blocks * c.block_size + tile - 1) / tile;
     const int64_t ranges = packed ? (tiles + 1) / 2 : tiles;
@@ -256,8 +265,9 @@ int prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const v
     // 4 sequences of up to 2048 / 4096 own tokens in bf16 pages, 8 kv heads, take
     // 28 / 38 us against 29 / 32 by the split kernel and a merge, 128 sequences
     // 169 / 310 against 181 / 325. Packed blocks need an SM's shared memory for a
-    // unit: with a CTA per SM 16 sequences take 21 .. 32 us against 23 .. 37 (up to
-    // 64 .. 2048 tokens; 4096: 39 against 41).
+    // unit: with a CTA per SM 16 sequences behind 4096 tokens take 21 .. 34 us
+    // against 24 .. 39 (up to 64 .. 2048 own tokens), 4 sequences 20 .. 33 against
+    // 22 .. 34, though 25 .. 28 against 22 .. 23 with 256 to 1024.
     const bool join = (int64_t)max_blocks * c.block_size <= kJoinTokens &&
                       (!PACKED || (int64_t)batch * c.n_kv_heads <= current_device_sms());
     if constexpr (PACKED) {

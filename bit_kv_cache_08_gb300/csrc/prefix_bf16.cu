@@ -28,16 +28,16 @@
 // two products, within 2^-16, as the decode attention does. (P rounded to one
 // bf16 value left errors of 2^-9 of sum p |v|, for 14 us of 119 at 128 x 32 768.)
 //
-// Measured (32 query heads on 8 kv heads, 128 channels): 512 rows a head
-// behind 32 768 tokens (69 GFLOP, 134 MB) in 66 us, 1.05 PFLOP/s, 0.55 of a
-// library bf16 product; 256 rows behind 8192 (34 MB) in 14 us of a call, 21
-// alone and cold. The tensor pipe is busy 52 % of the time and HBM a third: the
-// bound is a step's chain (product, softmax, product and the waits between),
-// of which two streams hide half. Timing stand-ins of the whole call (119.5 us
-// then): no exponentials 115.6, no softmax 109.5, an eighth of the products
-// 111, no pages after the first two tiles 119.3. A product warp for each stream
-// (124), half a row a thread (129), P in two halves (the same), S read twice in
-// fewer registers (131) and fewer token ranges (132) were slower or no faster.
+// Measured (32 query heads on 8 kv heads, 128 channels; alone and cold): 512
+// rows a head behind 32 768 tokens in 79 us; its products (34 GFLOP of scores,
+// 69 of the two halves of P) at 1.31 PFLOP/s, 0.69 of a library bf16 product;
+// 256 rows behind 8192 in 23. The tensor pipe is busy 64 % of the time and HBM
+// a quarter: the bound is a step's chain (product, softmax, products and the
+// waits between), of which two streams hide the larger part. Timing stand-ins
+// of a whole call, with P in one half (119.5 us then): no exponentials 115.6, no
+// softmax 109.5, an eighth of the products 111, no pages after the first two
+// tiles 119.3. A product warp for each stream (124), half a row a thread (129),
+// S read twice in fewer registers (131) and fewer token ranges (132) were slower.
 #include "prefix.cuh"
 
 #include <cuda.h>

@@ -30,18 +30,18 @@
 // operands without meeting at a barrier: one group's share of a record of the
 // packed format (K: 4 tokens x 8 channels, V: 8 tokens x 4 channels) is four
 // whole 16-byte units of the swizzled operand rows, so a lane reads a record's
-// words and writes units. Building costs about 3200 warp-instructions a tile,
-// a softmax tile 960; two row tiles share a build.
+// words and writes units. A build and the two softmax tiles that share it cost
+// about 10 700 warp-instructions.
 //
-// Measured (32 query heads on 8 kv heads): 512 rows a head behind 32 768
-// 4-bit tokens in 140 us, 256 rows behind 8192 2-bit tokens in 32 (alone and
-// cold), 20 behind 1111 in 13. Three score products and one of the values make
-// twice the operations of the bf16 kernel, 0.98 PFLOP/s of them; the tensor pipe
-// is busy 45 % of the time, the SM issues 48 %, HBM idles. As there, a step's
-// chain bounds it, not one unit. Timing stand-ins of the whole call (183.5 us
-// then): no softmax 174.6, a quarter of the building 170.2, one product in
-// eight 145.9. One row tile for more than 128 rows took 292 us (each tile
-// built twice), 16 builder warps gained nothing, half a row a thread 218.
+// Measured (32 query heads on 8 kv heads; alone and cold): 512 rows a head
+// behind 32 768 4-bit tokens in 187 us, 256 rows behind 8192 2-bit tokens in 40,
+// 20 behind 1111 in 17. Three products of the scores and three of the values make
+// 206 GFLOP of the first, 1.10 PFLOP/s; the tensor pipe is busy 54 % of the time,
+// the SM issues 47 %, HBM idles. As there, a step's chain bounds it, not one
+// unit. Timing stand-ins of a whole call, with one product of the values (183.5
+// us then): no softmax 174.6, a quarter of the building 170.2, one product in
+// eight 145.9. One row tile for more than 128 rows took 292 us (each tile built
+// twice), 16 builder warps gained nothing, half a row a thread 218.
 #include "prefix.cuh"
 
 #include "host_checks.h"
@@ -50,9 +50,9 @@
 namespace kvarn {
 
 constexpr int kPkTok = 64;                       // tokens of a tile
-constexpr int kPkK = kPkTok * kD * 2;            // bytes of one 64 x 128 bf16 operand (two 64-channel blocks)
+constexpr int kPkK = kPkTok * kD * 2;            // bytes of one 64 x 128 fp16 operand (two 64-channel blocks)
 constexpr int kPkV = kD * kPkTok * 2;            // 128 channel rows x 64 tokens, fp16
-constexpr int kPkQ = kPRows * kD * 2;            // 128 query rows, bf16
+constexpr int kPkQ = kPRows * kD * 2;            // 128 query rows, fp16
 constexpr int kMaxRaw = 4;                       // stages of raw tiles, at most
 constexpr int kBuildWarps = 8;
 static_assert(kMaxRaw + 2 <= 8, "exponents in flight");

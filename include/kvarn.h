@@ -430,10 +430,12 @@ int kvarn_prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, c
  * kvarn_decode_attn_bf16; the last page of the prefix may be partly filled,
  * and its rows behind the longest prefix_lens may hold anything. The values
  * before that must be finite even for sequences that do not see them (their
- * weight of 0 takes part in the product). Softmax weights of the prefix enter
- * the product as two bf16 halves, as in kvarn_decode_attn_bf16 (within 2^-16;
- * kvarn_prefix_attn: weights and values as two fp16 halves, within 2^-22, and
- * for values below 2^-18 of the largest of their 64 tokens within 2^-40 of it).
+ * weight of 0 takes part in the product). Softmax weights and an fp32 query
+ * enter the products as two bf16 halves, within 2^-16, as in
+ * kvarn_decode_attn_bf16. In kvarn_prefix_attn queries, keys, weights and values
+ * of blocks enter them as two fp16 halves, within 2^-22 (the prefix's keys and
+ * values below 2^-18 of the largest of their 64 tokens: within 2^-39 of that one),
+ * and weights and fp32 queries of the raw rows as two bf16 halves.
  */
 int kvarn_prefix_attn_bf16(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* kv_pool,
                            int64_t n_pool_blocks, const int32_t* prefix_table, int32_t prefix_blocks,
