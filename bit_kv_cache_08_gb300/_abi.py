@@ -27,6 +27,7 @@ BF16, FP32 = 0, 1
 KIND_K, KIND_V = 0, 1
 FLAG_NO_ROTATION, FLAG_NO_TOKEN_PASS, FLAG_NO_CHANNEL_PASS = 0x1, 0x2, 0x4
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+MAX_DRAFTS = 128
 FLAG_TEST_WAIT_TIMEOUT = 0x100   # test only: the decode kernel's first copy waits give up at once
 
 
@@ -96,6 +97,20 @@ _SIGS = {
                                          _i32, _vp, _sz, _vp]),
     "kvarn_prefix_attn_bf16": (ctypes.c_int, [_cfgp, _vp, _i32, _vp, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp,
                                               _i32, _vp, _sz, _vp]),
+    "kvarn_tree_workspace_bytes": (_sz, [_cfgp, _i32, _i32, _i32]),
+    "kvarn_tree_attn": (ctypes.c_int, [_cfgp, _vp, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _i64, _i64, _vp, _vp,
+                                       _i32, _i32, _vp, _i32, _vp, _sz, _vp]),
+    "kvarn_tree_attn_bf16": (ctypes.c_int, [_cfgp, _vp, _i32, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _i64, _i64, _vp, _vp,
+                                            _i32, _i32, _vp, _i32, _vp, _sz, _vp]),
+    "kvarn_weights_workspace_bytes": (_sz, [_cfgp, _i32, _i32]),
+    "kvarn_decode_attn_weights": (ctypes.c_int, [_cfgp, _vp, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp,
+                                                 _vp, _i64, ctypes.c_float, _vp, _sz, _vp]),
+    "kvarn_decode_attn_weights_bf16": (ctypes.c_int, [_cfgp, _vp, _i32, _vp, _i64, _vp, _i32, _vp, _i32, _vp, _i32, _vp,
+                                                      _vp, _i64, ctypes.c_float, _vp, _sz, _vp]),
+    "kvarn_evict": (ctypes.c_int, [_cfgp, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _i32, _i32, _vp, _i32, _vp, _vp, _i64,
+                                   _vp, _i32, _vp, _vp]),
+    "kvarn_evict_bf16": (ctypes.c_int, [_cfgp, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _i32, _i32, _vp, _i32, _vp, _vp,
+                                        _i64, _vp, _i32, _vp, _vp]),
     "kvarn_error_decomposition": (ctypes.c_int, [_cfgp, _i32, _vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
     "kvarn_read_error": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]),
     "kvarn_clear_error": (ctypes.c_int, [_vp, _vp]),
@@ -200,6 +215,28 @@ def alloc_prefix_workspace(cfg: Config, batch: int, prefix_blocks: int, device="
     n = prefix_workspace_bytes(cfg, batch, prefix_blocks)
     if n == 0:
         raise KVarNError(ERR_CUDA, "kvarn_prefix_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def tree_workspace_bytes(cfg: Config, batch: int, drafts: int, max_blocks_per_seq: int) -> int:
+    return int(lib().kvarn_tree_workspace_bytes(ctypes.byref(cfg), batch, drafts, max_blocks_per_seq))
+
+
+def alloc_tree_workspace(cfg: Config, batch: int, drafts: int, max_blocks_per_seq: int, device="cuda") -> torch.Tensor:
+    n = tree_workspace_bytes(cfg, batch, drafts, max_blocks_per_seq)
+    if n == 0:
+        raise KVarNError(ERR_CUDA, "kvarn_tree_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def weights_workspace_bytes(cfg: Config, batch: int, max_blocks_per_seq: int) -> int:
+    return int(lib().kvarn_weights_workspace_bytes(ctypes.byref(cfg), batch, max_blocks_per_seq))
+
+
+def alloc_weights_workspace(cfg: Config, batch: int, max_blocks_per_seq: int, device="cuda") -> torch.Tensor:
+    n = weights_workspace_bytes(cfg, batch, max_blocks_per_seq)
+    if n == 0:
+        raise KVarNError(ERR_CUDA, "kvarn_weights_workspace_bytes")
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
@@ -653,6 +690,286 @@ def prefix_attn_bf16(cfg: Config, q: torch.Tensor, kv_pool: torch.Tensor, prefix
     r = lib().kvarn_prefix_attn_bf16(ctypes.byref(cfg), q.data_ptr(), code, kv_pool.data_ptr(), kv_pool.shape[0], *rest)
     if r:
         _check(r, "kvarn_prefix_attn_bf16")
+
+
+def tree_mask(parents) -> torch.Tensor:
+    """The mask of tree_attn for trees of drafted tokens: parents [drafts] or
+    [batch][drafts] (whole numbers, host), the index of the draft that each one
+    continues, below its own, or -1 for the last cached token. Row r sees its
+    ancestors and itself: int32 [...][drafts][(drafts + 31) / 32] (host)."""
+    p = np.asarray(parents)
+    if p.ndim not in (1, 2) or not np.issubdtype(p.dtype, np.integer):
+        raise ValueError("parents must be [drafts] or [batch][drafts] whole numbers")
+    T = p.shape[-1]
+    if not 1 <= T <= MAX_DRAFTS:
+        raise ValueError(f"1 to {MAX_DRAFTS} drafts, got {T}")
+    rows = p.reshape(-1, T)
+    if (rows < -1).any() or (rows >= np.arange(T)).any():
+        raise ValueError("a draft's parent must be -1 or come before it")
+    every = np.arange(len(rows))
+    words = (T + 31) // 32
+    mask = np.zeros((len(rows), T, words), np.uint32)
+    for i in range(T):
+        mask[:, i] = np.where(rows[:, i, None] >= 0, mask[every, np.maximum(rows[:, i], 0)], 0)
+        mask[:, i, i // 32] |= np.uint32(1 << (i % 32))
+    return torch.from_numpy(mask.view(np.int32).reshape(*p.shape, words))
+
+
+def _refuse_tree(cfg, q, pool, staging, block_table, seq_lens, k, v, mask, out, workspace, draft_lens):
+    """Why _tree_args does not pass its arguments: always raises."""
+    _need_cuda(q, "q")
+    _need_cuda(out, "out")
+    _dtype_code(q), _dtype_code(out)
+    _need_cuda(block_table, "block_table", _i32t)
+    _need_cuda(seq_lens, "seq_lens", _i32t)
+    _need_cuda(mask, "mask", _i32t)
+    _need_cuda(workspace, "workspace", _u8)
+    for t, name in ((k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not _bf16:
+            raise ValueError(f"{name} must be a bf16 CUDA tensor")
+    _need_device(pool, staging, q, out, block_table, seq_lens, k, v, mask, workspace, draft_lens)
+    if q.dim() != 4 or q.shape[2:] != (cfg.n_q_heads, 128) or out.shape != q.shape:
+        raise ValueError("q and out must be [batch][drafts][n_q][128]")
+    batch, T = q.shape[:2]
+    if block_table.dim() != 2 or block_table.shape[0] != batch or seq_lens.numel() != batch:
+        raise ValueError("seq_lens and block_table must have a row for each sequence of q")
+    for t, name in ((k, "k"), (v, "v")):
+        if t.shape != (batch, T, cfg.n_kv_heads, 128):
+            raise ValueError(f"{name} must be {[batch, T, cfg.n_kv_heads, 128]}, got {list(t.shape)}")
+        s0, s1, s2, s3 = t.stride()
+        if s3 != 1 or (s2 != 128 and t.shape[2] > 1) or (s0 != T * s1 and batch > 1 and T > 1):
+            raise ValueError(f"{name}: the heads of a token must be contiguous, and all tokens one stride apart")
+    if mask.shape != (batch, T, (T + 31) // 32):
+        raise ValueError(f"mask must be {[batch, T, (T + 31) // 32]}, got {list(mask.shape)}")
+    if draft_lens is not None:
+        _need_vec(draft_lens, "draft_lens", _i32t, batch)
+    raise ValueError("tree attention: the arguments do not fit together")
+
+
+def _tree_args(cfg, q, pool, staging, block_table, seq_lens, k, v, mask, out, workspace, draft_lens):
+    # (as in _append_rope: each attribute read once)
+    dev, i32, bf16 = _current_device(), _i32t, _bf16
+    lens_ptr = None
+    try:
+        shape, q_type, out_type, n_kv = q.shape, q.dtype, out.dtype, cfg.n_kv_heads
+        batch, T, n_q, d = shape
+        rows, max_blocks = block_table.shape
+        k0, k1, k2, k3 = k.stride()
+        v0, v1, v2, v3 = v.stride()
+        good = (dev == pool.get_device() == q.get_device() == out.get_device() == block_table.get_device()
+                == seq_lens.get_device() == k.get_device() == v.get_device() == mask.get_device()
+                == workspace.get_device() and (staging is None or staging.get_device() == dev)
+                and block_table.dtype is i32 and seq_lens.dtype is i32 and mask.dtype is i32 and workspace.dtype is _u8
+                and (q_type is bf16 or q_type is _f32) and (out_type is bf16 or out_type is _f32) and k.dtype is bf16
+                and v.dtype is bf16 and n_q == cfg.n_q_heads and d == 128 and out.shape == shape
+                and k.shape == v.shape == (batch, T, n_kv, 128) and rows == batch and seq_lens.numel() == batch
+                and k3 == 1 == v3 and (k2 == 128 == v2 or n_kv == 1) and ((k0 == T * k1 and v0 == T * v1) or batch == 1 or T == 1)
+                and mask.shape == (batch, T, (T + 31) // 32) and q.is_contiguous() and out.is_contiguous()
+                and block_table.is_contiguous() and seq_lens.is_contiguous() and mask.is_contiguous()
+                and workspace.is_contiguous())
+        if draft_lens is not None:
+            good = (good and draft_lens.dtype is i32 and draft_lens.get_device() == dev and draft_lens.numel() == batch
+                    and draft_lens.is_contiguous())
+            lens_ptr = draft_lens.data_ptr()
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_tree(cfg, q, pool, staging, block_table, seq_lens, k, v, mask, out, workspace, draft_lens)
+    if T == 1:   # (tokens are one sequence apart)
+        k1, v1 = (k0, v0) if batch > 1 else (n_kv * 128, n_kv * 128)
+    return (FP32 if q_type is _f32 else BF16,
+            (block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), k.data_ptr(), v.data_ptr(), k1, v1,
+             mask.data_ptr(), lens_ptr, batch, T, out.data_ptr(), FP32 if out_type is _f32 else BF16,
+             workspace.data_ptr(), workspace.numel(), _stream_of(dev)))
+
+
+def tree_attn(cfg: Config, q: torch.Tensor, pool: torch.Tensor, staging: torch.Tensor, block_table: torch.Tensor,
+              seq_lens: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: torch.Tensor, out: torch.Tensor,
+              workspace: torch.Tensor, *, draft_lens: Optional[torch.Tensor] = None):
+    """Attention of drafted tokens, which are not cached yet, over the packed
+    cache and one another: q, out (bf16|fp32) [batch][drafts][n_q][128]; k, v bf16
+    [batch][drafts][n_kv][128], tokens at any one stride that is a multiple of 8. Row r
+    of sequence b sees its seq_lens[b] cached tokens and the drafts whose bits
+    are set in mask[b][r] (int32 words; tree_mask makes it from the drafts'
+    parents). draft_lens int32 [batch]: rows from there on are padding."""
+    _need_packed(cfg, pool, staging, seq_lens.numel(), "q")
+    code, rest = _tree_args(cfg, q, pool, staging, block_table, seq_lens, k, v, mask, out, workspace, draft_lens)
+    r = lib().kvarn_tree_attn(ctypes.byref(cfg), q.data_ptr(), code, pool.data_ptr(), pool.shape[0], staging.data_ptr(),
+                              *rest)
+    if r:
+        _check(r, "kvarn_tree_attn")
+
+
+def tree_attn_bf16(cfg: Config, q: torch.Tensor, kv_pool: torch.Tensor, block_table: torch.Tensor,
+                   seq_lens: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: torch.Tensor, out: torch.Tensor,
+                   workspace: torch.Tensor, *, draft_lens: Optional[torch.Tensor] = None):
+    """tree_attn over the bf16 pages [n_blocks][n_kv][2][B][128] of decode_attn_bf16."""
+    _need_pages(cfg, kv_pool)
+    code, rest = _tree_args(cfg, q, kv_pool, None, block_table, seq_lens, k, v, mask, out, workspace, draft_lens)
+    r = lib().kvarn_tree_attn_bf16(ctypes.byref(cfg), q.data_ptr(), code, kv_pool.data_ptr(), kv_pool.shape[0], *rest)
+    if r:
+        _check(r, "kvarn_tree_attn_bf16")
+
+
+def _refuse_weights(cfg, q, pool, staging, block_table, seq_lens, out, weights, weights_in, workspace):
+    """Why _weights_args does not pass its arguments: always raises."""
+    _need_cuda(q, "q")
+    _need_cuda(out, "out")
+    _dtype_code(q), _dtype_code(out)
+    _need_cuda(block_table, "block_table", _i32t)
+    _need_cuda(seq_lens, "seq_lens", _i32t)
+    _need_cuda(weights, "weights", _f32)
+    _need_cuda(workspace, "workspace", _u8)
+    if weights_in is not None:
+        _need_cuda(weights_in, "weights_in", _f32)
+    _need_device(pool, staging, q, out, block_table, seq_lens, weights, weights_in, workspace)
+    if q.dim() != 3 or q.shape[1:] != (cfg.n_q_heads, 128) or out.shape != q.shape:
+        raise ValueError("q and out must be [batch][n_q][128]")
+    if block_table.dim() != 2 or block_table.shape[0] != q.shape[0] or seq_lens.numel() != q.shape[0]:
+        raise ValueError("seq_lens and block_table must have a row for each sequence of q")
+    if weights.dim() != 3 or weights.shape[:2] != (q.shape[0], cfg.n_kv_heads):
+        raise ValueError("weights must be [batch][n_kv][columns]")
+    raise ValueError("weights_in must have the shape of weights")
+
+
+def _weights_args(cfg, q, pool, staging, block_table, seq_lens, out, weights, weights_in, workspace):
+    # (as in _append_rope: each attribute read once)
+    dev, i32, f32 = _current_device(), _i32t, _f32
+    if weights_in is None:
+        weights_in = weights
+    try:
+        shape, q_type, out_type = q.shape, q.dtype, out.dtype
+        batch, n_q, d = shape
+        rows, max_blocks = block_table.shape
+        w_batch, w_heads, columns = w_shape = weights.shape
+        good = (dev == pool.get_device() == q.get_device() == out.get_device() == block_table.get_device()
+                == seq_lens.get_device() == weights.get_device() == weights_in.get_device() == workspace.get_device()
+                and (staging is None or staging.get_device() == dev) and block_table.dtype is i32
+                and seq_lens.dtype is i32 and workspace.dtype is _u8 and (q_type is _bf16 or q_type is f32)
+                and (out_type is _bf16 or out_type is f32) and weights.dtype is f32 and weights_in.dtype is f32
+                and n_q == cfg.n_q_heads and d == 128 and out.shape == shape and rows == batch == w_batch
+                and w_heads == cfg.n_kv_heads and weights_in.shape == w_shape and seq_lens.numel() == batch
+                and q.is_contiguous() and out.is_contiguous() and block_table.is_contiguous()
+                and seq_lens.is_contiguous() and weights.is_contiguous() and weights_in.is_contiguous()
+                and workspace.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_weights(cfg, q, pool, staging, block_table, seq_lens, out, weights, weights_in, workspace)
+    return (FP32 if q_type is f32 else BF16,
+            (block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), batch, out.data_ptr(),
+             FP32 if out_type is f32 else BF16, weights_in.data_ptr(), weights.data_ptr(), columns),
+            (workspace.data_ptr(), workspace.numel(), _stream_of(dev)))
+
+
+def decode_attn_weights(cfg: Config, q: torch.Tensor, pool: torch.Tensor, staging: torch.Tensor,
+                        block_table: torch.Tensor, seq_lens: torch.Tensor, out: torch.Tensor, weights: torch.Tensor,
+                        workspace: torch.Tensor, *, weights_in: Optional[torch.Tensor] = None, decay: float = 1.0):
+    """decode_attn (out bf16|fp32) that also leaves in weights, fp32 [batch][n_kv]
+    [columns], decay times weights_in (default: weights itself) plus the softmax
+    weight of each cached token, summed over the query heads of its kv head.
+    columns: a multiple of 4, at least those of the block table's tokens."""
+    _need_packed(cfg, pool, staging, seq_lens.numel(), "q")
+    code, most, rest = _weights_args(cfg, q, pool, staging, block_table, seq_lens, out, weights, weights_in, workspace)
+    r = lib().kvarn_decode_attn_weights(ctypes.byref(cfg), q.data_ptr(), code, pool.data_ptr(), pool.shape[0],
+                                        staging.data_ptr(), *most, decay, *rest)
+    if r:
+        _check(r, "kvarn_decode_attn_weights")
+
+
+def decode_attn_weights_bf16(cfg: Config, q: torch.Tensor, kv_pool: torch.Tensor, block_table: torch.Tensor,
+                             seq_lens: torch.Tensor, out: torch.Tensor, weights: torch.Tensor, workspace: torch.Tensor,
+                             *, weights_in: Optional[torch.Tensor] = None, decay: float = 1.0):
+    """decode_attn_weights over the bf16 pages [n_blocks][n_kv][2][B][128] of decode_attn_bf16."""
+    _need_pages(cfg, kv_pool)
+    code, most, rest = _weights_args(cfg, q, kv_pool, None, block_table, seq_lens, out, weights, weights_in, workspace)
+    r = lib().kvarn_decode_attn_weights_bf16(ctypes.byref(cfg), q.data_ptr(), code, kv_pool.data_ptr(), kv_pool.shape[0],
+                                             *most, decay, *rest)
+    if r:
+        _check(r, "kvarn_decode_attn_weights_bf16")
+
+
+def _refuse_evict(cfg, pool, block_table, seq_lens, weights, new_table, new_lens, new_weights, kept, workspace, places):
+    """Why _evict's arguments do not pass: always raises."""
+    for t, name, dtype in ((block_table, "block_table", _i32t), (seq_lens, "seq_lens", _i32t), (weights, "weights", _f32),
+                           (new_table, "new_table", _i32t), (new_lens, "new_lens", _i32t),
+                           (new_weights, "new_weights", _f32), (kept, "kept", _i32t), (workspace, "workspace", _u8)):
+        _need_cuda(t, name, dtype)
+    _need_device(pool, block_table, seq_lens, weights, new_table, new_lens, new_weights, kept, workspace)
+    batch, n_kv = seq_lens.numel(), cfg.n_kv_heads
+    for t, name in ((block_table, "block_table"), (new_table, "new_table")):
+        if t.dim() != 2 or t.shape[0] != batch:
+            raise ValueError(f"{name} must be [batch][blocks]")
+    if new_lens.numel() != batch:
+        raise ValueError("new_lens must hold a length for each sequence")
+    for t, name in ((weights, "weights"), (new_weights, "new_weights")):
+        if t.dim() != 3 or t.shape[:2] != (batch, n_kv):
+            raise ValueError(f"{name} must be [batch][n_kv][columns]")
+    if kept.shape != (batch, n_kv, places):
+        raise ValueError(f"kept must be {[batch, n_kv, places]}, got {list(kept.shape)}")
+    raise ValueError("workspace must hold 256 bytes")
+
+
+def _evict(fn, name, cfg, pool, block_table, seq_lens, weights, new_table, new_lens, new_weights, kept, workspace, budget,
+           recent, unit):
+    # (as in _append_rope: each attribute read once)
+    dev, i32, f32 = _current_device(), _i32t, _f32
+    places = budget // unit
+    try:
+        rows, max_blocks = block_table.shape
+        new_rows, new_blocks = new_table.shape
+        w_batch, w_heads, columns = weights.shape
+        n_batch, n_heads, new_columns = new_weights.shape
+        batch, n_kv = seq_lens.numel(), cfg.n_kv_heads
+        good = (dev == pool.get_device() == block_table.get_device() == seq_lens.get_device() == weights.get_device()
+                == new_table.get_device() == new_lens.get_device() == new_weights.get_device() == kept.get_device()
+                == workspace.get_device() and block_table.dtype is i32 and seq_lens.dtype is i32
+                and weights.dtype is f32 and new_table.dtype is i32 and new_lens.dtype is i32
+                and new_weights.dtype is f32 and kept.dtype is i32 and workspace.dtype is _u8
+                and rows == new_rows == w_batch == n_batch == batch == new_lens.numel() and w_heads == n_heads == n_kv
+                and kept.shape == (batch, n_kv, places) and workspace.numel() >= 256 and block_table.is_contiguous()
+                and seq_lens.is_contiguous() and weights.is_contiguous() and new_table.is_contiguous()
+                and new_lens.is_contiguous() and new_weights.is_contiguous() and kept.is_contiguous()
+                and workspace.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_evict(cfg, pool, block_table, seq_lens, weights, new_table, new_lens, new_weights, kept, workspace, places)
+    r = fn(ctypes.byref(cfg), pool.data_ptr(), pool.shape[0], block_table.data_ptr(), max_blocks, seq_lens.data_ptr(),
+           weights.data_ptr(), columns, budget, recent, new_table.data_ptr(), new_blocks, new_lens.data_ptr(),
+           new_weights.data_ptr(), new_columns, kept.data_ptr(), batch, workspace.data_ptr(), _stream_of(dev))
+    if r:
+        _check(r, name)
+
+
+def evict(cfg: Config, pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, weights: torch.Tensor,
+          new_table: torch.Tensor, new_lens: torch.Tensor, new_weights: torch.Tensor, kept: torch.Tensor,
+          workspace: torch.Tensor, *, budget: int, recent: int):
+    """evict_bf16 over the packed cache, by whole blocks: budget and recent are
+    multiples of the block size, kept is [batch][n_kv][budget / block] and names blocks,
+    a block's weight is the sum of its tokens'. The incomplete block stays in
+    staging, behind the kept blocks."""
+    if (not isinstance(pool, torch.Tensor) or pool.dtype is not _u8 or pool.dim() != 2 or not pool.is_contiguous()
+            or pool.shape[1] != _block_bytes_of(cfg.n_kv_heads, cfg.block_size, cfg.bits)):
+        _need_cuda(pool, "pool", _u8)
+        raise ValueError("pool must be [n_blocks][block_bytes]")
+    _evict(lib().kvarn_evict, "kvarn_evict", cfg, pool, block_table, seq_lens, weights, new_table, new_lens, new_weights,
+           kept, workspace, budget, recent, cfg.block_size)
+
+
+def evict_bf16(cfg: Config, kv_pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+               weights: torch.Tensor, new_table: torch.Tensor, new_lens: torch.Tensor, new_weights: torch.Tensor,
+               kept: torch.Tensor, workspace: torch.Tensor, *, budget: int, recent: int):
+    """Cuts sequences longer than `budget` tokens down to it, each kv head by its own
+    weights (fp32 [batch][n_kv][columns], as decode_attn_weights_bf16 leaves them):
+    the last `recent` tokens and those of the others with the greatest weights go,
+    in order, to the pages new_table [batch][new_blocks] (none that the call
+    reads). new_lens [batch], kept int32 [batch][n_kv][budget] (the token now at each place,
+    -1 behind) and new_weights [batch][n_kv][new columns] are filled in; the old pages
+    are only read."""
+    _need_pages(cfg, kv_pool)
+    _evict(lib().kvarn_evict_bf16, "kvarn_evict_bf16", cfg, kv_pool, block_table, seq_lens, weights, new_table, new_lens,
+           new_weights, kept, workspace, budget, recent, 1)
 
 
 def decode_attn_noalloc(cfg: Config, q: torch.Tensor, pool: torch.Tensor, staging: torch.Tensor,

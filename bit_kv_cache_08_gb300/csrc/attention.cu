@@ -95,7 +95,8 @@ constexpr int attn_warp_bytes() {
 struct UnitShare {
     int b, h, part, parts;
 };
-template <int B, int BITS, int S, bool UNIT>
+// SCORES: every token's score goes to a.scores as well (see AttnArgs).
+template <int B, int BITS, int S, bool UNIT, bool SCORES = false>
 __device__ __forceinline__ bool decode_attn_2bit_body(const AttnArgs& a, uint8_t* smem, const UnitShare u) {
     static_assert(BITS >= 2 && BITS <= 4, "2-, 3- or 4-bit codes");
     constexpr int HB = head_block_bytes(B, BITS);
@@ -483,6 +484,15 @@ __device__ __forceinline__ bool decode_attn_2bit_body(const AttnArgs& a, uint8_t
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) sc[sb][mt] = __fmul2_rn(__fmul2_rn(s_[mt], Rv[mt]), kmb2);
             }
+            if constexpr (SCORES) {   // tokens 32 sb + 4 gq .. + 3 of head tq: whole 128-byte lines
+                if (head_ok) {
+                    float* dst = a.scores + ((int64_t)cc.b * n_q + cc.h * G + tq) * a.score_stride + (int64_t)cc.j * B + 4 * gq;
+#pragma unroll
+                    for (int sb = 0; sb < NSB; ++sb)
+                        *reinterpret_cast<float4*>(dst + 32 * sb) =
+                            make_float4(sc[sb][0].x, sc[sb][0].y, sc[sb][1].x, sc[sb][1].y);
+                }
+            }
             // ---------------- online softmax over the block (head tq: 8 lanes x 4 tokens per sub-block)
             float bm = -INFINITY;
 #pragma unroll
@@ -696,20 +706,20 @@ __device__ __forceinline__ bool decode_attn_2bit_body(const AttnArgs& a, uint8_t
 // LATE: behind a kernel that lets this one start beside it (see
 // let_next_grid_start), the wait comes last, and in one CTA (the grid has not
 // ended before that one has).
-template <int B, int BITS, int S, bool LATE>
+template <int B, int BITS, int S, bool LATE, bool SCORES = false>
 __global__ void __launch_bounds__(32) decode_attn_2bit_kernel(AttnArgs a) {
     if (LATE) let_next_grid_start();   // the merge, which waits for this one at its beginning
     else wait_prior_grids();
     extern __shared__ __align__(16) uint8_t smem[];
-    decode_attn_2bit_body<B, BITS, S, false>(a, smem, UnitShare{});
+    decode_attn_2bit_body<B, BITS, S, false, SCORES>(a, smem, UnitShare{});
     if (LATE && blockIdx.x == gridDim.x - 1) wait_prior_grids();
 }
-template <int B, int BITS, int S, int MINB, bool LATE>
+template <int B, int BITS, int S, int MINB, bool LATE, bool SCORES = false>
 __global__ void __launch_bounds__(32, MINB) decode_attn_2bit_kernel_minb(AttnArgs a) {
     if (LATE) let_next_grid_start();   // the merge, which waits for this one at its beginning
     else wait_prior_grids();
     extern __shared__ __align__(16) uint8_t smem[];
-    decode_attn_2bit_body<B, BITS, S, false>(a, smem, UnitShare{});
+    decode_attn_2bit_body<B, BITS, S, false, SCORES>(a, smem, UnitShare{});
     if (LATE && blockIdx.x == gridDim.x - 1) wait_prior_grids();
 }
 
@@ -780,11 +790,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 1) prefix_join_packed_kernel(
 template <int B, int BITS>
 constexpr int attn_min_ctas() { return BITS != 3 ? 0 : (B == 64 ? 1 : 16); }
 
-template <int B, int BITS, bool LATE>
+template <int B, int BITS, bool LATE, bool SCORES>
 constexpr auto attn_kernel_fn() {
     constexpr int S = stages_for<B, BITS>(), M = attn_min_ctas<B, BITS>();
-    if constexpr (M > 0) return decode_attn_2bit_kernel_minb<B, BITS, S, M, LATE>;
-    else return decode_attn_2bit_kernel<B, BITS, S, LATE>;
+    if constexpr (M > 0) return decode_attn_2bit_kernel_minb<B, BITS, S, M, LATE, SCORES>;
+    else return decode_attn_2bit_kernel<B, BITS, S, LATE, SCORES>;
 }
 
 template <int B, int BITS>
@@ -795,8 +805,9 @@ size_t attn_smem_bytes() {
 template <int B, int BITS>
 struct AttnKernel {
     static constexpr int kB = B, kBits = BITS;
-    static constexpr auto fn = attn_kernel_fn<B, BITS, false>();
-    static constexpr auto late = attn_kernel_fn<B, BITS, true>();
+    static constexpr auto fn = attn_kernel_fn<B, BITS, false, false>();
+    static constexpr auto late = attn_kernel_fn<B, BITS, true, false>();
+    static constexpr auto scores = attn_kernel_fn<B, BITS, false, true>();
     static size_t smem() { return attn_smem_bytes<B, BITS>(); }
 };
 
@@ -904,6 +915,17 @@ cudaError_t launch_decode_attn(const kvarn_config& cfg, const void* q, int q_dty
     // up to one wave of wide CTAs (4 per SM), so that 8 warps share each
     // row's raw tail rows
     return cfg.block_size == 32 ? launch_merge<32, true>(a, nw, 4, st) : launch_merge<64, true>(a, nw, 4, st);
+}
+
+// The split kernel that leaves every score, and the merge that leaves the rows'
+// maxima and sums (weights.cu).
+cudaError_t launch_decode_scores(const kvarn_config& cfg, const AttnArgs& a, cudaStream_t st) {
+    const cudaError_t e = with_attn_kernel(cfg.block_size, cfg.bits, [&](auto k) {
+        using K = decltype(k);
+        return launch_pdl(K::scores, a.nw, 32, K::smem(), st, a);
+    });
+    if (e != cudaSuccess) return e;
+    return cfg.block_size == 32 ? launch_merge<32, true, true>(a, a.nw, 4, st) : launch_merge<64, true, true>(a, a.nw, 4, st);
 }
 
 }  // namespace kvarn

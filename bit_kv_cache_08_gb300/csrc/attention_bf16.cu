@@ -51,7 +51,8 @@ __device__ __forceinline__ void split_bf16x2(float v0, float v1, uint32_t& hi, u
     lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-template <int B>
+// SCORES: every token's score goes to a.scores as well (see AttnArgs).
+template <int B, bool SCORES>
 __device__ __forceinline__ void decode_attn_bf16_body(const AttnArgs& a) {
     constexpr int CPB = B / kChunk;   // chunks per page
     extern __shared__ __align__(16) uint8_t smem[];
@@ -202,6 +203,13 @@ __device__ __forceinline__ void decode_attn_bf16_body(const AttnArgs& a) {
             float s0 = (sacc[0] + sacc[1]) * qs, s1 = (sacc[2] + sacc[3]) * qs;
             if (gq >= nvalid) s0 = -INFINITY;
             if (gq + 8 >= nvalid) s1 = -INFINITY;
+            if constexpr (SCORES) {
+                if (tq < G) {
+                    float* dst = a.scores + ((int64_t)cc.b * a.n_q + cc.h * G + tq) * a.score_stride + (int64_t)cc.j * kChunk + gq;
+                    dst[0] = s0;
+                    dst[8] = s1;
+                }
+            }
             float bm = fmaxf(s0, s1);
             bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 4));
             bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 8));
@@ -255,11 +263,11 @@ __device__ __forceinline__ void decode_attn_bf16_body(const AttnArgs& a) {
 
 // LATE: behind a kernel that lets this one start beside it, the wait comes
 // last, and in one CTA (the grid has not ended before that one has).
-template <int B, bool LATE>
+template <int B, bool LATE, bool SCORES = false>
 __global__ void __launch_bounds__(32) decode_attn_bf16_kernel(AttnArgs a) {
     if (LATE) let_next_grid_start();   // the merge, which waits for this one at its beginning
     else wait_prior_grids();
-    decode_attn_bf16_body<B>(a);
+    decode_attn_bf16_body<B, SCORES>(a);
     if (LATE && blockIdx.x == gridDim.x - 1) wait_prior_grids();
 }
 
@@ -282,13 +290,11 @@ int attn_bf16_grid_warps(int block_size, int device) {
     return cache[bi][device];
 }
 
-// The arguments of a launch, and its split kernel alone (the caller merges).
-cudaError_t launch_decode_split_bf16(const kvarn_config& cfg, const void* q, int q_dtype, const void* kv_pool,
-                                    int64_t n_pool_blocks, const int32_t* block_table, int max_blocks,
-                                    const int32_t* seq_lens, int batch, float* out, void* workspace, int nw,
-                                     bool late, AttnArgs* args, cudaStream_t st) {
-    AttnArgs& a = *args;
-    a = {};
+// The arguments of a launch.
+AttnArgs decode_split_args_bf16(const kvarn_config& cfg, const void* q, int q_dtype, const void* kv_pool, int64_t n_pool_blocks,
+                                const int32_t* block_table, int max_blocks, const int32_t* seq_lens, int batch, float* out,
+                                void* workspace, int nw) {
+    AttnArgs a = {};
     a.q = q;
     a.q_dtype = q_dtype;
     a.pool = (const uint8_t*)kv_pool;
@@ -314,11 +320,30 @@ cudaError_t launch_decode_split_bf16(const kvarn_config& cfg, const void* q, int
     a.sm_scale = cfg.sm_scale;
     a.flags = cfg.flags;
     for (int i = 0; i < 4; ++i) a.sb[i] = cfg.sign_bits[i];
+    return a;
+}
+
+// The split kernel alone (the caller merges) and its arguments.
+cudaError_t launch_decode_split_bf16(const kvarn_config& cfg, const void* q, int q_dtype, const void* kv_pool,
+                                    int64_t n_pool_blocks, const int32_t* block_table, int max_blocks,
+                                    const int32_t* seq_lens, int batch, float* out, void* workspace, int nw,
+                                    bool late, AttnArgs* args, cudaStream_t st) {
+    const AttnArgs a = *args = decode_split_args_bf16(cfg, q, q_dtype, kv_pool, n_pool_blocks, block_table, max_blocks,
+                                                      seq_lens, batch, out, workspace, nw);
     if (cfg.block_size == 32)
         return launch_pdl(late ? decode_attn_bf16_kernel<32, true> : decode_attn_bf16_kernel<32, false>, nw, 32,
                           attn_bf16_smem_bytes(), st, a);
     return launch_pdl(late ? decode_attn_bf16_kernel<64, true> : decode_attn_bf16_kernel<64, false>, nw, 32,
                       attn_bf16_smem_bytes(), st, a);
+}
+
+// The split kernel that leaves every score, and the merge that leaves the rows'
+// maxima and sums (weights.cu).
+cudaError_t launch_decode_scores_bf16(const kvarn_config& cfg, const AttnArgs& a, cudaStream_t st) {
+    const cudaError_t e = launch_pdl(cfg.block_size == 32 ? decode_attn_bf16_kernel<32, false, true>
+                                                          : decode_attn_bf16_kernel<64, false, true>,
+                                     a.nw, 32, attn_bf16_smem_bytes(), st, a);
+    return e == cudaSuccess ? launch_merge<kChunk, false, true>(a, a.nw, 0, st) : e;
 }
 
 cudaError_t launch_decode_attn_bf16(const kvarn_config& cfg, const void* q, int q_dtype, const void* kv_pool,

@@ -40,6 +40,13 @@ struct AttnArgs {
     // (first, last) warp of each (sequence, kv head) unit, written by the split
     // kernel for the merge; nullptr: the merge finds them from the split arithmetic
     int32_t* unit_map;
+    // decode attention that keeps its weights (the WEIGHTS kernels; not read by the
+    // others): every token's score, log2 domain, [row][query head][score_stride], and
+    // each row's final maximum and 1 / sum; out in bf16 where out_bf16
+    float* scores;
+    float2* stats;
+    int64_t score_stride;
+    int out_bf16;
 };
 
 // ---------------------------------------------------------------- small helpers
@@ -278,9 +285,10 @@ __device__ __forceinline__ void combine_slices(const float* sl, int n, int lane,
 // log2 e, this lane's 4 channels in qv) against the bf16 staging rows. Each
 // lane scores its 4 channels of every row, a warp sum gives the score; m, l
 // and acc (this lane's 4 channels) start at -inf, 0 and 0.
+// scores: where to leave the rows' scores (row r at r), or nullptr.
 template <int B, int STEP>
 __device__ __forceinline__ void tail_slice(const uint16_t* kst, int ntail, int first, const float (&qv)[4], int lane,
-                                           float& m, float& l, float (&acc)[4]) {
+                                           float& m, float& l, float (&acc)[4], float* scores = nullptr) {
     constexpr int R = (B + STEP - 1) / STEP;   // rows of this slice at most
     const uint16_t* vst = kst + B * kD;
     uint2 ku[R], vu[R];
@@ -308,6 +316,11 @@ __device__ __forceinline__ void tail_slice(const uint16_t* kst, int ntail, int f
     for (int o = 16; o >= 1; o >>= 1)
 #pragma unroll
         for (int i = 0; i < R; ++i) sc[i] += __shfl_xor_sync(kFull, sc[i], o);
+    if (scores != nullptr && lane == 0) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (first + i * STEP < ntail) scores[first + i * STEP] = sc[i];
+    }
     float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -336,7 +349,8 @@ __device__ __forceinline__ void tail_slice(const uint16_t* kst, int ntail, int f
 // pages. qsh: 128 floats of this warp's shared memory. gw = row * n_q +
 // query head. With NWIDE > 0 (the wide merge's warp 0) the partials and the
 // tail rows arrive as NWIDE per-warp LSE slices in shared memory (wide, tails).
-template <int B, bool ROT, int NWIDE = 0>
+// WEIGHTS: the tail rows' scores and the row's maximum and 1 / sum are kept.
+template <int B, bool ROT, int NWIDE = 0, bool WEIGHTS = false>
 __device__ __forceinline__ void merge_row(const AttnArgs& a, int64_t gw, int np, const float* p0, float* qsh,
                                           int lane, const float* wide = nullptr, const float* tails = nullptr) {
     const int b = (int)(gw / a.n_q), hq = (int)(gw % a.n_q);   // b: a (virtual) row sequence
@@ -346,7 +360,8 @@ __device__ __forceinline__ void merge_row(const AttnArgs& a, int64_t gw, int np,
     float* out = a.out + gw * kD;
     if (L < 0 || L > a.max_blocks * B) {
         if (lane == 0) raise_error(a.err, KVARN_DEVERR_POSITION);
-        reinterpret_cast<float4*>(out)[lane] = make_float4(NAN, NAN, NAN, NAN);
+        if (WEIGHTS && a.out_bf16) reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + gw * kD)[lane] = make_uint2(0x7fc07fc0u, 0x7fc07fc0u);
+        else reinterpret_cast<float4*>(out)[lane] = make_float4(NAN, NAN, NAN, NAN);
         return;
     }
     const SplitArgs sp{a.seq_lens, a.batch, a.n_kv, a.max_blocks, B, ROT ? 0 : 1, a.chunk};
@@ -429,6 +444,11 @@ __device__ __forceinline__ void merge_row(const AttnArgs& a, int64_t gw, int np,
                 mine[half] = d;
             }
         }
+        if (WEIGHTS) {
+            float* sc = a.scores + gw * a.score_stride + (int64_t)nb * B;
+            if (lane < ntail) sc[lane] = mine[0];
+            if (lane + 32 < ntail) sc[lane + 32] = mine[1];
+        }
         const float mt = warp_max(fmaxf(mine[0], mine[1]));
         const float mn = fmaxf(m, mt);                      // finite: ntail > 0
         const float fa = (m == -INFINITY) ? 0.f : exp2f(m - mn);
@@ -457,7 +477,14 @@ __device__ __forceinline__ void merge_row(const AttnArgs& a, int64_t gw, int np,
         }
     }
     const float inv = (l > 0.f) ? 1.f / l : 0.f;
-    reinterpret_cast<float4*>(out)[lane] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+    if (WEIGHTS && lane == 0) a.stats[gw] = make_float2(m, inv);
+    if (WEIGHTS && a.out_bf16) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv), y = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
+        reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + gw * kD)[lane] =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    } else {
+        reinterpret_cast<float4*>(out)[lane] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+    }
 }
 
 // The partials of row gw's unit: their count np and the first p0 (np = 0
@@ -502,7 +529,7 @@ __device__ __forceinline__ void merge_locate(const AttnArgs& a, int64_t gw, int 
 
 // The merge kernel: one warp per (row, query head), which finds its unit's
 // partials from the split arithmetic or the split kernel's unit map.
-template <int B, bool ROT>
+template <int B, bool ROT, bool WEIGHTS = false>
 __global__ void __launch_bounds__(128) merge_kernel(AttnArgs a) {
     wait_prior_grids();
     const int lane = threadIdx.x & 31;
@@ -512,7 +539,7 @@ __global__ void __launch_bounds__(128) merge_kernel(AttnArgs a) {
     int np;
     const float* p0;
     merge_locate<B, ROT>(a, gw, lane, np, p0);
-    merge_row<B, ROT>(a, gw, np, p0, q_all[threadIdx.x >> 5], lane);
+    merge_row<B, ROT, 0, WEIGHTS>(a, gw, np, p0, q_all[threadIdx.x >> 5], lane);
 }
 
 // The wide merge, for units cut into many partials (few long sequences) or
@@ -525,7 +552,7 @@ __global__ void __launch_bounds__(128) merge_kernel(AttnArgs a) {
 // NB: partials per load round trip of a warp's LSE merge. With 8 the kernel
 // needs 110 registers (2 CTAs per SM); with 4, 64 (4 CTAs per SM).
 constexpr int kWideWarps = 8;
-template <int B, bool ROT, int NB>
+template <int B, bool ROT, int NB, bool WEIGHTS>
 __global__ void __launch_bounds__(32 * kWideWarps, NB == 8 ? 2 : 4) merge_wide_kernel(AttnArgs a) {
     wait_prior_grids();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
@@ -569,7 +596,10 @@ __global__ void __launch_bounds__(32 * kWideWarps, NB == 8 ? 2 : 4) merge_wide_k
         const float qs = a.sm_scale * kLog2e;
 #pragma unroll
         for (int k = 0; k < 4; ++k) qv[k] *= qs;
-        tail_slice<B, kWideWarps>(kst, ntail, wp, qv, lane, tm, tl, tacc);
+        float* sc = nullptr;
+        if constexpr (WEIGHTS)   // (the tail begins behind the last complete block)
+            sc = a.scores + gw * a.score_stride + (a.seq_lens[gw / a.n_q] - ntail);
+        tail_slice<B, kWideWarps>(kst, ntail, wp, qv, lane, tm, tl, tacc, sc);
     }
     if (lane == 0) {
         slices[wp][0] = m;
@@ -580,7 +610,7 @@ __global__ void __launch_bounds__(32 * kWideWarps, NB == 8 ? 2 : 4) merge_wide_k
     *reinterpret_cast<float4*>(&slices[wp][4 + 4 * lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
     *reinterpret_cast<float4*>(&tails[wp][4 + 4 * lane]) = make_float4(tacc[0], tacc[1], tacc[2], tacc[3]);
     __syncthreads();
-    if (wp == 0) merge_row<B, ROT, kWideWarps>(a, gw, np, p0, qsh, lane, &slices[0][0], &tails[0][0]);
+    if (wp == 0) merge_row<B, ROT, kWideWarps, WEIGHTS>(a, gw, np, p0, qsh, lane, &slices[0][0], &tails[0][0]);
 }
 
 // Whether the merge of a launch with nw split warps over `units` (sequence,
@@ -615,16 +645,16 @@ inline int64_t current_device_sms() {
 // Launches the merge of a split launch with nw warps: the wide kernel (with
 // its batch) or the one-warp-per-row kernel. wide_ctas_per_sm > 0 also takes
 // the wide kernel for up to that many rows per SM.
-template <int B, bool ROT>
+template <int B, bool ROT, bool WEIGHTS = false>
 cudaError_t launch_merge(const AttnArgs& a, int64_t nw, int wide_ctas_per_sm, cudaStream_t st) {
     const int64_t units = (int64_t)a.batch * a.n_kv, rows = (int64_t)a.batch * a.n_q;
     const int64_t sms = current_device_sms();
     if (merge_wide(nw, units, rows, wide_ctas_per_sm * sms)) {
         if (wide_merge_batch(nw, units, rows, sms) == 8)
-            return launch_pdl(merge_wide_kernel<B, ROT, 8>, (unsigned)rows, 32 * kWideWarps, 0, st, a);
-        return launch_pdl(merge_wide_kernel<B, ROT, 4>, (unsigned)rows, 32 * kWideWarps, 0, st, a);
+            return launch_pdl(merge_wide_kernel<B, ROT, 8, WEIGHTS>, (unsigned)rows, 32 * kWideWarps, 0, st, a);
+        return launch_pdl(merge_wide_kernel<B, ROT, 4, WEIGHTS>, (unsigned)rows, 32 * kWideWarps, 0, st, a);
     }
-    return launch_pdl(merge_kernel<B, ROT>, (unsigned)((rows + 3) / 4), 128, 0, st, a);
+    return launch_pdl(merge_kernel<B, ROT, WEIGHTS>, (unsigned)((rows + 3) / 4), 128, 0, st, a);
 }
 
 }  // namespace kvarn

@@ -129,8 +129,8 @@ typedef struct kvarn_config {
 /*
  * Test switch (no counterpart in the paper): with it, every warp of
  * kvarn_decode_attn's split kernel gives up its first shared-memory copy
- * wait at once (and kvarn_prefix_attn's and kvarn_prefix_attn_bf16's prefix
- * kernels act as if their first had), so the wait-timeout path runs without
+ * wait at once (and the tensor-core kernels of kvarn_prefix_attn, kvarn_tree_attn and
+ * their bf16 forms act as if their first had), so the wait-timeout path runs without
  * anything hanging:
  * KVARN_DEVERR_WAIT_TIMEOUT is raised, the copies already in flight are
  * waited for, the warp stops, the call's outputs are unspecified and the
@@ -442,6 +442,138 @@ int kvarn_prefix_attn_bf16(const kvarn_config* cfg, const void* q, int32_t q_dty
                            const int32_t* prefix_lens, const int32_t* block_table, int32_t max_blocks_per_seq,
                            const int32_t* seq_lens, int32_t batch, void* out, int32_t out_dtype, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/* Workspace bytes for kvarn_tree_attn / kvarn_tree_attn_bf16 with this batch
+ * number of drafts and table width on the CURRENT device. 0 on a bad config or
+ * size. */
+size_t kvarn_tree_workspace_bytes(const kvarn_config* cfg, int32_t batch, int32_t drafts,
+                                  int32_t max_blocks_per_seq);
+
+/*
+ * kvarn_tree_attn -- attention for a tree of drafted tokens over the packed
+ * cache (verification of several guessed continuations in one pass). (A serving
+ * convenience; the query is multiplied by the same Hadamard matrix, section 三 3.1.)
+ *
+ * Every sequence has `drafts` rows (1 .. KVARN_MAX_DRAFTS): q [batch][drafts]
+ * [n_q][128] (q_dtype KVARN_BF16 or KVARN_FP32), and k, v [batch][drafts][n_kv]
+ * [128] (bf16, the heads of a token contiguous, k_stride / v_stride elements, a
+ * multiple of 8, from one token to the next, the sequences one after the
+ * other: columns of one projection's output serve as they are). The drafted
+ * tokens are not in the cache; those that are accepted can be appended later.
+ * draft_lens (device int32 [batch], 0 .. drafts; NULL: all of them): the rows
+ * from draft_lens[b] on are padding, whose inputs are not looked at and whose
+ * outputs are left as they were.
+ *
+ * Row r of sequence b sees every cached token (seq_lens[b], as for
+ * kvarn_decode_attn) and the drafted tokens i < draft_lens[b] for which bit i % 32
+ * of mask[b][r][i / 32] is set (device uint32 [batch][drafts][(drafts + 31) / 32]):
+ * its ancestors in the tree and itself, or any other set.
+ *   out[b][r][j] = sum_t softmax_t(sm_scale * q.k_t) v_t
+ * over those; a row that sees nothing gives zeros, one with a score that is not a
+ * number NaN. out: device [batch][drafts][n_q][128], out_dtype KVARN_BF16 or
+ * KVARN_FP32. A drafted value that is not finite makes the rows that see it NaN,
+ * and no other row. workspace: at least kvarn_tree_workspace_bytes(cfg, batch,
+ * drafts, max_blocks_per_seq) bytes, 16-byte aligned; calls that may overlap need one each. Device
+ * faults: KVARN_DEVERR_BLOCK_ID, KVARN_DEVERR_POSITION (a length outside its
+ * range: NaN rows), KVARN_DEVERR_WAIT_TIMEOUT.
+ */
+#define KVARN_MAX_DRAFTS 128
+int kvarn_tree_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* pool,
+                    int64_t n_pool_blocks, const void* staging, const int32_t* block_table,
+                    int32_t max_blocks_per_seq, const int32_t* seq_lens, const void* k, const void* v,
+                    int64_t k_stride, int64_t v_stride, const uint32_t* mask, const int32_t* draft_lens,
+                    int32_t batch, int32_t drafts, void* out, int32_t out_dtype, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* kvarn_tree_attn_bf16 -- the same over the bf16 pages of kvarn_decode_attn_bf16. */
+int kvarn_tree_attn_bf16(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* kv_pool,
+                         int64_t n_pool_blocks, const int32_t* block_table, int32_t max_blocks_per_seq,
+                         const int32_t* seq_lens, const void* k, const void* v, int64_t k_stride,
+                         int64_t v_stride, const uint32_t* mask, const int32_t* draft_lens, int32_t batch,
+                         int32_t drafts, void* out, int32_t out_dtype, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Workspace bytes for kvarn_decode_attn_weights / kvarn_decode_attn_weights_bf16
+ * on the CURRENT device: kvarn_workspace_bytes, a maximum and a sum per query
+ * head and the scores of a full block table. 0 on a bad config or size. */
+size_t kvarn_weights_workspace_bytes(const kvarn_config* cfg, int32_t batch, int32_t max_blocks_per_seq);
+
+/*
+ * kvarn_decode_attn_weights -- kvarn_decode_attn that also keeps how much
+ * attention each cached token gets. (A library convenience: what eviction
+ * from a cache goes by.)
+ *
+ * Beside out (device [batch][n_q][128], out_dtype KVARN_BF16 or KVARN_FP32; the fp32
+ * values are those of kvarn_decode_attn), for every token t < seq_lens[b] and kv head h,
+ *   weights_out[b][h][t] = decay * weights_in[b][h][t]
+ *                          + sum over the query heads j of h of softmax_t(sm_scale * q_j.k_t)
+ * weights_in, weights_out: device fp32 [batch][n_kv][weights_stride], 16-byte
+ * aligned, weights_stride a multiple of 4 and at least max_blocks_per_seq * B;
+ * weights_out behind a sequence's end is left as it was. They may be the same
+ * buffer (weights kept from step to step) or two that do not overlap.
+ * weights_in NULL or decay 0: this step's weights alone. decay in 0 .. 1.
+ * workspace: at least kvarn_weights_workspace_bytes bytes, 16-byte aligned.
+ * Device faults as kvarn_decode_attn; a sequence with one has its weights unspecified.
+ */
+int kvarn_decode_attn_weights(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* pool,
+                              int64_t n_pool_blocks, const void* staging, const int32_t* block_table,
+                              int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch, void* out,
+                              int32_t out_dtype, const float* weights_in, float* weights_out,
+                              int64_t weights_stride, float decay, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* kvarn_decode_attn_weights_bf16 -- the same over the bf16 pages of kvarn_decode_attn_bf16. */
+int kvarn_decode_attn_weights_bf16(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* kv_pool,
+                                   int64_t n_pool_blocks, const int32_t* block_table,
+                                   int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch, void* out,
+                                   int32_t out_dtype, const float* weights_in, float* weights_out,
+                                   int64_t weights_stride, float decay, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * kvarn_evict_bf16 -- cuts the sequences of a bf16 paged cache down to a budget
+ * of tokens, by the weights that kvarn_decode_attn_weights_bf16 keeps. (A library
+ * convenience; keys are rotated already, so that attention does not ask for a
+ * token's place.)
+ *
+ * For every (sequence b, kv head h) with L = seq_lens[b] tokens (device int32 [batch]):
+ * L <= budget keeps all; otherwise the last `recent` tokens stay (0 .. budget), and of
+ * the others the budget - recent with the greatest weights[b][h][t] (device fp32
+ * [batch][n_kv][weights_stride], 16-byte aligned, the stride a multiple of 4; not
+ * negative; what is not a number counts as 0; ties go to the lowest t). Each kv head keeps its own. What is kept goes, in
+ * order, to the pages new_table (device int32 [batch][new_max_blocks]), which must not be
+ * among those that the call reads; old pages are only read, so that they may be shared
+ * with other sequences, and are free afterwards.
+ *   new_lens[b]           min(L, budget)  (device int32 [batch], not seq_lens itself)
+ *   kept[b][h][i]         the token now at place i, -1 from the new length on
+ *                         (device int32 [batch][n_kv][budget])
+ *   new_weights[b][h][i]  its weight, 0 from the new length on (device fp32 [batch][n_kv]
+ *                         [new_weights_stride], the first new_max_blocks * B columns
+ *                         written; must not overlap weights)
+ * Rows of the new pages behind the new length are left as they were.
+ * budget >= 1, new_max_blocks * B >= budget. workspace: >= 256 bytes, for the error
+ * word. Device faults: KVARN_DEVERR_BLOCK_ID (the row or block is not moved),
+ * KVARN_DEVERR_POSITION (a length beyond the block table: new length 0, nothing moved).
+ */
+int kvarn_evict_bf16(const kvarn_config* cfg, void* kv_pool, int64_t n_pool_blocks, const int32_t* block_table,
+                     int32_t max_blocks_per_seq, const int32_t* seq_lens, const float* weights,
+                     int64_t weights_stride, int32_t budget, int32_t recent, const int32_t* new_table,
+                     int32_t new_max_blocks, int32_t* new_lens, float* new_weights, int64_t new_weights_stride,
+                     int32_t* kept, int32_t batch, void* workspace, void* stream);
+
+/*
+ * kvarn_evict -- the same over the packed cache, by whole blocks, whose codes
+ * share their factors: budget and recent are multiples of B, a block's weight is
+ * the sum of its tokens' (rounded to fp32), and kept [batch][n_kv][budget / B] names
+ * blocks. The L % B tokens of the incomplete block stay where they are in staging, behind
+ * the kept blocks: new_lens[b] = min(L - L % B, budget) + L % B, their weights
+ * move along, and new_max_blocks * B > budget.
+ */
+int kvarn_evict(const kvarn_config* cfg, void* pool, int64_t n_pool_blocks, const int32_t* block_table,
+                int32_t max_blocks_per_seq, const int32_t* seq_lens, const float* weights, int64_t weights_stride,
+                int32_t budget, int32_t recent, const int32_t* new_table, int32_t new_max_blocks,
+                int32_t* new_lens, float* new_weights, int64_t new_weights_stride, int32_t* kept, int32_t batch,
+                void* workspace, void* stream);
 
 /*
  * kvarn_decode_attn_noalloc -- kvarn_decode_attn for callers that cannot
