@@ -307,6 +307,23 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
+}  // namespace
+
+// Tile copies of 64 channels of a page's K or V rows of one kv head, 128-byte
+// swizzled: rows of 128 channels, page after page, (K, V) of each kv head.
+cudaError_t bf16_page_map(CUtensorMap* map, const uint8_t* pool, int64_t n_pool_blocks, int n_kv, int block_size) {
+    const EncodeTiled enc = encode_tiled();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)n_pool_blocks * n_kv * 2 * block_size};
+    const cuuint64_t strides[1] = {kD * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)block_size}, one[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t*>(pool), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+namespace {
+
 template <int B, int MODE>
 cudaError_t launch_mode(const CUtensorMap& map, const PrefixArgs& p, cudaStream_t st) {
     constexpr int rows = MODE == 0 ? 2 * kPRows : kPRows;
@@ -328,16 +345,9 @@ cudaError_t launch_mode(const CUtensorMap& map, const PrefixArgs& p, cudaStream_
 }  // namespace
 
 cudaError_t launch_prefix_bf16(const PrefixArgs& p, int block_size, cudaStream_t st) {
-    const EncodeTiled enc = encode_tiled();
-    if (!enc) return cudaErrorNotSupported;
     CUtensorMap map;
-    const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)p.n_pool_blocks * p.n_kv * 2 * block_size};
-    const cuuint64_t strides[1] = {kD * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)block_size}, one[2] = {1, 1};
-    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t*>(p.pool), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
+    const cudaError_t e = bf16_page_map(&map, p.pool, p.n_pool_blocks, p.n_kv, block_size);
+    if (e != cudaSuccess) return e;
     const int64_t R = (int64_t)p.batch * p.G;
     const int mode = p.q_dtype == KVARN_FP32 ? 2 : (R > kPRows ? 0 : 1);
     if (block_size == 32)

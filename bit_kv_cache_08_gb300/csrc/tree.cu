@@ -2,9 +2,11 @@
 // over all cached tokens and over the drafted ones that its mask shows.
 #include "host_checks.h"
 #include "quantize.cuh"
-#include "tree.cuh"
+#include "tree_join.cuh"
 
 namespace kvarn {
+
+cudaError_t launch_tree_bf16(const TreeArgs& a, cudaStream_t st);
 
 constexpr int kSimpleRows = 16;   // query rows of a CTA: 4 a warp
 
@@ -169,7 +171,27 @@ __global__ void __launch_bounds__(128) tree_simple_kernel(TreeArgs a) {
 
 namespace {
 
-size_t tree_ws_bytes(const kvarn_config&, int32_t, int32_t, int32_t) { return kWsHeader; }
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// How a call is cut: its row tiles, and the ranges of cached tokens that fill the
+// GPU with them, two CTAs an SM.
+struct TreePlan {
+    int row_tiles, rows_pad, ranges;
+};
+TreePlan tree_plan(const kvarn_config& c, int drafts) {
+    const int R = drafts * (c.n_q_heads / c.n_kv_heads);
+    TreePlan p{(R + kPRows - 1) / kPRows, (R + 31) / 32 * 32, 0};
+    p.ranges = (int)(2 * current_device_sms() / p.row_tiles);
+    return p;
+}
+
+size_t tree_ws_bytes(const kvarn_config& c, int32_t batch, int32_t drafts, int32_t) {
+    if (batch == 0) return kWsHeader;
+    const TreePlan p = tree_plan(c, drafts);
+    if (p.ranges <= 0) return 0;
+    const size_t units = (size_t)batch * c.n_kv_heads;
+    return align256(kWsHeader + units * 2 * sizeof(int32_t)) + (units + p.ranges) * 33 * p.rows_pad * sizeof(float4);
+}
 
 template <bool PACKED>
 int tree_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* pool, int64_t n_pool_blocks,
@@ -192,6 +214,7 @@ int tree_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const voi
     if (k_stride % 8 || v_stride % 8 || k_stride < (int64_t)c.n_kv_heads * kD || v_stride < (int64_t)c.n_kv_heads * kD)
         return KVARN_ERR_INVALID_ARG;
     if (batch > 65535 || c.n_kv_heads > 65535) return KVARN_ERR_INVALID_ARG;
+    if (!PACKED && n_pool_blocks > 0x7fffffff / ((int64_t)c.n_kv_heads * 2 * c.block_size)) return KVARN_ERR_INVALID_ARG;
     const size_t need = tree_ws_bytes(c, batch, drafts, max_blocks);
     if (need == 0) return KVARN_ERR_CUDA;
     if (workspace_bytes < need) return KVARN_ERR_WORKSPACE;
@@ -225,6 +248,24 @@ int tree_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const voi
     a.sm_scale = c.sm_scale;
     a.flags = c.flags;
     for (int i = 0; i < 4; ++i) a.sb[i] = c.sign_bits[i];
+    const TreePlan plan = tree_plan(c, drafts);
+    a.B = c.block_size;
+    a.unit_map = (int32_t*)((uint8_t*)workspace + kWsHeader);
+    const int64_t units = (int64_t)batch * c.n_kv_heads;
+    a.partials = (float4*)((uint8_t*)workspace + align256(kWsHeader + units * 2 * sizeof(int32_t)));
+    a.row_tiles = plan.row_tiles;
+    a.rows_pad = plan.rows_pad;
+    a.ranges = plan.ranges;
+    a.late = max_blocks > 0;
+    if constexpr (!PACKED) {
+        cudaError_t e = max_blocks > 0 ? launch_tree_bf16(a, st) : cudaSuccess;
+        if (e != cudaSuccess) return KVARN_ERR_CUDA;
+        const int64_t warps = units * ((drafts * a.G + kJoinRows - 1) / kJoinRows);
+        const unsigned ctas = (unsigned)((warps + kTreeJoinWarps - 1) / kTreeJoinWarps);
+        e = q_dtype == KVARN_FP32 ? launch_pdl(tree_join_kernel<false, true>, ctas, 32 * kTreeJoinWarps, 0, st, a)
+                                  : launch_pdl(tree_join_kernel<false, false>, ctas, 32 * kTreeJoinWarps, 0, st, a);
+        return e == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
+    }
     const dim3 grid((drafts * a.G + kSimpleRows - 1) / kSimpleRows, c.n_kv_heads, batch);
     const cudaError_t e = dispatch(c, [&](auto b, auto w) {
         return launch_pdl(tree_simple_kernel<decltype(b)::value, decltype(w)::value, PACKED>, grid, 128, 0, st, a);
