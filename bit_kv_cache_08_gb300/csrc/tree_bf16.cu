@@ -89,52 +89,60 @@ __global__ void __launch_bounds__(192, Q32 ? 1 : 2) tree_bf16_kernel(const __gri
 
     if (warp == 5) {
         // ---------------------------------------------------------- page copies
+        // Keys of tile g + 2 right behind the values of tile g: what S(g) and the
+        // product of P(g - 2), issued together, set free. (Keys and values of one tile
+        // together had the keys wait for the values' stage: 64 x 16 drafts over 8K 342 us a call, 268 so.)
         constexpr int PPT = kTreeTok / B;                // pages per tile
-        for (int64_t x = x_beg; x < x_end && ok;) {
-            const int n = (int)min((int64_t)(c.tiles - c.t), x_end - x);
-            const int used = (c.tokens + B - 1) / B;     // pages that hold a token
-            int held = -1, held0 = -32;                  // lane i: page held0 + i of the sequence
-            for (int i = 0; i < n && ok; ++i, ++g) {
-                const int t = c.t + i, st = g & 1, first = t * PPT;
-                if (first >= held0 + 32) {               // (32 is a multiple of PPT, and the first one even)
-                    held0 = first;
-                    held = first + lane < used ? a.table[(int64_t)c.b * a.max_blocks + first + lane] : -1;
-                    if (first + lane < used && (held < 0 || held >= a.n_pool_blocks)) {
+        const int total = (int)(x_end - x_beg);
+        struct {
+            TreeCursor c;
+            int held, held0;                             // lane i holds page held0 + i of the sequence
+        } at[2] = {{c, -1, -32}, {c, -1, -32}};
+        for (int step = 0; step < total + 2 && ok; ++step) {
+#pragma unroll
+            for (int kind = 1; kind >= 0; --kind) {      // V of tile step - 2, K of tile step
+                const int i = kind ? step - 2 : step, st = i & 1;
+                if (i < 0 || i >= total || !ok) continue;
+                auto& me = at[kind];
+                const int first = me.c.t * PPT, used = (me.c.tokens + B - 1) / B;   // pages: of the tile; that hold a token
+                if (first >= me.held0 + 32) {            // (32 is a multiple of PPT, and so is every `first`)
+                    me.held0 = first;
+                    me.held = first + lane < used ? a.table[(int64_t)me.c.b * a.max_blocks + first + lane] : -1;
+                    if (first + lane < used && (me.held < 0 || me.held >= a.n_pool_blocks)) {
                         raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
-                        held = -1;
+                        me.held = -1;
                     }
                 }
                 const int p = lane >> 1, half = lane & 1;
-                int page = __shfl_sync(kFull, held, (first - held0 + p) & 31);
+                int page = __shfl_sync(kFull, me.held, (first - me.held0 + p) & 31);
                 if (p >= PPT) page = -1;                 // (a page behind the end is -1 too)
                 const uint32_t bytes = __popc(__ballot_sync(kFull, page >= 0)) * (B * 128);
-                const int y = (int)(((int64_t)max(page, 0) * a.n_kv + c.h) * 2 * B);
-                for (int kind = 0; kind < 2; ++kind) {
-                    uint64_t* full = kind ? &s.v_full[st] : &s.k_full[st];
-                    if (g >= 2) ok = warp_wait_or_stop(kind ? &s.v_empty[st] : &s.k_empty[st], ((g >> 1) - 1) & 1, stop, kWaitLimit);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-                    __syncwarp();
-                    if (page >= 0)
-                        tile_g2s((kind ? v_op : k_op) + st * kTbKv + half * (kTbKv / 2) + p * B * 128, &map, 64 * half,
-                                 y + kind * B, full);
-                    __syncwarp();
-                    (kind ? issued_v : issued_k) = g + 1;
-                }
+                const int y = (int)(((int64_t)max(page, 0) * a.n_kv + me.c.h) * 2 * B);
+                uint64_t* full = kind ? &s.v_full[st] : &s.k_full[st];
+                if (i >= 2) ok = warp_wait_or_stop(kind ? &s.v_empty[st] : &s.k_empty[st], ((i >> 1) - 1) & 1, stop, kWaitLimit);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                __syncwarp();
+                if (page >= 0)
+                    tile_g2s((kind ? v_op : k_op) + st * kTbKv + half * (kTbKv / 2) + p * B * 128, &map, 64 * half, y + kind * B, full);
+                __syncwarp();
+                (kind ? issued_v : issued_k) = i + 1;
                 // value rows behind the sequence's end: a weight of 0 times whatever the
                 // page or an earlier tile holds must be 0
-                const int valid = c.tokens - t * kTreeTok;
-                if (ok && valid < kTreeTok) {
-                    ok = warp_wait_or_stop(&s.v_full[st], (g >> 1) & 1, stop, kWaitLimit);
+                const int valid = me.c.tokens - me.c.t * kTreeTok;
+                if (kind && valid < kTreeTok) {
+                    ok = warp_wait_or_stop(&s.v_full[st], (i >> 1) & 1, stop, kWaitLimit);
                     for (int r = valid * 8 + lane; r < kTreeTok * 8; r += 32)
                         for (int k = 0; k < 2; ++k)
                             *reinterpret_cast<uint4*>(v_op + st * kTbKv + k * (kTbKv / 2) + r * 16) = make_uint4(0, 0, 0, 0);
                     fence_async_smem();
                     warp_arrive(&s.v_clean[st]);
                 }
+                if (++me.c.t == me.c.tiles && i + 1 < total) {
+                    tree_next<false>(a, me.c);
+                    me.held0 = -32;
+                }
             }
-            x += n;
-            if (x < x_end) tree_next<false>(a, c);
         }
     } else if (warp == 4) {
         // ---------------------------------------------------------- products
