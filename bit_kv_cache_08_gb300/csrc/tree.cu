@@ -6,7 +6,7 @@
 
 namespace kvarn {
 
-cudaError_t launch_tree_bf16(const TreeArgs& a, cudaStream_t st);
+cudaError_t launch_tree_bf16(const TreeArgs& a, bool wide, cudaStream_t st);
 
 constexpr int kSimpleRows = 16;   // query rows of a CTA: 4 a warp
 
@@ -173,24 +173,28 @@ namespace {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// How a call is cut: its row tiles, and the ranges of cached tokens that fill the
-// GPU with them, two CTAs an SM.
+// How a call is cut: CTAs that share a unit's query rows (128 each, or 256 where
+// there are more: `wide`), and ranges of cached tokens, as many as fill the GPU with them.
 struct TreePlan {
+    bool wide;
     int row_tiles, rows_pad, ranges;
 };
-TreePlan tree_plan(const kvarn_config& c, int drafts) {
+TreePlan tree_plan(const kvarn_config& c, int drafts, int q_dtype) {
     const int R = drafts * (c.n_q_heads / c.n_kv_heads);
-    TreePlan p{(R + kPRows - 1) / kPRows, (R + 31) / 32 * 32, 0};
-    p.ranges = (int)(2 * current_device_sms() / p.row_tiles);
+    TreePlan p{R > kPRows && q_dtype == KVARN_BF16, 0, (R + 31) / 32 * 32, 0};
+    const int rows = p.wide ? 2 * kPRows : kPRows;
+    p.row_tiles = (R + rows - 1) / rows;
+    const int ctas = p.wide || q_dtype == KVARN_FP32 ? 1 : 2;   // an SM
+    p.ranges = (int)(ctas * current_device_sms() / p.row_tiles);
     return p;
 }
 
 size_t tree_ws_bytes(const kvarn_config& c, int32_t batch, int32_t drafts, int32_t) {
     if (batch == 0) return kWsHeader;
-    const TreePlan p = tree_plan(c, drafts);
-    if (p.ranges <= 0) return 0;
-    const size_t units = (size_t)batch * c.n_kv_heads;
-    return align256(kWsHeader + units * 2 * sizeof(int32_t)) + (units + p.ranges) * 33 * p.rows_pad * sizeof(float4);
+    const TreePlan p = tree_plan(c, drafts, KVARN_BF16), q = tree_plan(c, drafts, KVARN_FP32);
+    if (p.ranges <= 0 || q.ranges <= 0) return 0;
+    const size_t units = (size_t)batch * c.n_kv_heads, ranges = p.ranges > q.ranges ? p.ranges : q.ranges;
+    return align256(kWsHeader + units * 2 * sizeof(int32_t)) + (units + ranges) * 33 * p.rows_pad * sizeof(float4);
 }
 
 template <bool PACKED>
@@ -248,7 +252,7 @@ int tree_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const voi
     a.sm_scale = c.sm_scale;
     a.flags = c.flags;
     for (int i = 0; i < 4; ++i) a.sb[i] = c.sign_bits[i];
-    const TreePlan plan = tree_plan(c, drafts);
+    const TreePlan plan = tree_plan(c, drafts, q_dtype);
     a.B = c.block_size;
     a.unit_map = (int32_t*)((uint8_t*)workspace + kWsHeader);
     const int64_t units = (int64_t)batch * c.n_kv_heads;
@@ -258,12 +262,9 @@ int tree_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const voi
     a.ranges = plan.ranges;
     a.late = max_blocks > 0;
     if constexpr (!PACKED) {
-        cudaError_t e = max_blocks > 0 ? launch_tree_bf16(a, st) : cudaSuccess;
+        cudaError_t e = max_blocks > 0 ? launch_tree_bf16(a, plan.wide, st) : cudaSuccess;
         if (e != cudaSuccess) return KVARN_ERR_CUDA;
-        const int64_t warps = units * ((drafts * a.G + kJoinRows - 1) / kJoinRows);
-        const unsigned ctas = (unsigned)((warps + kTreeJoinWarps - 1) / kTreeJoinWarps);
-        e = q_dtype == KVARN_FP32 ? launch_pdl(tree_join_kernel<false, true>, ctas, 32 * kTreeJoinWarps, 0, st, a)
-                                  : launch_pdl(tree_join_kernel<false, false>, ctas, 32 * kTreeJoinWarps, 0, st, a);
+        e = launch_tree_join<false>(a, st);
         return e == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
     }
     const dim3 grid((drafts * a.G + kSimpleRows - 1) / kSimpleRows, c.n_kv_heads, batch);

@@ -5,7 +5,6 @@
 
 namespace kvarn {
 
-constexpr int kTreeTok = 64;      // cached tokens of a tile
 
 struct TreeArgs {
     const void* q;               // [batch][drafts][n_q][128]
@@ -24,7 +23,7 @@ struct TreeArgs {
     int q_dtype, out_bf16;
     int max_blocks, B, batch, drafts, words;
     int n_q, n_kv, G;
-    int row_tiles, rows_pad;     // of 128 query rows; query rows of a unit, to a multiple of 32
+    int row_tiles, rows_pad;     // CTAs that share a unit's query rows; the rows, to a multiple of 32
     int ranges;                  // that the tiles of all units are cut into, at most
     int late;                    // the join comes behind a kernel of this call
     float sm_scale;
@@ -48,25 +47,25 @@ __device__ __forceinline__ int tree_tokens(const TreeArgs& a, int b) {
     return PACKED ? L / a.B * a.B : L;
 }
 
-// A unit is a (sequence, kv head). The 64-token tiles of all units lie end to end, sequence by
+// A unit is a (sequence, kv head). The tiles (of TOK tokens) of all units lie end to end, sequence by
 // sequence, kv head by kv head, and range r of the n in use takes tiles
 // [r W / n, (r + 1) W / n) of the W, so that ragged lengths are balanced; a range
 // writes a partial for each unit that it touches, in slot unit + range.
 struct TreeCursor {
     int b, h, t, tiles, tokens;   // tile t of `tiles`, which hold `tokens`
 };
-template <bool PACKED>
+template <int TOK, bool PACKED>
 __device__ __forceinline__ void tree_enter(const TreeArgs& a, TreeCursor& c) {
     c.tokens = tree_tokens<PACKED>(a, c.b);
-    c.tiles = (c.tokens + kTreeTok - 1) / kTreeTok;
+    c.tiles = (c.tokens + TOK - 1) / TOK;
 }
 // All tiles (warp-cooperative); where x is one of them, c is put there.
-template <bool PACKED>
+template <int TOK, bool PACKED>
 __device__ __forceinline__ int64_t tree_locate(const TreeArgs& a, int64_t x, int lane, TreeCursor& c) {
     int64_t before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
         const int b = b0 + lane;
-        const int64_t mine = b < a.batch ? (int64_t)((tree_tokens<PACKED>(a, b) + kTreeTok - 1) / kTreeTok) * a.n_kv : 0;
+        const int64_t mine = b < a.batch ? (int64_t)((tree_tokens<PACKED>(a, b) + TOK - 1) / TOK) * a.n_kv : 0;
         int64_t upto = mine;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
@@ -79,7 +78,7 @@ __device__ __forceinline__ int64_t tree_locate(const TreeArgs& a, int64_t x, int
             const int src = __ffs(hit) - 1;
             const int64_t in = x - __shfl_sync(kFull, upto - mine, src);
             c.b = b0 + src;
-            tree_enter<PACKED>(a, c);
+            tree_enter<TOK, PACKED>(a, c);
             c.h = (int)(in / c.tiles);
             c.t = (int)(in % c.tiles);
         }
@@ -88,14 +87,14 @@ __device__ __forceinline__ int64_t tree_locate(const TreeArgs& a, int64_t x, int
     return before;
 }
 // The next unit that has tiles (the caller knows that there is one).
-template <bool PACKED>
+template <int TOK, bool PACKED>
 __device__ __forceinline__ void tree_next(const TreeArgs& a, TreeCursor& c) {
     c.t = 0;
     if (++c.h < a.n_kv) return;
     c.h = 0;
     do {
         ++c.b;
-        tree_enter<PACKED>(a, c);
+        tree_enter<TOK, PACKED>(a, c);
     } while (c.tiles == 0);
 }
 // Ranges in use.

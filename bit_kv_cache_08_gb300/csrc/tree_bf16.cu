@@ -3,21 +3,25 @@
 //
 // The R = drafts * G query rows of a (sequence, kv head) meet the same tokens, so
 // that S = Q K^T, P = 2^(scale S - m) and O += P V are matrix products of R rows, and
-// the pages are read once for all drafts. A CTA takes 128 rows and a range of
-// 64-token tiles (tree.cuh), which may go on from one unit to the next; it leaves
-// a partial (m, l, O) of each. CTAs of the row tiles of one range are neighbours, so
-// that the second reads what the first has just brought to L2.
-//
-// Two CTAs share an SM. In each:
-//   S (128 x 64 fp32)  two in tensor memory: one tile's products run under the
-//                      softmax of the tile before
-//   softmax            128 threads, a row each; P as two bf16 halves over S, the A
-//                      operand of
-//   O (128 x 128 fp32) tensor memory; V straight from its page rows
-// Warps 0-3 softmax, 4 issues the products, 5 copies pages (a tile copy per page
-// and 64-channel half, swizzled; two stages each of K and V), across the units'
-// borders: the next unit's pages are on their way while this one's result is stored
-// and the next queries are loaded.
+// the pages are read once for all drafts. A CTA takes a range of tiles of tokens
+// (tree.cuh), which may go on from one unit to the next, and leaves a partial (m, l, O) of each
+// unit. Two forms:
+//   NT 1  up to 128 rows and 64-token tiles, two CTAs an SM. HBM bounds it: two CTAs cover
+//         each other's waits and ends of units. S of a tile runs under the softmax of the
+//         tile before (two S in tensor memory, one O).
+//   NT 2  up to 256 rows and 128-token tiles, a CTA an SM. The tensor core bounds it (three products
+//         of 256 rows for 512 bytes a token): two row tiles share the keys and
+//         values in shared memory and take turns, one in its products while the other is
+//         in its softmax; products of 128 tokens read shared memory at the rate of the tensor core,
+//         those of 64 do not.
+// Per row tile:
+//   S (128 rows, fp32)  tensor memory
+//   softmax             128 threads, a row each; P as two bf16 halves over S, the A operand of
+//   O (128 x 128 fp32)  tensor memory; V straight from its page rows
+// Warps: 4 a row tile for the softmax, one that issues the products, one that copies pages (a tile copy
+// per page and 64-channel half, swizzled; two stages each of K and V), across the
+// units' borders: the next unit's pages are on their way while this one's result is
+// stored and the next queries are loaded.
 //
 // Rounding: as in the shared prefix over bf16 pages (P two halves, 2^-16; an fp32
 // query two, one more product).
@@ -29,37 +33,48 @@ namespace kvarn {
 
 cudaError_t bf16_page_map(CUtensorMap* map, const uint8_t* pool, int64_t n_pool_blocks, int n_kv, int block_size);
 
-constexpr int kTbQ = kPRows * kD * 2;        // bytes of the 128 x 128 query operand
-constexpr int kTbKv = kTreeTok * kD * 2;     // of a 64 x 128 tile: two 64-channel blocks
+constexpr int kTbQ = kPRows * kD * 2;        // bytes of a 128 x 128 query operand
 
 struct TreeBf16Smem {
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], v_clean[2], o_full, q_full, drained;
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], v_clean[2], o_full[2], q_full, drained;
     uint32_t tmem;
     int stop;
 };
 constexpr int kTbHeader = 1024;
 static_assert(sizeof(TreeBf16Smem) <= kTbHeader, "header");
-constexpr size_t tree_bf16_smem(bool q32) { return 1024 + kTbHeader + (q32 ? 2 : 1) * kTbQ + 4 * kTbKv; }
 
-template <int B, bool Q32>
-__global__ void __launch_bounds__(192, Q32 ? 1 : 2) tree_bf16_kernel(const __grid_constant__ CUtensorMap map, TreeArgs a) {
+template <bool Q32, int NT>
+struct TreeBf16Form {
+    static_assert(!Q32 || NT == 1, "an fp32 query is two operands");
+    static constexpr int kTok = 64 * NT, kKv = kTok * kD * 2;   // tokens of a tile, bytes of its K or V: two 64-channel blocks
+    static constexpr int kSoft = 4 * NT, kThreads = 32 * (kSoft + 2);
+    static constexpr int kQ = (Q32 ? 2 : 1) * NT * kTbQ;
+    static constexpr uint32_t kColumns = 256 * NT;              // of tensor memory: two S, and NT O
+    static constexpr size_t kSmem = 1024 + kTbHeader + kQ + 4 * kKv;
+};
+
+template <int B, bool Q32, int NT>
+__global__ void __launch_bounds__(TreeBf16Form<Q32, NT>::kThreads, Q32 || NT == 2 ? 1 : 2) tree_bf16_kernel(const __grid_constant__ CUtensorMap map, TreeArgs a) {
     wait_prior_grids();
     let_next_grid_start();   // the join
+    using Form = TreeBf16Form<Q32, NT>;
+    constexpr int TOK = Form::kTok, kKv = Form::kKv, kSoft = Form::kSoft;
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);   // the swizzle's period
     TreeBf16Smem& s = *reinterpret_cast<TreeBf16Smem*>(base);
     uint8_t* q_op = base + kTbHeader;
-    uint8_t* k_op = q_op + (Q32 ? 2 : 1) * kTbQ;
-    uint8_t* v_op = k_op + 2 * kTbKv;
+    uint8_t* k_op = q_op + Form::kQ;
+    uint8_t* v_op = k_op + 2 * kKv;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rt = blockIdx.x % a.row_tiles;
     const int64_t range = blockIdx.x / a.row_tiles;
 
     TreeCursor c = {};
-    const int64_t W = tree_locate<false>(a, -1, lane, c), n_ranges = tree_ranges(W, a.ranges);
+    const int64_t W = tree_locate<TOK, false>(a, -1, lane, c), n_ranges = tree_ranges(W, a.ranges);
     if (range >= n_ranges) return;
-    const int64_t x_beg = range * W / n_ranges, x_end = (range + 1) * W / n_ranges;
-    tree_locate<false>(a, x_beg, lane, c);
+    const int64_t x_beg = range * W / n_ranges;
+    const int total = (int)((range + 1) * W / n_ranges - x_beg);   // tiles of this CTA
+    tree_locate<TOK, false>(a, x_beg, lane, c);
 
     if (tid == 0) {
         s.stop = 0;
@@ -71,29 +86,29 @@ __global__ void __launch_bounds__(192, Q32 ? 1 : 2) tree_bf16_kernel(const __gri
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_ready[i], 4);
             mbar_init(&s.v_clean[i], 1);
+            mbar_init(&s.o_full[i], 1);
         }
-        mbar_init(&s.o_full, 1);
-        mbar_init(&s.q_full, 4);
+        mbar_init(&s.q_full, kSoft);
         mbar_init(&s.drained, 1);
         fence_mbar_init();
     }
-    if (warp == 4) tmem_alloc(&s.tmem, 256);
+    if (warp == kSoft) tmem_alloc(&s.tmem, Form::kColumns);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm_s = s.tmem, tm_o = s.tmem + 128;   // S (and P) of tile g at + 64 (g % 2)
+    // S (and P) at + TOK w: of tile g, w = g % 2 (NT 1), of row tile w (NT 2); O of a row tile at + 128
+    const uint32_t tm_s = s.tmem, tm_o = s.tmem + 2 * TOK;
     int* stop = &s.stop;
-    int issued_k = 0, issued_v = 0;                      // tiles whose copies warp 5 has issued
+    int issued_k = 0, issued_v = 0;                      // tiles whose copies have been issued
     int g = 0;                                           // tiles of this CTA so far: stage g % 2, phase g / 2
     bool ok = true;
 
-    if (warp == 5) {
+    if (warp == kSoft + 1) {
         // ---------------------------------------------------------- page copies
         // Keys of tile g + 2 right behind the values of tile g: what S(g) and the
         // product of P(g - 2), issued together, set free. (Keys and values of one tile
         // together had the keys wait for the values' stage: 64 x 16 drafts over 8K 342 us a call, 268 so.)
-        constexpr int PPT = kTreeTok / B;                // pages per tile
-        const int total = (int)(x_end - x_beg);
+        constexpr int PPT = TOK / B;                // pages per tile
         struct {
             TreeCursor c;
             int held, held0;                             // lane i holds page held0 + i of the sequence
@@ -124,88 +139,94 @@ __global__ void __launch_bounds__(192, Q32 ? 1 : 2) tree_bf16_kernel(const __gri
                 if (lane == 0) mbar_arrive_expect_tx(full, bytes);
                 __syncwarp();
                 if (page >= 0)
-                    tile_g2s((kind ? v_op : k_op) + st * kTbKv + half * (kTbKv / 2) + p * B * 128, &map, 64 * half, y + kind * B, full);
+                    tile_g2s((kind ? v_op : k_op) + st * kKv + half * (kKv / 2) + p * B * 128, &map, 64 * half, y + kind * B, full);
                 __syncwarp();
                 (kind ? issued_v : issued_k) = i + 1;
                 // value rows behind the sequence's end: a weight of 0 times whatever the
                 // page or an earlier tile holds must be 0
-                const int valid = me.c.tokens - me.c.t * kTreeTok;
-                if (kind && valid < kTreeTok) {
+                const int valid = me.c.tokens - me.c.t * TOK;
+                if (kind && valid < TOK) {
                     ok = warp_wait_or_stop(&s.v_full[st], (i >> 1) & 1, stop, kWaitLimit);
-                    for (int r = valid * 8 + lane; r < kTreeTok * 8; r += 32)
+                    for (int r = valid * 8 + lane; r < TOK * 8; r += 32)
                         for (int k = 0; k < 2; ++k)
-                            *reinterpret_cast<uint4*>(v_op + st * kTbKv + k * (kTbKv / 2) + r * 16) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(v_op + st * kKv + k * (kKv / 2) + r * 16) = make_uint4(0, 0, 0, 0);
                     fence_async_smem();
                     warp_arrive(&s.v_clean[st]);
                 }
                 if (++me.c.t == me.c.tiles && i + 1 < total) {
-                    tree_next<false>(a, me.c);
+                    tree_next<TOK, false>(a, me.c);
                     me.held0 = -32;
                 }
             }
         }
-    } else if (warp == 4) {
+    } else if (warp == kSoft) {
         // ---------------------------------------------------------- products
-        constexpr uint32_t kQk = mma_shape(kMmaBf16, kTreeTok, false), kPv = mma_shape(kMmaBf16, kD, true);
+        constexpr uint32_t kQk = mma_shape(kMmaBf16, TOK, false), kPv = mma_shape(kMmaBf16, kD, true);
         const uint32_t q_desc = smem_operand(smem_addr(q_op), 16), k_desc = smem_operand(smem_addr(k_op), 16);
-        const uint32_t v_desc = smem_operand(smem_addr(v_op), kTbKv / 2);
+        const uint32_t v_desc = smem_operand(smem_addr(v_op), kKv / 2);
         int units = 0, cleaned = 0;                      // (cleaned: bit w, the phase of v_clean[w])
         ok = !(a.flags & KVARN_FLAG_TEST_WAIT_TIMEOUT);
         if (!ok && lane == 0) *stop = 1;                 // (test switch: as if the first wait had run out)
-        for (int64_t x = x_beg; x < x_end && ok;) {
-            const int n = (int)min((int64_t)(c.tiles - c.t), x_end - x);
-            const bool cut = c.tokens % kTreeTok != 0 && c.t + n == c.tiles;   // the last tile has rows behind the end
+        while (g < total && ok) {
+            const int n = min(c.tiles - c.t, total - g);
+            const bool cut = c.tokens % TOK != 0 && c.t + n == c.tiles;   // the last tile has rows behind the end
             ok = warp_wait_or_stop(&s.q_full, units & 1, stop, kWaitLimit);
-            for (int i = 0; i < n + 2 && ok; ++i) {      // O (+)= P V of tile j, then S = Q K^T of tile i
-                const int j = i - 2, gi = g + i, gj = g + j, w = gi & 1;
-                if (i < n) ok = warp_wait_or_stop(&s.k_full[w], (gi >> 1) & 1, stop, kWaitLimit);
+            // O (+)= P V of step i - 2, then S = Q K^T of step i; a step is a tile (NT 1) or a
+            // row tile of one, the second behind the first (NT 2)
+            for (int i = 0; i < NT * n + 2 && ok; ++i) {
+                const int j = i - 2, ti = g + i / NT, tj = g + (NT == 2 ? (i >> 1) - 1 : j);   // (tiles)
+                const int w = NT == 2 ? i & 1 : ti & 1, x = NT == 2 ? w : 0;
+                const bool lead = NT == 1 || w == 0, trail = NT == 1 || w == 1;
+                if (i < NT * n && lead) ok = warp_wait_or_stop(&s.k_full[ti & 1], (ti >> 1) & 1, stop, kWaitLimit);
                 if (j >= 0) {
-                    ok = ok && warp_wait_or_stop(&s.v_full[w], (gj >> 1) & 1, stop, kWaitLimit);
-                    if (ok && cut && j == n - 1) ok = warp_wait_or_stop(&s.v_clean[w], cleaned >> w & 1, stop, kWaitLimit);
-                    ok = ok && warp_wait_or_stop(&s.p_ready[w], (gj >> 1) & 1, stop, kWaitLimit);
+                    if (lead) {
+                        ok = ok && warp_wait_or_stop(&s.v_full[tj & 1], (tj >> 1) & 1, stop, kWaitLimit);
+                        if (ok && cut && tj == g + n - 1) ok = warp_wait_or_stop(&s.v_clean[tj & 1], cleaned >> (tj & 1) & 1, stop, kWaitLimit);
+                    }
+                    ok = ok && warp_wait_or_stop(&s.p_ready[w], (NT == 2 ? tj : tj >> 1) & 1, stop, kWaitLimit);
                 }
                 if (!ok) break;
                 tc_fence_after();
                 if (j >= 0) {
-                    const uint32_t p = tm_s + 64 * w, vd = v_desc + w * (kTbKv >> 4);
+                    const uint32_t p = tm_s + TOK * w, vd = v_desc + (tj & 1) * (kKv >> 4);
 #pragma unroll
-                    for (int k = 0; k < kTreeTok / 16; ++k) {   // 16 tokens: 8 columns of each half of P, 2048 bytes of V rows
-                        mma_ts(tm_o, p + 16 * k, vd + k * (2048 >> 4), kPv, j > 0 || k > 0);
-                        mma_ts(tm_o, p + 16 * k + kPLow, vd + k * (2048 >> 4), kPv, true);
+                    for (int k = 0; k < TOK / 16; ++k) {   // 16 tokens: 8 columns of each half of P, 2048 bytes of V rows
+                        mma_ts(tm_o + 128 * x, p + 16 * k, vd + k * (2048 >> 4), kPv, j >= NT || k > 0);
+                        mma_ts(tm_o + 128 * x, p + 16 * k + kPLow, vd + k * (2048 >> 4), kPv, true);
                     }
-                    mma_commit(&s.v_empty[w]);
-                    if (j == n - 1) mma_commit(&s.o_full);
+                    if (trail) mma_commit(&s.v_empty[tj & 1]);
+                    if (tj == g + n - 1) mma_commit(&s.o_full[x]);
                 }
-                if (i < n) {
-                    const uint32_t kd = k_desc + w * (kTbKv >> 4);
+                if (i < NT * n) {
+                    const uint32_t kd = k_desc + (ti & 1) * (kKv >> 4);
 #pragma unroll
                     for (int k = 0; k < (Q32 ? 16 : 8); ++k) {  // (k >= 8: the query's low halves)
                         const uint32_t in = (k & 3) * 32;
-                        mma_ss(tm_s + 64 * w, q_desc + (k >> 3) * (kTbQ >> 4) + (((k >> 2 & 1) * (kTbQ / 2) + in) >> 4),
-                               kd + (((k >> 2 & 1) * (kTbKv / 2) + in) >> 4), kQk, k > 0);
+                        mma_ss(tm_s + TOK * w, q_desc + (x + (k >> 3)) * (kTbQ >> 4) + (((k >> 2 & 1) * (kTbQ / 2) + in) >> 4),
+                               kd + (((k >> 2 & 1) * (kKv / 2) + in) >> 4), kQk, k > 0);
                     }
                     mma_commit(&s.s_full[w]);
-                    mma_commit(&s.k_empty[w]);
+                    if (trail) mma_commit(&s.k_empty[ti & 1]);
                 }
             }
             if (cut) cleaned ^= 1 << (g + n - 1 & 1);
             g += n;
-            x += n;
             ++units;
-            if (x < x_end) tree_next<false>(a, c);
+            if (g < total) tree_next<TOK, false>(a, c);
         }
         // products in flight end before the operands and tensor memory go
         mma_commit(&s.drained);
         if (!mbar_wait_bounded(&s.drained, 0, kWaitLimit)) *stop = 1;
     } else {
         // ---------------------------------------------------------- softmax
-        const int r = rt * kPRows + tid;                 // this thread's query row of a unit
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        const uint32_t my_o = tm_o + lanes;
+        const int x = warp >> 2;                         // row tile of the CTA
+        const int r = rt * NT * kPRows + tid;            // this thread's query row of a unit
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t my_o = tm_o + 128 * x + lanes;
         const float scale = a.sm_scale * kLog2e;
         int units = 0;
-        for (int64_t x = x_beg; x < x_end && ok; ++units) {
-            const int n = (int)min((int64_t)(c.tiles - c.t), x_end - x);
+        for (; g < total && ok; ++units) {
+            const int n = min(c.tiles - c.t, total - g);
             const int rows = tree_rows(a, c.b) * a.G;
             const bool valid = r < rows, some = __any_sync(kFull, valid);
             // the query rows as a swizzled operand (rows behind the last draft: zeros):
@@ -216,7 +237,7 @@ __global__ void __launch_bounds__(192, Q32 ? 1 : 2) tree_bf16_kernel(const __gri
                 uint4 v0[kBatch], v1[Q32 ? kBatch : 1];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const int row = rt * kPRows + warp * 32 + 2 * (i0 + i) + (lane >> 4);
+                    const int row = rt * NT * kPRows + warp * 32 + 2 * (i0 + i) + (lane >> 4);
                     v0[i] = make_uint4(0, 0, 0, 0);
                     if (Q32) v1[i] = v0[i];
                     if (row < rows) {
@@ -229,7 +250,7 @@ __global__ void __launch_bounds__(192, Q32 ? 1 : 2) tree_bf16_kernel(const __gri
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     const int u = lane & 15;
-                    uint8_t* dst = q_op + (u >> 3) * (kTbQ / 2) + swizzled(warp * 32 + 2 * (i0 + i) + (lane >> 4), u & 7);
+                    uint8_t* dst = q_op + x * kTbQ + (u >> 3) * (kTbQ / 2) + swizzled((warp & 3) * 32 + 2 * (i0 + i) + (lane >> 4), u & 7);
                     if (Q32) {
                         const uint32_t f[8] = {v0[i].x, v0[i].y, v0[i].z, v0[i].w, v1[i].x, v1[i].y, v1[i].z, v1[i].w};
                         uint32_t hi[4], lo[4];
@@ -249,25 +270,27 @@ __global__ void __launch_bounds__(192, Q32 ? 1 : 2) tree_bf16_kernel(const __gri
             RowState st{-INFINITY, 0.f};
             const int len = valid ? c.tokens : 0;
             for (int i = 0; i < n; ++i, ++g) {
-                const int w = g & 1;
-                ok = warp_wait_or_stop(&s.s_full[w], (g >> 1) & 1, stop, kWaitLimit);
+                const int w = NT == 2 ? x : g & 1;
+                ok = warp_wait_or_stop(&s.s_full[w], (NT == 2 ? g : g >> 1) & 1, stop, kWaitLimit);
                 if (!ok) break;
                 tc_fence_after();
                 if (!some) {                             // (rows that nothing reads)
                     warp_arrive(&s.p_ready[w]);
                     continue;
                 }
-                ok = softmax_tile<kTreeTok, kTreeTok, false>(tm_s + 64 * w + lanes, my_o, len - (c.t + i) * kTreeTok, scale, 0.f, 1.f, 0.f,
-                                                             i == 0, st, &s.p_ready[w], [&] {
-                    // O is idle once tile i - 1's product has freed its values
+                ok = softmax_tile<TOK, TOK, false>(tm_s + TOK * w + lanes, my_o, len - (c.t + i) * TOK, scale, 0.f, 1.f, 0.f, i == 0, st,
+                                                   &s.p_ready[w], [&] {
+                    // O is idle once the last product into it has completed: with two row
+                    // tiles S came behind it, with one it has freed tile g - 1's values
+                    if (NT == 2) return true;
                     const bool idle = warp_wait_or_stop(&s.v_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, stop, kWaitLimit);
                     tc_fence_after();
                     return idle;
                 });
                 if (!ok) break;
             }
-            // (the unit's products are over: O is complete, the query's memory free)
-            ok = ok && warp_wait_or_stop(&s.o_full, units & 1, stop, kWaitLimit);
+            // (the row tile's products are over: O is complete, its query's memory free)
+            ok = ok && warp_wait_or_stop(&s.o_full[x], units & 1, stop, kWaitLimit);
             if (!ok) break;
             tc_fence_after();
             const int64_t u = (int64_t)c.b * a.n_kv + c.h;
@@ -276,52 +299,58 @@ __global__ void __launch_bounds__(192, Q32 ? 1 : 2) tree_bf16_kernel(const __gri
                 if (c.t == 0) a.unit_map[2 * u] = (int)range;
                 if (c.t + n == c.tiles) a.unit_map[2 * u + 1] = (int)range;
             }
-            x += n;
-            if (x < x_end) tree_next<false>(a, c);
+            if (g < total) tree_next<TOK, false>(a, c);
         }
         tc_fence_before();
     }
     __syncthreads();
     if (*stop) {   // a wait ran out: copies in flight land before the CTA ends
         if (tid == 0) raise_error(a.err, KVARN_DEVERR_WAIT_TIMEOUT);
-        if (warp == 5) {
+        if (warp == kSoft + 1) {
             for (int i = max(0, issued_k - 2); i < issued_k; ++i) mbar_wait_bounded(&s.k_full[i & 1], (i >> 1) & 1, kWaitLimit);
             for (int i = max(0, issued_v - 2); i < issued_v; ++i) mbar_wait_bounded(&s.v_full[i & 1], (i >> 1) & 1, kWaitLimit);
         }
         __syncthreads();
     }
-    if (warp == 4) {
+    if (warp == kSoft) {
         tc_fence_after();
-        tmem_free(s.tmem, 256);
+        tmem_free(s.tmem, Form::kColumns);
     }
 }
 
 // ---------------------------------------------------------------- host side
 namespace {
 
-template <int B, bool Q32>
+template <int B, bool Q32, int NT>
 cudaError_t launch_tree_bf16_as(const CUtensorMap& map, const TreeArgs& a, cudaStream_t st) {
+    using Form = TreeBf16Form<Q32, NT>;
+    const auto fn = tree_bf16_kernel<B, Q32, NT>;
     static bool ready[64];
     int d = 0;
     cudaError_t e = cudaGetDevice(&d);
     if (e != cudaSuccess) return e;
     if (d < 0 || d >= 64) return cudaErrorInvalidDevice;
     if (!ready[d]) {
-        e = cudaFuncSetAttribute(tree_bf16_kernel<B, Q32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tree_bf16_smem(Q32));
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Form::kSmem);
         if (e != cudaSuccess) return e;
         ready[d] = true;
     }
-    return launch_pdl(tree_bf16_kernel<B, Q32>, a.ranges * a.row_tiles, 192, tree_bf16_smem(Q32), st, map, a);
+    return launch_pdl(fn, a.ranges * a.row_tiles, Form::kThreads, Form::kSmem, st, map, a);
+}
+template <int B>
+cudaError_t launch_tree_bf16_block(const CUtensorMap& map, const TreeArgs& a, bool wide, cudaStream_t st) {
+    return a.q_dtype == KVARN_FP32 ? launch_tree_bf16_as<B, true, 1>(map, a, st)
+           : wide                  ? launch_tree_bf16_as<B, false, 2>(map, a, st)
+                                   : launch_tree_bf16_as<B, false, 1>(map, a, st);
 }
 
 }  // namespace
 
-cudaError_t launch_tree_bf16(const TreeArgs& a, cudaStream_t st) {
+cudaError_t launch_tree_bf16(const TreeArgs& a, bool wide, cudaStream_t st) {
     CUtensorMap map;
     const cudaError_t e = bf16_page_map(&map, a.pool, a.n_pool_blocks, a.n_kv, a.B);
     if (e != cudaSuccess) return e;
-    if (a.q_dtype == KVARN_FP32) return a.B == 32 ? launch_tree_bf16_as<32, true>(map, a, st) : launch_tree_bf16_as<64, true>(map, a, st);
-    return a.B == 32 ? launch_tree_bf16_as<32, false>(map, a, st) : launch_tree_bf16_as<64, false>(map, a, st);
+    return a.B == 32 ? launch_tree_bf16_block<32>(map, a, wide, st) : launch_tree_bf16_block<64>(map, a, wide, st);
 }
 
 }  // namespace kvarn

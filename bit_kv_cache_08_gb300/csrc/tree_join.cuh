@@ -12,8 +12,9 @@
 //   O += P V    B = 8 channels; a lane's 16-byte loads of V's rows hold 8 channels, one for each
 //               of 8 products, in which the lane's column stands for the channel
 // P and an fp32 query enter as two bf16 halves (2^-16). The mask of a row is 16 bits of
-// its words a step; a step that no row of the warp sees is left out. Nothing passes
-// through shared memory.
+// its words a step; a step that no row of the warp sees is left out. Where there
+// are few rows, several warps share them: each takes its part of the partials and of the
+// steps, and their states are joined through shared memory.
 #pragma once
 #include "prefix_merge.cuh"
 #include "tree.cuh"
@@ -21,7 +22,6 @@
 namespace kvarn {
 
 constexpr int kJoinRows = 16;
-constexpr int kTreeJoinWarps = 4;
 
 // Channel of accumulator x (0, 1: the lane's columns 2 tq, 2 tq + 1) of product (j, e):
 // 64 j + 16 tq + 8 x + e. The Hadamard transform over channels, for rows gq (d = 0) and gq + 8
@@ -191,12 +191,20 @@ __device__ __forceinline__ void join_step(JoinRows<Q32>& s, const uint16_t* k, c
     }
 }
 
-template <bool PACKED, bool Q32>
-__global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(TreeArgs a) {
+// Warps that share a group of 16 rows (WARPS > 1: a CTA), or 4 groups to a CTA.
+template <int WARPS>
+constexpr int tree_join_threads() { return WARPS == 1 ? 128 : 32 * WARPS; }
+template <int WARPS>
+constexpr size_t tree_join_smem() { return WARPS == 1 ? 0 : (size_t)WARPS * (16 * 32 * sizeof(float4) + kJoinRows * sizeof(float4)); }
+
+template <bool PACKED, bool Q32, int WARPS>
+__global__ void __launch_bounds__(tree_join_threads<WARPS>()) tree_join_kernel(TreeArgs a) {
     if (!a.late) wait_prior_grids();   // (no kernel of this call before it, which would have waited)
-    const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+    extern __shared__ __align__(16) float4 shared[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, tq = lane & 3;
     const int R = a.drafts * a.G, groups = (R + kJoinRows - 1) / kJoinRows;
-    const int64_t gw = (int64_t)blockIdx.x * kTreeJoinWarps + (threadIdx.x >> 5), u = gw / groups;
+    const int64_t gw = WARPS == 1 ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x, u = gw / groups;
+    const int part = WARPS == 1 ? 0 : warp;
     if (u >= (int64_t)a.batch * a.n_kv) {
         wait_prior_grids();
         return;
@@ -248,12 +256,31 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(TreeArgs
 #pragma unroll
         for (int e = 0; e < 8; ++e) s.o[j][e][0] = s.o[j][e][1] = s.o[j][e][2] = s.o[j][e][3] = 0.f;
 
-    wait_prior_grids();   // the cached tokens' kernel, beside which this one may have started
+    // the drafts' steps, 16 tokens each; this warp's are those whose number it has
+    const float scale = a.sm_scale * kLog2e;
+    auto drafts = [&] {
+        for (int t = 0; t < T; t += 16) {     // (T: -1 for a bad length)
+            const uint32_t all = T - t >= 16 ? 0xffffu : (1u << (T - t)) - 1;
+            uint32_t seen[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                seen[x] = 0;
+                if (mine[x] < rows) seen[x] = a.mask[((int64_t)b * a.drafts + mine[x] / a.G) * a.words + t / 32] >> (t % 32) & all;
+                any[x] = any[x] || seen[x];
+            }
+            if ((WARPS > 1 && t / 16 % WARPS != part) || !__any_sync(kFull, seen[0] | seen[1])) continue;
+            const int64_t at = (int64_t)b * a.drafts + t;
+            join_step<Q32>(s, a.k + at * a.k_stride + h * kD, a.v + at * a.v_stride + h * kD, a.k_stride, a.v_stride, T - t, seen, scale,
+                           lane, wrong);
+        }
+    };
+    if (!PACKED) drafts();   // (they wait for nothing; O is in their space)
+    wait_prior_grids();      // the cached tokens' kernel, beside which this one may have started
     if (!bad && tree_tokens<PACKED>(a, b) > 0) {
         // (a range outside the grid, left by a CTA that gave up, is none)
         const int2 um = __ldcg(reinterpret_cast<const int2*>(a.unit_map) + u);
         const int first = um.x, last = um.x >= 0 && um.y >= um.x && um.y < a.ranges ? um.y : um.x - 1;
-        for (int i = first; i <= last; ++i) {
+        for (int i = first + part; i <= last; i += WARPS) {
             float4 y[2][2][4], ml[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -286,7 +313,7 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(TreeArgs
                     }
             }
         }
-        if (PACKED && !(a.flags & KVARN_FLAG_NO_ROTATION)) {
+        if (PACKED && first + part <= last && !(a.flags & KVARN_FLAG_NO_ROTATION)) {
             fwht_fragment(s.o, tq);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -299,37 +326,78 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(TreeArgs
             }
         }
     }
-    const float scale = a.sm_scale * kLog2e;
-    if (PACKED && !bad) {
-        const int tail = L % a.B;
+    if (PACKED) {
+        const int tail = bad ? 0 : L % a.B;
         const uint16_t* st = a.staging + ((int64_t)b * a.n_kv + h) * 2 * a.B * kD;
         for (int t = 0; t < tail; t += 16) {
+            if (WARPS > 1 && (WARPS - 1 - t / 16 % WARPS) != part) continue;   // (from the last warp on)
             const int there = tail - t;
             const uint32_t all = there >= 16 ? 0xffffu : (1u << there) - 1;
             const uint32_t seen[2] = {all, all};
             join_step<Q32>(s, st + t * kD, st + (a.B + t) * kD, kD, kD, there, seen, scale, lane, wrong);
         }
-    }
-    for (int t = 0; t < T; t += 16) {     // (T: -1 for a bad length)
-        const uint32_t all = T - t >= 16 ? 0xffffu : (1u << (T - t)) - 1;
-        uint32_t seen[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            seen[x] = 0;
-            if (mine[x] < rows) seen[x] = a.mask[((int64_t)b * a.drafts + mine[x] / a.G) * a.words + t / 32] >> (t % 32) & all;
-            any[x] = any[x] || seen[x];
-        }
-        if (!__any_sync(kFull, seen[0] | seen[1])) continue;
-        const int64_t at = (int64_t)b * a.drafts + t;
-        join_step<Q32>(s, a.k + at * a.k_stride + h * kD, a.v + at * a.v_stride + h * kD, a.k_stride, a.v_stride, T - t, seen, scale,
-                       lane, wrong);
+        drafts();
     }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        float l = s.l[x];
-        l += __shfl_xor_sync(kFull, l, 1);
-        l += __shfl_xor_sync(kFull, l, 2);
+        s.l[x] += __shfl_xor_sync(kFull, s.l[x], 1);
+        s.l[x] += __shfl_xor_sync(kFull, s.l[x], 2);
+    }
+    if constexpr (WARPS > 1) {
+        // the warps' states: rows (m, l, wrong) behind the fragments; this warp then
+        // has products WARPS apart
+        float4* rows_of = shared + WARPS * 16 * 32;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                shared[(warp * 16 + 8 * j + e) * 32 + lane] = make_float4(s.o[j][e][0], s.o[j][e][1], s.o[j][e][2], s.o[j][e][3]);
+        if (tq == 0) {
+            rows_of[warp * kJoinRows + gq] = make_float4(s.m[0], s.l[0], wrong[0] ? 1.f : 0.f, 0.f);
+            rows_of[warp * kJoinRows + gq + 8] = make_float4(s.m[1], s.l[1], wrong[1] ? 1.f : 0.f, 0.f);
+        }
+        __syncthreads();
+        float w[2][WARPS];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float m = -INFINITY, l = 0.f;
+            bool off = false;
+#pragma unroll
+            for (int k = 0; k < WARPS; ++k) m = fmaxf(m, rows_of[k * kJoinRows + gq + 8 * x].x);
+#pragma unroll
+            for (int k = 0; k < WARPS; ++k) {
+                const float4 r = rows_of[k * kJoinRows + gq + 8 * x];
+                w[x][k] = r.x == -INFINITY ? 0.f : exp2f(r.x - m);
+                l = fmaf(r.y, w[x][k], l);
+                off = off || r.z != 0.f;
+            }
+            s.m[x] = m;
+            s.l[x] = l;
+            wrong[x] = off;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if ((8 * j + e) / (16 / WARPS) != part) continue;
+                float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < WARPS; ++k) {
+                    const float4 y = shared[(k * 16 + 8 * j + e) * 32 + lane];
+                    o[0] = fmaf(y.x, w[0][k], o[0]);
+                    o[1] = fmaf(y.y, w[0][k], o[1]);
+                    o[2] = fmaf(y.z, w[1][k], o[2]);
+                    o[3] = fmaf(y.w, w[1][k], o[3]);
+                }
+#pragma unroll
+                for (int d = 0; d < 4; ++d) s.o[j][e][d] = o[d];
+            }
+    }
+    constexpr int kRun = WARPS == 1 ? 8 : 16 / WARPS > 8 ? 8 : 16 / WARPS;   // channels next to one another that this warp has
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
         // Maxima drop NaN: tokens without a score above -inf have scores of NaN, or all -inf
+        float l = s.l[x];
         if (wrong[x] || (any[x] && s.m[x] == -INFINITY)) l = NAN;
         if (mine[x] >= rows) continue;
         const float inv = l > 0.f ? 1.f / l : l;   // (0 for nothing seen; NaN stays)
@@ -337,25 +405,66 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) tree_join_kernel(TreeArgs
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {          // 8 channels
-                float z[8];
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = s.o[j][e][2 * x + c] * inv;
-                if (a.out_bf16) {
-                    uint32_t w[4];
+                for (int e0 = 0; e0 < 8; e0 += kRun) {
+                    if (WARPS > 1 && (8 * j + e0) / (16 / WARPS) != part) continue;
+                    float z[kRun];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const __nv_bfloat162 y = __floats2bfloat162_rn(z[2 * k], z[2 * k + 1]);
-                        w[k] = *reinterpret_cast<const uint32_t*>(&y);
+                    for (int e = 0; e < kRun; ++e) z[e] = s.o[j][e0 + e][2 * x + c] * inv;
+                    const int64_t to = at + 64 * j + 8 * c + e0;
+                    if (a.out_bf16) {
+                        uint32_t y[kRun / 2];
+#pragma unroll
+                        for (int k = 0; k < kRun / 2; ++k) {
+                            const __nv_bfloat162 p = __floats2bfloat162_rn(z[2 * k], z[2 * k + 1]);
+                            y[k] = *reinterpret_cast<const uint32_t*>(&p);
+                        }
+                        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + to);
+                        if constexpr (kRun == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+                        else if constexpr (kRun == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+                        else *dst = y[0];
+                    } else {
+                        float* dst = static_cast<float*>(a.out) + to;
+                        if constexpr (kRun == 2) {
+                            *reinterpret_cast<float2*>(dst) = make_float2(z[0], z[1]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < kRun; k += 4) *reinterpret_cast<float4*>(dst + k) = make_float4(z[k], z[k + 1], z[k + 2], z[k + 3]);
+                        }
                     }
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at + 64 * j + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
-                } else {
-                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + 64 * j + 8 * c);
-                    dst[0] = make_float4(z[0], z[1], z[2], z[3]);
-                    dst[1] = make_float4(z[4], z[5], z[6], z[7]);
                 }
-            }
     }
+}
+
+// As many warps to a group of rows as leave 8 an SM (which holds that many).
+template <bool PACKED, int WARPS>
+cudaError_t launch_tree_join_as(const TreeArgs& a, int64_t groups, cudaStream_t st) {
+    const auto fn = a.q_dtype == KVARN_FP32 ? tree_join_kernel<PACKED, true, WARPS> : tree_join_kernel<PACKED, false, WARPS>;
+    constexpr size_t smem = tree_join_smem<WARPS>();
+    if (smem > 48 * 1024) {
+        static bool ready[2][64];
+        int d = 0;
+        cudaError_t e = cudaGetDevice(&d);
+        if (e != cudaSuccess) return e;
+        if (d < 0 || d >= 64) return cudaErrorInvalidDevice;
+        bool& done = ready[a.q_dtype == KVARN_FP32][d];
+        if (!done) {
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+            done = true;
+        }
+    }
+    const unsigned ctas = (unsigned)(WARPS == 1 ? (groups + 3) / 4 : groups);
+    return launch_pdl(fn, ctas, tree_join_threads<WARPS>(), smem, st, a);
+}
+template <bool PACKED>
+cudaError_t launch_tree_join(const TreeArgs& a, cudaStream_t st) {
+    const int64_t groups = (int64_t)a.batch * a.n_kv * ((a.drafts * a.G + kJoinRows - 1) / kJoinRows), sms = current_device_sms();
+    return groups <= sms       ? launch_tree_join_as<PACKED, 8>(a, groups, st)
+           : groups <= 2 * sms ? launch_tree_join_as<PACKED, 4>(a, groups, st)
+           : groups <= 4 * sms ? launch_tree_join_as<PACKED, 2>(a, groups, st)
+                               : launch_tree_join_as<PACKED, 1>(a, groups, st);
 }
 
 }  // namespace kvarn
