@@ -20,7 +20,7 @@ OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvarn.so")
 SOURCES = ["api.cu", "quantize.cu", "attention.cu", "attention_bf16.cu", "prefill.cu", "noalloc.cu", "append_rope.cu",
            "prefix.cu", "prefix_bf16.cu", "prefix_packed.cu", "weights.cu", "evict.cu", "tree.cu",
-           "tree_bf16.cu"]
+           "tree_bf16.cu", "tree_packed.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE]

@@ -27,10 +27,7 @@
 //
 // Warps: 4 a row tile for the softmax (a row a thread), one that issues the
 // products, one that copies raw tiles and finds their exponents, 8 that build
-// operands without meeting at a barrier: one group's share of a record of the
-// packed format (K: 4 tokens x 8 channels, V: 8 tokens x 4 channels) is four
-// whole 16-byte units of the swizzled operand rows, so a lane reads a record's
-// words and writes units. A build and the two softmax tiles that share it cost
+// operands (packed_build.cuh). A build and the two softmax tiles that share it cost
 // about 10 700 warp-instructions.
 //
 // Measured (32 query heads on 8 kv heads; alone and cold): 512 rows a head
@@ -42,23 +39,14 @@
 // us then): no softmax 174.6, a quarter of the building 170.2, one product in
 // eight 145.9. One row tile for more than 128 rows took 292 us (each tile built
 // twice), 16 builder warps gained nothing, half a row a thread 218.
-#include "prefix.cuh"
+#include "packed_build.cuh"
 
 #include "host_checks.h"
 #include "quantize.cuh"
 
 namespace kvarn {
 
-constexpr int kPkTok = 64;                       // tokens of a tile
-constexpr int kPkK = kPkTok * kD * 2;            // bytes of one 64 x 128 fp16 operand (two 64-channel blocks)
-constexpr int kPkV = kD * kPkTok * 2;            // 128 channel rows x 64 tokens, fp16
-constexpr int kPkQ = kPRows * kD * 2;            // 128 query rows, fp16
-constexpr int kMaxRaw = 4;                       // stages of raw tiles, at most
-constexpr int kBuildWarps = 8;
-static_assert(kMaxRaw + 2 <= 8, "exponents in flight");
 static_assert(2 * kPkV == kD * kD * 2, "the rotation matrix fits V's first stage");
-constexpr float kLift = 7.f;                     // P up to 2^(8 + 7), small weights normal down to 2^-21
-constexpr int kTopExp = 15;                      // K' and V' up to 2^15: halves of small values stay normal
 constexpr int kTopQuery = 11;                    // the query's channels up to 2^11, rotated up to sqrt(128) times that
 
 struct PackedSmem {
@@ -91,15 +79,6 @@ struct PackedLayout {
 __device__ __forceinline__ uint32_t sign_word(uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3, int w) {
     return w == 0 ? s0 : w == 1 ? s1 : w == 2 ? s2 : s3;
 }
-// Pair j of a record word as fp16 code 2^-9 (attn_common.cuh); for 3-bit
-// codes jh is the pair's place in the high-bit word.
-template <int BITS>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t w8, uint32_t hw, int j, int jh) {
-    if constexpr (BITS == 2) return code2_s(w, w8, j);
-    else if constexpr (BITS == 3) return code3_s(w, w8, hw, j, jh);
-    else return code4_s(w, w8, j);
-}
-
 template <int B, int BITS, int NT>
 __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix_packed_kernel(PrefixArgs a) {
     wait_prior_grids();
@@ -312,41 +291,11 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
             const int st = i % kRawStages;
             ok = ok && warp_wait_or_stop(&s.raw_full[st], (i / kRawStages) & 1, stop, kWaitLimit);
             if (!ok) break;
-            // 2^e over the tile's keys and over its values: the largest (|zero|, |top
-            // level|) R times the largest C (a lane: 8 (group, token) pairs, 4 or 8 channels)
-            constexpr int kPer = 32 / Lay::kBlocks;                // lanes per block
-            const int x = lane / kPer, at = 8 * (lane % kPer);
+            // 2^e over the tile's keys and over its values
+            const int x = lane / (32 / Lay::kBlocks);              // this lane's block
             const bool there = (t_beg + i) * Lay::kBlocks + x < used;
-            auto exponent = [&](const uint8_t* hb) {
-                float vmax = 0.f, cmax = 0.f;
-                if (there) {
-                    const uint4 su = *reinterpret_cast<const uint4*>(hb + off_s(B, BITS) + 2 * at);
-                    const uint4 zu = *reinterpret_cast<const uint4*>(hb + off_z(B, BITS) + 2 * at);
-                    const uint4 ru = *reinterpret_cast<const uint4*>(hb + off_R(B, BITS) + 2 * (at % B));
-                    const uint32_t sw[4] = {su.x, su.y, su.z, su.w}, zw[4] = {zu.x, zu.y, zu.z, zu.w}, rw[4] = {ru.x, ru.y, ru.z, ru.w};
-                    constexpr float kTop = (float)((1 << BITS) - 1);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 sf = __half22float2(u32_as_h2(sw[k])), zf = __half22float2(u32_as_h2(zw[k]));
-                        const float2 rf = __half22float2(u32_as_h2(rw[k]));
-                        vmax = fmaxf(vmax, fmaxf(fabsf(zf.x), fabsf(fmaf(sf.x, kTop, zf.x))) * fabsf(rf.x));
-                        vmax = fmaxf(vmax, fmaxf(fabsf(zf.y), fabsf(fmaf(sf.y, kTop, zf.y))) * fabsf(rf.y));
-                    }
-                    constexpr int kCh = kD / kPer;
-#pragma unroll
-                    for (int k = 0; k < kCh; k += 2) {
-                        const float2 cf = __half22float2(
-                            u32_as_h2(*reinterpret_cast<const uint32_t*>(hb + off_C(B, BITS) + 2 * (kCh * (lane % kPer) + k))));
-                        cmax = fmaxf(cmax, fmaxf(fabsf(cf.x), fabsf(cf.y)));
-                    }
-                }
-                const float bound = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vmax))) *
-                                    __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(cmax)));
-                // (the clamps keep 2^-e and 2^e finite)
-                return (bound > 0x1p-60f ? min(ceil_log2(bound), 100) : -60) - kTopExp;
-            };
             const uint8_t* hb = raw + st * Lay::kRaw + x * 2 * Lay::HB;
-            const int ke = exponent(hb), ve = exponent(hb + Lay::HB);
+            const int ke = tile_exponent<B, BITS>(hb, there, lane), ve = tile_exponent<B, BITS>(hb + Lay::HB, there, lane);
             if (lane == 0) {
                 s.kexp[i & 7] = ke;
                 s.vexp[i & 7] = ve;
@@ -356,10 +305,7 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
     } else if (warp > kSoft) {
         // ---------------------------------------------------------- operands from codes
         // warp bw: group g of the 32 records of half sb, a record a lane
-        const int bw = warp - (kSoft + 2), g = bw & 3, sb = bw >> 2, ra = lane >> 2, rb = lane & 3;
-        const int half0 = B == 64 ? 32 * sb : 0;          // the half's first token within its block
-        // (code 2^-9) s + z 2^-9, times the rest of the value's factors and 2^9
-        constexpr float kUp = 512.f;
+        const int bw = warp - (kSoft + 2), g = bw & 3, sb = bw >> 2;
         bool ok = true;
         for (int i = 0; i < n && ok; ++i) {
             const int st = i % kRawStages, par = i & 1;
@@ -368,117 +314,25 @@ __global__ void __launch_bounds__(PackedLayout<B, BITS, NT>::kThreads, 1) prefix
             if (!ok) break;
             const uint8_t* hb = raw + st * Lay::kRaw + (B == 64 ? 0 : sb) * 2 * Lay::HB;
             const bool there = (t_beg + i) * Lay::kBlocks + (B == 64 ? 0 : sb) < used;   // else its values are zero
-            // ---- K: 4 tokens 4 ra + k of the half, channels 32 g + 8 rb .. + 7
-            {
-                const uint8_t* codes = hb + (half0 + lane) * 16 * BITS;
-                uint32_t w[4], hw[4];              // token k's word with this group's fields at its low end
-                const uint4* src = reinterpret_cast<const uint4*>(codes);
-                if constexpr (BITS == 4) {         // word 4 k + g
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint4 u = src[k];
-                        w[k] = g == 0 ? u.x : g == 1 ? u.y : g == 2 ? u.z : u.w;
-                    }
-                } else {                           // word 2 k + g / 2, fields 4 (g % 2) ..
-                    const uint4 u = src[0], v = src[1];
-                    w[0] = (g & 2 ? u.y : u.x) >> 8 * (g & 1);
-                    w[1] = (g & 2 ? u.w : u.z) >> 8 * (g & 1);
-                    w[2] = (g & 2 ? v.y : v.x) >> 8 * (g & 1);
-                    w[3] = (g & 2 ? v.w : v.z) >> 8 * (g & 1);
-                    if constexpr (BITS == 3) {     // high bits in word 8 + k from bit 4 g
-                        const uint4 x = src[2];
-                        hw[0] = x.x >> 4 * g; hw[1] = x.y >> 4 * g; hw[2] = x.z >> 4 * g; hw[3] = x.w >> 4 * g;
-                    }
-                }
-                const int t0 = half0 + 4 * ra;
-                const uint2 su = *reinterpret_cast<const uint2*>(hb + off_s(B, BITS) + 2 * (g * B + t0));
-                const uint2 zu = *reinterpret_cast<const uint2*>(hb + off_z(B, BITS) + 2 * (g * B + t0));
-                const uint2 ru = *reinterpret_cast<const uint2*>(hb + off_R(B, BITS) + 2 * t0);
-                const uint4 cu = *reinterpret_cast<const uint4*>(hb + off_C(B, BITS) + 2 * (32 * g + 8 * rb));
-                float2 cc[4] = {__half22float2(u32_as_h2(cu.x)), __half22float2(u32_as_h2(cu.y)),
-                                __half22float2(u32_as_h2(cu.z)), __half22float2(u32_as_h2(cu.w))};
-                if (i >= 2) ok = warp_wait_or_stop(&s.k_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
-                if (i == 0 && q32) ok = warp_wait_or_stop(&s.q_done, 0, stop, kWaitLimit);   // (the query's low half was here)
-                if (!ok) break;
-                uint8_t* dst = k_op + par * 2 * kPkK + (g >> 1) * (kPkK / 2);
-                const float up = kUp * exp2i(-*reinterpret_cast<volatile int*>(&s.kexp[i & 7]));
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t step = k < 2 ? su.x : su.y;
-                    const float2 z2 = __half22float2(u32_as_h2(k < 2 ? zu.x : zu.y)), r2 = __half22float2(u32_as_h2(k < 2 ? ru.x : ru.y));
-                    const float zero = ((k & 1) ? z2.y : z2.x) * kCodeScale, fac = ((k & 1) ? r2.y : r2.x) * up;
-                    const uint32_t w8 = w[k] >> 8;
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        const uint32_t f = code_pair<BITS>(w[k], w8, hw[k], p, p);
-                        float2 y = make_float2(fma_half(f, step, zero, false, k & 1), fma_half(f, step, zero, true, k & 1));
-                        y = __fmul2_rn(__fmul2_rn(y, make_float2(fac, fac)), cc[p]);
-                        split_pair<true>(y.x, y.y, hi[p], lo[p]);
-                    }
-                    const uint32_t at = swizzled(32 * sb + 4 * ra + k, 4 * (g & 1) + rb);
-                    // (an absent half's scores are masked, whatever its raw bytes were)
-                    *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(dst + kPkK + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-                fence_async_smem();
-                warp_arrive(&s.k_full[par]);
-            }
-            // ---- V: channels 32 g + 4 ra + k, 8 tokens 8 rb .. + 7 of the half
-            {
-                const uint8_t* vb = hb + Lay::HB;
-                const uint8_t* codes = vb + (half0 + lane) * 16 * BITS;
-                uint32_t w[4], hw = 0;             // 4-bit: word 4 g + k; else 2 g + k / 2, and its high bits in word 8 + g
-                if constexpr (BITS == 4) {
-                    const uint4 u = reinterpret_cast<const uint4*>(codes)[g];
-                    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-                } else {
-                    const uint2 u = reinterpret_cast<const uint2*>(codes)[g];
-                    w[0] = w[1] = u.x;
-                    w[2] = w[3] = u.y;
-                    if constexpr (BITS == 3) hw = reinterpret_cast<const uint32_t*>(codes)[8 + g];
-                }
-                const int t0 = half0 + 8 * rb;
-                const uint4 su = *reinterpret_cast<const uint4*>(vb + off_s(B, BITS) + 2 * (g * B + t0));
-                const uint4 zu = *reinterpret_cast<const uint4*>(vb + off_z(B, BITS) + 2 * (g * B + t0));
-                const uint4 ru = *reinterpret_cast<const uint4*>(vb + off_R(B, BITS) + 2 * t0);
-                const uint2 cu = *reinterpret_cast<const uint2*>(vb + off_C(B, BITS) + 2 * (32 * g + 4 * ra));
-                const uint32_t sw[4] = {su.x, su.y, su.z, su.w}, zw[4] = {zu.x, zu.y, zu.z, zu.w}, rw[4] = {ru.x, ru.y, ru.z, ru.w};
-                // (warps of an absent half, whose raw bytes may be anything, write zeros)
-                const float up = kUp * exp2i(-*reinterpret_cast<volatile int*>(&s.vexp[i & 7]));
-                float2 zero[4], fac[4];            // token pairs
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    zero[p] = __fmul2_rn(__half22float2(u32_as_h2(zw[p])), make_float2(kCodeScale, kCodeScale));
-                    fac[p] = __fmul2_rn(__half22float2(u32_as_h2(rw[p])), make_float2(up, up));
-                }
-                const float2 c01 = __half22float2(u32_as_h2(cu.x)), c23 = __half22float2(u32_as_h2(cu.y));
-                const float cf[4] = {c01.x, c01.y, c23.x, c23.y};
-                if (i >= 2) ok = warp_wait_or_stop(&s.v_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
-                if (i == 0) ok = warp_wait_or_stop(&s.q_done, 0, stop, kWaitLimit);   // (H was here)
-                if (!ok) break;
-                uint8_t* dst = v_op + par * 2 * kPkV;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t w8 = w[k] >> 8;
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {                 // tokens 2p, 2p + 1
-                        const int j = BITS == 4 ? p : 4 * (p >> 1) + 2 * (p & 1) + (k & 1);
-                        const uint32_t f = code_pair<BITS>(w[k], w8, hw, j, 8 * (k >> 1) + j);
-                        float2 y = make_float2(fma_half(f, sw[p], zero[p].x, false, false), fma_half(f, sw[p], zero[p].y, true, true));
-                        y = __fmul2_rn(__fmul2_rn(y, fac[p]), make_float2(cf[k], cf[k]));
-                        split_pair<true>(y.x, y.y, hi[p], lo[p]);
-                        if (!there) hi[p] = lo[p] = 0u;
-                    }
-                    const uint32_t at = swizzled(32 * g + 4 * ra + k, 4 * sb + rb);
-                    *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(dst + kPkV + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-                fence_async_smem();
-                warp_arrive(&s.v_full[par]);
-                warp_arrive(&s.raw_empty[st]);
-            }
+            ok = build_keys<B, BITS>(hb, g, sb, lane, &s.kexp[i & 7], k_op + par * 2 * kPkK, [&] {
+                bool free = true;
+                if (i >= 2) free = warp_wait_or_stop(&s.k_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
+                if (i == 0 && q32) free = warp_wait_or_stop(&s.q_done, 0, stop, kWaitLimit);   // (the query's low half was here)
+                return free;
+            });
+            if (!ok) break;
+            fence_async_smem();
+            warp_arrive(&s.k_full[par]);
+            ok = build_values<B, BITS>(hb + Lay::HB, there, g, sb, lane, &s.vexp[i & 7], v_op + par * 2 * kPkV, [&] {
+                bool free = true;
+                if (i >= 2) free = warp_wait_or_stop(&s.v_empty[par], ((i >> 1) - 1) & 1, stop, kWaitLimit);
+                if (i == 0) free = warp_wait_or_stop(&s.q_done, 0, stop, kWaitLimit);   // (H was here)
+                return free;
+            });
+            if (!ok) break;
+            fence_async_smem();
+            warp_arrive(&s.v_full[par]);
+            warp_arrive(&s.raw_empty[st]);
         }
     } else if (warp == kSoft) {
         // ---------------------------------------------------------- products

@@ -19,6 +19,8 @@ struct TreeArgs {
     uint32_t* err;
     float4* partials;            // see tree_partial
     int32_t* unit_map;           // (first, last) range of each unit
+    uint16_t* turned;            // packed cache: the rotated queries, two fp16 halves, and their scales
+    float* turned_scale;
     int64_t n_pool_blocks, block_bytes, k_stride, v_stride;
     int q_dtype, out_bf16;
     int max_blocks, B, batch, drafts, words;

@@ -168,7 +168,9 @@ __global__ void __launch_bounds__(TreeBf16Form<Q32, NT>::kThreads, Q32 || NT == 
         ok = !(a.flags & KVARN_FLAG_TEST_WAIT_TIMEOUT);
         if (!ok && lane == 0) *stop = 1;                 // (test switch: as if the first wait had run out)
         while (g < total && ok) {
-            const int n = min(c.tiles - c.t, total - g);
+            // (through a warp reduction, whose result the compiler knows to be the same in
+            // all lanes: a product's operands then stay in uniform registers)
+            const int n = __reduce_min_sync(kFull, min(c.tiles - c.t, total - g));
             const bool cut = c.tokens % TOK != 0 && c.t + n == c.tiles;   // the last tile has rows behind the end
             ok = warp_wait_or_stop(&s.q_full, units & 1, stop, kWaitLimit);
             // O (+)= P V of step i - 2, then S = Q K^T of step i; a step is a tile (NT 1) or a

@@ -199,7 +199,7 @@ def test_two_graphs_at_once(kvlib, bits):
     drafts = [Drafts(c, T, seed=T) for T in (6, 40)]
     want = [_call(c, d) for d in drafts]
     torch.cuda.synchronize()
-    graphs, outs, streams = [], [], []
+    graphs, outs, streams, spaces = [], [], [], []   # (a graph's workspace has to outlive it)
     for d in drafts:
         st = torch.cuda.Stream()
         ws, out = c.kv.alloc_tree_workspace(c.cfg, 3, d.T, c.table.shape[1]), torch.full_like(d.q, 3.0, dtype=torch.float32)
@@ -208,7 +208,7 @@ def test_two_graphs_at_once(kvlib, bits):
             graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(graph, stream=st):
                 _call(c, d, ws=ws, out=out, check=False)
-        graphs.append(graph), outs.append(out), streams.append(st)
+        graphs.append(graph), outs.append(out), streams.append(st), spaces.append(ws)
     for _ in range(5):
         for graph, st in zip(graphs, streams):
             with torch.cuda.stream(st):
