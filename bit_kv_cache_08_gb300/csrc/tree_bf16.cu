@@ -179,7 +179,6 @@ __global__ void __launch_bounds__(TreeBf16Form<Q32, NT>::kThreads, Q32 || NT == 
                 const int j = i - 2, ti = g + i / NT, tj = g + (NT == 2 ? (i >> 1) - 1 : j);   // (tiles)
                 const int w = NT == 2 ? i & 1 : ti & 1, x = NT == 2 ? w : 0;
                 const bool lead = NT == 1 || w == 0, trail = NT == 1 || w == 1;
-                if (i < NT * n && lead) ok = warp_wait_or_stop(&s.k_full[ti & 1], (ti >> 1) & 1, stop, kWaitLimit);
                 if (j >= 0) {
                     if (lead) {
                         ok = ok && warp_wait_or_stop(&s.v_full[tj & 1], (tj >> 1) & 1, stop, kWaitLimit);
@@ -188,8 +187,8 @@ __global__ void __launch_bounds__(TreeBf16Form<Q32, NT>::kThreads, Q32 || NT == 
                     ok = ok && warp_wait_or_stop(&s.p_ready[w], (NT == 2 ? tj : tj >> 1) & 1, stop, kWaitLimit);
                 }
                 if (!ok) break;
-                tc_fence_after();
                 if (j >= 0) {
+                    tc_fence_after();
                     const uint32_t p = tm_s + TOK * w, vd = v_desc + (tj & 1) * (kKv >> 4);
 #pragma unroll
                     for (int k = 0; k < TOK / 16; ++k) {   // 16 tokens: 8 columns of each half of P, 2048 bytes of V rows
@@ -199,6 +198,10 @@ __global__ void __launch_bounds__(TreeBf16Form<Q32, NT>::kThreads, Q32 || NT == 
                     if (trail) mma_commit(&s.v_empty[tj & 1]);
                     if (tj == g + n - 1) mma_commit(&s.o_full[x]);
                 }
+                // (the keys' wait comes behind the products that do not need them)
+                if (i < NT * n && lead) ok = warp_wait_or_stop(&s.k_full[ti & 1], (ti >> 1) & 1, stop, kWaitLimit);
+                if (!ok) break;
+                tc_fence_after();
                 if (i < NT * n) {
                     const uint32_t kd = k_desc + (ti & 1) * (kKv >> 4);
 #pragma unroll
