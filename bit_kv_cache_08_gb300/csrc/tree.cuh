@@ -110,6 +110,136 @@ __device__ __forceinline__ float4* tree_partial(const TreeArgs& a, int64_t slot,
     return a.partials + (slot * 33 + quad) * a.rows_pad + row;
 }
 
+// softmax_tile (prefix.cuh) with S read from tensor memory twice, 16 columns at a time in
+// rolled loops: a tenth of its instructions in memory, for kernels whose warps' code together
+// does not fit the instruction caches.
+template <int TOK, bool HALF, typename Idle>
+__device__ __forceinline__ bool softmax_rolled(uint32_t my_s, uint32_t my_o, int shown, float scale, float bias, float unbias, float lift,
+                                               bool first, RowState& st, uint64_t* p_ready, Idle&& o_idle) {
+    const bool cut = __any_sync(kFull, shown < TOK);
+    auto load = [&](int c0, uint32_t (&x)[16]) {
+        tmem_ld16(my_s + c0, x);
+        tmem_wait_ld();
+        if (cut) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (c0 + i >= shown) x[i] = 0xff800000u;   // -inf, whatever was there
+        }
+    };
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c0 = 0; c0 < TOK; c0 += 16) {
+        uint32_t x[16];
+        load(c0, x);
+        float a = mx, b = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {                  // (three-input maxima)
+            a = fmaxf(fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), a);
+            b = fmaxf(fmaxf(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), b);
+        }
+        mx = fmaxf(a, b);
+    }
+    const float top = fmaf(mx, scale, bias);
+    const bool grow = top - st.m > 8.f;                    // (from -inf at once; false where nothing is shown)
+    if (!first && __any_sync(kFull, grow)) {
+        if (!o_idle()) return false;
+        const float f = grow && st.m != -INFINITY ? ex2(st.m - top) : 1.f;
+        st.l *= f;
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(my_o + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(my_o + c, o);
+        }
+    }
+    if (grow) st.m = top;
+    const float off = st.m == -INFINITY ? 0.f : bias + lift - st.m;
+    const float2 scale2 = make_float2(scale, scale), off2 = make_float2(off, off);
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int c0 = 0; c0 < TOK; c0 += 16) {
+        uint32_t x[16], y[16];                             // (y: high halves, low halves)
+        load(c0, x);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, off2);
+            const float2 p = make_float2(ex2(e.x), ex2(e.y));
+            sum = __fadd2_rn(sum, p);
+            split_pair<HALF>(p.x, p.y, y[i >> 1], y[8 + (i >> 1)]);
+        }
+        tmem_st16(my_s + c0, y);                           // (over columns of S that have been read)
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    warp_arrive(p_ready);
+    st.l += (sum.x + sum.y) * unbias;
+    return true;
+}
+
+// ---------------------------------------------------------------- products in runs
+// Products of one step as one piece of PTX, for a whole warp with the same operands in all lanes: the lane
+// that issues is elected once, and a product costs the additions to its operands alone. (A product at a time,
+// each with an election of its own, took 70 to 80 cycles beside busy warps on the same scheduler,
+// where the tensor core takes one in 32 to 64.) Operand %0 is the shape, %1 the descriptors' high word.
+//   TREE_TS(d, a, +, b, +, p)  [d] (+)= A at tensor memory a + times B at descriptor b +; p: none, one
+//   TREE_SS                    the same with A at a descriptor
+#define TREE_RUN                                                                                                              \
+    "{\n .reg .pred e, none, one;\n .reg .b32 ta, tb;\n .reg .b64 da, db;\n elect.sync _|e, 0xffffffff;\n"                   \
+    " setp.ne.u32 none, %2, 0;\n setp.ne.u32 one, 1, 0;\n"
+#define TREE_TS(d, a, a_off, b, b_off, p)                                                                                     \
+    " add.u32 ta, " a ", " a_off ";\n add.u32 tb, " b ", " b_off ";\n mov.b64 db, {tb, %1};\n"                               \
+    " @e tcgen05.mma.cta_group::1.kind::f16 [" d "], [ta], db, %0, " p ";\n"
+#define TREE_SS(d, a, a_off, b, b_off, p)                                                                                     \
+    " add.u32 ta, " a ", " a_off ";\n add.u32 tb, " b ", " b_off ";\n mov.b64 da, {ta, %1};\n mov.b64 db, {tb, %1};\n"       \
+    " @e tcgen05.mma.cta_group::1.kind::f16 [" d "], da, db, %0, " p ";\n"
+
+// S = Q K^T of bf16 tiles: Q and K as 64-channel blocks, BLOCK bytes apart in K.
+template <int BLOCK>
+__device__ __forceinline__ void run_qk_bf16(uint32_t d, uint32_t q, uint32_t k, uint32_t shape, bool acc) {
+    static_assert(BLOCK == 8192 || BLOCK == 16384, "tiles of 64 or 128 tokens");
+#define TREE_QK(q_at, k_at, p) TREE_SS("%3", "%4", q_at, "%5", k_at, p)
+    if (BLOCK == 8192)
+        asm volatile(TREE_RUN TREE_QK("0", "0", "none") TREE_QK("2", "2", "one") TREE_QK("4", "4", "one") TREE_QK("6", "6", "one")
+                     TREE_QK("1024", "512", "one") TREE_QK("1026", "514", "one") TREE_QK("1028", "516", "one") TREE_QK("1030", "518", "one") "}\n"
+                     ::"r"(shape), "r"(kOperandHigh), "r"((uint32_t)acc), "r"(d), "r"(q), "r"(k) : "memory");
+    else
+        asm volatile(TREE_RUN TREE_QK("0", "0", "none") TREE_QK("2", "2", "one") TREE_QK("4", "4", "one") TREE_QK("6", "6", "one")
+                     TREE_QK("1024", "1024", "one") TREE_QK("1026", "1026", "one") TREE_QK("1028", "1028", "one") TREE_QK("1030", "1030", "one") "}\n"
+                     ::"r"(shape), "r"(kOperandHigh), "r"((uint32_t)acc), "r"(d), "r"(q), "r"(k) : "memory");
+#undef TREE_QK
+}
+// O (+)= P V of 64 tokens of bf16 tiles: 16 tokens are 8 columns of each half of P, and 2048 bytes of V's rows.
+__device__ __forceinline__ void run_pv_bf16(uint32_t d, uint32_t p, uint32_t v, uint32_t shape, bool acc) {
+#define TREE_PV(p_hi, p_lo, v_at, x) TREE_TS("%3", "%4", p_hi, "%5", v_at, x) TREE_TS("%3", "%4", p_lo, "%5", v_at, "one")
+    asm volatile(TREE_RUN TREE_PV("0", "8", "0", "none") TREE_PV("16", "24", "128", "one") TREE_PV("32", "40", "256", "one")
+                 TREE_PV("48", "56", "384", "one") "}\n"
+                 ::"r"(shape), "r"(kOperandHigh), "r"((uint32_t)acc), "r"(d), "r"(p), "r"(v) : "memory");
+#undef TREE_PV
+    static_assert(kPLow == 8, "the halves of P");
+}
+// S = Q K'^T of a packed tile: high halves of Q in tensor memory (qa), low ones at q; K' high (kh) and low (kl).
+__device__ __forceinline__ void run_qk_packed(uint32_t d, uint32_t qa, uint32_t q, uint32_t kh, uint32_t kl, uint32_t shape) {
+#define TREE_QK(t_at, q_at, k_at, x) \
+    TREE_TS("%3", "%4", t_at, "%6", k_at, x) TREE_TS("%3", "%4", t_at, "%7", k_at, "one") TREE_SS("%3", "%5", q_at, "%6", k_at, "one")
+    asm volatile(TREE_RUN TREE_QK("0", "0", "0", "none") TREE_QK("8", "2", "2", "one") TREE_QK("16", "4", "4", "one") TREE_QK("24", "6", "6", "one")
+                 TREE_QK("32", "1024", "512", "one") TREE_QK("40", "1026", "514", "one") TREE_QK("48", "1028", "516", "one")
+                 TREE_QK("56", "1030", "518", "one") "}\n"
+                 ::"r"(shape), "r"(kOperandHigh), "r"(0u), "r"(d), "r"(qa), "r"(q), "r"(kh), "r"(kl) : "memory");
+#undef TREE_QK
+}
+// O (+)= P V' of a packed tile: V' high (vh) and low (vl).
+__device__ __forceinline__ void run_pv_packed(uint32_t d, uint32_t p, uint32_t vh, uint32_t vl, uint32_t shape, bool acc) {
+#define TREE_PV(p_hi, p_lo, v_at, x) \
+    TREE_TS("%3", "%4", p_hi, "%5", v_at, x) TREE_TS("%3", "%4", p_hi, "%6", v_at, "one") TREE_TS("%3", "%4", p_lo, "%5", v_at, "one")
+    asm volatile(TREE_RUN TREE_PV("0", "8", "0", "none") TREE_PV("16", "24", "2", "one") TREE_PV("32", "40", "4", "one")
+                 TREE_PV("48", "56", "6", "one") "}\n"
+                 ::"r"(shape), "r"(kOperandHigh), "r"((uint32_t)acc), "r"(d), "r"(p), "r"(vh), "r"(vl) : "memory");
+#undef TREE_PV
+}
+
 // A thread's row of a result (m in the log2 domain, l, O in tensor memory) as a partial.
 __device__ __forceinline__ void tree_store(const TreeArgs& a, int64_t slot, int row, bool valid, float m, float l, uint32_t my_o) {
     if (valid) *tree_partial(a, slot, 0, row) = make_float4(m, l, 0.f, 0.f);

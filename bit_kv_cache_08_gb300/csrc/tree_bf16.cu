@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(TreeBf16Form<Q32, NT>::kThreads, Q32 || NT == 
     __syncthreads();
     tc_fence_after();
     // S (and P) at + TOK w: of tile g, w = g % 2 (NT 1), of row tile w (NT 2); O of a row tile at + 128
-    const uint32_t tm_s = s.tmem, tm_o = s.tmem + 2 * TOK;
+    const uint32_t tm_s = __reduce_max_sync(kFull, s.tmem), tm_o = tm_s + 2 * TOK;   // (uniform to the compiler)
     int* stop = &s.stop;
     int issued_k = 0, issued_v = 0;                      // tiles whose copies have been issued
     int g = 0;                                           // tiles of this CTA so far: stage g % 2, phase g / 2
@@ -189,12 +189,10 @@ __global__ void __launch_bounds__(TreeBf16Form<Q32, NT>::kThreads, Q32 || NT == 
                 if (!ok) break;
                 if (j >= 0) {
                     tc_fence_after();
-                    const uint32_t p = tm_s + TOK * w, vd = v_desc + (tj & 1) * (kKv >> 4);
+                    const uint32_t vd = v_desc + (tj & 1) * (kKv >> 4);
 #pragma unroll
-                    for (int k = 0; k < TOK / 16; ++k) {   // 16 tokens: 8 columns of each half of P, 2048 bytes of V rows
-                        mma_ts(tm_o + 128 * x, p + 16 * k, vd + k * (2048 >> 4), kPv, j >= NT || k > 0);
-                        mma_ts(tm_o + 128 * x, p + 16 * k + kPLow, vd + k * (2048 >> 4), kPv, true);
-                    }
+                    for (int k = 0; k < NT; ++k)          // 64 tokens
+                        run_pv_bf16(tm_o + 128 * x, tm_s + TOK * w + 64 * k, vd + k * (8192 >> 4), kPv, j >= NT || k > 0);
                     if (trail) mma_commit(&s.v_empty[tj & 1]);
                     if (tj == g + n - 1) mma_commit(&s.o_full[x]);
                 }
@@ -204,12 +202,8 @@ __global__ void __launch_bounds__(TreeBf16Form<Q32, NT>::kThreads, Q32 || NT == 
                 tc_fence_after();
                 if (i < NT * n) {
                     const uint32_t kd = k_desc + (ti & 1) * (kKv >> 4);
-#pragma unroll
-                    for (int k = 0; k < (Q32 ? 16 : 8); ++k) {  // (k >= 8: the query's low halves)
-                        const uint32_t in = (k & 3) * 32;
-                        mma_ss(tm_s + TOK * w, q_desc + (x + (k >> 3)) * (kTbQ >> 4) + (((k >> 2 & 1) * (kTbQ / 2) + in) >> 4),
-                               kd + (((k >> 2 & 1) * (kKv / 2) + in) >> 4), kQk, k > 0);
-                    }
+                    run_qk_bf16<kKv / 2>(tm_s + TOK * w, q_desc + x * (kTbQ >> 4), kd, kQk, false);
+                    if (Q32) run_qk_bf16<kKv / 2>(tm_s + TOK * w, q_desc + (kTbQ >> 4), kd, kQk, true);   // (the low halves)
                     mma_commit(&s.s_full[w]);
                     if (trail) mma_commit(&s.k_empty[ti & 1]);
                 }

@@ -11,7 +11,8 @@
 // (64 columns a row tile), its low half in shared memory, beside S / P of two steps
 // (2 x 64 columns) and O (128 a row tile).
 // Warps: 4 a row tile for the softmax, one that issues the products, one that copies raw
-// tiles and finds their exponents, 8 that build operands (packed_build.cuh).
+// tiles and prepares the levels of their keys, one for those of the values, 8 that build
+// operands, as in packed_build.cuh without meeting at a barrier.
 #include "packed_build.cuh"
 #include "host_checks.h"
 #include "quantize.cuh"
@@ -53,23 +54,237 @@ __global__ void __launch_bounds__(256) tree_rotate_kernel(TreeArgs a) {
     if (lane == 0) a.turned_scale[to] = exp2i(e - kTreeTopQuery);
 }
 
+// ---------------------------------------------------------------- operands from codes
+// A value is (code S + Z) C with S = s R and Z = z R of its (token, group), C of its
+// channel. Two warps prepare S and Z of a tile's keys and of its values: scaled by a
+// power of two of the tile's (the largest level up to 2^6, the largest C up to 2^9, so that
+// products reach 2^15) and split at a quantum u of the (token, group)'s own, the power of two
+// with its largest level within 2040 u:
+//   Sh, Zh  multiples of u: every level code Sh + Zh is one of up to 2047 u, exact in fp16
+//   Sl, Zl  the rests, up to u / 2: a level's rest code Sl + Zl is up to 2 u (2 bits), 4 u (3), 8 u (4)
+// The 8 builder warps then need fp16 arithmetic only, on pairs:
+//   Lh = code Sh + Zh (exact), Ll = code Sl + Zl (within 2^-9 u at 4 bits),
+//   hi = RN(Lh C), lo = RN(RN(Lh C - hi) + Ll C)  (Lh C - hi is exact)
+// so that hi + lo is within 2^-18 of the (token, group)'s largest level times C (2^-20 at 2
+// bits), plus 2^-22 of itself. In fp32 (a mixed multiply-add, two products and a split into halves
+// by conversions, as the shared prefix builds) a pair cost half as many instructions again, several of
+// them at lower rates: XXX.
+constexpr int kTopLevel = 6, kTopChannel = 9;
+constexpr float kCodeUp = 512.f;      // (codes come as code 2^-9)
+constexpr int kRest = 4 * kPkTok * 2; // bytes of one plane of rests: [block][4][B] fp16
+
+// S and Z of a head-block hb of the tile (its 8 (group, token) pairs of this lane), Sh 2^9 and Zh
+// in place of s and z, Sl 2^9 and Zl at rest; returns the tile's exponent, and C's in
+// c_exp. `there`: the lane's block is.
+template <int B, int BITS>
+__device__ __forceinline__ int prepare_levels(uint8_t* hb, bool there, int lane, uint8_t* rest, int& c_exp) {
+    constexpr int kPer = 32 / (kPkTok / B), kCh = kD / kPer;   // lanes and channels of a block
+    constexpr float kTop = (float)((1 << BITS) - 1);
+    const int at = 8 * (lane % kPer);
+    float S[8], Z[8], top[8], vmax = 0.f, cmax = 0.f;
+    if (there) {
+        const uint4 su = *reinterpret_cast<const uint4*>(hb + off_s(B, BITS) + 2 * at);
+        const uint4 zu = *reinterpret_cast<const uint4*>(hb + off_z(B, BITS) + 2 * at);
+        const uint4 ru = *reinterpret_cast<const uint4*>(hb + off_R(B, BITS) + 2 * (at % B));
+        const uint32_t sw[4] = {su.x, su.y, su.z, su.w}, zw[4] = {zu.x, zu.y, zu.z, zu.w}, rw[4] = {ru.x, ru.y, ru.z, ru.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 rf = __half22float2(u32_as_h2(rw[k]));
+            const float2 sf = __fmul2_rn(__half22float2(u32_as_h2(sw[k])), rf), zf = __fmul2_rn(__half22float2(u32_as_h2(zw[k])), rf);
+            S[2 * k] = sf.x, S[2 * k + 1] = sf.y, Z[2 * k] = zf.x, Z[2 * k + 1] = zf.y;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            top[k] = fmaxf(fabsf(Z[k]), fabsf(fmaf(S[k], kTop, Z[k])));
+            vmax = fmaxf(vmax, top[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kCh; k += 2) {
+            const float2 cf = __half22float2(
+                u32_as_h2(*reinterpret_cast<const uint32_t*>(hb + off_C(B, BITS) + 2 * (kCh * (lane % kPer) + k))));
+            cmax = fmaxf(cmax, fmaxf(fabsf(cf.x), fabsf(cf.y)));
+        }
+    }
+    vmax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(vmax)));
+    cmax = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(cmax)));
+    // (the clamps keep every power of two below finite)
+    const int v_exp = (vmax > 0x1p-60f ? min(ceil_log2(vmax), 60) : -60) - kTopLevel;
+    c_exp = (cmax > 0x1p-30f ? min(ceil_log2(cmax), 30) : -30) - kTopChannel;
+    if (there) {
+        const float down = exp2i(-v_exp);
+        uint32_t sh[4], zh[4], sl[4], zl[4];
+        float y[4][2];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float s0 = S[k] * down, z0 = Z[k] * down;
+            // 1.5 2^23 u, u = 2^(e - 10), 2^e the power of two below the largest level and a
+            // little: adding and subtracting it rounds to multiples of u
+            const uint32_t e = __float_as_uint(fmaf(top[k] * down, 0x1p-7f, top[k] * down)) & 0x7f800000u;
+            const float round = __uint_as_float(max(e, 0x08000000u) + (13u << 23)) * 1.5f;
+            const float a = __fsub_rn(__fadd_rn(s0, round), round), b = __fsub_rn(__fadd_rn(z0, round), round);
+            y[0][k & 1] = a * kCodeUp;
+            y[1][k & 1] = b;
+            y[2][k & 1] = (s0 - a) * kCodeUp;
+            y[3][k & 1] = z0 - b;
+            if (k & 1) {
+                sh[k >> 1] = pack_h2(y[0][0], y[0][1]);
+                zh[k >> 1] = pack_h2(y[1][0], y[1][1]);
+                sl[k >> 1] = pack_h2(y[2][0], y[2][1]);
+                zl[k >> 1] = pack_h2(y[3][0], y[3][1]);
+            }
+        }
+        const int plane = lane / kPer * 4 * B * 2 + 2 * at;
+        *reinterpret_cast<uint4*>(hb + off_s(B, BITS) + 2 * at) = make_uint4(sh[0], sh[1], sh[2], sh[3]);
+        *reinterpret_cast<uint4*>(hb + off_z(B, BITS) + 2 * at) = make_uint4(zh[0], zh[1], zh[2], zh[3]);
+        *reinterpret_cast<uint4*>(rest + plane) = make_uint4(sl[0], sl[1], sl[2], sl[3]);
+        *reinterpret_cast<uint4*>(rest + kRest + plane) = make_uint4(zl[0], zl[1], zl[2], zl[3]);
+    }
+    return v_exp + c_exp;
+}
+
+// A pair of values as two fp16 halves.
+__device__ __forceinline__ void build_pair(uint32_t code, __half2 sh, __half2 zh, __half2 sl, __half2 zl, __half2 c, uint32_t& hi, uint32_t& lo) {
+    const __half2 f = u32_as_h2(code);
+    const __half2 top = __hfma2(f, sh, zh), rest = __hfma2(f, sl, zl);
+    const __half2 h = __hmul2(top, c);
+    hi = h2_as_u32(h);
+    lo = h2_as_u32(__hfma2(rest, c, __hfma2(top, c, __hneg2(h))));
+}
+__device__ __forceinline__ __half2 scaled_channels(uint32_t c, float up) {
+    const float2 f = __half22float2(u32_as_h2(c));
+    return __floats2half2_rn(f.x * up, f.y * up);
+}
+// Both halves of a register one of them.
+__device__ __forceinline__ __half2 both(uint32_t x, int high) { return u32_as_h2(__byte_perm(x, x, high ? 0x3232 : 0x1010)); }
+
+// Four halves, one down.
+__device__ __forceinline__ void next_half(uint2& x) {
+    x.x = __funnelshift_r(x.x, x.y, 16);
+    x.y >>= 16;
+}
+
+// K' of group g of the 32 records of half sb of a tile, a record a lane: tokens 4 (lane / 4) + k,
+// channels 32 g + 8 (lane % 4) .. + 7. hb: the half's K head-block, rest: its rests; up:
+// 2^-(C's exponent); ready(): waits until dst (hi, then lo) may be written (false: gave up).
+template <int B, int BITS, typename Ready>
+__device__ __forceinline__ bool tree_keys(const uint8_t* hb, const uint8_t* rest, int g, int sb, int lane, float up, uint8_t* dst, Ready&& ready) {
+    const int ra = lane >> 2, rb = lane & 3;
+    const int half0 = B == 64 ? 32 * sb : 0;             // the half's first token within its block
+    const uint8_t* codes = hb + (half0 + lane) * 16 * BITS;
+    uint32_t w[4], hw[4];              // token k's word with this group's fields at its low end
+    const uint4* src = reinterpret_cast<const uint4*>(codes);
+    if constexpr (BITS == 4) {         // word 4 k + g
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = reinterpret_cast<const uint32_t*>(codes)[4 * k + g];
+    } else {                           // word 2 k + g / 2, fields 4 (g % 2) ..
+        const uint4 u = src[0], v = src[1];
+        w[0] = (g & 2 ? u.y : u.x) >> 8 * (g & 1);
+        w[1] = (g & 2 ? u.w : u.z) >> 8 * (g & 1);
+        w[2] = (g & 2 ? v.y : v.x) >> 8 * (g & 1);
+        w[3] = (g & 2 ? v.w : v.z) >> 8 * (g & 1);
+        if constexpr (BITS == 3) {     // high bits in word 8 + k from bit 4 g
+            const uint4 x = src[2];
+            hw[0] = x.x >> 4 * g; hw[1] = x.y >> 4 * g; hw[2] = x.z >> 4 * g; hw[3] = x.w >> 4 * g;
+        }
+    }
+    const int at = 2 * (g * B + half0 + 4 * ra), block = B == 64 ? 0 : sb * 4 * B * 2;
+    uint2 sh = *reinterpret_cast<const uint2*>(hb + off_s(B, BITS) + at);   // (4 tokens)
+    uint2 zh = *reinterpret_cast<const uint2*>(hb + off_z(B, BITS) + at);
+    uint2 sl = *reinterpret_cast<const uint2*>(rest + block + at);
+    uint2 zl = *reinterpret_cast<const uint2*>(rest + kRest + block + at);
+    const uint4 cu = *reinterpret_cast<const uint4*>(hb + off_C(B, BITS) + 2 * (32 * g + 8 * rb));
+    const __half2 c[4] = {scaled_channels(cu.x, up), scaled_channels(cu.y, up), scaled_channels(cu.z, up), scaled_channels(cu.w, up)};
+    if (!ready()) return false;
+    dst += (g >> 1) * (kPkK / 2);
+    // (rolled, what belongs to a token moving down: see the head of the kernel)
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        const __half2 s1 = both(sh.x, 0), z1 = both(zh.x, 0), s2 = both(sl.x, 0), z2 = both(zl.x, 0);
+        const uint32_t w8 = w[0] >> 8;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) build_pair(code_pair<BITS>(w[0], w8, hw[0], p, p), s1, z1, s2, z2, c[p], hi[p], lo[p]);
+        const uint32_t to = swizzled(32 * sb + 4 * ra + k, 4 * (g & 1) + rb);
+        // (an absent half's scores are masked, whatever its raw bytes were)
+        *reinterpret_cast<uint4*>(dst + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + kPkK + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        next_half(sh), next_half(zh), next_half(sl), next_half(zl);
+        w[0] = w[1], w[1] = w[2], w[2] = w[3];
+        if (BITS == 3) hw[0] = hw[1], hw[1] = hw[2], hw[2] = hw[3];
+    }
+    return true;
+}
+
+// V' likewise: channels 32 g + 4 (lane / 4) + k, tokens 8 (lane % 4) .. + 7 of the half. `there`: the
+// half is (else, whatever its raw bytes are, its values are zeros).
+template <int B, int BITS, typename Ready>
+__device__ __forceinline__ bool tree_values(const uint8_t* vb, const uint8_t* rest, bool there, int g, int sb, int lane, float up, uint8_t* dst,
+                                            Ready&& ready) {
+    const int ra = lane >> 2, rb = lane & 3;
+    const int half0 = B == 64 ? 32 * sb : 0;
+    const uint8_t* codes = vb + (half0 + lane) * 16 * BITS;
+    uint32_t w[4], hw = 0;             // 4-bit: word 4 g + k; else 2 g + k / 2, and its high bits in word 8 + g
+    if constexpr (BITS == 4) {
+        const uint4 u = reinterpret_cast<const uint4*>(codes)[g];
+        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+    } else {
+        const uint2 u = reinterpret_cast<const uint2*>(codes)[g];
+        w[0] = w[1] = u.x;
+        w[2] = w[3] = u.y;
+        if constexpr (BITS == 3) hw = reinterpret_cast<const uint32_t*>(codes)[8 + g];
+    }
+    const int at = 2 * (g * B + half0 + 8 * rb), block = B == 64 ? 0 : sb * 4 * B * 2;
+    const uint4 sh = *reinterpret_cast<const uint4*>(vb + off_s(B, BITS) + at);
+    const uint4 zh = *reinterpret_cast<const uint4*>(vb + off_z(B, BITS) + at);
+    const uint4 sl = *reinterpret_cast<const uint4*>(rest + block + at);
+    const uint4 zl = *reinterpret_cast<const uint4*>(rest + kRest + block + at);
+    const uint32_t s1[4] = {sh.x, sh.y, sh.z, sh.w}, z1[4] = {zh.x, zh.y, zh.z, zh.w};
+    const uint32_t s2[4] = {sl.x, sl.y, sl.z, sl.w}, z2[4] = {zl.x, zl.y, zl.z, zl.w};
+    const uint2 cu = *reinterpret_cast<const uint2*>(vb + off_C(B, BITS) + 2 * (32 * g + 4 * ra));
+    uint2 c = make_uint2(h2_as_u32(scaled_channels(cu.x, up)), h2_as_u32(scaled_channels(cu.y, up)));   // (4 channels)
+    if (!ready()) return false;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        // 4-bit: a word a channel; else a word for two, the second's fields behind the first's
+        const uint32_t x = BITS == 4 ? w[0] : w[0] >> 2 * (k & 1), x8 = BITS == 4 ? x >> 8 : w[0] >> 8 + 2 * (k & 1);
+        const uint32_t xh = BITS == 3 ? hw >> (8 * (k >> 1) + (k & 1)) : 0u;
+        const __half2 ck = both(c.x, 0);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {                 // tokens 2p, 2p + 1
+            const int j = BITS == 4 ? p : 4 * (p >> 1) + 2 * (p & 1);
+            build_pair(code_pair<BITS>(x, x8, xh, j, j), u32_as_h2(s1[p]), u32_as_h2(z1[p]), u32_as_h2(s2[p]), u32_as_h2(z2[p]), ck, hi[p], lo[p]);
+            if (!there) hi[p] = lo[p] = 0u;
+        }
+        const uint32_t to = swizzled(32 * g + 4 * ra + k, 4 * sb + rb);
+        *reinterpret_cast<uint4*>(dst + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + kPkV + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        next_half(c);
+        if (BITS == 4) w[0] = w[1], w[1] = w[2], w[2] = w[3];
+        else if (k == 1) w[0] = w[2];
+    }
+    return true;
+}
+
 // ---------------------------------------------------------------- cached tokens
 struct TreePackedSmem {
-    // ready: a raw tile's exponents are known; raw_empty: its operands are built
-    uint64_t raw_full[kMaxRaw], ready[kMaxRaw], raw_empty[kMaxRaw];
+    // ready: a raw tile's levels are prepared [K, V]; raw_empty: its operands are built
+    uint64_t raw_full[kMaxRaw], ready[2][kMaxRaw], raw_empty[kMaxRaw];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], q_full, drained;
     uint32_t tmem;
     int stop;
-    // the exponents of the last tiles (see the prefix kernel: at most 6 are in use)
-    int kexp[8], vexp[8];
+    // the exponents of the last tiles [K, V], and of their C: the warps that find them are at most kMaxRaw
+    // tiles ahead of the V' that is built, which is at most two ahead of the softmax
+    int exps[2][8], c_exps[2][8];
 };
 
 template <int B, int BITS, int NT>
 struct TreePackedLayout {
-    static constexpr int kSoft = 4 * NT, kThreads = 32 * (kSoft + 2 + kBuildWarps);
+    static constexpr int kSoft = 4 * NT, kThreads = 32 * (kSoft + 3 + 2 * kBuildWarps);
     static constexpr int HB = head_block_bytes(B, BITS);
     static constexpr int kBlocks = kPkTok / B;                 // blocks per tile
-    static constexpr int kRaw = kBlocks * 2 * HB;              // bytes of a raw tile: (K, V) per block
+    static constexpr int kTile = kBlocks * 2 * HB;             // bytes of a raw tile: (K, V) per block,
+    static constexpr int kRaw = kTile + 4 * kRest;             // and the rests of its levels [K, V][S, Z]
     static constexpr int kHeader = 1024;
     static_assert(sizeof(TreePackedSmem) <= kHeader, "header");
     static constexpr int kFixed = 1024 + kHeader + NT * kPkQ + 4 * kPkK + 4 * kPkV;
@@ -91,7 +306,7 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
     uint8_t* q_lo = base + Lay::kHeader;          // [row tile]
     uint8_t* k_op = q_lo + NT * kPkQ;             // [stage][hi, lo]
     uint8_t* v_op = k_op + 4 * kPkK;              // [stage][hi, lo]
-    uint8_t* raw = v_op + 4 * kPkV;               // [raw stage][block][K, V]
+    uint8_t* raw = v_op + 4 * kPkV;               // [raw stage]: [block][K, V], rests
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rt = blockIdx.x % a.row_tiles;
     const int64_t range = blockIdx.x / a.row_tiles;
@@ -107,8 +322,9 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
         s.stop = 0;
         for (int i = 0; i < kRawStages; ++i) {
             mbar_init(&s.raw_full[i], 1);
-            mbar_init(&s.ready[i], 1);
-            mbar_init(&s.raw_empty[i], kBuildWarps);
+            mbar_init(&s.ready[0][i], 1);
+            mbar_init(&s.ready[1][i], 1);
+            mbar_init(&s.raw_empty[i], 2 * kBuildWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.k_full[i], kBuildWarps);
@@ -129,14 +345,15 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
     tc_fence_after();
     // Q of row tile x at + 64 x; S (and P) at + 64 w, of tile g, w = g % 2 (NT 1), or of row
     // tile w (NT 2); O at + 128 x
-    const uint32_t tm_q = s.tmem, tm_s = s.tmem + 128, tm_o = s.tmem + 256;
+    const uint32_t tm_q = __reduce_max_sync(kFull, s.tmem), tm_s = tm_q + 128, tm_o = tm_q + 256;   // (uniform to the compiler)
     int* stop = &s.stop;
     int fetched = 0;                              // raw tiles whose copies have been issued
     int g = 0;                                    // tiles of this CTA so far
     bool ok = true;
 
-    if (warp == kSoft + 1) {
-        // ---------------------------------------------------------- raw tiles and their exponents
+    if (warp == kSoft + 1 || warp == kSoft + 2) {
+        // ---------------------------------------------------------- raw tiles, and the levels of their keys / values
+        const int kind = warp - (kSoft + 1);      // the keys' warp copies
         TreeCursor f = c;                         // of the copies
         int held = -1, held0 = -32;               // lane i holds block held0 + i of the sequence
         auto fetch = [&] {
@@ -165,7 +382,7 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
         };
         for (; g < total && ok; ++g) {
             // (one stage less in flight than there are: its wait is for tile g - 2)
-            while (fetched < total && fetched < g + kRawStages - 1 && ok) {
+            while (kind == 0 && fetched < total && fetched < g + kRawStages - 1 && ok) {
                 if (fetched >= kRawStages)        // the stage's last tile has been built
                     ok = warp_wait_or_stop(&s.raw_empty[fetched % kRawStages], (fetched / kRawStages - 1) & 1, stop, kWaitLimit);
                 if (ok) fetch();
@@ -175,38 +392,43 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
             if (!ok) break;
             const int x = lane / (32 / Lay::kBlocks);              // this lane's block
             const bool there = c.t * Lay::kBlocks + x < c.tokens / B;
-            const uint8_t* hb = raw + st * Lay::kRaw + x * 2 * Lay::HB;
-            const int ke = tile_exponent<B, BITS>(hb, there, lane), ve = tile_exponent<B, BITS>(hb + Lay::HB, there, lane);
+            uint8_t* tile = raw + st * Lay::kRaw;
+            int c_exp;
+            const int e = prepare_levels<B, BITS>(tile + (2 * x + kind) * Lay::HB, there, lane, tile + Lay::kTile + 2 * kind * kRest, c_exp);
+            fence_async_smem();                   // (before the stage's next copy writes over it)
             if (lane == 0) {
-                s.kexp[g & 7] = ke;
-                s.vexp[g & 7] = ve;
-                mbar_arrive(&s.ready[st]);
+                s.exps[kind][g & 7] = e;
+                s.c_exps[kind][g & 7] = c_exp;
             }
+            warp_arrive(&s.ready[kind][st]);
             if (++c.t == c.tiles && g + 1 < total) tree_next<TOK, true>(a, c);
         }
     } else if (warp > kSoft) {
         // ---------------------------------------------------------- operands from codes
-        // warp bw: group grp of the 32 records of half sb, a record a lane
-        const int bw = warp - (kSoft + 2), grp = bw & 3, sb = bw >> 2;
+        // 8 warps the keys, 8 the values: warp bw of each group grp of the 32 records of half
+        // sb, a record a lane
+        const int kind = (warp - (kSoft + 3)) / kBuildWarps, bw = (warp - (kSoft + 3)) % kBuildWarps, grp = bw & 3, sb = bw >> 2;
         for (; g < total && ok; ++g) {
             const int st = g % kRawStages, par = g & 1;
-            ok = warp_wait_or_stop(&s.ready[st], (g / kRawStages) & 1, stop, kWaitLimit) &&
+            ok = warp_wait_or_stop(&s.ready[kind][st], (g / kRawStages) & 1, stop, kWaitLimit) &&
                  warp_wait_or_stop(&s.raw_full[st], (g / kRawStages) & 1, stop, kWaitLimit);
             if (!ok) break;
-            const uint8_t* hb = raw + st * Lay::kRaw + (B == 64 ? 0 : sb) * 2 * Lay::HB;
-            const bool there = B == 64 || c.t * Lay::kBlocks + sb < c.tokens / B;   // else its values are zero
-            ok = build_keys<B, BITS>(hb, grp, sb, lane, &s.kexp[g & 7], k_op + par * 2 * kPkK, [&] {
-                return g < 2 || warp_wait_or_stop(&s.k_empty[par], ((g >> 1) - 1) & 1, stop, kWaitLimit);
-            });
+            const uint8_t* tile = raw + st * Lay::kRaw;
+            const uint8_t* hb = tile + ((B == 64 ? 0 : sb) * 2 + kind) * Lay::HB;
+            const float up = exp2i(-*reinterpret_cast<volatile int*>(&s.c_exps[kind][g & 7]));
+            if (kind == 0) {
+                ok = tree_keys<B, BITS>(hb, tile + Lay::kTile, grp, sb, lane, up, k_op + par * 2 * kPkK, [&] {
+                    return g < 2 || warp_wait_or_stop(&s.k_empty[par], ((g >> 1) - 1) & 1, stop, kWaitLimit);
+                });
+            } else {
+                const bool there = B == 64 || c.t * Lay::kBlocks + sb < c.tokens / B;   // else its values are zero
+                ok = tree_values<B, BITS>(hb, tile + Lay::kTile + 2 * kRest, there, grp, sb, lane, up, v_op + par * 2 * kPkV, [&] {
+                    return g < 2 || warp_wait_or_stop(&s.v_empty[par], ((g >> 1) - 1) & 1, stop, kWaitLimit);
+                });
+            }
             if (!ok) break;
             fence_async_smem();
-            warp_arrive(&s.k_full[par]);
-            ok = build_values<B, BITS>(hb + Lay::HB, there, grp, sb, lane, &s.vexp[g & 7], v_op + par * 2 * kPkV, [&] {
-                return g < 2 || warp_wait_or_stop(&s.v_empty[par], ((g >> 1) - 1) & 1, stop, kWaitLimit);
-            });
-            if (!ok) break;
-            fence_async_smem();
-            warp_arrive(&s.v_full[par]);
+            warp_arrive(kind ? &s.v_full[par] : &s.k_full[par]);
             warp_arrive(&s.raw_empty[st]);
             if (B != 64 && ++c.t == c.tiles && g + 1 < total) tree_next<TOK, true>(a, c);
         }
@@ -234,13 +456,8 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
                 if (!ok) break;
                 if (j >= 0) {
                     tc_fence_after();
-                    const uint32_t p = tm_s + 64 * w, vd = v_desc + (tj & 1) * (2 * kPkV >> 4);
-#pragma unroll
-                    for (int k = 0; k < TOK / 16; ++k) {          // hi hi, hi lo, lo hi
-                        mma_ts(tm_o + 128 * x, p + 16 * k, vd + 2 * k, kPv, j >= NT || k > 0);
-                        mma_ts(tm_o + 128 * x, p + 16 * k, vd + (kPkV >> 4) + 2 * k, kPv, true);
-                        mma_ts(tm_o + 128 * x, p + 16 * k + kPLow, vd + 2 * k, kPv, true);
-                    }
+                    const uint32_t vd = v_desc + (tj & 1) * (2 * kPkV >> 4);
+                    run_pv_packed(tm_o + 128 * x, tm_s + 64 * w, vd, vd + (kPkV >> 4), kPv, j >= NT);
                     if (trail) mma_commit(&s.v_empty[tj & 1]);
                     if (tj == g + n - 1) mma_commit(&s.o_full[x]);
                 }
@@ -249,13 +466,8 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
                 if (!ok) break;
                 tc_fence_after();
                 if (i < NT * n) {
-                    const uint32_t kd = k_desc + (ti & 1) * (2 * kPkK >> 4), qa = tm_q + 64 * x, qd = q_desc + x * (kPkQ >> 4);
-#pragma unroll
-                    for (int k = 0; k < 24; ++k) {                // hi hi, hi lo, lo hi
-                        const uint32_t kb = kd + (((k >> 3) == 1 ? kPkK >> 4 : 0) + (((k >> 2 & 1) * (kPkK / 2) + (k & 3) * 32) >> 4));
-                        if (k < 16) mma_ts(tm_s + 64 * w, qa + 8 * (k & 7), kb, kQk, k > 0);
-                        else mma_ss(tm_s + 64 * w, qd + (((k >> 2 & 1) * (kPkQ / 2) + (k & 3) * 32) >> 4), kb, kQk, true);
-                    }
+                    const uint32_t kd = k_desc + (ti & 1) * (2 * kPkK >> 4);
+                    run_qk_packed(tm_s + 64 * w, tm_q + 64 * x, q_desc + x * (kPkQ >> 4), kd, kd + (kPkK >> 4), kQk);
                     mma_commit(&s.s_full[w]);
                     if (trail) mma_commit(&s.k_empty[ti & 1]);
                 }
@@ -316,10 +528,10 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
                     warp_arrive(&s.p_ready[w]);
                     continue;
                 }
-                const int e = *reinterpret_cast<volatile int*>(&s.vexp[g & 7]);
+                const int e = *reinterpret_cast<volatile int*>(&s.exps[1][g & 7]);
                 // (finite and not 0, so that what is masked stays masked)
-                const float here = fminf(fmaxf(scale * exp2i(*reinterpret_cast<volatile int*>(&s.kexp[g & 7])), 0x1p-126f), 0x1p127f);
-                ok = softmax_tile<TOK, NT == 2 ? 32 : 64, true>(tm_s + 64 * w + lanes, my_o, len - (c.t + i) * TOK, here, (float)e, exp2i(-e),
+                const float here = fminf(fmaxf(scale * exp2i(*reinterpret_cast<volatile int*>(&s.exps[0][g & 7])), 0x1p-126f), 0x1p127f);
+                ok = softmax_rolled<TOK, true>(tm_s + 64 * w + lanes, my_o, len - (c.t + i) * TOK, here, (float)e, exp2i(-e),
                                                                kLift, i == 0, st, &s.p_ready[w], [&] {
                     // O is idle once the last product into it has completed: with two row
                     // tiles S came behind it, with one it has freed tile g - 1's V stage
