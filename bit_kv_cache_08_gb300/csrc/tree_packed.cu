@@ -268,8 +268,8 @@ __device__ __forceinline__ bool tree_values(const uint8_t* vb, const uint8_t* re
 
 // ---------------------------------------------------------------- cached tokens
 struct TreePackedSmem {
-    // ready: a raw tile's levels are prepared [K, V]; raw_empty: its operands are built
-    uint64_t raw_full[kMaxRaw], ready[2][kMaxRaw], raw_empty[kMaxRaw];
+    // of raw tiles of keys and of values: ready: the levels are prepared; raw_empty: the operands are built
+    uint64_t raw_full[2][kMaxRaw], ready[2][kMaxRaw], raw_empty[2][kMaxRaw];
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], q_full, drained;
     uint32_t tmem;
     int stop;
@@ -283,15 +283,15 @@ struct TreePackedLayout {
     static constexpr int kSoft = 4 * NT, kThreads = 32 * (kSoft + 3 + 2 * kBuildWarps);
     static constexpr int HB = head_block_bytes(B, BITS);
     static constexpr int kBlocks = kPkTok / B;                 // blocks per tile
-    static constexpr int kTile = kBlocks * 2 * HB;             // bytes of a raw tile: (K, V) per block,
-    static constexpr int kRaw = kTile + 4 * kRest;             // and the rests of its levels [K, V][S, Z]
+    static constexpr int kTile = kBlocks * HB;                 // bytes of a raw tile of keys or of values: its blocks,
+    static constexpr int kRaw = kTile + 2 * kRest;             // and the rests of its levels [S, Z]
     static constexpr int kHeader = 1024;
     static_assert(sizeof(TreePackedSmem) <= kHeader, "header");
     static constexpr int kFixed = 1024 + kHeader + NT * kPkQ + 4 * kPkK + 4 * kPkV;
-    static constexpr int kFit = (227 * 1024 - kFixed) / kRaw;
+    static constexpr int kFit = (227 * 1024 - kFixed) / (2 * kRaw);
     static constexpr int kRawStages = kFit < kMaxRaw ? kFit : kMaxRaw;
     static_assert(kRawStages >= 2, "a raw tile in flight while another is built");
-    static constexpr size_t bytes = kFixed + kRawStages * kRaw;
+    static constexpr size_t bytes = kFixed + 2 * kRawStages * kRaw;
 };
 
 template <int B, int BITS, int NT>
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
     uint8_t* q_lo = base + Lay::kHeader;          // [row tile]
     uint8_t* k_op = q_lo + NT * kPkQ;             // [stage][hi, lo]
     uint8_t* v_op = k_op + 4 * kPkK;              // [stage][hi, lo]
-    uint8_t* raw = v_op + 4 * kPkV;               // [raw stage]: [block][K, V], rests
+    uint8_t* raw = v_op + 4 * kPkV;               // [K, V][raw stage]: blocks, rests
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rt = blockIdx.x % a.row_tiles;
     const int64_t range = blockIdx.x / a.row_tiles;
@@ -320,11 +320,10 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
 
     if (tid == 0) {
         s.stop = 0;
-        for (int i = 0; i < kRawStages; ++i) {
-            mbar_init(&s.raw_full[i], 1);
-            mbar_init(&s.ready[0][i], 1);
-            mbar_init(&s.ready[1][i], 1);
-            mbar_init(&s.raw_empty[i], 2 * kBuildWarps);
+        for (int i = 0; i < 2 * kRawStages; ++i) {
+            mbar_init(&s.raw_full[i & 1][i >> 1], 1);
+            mbar_init(&s.ready[i & 1][i >> 1], 1);
+            mbar_init(&s.raw_empty[i & 1][i >> 1], kBuildWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.k_full[i], kBuildWarps);
@@ -352,8 +351,10 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
     bool ok = true;
 
     if (warp == kSoft + 1 || warp == kSoft + 2) {
-        // ---------------------------------------------------------- raw tiles, and the levels of their keys / values
-        const int kind = warp - (kSoft + 1);      // the keys' warp copies
+        // ---------------------------------------------------------- raw tiles and their levels: a warp for the keys, one for the values
+        // (in rings of their own: a tile's values are built two tiles behind its keys)
+        const int kind = warp - (kSoft + 1);
+        uint8_t* ring = raw + kind * kRawStages * Lay::kRaw;
         TreeCursor f = c;                         // of the copies
         int held = -1, held0 = -32;               // lane i holds block held0 + i of the sequence
         auto fetch = [&] {
@@ -368,12 +369,12 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
             }
             int64_t page = __shfl_sync(kFull, held, (first - held0 + lane) & 31);   // lane x: block x of the tile
             if (lane >= Lay::kBlocks) page = -1;
-            const uint32_t bytes = __popc(__ballot_sync(kFull, page >= 0)) * (2 * Lay::HB);
-            if (lane == 0) mbar_arrive_expect_tx(&s.raw_full[st], bytes);
+            const uint32_t bytes = __popc(__ballot_sync(kFull, page >= 0)) * Lay::HB;
+            if (lane == 0) mbar_arrive_expect_tx(&s.raw_full[kind][st], bytes);
             __syncwarp();
             if (page >= 0)
-                bulk_g2s(raw + st * Lay::kRaw + lane * 2 * Lay::HB, a.pool + page * a.block_bytes + (int64_t)(2 * f.h) * Lay::HB,
-                         2 * Lay::HB, &s.raw_full[st]);
+                bulk_g2s(ring + st * Lay::kRaw + lane * Lay::HB, a.pool + page * a.block_bytes + (int64_t)(2 * f.h + kind) * Lay::HB,
+                         Lay::HB, &s.raw_full[kind][st]);
             ++fetched;
             if (++f.t == f.tiles && fetched < total) {
                 tree_next<TOK, true>(a, f);
@@ -382,19 +383,19 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
         };
         for (; g < total && ok; ++g) {
             // (one stage less in flight than there are: its wait is for tile g - 2)
-            while (kind == 0 && fetched < total && fetched < g + kRawStages - 1 && ok) {
+            while (fetched < total && fetched < g + kRawStages - 1 && ok) {
                 if (fetched >= kRawStages)        // the stage's last tile has been built
-                    ok = warp_wait_or_stop(&s.raw_empty[fetched % kRawStages], (fetched / kRawStages - 1) & 1, stop, kWaitLimit);
+                    ok = warp_wait_or_stop(&s.raw_empty[kind][fetched % kRawStages], (fetched / kRawStages - 1) & 1, stop, kWaitLimit);
                 if (ok) fetch();
             }
             const int st = g % kRawStages;
-            ok = ok && warp_wait_or_stop(&s.raw_full[st], (g / kRawStages) & 1, stop, kWaitLimit);
+            ok = ok && warp_wait_or_stop(&s.raw_full[kind][st], (g / kRawStages) & 1, stop, kWaitLimit);
             if (!ok) break;
             const int x = lane / (32 / Lay::kBlocks);              // this lane's block
             const bool there = c.t * Lay::kBlocks + x < c.tokens / B;
-            uint8_t* tile = raw + st * Lay::kRaw;
+            uint8_t* tile = ring + st * Lay::kRaw;
             int c_exp;
-            const int e = prepare_levels<B, BITS>(tile + (2 * x + kind) * Lay::HB, there, lane, tile + Lay::kTile + 2 * kind * kRest, c_exp);
+            const int e = prepare_levels<B, BITS>(tile + x * Lay::HB, there, lane, tile + Lay::kTile, c_exp);
             fence_async_smem();                   // (before the stage's next copy writes over it)
             if (lane == 0) {
                 s.exps[kind][g & 7] = e;
@@ -411,10 +412,10 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
         for (; g < total && ok; ++g) {
             const int st = g % kRawStages, par = g & 1;
             ok = warp_wait_or_stop(&s.ready[kind][st], (g / kRawStages) & 1, stop, kWaitLimit) &&
-                 warp_wait_or_stop(&s.raw_full[st], (g / kRawStages) & 1, stop, kWaitLimit);
+                 warp_wait_or_stop(&s.raw_full[kind][st], (g / kRawStages) & 1, stop, kWaitLimit);
             if (!ok) break;
-            const uint8_t* tile = raw + st * Lay::kRaw;
-            const uint8_t* hb = tile + ((B == 64 ? 0 : sb) * 2 + kind) * Lay::HB;
+            const uint8_t* tile = raw + (kind * kRawStages + st) * Lay::kRaw;
+            const uint8_t* hb = tile + (B == 64 ? 0 : sb) * Lay::HB;
             const float up = exp2i(-*reinterpret_cast<volatile int*>(&s.c_exps[kind][g & 7]));
             if (kind == 0) {
                 ok = tree_keys<B, BITS>(hb, tile + Lay::kTile, grp, sb, lane, up, k_op + par * 2 * kPkK, [&] {
@@ -422,14 +423,14 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
                 });
             } else {
                 const bool there = B == 64 || c.t * Lay::kBlocks + sb < c.tokens / B;   // else its values are zero
-                ok = tree_values<B, BITS>(hb, tile + Lay::kTile + 2 * kRest, there, grp, sb, lane, up, v_op + par * 2 * kPkV, [&] {
+                ok = tree_values<B, BITS>(hb, tile + Lay::kTile, there, grp, sb, lane, up, v_op + par * 2 * kPkV, [&] {
                     return g < 2 || warp_wait_or_stop(&s.v_empty[par], ((g >> 1) - 1) & 1, stop, kWaitLimit);
                 });
             }
             if (!ok) break;
             fence_async_smem();
             warp_arrive(kind ? &s.v_full[par] : &s.k_full[par]);
-            warp_arrive(&s.raw_empty[st]);
+            warp_arrive(&s.raw_empty[kind][st]);
             if (B != 64 && ++c.t == c.tiles && g + 1 < total) tree_next<TOK, true>(a, c);
         }
     } else if (warp == kSoft) {
@@ -558,9 +559,9 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
     __syncthreads();
     if (*stop) {   // a wait ran out: copies in flight land before the CTA ends
         if (tid == 0) raise_error(a.err, KVARN_DEVERR_WAIT_TIMEOUT);
-        if (warp == kSoft + 1)
+        if (warp == kSoft + 1 || warp == kSoft + 2)
             for (int i = max(0, fetched - kRawStages); i < fetched; ++i)
-                mbar_wait_bounded(&s.raw_full[i % kRawStages], (i / kRawStages) & 1, kWaitLimit);
+                mbar_wait_bounded(&s.raw_full[warp - (kSoft + 1)][i % kRawStages], (i / kRawStages) & 1, kWaitLimit);
         __syncthreads();
     }
     if (warp == kSoft) {
