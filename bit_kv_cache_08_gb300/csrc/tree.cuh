@@ -220,8 +220,17 @@ __device__ __forceinline__ void run_pv_bf16(uint32_t d, uint32_t p, uint32_t v, 
 #undef TREE_PV
     static_assert(kPLow == 8, "the halves of P");
 }
-// S = Q K'^T of a packed tile: high halves of Q in tensor memory (qa), low ones at q; K' high (kh) and low (kl).
-__device__ __forceinline__ void run_qk_packed(uint32_t d, uint32_t qa, uint32_t q, uint32_t kh, uint32_t kl, uint32_t shape) {
+// S = Q K'^T of a packed tile: high halves of Q in tensor memory (qh), low ones there too (ql) or, run_qk_packed_low,
+// at a descriptor; K' high (kh) and low (kl).
+__device__ __forceinline__ void run_qk_packed(uint32_t d, uint32_t qh, uint32_t ql, uint32_t kh, uint32_t kl, uint32_t shape) {
+#define TREE_QK(t_at, k_at, x) \
+    TREE_TS("%3", "%4", t_at, "%6", k_at, x) TREE_TS("%3", "%5", t_at, "%6", k_at, "one") TREE_TS("%3", "%4", t_at, "%7", k_at, "one")
+    asm volatile(TREE_RUN TREE_QK("0", "0", "none") TREE_QK("8", "2", "one") TREE_QK("16", "4", "one") TREE_QK("24", "6", "one")
+                 TREE_QK("32", "512", "one") TREE_QK("40", "514", "one") TREE_QK("48", "516", "one") TREE_QK("56", "518", "one") "}\n"
+                 ::"r"(shape), "r"(kOperandHigh), "r"(0u), "r"(d), "r"(qh), "r"(ql), "r"(kh), "r"(kl) : "memory");
+#undef TREE_QK
+}
+__device__ __forceinline__ void run_qk_packed_low(uint32_t d, uint32_t qa, uint32_t q, uint32_t kh, uint32_t kl, uint32_t shape) {
 #define TREE_QK(t_at, q_at, k_at, x) \
     TREE_TS("%3", "%4", t_at, "%6", k_at, x) TREE_TS("%3", "%4", t_at, "%7", k_at, "one") TREE_SS("%3", "%5", q_at, "%6", k_at, "one")
     asm volatile(TREE_RUN TREE_QK("0", "0", "0", "none") TREE_QK("8", "2", "2", "one") TREE_QK("16", "4", "4", "one") TREE_QK("24", "6", "6", "one")

@@ -8,8 +8,8 @@
 // tree_rotate_kernel turns the queries once: H (sigma q) / sqrt(128), each row scaled by a
 // power of two and split into two fp16 halves. In the main kernel a CTA has one or two
 // tiles of 128 rows (NT), which share the built operands; Q's high half lies in tensor memory
-// (64 columns a row tile), its low half in shared memory, beside S / P of two steps
-// (2 x 64 columns) and O (128 a row tile).
+// (64 columns a row tile), beside S / P of two steps (2 x 64 columns) and O (128 a row tile); its
+// low half too, where one row tile leaves room, else in shared memory.
 // Warps: 4 a row tile for the softmax, one that issues the products, one that copies raw
 // tiles and prepares the levels of their keys, one for those of the values, 8 that build
 // operands, as in packed_build.cuh without meeting at a barrier.
@@ -21,6 +21,7 @@
 namespace kvarn {
 
 constexpr int kTreeTopQuery = 14;    // a rotated query's channels up to 2^14
+constexpr uint32_t kQLow = 384;      // column of the queries' low halves (one row tile)
 
 // ---------------------------------------------------------------- queries
 // A warp a row: [unit][rows_pad][hi 128 | lo 128] fp16, and what the scores are to be
@@ -287,7 +288,8 @@ struct TreePackedLayout {
     static constexpr int kRaw = kTile + 2 * kRest;             // and the rests of its levels [S, Z]
     static constexpr int kHeader = 1024;
     static_assert(sizeof(TreePackedSmem) <= kHeader, "header");
-    static constexpr int kFixed = 1024 + kHeader + NT * kPkQ + 4 * kPkK + 4 * kPkV;
+    static constexpr int kQLowBytes = NT == 2 ? 2 * kPkQ : 0;  // (with one row tile in tensor memory)
+    static constexpr int kFixed = 1024 + kHeader + kQLowBytes + 4 * kPkK + 4 * kPkV;
     static constexpr int kFit = (227 * 1024 - kFixed) / (2 * kRaw);
     static constexpr int kRawStages = kFit < kMaxRaw ? kFit : kMaxRaw;
     static_assert(kRawStages >= 2, "a raw tile in flight while another is built");
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
     uint8_t* base = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
     TreePackedSmem& s = *reinterpret_cast<TreePackedSmem*>(base);
     uint8_t* q_lo = base + Lay::kHeader;          // [row tile]
-    uint8_t* k_op = q_lo + NT * kPkQ;             // [stage][hi, lo]
+    uint8_t* k_op = q_lo + Lay::kQLowBytes;       // [stage][hi, lo]
     uint8_t* v_op = k_op + 4 * kPkK;              // [stage][hi, lo]
     uint8_t* raw = v_op + 4 * kPkV;               // [K, V][raw stage]: blocks, rests
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -318,6 +320,8 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
     const int total = (int)((range + 1) * W / n_ranges - x_beg);   // tiles of this CTA
     tree_locate<TOK, true>(a, x_beg, lane, c);
 
+    // softmax warps of row tile x that have rows (one at least): the others leave at once
+    const auto alive = [&](int x) { return min(4, max(1, (a.drafts * a.G - (rt * NT + x) * kPRows + 31) / 32)); };
     if (tid == 0) {
         s.stop = 0;
         for (int i = 0; i < 2 * kRawStages; ++i) {
@@ -331,10 +335,10 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
             mbar_init(&s.v_full[i], kBuildWarps);
             mbar_init(&s.v_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_ready[i], 4);
+            mbar_init(&s.p_ready[i], NT == 2 ? alive(i) : alive(0));
             mbar_init(&s.o_full[i], 1);
         }
-        mbar_init(&s.q_full, kSoft);
+        mbar_init(&s.q_full, NT == 2 ? alive(0) + alive(1) : alive(0));
         mbar_init(&s.drained, 1);
         fence_mbar_init();
     }
@@ -468,7 +472,8 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
                 tc_fence_after();
                 if (i < NT * n) {
                     const uint32_t kd = k_desc + (ti & 1) * (2 * kPkK >> 4);
-                    run_qk_packed(tm_s + 64 * w, tm_q + 64 * x, q_desc + x * (kPkQ >> 4), kd, kd + (kPkK >> 4), kQk);
+                    if (NT == 1) run_qk_packed(tm_s + 64 * w, tm_q, tm_q + kQLow, kd, kd + (kPkK >> 4), kQk);
+                    else run_qk_packed_low(tm_s + 64 * w, tm_q + 64 * x, q_desc + x * (kPkQ >> 4), kd, kd + (kPkK >> 4), kQk);
                     mma_commit(&s.s_full[w]);
                     if (trail) mma_commit(&s.k_empty[ti & 1]);
                 }
@@ -487,6 +492,7 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t my_o = tm_o + 128 * x + lanes;
         int units = 0;
+        if ((warp & 3) >= alive(x)) g = total;
         for (; g < total && ok; ++units) {
             const int n = min(c.tiles - c.t, total - g);
             const bool valid = r < tree_rows(a, c.b) * a.G, some = __any_sync(kFull, valid);
@@ -509,9 +515,14 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
                     y[4 * i + 2] = hi[i].z;
                     y[4 * i + 3] = hi[i].w;
                     const int at = 4 * k + i;
-                    *reinterpret_cast<uint4*>(q_lo + x * kPkQ + (at >> 3) * (kPkQ / 2) + swizzled((warp & 3) * 32 + lane, at & 7)) = lo[i];
+                    if (NT == 2) *reinterpret_cast<uint4*>(q_lo + x * kPkQ + (at >> 3) * (kPkQ / 2) + swizzled((warp & 3) * 32 + lane, at & 7)) = lo[i];
                 }
                 tmem_st16(tm_q + 64 * x + 16 * k + lanes, y);
+                if (NT == 1) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[4 * i] = lo[i].x, y[4 * i + 1] = lo[i].y, y[4 * i + 2] = lo[i].z, y[4 * i + 3] = lo[i].w;
+                    tmem_st16(tm_q + kQLow + 16 * k + lanes, y);
+                }
             }
             const float scale = valid ? a.sm_scale * kLog2e * a.turned_scale[u * a.rows_pad + r] : 0.f;
             tmem_wait_st();
