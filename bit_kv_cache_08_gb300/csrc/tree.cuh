@@ -110,67 +110,73 @@ __device__ __forceinline__ float4* tree_partial(const TreeArgs& a, int64_t slot,
     return a.partials + (slot * 33 + quad) * a.rows_pad + row;
 }
 
-// softmax_tile (prefix.cuh) with S read from tensor memory twice, 16 columns at a time in
-// rolled loops: a tenth of its instructions in memory, for kernels whose warps' code together
-// does not fit the instruction caches.
+// softmax_tile (prefix.cuh) with S read from tensor memory twice, 32 columns at a time in
+// rolled loops: a fifth of its instructions in memory, for kernels whose warps' code together
+// does not fit the instruction caches. The reference is put kAhead above the largest score when it
+// moves, so that it moves the less often: a weight is then at most 2^(8 + lift), the largest
+// of the tile that moved it 2^(lift - kAhead).
+constexpr float kAhead = 4.f;
 template <int TOK, bool HALF, typename Idle>
 __device__ __forceinline__ bool softmax_rolled(uint32_t my_s, uint32_t my_o, int shown, float scale, float bias, float unbias, float lift,
                                                bool first, RowState& st, uint64_t* p_ready, Idle&& o_idle) {
     const bool cut = __any_sync(kFull, shown < TOK);
-    auto load = [&](int c0, uint32_t (&x)[16]) {
-        tmem_ld16(my_s + c0, x);
+    auto load = [&](int c0, uint32_t (&x)[32]) {
+        tmem_ld32(my_s + c0, x);
         tmem_wait_ld();
         if (cut) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < 32; ++i)
                 if (c0 + i >= shown) x[i] = 0xff800000u;   // -inf, whatever was there
         }
     };
     float mx = -INFINITY;
 #pragma unroll 1
-    for (int c0 = 0; c0 < TOK; c0 += 16) {
-        uint32_t x[16];
+    for (int c0 = 0; c0 < TOK; c0 += 32) {
+        uint32_t x[32];
         load(c0, x);
-        float a = mx, b = -INFINITY;
+        float y[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {                  // (three-input maxima)
-            a = fmaxf(fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), a);
-            b = fmaxf(fmaxf(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), b);
-        }
-        mx = fmaxf(a, b);
+        for (int i = 0; i < 32; i += 2)                    // (three-input maxima)
+            y[(i >> 1) & 3] = fmaxf(fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), y[(i >> 1) & 3]);
+        mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
     }
     const float top = fmaf(mx, scale, bias);
     const bool grow = top - st.m > 8.f;                    // (from -inf at once; false where nothing is shown)
+    const float ref = top + kAhead;
     if (!first && __any_sync(kFull, grow)) {
         if (!o_idle()) return false;
-        const float f = grow && st.m != -INFINITY ? ex2(st.m - top) : 1.f;
+        const float f = grow && st.m != -INFINITY ? ex2(st.m - ref) : 1.f;
         st.l *= f;
 #pragma unroll 1
-        for (int c = 0; c < kD; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(my_o + c, o);
+        for (int c = 0; c < kD; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(my_o + c, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st16(my_o + c, o);
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(my_o + c, o);
         }
     }
-    if (grow) st.m = top;
+    if (grow) st.m = ref;
     const float off = st.m == -INFINITY ? 0.f : bias + lift - st.m;
     const float2 scale2 = make_float2(scale, scale), off2 = make_float2(off, off);
     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
-    for (int c0 = 0; c0 < TOK; c0 += 16) {
-        uint32_t x[16], y[16];                             // (y: high halves, low halves)
+    for (int c0 = 0; c0 < TOK; c0 += 32) {
+        uint32_t x[32];
         load(c0, x);
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), scale2, off2);
-            const float2 p = make_float2(ex2(e.x), ex2(e.y));
-            sum = __fadd2_rn(sum, p);
-            split_pair<HALF>(p.x, p.y, y[i >> 1], y[8 + (i >> 1)]);
+        for (int c = 0; c < 32; c += 16) {
+            uint32_t y[16];                                // high halves, low halves
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[c + i]), __uint_as_float(x[c + i + 1])), scale2, off2);
+                const float2 p = make_float2(ex2(e.x), ex2(e.y));
+                sum = __fadd2_rn(sum, p);
+                split_pair<HALF>(p.x, p.y, y[i >> 1], y[8 + (i >> 1)]);
+            }
+            tmem_st16(my_s + c0 + c, y);                   // (over columns of S that have been read)
         }
-        tmem_st16(my_s + c0, y);                           // (over columns of S that have been read)
     }
     tmem_wait_st();
     tc_fence_before();

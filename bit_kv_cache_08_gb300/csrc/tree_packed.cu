@@ -20,6 +20,7 @@
 
 namespace kvarn {
 
+constexpr int kTreeBuild = 4;        // warps that build a tile's keys, and as many its values
 constexpr int kTreeTopQuery = 14;    // a rotated query's channels up to 2^14
 constexpr uint32_t kQLow = 384;      // column of the queries' low halves (one row tile)
 
@@ -158,12 +159,6 @@ __device__ __forceinline__ __half2 scaled_channels(uint32_t c, float up) {
 // Both halves of a register one of them.
 __device__ __forceinline__ __half2 both(uint32_t x, int high) { return u32_as_h2(__byte_perm(x, x, high ? 0x3232 : 0x1010)); }
 
-// Four halves, one down.
-__device__ __forceinline__ void next_half(uint2& x) {
-    x.x = __funnelshift_r(x.x, x.y, 16);
-    x.y >>= 16;
-}
-
 // K' of group g of the 32 records of half sb of a tile, a record a lane: tokens 4 (lane / 4) + k,
 // channels 32 g + 8 (lane % 4) .. + 7. hb: the half's K head-block, rest: its rests; up:
 // 2^-(C's exponent); ready(): waits until dst (hi, then lo) may be written (false: gave up).
@@ -189,29 +184,26 @@ __device__ __forceinline__ bool tree_keys(const uint8_t* hb, const uint8_t* rest
         }
     }
     const int at = 2 * (g * B + half0 + 4 * ra), block = B == 64 ? 0 : sb * 4 * B * 2;
-    uint2 sh = *reinterpret_cast<const uint2*>(hb + off_s(B, BITS) + at);   // (4 tokens)
-    uint2 zh = *reinterpret_cast<const uint2*>(hb + off_z(B, BITS) + at);
-    uint2 sl = *reinterpret_cast<const uint2*>(rest + block + at);
-    uint2 zl = *reinterpret_cast<const uint2*>(rest + kRest + block + at);
+    const uint2 sh = *reinterpret_cast<const uint2*>(hb + off_s(B, BITS) + at);
+    const uint2 zh = *reinterpret_cast<const uint2*>(hb + off_z(B, BITS) + at);
+    const uint2 sl = *reinterpret_cast<const uint2*>(rest + block + at);
+    const uint2 zl = *reinterpret_cast<const uint2*>(rest + kRest + block + at);
     const uint4 cu = *reinterpret_cast<const uint4*>(hb + off_C(B, BITS) + 2 * (32 * g + 8 * rb));
     const __half2 c[4] = {scaled_channels(cu.x, up), scaled_channels(cu.y, up), scaled_channels(cu.z, up), scaled_channels(cu.w, up)};
     if (!ready()) return false;
     dst += (g >> 1) * (kPkK / 2);
-    // (rolled, what belongs to a token moving down: see the head of the kernel)
-#pragma unroll 1
+#pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const __half2 s1 = both(sh.x, 0), z1 = both(zh.x, 0), s2 = both(sl.x, 0), z2 = both(zl.x, 0);
-        const uint32_t w8 = w[0] >> 8;
+        const __half2 s1 = both(k < 2 ? sh.x : sh.y, k & 1), z1 = both(k < 2 ? zh.x : zh.y, k & 1);
+        const __half2 s2 = both(k < 2 ? sl.x : sl.y, k & 1), z2 = both(k < 2 ? zl.x : zl.y, k & 1);
+        const uint32_t w8 = w[k] >> 8;
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) build_pair(code_pair<BITS>(w[0], w8, hw[0], p, p), s1, z1, s2, z2, c[p], hi[p], lo[p]);
+        for (int p = 0; p < 4; ++p) build_pair(code_pair<BITS>(w[k], w8, hw[k], p, p), s1, z1, s2, z2, c[p], hi[p], lo[p]);
         const uint32_t to = swizzled(32 * sb + 4 * ra + k, 4 * (g & 1) + rb);
         // (an absent half's scores are masked, whatever its raw bytes were)
         *reinterpret_cast<uint4*>(dst + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(dst + kPkK + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        next_half(sh), next_half(zh), next_half(sl), next_half(zl);
-        w[0] = w[1], w[1] = w[2], w[2] = w[3];
-        if (BITS == 3) hw[0] = hw[1], hw[1] = hw[2], hw[2] = hw[3];
     }
     return true;
 }
@@ -242,27 +234,23 @@ __device__ __forceinline__ bool tree_values(const uint8_t* vb, const uint8_t* re
     const uint32_t s1[4] = {sh.x, sh.y, sh.z, sh.w}, z1[4] = {zh.x, zh.y, zh.z, zh.w};
     const uint32_t s2[4] = {sl.x, sl.y, sl.z, sl.w}, z2[4] = {zl.x, zl.y, zl.z, zl.w};
     const uint2 cu = *reinterpret_cast<const uint2*>(vb + off_C(B, BITS) + 2 * (32 * g + 4 * ra));
-    uint2 c = make_uint2(h2_as_u32(scaled_channels(cu.x, up)), h2_as_u32(scaled_channels(cu.y, up)));   // (4 channels)
+    const uint32_t c[2] = {h2_as_u32(scaled_channels(cu.x, up)), h2_as_u32(scaled_channels(cu.y, up))};
     if (!ready()) return false;
-#pragma unroll 1
+#pragma unroll
     for (int k = 0; k < 4; ++k) {
-        // 4-bit: a word a channel; else a word for two, the second's fields behind the first's
-        const uint32_t x = BITS == 4 ? w[0] : w[0] >> 2 * (k & 1), x8 = BITS == 4 ? x >> 8 : w[0] >> 8 + 2 * (k & 1);
-        const uint32_t xh = BITS == 3 ? hw >> (8 * (k >> 1) + (k & 1)) : 0u;
-        const __half2 ck = both(c.x, 0);
+        const uint32_t w8 = w[k] >> 8;
+        const __half2 ck = both(c[k >> 1], k & 1);
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {                 // tokens 2p, 2p + 1
-            const int j = BITS == 4 ? p : 4 * (p >> 1) + 2 * (p & 1);
-            build_pair(code_pair<BITS>(x, x8, xh, j, j), u32_as_h2(s1[p]), u32_as_h2(z1[p]), u32_as_h2(s2[p]), u32_as_h2(z2[p]), ck, hi[p], lo[p]);
+            const int j = BITS == 4 ? p : 4 * (p >> 1) + 2 * (p & 1) + (k & 1);
+            build_pair(code_pair<BITS>(w[k], w8, hw, j, 8 * (k >> 1) + j), u32_as_h2(s1[p]), u32_as_h2(z1[p]), u32_as_h2(s2[p]),
+                       u32_as_h2(z2[p]), ck, hi[p], lo[p]);
             if (!there) hi[p] = lo[p] = 0u;
         }
         const uint32_t to = swizzled(32 * g + 4 * ra + k, 4 * sb + rb);
         *reinterpret_cast<uint4*>(dst + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(dst + kPkV + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        next_half(c);
-        if (BITS == 4) w[0] = w[1], w[1] = w[2], w[2] = w[3];
-        else if (k == 1) w[0] = w[2];
     }
     return true;
 }
@@ -281,7 +269,7 @@ struct TreePackedSmem {
 
 template <int B, int BITS, int NT>
 struct TreePackedLayout {
-    static constexpr int kSoft = 4 * NT, kThreads = 32 * (kSoft + 3 + 2 * kBuildWarps);
+    static constexpr int kSoft = 4 * NT, kThreads = 32 * (kSoft + 3 + 2 * kTreeBuild);
     static constexpr int HB = head_block_bytes(B, BITS);
     static constexpr int kBlocks = kPkTok / B;                 // blocks per tile
     static constexpr int kTile = kBlocks * HB;                 // bytes of a raw tile of keys or of values: its blocks,
@@ -327,12 +315,12 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
         for (int i = 0; i < 2 * kRawStages; ++i) {
             mbar_init(&s.raw_full[i & 1][i >> 1], 1);
             mbar_init(&s.ready[i & 1][i >> 1], 1);
-            mbar_init(&s.raw_empty[i & 1][i >> 1], kBuildWarps);
+            mbar_init(&s.raw_empty[i & 1][i >> 1], kTreeBuild);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.k_full[i], kBuildWarps);
+            mbar_init(&s.k_full[i], kTreeBuild);
             mbar_init(&s.k_empty[i], 1);
-            mbar_init(&s.v_full[i], kBuildWarps);
+            mbar_init(&s.v_full[i], kTreeBuild);
             mbar_init(&s.v_empty[i], 1);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_ready[i], NT == 2 ? alive(i) : alive(0));
@@ -410,26 +398,30 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
         }
     } else if (warp > kSoft) {
         // ---------------------------------------------------------- operands from codes
-        // 8 warps the keys, 8 the values: warp bw of each group grp of the 32 records of half
-        // sb, a record a lane
-        const int kind = (warp - (kSoft + 3)) / kBuildWarps, bw = (warp - (kSoft + 3)) % kBuildWarps, grp = bw & 3, sb = bw >> 2;
+        // kTreeBuild warps the keys, as many the values; a warp has group grp of the 32 records of
+        // one half of the tile, or of both, a record a lane
+        const int kind = (warp - (kSoft + 3)) / kTreeBuild, bw = (warp - (kSoft + 3)) % kTreeBuild, grp = bw & 3;
         for (; g < total && ok; ++g) {
             const int st = g % kRawStages, par = g & 1;
-            ok = warp_wait_or_stop(&s.ready[kind][st], (g / kRawStages) & 1, stop, kWaitLimit) &&
-                 warp_wait_or_stop(&s.raw_full[kind][st], (g / kRawStages) & 1, stop, kWaitLimit);
+            // (the copies' barrier has been waited for by the warp that prepared the levels)
+            ok = warp_wait_or_stop(&s.ready[kind][st], (g / kRawStages) & 1, stop, kWaitLimit);
             if (!ok) break;
             const uint8_t* tile = raw + (kind * kRawStages + st) * Lay::kRaw;
-            const uint8_t* hb = tile + (B == 64 ? 0 : sb) * Lay::HB;
             const float up = exp2i(-*reinterpret_cast<volatile int*>(&s.c_exps[kind][g & 7]));
-            if (kind == 0) {
-                ok = tree_keys<B, BITS>(hb, tile + Lay::kTile, grp, sb, lane, up, k_op + par * 2 * kPkK, [&] {
-                    return g < 2 || warp_wait_or_stop(&s.k_empty[par], ((g >> 1) - 1) & 1, stop, kWaitLimit);
-                });
-            } else {
-                const bool there = B == 64 || c.t * Lay::kBlocks + sb < c.tokens / B;   // else its values are zero
-                ok = tree_values<B, BITS>(hb, tile + Lay::kTile, there, grp, sb, lane, up, v_op + par * 2 * kPkV, [&] {
-                    return g < 2 || warp_wait_or_stop(&s.v_empty[par], ((g >> 1) - 1) & 1, stop, kWaitLimit);
-                });
+#pragma unroll 1
+            for (int sb = bw >> 2; sb < 2 && ok; sb += kTreeBuild / 4) {
+                const uint8_t* hb = tile + (B == 64 ? 0 : sb) * Lay::HB;
+                const bool wait = g >= 2 && sb == bw >> 2;
+                if (kind == 0) {
+                    ok = tree_keys<B, BITS>(hb, tile + Lay::kTile, grp, sb, lane, up, k_op + par * 2 * kPkK, [&] {
+                        return !wait || warp_wait_or_stop(&s.k_empty[par], ((g >> 1) - 1) & 1, stop, kWaitLimit);
+                    });
+                } else {
+                    const bool there = B == 64 || c.t * Lay::kBlocks + sb < c.tokens / B;   // else its values are zero
+                    ok = tree_values<B, BITS>(hb, tile + Lay::kTile, there, grp, sb, lane, up, v_op + par * 2 * kPkV, [&] {
+                        return !wait || warp_wait_or_stop(&s.v_empty[par], ((g >> 1) - 1) & 1, stop, kWaitLimit);
+                    });
+                }
             }
             if (!ok) break;
             fence_async_smem();
