@@ -73,7 +73,9 @@ constexpr size_t prefill_smem_bytes() {
            kPrefillVecs * 4;
 }
 
-template <int B, int BITS, int S>
+// ALL: every row sees every complete block, whatever its place in the chunk (drafted
+// tokens: tree.cu).
+template <int B, int BITS, int S, bool ALL = false>
 __global__ void __launch_bounds__(32) prefill_attn_kernel(AttnArgs a) {
     static_assert(BITS >= 2 && BITS <= 4, "2-, 3- or 4-bit codes");
     wait_prior_grids();
@@ -113,10 +115,10 @@ __global__ void __launch_bounds__(32) prefill_attn_kernel(AttnArgs a) {
     // this lane's vector (row gq of the MMAs) and the tokens it may see
     const int my_row = r0 + gq / G;
     const bool my_ok = gq < P * G && my_row < chunk;
-    const int my_vis = my_ok ? L - chunk + my_row + 1 : 0;
+    const int my_vis = !my_ok ? 0 : ALL ? L : L - chunk + my_row + 1;
     // the warp's last row sees the most
     const int last_row = min(chunk - 1, r0 + P - 1);
-    const int max_vis = L - chunk + last_row + 1;
+    const int max_vis = ALL ? L : L - chunk + last_row + 1;
     const int nvis = max_vis > 0 ? min(L / B, (max_vis + B - 1) / B) : 0;
     // this warp's share of those blocks (possibly none: its partial is then empty)
     const int jb = (int)((int64_t)split * nvis / NS), je = (int)((int64_t)(split + 1) * nvis / NS);
@@ -638,6 +640,44 @@ cudaError_t launch_prefill_attn(const kvarn_config& cfg, const void* q, int q_dt
     const unsigned mgrid = (unsigned)(((int64_t)a.batch * a.n_q + 3) / 4);
     return cfg.block_size == 32 ? launch_pdl(merge_kernel<32, true>, mgrid, 128, 0, st, a)
                                 : launch_pdl(merge_kernel<64, true>, mgrid, 128, 0, st, a);
+}
+
+// The partials of few drafted rows a sequence (their rows' queries q): `splits` of each, at `partials`
+// [batch * chunk][n_kv][splits][G][kPartialStride].
+cudaError_t launch_prefill_all(const kvarn_config& cfg, const void* q, int q_dtype, const void* pool, int64_t n_pool_blocks,
+                               int64_t block_bytes, const int32_t* block_table, int max_blocks, const int32_t* seq_lens, int batch,
+                               int chunk, float* partials, uint32_t* err, int splits, cudaStream_t st) {
+    AttnArgs a = {};
+    a.q = q;
+    a.q_dtype = q_dtype;
+    a.pool = (const uint8_t*)pool;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.err = err;
+    a.partials = partials;
+    a.n_pool_blocks = n_pool_blocks;
+    a.block_bytes = block_bytes;
+    a.max_blocks = max_blocks;
+    a.batch = batch;
+    a.n_q = cfg.n_q_heads;
+    a.n_kv = cfg.n_kv_heads;
+    a.G = cfg.n_q_heads / cfg.n_kv_heads;
+    a.chunk = chunk;
+    a.single = splits;
+    a.sm_scale = cfg.sm_scale;
+    a.flags = cfg.flags;
+    for (int i = 0; i < 4; ++i) a.sb[i] = cfg.sign_bits[i];
+    const int P = kPrefillVecs / a.G;
+    const int64_t warps = (int64_t)batch * a.n_kv * ((chunk + P - 1) / P) * splits;
+    if (warps > 0x7fffffff) return cudaErrorInvalidValue;
+    auto go = [&](auto kernel, size_t smem) { return launch_pdl(kernel, (unsigned)warps, 32, smem, st, a); };
+    if (cfg.block_size == 32)
+        return cfg.bits == 4   ? go(prefill_attn_kernel<32, 4, prefill_stages<32>(), true>, prefill_smem_bytes<32, 4>())
+               : cfg.bits == 3 ? go(prefill_attn_kernel<32, 3, prefill_stages<32>(), true>, prefill_smem_bytes<32, 3>())
+                               : go(prefill_attn_kernel<32, 2, prefill_stages<32>(), true>, prefill_smem_bytes<32, 2>());
+    return cfg.bits == 4   ? go(prefill_attn_kernel<64, 4, prefill_stages<64>(), true>, prefill_smem_bytes<64, 4>())
+           : cfg.bits == 3 ? go(prefill_attn_kernel<64, 3, prefill_stages<64>(), true>, prefill_smem_bytes<64, 3>())
+                           : go(prefill_attn_kernel<64, 2, prefill_stages<64>(), true>, prefill_smem_bytes<64, 2>());
 }
 
 }  // namespace kvarn

@@ -6,6 +6,10 @@
 namespace kvarn {
 
 cudaError_t launch_tree_bf16(const TreeArgs& a, bool wide, cudaStream_t st);
+cudaError_t launch_prefill_all(const kvarn_config& cfg, const void* q, int q_dtype, const void* pool, int64_t n_pool_blocks,
+                               int64_t block_bytes, const int32_t* block_table, int max_blocks, const int32_t* seq_lens, int batch,
+                               int chunk, float* partials, uint32_t* err, int splits, cudaStream_t st);
+int64_t prefill_splits(const kvarn_config& cfg, int64_t batch, int64_t chunk, int device);
 cudaError_t launch_tree_packed(const kvarn_config& c, const TreeArgs& a, bool wide, cudaStream_t st);
 
 namespace {
@@ -28,6 +32,15 @@ TreePlan tree_plan(const kvarn_config& c, int drafts, bool packed, int q_dtype) 
     return p;
 }
 
+// Query rows of a unit up to which the prefill kernel takes the packed cache's
+// tokens: 8 rows a warp, each warp expanding the codes for itself on mma.sync, so
+// its time grows by the warp, where a 128-row tile of tcgen05 costs the same for
+// one row as for all. 64 sequences x 8192 2-bit tokens, 8 kv heads, prefill kernel
+// against tree_packed_kernel: 8 rows 181 / 510 us, 16 293 / 519, 24 411 / 532,
+// 32 553 / 460; 2 x 2000 tokens 20.7 / 24.2, 22.7 / 26.8, 24.6 / 26.9, 25.0 / 26.8.
+constexpr int kFewRows = 24;
+bool few_rows(const kvarn_config& c, int drafts) { return drafts * (c.n_q_heads / c.n_kv_heads) <= kFewRows; }
+
 // The workspace: header, unit map, rotated queries and their scales, partials.
 struct TreeSpace {
     size_t turned, scales, partials, bytes;
@@ -46,6 +59,11 @@ TreeSpace tree_space(const kvarn_config& c, int32_t batch, int32_t drafts) {
     t.scales = t.turned + units * pad * 2 * kD * sizeof(uint16_t);
     t.partials = align256(t.scales + units * pad * sizeof(float));
     t.bytes = ranges > 0 ? t.partials + (units + ranges) * 33 * pad * sizeof(float4) : 0;
+    if (few_rows(c, drafts)) {
+        const size_t few = t.partials + (size_t)batch * drafts * c.n_q_heads * prefill_splits(c, batch, drafts, current_device()) *
+                                            kPartialStride * sizeof(float);
+        t.bytes = t.bytes > 0 && few > t.bytes ? few : t.bytes;
+    }
     return t;
 }
 
@@ -116,7 +134,17 @@ int tree_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const voi
     a.ranges = plan.ranges;
     a.late = max_blocks > 0;
     cudaError_t e = cudaSuccess;
-    if (max_blocks > 0) e = PACKED ? launch_tree_packed(c, a, plan.wide, st) : launch_tree_bf16(a, plan.wide, st);
+    if (max_blocks > 0) {
+        if (!PACKED) {
+            e = launch_tree_bf16(a, plan.wide, st);
+        } else if (few_rows(c, drafts)) {
+            a.few = (int)prefill_splits(c, batch, drafts, current_device());
+            e = launch_prefill_all(c, q, q_dtype, pool, n_pool_blocks, a.block_bytes, block_table, max_blocks, seq_lens, batch, drafts,
+                                   (float*)a.partials, a.err, a.few, st);
+        } else {
+            e = launch_tree_packed(c, a, plan.wide, st);
+        }
+    }
     if (e == cudaSuccess) e = launch_tree_join<PACKED>(a, st);
     return e == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }

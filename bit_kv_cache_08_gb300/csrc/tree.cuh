@@ -17,7 +17,7 @@ struct TreeArgs {
     const int32_t* draft_lens;   // nullptr: drafts
     void* out;
     uint32_t* err;
-    float4* partials;            // see tree_partial
+    float4* partials;            // see tree_partial; of few rows, see few
     int32_t* unit_map;           // (first, last) range of each unit
     uint16_t* turned;            // packed cache: the rotated queries, two fp16 halves, and their scales
     float* turned_scale;
@@ -27,6 +27,7 @@ struct TreeArgs {
     int n_q, n_kv, G;
     int row_tiles, rows_pad;     // CTAs that share a unit's query rows; the rows, to a multiple of 32
     int ranges;                  // that the tiles of all units are cut into, at most
+    int few;                     // > 0: so many partials of each row from the prefill kernel, in its layout
     int late;                    // the join comes behind a kernel of this call
     float sm_scale;
     uint32_t flags;

@@ -277,19 +277,36 @@ __global__ void __launch_bounds__(tree_join_threads<WARPS>()) tree_join_kernel(T
     if (!PACKED) drafts();   // (they wait for nothing; O is in their space)
     wait_prior_grids();      // the cached tokens' kernel, beside which this one may have started
     if (!bad && tree_tokens<PACKED>(a, b) > 0) {
-        // (a range outside the grid, left by a CTA that gave up, is none)
-        const int2 um = __ldcg(reinterpret_cast<const int2*>(a.unit_map) + u);
-        const int first = um.x, last = um.x >= 0 && um.y >= um.x && um.y < a.ranges ? um.y : um.x - 1;
+        int first = 0, last = a.few - 1;
+        const float4* row_at[2];
+        int64_t slot_stride, quad_stride;
+        if (a.few > 0) {
+            slot_stride = (int64_t)a.G * 33;
+            quad_stride = 1;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int row = min(mine[x], rows - 1);
+                row_at[x] = a.partials + ((((int64_t)b * a.drafts + row / a.G) * a.n_kv + h) * a.few * a.G + row % a.G) * 33;
+            }
+        } else {
+            // (a range outside the grid, left by a CTA that gave up, is none)
+            const int2 um = __ldcg(reinterpret_cast<const int2*>(a.unit_map) + u);
+            first = um.x, last = um.x >= 0 && um.y >= um.x && um.y < a.ranges ? um.y : um.x - 1;
+            slot_stride = (int64_t)33 * a.rows_pad;
+            quad_stride = a.rows_pad;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) row_at[x] = tree_partial(a, u, 0, min(mine[x], a.rows_pad - 1));
+        }
         for (int i = first + part; i <= last; i += WARPS) {
             float4 y[2][2][4], ml[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const int row = min(mine[x], a.rows_pad - 1);
-                ml[x] = __ldcg(tree_partial(a, u + i, 0, row));
+                const float4* p = row_at[x] + i * slot_stride;
+                ml[x] = __ldcg(p);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) y[x][j][k] = __ldcg(tree_partial(a, u + i, 1 + 16 * j + 4 * tq + k, row));
+                    for (int k = 0; k < 4; ++k) y[x][j][k] = __ldcg(p + (1 + 16 * j + 4 * tq + k) * quad_stride);
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {

@@ -64,13 +64,15 @@ __global__ void __launch_bounds__(256) tree_rotate_kernel(TreeArgs a) {
 // with its largest level within 2040 u:
 //   Sh, Zh  multiples of u: every level code Sh + Zh is one of up to 2047 u, exact in fp16
 //   Sl, Zl  the rests, up to u / 2: a level's rest code Sl + Zl is up to 2 u (2 bits), 4 u (3), 8 u (4)
-// The 8 builder warps then need fp16 arithmetic only, on pairs:
+// The builder warps then need fp16 arithmetic only, on pairs:
 //   Lh = code Sh + Zh (exact), Ll = code Sl + Zl (within 2^-9 u at 4 bits),
 //   hi = RN(Lh C), lo = RN(RN(Lh C - hi) + Ll C)  (Lh C - hi is exact)
 // so that hi + lo is within 2^-18 of the (token, group)'s largest level times C (2^-20 at 2
 // bits), plus 2^-22 of itself. In fp32 (a mixed multiply-add, two products and a split into halves
-// by conversions, as the shared prefix builds) a pair cost half as many instructions again, several of
-// them at lower rates: XXX.
+// by conversions, as the shared prefix builds) a pair costs half as many instructions again, several of
+// them at lower rates. That alone gained nothing while the builders waited for their raw
+// tiles (48 x 16 drafts over 8192 4-bit tokens: 448 us with either); with rings of raw
+// tiles and 4 warps each for keys and values it is 390.
 constexpr int kTopLevel = 6, kTopChannel = 9;
 constexpr float kCodeUp = 512.f;      // (codes come as code 2^-9)
 constexpr int kRest = 4 * kPkTok * 2; // bytes of one plane of rests: [block][4][B] fp16

@@ -268,3 +268,29 @@ def test_no_table_at_all(kvlib):
         assert c.table.shape[1] == 0
         d = Drafts(c, 11)
         _check(c, d, _call(c, d))
+
+
+@pytest.mark.parametrize("bits,B", [(0, 32), (2, 32), (3, 64), (4, 64)])
+@pytest.mark.parametrize("T,n_q", [(1, 4), (5, 4), (6, 4), (7, 4), (8, 3), (9, 3), (13, 2), (23, 1), (24, 1), (25, 1)])
+def test_few_rows(kvlib, bits, B, T, n_q):
+    """Around 24 query rows a (sequence, kv head), where the packed cache's kernels change, with lengths of every kind."""
+    c = Cache(kvlib, 41, [1030, 31, 0, B, 700], n_q, 1, B, bits, wild=T % 2 == 0)
+    for q_dtype in (torch.float32, torch.bfloat16):
+        d = Drafts(c, T, seed=T, lens=[T, T, T // 2, T, max(1, T - 1)], q_dtype=q_dtype)
+        _check(c, d, _call(c, d))
+
+
+@pytest.mark.parametrize("bits", [2, 4])
+def test_few_rows_that_are_not_finite(kvlib, bits):
+    c = Cache(kvlib, 42, [500, 33, 64], 8, 2, 32, bits)
+    clean = Drafts(c, 5, lens=[5, 5, 3])
+    want = _call(c, clean)
+    d = Drafts(c, 5, lens=[5, 5, 3])
+    d.q[2, 3:] = float("nan")
+    d.q[0, 2, 3, 7] = float("nan")
+    d.q[1, 1, 6, 7] = float("inf")
+    out = _call(c, d)
+    same = torch.ones(3, 5, 8, dtype=torch.bool, device="cuda")
+    same[0, 2, 3] = same[1, 1, 6] = False
+    assert torch.isnan(out[0, 2, 3]).all() and torch.isnan(out[1, 1, 6]).all()
+    assert torch.equal(out[same], want[same])
