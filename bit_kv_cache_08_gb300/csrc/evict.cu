@@ -22,7 +22,6 @@ struct EvictArgs {
     uint32_t* err;
     int64_t n_pool_blocks, block_bytes, stride, new_stride, units;
     int n_kv, B, max_blocks, new_max_blocks;
-    int unit;              // tokens of a place: 1 or B
     int budget, recent;    // in places
     int64_t head_bytes;    // of a kv head's K and V in a block
 };
@@ -30,9 +29,13 @@ struct EvictArgs {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kDigit = 2048;             // values of an 11-bit digit
+constexpr int kBins = kDigit / kSelThreads;
+constexpr int kSelKeys = 9728;           // keys held in shared memory (48 KB with the rest: 4 CTAs an SM)
 
 // A weight as a key: its bits order as it does; what is not above 0 counts as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) { return w > 0.f ? __float_as_uint(w) : 0u; }
+
+__device__ __forceinline__ float tidy(float w) { return w > 0.f ? w : 0.f; }
 
 // (hi, lo) += w, exactly but for the last bits of lo: hi + lo keeps about 48
 // bits, so that its rounding to 32 is that of the sum in 64 bits.
@@ -42,155 +45,247 @@ __device__ __forceinline__ void add_pair(float& hi, float& lo, float w) {
     hi = s;
 }
 
-__device__ __forceinline__ float tidy(float w) { return w > 0.f ? w : 0.f; }
-
-// The key of place i of a row of weights.
-__device__ __forceinline__ uint32_t place_key(const float* w, int i, int unit) {
-    if (unit == 1) return weight_key(w[i]);
-    float hi = 0.f, lo = 0.f;
-    const float4* x = reinterpret_cast<const float4*>(w + (int64_t)i * unit);
-    for (int k = 0; k < unit / 4; ++k) {
-        const float4 v = x[k];
-        add_pair(hi, lo, tidy(v.x));
-        add_pair(hi, lo, tidy(v.y));
-        add_pair(hi, lo, tidy(v.z));
-        add_pair(hi, lo, tidy(v.w));
+// The key of place i0 + lane of a row of weights with n places (0 behind them). Of a
+// place of 32 or 64 tokens 8 lanes add up a part each, 16 bytes a load, 4 places a warp at once.
+template <int UNIT>
+__device__ __forceinline__ uint32_t place_key(const float* w, uint32_t i0, uint32_t n, int lane) {
+    if constexpr (UNIT == 1) return i0 + lane < n ? weight_key(w[i0 + lane]) : 0u;
+    constexpr int kParts = UNIT >= 32 ? UNIT / 32 : 1, kBatch = 4;
+    uint32_t key = 0;
+#pragma unroll
+    for (int s0 = 0; s0 < 8; s0 += kBatch) {
+        float4 v[kBatch][kParts];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                const uint32_t i = i0 + 4 * (s0 + k) + (lane >> 3);
+                v[k][p] = i < n ? __ldg(reinterpret_cast<const float4*>(w + (int64_t)i * UNIT + 4 * (lane & 7) + 32 * p))
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            float hi = 0.f, lo = 0.f;
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                add_pair(hi, lo, tidy(v[k][p].x));
+                add_pair(hi, lo, tidy(v[k][p].y));
+                add_pair(hi, lo, tidy(v[k][p].z));
+                add_pair(hi, lo, tidy(v[k][p].w));
+            }
+#pragma unroll
+            for (int m = 1; m < 8; m <<= 1) {   // (both lanes of a pair add the same two in the same order)
+                const float oh = __shfl_xor_sync(kFull, hi, m), ol = __shfl_xor_sync(kFull, lo, m);
+                const float mh = hi;
+                const bool upper = lane & m;
+                hi = upper ? oh : mh;
+                lo += ol;
+                add_pair(hi, lo, upper ? mh : oh);
+            }
+            const uint32_t mine = weight_key(isinf(hi) ? hi : hi + lo);
+            const uint32_t its = __shfl_sync(kFull, mine, 8 * (lane & 3));
+            if (lane >> 2 == s0 + k) key = its;
+        }
     }
-    return weight_key(isinf(hi) ? hi : hi + lo);
+    return key;
 }
 
+template <int UNIT>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
     wait_prior_grids();
-    __shared__ uint32_t hist[kDigit];
+    let_next_grid_start();               // the copies
+    __shared__ uint32_t hist[kDigit], keys[kSelKeys];
     __shared__ int2 sums[kSelWarps];
-    __shared__ int found_digit, found_above;
+    __shared__ int found_digit, found_above, found_count;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < kDigit; i += kSelThreads) hist[i] = 0;   // (and so each pass leaves them)
     for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
         const int b = (int)(u / a.n_kv), h = (int)(u % a.n_kv);
         const int L = a.lens[b];
         int32_t* kept = a.kept + u * a.budget;
         const bool bad = L < 0 || (int64_t)L > (int64_t)a.max_blocks * a.B;
-        const int have = bad ? 0 : L / a.unit, size = min(have, a.budget);
+        const int have = bad ? 0 : L / UNIT, size = min(have, a.budget);
         if (h == 0 && tid == 0) {
             if (bad) raise_error(a.err, KVARN_DEVERR_POSITION);
-            a.new_lens[b] = bad ? 0 : size * a.unit + L % a.unit;
+            a.new_lens[b] = bad ? 0 : size * UNIT + L % UNIT;
         }
         const int fill = have > a.budget ? a.budget - a.recent : 0;   // to be chosen among the first n
-        const int n = have > a.budget ? have - a.recent : 0;
+        const uint32_t n = have > a.budget ? have - a.recent : 0;
         for (int i = tid; i < a.budget - fill; i += kSelThreads) {
             const int at = fill + i;
-            kept[at] = at < size ? (have > a.budget ? n + i : at) : -1;
+            kept[at] = at < size ? (have > a.budget ? (int)n + i : at) : -1;
         }
         if (fill == 0) continue;
         const float* w = a.weights + u * a.stride;
-        // T: the key of the fill-th greatest, digit by digit
+        __syncthreads();                  // (the unit before has read its keys)
+        // T: the key of the fill-th greatest, digit by digit. Keys that shared memory does
+        // not hold are made again from the weights (L2) in each pass.
+        const bool held = n <= kSelKeys;
         uint32_t T = 0;
         int need = fill;                  // of the places whose upper digits are T's
         for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
-            for (int i = tid; i < kDigit; i += kSelThreads) hist[i] = 0;
-            __syncthreads();
-            for (int i = tid; i < n; i += kSelThreads) {
-                const uint32_t key = place_key(w, i, a.unit);
-                const int up = shift + width;
-                if (pass == 0 || key >> up == T >> up) atomicAdd(&hist[key >> shift & (1u << width) - 1], 1u);
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11, up = shift + width;
+            if (pass == 0 || !held) {
+                constexpr int kBatch = UNIT == 1 ? 8 : 1;
+                for (uint32_t i0 = 32 * warp; i0 < n; i0 += kSelThreads * kBatch) {
+                    uint32_t key[kBatch];
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) key[k] = place_key<UNIT>(w, i0 + kSelThreads * k, n, lane);
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const uint32_t i = i0 + kSelThreads * k + lane;
+                        if (i >= n) continue;
+                        if (held) keys[i] = key[k];
+                        if (pass == 0 || key[k] >> up == T >> up) atomicAdd(&hist[key[k] >> shift & (1u << width) - 1], 1u);
+                    }
+                }
+            } else {
+                for (uint32_t i = tid; i < n; i += kSelThreads)
+                    if (keys[i] >> up == T >> up) atomicAdd(&hist[keys[i] >> shift & (1u << width) - 1], 1u);
             }
             __syncthreads();
-            if (warp == 0) {              // the digit at which the count from the top reaches need
-                int above = 0;
-                for (int d0 = kDigit - 32; d0 >= 0; d0 -= 32) {
-                    const int c = hist[d0 + 31 - lane];   // lane 0: the greatest digit
-                    int inc = c;
-                    for (int m = 1; m < 32; m <<= 1) {
-                        const int o = __shfl_up_sync(kFull, inc, m);
-                        if (lane >= m) inc += o;
+            // the digit at which the count from the top reaches need; thread t has digits
+            // kDigit - 1 - kBins t and those below
+            int c[kBins], mine = 0;
+#pragma unroll
+            for (int k = 0; k < kBins; ++k) {
+                uint32_t& bin = hist[kDigit - 1 - kBins * tid - k];
+                mine += c[k] = (int)bin;
+                bin = 0;
+            }
+            int inc = mine;
+            for (int m = 1; m < 32; m <<= 1) {
+                const int o = __shfl_up_sync(kFull, inc, m);
+                if (lane >= m) inc += o;
+            }
+            if (lane == 31) sums[warp].x = inc;
+            __syncthreads();
+            int before = lane < kSelWarps ? sums[lane].x : 0;
+            before = __reduce_add_sync(kFull, lane < warp ? before : 0);
+            int above = before + inc - mine;
+            if (above < need && above + mine >= need) {
+#pragma unroll
+                for (int k = 0; k < kBins; ++k) {
+                    if (above < need && above + c[k] >= need) {
+                        found_digit = kDigit - 1 - kBins * tid - k;
+                        found_above = above;
+                        found_count = c[k];
                     }
-                    const uint32_t hit = __ballot_sync(kFull, above + inc >= need);
-                    if (hit) {
-                        const int first = __ffs(hit) - 1;
-                        if (lane == first) {
-                            found_digit = d0 + 31 - lane;
-                            found_above = above + inc - c;
-                        }
-                        break;
-                    }
-                    above += __shfl_sync(kFull, inc, 31);
+                    above += c[k];
                 }
             }
             __syncthreads();
             T |= (uint32_t)found_digit << shift;
             need -= found_above;
-            __syncthreads();
-        }
-        // what is above T, and the first `need` that equal it, in order
-        int2 base = make_int2(0, 0);      // (above, equal) so far
-        for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-            const int i = i0 + tid;
-            const uint32_t key = i < n ? place_key(w, i, a.unit) : 0u;
-            const bool above = i < n && key > T, equal = i < n && key == T;
-            const uint32_t ba = __ballot_sync(kFull, above), be = __ballot_sync(kFull, equal);
-            if (lane == 0) sums[warp] = make_int2(__popc(ba), __popc(be));
-            __syncthreads();
-            int2 mine = base;
-            for (int k = 0; k < kSelWarps; ++k) {
-                const int2 s = sums[k];
-                if (k < warp) mine = make_int2(mine.x + s.x, mine.y + s.y);
-                base = make_int2(base.x + s.x, base.y + s.y);
+            if (need == found_count) {    // all places of T's digits so far are kept: those of T and above
+                --T;                      // (T > 0: some place is not kept)
+                need = 0;
+                break;
             }
-            const uint32_t below = (1u << lane) - 1;
-            mine.x += __popc(ba & below);
-            mine.y += __popc(be & below);
-            if (above || (equal && mine.y < need)) kept[mine.x + min(mine.y, need)] = i;
-            __syncthreads();
+            // (the next write of found_* and sums is two barriers away)
+        }
+        // what is above T, and the first `need` that equal it, in order: a warp takes
+        // places next to one another, counts, and then writes
+        const uint32_t run = ((n - 1) / (32 * kSelWarps) + 1) * 32, beg = min(n, warp * run), end = min(n, beg + run);
+        auto key_of = [&](uint32_t i0) { return !held ? place_key<UNIT>(w, i0, end, lane) : i0 + lane < end ? keys[i0 + lane] : 0u; };
+        int2 mine = make_int2(0, 0);      // (above, equal)
+        for (uint32_t i0 = beg; i0 < end; i0 += 32) {
+            const uint32_t key = key_of(i0);
+            mine.x += i0 + lane < end && key > T;
+            mine.y += i0 + lane < end && key == T;
+        }
+        mine.x = __reduce_add_sync(kFull, mine.x);
+        mine.y = __reduce_add_sync(kFull, mine.y);
+        if (lane == 0) sums[warp] = mine;
+        __syncthreads();
+        const int2 s = lane < warp ? sums[lane] : make_int2(0, 0);
+        mine.x = __reduce_add_sync(kFull, s.x);
+        mine.y = __reduce_add_sync(kFull, s.y);
+        for (uint32_t i0 = beg; i0 < end; i0 += 32) {
+            const uint32_t i = i0 + lane, key = key_of(i0);
+            const bool above = i < end && key > T, equal = i < end && key == T;
+            const uint32_t ba = __ballot_sync(kFull, above), be = __ballot_sync(kFull, equal), below = (1u << lane) - 1;
+            const int x = mine.x + __popc(ba & below), y = mine.y + __popc(be & below);
+            if (above || (equal && y < need)) kept[x + min(y, need)] = i;
+            mine.x += __popc(ba);
+            mine.y += __popc(be);
         }
     }
 }
 
-// Places one after the other, 16 bytes a thread; then the weights of the new columns.
-constexpr int kCopyThreads = 256, kCopyPlaces = 64;
-__global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(EvictArgs a) {
+// A warp takes kRowsPerWarp tokens (a K and a V row of 256 bytes each, 16 bytes a
+// lane), or one block's head, with as many loads in flight, and its weights' new columns.
+constexpr int kCopyWarps = 4, kRowsPerWarp = 8;
+template <bool PACKED>
+__global__ void __launch_bounds__(32 * kCopyWarps) evict_copy_kernel(EvictArgs a) {
     wait_prior_grids();
-    const int tid = threadIdx.x;
-    const int i0 = blockIdx.x * (kCopyPlaces / a.unit), per = kCopyPlaces / a.unit;   // places of this CTA
+    constexpr int kPlaces = PACKED ? 1 : kRowsPerWarp;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, unit = PACKED ? a.B : 1;
+    const int64_t columns = (int64_t)a.new_max_blocks * a.B;
+    const int64_t i0 = ((int64_t)blockIdx.x * kCopyWarps + warp) * kPlaces;
+    if (i0 * unit >= columns) return;
     for (int64_t u = blockIdx.y; u < a.units; u += gridDim.y) {
         const int b = (int)(u / a.n_kv), h = (int)(u % a.n_kv);
         const int L = a.lens[b];
         const bool bad = L < 0 || (int64_t)L > (int64_t)a.max_blocks * a.B;
-        const int have = bad ? 0 : L / a.unit, size = min(have, a.budget), tail = bad ? 0 : L % a.unit;
-        const int32_t* kept = a.kept + u * a.budget;
-        const int32_t* table = a.table + (int64_t)b * a.max_blocks;
-        const int32_t* to = a.new_table + (int64_t)b * a.new_max_blocks;
-        // 16-byte pieces: of a token's K and V row (2 x 16), or of a block's head
-        const int pieces = a.unit == 1 ? 32 : (int)(a.head_bytes / 16);
-        for (int x = tid; x < per * pieces; x += kCopyThreads) {
-            const int i = i0 + x / pieces, p = x % pieces;
-            if (i >= size) break;
-            const int at = kept[i];
-            const int64_t from_page = table[a.unit == 1 ? at / a.B : at], to_page = to[a.unit == 1 ? i / a.B : i];
-            if (from_page < 0 || from_page >= a.n_pool_blocks || to_page < 0 || to_page >= a.n_pool_blocks) {
-                raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
-                continue;
+        const int have = bad ? 0 : L / unit, size = min(have, a.budget), tail = bad ? 0 : L % unit;
+        const float* w = a.weights + u * a.stride;
+        float* new_w = a.new_weights + u * a.new_stride;
+        // lane x: place i0 + x (packed: i0)
+        const int64_t i = i0 + (PACKED ? 0 : lane);
+        int64_t src = -1, dst = 0;
+        int at = -1;
+        if (lane < kPlaces || PACKED) {
+            if (i < size) {
+                at = a.kept[u * a.budget + i];
+                const int64_t from_page = a.table[(int64_t)b * a.max_blocks + (PACKED ? at : at / a.B)];
+                const int64_t to_page = a.new_table[(int64_t)b * a.new_max_blocks + (PACKED ? i : i / a.B)];
+                if (from_page < 0 || from_page >= a.n_pool_blocks || to_page < 0 || to_page >= a.n_pool_blocks) {
+                    if (lane < kPlaces) raise_error(a.err, KVARN_DEVERR_BLOCK_ID);
+                } else {
+                    src = from_page * a.block_bytes + h * a.head_bytes + (PACKED ? 0 : (int64_t)(at % a.B) * kD * 2);
+                    dst = to_page * a.block_bytes + h * a.head_bytes + (PACKED ? 0 : (int64_t)(i % a.B) * kD * 2);
+                }
             }
-            int64_t src = from_page * a.block_bytes + h * a.head_bytes, dst = to_page * a.block_bytes + h * a.head_bytes;
-            if (a.unit == 1) {
-                const int64_t kind = (int64_t)(p >> 4) * a.B * kD * 2 + 16 * (p & 15);
-                src += kind + (int64_t)(at % a.B) * kD * 2;
-                dst += kind + (int64_t)(i % a.B) * kD * 2;
-            } else {
-                src += 16 * p;
-                dst += 16 * p;
-            }
-            *reinterpret_cast<uint4*>(a.pool + dst) = *reinterpret_cast<const uint4*>(a.pool + src);
         }
-        const int64_t columns = (int64_t)a.new_max_blocks * a.B;
-        const int64_t c = (int64_t)blockIdx.x * kCopyPlaces + tid;
-        if (tid < kCopyPlaces && c < columns) {
-            const float* w = a.weights + u * a.stride;
-            const int64_t kept_tokens = (int64_t)size * a.unit;
-            float v = 0.f;
-            if (c < kept_tokens) v = w[(int64_t)kept[c / a.unit] * a.unit + c % a.unit];
-            else if (c < kept_tokens + tail) v = w[(int64_t)have * a.unit + c - kept_tokens];
-            a.new_weights[u * a.new_stride + c] = v;
+        if constexpr (PACKED) {
+            for (int x = lane; x < a.B; x += 32) {
+                const int64_t c = i * a.B + x, kept_tokens = (int64_t)size * a.B;
+                float v = 0.f;
+                if (at >= 0) v = w[(int64_t)at * a.B + x];
+                else if (c < kept_tokens + tail) v = w[(int64_t)have * a.B + c - kept_tokens];
+                new_w[c] = v;
+            }
+            if (src >= 0) {
+                const uint4* from = reinterpret_cast<const uint4*>(a.pool + src);
+                uint4* to = reinterpret_cast<uint4*>(a.pool + dst);
+                const int pieces = (int)(a.head_bytes / 16);
+                constexpr int kBatch = 8;
+                for (int p0 = lane; p0 < pieces; p0 += 32 * kBatch) {
+                    uint4 v[kBatch];
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k)
+                        if (p0 + 32 * k < pieces) v[k] = __ldcs(from + p0 + 32 * k);
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k)
+                        if (p0 + 32 * k < pieces) to[p0 + 32 * k] = v[k];
+                }
+            }
+        } else {
+            if (lane < kPlaces && i < columns) new_w[i] = at >= 0 ? w[at] : 0.f;
+            const int64_t piece = (int64_t)(lane >> 4) * a.B * kD * 2 + 16 * (lane & 15);
+            uint4 v[kPlaces];
+            int64_t from[kPlaces];
+#pragma unroll
+            for (int k = 0; k < kPlaces; ++k) {
+                from[k] = __shfl_sync(kFull, src, k);
+                if (from[k] >= 0) v[k] = __ldcs(reinterpret_cast<const uint4*>(a.pool + from[k] + piece));
+            }
+#pragma unroll
+            for (int k = 0; k < kPlaces; ++k) {
+                const int64_t to = __shfl_sync(kFull, dst, k);
+                if (from[k] >= 0) *reinterpret_cast<uint4*>(a.pool + to + piece) = v[k];
+            }
         }
     }
 }
@@ -242,14 +337,15 @@ int evict(const kvarn_config* cfg, void* pool, int64_t n_pool_blocks, const int3
     a.B = B;
     a.max_blocks = max_blocks;
     a.new_max_blocks = new_max_blocks;
-    a.unit = PACKED ? B : 1;
-    a.budget = budget / a.unit;
-    a.recent = recent / a.unit;
+    a.budget = PACKED ? budget / B : budget;
+    a.recent = PACKED ? recent / B : recent;
     const cudaStream_t st = (cudaStream_t)stream;
     const unsigned units = (unsigned)(a.units < 65535 ? a.units : 65535);
-    cudaError_t e = launch_pdl(evict_select_kernel, units, kSelThreads, 0, st, a);
+    const auto select = !PACKED ? evict_select_kernel<1> : B == 32 ? evict_select_kernel<32> : evict_select_kernel<64>;
+    cudaError_t e = launch_pdl(select, units, kSelThreads, 0, st, a);
+    const int per = PACKED ? kCopyWarps * B : kCopyWarps * kRowsPerWarp;   // new columns of a CTA
     if (e == cudaSuccess)
-        e = launch_pdl(evict_copy_kernel, dim3((unsigned)((new_columns + kCopyPlaces - 1) / kCopyPlaces), units), kCopyThreads, 0, st, a);
+        e = launch_pdl(evict_copy_kernel<PACKED>, dim3((unsigned)((new_columns + per - 1) / per), units), 32 * kCopyWarps, 0, st, a);
     return e == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 

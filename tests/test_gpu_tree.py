@@ -294,3 +294,22 @@ def test_few_rows_that_are_not_finite(kvlib, bits):
     same[0, 2, 3] = same[1, 1, 6] = False
     assert torch.isnan(out[0, 2, 3]).all() and torch.isnan(out[1, 1, 6]).all()
     assert torch.equal(out[same], want[same])
+
+
+@pytest.mark.parametrize("bits,q_dtype", [(0, torch.bfloat16), (0, torch.float32), (2, torch.bfloat16)])
+@pytest.mark.parametrize("T", [10, 48])
+def test_wait_timeout_path(kvlib, bits, q_dtype, T):
+    """With the test switch the product warp of the cached tokens' kernel leaves at once: the other warps follow, the flag
+    is raised, and the workspace serves the next call."""
+    kv = kvlib
+    c = Cache(kv, 24, [900, 400, 64], 8, 2, 64, bits)
+    d = Drafts(c, T, q_dtype=q_dtype)
+    ws = kv.alloc_tree_workspace(c.cfg, 3, T, c.table.shape[1])
+    good = _call(c, d, ws=ws)
+    c.cfg.flags |= kv.FLAG_TEST_WAIT_TIMEOUT
+    for _ in range(3):
+        _call(c, d, ws=ws, check=False)
+        assert kv.read_error(ws) == kv.DEVERR_WAIT_TIMEOUT
+        kv.clear_error(ws)
+    c.cfg.flags &= ~kv.FLAG_TEST_WAIT_TIMEOUT
+    assert torch.equal(_call(c, d, ws=ws), good)
