@@ -532,6 +532,7 @@ __device__ __forceinline__ void merge_locate(const AttnArgs& a, int64_t gw, int 
 template <int B, bool ROT, bool WEIGHTS = false>
 __global__ void __launch_bounds__(128) merge_kernel(AttnArgs a) {
     wait_prior_grids();
+    if (WEIGHTS) let_next_grid_start();   // (it reads the scores meanwhile)
     const int lane = threadIdx.x & 31;
     const int64_t gw = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (gw >= (int64_t)a.batch * a.n_q) return;
@@ -555,6 +556,7 @@ constexpr int kWideWarps = 8;
 template <int B, bool ROT, int NB, bool WEIGHTS>
 __global__ void __launch_bounds__(32 * kWideWarps, NB == 8 ? 2 : 4) merge_wide_kernel(AttnArgs a) {
     wait_prior_grids();
+    if (WEIGHTS) let_next_grid_start();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int64_t gw = blockIdx.x;
     if (gw >= (int64_t)a.batch * a.n_q) return;   // (uniform over the CTA)

@@ -11,6 +11,8 @@
 #include "attn_common.cuh"
 #include "host_checks.h"
 
+#include <type_traits>
+
 namespace kvarn {
 
 AttnArgs decode_split_args(const kvarn_config& cfg, const void* q, int q_dtype, const void* pool, int64_t n_pool_blocks,
@@ -34,31 +36,39 @@ struct WeighArgs {
     float decay;
 };
 
-// A thread takes 4 tokens of one (sequence, kv head).
+// A thread takes 4 tokens of one (sequence, kv head). The kernel starts beside the
+// merge, and a thread of the first wave has its loads of scores and of `in` on their way
+// before it waits for the merge's (m, 1 / l). The merge's own scores, of the
+// packed cache's raw tail rows, are read behind the wait.
 constexpr int kWeighThreads = 256, kWeighTokens = 4 * kWeighThreads;
-template <int G>
+template <int G, int TAIL>
 __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(WeighArgs a) {
-    wait_prior_grids();
     const int t = blockIdx.x * kWeighTokens + 4 * threadIdx.x;
+    bool waited = false;
     for (int64_t u = blockIdx.y; u < a.units; u += gridDim.y) {
         const int L = a.seq_lens[u / a.n_kv];
-        if (t >= L || L > a.score_stride) continue;   // (a length out of range: flagged by the merge)
+        const bool mine = t < L && L <= a.score_stride;   // (a length out of range: flagged by the merge)
+        if (!waited && (!mine || (TAIL > 0 && t >= L - L % max(TAIL, 1)))) wait_prior_grids(), waited = true;
+        if (!mine) continue;
         float w[4] = {0.f, 0.f, 0.f, 0.f};
         if (a.in != nullptr) {
-            const float4 x = *reinterpret_cast<const float4*>(a.in + u * a.stride + t);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.in + u * a.stride + t));
             w[0] = a.decay * x.x;
             w[1] = a.decay * x.y;
             w[2] = a.decay * x.z;
             w[3] = a.decay * x.w;
         }
+        float4 s[G];
+#pragma unroll
+        for (int j = 0; j < G; ++j) s[j] = __ldcg(reinterpret_cast<const float4*>(a.scores + (u * G + j) * a.score_stride + t));
+        if (!waited) wait_prior_grids(), waited = true;
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-            const float4 s = __ldcs(reinterpret_cast<const float4*>(a.scores + (u * G + j) * a.score_stride + t));
-            const float2 st = a.stats[u * G + j];
-            w[0] = fmaf(exp2f(s.x - st.x), st.y, w[0]);
-            w[1] = fmaf(exp2f(s.y - st.x), st.y, w[1]);
-            w[2] = fmaf(exp2f(s.z - st.x), st.y, w[2]);
-            w[3] = fmaf(exp2f(s.w - st.x), st.y, w[3]);
+            const float2 st = __ldcg(a.stats + u * G + j);
+            w[0] = fmaf(exp2f(s[j].x - st.x), st.y, w[0]);
+            w[1] = fmaf(exp2f(s[j].y - st.x), st.y, w[1]);
+            w[2] = fmaf(exp2f(s[j].z - st.x), st.y, w[2]);
+            w[3] = fmaf(exp2f(s[j].w - st.x), st.y, w[3]);
         }
         float* dst = a.out + u * a.stride + t;
         if (t + 4 <= L) {
@@ -69,6 +79,7 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(WeighArgs a) {
                 if (t + k < L) dst[k] = w[k];
         }
     }
+    if (!waited) wait_prior_grids();
 }
 
 namespace {
@@ -135,12 +146,13 @@ int attn_weights(const kvarn_config* cfg, const void* q, int32_t q_dtype, const 
     w.n_kv = c.n_kv_heads;
     w.decay = decay;
     const dim3 grid((unsigned)((columns + kWeighTokens - 1) / kWeighTokens), (unsigned)(units < 65535 ? units : 65535));
-    switch (a.G) {
-        case 1: e = launch_pdl(weigh_kernel<1>, grid, kWeighThreads, 0, st, w); break;
-        case 2: e = launch_pdl(weigh_kernel<2>, grid, kWeighThreads, 0, st, w); break;
-        case 3: e = launch_pdl(weigh_kernel<3>, grid, kWeighThreads, 0, st, w); break;
-        default: e = launch_pdl(weigh_kernel<4>, grid, kWeighThreads, 0, st, w);
-    }
+    auto weigh = [&](auto tail) {
+        constexpr int TAIL = decltype(tail)::value;
+        return a.G == 1 ? weigh_kernel<1, TAIL> : a.G == 2 ? weigh_kernel<2, TAIL> : a.G == 3 ? weigh_kernel<3, TAIL> : weigh_kernel<4, TAIL>;
+    };
+    using std::integral_constant;
+    const auto fn = !PACKED ? weigh(integral_constant<int, 0>()) : c.block_size == 32 ? weigh(integral_constant<int, 32>()) : weigh(integral_constant<int, 64>());
+    e = launch_pdl(fn, grid, kWeighThreads, 0, st, w);
     return e == cudaSuccess ? KVARN_OK : KVARN_ERR_CUDA;
 }
 

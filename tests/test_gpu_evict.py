@@ -210,3 +210,8 @@ def test_faults_are_flagged(kvlib, bits):
     c.table[0] = c.n_pool
     _run(c, w, 160, 32, ws=ws, check=False)
     assert kv.read_error(ws) == kv.DEVERR_BLOCK_ID
+
+
+def test_more_blocks_than_shared_memory_holds(kvlib):
+    c = Cache(kvlib, 16, [330016, 64], 1, 1, 32, 2, spare=2 * 5001)
+    _check(c, _weights(c, 10, "ties"), 5000 * 32, 320)
