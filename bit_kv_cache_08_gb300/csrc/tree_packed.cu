@@ -172,8 +172,16 @@ __device__ __forceinline__ bool tree_keys(const uint8_t* hb, const uint8_t* rest
     uint32_t w[4], hw[4];              // token k's word with this group's fields at its low end
     const uint4* src = reinterpret_cast<const uint4*>(codes);
     if constexpr (BITS == 4) {         // word 4 k + g
+        // (records are 16 words apart, two banks for all lanes: in load j a lane takes k = j + lane / 2,
+        // 8 banks, and turns the words back in registers)
+        const int turn = lane >> 1 & 3;
+        uint32_t x[4], y[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = reinterpret_cast<const uint32_t*>(codes)[4 * k + g];
+        for (int j = 0; j < 4; ++j) x[j] = reinterpret_cast<const uint32_t*>(codes)[4 * (j + turn & 3) + g];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = turn & 1 ? x[k + 3 & 3] : x[k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = turn & 2 ? y[k + 2 & 3] : y[k];
     } else {                           // word 2 k + g / 2, fields 4 (g % 2) ..
         const uint4 u = src[0], v = src[1];
         w[0] = (g & 2 ? u.y : u.x) >> 8 * (g & 1);
@@ -265,9 +273,28 @@ struct TreePackedSmem {
     uint32_t tmem;
     int stop;
     // the exponents of the last tiles [K, V], and of their C: the warps that find them are at most kMaxRaw
-    // tiles ahead of the V' that is built, which is at most two ahead of the softmax
+    // tiles ahead of the operands that are built, and those at most three ahead of the softmax. The softmax of a
+    // tile follows the keys by way of S but nothing of its values, so that exps has the tile's
+    // number in its upper half, which the softmax waits for
     int exps[2][8], c_exps[2][8];
 };
+
+// A tile's number (its low 16 bits) and exponent; the exponent of tile g, waited for (the limit
+// run out: raises stop, with which the call's result is void).
+__device__ __forceinline__ int tile_exps(int g, int e) { return (int)((uint32_t)g << 16 | (uint32_t)e & 0xffffu); }
+__device__ __forceinline__ int exponent_of(const int* at, int g, int* stop) {
+    int x = *reinterpret_cast<const volatile int*>(at);
+    if (((uint32_t)x >> 16) != ((uint32_t)g & 0xffffu)) {   // (seldom: its tile is on its way two tiles ahead)
+#pragma unroll 1
+        for (uint32_t n = 0; ((uint32_t)x >> 16) != ((uint32_t)g & 0xffffu); ++n) {
+            if (n == kWaitLimit) *reinterpret_cast<volatile int*>(stop) = 1;
+            if (*reinterpret_cast<volatile int*>(stop)) break;
+            x = *reinterpret_cast<const volatile int*>(at);
+        }
+    }
+    __syncwarp();
+    return (int16_t)x;
+}
 
 template <int B, int BITS, int NT>
 struct TreePackedLayout {
@@ -314,6 +341,7 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
     const auto alive = [&](int x) { return min(4, max(1, (a.drafts * a.G - (rt * NT + x) * kPRows + 31) / 32)); };
     if (tid == 0) {
         s.stop = 0;
+        for (int i = 0; i < 8; ++i) s.exps[0][i] = s.exps[1][i] = -1;   // (no tile 65535 that is the first of its place)
         for (int i = 0; i < 2 * kRawStages; ++i) {
             mbar_init(&s.raw_full[i & 1][i >> 1], 1);
             mbar_init(&s.ready[i & 1][i >> 1], 1);
@@ -392,7 +420,7 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
             const int e = prepare_levels<B, BITS>(tile + x * Lay::HB, there, lane, tile + Lay::kTile, c_exp);
             fence_async_smem();                   // (before the stage's next copy writes over it)
             if (lane == 0) {
-                s.exps[kind][g & 7] = e;
+                *reinterpret_cast<volatile int*>(&s.exps[kind][g & 7]) = tile_exps(g, e);
                 s.c_exps[kind][g & 7] = c_exp;
             }
             warp_arrive(&s.ready[kind][st]);
@@ -534,9 +562,9 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
                     warp_arrive(&s.p_ready[w]);
                     continue;
                 }
-                const int e = *reinterpret_cast<volatile int*>(&s.exps[1][g & 7]);
+                const int e = exponent_of(&s.exps[1][g & 7], g, stop);
                 // (finite and not 0, so that what is masked stays masked)
-                const float here = fminf(fmaxf(scale * exp2i(*reinterpret_cast<volatile int*>(&s.exps[0][g & 7])), 0x1p-126f), 0x1p127f);
+                const float here = fminf(fmaxf(scale * exp2i((int16_t)*reinterpret_cast<volatile int*>(&s.exps[0][g & 7])), 0x1p-126f), 0x1p127f);
                 ok = softmax_rolled<TOK, true>(tm_s + 64 * w + lanes, my_o, len - (c.t + i) * TOK, here, (float)e, exp2i(-e),
                                                                kLift, i == 0, st, &s.p_ready[w], [&] {
                     // O is idle once the last product into it has completed: with two row
