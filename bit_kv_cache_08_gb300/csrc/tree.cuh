@@ -27,6 +27,7 @@ struct TreeArgs {
     int n_q, n_kv, G;
     int row_tiles, rows_pad;     // CTAs that share a unit's query rows; the rows, to a multiple of 32
     int ranges;                  // that the tiles of all units are cut into, at most
+    int extra;                   // rows 128 .. 135 of bf16 pages have two partials, kExtraRows apart
     int few;                     // > 0: so many partials of each row from the prefill kernel, in its layout
     int late;                    // the join comes behind a kernel of this call
     float sm_scale;
@@ -102,6 +103,9 @@ __device__ __forceinline__ void tree_next(const TreeArgs& a, TreeCursor& c) {
 }
 // Ranges in use.
 __device__ __forceinline__ int64_t tree_ranges(int64_t W, int ranges) { return W < ranges ? W : ranges; }
+
+// Rows beyond 128 that the bf16 kernel takes beside a row tile (tree_bf16.cu).
+constexpr int kExtraRows = 8;
 
 // Partials: [slot][33][rows_pad] of four floats, (m, l, -, -) and then four channels at a
 // time: a warp's 32 rows of four channels are one run of memory for the kernel that

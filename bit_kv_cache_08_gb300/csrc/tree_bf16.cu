@@ -5,7 +5,7 @@
 // that S = Q K^T, P = 2^(scale S - m) and O += P V are matrix products of R rows, and
 // the pages are read once for all drafts. A CTA takes a range of tiles of tokens
 // (tree.cuh), which may go on from one unit to the next, and leaves a partial (m, l, O) of each
-// unit. Two forms:
+// unit. Three forms:
 //   NT 1  up to 128 rows and 64-token tiles, two CTAs an SM. HBM bounds it: two CTAs cover
 //         each other's waits and ends of units. S of a tile runs under the softmax of the
 //         tile before (two S in tensor memory, one O).
@@ -14,6 +14,8 @@
 //         values in shared memory and take turns, one in its products while the other is
 //         in its softmax; products of 128 tokens read shared memory at the rate of the tensor core,
 //         those of 64 do not.
+//   extra NT 1, with up to 8 rows more on mma.sync by 4 warps of their own from the same tiles: a second
+//         row tile costs as many products for 4 rows (33 drafts) as for 128.
 // Per row tile:
 //   S (128 rows, fp32)  tensor memory
 //   softmax             128 threads, a row each; P as two bf16 halves over S, the A operand of
@@ -25,6 +27,7 @@
 //
 // Rounding: as in the shared prefix over bf16 pages (P two halves, 2^-16; an fp32
 // query two, one more product).
+#include "prefix_merge.cuh"
 #include "tree.cuh"
 
 #include <cuda.h>
@@ -43,21 +46,157 @@ struct TreeBf16Smem {
 constexpr int kTbHeader = 1024;
 static_assert(sizeof(TreeBf16Smem) <= kTbHeader, "header");
 
-template <bool Q32, int NT>
+template <bool Q32, int NT, bool EXTRA>
 struct TreeBf16Form {
     static_assert(!Q32 || NT == 1, "an fp32 query is two operands");
+    static_assert(!EXTRA || (!Q32 && NT == 1), "extra rows of bf16 queries beside one row tile");
+    static constexpr int kExtra = EXTRA ? 4 : 0;                // warps
     static constexpr int kTok = 64 * NT, kKv = kTok * kD * 2;   // tokens of a tile, bytes of its K or V: two 64-channel blocks
-    static constexpr int kSoft = 4 * NT, kThreads = 32 * (kSoft + 2);
+    static constexpr int kSoft = 4 * NT, kThreads = 32 * (kSoft + 2 + kExtra);
     static constexpr int kQ = (Q32 ? 2 : 1) * NT * kTbQ;
     static constexpr uint32_t kColumns = 256 * NT;              // of tensor memory: two S, and NT O
     static constexpr size_t kSmem = 1024 + kTbHeader + kQ + 4 * kKv;
 };
 
-template <int B, bool Q32, int NT>
-__global__ void __launch_bounds__(TreeBf16Form<Q32, NT>::kThreads, Q32 || NT == 2 ? 1 : 2) tree_bf16_kernel(const __grid_constant__ CUtensorMap map, TreeArgs a) {
+// The rows from 128 on (up to 8) of a range's units, on mma.sync by 4 warps from the tiles in shared memory:
+// warp e takes tokens 32 (e / 2) .. + 31 of a tile and, of O, channels 64 (e % 2) .. + 63. What each half of
+// the tokens gives is a partial of its own (the join adds them). The rows are the products' 8 columns:
+//   S' = K Q'    A = 16 tokens of K by ldmatrix, B = the rows' queries, in registers
+//   O' += V' P'  A = 16 channels of V by ldmatrix.trans, B = S' as two bf16 halves, transposed by movmatrix
+__device__ __forceinline__ void ldmatrix4(uint32_t at, uint32_t (&x)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t at, uint32_t (&x)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <int TOK>
+__device__ __forceinline__ void tree_extra_rows(const TreeArgs& a, TreeBf16Smem& s, TreeCursor c, const uint8_t* k_op, const uint8_t* v_op,
+                                                int64_t range, int total, int e, int lane, int* stop) {
+    static_assert(TOK == 64 && kExtraRows == 8, "two halves of 32 tokens, blocks of 64 channels with rows of 128 bytes");
+    constexpr int kKv = TOK * kD * 2;
+    const int gq = lane >> 2, tq = lane & 3, token0 = 32 * (e >> 1), block = e & 1;
+    const float scale = a.sm_scale * kLog2e;
+    int g = 0, cleaned = 0;
+    bool ok = true;
+    while (g < total && ok) {
+        const int n = min(c.tiles - c.t, total - g), rows = tree_rows(a, c.b) * a.G;
+        const bool cut = c.tokens % TOK != 0 && c.t + n == c.tiles;
+        uint32_t q[8][2];                                // B fragments of 16 channels: row gq
+        {
+            const int row = kPRows + gq;
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
+                                                                    (((int64_t)c.b * a.drafts + row / a.G) * a.n_q + c.h * a.G + row % a.G) * kD);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) q[k][i] = row < rows ? src[8 * k + 4 * i + tq] : 0u;
+        }
+        // of rows 2 tq + x: channels 16 j + gq (o[j][x]) and + 8 (o[j][2 + x])
+        float o[4][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        for (int i = 0; i < n && ok; ++i, ++g) {
+            const int st = g & 1, shown = c.tokens - (c.t + i) * TOK - token0;   // tokens of this half that there are
+            ok = warp_wait_or_stop(&s.k_full[st], (g >> 1) & 1, stop, kWaitLimit);
+            if (!ok) break;
+            float sc[2][4];                              // [16 tokens][token gq: rows 2 tq, 2 tq + 1; token gq + 8]
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {            // matrices: tokens 0, 8 of the first 8 channels, of the others
+                    uint32_t x[4];
+                    ldmatrix4(smem_addr(k_op + st * kKv + (k >> 2) * (kKv / 2) +
+                                        swizzled(token0 + 16 * t + 8 * (lane >> 3 & 1) + (lane & 7), 2 * (k & 3) + (lane >> 4))), x);
+                    mma_bf16(sc[t], x[0], x[1], x[2], x[3], q[k][0], q[k][1]);
+                }
+            }
+            warp_arrive(&s.k_empty[st]);
+            float f[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float& z = sc[t][2 * j + x];
+                        z = 16 * t + 8 * j + gq < shown ? z * scale : -INFINITY;
+                        top = fmaxf(top, z);
+                    }
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, k));
+                const bool grow = top - m[x] > 8.f;      // (from -inf at once; false where nothing is shown)
+                f[x] = grow && m[x] != -INFINITY ? ex2(m[x] - top) : 1.f;
+                if (grow) m[x] = top;
+                const float off = m[x] == -INFINITY ? 0.f : m[x];
+                float sum = 0.f;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) sum += sc[t][2 * j + x] = ex2(sc[t][2 * j + x] - off);
+                l[x] = l[x] * f[x] + sum;
+            }
+            if (__any_sync(kFull, f[0] != 1.f || f[1] != 1.f))
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    o[j][0] *= f[0];
+                    o[j][1] *= f[1];
+                    o[j][2] *= f[0];
+                    o[j][3] *= f[1];
+                }
+            uint32_t p[2][2][2];                         // [16 tokens][half][8 tokens]: row gq, tokens 2 tq, 2 tq + 1
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    split_pair<false>(sc[t][2 * j], sc[t][2 * j + 1], p[t][0][j], p[t][1][j]);
+                    p[t][0][j] = transposed(p[t][0][j]);
+                    p[t][1][j] = transposed(p[t][1][j]);
+                }
+            ok = warp_wait_or_stop(&s.v_full[st], (g >> 1) & 1, stop, kWaitLimit);
+            if (ok && cut && i == n - 1) ok = warp_wait_or_stop(&s.v_clean[st], cleaned >> st & 1, stop, kWaitLimit);
+            if (!ok) break;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {            // matrices: channels 0, 8 of the first 8 tokens, of the others
+                    uint32_t x[4];
+                    ldmatrix4_trans(smem_addr(v_op + st * kKv + block * (kKv / 2) +
+                                              swizzled(token0 + 16 * t + 8 * (lane >> 4) + (lane & 7), 2 * j + (lane >> 3 & 1))), x);
+                    mma_bf16(o[j], x[0], x[1], x[2], x[3], p[t][0][0], p[t][0][1]);
+                    mma_bf16(o[j], x[0], x[1], x[2], x[3], p[t][1][0], p[t][1][1]);
+                }
+            warp_arrive(&s.v_empty[st]);
+        }
+        if (!ok) break;
+        if (cut) cleaned ^= 1 << (g - 1 & 1);
+        const int64_t slot = (int64_t)c.b * a.n_kv + c.h + range;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) l[x] += __shfl_xor_sync(kFull, l[x], k);
+            if (kPRows + 2 * tq + x >= rows) continue;
+            const int row = kPRows + 2 * tq + x + kExtraRows * (e >> 1);
+            if (block == 0 && gq == 0) *tree_partial(a, slot, 0, row) = make_float4(m[x], l[x], 0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)                  // channels 64 block + 8 j + gq
+                reinterpret_cast<float*>(tree_partial(a, slot, 1 + 16 * block + 2 * j + (gq >> 2), row))[gq & 3] = o[j >> 1][2 * (j & 1) + x];
+        }
+        if (g < total) tree_next<TOK, false>(a, c);
+    }
+}
+
+template <int B, bool Q32, int NT, bool EXTRA>
+__global__ void __launch_bounds__(TreeBf16Form<Q32, NT, EXTRA>::kThreads, Q32 || NT == 2 ? 1 : 2) tree_bf16_kernel(const __grid_constant__ CUtensorMap map, TreeArgs a) {
     wait_prior_grids();
     let_next_grid_start();   // the join
-    using Form = TreeBf16Form<Q32, NT>;
+    using Form = TreeBf16Form<Q32, NT, EXTRA>;
     constexpr int TOK = Form::kTok, kKv = Form::kKv, kSoft = Form::kSoft;
     extern __shared__ uint8_t raw[];
     uint8_t* base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);   // the swizzle's period
@@ -80,9 +219,9 @@ __global__ void __launch_bounds__(TreeBf16Form<Q32, NT>::kThreads, Q32 || NT == 
         s.stop = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.k_full[i], 1);
-            mbar_init(&s.k_empty[i], 1);
+            mbar_init(&s.k_empty[i], 1 + Form::kExtra);
             mbar_init(&s.v_full[i], 1);
-            mbar_init(&s.v_empty[i], 1);
+            mbar_init(&s.v_empty[i], 1 + Form::kExtra);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_ready[i], 4);
             mbar_init(&s.v_clean[i], 1);
@@ -159,6 +298,9 @@ __global__ void __launch_bounds__(TreeBf16Form<Q32, NT>::kThreads, Q32 || NT == 
                 }
             }
         }
+    } else if (EXTRA && warp > kSoft + 1) {
+        // ---------------------------------------------------------- extra rows
+        if constexpr (EXTRA) tree_extra_rows<TOK>(a, s, c, k_op, v_op, range, total, warp - (kSoft + 2), lane, stop);
     } else if (warp == kSoft) {
         // ---------------------------------------------------------- products
         constexpr uint32_t kQk = mma_shape(kMmaBf16, TOK, false), kPv = mma_shape(kMmaBf16, kD, true);
@@ -277,7 +419,7 @@ __global__ void __launch_bounds__(TreeBf16Form<Q32, NT>::kThreads, Q32 || NT == 
                     warp_arrive(&s.p_ready[w]);
                     continue;
                 }
-                ok = softmax_tile<TOK, TOK, false>(tm_s + TOK * w + lanes, my_o, len - (c.t + i) * TOK, scale, 0.f, 1.f, 0.f, i == 0, st,
+                ok = softmax_tile<TOK, EXTRA ? 32 : TOK, false>(tm_s + TOK * w + lanes, my_o, len - (c.t + i) * TOK, scale, 0.f, 1.f, 0.f, i == 0, st,
                                                    &s.p_ready[w], [&] {
                     // O is idle once the last product into it has completed: with two row
                     // tiles S came behind it, with one it has freed tile g - 1's values
@@ -320,10 +462,10 @@ __global__ void __launch_bounds__(TreeBf16Form<Q32, NT>::kThreads, Q32 || NT == 
 // ---------------------------------------------------------------- host side
 namespace {
 
-template <int B, bool Q32, int NT>
+template <int B, bool Q32, int NT, bool EXTRA = false>
 cudaError_t launch_tree_bf16_as(const CUtensorMap& map, const TreeArgs& a, cudaStream_t st) {
-    using Form = TreeBf16Form<Q32, NT>;
-    const auto fn = tree_bf16_kernel<B, Q32, NT>;
+    using Form = TreeBf16Form<Q32, NT, EXTRA>;
+    const auto fn = tree_bf16_kernel<B, Q32, NT, EXTRA>;
     static bool ready[64];
     int d = 0;
     cudaError_t e = cudaGetDevice(&d);
@@ -340,6 +482,7 @@ template <int B>
 cudaError_t launch_tree_bf16_block(const CUtensorMap& map, const TreeArgs& a, bool wide, cudaStream_t st) {
     return a.q_dtype == KVARN_FP32 ? launch_tree_bf16_as<B, true, 1>(map, a, st)
            : wide                  ? launch_tree_bf16_as<B, false, 2>(map, a, st)
+           : a.extra               ? launch_tree_bf16_as<B, false, 1, true>(map, a, st)
                                    : launch_tree_bf16_as<B, false, 1>(map, a, st);
 }
 

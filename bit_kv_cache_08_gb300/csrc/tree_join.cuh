@@ -297,11 +297,12 @@ __global__ void __launch_bounds__(tree_join_threads<WARPS>()) tree_join_kernel(T
 #pragma unroll
             for (int x = 0; x < 2; ++x) row_at[x] = tree_partial(a, u, 0, min(mine[x], a.rows_pad - 1));
         }
-        for (int i = first + part; i <= last; i += WARPS) {
+        const int each = !PACKED && a.extra && row0 >= kPRows ? 2 : 1;
+        for (int i = part; i < (last - first + 1) * each; i += WARPS) {
             float4 y[2][2][4], ml[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const float4* p = row_at[x] + i * slot_stride;
+                const float4* p = row_at[x] + (first + i / each) * slot_stride + i % each * kExtraRows;
                 ml[x] = __ldcg(p);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)

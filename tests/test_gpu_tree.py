@@ -313,3 +313,49 @@ def test_wait_timeout_path(kvlib, bits, q_dtype, T):
         kv.clear_error(ws)
     c.cfg.flags &= ~kv.FLAG_TEST_WAIT_TIMEOUT
     assert torch.equal(_call(c, d, ws=ws), good)
+
+
+@pytest.mark.parametrize("B", [32, 64])
+@pytest.mark.parametrize("room", [False, True])
+@pytest.mark.parametrize("T,n_q", [(33, 4), (34, 4), (35, 4), (43, 3), (45, 3), (46, 3), (65, 2), (68, 2), (69, 2)])
+def test_rows_beyond_a_row_tile(kvlib, B, room, T, n_q):
+    """Up to 8 query rows a (sequence, kv head) more than the 128 of one row tile, and the first counts past that; lengths
+    that end anywhere in a tile, drafts that leave the rows beyond without a query, tables with room for long sequences and without."""
+    c = Cache(kvlib, 43, [1030, 31, 0, 64, 700, 97, 1], n_q, 1, B, 0, wild=T % 2 == 0)
+    if room:   # (columns behind the sequences are not read)
+        c.table = torch.cat([c.table, torch.full((7, 50000 // B), -1, dtype=torch.int32, device="cuda")], 1).contiguous()
+    for q_dtype in (torch.bfloat16, torch.float32):
+        d = Drafts(c, T, seed=T, lens=[T, T, T // 2, T, T - 1, T, T], q_dtype=q_dtype)
+        _check(c, d, _call(c, d))
+        _check(c, d, _call(c, d, torch.bfloat16))
+
+
+def test_wait_timeout_path_with_extra_rows(kvlib):
+    kv = kvlib
+    c = Cache(kv, 44, [900, 400, 64], 4, 1, 64, 0)
+    c.table = torch.cat([c.table, torch.full((3, 2000), -1, dtype=torch.int32, device="cuda")], 1).contiguous()
+    d = Drafts(c, 33)
+    ws = kv.alloc_tree_workspace(c.cfg, 3, 33, c.table.shape[1])
+    good = _call(c, d, ws=ws)
+    c.cfg.flags |= kv.FLAG_TEST_WAIT_TIMEOUT
+    for _ in range(3):
+        _call(c, d, ws=ws, check=False)
+        assert kv.read_error(ws) == kv.DEVERR_WAIT_TIMEOUT
+        kv.clear_error(ws)
+    c.cfg.flags &= ~kv.FLAG_TEST_WAIT_TIMEOUT
+    assert torch.equal(_call(c, d, ws=ws), good)
+
+
+def test_extra_rows_that_are_not_finite(kvlib):
+    c = Cache(kvlib, 45, [300, 33, 64], 4, 1, 32, 0)
+    c.table = torch.cat([c.table, torch.full((3, 4000), -1, dtype=torch.int32, device="cuda")], 1).contiguous()
+    d = Drafts(c, 33, parents="chain")
+    want = _call(c, d)
+    d.q[0, 32, 2, 7] = float("nan")
+    d.q[1, 32, 0, 9] = float("inf")
+    d.q[2, 0, 1, 0] = float("nan")
+    out = _call(c, d)
+    same = torch.ones(3, 33, 4, dtype=torch.bool, device="cuda")
+    same[0, 32, 2] = same[1, 32, 0] = same[2, 0, 1] = False
+    assert torch.isnan(out[~same]).all()
+    assert torch.equal(out[same], want[same])
