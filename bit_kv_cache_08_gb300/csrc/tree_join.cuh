@@ -14,7 +14,9 @@
 // P and an fp32 query enter as two bf16 halves (2^-16). The mask of a row is 16 bits of
 // its words a step; a step that no row of the warp sees is left out. Where there
 // are few rows, several warps share them: each takes its part of the partials and of the
-// steps, and their states are joined through shared memory.
+// steps, and their states are joined through shared memory. Its time is a chain of loads (13 us alone and cold
+// for 128 units of 64 rows, 24 for 256 of 132, of which a call sees about half); 16 or 24 warps an SM instead of
+// 8 spill and lose (32 x 33 drafts over 8192 tokens 192 -> 197, 205 us).
 #pragma once
 #include "prefix_merge.cuh"
 #include "tree.cuh"

@@ -472,7 +472,11 @@ size_t kvarn_tree_workspace_bytes(const kvarn_config* cfg, int32_t batch, int32_
  * over those; a row that sees nothing gives zeros, one with a score that is not a
  * number NaN. out: device [batch][drafts][n_q][128], out_dtype KVARN_BF16 or
  * KVARN_FP32. A drafted value that is not finite makes the rows that see it NaN,
- * and no other row. workspace: at least kvarn_tree_workspace_bytes(cfg, batch,
+ * and no other row. fp32 queries (of bf16 pages and raw rows) and softmax weights
+ * enter the products as two 16-bit halves, within 2^-16; over the packed cache
+ * rotated queries and weights within 2^-22 and, beyond 24 query rows a kv head, keys
+ * and values within 2^-18 (4 bits) to 2^-20 (2 bits) of the largest level of their token's
+ * 32 channels. workspace: at least kvarn_tree_workspace_bytes(cfg, batch,
  * drafts, max_blocks_per_seq) bytes, 16-byte aligned; calls that may overlap need one each. Device
  * faults: KVARN_DEVERR_BLOCK_ID, KVARN_DEVERR_POSITION (a length outside its
  * range: NaN rows), KVARN_DEVERR_WAIT_TIMEOUT.
