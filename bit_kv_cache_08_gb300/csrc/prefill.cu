@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(32) prefill_attn_kernel(AttnArgs a) {
 // ---------------------------------------------------------------- host side
 // Resident one-warp CTAs of the prefill kernel on `device` (cached per
 // device and configuration).
-static int prefill_grid_warps(int block_size, int bits, int device) {
+int prefill_grid_warps(int block_size, int bits, int device) {
     static int cache[2][3][64];
     const int bi = block_size == 32 ? 0 : 1, wi = bits - 2;
     if (device < 0 || device >= 64 || wi < 0 || wi > 2) return 0;

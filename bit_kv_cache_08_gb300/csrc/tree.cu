@@ -13,6 +13,7 @@ cudaError_t launch_prefill_all(const kvarn_config& cfg, const void* q, int q_dty
                                int64_t block_bytes, const int32_t* block_table, int max_blocks, const int32_t* seq_lens, int batch,
                                int chunk, float* partials, uint32_t* err, int splits, cudaStream_t st);
 int64_t prefill_splits(const kvarn_config& cfg, int64_t batch, int64_t chunk, int device);
+int prefill_grid_warps(int block_size, int bits, int device);
 cudaError_t launch_tree_packed(const kvarn_config& c, const TreeArgs& a, bool wide, cudaStream_t st);
 
 namespace {
@@ -42,20 +43,36 @@ TreePlan tree_plan(const kvarn_config& c, int drafts, bool packed, int q_dtype, 
     return p;
 }
 
-// Query rows of a unit up to which the prefill kernel takes the packed cache's
-// tokens: 8 rows a warp, each warp expanding the codes for itself on mma.sync, so
+// Whether the prefill kernel takes the packed cache's tokens: up to three of its warps a unit, 8 / G
+// drafts each, every warp expanding the codes for itself on mma.sync, so that
 // its time grows by the warp, where a 128-row tile of tcgen05 costs the same for
 // one row as for all. 64 sequences x 8192 2-bit tokens, 8 kv heads, prefill kernel
-// against tree_packed_kernel: 8 rows 181 / 510 us, 16 293 / 519, 24 411 / 532,
-// 32 553 / 460; 2 x 2000 tokens 20.7 / 24.2, 22.7 / 26.8, 24.6 / 26.9, 25.0 / 26.8.
-constexpr int kFewRows = 24;
-bool few_rows(const kvarn_config& c, int drafts) { return drafts * (c.n_q_heads / c.n_kv_heads) <= kFewRows; }
+// against tree_packed_kernel: a warp 181 / 510 us, two 293 / 519, three 411 / 532,
+// four 553 / 460; 2 x 2000 tokens 20.7 / 24.2, 22.7 / 26.8, 24.6 / 26.9, 25.0 / 26.8.
+constexpr int kFewWarps = 3;
+bool few_rows(const kvarn_config& c, int drafts) {
+    const int per = 8 / (c.n_q_heads / c.n_kv_heads);
+    return (drafts + per - 1) / per <= kFewWarps;
+}
+
+// Warps that share a unit's blocks there: as many as fill the GPU, two blocks each at least, 32 at
+// most (1 x 2 drafts over 16384 tokens: 16 35.1 us, 32 28.3, 64 27.7, 128 35.6; 1 x 6 37.1, 36.8,
+// 38.6, 40.4; 4 x 2 42.9, 39.3, 41.5, 42.1: the join reads a partial of each).
+constexpr int kFewSplits = 32;
+int few_splits(const kvarn_config& c, int64_t batch, int drafts, int max_blocks) {
+    const int device = current_device(), per = 8 / (c.n_q_heads / c.n_kv_heads);
+    const int64_t units = batch * c.n_kv_heads * ((drafts + per - 1) / per), warps = prefill_grid_warps(c.block_size, c.bits, device);
+    int64_t n = prefill_splits(c, batch, drafts, device);
+    if (units > 0 && 2 * units <= warps) n = warps / units;
+    n = n < max_blocks / 2 ? n : max_blocks / 2;
+    return (int)(n < 1 ? 1 : n < kFewSplits ? n : kFewSplits);
+}
 
 // The workspace: header, unit map, rotated queries and their scales, partials.
 struct TreeSpace {
     size_t turned, scales, partials, bytes;
 };
-TreeSpace tree_space(const kvarn_config& c, int32_t batch, int32_t drafts) {
+TreeSpace tree_space(const kvarn_config& c, int32_t batch, int32_t drafts, int32_t max_blocks) {
     TreeSpace t = {0, 0, 0, kWsHeader};
     if (batch == 0) return t;
     int ranges = 0, pad = 0;   // the most that either cache and query type and any length needs
@@ -70,7 +87,7 @@ TreeSpace tree_space(const kvarn_config& c, int32_t batch, int32_t drafts) {
     t.partials = align256(t.scales + units * pad * sizeof(float));
     t.bytes = ranges > 0 ? t.partials + (units + ranges) * 33 * pad * sizeof(float4) : 0;
     if (few_rows(c, drafts)) {
-        const size_t few = t.partials + (size_t)batch * drafts * c.n_q_heads * prefill_splits(c, batch, drafts, current_device()) *
+        const size_t few = t.partials + (size_t)batch * drafts * c.n_q_heads * few_splits(c, batch, drafts, max_blocks) *
                                             kPartialStride * sizeof(float);
         t.bytes = t.bytes > 0 && few > t.bytes ? few : t.bytes;
     }
@@ -99,7 +116,7 @@ int tree_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const voi
         return KVARN_ERR_INVALID_ARG;
     if (batch > 65535 || c.n_kv_heads > 65535) return KVARN_ERR_INVALID_ARG;
     if (!PACKED && n_pool_blocks > 0x7fffffff / ((int64_t)c.n_kv_heads * 2 * c.block_size)) return KVARN_ERR_INVALID_ARG;
-    const TreeSpace space = tree_space(c, batch, drafts);
+    const TreeSpace space = tree_space(c, batch, drafts, max_blocks);
     if (space.bytes == 0) return KVARN_ERR_CUDA;
     if (workspace_bytes < space.bytes) return KVARN_ERR_WORKSPACE;
     const cudaStream_t st = (cudaStream_t)stream;
@@ -149,7 +166,7 @@ int tree_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const voi
         if (!PACKED) {
             e = launch_tree_bf16(a, plan.wide, st);
         } else if (few_rows(c, drafts)) {
-            a.few = (int)prefill_splits(c, batch, drafts, current_device());
+            a.few = few_splits(c, batch, drafts, max_blocks);
             e = launch_prefill_all(c, q, q_dtype, pool, n_pool_blocks, a.block_bytes, block_table, max_blocks, seq_lens, batch, drafts,
                                    (float*)a.partials, a.err, a.few, st);
         } else {
@@ -172,7 +189,7 @@ size_t kvarn_tree_workspace_bytes(const kvarn_config* cfg, int32_t batch, int32_
     if (check_config(cfg, &c) != KVARN_OK || batch < 0 || drafts < 1 || drafts > KVARN_MAX_DRAFTS || max_blocks_per_seq < 0 ||
         (int64_t)batch * drafts > 0x7fffffff / c.n_q_heads || (int64_t)max_blocks_per_seq * c.block_size > 0x7fffffff)
         return 0;
-    return tree_space(c, batch, drafts).bytes;
+    return tree_space(c, batch, drafts, max_blocks_per_seq).bytes;
 }
 
 int kvarn_tree_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* pool, int64_t n_pool_blocks,

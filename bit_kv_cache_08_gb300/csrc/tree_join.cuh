@@ -301,6 +301,10 @@ __global__ void __launch_bounds__(tree_join_threads<WARPS>()) tree_join_kernel(T
         }
         const int each = !PACKED && a.extra && row0 >= kPRows ? 2 : 1;
         for (int i = part; i < (last - first + 1) * each; i += WARPS) {
+            if (PACKED && a.few > 0) {   // (a split without blocks)
+                const int n = L / a.B;
+                if ((int64_t)(i + 1) * n / a.few == (int64_t)i * n / a.few) continue;
+            }
             float4 y[2][2][4], ml[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {

@@ -474,7 +474,7 @@ size_t kvarn_tree_workspace_bytes(const kvarn_config* cfg, int32_t batch, int32_
  * KVARN_FP32. A drafted value that is not finite makes the rows that see it NaN,
  * and no other row. fp32 queries (of bf16 pages and raw rows) and softmax weights
  * enter the products as two 16-bit halves, within 2^-16; over the packed cache
- * rotated queries and weights within 2^-22 and, beyond 24 query rows a kv head, keys
+ * rotated queries and weights within 2^-22 and, with more than a few query rows, keys
  * and values within 2^-18 (4 bits) to 2^-20 (2 bits) of the largest level of their token's
  * 32 channels. workspace: at least kvarn_tree_workspace_bytes(cfg, batch,
  * drafts, max_blocks_per_seq) bytes, 16-byte aligned; calls that may overlap need one each. Device

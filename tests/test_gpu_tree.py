@@ -271,7 +271,7 @@ def test_no_table_at_all(kvlib):
 
 
 @pytest.mark.parametrize("bits,B", [(0, 32), (2, 32), (3, 64), (4, 64)])
-@pytest.mark.parametrize("T,n_q", [(1, 4), (5, 4), (6, 4), (7, 4), (8, 3), (9, 3), (13, 2), (23, 1), (24, 1), (25, 1)])
+@pytest.mark.parametrize("T,n_q", [(1, 4), (5, 4), (6, 4), (7, 4), (6, 3), (7, 3), (8, 3), (9, 3), (12, 2), (13, 2), (23, 1), (24, 1), (25, 1)])
 def test_few_rows(kvlib, bits, B, T, n_q):
     """Around 24 query rows a (sequence, kv head), where the packed cache's kernels change, with lengths of every kind."""
     c = Cache(kvlib, 41, [1030, 31, 0, B, 700], n_q, 1, B, bits, wild=T % 2 == 0)
@@ -359,3 +359,56 @@ def test_extra_rows_that_are_not_finite(kvlib):
     same[0, 32, 2] = same[1, 32, 0] = same[2, 0, 1] = False
     assert torch.isnan(out[~same]).all()
     assert torch.equal(out[same], want[same])
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4])
+@pytest.mark.parametrize("flags", [1, 6])
+def test_few_rows_with_ablation_flags(kvlib, bits, flags):
+    c = Cache(kvlib, 46, [150, 31], 8, 2, 32, bits, flags=flags)
+    d = Drafts(c, 3)
+    _check(c, d, _call(c, d))
+
+
+def test_faults_with_few_rows(kvlib):
+    kv = kvlib
+    c = Cache(kv, 47, [100, 60, 40], 8, 2, 32, 2)
+    d = Drafts(c, 4, lens=[4, 2, 4])
+    ws = kv.alloc_tree_workspace(c.cfg, 3, 4, c.table.shape[1])
+    good = _call(c, d, ws=ws)
+    for lens in ([100, -1, 40], [100, c.table.shape[1] * 32 + 1, 40]):
+        out = _call(c, d, ws=ws, lens=i32(lens), check=False)
+        assert kv.read_error(ws) == kv.DEVERR_POSITION
+        assert torch.isnan(out[1]).all() and torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+        kv.clear_error(ws)
+    d.lens = i32([4, 5, 4])
+    out = _call(c, d, ws=ws, check=False)
+    assert kv.read_error(ws) == kv.DEVERR_POSITION
+    assert torch.isnan(out[1]).all() and torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+    kv.clear_error(ws)
+    d.lens = i32([4, 2, 4])
+    c.table[1, 0] = -1
+    out = _call(c, d, ws=ws, check=False)
+    assert kv.read_error(ws) == kv.DEVERR_BLOCK_ID
+    assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+
+
+def test_empty_batch(kvlib):
+    kv = kvlib
+    c = Cache(kv, 48, [64], 8, 2, 32, 2)
+    pages = Cache(kv, 48, [64], 8, 2, 32, 0)
+    q = torch.empty(0, 3, 8, D, dtype=torch.bfloat16, device="cuda")
+    k = torch.empty(0, 3, 2, D, dtype=torch.bfloat16, device="cuda")
+    table, lens, mask = (torch.empty(s, dtype=torch.int32, device="cuda") for s in ((0, 2), (0,), (0, 3, 1)))
+    ws = kv.alloc_tree_workspace(c.cfg, 0, 3, 2)
+    kv.tree_attn(c.cfg, q, c.pool, c.staging, table, lens, k, k, mask, torch.empty_like(q), ws)
+    kv.tree_attn_bf16(pages.cfg, q, pages.pool, table, lens, k, k, mask, torch.empty_like(q), ws)
+    assert kv.read_error(ws) == 0
+
+
+@pytest.mark.parametrize("bits,B", [(2, 32), (4, 64)])
+def test_few_rows_over_long_and_short_sequences(kvlib, bits, B):
+    """More warps than a short sequence has blocks, and many blocks a warp."""
+    c = Cache(kvlib, 49, [9000, 70, B], 4, 1, B, bits)
+    for T in (1, 6):
+        d = Drafts(c, T, seed=T)
+        _check(c, d, _call(c, d))
