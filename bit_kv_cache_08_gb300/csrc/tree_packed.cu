@@ -35,6 +35,7 @@ constexpr uint32_t kQLow = 384;      // column of the queries' low halves (one r
 // multiplied with, 2^e, [unit][rows_pad].
 __global__ void __launch_bounds__(256) tree_rotate_kernel(TreeArgs a) {
     wait_prior_grids();
+    let_next_grid_start();   // the cached tokens' kernel, whose first operands need no query
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);   // of [batch][drafts][n_q]
     if (row >= (int64_t)a.batch * a.drafts * a.n_q) return;
@@ -321,7 +322,8 @@ struct TreePackedLayout {
 
 template <int B, int BITS, int NT>
 __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tree_packed_kernel(TreeArgs a) {
-    wait_prior_grids();
+    // (it starts beside tree_rotate_kernel, which has waited for what came before; the softmax warps
+    // wait for the turned queries, so that this grid ends behind that one)
     let_next_grid_start();   // the join
     using Lay = TreePackedLayout<B, BITS, NT>;
     constexpr int kSoft = Lay::kSoft, kRawStages = Lay::kRawStages, TOK = kPkTok;
@@ -338,7 +340,10 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
 
     TreeCursor c = {};
     const int64_t W = tree_locate<TOK, true>(a, -1, lane, c), n_ranges = tree_ranges(W, a.ranges);
-    if (range >= n_ranges) return;
+    if (range >= n_ranges) {
+        wait_prior_grids();
+        return;
+    }
     const int64_t x_beg = range * W / n_ranges;
     const int total = (int)((range + 1) * W / n_ranges - x_beg);   // tiles of this CTA
     tree_locate<TOK, true>(a, x_beg, lane, c);
@@ -515,6 +520,7 @@ __global__ void __launch_bounds__(TreePackedLayout<B, BITS, NT>::kThreads, 1) tr
         if (!mbar_wait_bounded(&s.drained, 0, kWaitLimit)) *stop = 1;
     } else {
         // ---------------------------------------------------------- softmax
+        wait_prior_grids();
         const int x = warp >> 2;                                  // row tile of the CTA
         const int r = rt * NT * kPRows + tid;                     // this thread's query row of a unit
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
