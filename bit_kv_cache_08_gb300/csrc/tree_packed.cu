@@ -14,7 +14,7 @@
 // tiles and prepares the levels of their keys, one for those of the values, 8 that build
 // operands, as in packed_build.cuh without meeting at a barrier.
 //
-// Measured (48 sequences x 16 drafts, up to 8192 4-bit tokens, 8 kv heads): 388 us a call, of which this
+// Measured (48 sequences x 16 drafts, up to 8192 4-bit tokens, 8 kv heads): 383 us a call, of which this
 // kernel is 365, 2380 cycles a tile of 64 tokens. The tensor core is busy 1480 of them (six products of halves),
 // a warp that builds 1500, shared memory about 2000 (operands written once, read three times); each waits for
 // the others in turn. Not faster: four S in tensor memory and products of P three steps behind, 8 + 8 builder
