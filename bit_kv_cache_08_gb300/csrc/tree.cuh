@@ -5,7 +5,6 @@
 
 namespace kvarn {
 
-
 struct TreeArgs {
     const void* q;               // [batch][drafts][n_q][128]
     const uint8_t* pool;

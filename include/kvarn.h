@@ -443,7 +443,7 @@ int kvarn_prefix_attn_bf16(const kvarn_config* cfg, const void* q, int32_t q_dty
                            const int32_t* seq_lens, int32_t batch, void* out, int32_t out_dtype, void* workspace,
                            size_t workspace_bytes, void* stream);
 
-/* Workspace bytes for kvarn_tree_attn / kvarn_tree_attn_bf16 with this batch
+/* Workspace bytes for kvarn_tree_attn / kvarn_tree_attn_bf16 with this batch,
  * number of drafts and table width on the CURRENT device. 0 on a bad config or
  * size. */
 size_t kvarn_tree_workspace_bytes(const kvarn_config* cfg, int32_t batch, int32_t drafts,
