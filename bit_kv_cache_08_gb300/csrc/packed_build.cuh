@@ -19,7 +19,7 @@ constexpr int kPkQ = kPRows * kD * 2;            // 128 query rows, fp16
 constexpr int kMaxRaw = 4;                       // stages of raw tiles, at most
 constexpr int kBuildWarps = 8;
 static_assert(kMaxRaw + 2 <= 8, "exponents in flight");
-constexpr float kLift = 7.f;                     // P up to 2^(8 + 7), small weights normal down to 2^-21
+constexpr float kLift = 7.f;                     // P up to 2^(8 + 7); weights normal down to 2^-21 of the reference's
 constexpr int kTopExp = 15;                      // K' and V' up to 2^15: halves of small values stay normal
 
 // Pair j of a record word as fp16 code 2^-9 (attn_common.cuh); for 3-bit

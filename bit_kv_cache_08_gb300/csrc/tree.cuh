@@ -116,10 +116,14 @@ __device__ __forceinline__ float4* tree_partial(const TreeArgs& a, int64_t slot,
 
 // softmax_tile (prefix.cuh) with S read from tensor memory twice, 32 columns at a time in
 // rolled loops: a fifth of its instructions in memory, for kernels whose warps' code together
-// does not fit the instruction caches. The reference is put kAhead above the largest score when it
-// moves, so that it moves the less often: a weight is then at most 2^(8 + lift), the largest
-// of the tile that moved it 2^(lift - kAhead).
-constexpr float kAhead = 4.f;
+// does not fit the instruction caches. The reference moves when a score passes it by 8 and is put kBelow
+// below the largest one: weights are at most 2^(8 + lift), and the row's largest is at least
+// 2^(lift + kBelow). With a lift of 7 that is 2^11 .. 2^15, and fp16 halves, whose steps end at 2^-24,
+// hold every weight within 2^-36 of the row's largest: an output of many small weights beside a large one
+// (a first token that takes most of the attention and has next to no value) is made of those. A
+// reference above the largest score moves less often (48 x 16 drafts over 8192 4-bit tokens 392 us a call
+// at 2^4 above, 397 at the score, 401 so, 407 at 2^6 below), but 2^4 above holds them within 2^-28 alone.
+constexpr float kBelow = 4.f;
 template <int TOK, bool HALF, typename Idle>
 __device__ __forceinline__ bool softmax_rolled(uint32_t my_s, uint32_t my_o, int shown, float scale, float bias, float unbias, float lift,
                                                bool first, RowState& st, uint64_t* p_ready, Idle&& o_idle) {
@@ -146,7 +150,7 @@ __device__ __forceinline__ bool softmax_rolled(uint32_t my_s, uint32_t my_o, int
     }
     const float top = fmaf(mx, scale, bias);
     const bool grow = top - st.m > 8.f;                    // (from -inf at once; false where nothing is shown)
-    const float ref = top + kAhead;
+    const float ref = top - kBelow;
     if (!first && __any_sync(kFull, grow)) {
         if (!o_idle()) return false;
         const float f = grow && st.m != -INFINITY ? ex2(st.m - ref) : 1.f;

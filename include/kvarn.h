@@ -434,8 +434,9 @@ int kvarn_prefix_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, c
  * enter the products as two bf16 halves, within 2^-16, as in
  * kvarn_decode_attn_bf16. In kvarn_prefix_attn queries, keys, weights and values
  * of blocks enter them as two fp16 halves, within 2^-22 (the prefix's keys and
- * values below 2^-18 of the largest of their 64 tokens: within 2^-39 of that one),
- * and weights and fp32 queries of the raw rows as two bf16 halves.
+ * values below 2^-18 of the largest of their 64 tokens: within 2^-39 of that one; its
+ * weights below 2^-10 of the row's largest: within 2^-32 of that one), and weights and
+ * fp32 queries of the raw rows as two bf16 halves.
  */
 int kvarn_prefix_attn_bf16(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* kv_pool,
                            int64_t n_pool_blocks, const int32_t* prefix_table, int32_t prefix_blocks,
@@ -474,12 +475,17 @@ size_t kvarn_tree_workspace_bytes(const kvarn_config* cfg, int32_t batch, int32_
  * KVARN_FP32. A drafted value that is not finite makes the rows that see it NaN,
  * and no other row. fp32 queries (of bf16 pages and raw rows) and softmax weights
  * enter the products as two 16-bit halves, within 2^-16; over the packed cache
- * rotated queries and weights within 2^-22 and, with more than a few query rows, keys
- * and values within 2^-18 (4 bits) to 2^-20 (2 bits) of the largest level of their token's
- * 32 channels. workspace: at least kvarn_tree_workspace_bytes(cfg, batch,
- * drafts, max_blocks_per_seq) bytes, 16-byte aligned; calls that may overlap need one each. Device
- * faults: KVARN_DEVERR_BLOCK_ID, KVARN_DEVERR_POSITION (a length outside its
- * range: NaN rows), KVARN_DEVERR_WAIT_TIMEOUT.
+ * rotated queries and weights within 2^-22. With more than a few query rows weights
+ * there are, below 2^-14 of the row's largest, within 2^-36 of that one, and keys and
+ * values within 2^-18 (4 bits) to 2^-20 (2 bits) of the largest level of their token's
+ * 32 channels or, where that is more, 2^-29 of the largest level of their 64 tokens.
+ * Sums over tokens are the tensor core's, which cuts the fp32 sum at each step and drops
+ * what is below 2^-25 of it: beside a large weight whose value is not small, weights
+ * below 2^-25 of it may be missing from out.
+ * workspace: at least kvarn_tree_workspace_bytes(cfg, batch, drafts, max_blocks_per_seq)
+ * bytes, 16-byte aligned; calls that may overlap need one each. Device faults:
+ * KVARN_DEVERR_BLOCK_ID, KVARN_DEVERR_POSITION (a length outside its range: NaN rows),
+ * KVARN_DEVERR_WAIT_TIMEOUT.
  */
 #define KVARN_MAX_DRAFTS 128
 int kvarn_tree_attn(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* pool,
