@@ -68,29 +68,34 @@ int few_splits(const kvarn_config& c, int64_t batch, int drafts, int max_blocks)
     return (int)(n < 1 ? 1 : n < kFewSplits ? n : kFewSplits);
 }
 
-// The workspace: header, unit map, rotated queries and their scales, partials.
+// The workspace: header, unit map, rotated queries and their scales, partials. Its size grows with the batch, the
+// drafts and the table, so that one made for the largest call serves them all: what either cache and query type
+// and any length needs is bounded by terms that do not shrink.
+//   ranges: at most 2 an SM of up to 128 rows, or with `extra` 160 of partials; one of 256 rows (half as
+//   many ranges of 512) takes less than that
+//   few_splits: units splits <= warps with half a wave of units, <= 2.5 warps + units / 2 with more
+//   (prefill_splits), and a unit is up to 8 rows; one split is always taken
 struct TreeSpace {
     size_t turned, scales, partials, bytes;
 };
 TreeSpace tree_space(const kvarn_config& c, int32_t batch, int32_t drafts, int32_t max_blocks) {
     TreeSpace t = {0, 0, 0, kWsHeader};
     if (batch == 0) return t;
-    int ranges = 0, pad = 0;   // the most that either cache and query type and any length needs
-    for (int k = 0; k < 4; ++k) {
-        const TreePlan p = tree_plan(c, drafts, k == 0, k == 1 ? KVARN_FP32 : KVARN_BF16, k == 3 ? INT64_MAX : 0);
-        ranges = p.ranges > ranges ? p.ranges : ranges;
-        pad = p.rows_pad;
-    }
-    const size_t units = (size_t)batch * c.n_kv_heads;
+    const int64_t sms = current_device_sms(), G = c.n_q_heads / c.n_kv_heads;
+    const int64_t units = (int64_t)batch * c.n_kv_heads, pad = (drafts * G + 31) / 32 * 32;
     t.turned = align256(kWsHeader + units * 2 * sizeof(int32_t));
     t.scales = t.turned + units * pad * 2 * kD * sizeof(uint16_t);
     t.partials = align256(t.scales + units * pad * sizeof(float));
-    t.bytes = ranges > 0 ? t.partials + (units + ranges) * 33 * pad * sizeof(float4) : 0;
-    if (few_rows(c, drafts)) {
-        const size_t few = t.partials + (size_t)batch * drafts * c.n_q_heads * few_splits(c, batch, drafts, max_blocks) *
-                                            kPartialStride * sizeof(float);
-        t.bytes = t.bytes > 0 && few > t.bytes ? few : t.bytes;
-    }
+    constexpr int64_t kExtraPad = kPRows + 32;
+    const int64_t ranges = units * pad + 2 * sms * (pad < kExtraPad ? pad : kExtraPad);   // partial rows
+    const int64_t warps = prefill_grid_warps(c.block_size, c.bits, current_device()), per = 8 / G;
+    const int64_t d = drafts < kFewWarps * per ? drafts : kFewWarps * per, rows = batch * d * c.n_q_heads;
+    const int64_t cap = max_blocks / 2 < 1 ? 1 : max_blocks / 2 < kFewSplits ? max_blocks / 2 : kFewSplits;
+    const int64_t most = 20 * warps + 4 * units * ((d + per - 1) / per);
+    int64_t few = cap * rows < most ? cap * rows : most;
+    few = few > rows ? few : rows;
+    const size_t a = ranges * 33 * sizeof(float4), b = few * kPartialStride * sizeof(float);
+    t.bytes = sms > 0 && warps > 0 ? t.partials + (a > b ? a : b) : 0;
     return t;
 }
 

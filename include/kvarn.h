@@ -445,8 +445,8 @@ int kvarn_prefix_attn_bf16(const kvarn_config* cfg, const void* q, int32_t q_dty
                            size_t workspace_bytes, void* stream);
 
 /* Workspace bytes for kvarn_tree_attn / kvarn_tree_attn_bf16 with this batch,
- * number of drafts and table width on the CURRENT device. 0 on a bad config or
- * size. */
+ * number of drafts and table width on the CURRENT device. It grows with each of the
+ * three: a workspace for the largest call serves them all. 0 on a bad config or size. */
 size_t kvarn_tree_workspace_bytes(const kvarn_config* cfg, int32_t batch, int32_t drafts,
                                   int32_t max_blocks_per_seq);
 
