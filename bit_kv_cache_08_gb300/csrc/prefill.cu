@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(32) prefill_attn_kernel(AttnArgs a) {
     int stage = 0;
     uint32_t phase = 0;
     for (int j = 0; j < nblk; ++j) {
-        if (!mbar_wait_bounded(&bars[stage], phase, kWaitLimit)) {
+        if (!mbar_wait_bounded(&bars[stage], phase, ALL && j == 0 ? a.first_wait_limit : kWaitLimit)) {
             if (lane == 0) raise_error(err, KVARN_DEVERR_WAIT_TIMEOUT);
             uint32_t ph = phase;
             for (int k = 0, st2 = stage; k < S && j + k < nblk; ++k) {
@@ -666,6 +666,7 @@ cudaError_t launch_prefill_all(const kvarn_config& cfg, const void* q, int q_dty
     a.single = splits;
     a.sm_scale = cfg.sm_scale;
     a.flags = cfg.flags;
+    a.first_wait_limit = (cfg.flags & KVARN_FLAG_TEST_WAIT_TIMEOUT) ? 0u : kWaitLimit;
     for (int i = 0; i < 4; ++i) a.sb[i] = cfg.sign_bits[i];
     const int P = kPrefillVecs / a.G;
     const int64_t warps = (int64_t)batch * a.n_kv * ((chunk + P - 1) / P) * splits;

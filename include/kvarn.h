@@ -128,8 +128,9 @@ typedef struct kvarn_config {
 #define KVARN_FLAG_NO_CHANNEL_PASS 0x4u
 /*
  * Test switch (no counterpart in the paper): with it, every warp of
- * kvarn_decode_attn's split kernel gives up its first shared-memory copy
- * wait at once (and the tensor-core kernels of kvarn_prefix_attn, kvarn_tree_attn and
+ * kvarn_decode_attn's split kernel, which kvarn_decode_attn_weights shares, and of the one that
+ * kvarn_tree_attn has for few query rows gives up its first shared-memory copy wait
+ * at once (and the tensor-core kernels of kvarn_prefix_attn, kvarn_tree_attn and
  * their bf16 forms act as if their first had), so the wait-timeout path runs without
  * anything hanging:
  * KVARN_DEVERR_WAIT_TIMEOUT is raised, the copies already in flight are
