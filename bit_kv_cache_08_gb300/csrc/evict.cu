@@ -42,13 +42,47 @@ constexpr int kSelKeys = 9728;           // keys held in shared memory (48 KB wi
 __device__ __forceinline__ uint32_t weight_key(float w) { return w > 0.f ? __float_as_uint(w) : 0u; }
 
 __device__ __forceinline__ float tidy(float w) { return w > 0.f ? w : 0.f; }
+__device__ __forceinline__ float4 tidy(float4 w) { return make_float4(tidy(w.x), tidy(w.y), tidy(w.z), tidy(w.w)); }
 
-// (hi, lo) += w, exactly but for the last bits of lo: hi + lo keeps about 48
-// bits, so that its rounding to 32 is that of the sum in 64 bits.
-__device__ __forceinline__ void add_pair(float& hi, float& lo, float w) {
-    const float s = hi + w, b = s - hi;
-    lo += (hi - (s - b)) + (w - b);
-    hi = s;
+// A sum in three floats, of falling size: hi + mid is exact but for what mid rounds off, which lo takes
+// up. Together they keep about 72 bits, more than the 53 of a sum in 64 bits, in fp32 additions alone (64-bit
+// ones run at 1/64 of their rate). Two floats keep 48: 1 + 2^-24 + 2^-50 lost its last term, and with it
+// the rounding of the whole to 32 bits; they take as long (64 x 16384 2-bit tokens 92.0 us a call, 91.9 so; 5 x
+// 1500 8.3, 9.3).
+struct Sum3 {
+    float hi, mid, lo;
+};
+// (s, e) = a + b exactly, s rounded to nearest.
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+    s = __fadd_rn(a, b);
+    const float y = __fsub_rn(s, a);
+    e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, y)), __fsub_rn(b, y));
+}
+__device__ __forceinline__ Sum3 sum_of(float4 w) {
+    float a, b, c, d, e, f;
+    two_sum(w.x, w.y, a, c);
+    two_sum(w.z, w.w, b, d);
+    Sum3 s;
+    two_sum(a, b, s.hi, e);
+    two_sum(c, d, s.mid, f);
+    two_sum(s.mid, e, s.mid, s.lo);
+    s.lo = __fadd_rn(s.lo, f);
+    return s;
+}
+// (The same whichever of the two is added to the other: a two_sum's error is exact. Where weights are
+// infinite hi is, and mid and lo count no more.)
+__device__ __forceinline__ Sum3 sum_of(const Sum3& a, const Sum3& b) {
+    Sum3 s;
+    float e, f, g;
+    two_sum(a.hi, b.hi, s.hi, e);
+    two_sum(a.mid, b.mid, s.mid, f);
+    two_sum(s.mid, e, s.mid, g);
+    s.lo = __fadd_rn(__fadd_rn(a.lo, b.lo), __fadd_rn(f, g));
+    return s;
+}
+// Rounded to 64 bits, then to 32 (past the largest float: infinity).
+__device__ __forceinline__ float rounded(const Sum3& s) {
+    return isinf(s.hi) ? s.hi : __double2float_rn((double)s.hi + ((double)s.mid + (double)s.lo));
 }
 
 // The key of place i0 + lane of a row of weights with n places (0 behind them). Of a
@@ -57,7 +91,7 @@ template <int UNIT>
 __device__ __forceinline__ uint32_t place_key(const float* w, uint32_t i0, uint32_t n, int lane) {
     if constexpr (UNIT == 1) return i0 + lane < n ? weight_key(w[i0 + lane]) : 0u;
     constexpr int kParts = UNIT >= 32 ? UNIT / 32 : 1, kBatch = 4;
-    uint32_t key = 0;
+    Sum3 mine = {0.f, 0.f, 0.f};            // of this lane's place
 #pragma unroll
     for (int s0 = 0; s0 < 8; s0 += kBatch) {
         float4 v[kBatch][kParts];
@@ -66,34 +100,23 @@ __device__ __forceinline__ uint32_t place_key(const float* w, uint32_t i0, uint3
 #pragma unroll
             for (int p = 0; p < kParts; ++p) {
                 const uint32_t i = i0 + 4 * (s0 + k) + (lane >> 3);
-                v[k][p] = i < n ? __ldg(reinterpret_cast<const float4*>(w + (int64_t)i * UNIT + 4 * (lane & 7) + 32 * p))
+                v[k][p] = i < n ? tidy(__ldg(reinterpret_cast<const float4*>(w + (int64_t)i * UNIT + 4 * (lane & 7) + 32 * p)))
                                 : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            float hi = 0.f, lo = 0.f;
+            Sum3 sum = sum_of(v[k][0]);
 #pragma unroll
-            for (int p = 0; p < kParts; ++p) {
-                add_pair(hi, lo, tidy(v[k][p].x));
-                add_pair(hi, lo, tidy(v[k][p].y));
-                add_pair(hi, lo, tidy(v[k][p].z));
-                add_pair(hi, lo, tidy(v[k][p].w));
-            }
+            for (int p = 1; p < kParts; ++p) sum = sum_of(sum, sum_of(v[k][p]));
 #pragma unroll
-            for (int m = 1; m < 8; m <<= 1) {   // (both lanes of a pair add the same two in the same order)
-                const float oh = __shfl_xor_sync(kFull, hi, m), ol = __shfl_xor_sync(kFull, lo, m);
-                const float mh = hi;
-                const bool upper = lane & m;
-                hi = upper ? oh : mh;
-                lo += ol;
-                add_pair(hi, lo, upper ? mh : oh);
-            }
-            const uint32_t mine = weight_key(isinf(hi) ? hi : hi + lo);
-            const uint32_t its = __shfl_sync(kFull, mine, 8 * (lane & 3));
-            if (lane >> 2 == s0 + k) key = its;
+            for (int m = 1; m < 8; m <<= 1)
+                sum = sum_of(sum, Sum3{__shfl_xor_sync(kFull, sum.hi, m), __shfl_xor_sync(kFull, sum.mid, m), __shfl_xor_sync(kFull, sum.lo, m)});
+            const int from = 8 * (lane & 3);
+            const Sum3 its = {__shfl_sync(kFull, sum.hi, from), __shfl_sync(kFull, sum.mid, from), __shfl_sync(kFull, sum.lo, from)};
+            if (lane >> 2 == s0 + k) mine = its;
         }
     }
-    return key;
+    return weight_key(rounded(mine));
 }
 
 template <int UNIT>

@@ -575,7 +575,7 @@ int kvarn_evict_bf16(const kvarn_config* cfg, void* kv_pool, int64_t n_pool_bloc
 /*
  * kvarn_evict -- the same over the packed cache, by whole blocks, whose codes
  * share their factors: budget and recent are multiples of B, a block's weight is
- * the sum of its tokens' (rounded to fp32), and kept [batch][n_kv][budget / B] names
+ * the sum of its tokens' (in 64 bits, rounded to fp32), and kept [batch][n_kv][budget / B] names
  * blocks. The L % B tokens of the incomplete block stay where they are in staging, behind
  * the kept blocks: new_lens[b] = min(L - L % B, budget) + L % B, their weights
  * move along, and new_max_blocks * B > budget.
