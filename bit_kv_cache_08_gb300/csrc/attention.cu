@@ -787,12 +787,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 1) prefix_join_packed_kernel(
 // without spills, 15 warps per SM (shared memory) instead of 12 (218 -> 207
 // us). The 2- and 4-bit instantiations were fastest plain (bounds of 1, 10,
 // 11 at 2 bits, B = 64: 142, 129.5, 129.4 against 128.7 us).
-template <int B, int BITS>
-constexpr int attn_min_ctas() { return BITS != 3 ? 0 : (B == 64 ? 1 : 16); }
+// The kernel that leaves its scores runs on the plain one's grid, whose partition (and with it every bit of
+// the output) it shares, so that it must not hold fewer CTAs an SM: at 2 bits, B = 32 the
+// plain kernel takes 128 registers (16 CTAs) and this one by itself 158 (12, a second wave of a
+// quarter of the warps: 64 x 8192 tokens 187 us a call, 152 with 16, 132 without weights). The others lose no CTA.
+template <int B, int BITS, bool SCORES>
+constexpr int attn_min_ctas() { return BITS == 3 ? (B == 64 ? 1 : 16) : SCORES && BITS == 2 && B == 32 ? 16 : 0; }
 
 template <int B, int BITS, bool LATE, bool SCORES>
 constexpr auto attn_kernel_fn() {
-    constexpr int S = stages_for<B, BITS>(), M = attn_min_ctas<B, BITS>();
+    constexpr int S = stages_for<B, BITS>(), M = attn_min_ctas<B, BITS, SCORES>();
     if constexpr (M > 0) return decode_attn_2bit_kernel_minb<B, BITS, S, M, LATE, SCORES>;
     else return decode_attn_2bit_kernel<B, BITS, S, LATE, SCORES>;
 }
