@@ -948,7 +948,7 @@ def evict(cfg: Config, pool: torch.Tensor, block_table: torch.Tensor, seq_lens: 
     """evict_bf16 over the packed cache, by whole blocks: budget and recent are
     multiples of the block size, kept is [batch][n_kv][budget / block] and names blocks,
     a block's weight is the sum of its tokens'. The incomplete block stays in
-    staging, behind the kept blocks."""
+    staging, behind the kept blocks. Later appends: as there, with rope_pos."""
     if (not isinstance(pool, torch.Tensor) or pool.dtype is not _u8 or pool.dim() != 2 or not pool.is_contiguous()
             or pool.shape[1] != _block_bytes_of(cfg.n_kv_heads, cfg.block_size, cfg.bits)):
         _need_cuda(pool, "pool", _u8)
@@ -966,7 +966,8 @@ def evict_bf16(cfg: Config, kv_pool: torch.Tensor, block_table: torch.Tensor, se
     in order, to the pages new_table [batch][new_blocks] (none that the call
     reads). new_lens [batch], kept int32 [batch][n_kv][budget] (the token now at each place,
     -1 behind) and new_weights [batch][n_kv][new columns] are filled in; the old pages
-    are only read."""
+    are only read. Places are then no positions any more: append with pos=new_lens and
+    rope_pos= the position of each sequence's first new token."""
     _need_pages(cfg, kv_pool)
     _evict(lib().kvarn_evict_bf16, "kvarn_evict_bf16", cfg, kv_pool, block_table, seq_lens, weights, new_table, new_lens,
            new_weights, kept, workspace, budget, recent, 1)

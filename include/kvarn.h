@@ -562,6 +562,11 @@ int kvarn_decode_attn_weights_bf16(const kvarn_config* cfg, const void* q, int32
  *                         [new_weights_stride], the first new_max_blocks * B columns
  *                         written; must not overlap weights)
  * Rows of the new pages behind the new length are left as they were.
+ * After an eviction a token's place in the cache is no longer its position in the
+ * text: the caller keeps the positions, and appends with pos = new_lens and
+ * rope_pos = the position of the first new token (kvarn_append_rope_bf16, kvarn_append_rope;
+ * without rope_pos new keys and queries would be turned as if they stood before kept
+ * ones). Drafted keys and queries are turned by the caller likewise.
  * budget >= 1, new_max_blocks * B >= budget. workspace: >= 256 bytes, for the error
  * word. Device faults: KVARN_DEVERR_BLOCK_ID (the row or block is not moved),
  * KVARN_DEVERR_POSITION (a length beyond the block table: new length 0, nothing moved).
@@ -578,7 +583,7 @@ int kvarn_evict_bf16(const kvarn_config* cfg, void* kv_pool, int64_t n_pool_bloc
  * the sum of its tokens' (in 64 bits, rounded to fp32), and kept [batch][n_kv][budget / B] names
  * blocks. The L % B tokens of the incomplete block stay where they are in staging, behind
  * the kept blocks: new_lens[b] = min(L - L % B, budget) + L % B, their weights
- * move along, and new_max_blocks * B > budget.
+ * move along, and new_max_blocks * B > budget. rope_pos as there.
  */
 int kvarn_evict(const kvarn_config* cfg, void* pool, int64_t n_pool_blocks, const int32_t* block_table,
                 int32_t max_blocks_per_seq, const int32_t* seq_lens, const float* weights, int64_t weights_stride,
