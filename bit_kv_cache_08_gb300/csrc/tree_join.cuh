@@ -81,9 +81,10 @@ struct JoinRows {
 };
 
 // 16 raw tokens at k and v (rows ks / vs elements apart), of which the first `there` exist;
-// bit i of seen[x]: token i is shown to row x. wrong[x]: the row has seen a value that is
-// not finite (such a value's row of V is taken as zeros).
-template <bool Q32>
+// bit i of seen[x]: token i is shown to row x. APART: not every row sees every token, and a
+// value that is not finite must not reach the rows that do not see it (0 times it is NaN):
+// its row of V is taken as zeros, and wrong[x] says that the row has seen one.
+template <bool Q32, bool APART>
 __device__ __forceinline__ void join_step(JoinRows<Q32>& s, const uint16_t* k, const uint16_t* v, int64_t ks, int64_t vs, int there,
                                           const uint32_t (&seen)[2], float scale, int lane, bool (&wrong)[2]) {
     const int gq = lane >> 2, tq = lane & 3;
@@ -112,31 +113,33 @@ __device__ __forceinline__ void join_step(JoinRows<Q32>& s, const uint16_t* k, c
                 mma_bf16(sc[t], s.q[p][2 * j + 1][0], s.q[p][2 * j + 1][1], s.q[p][2 * j + 1][2], s.q[p][2 * j + 1][3], kk[t][j].z, kk[t][j].w);
             }
     }
-    // values that are not finite: 0 times one is NaN, 0 times any other 0
-    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
-    uint32_t bad = 0;
+    if constexpr (APART) {
+        // values that are not finite: 0 times one is NaN, 0 times any other 0
+        const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+        uint32_t bad = 0;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        __nv_bfloat162 n = zero;
+        for (int t = 0; t < 4; ++t) {
+            __nv_bfloat162 n = zero;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t w[4] = {vv[t][j].x, vv[t][j].y, vv[t][j].z, vv[t][j].w};
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t w[4] = {vv[t][j].x, vv[t][j].y, vv[t][j].z, vv[t][j].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) n = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), zero, n);
+                for (int e = 0; e < 4; ++e) n = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), zero, n);
+            }
+            const uint32_t bits = *reinterpret_cast<const uint32_t*>(&n);
+            // lanes of the same tq hold the token's other channels
+            const uint32_t lanes = __ballot_sync(kFull, (bits & 0x7fff7fffu) != 0);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (lanes & 0x11111111u << x) bad |= 1u << (2 * x + (t & 1) + 8 * (t >> 1));
         }
-        const uint32_t bits = *reinterpret_cast<const uint32_t*>(&n);
-        // lanes of the same tq hold the token's other channels
-        const uint32_t lanes = __ballot_sync(kFull, (bits & 0x7fff7fffu) != 0);
+        if (bad) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-            if (lanes & 0x11111111u << x) bad |= 1u << (2 * x + (t & 1) + 8 * (t >> 1));
-    }
-    if (bad) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (bad >> (2 * tq + (t & 1) + 8 * (t >> 1)) & 1) vv[t][0] = vv[t][1] = make_uint4(0, 0, 0, 0);
-        wrong[0] = wrong[0] || (bad & seen[0]);
-        wrong[1] = wrong[1] || (bad & seen[1]);
+            for (int t = 0; t < 4; ++t)
+                if (bad >> (2 * tq + (t & 1) + 8 * (t >> 1)) & 1) vv[t][0] = vv[t][1] = make_uint4(0, 0, 0, 0);
+            wrong[0] = wrong[0] || (bad & seen[0]);
+            wrong[1] = wrong[1] || (bad & seen[1]);
+        }
     }
     float p[2][4], f[2];
 #pragma unroll
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(tree_join_threads<WARPS>()) tree_join_kernel(T
             }
             if ((WARPS > 1 && t / 16 % WARPS != part) || !__any_sync(kFull, seen[0] | seen[1])) continue;
             const int64_t at = (int64_t)b * a.drafts + t;
-            join_step<Q32>(s, a.k + at * a.k_stride + h * kD, a.v + at * a.v_stride + h * kD, a.k_stride, a.v_stride, T - t, seen, scale,
+            join_step<Q32, true>(s, a.k + at * a.k_stride + h * kD, a.v + at * a.v_stride + h * kD, a.k_stride, a.v_stride, T - t, seen, scale,
                            lane, wrong);
         }
     };
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(tree_join_threads<WARPS>()) tree_join_kernel(T
             const int there = tail - t;
             const uint32_t all = there >= 16 ? 0xffffu : (1u << there) - 1;
             const uint32_t seen[2] = {all, all};
-            join_step<Q32>(s, st + t * kD, st + (a.B + t) * kD, kD, kD, there, seen, scale, lane, wrong);
+            join_step<Q32, false>(s, st + t * kD, st + (a.B + t) * kD, kD, kD, there, seen, scale, lane, wrong);
         }
         drafts();
     }
