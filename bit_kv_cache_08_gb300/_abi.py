@@ -913,6 +913,8 @@ def _refuse_evict(cfg, pool, block_table, seq_lens, weights, new_table, new_lens
 def _evict(fn, name, cfg, pool, block_table, seq_lens, weights, new_table, new_lens, new_weights, kept, workspace, budget,
            recent, unit):
     # (as in _append_rope: each attribute read once)
+    if not -0x80000000 <= budget <= 0x7fffffff or not -0x80000000 <= recent <= 0x7fffffff:   # (ctypes would cut them)
+        raise ValueError("budget and recent must fit 32 bits")
     dev, i32, f32 = _current_device(), _i32t, _f32
     places = budget // unit
     try:
