@@ -100,7 +100,7 @@ __device__ __forceinline__ uint32_t place_key(const float* w, uint32_t i0, uint3
 #pragma unroll
             for (int p = 0; p < kParts; ++p) {
                 const uint32_t i = i0 + 4 * (s0 + k) + (lane >> 3);
-                v[k][p] = i < n ? tidy(__ldg(reinterpret_cast<const float4*>(w + (int64_t)i * UNIT + 4 * (lane & 7) + 32 * p)))
+                v[k][p] = i < n ? tidy(__ldcg(reinterpret_cast<const float4*>(w + (int64_t)i * UNIT + 4 * (lane & 7) + 32 * p)))
                                 : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
