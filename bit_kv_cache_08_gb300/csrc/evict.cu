@@ -36,7 +36,8 @@ constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kDigit = 2048;             // values of an 11-bit digit
 constexpr int kBins = kDigit / kSelThreads;
-constexpr int kSelKeys = 9728;           // keys held in shared memory (48 KB with the rest: 4 CTAs an SM)
+constexpr int kSelKeys = 9728;           // keys held in shared memory (46 KB with the rest, the most without opting in; registers allow
+                                         // 3 CTAs an SM of tokens, 2 of blocks)
 
 // A weight as a key: its bits order as it does; what is not above 0 counts as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) { return w > 0.f ? __float_as_uint(w) : 0u; }

@@ -1,7 +1,10 @@
 // packed_build.cuh -- 64-token tiles of the packed cache as operands of the
-// tensor core, for the kernels that multiply them with many query rows.
+// tensor core, for the kernels that multiply them with many query rows: the tiles' sizes and
+// the reading of codes, which the shared prefix (prefix_packed.cu) and draft trees
+// (tree_packed.cu) have in common, and the prefix's builders. (Draft trees build with fp16 arithmetic
+// from levels prepared ahead, 4 warps for keys and 4 for values.)
 //
-// K' (64 tokens x 128 channels, channels along the contraction) and V' (128 channels x 64
+// The prefix's: K' (64 tokens x 128 channels, channels along the contraction) and V' (128 channels x 64
 // tokens, tokens along it) hold (code s + z) R C under a power of two of the tile's, each value
 // as two fp16 halves. 8 warps build them without meeting at a barrier: one group's
 // share of a record of the packed format (K: 4 tokens x 8 channels, V: 8 tokens x 4

@@ -1,8 +1,9 @@
 // tree.cu -- attention for a tree of drafted tokens: T rows a sequence, each
 // over all cached tokens and over the drafted ones that its mask shows.
 //
-// Calls as graph nodes (8 kv heads, 4 query heads each): 1 x 8 drafts over 1000 bf16 tokens 13.6 us, 64 x 16 over
-// up to 8192 260, 32 x 33 191; 3 x 12 over 1500 2-bit tokens 28, 48 x 16 over up to 8192 4-bit tokens 383.
+// Calls as graph nodes (8 kv heads, 4 query heads each): 1 x 8 drafts over 1000 bf16 tokens 13.6 to 14.4 us, 64 x 16
+// over up to 8192 260 to 267, 32 x 33 191 to 200; 3 x 12 over 1500 2-bit tokens 27, 48 x 16 over up to 8192 4-bit
+// tokens 400, 64 x 8 2-bit 490 (bf16 253).
 #include "host_checks.h"
 #include "tree_join.cuh"
 

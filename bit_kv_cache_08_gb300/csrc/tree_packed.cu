@@ -14,11 +14,14 @@
 // tiles and prepares the levels of their keys, one for those of the values, 8 that build
 // operands, as in packed_build.cuh without meeting at a barrier.
 //
-// Measured (48 sequences x 16 drafts, up to 8192 4-bit tokens, 8 kv heads): 383 us a call, of which this
-// kernel is 365, 2380 cycles a tile of 64 tokens. The tensor core is busy 1480 of them (six products of halves),
-// a warp that builds 1500, shared memory about 2000 (operands written once, read three times); each waits for
-// the others in turn. Not faster: four S in tensor memory and products of P three steps behind, 8 + 8 builder
-// warps, two streams of softmax, rows of up to 64 held twice so that P V is two products (401 us).
+// Measured (48 sequences x 16 drafts, up to 8192 4-bit tokens, 8 kv heads): 400 us a call, this kernel alone
+// and cold 365, about 2900 cycles a tile of 64 tokens. The tensor core is busy 1480 of them (six products of halves),
+// a warp that builds 1500, shared memory about as long (64 KB of operands written, 96 KB read by the products; the
+// LSU's share was 29 % of a smaller call): no unit is saturated, each waits for the others in turn. Rows are the
+// products' M, so that 32 cost what 128 do, and the width of a code does not matter: 2-bit tokens take as
+// long as 4-bit ones, and longer than bf16 pages (64 x 8 drafts 490 us, 253). Not faster: four S in tensor
+// memory and products of P three steps behind, 8 + 8 builder warps, two streams of softmax, rows of up to
+// 64 held twice so that P V is two products.
 #include "packed_build.cuh"
 #include "host_checks.h"
 #include "quantize.cuh"

@@ -7,9 +7,10 @@
 // split kernel (attention.cu, attention_bf16.cu) leaves its scores s (log2
 // domain, fp32) in the workspace, its merge m and 1 / l, and weigh_kernel reads
 // them once: 4 G bytes a token and kv head written and read, against the keys
-// read and multiplied a second time. That traffic is what the weights cost: 32 sequences x
-// 8192 bf16 tokens, 8 kv heads, 4 query heads each, 154 us without them and 167 with (84 MB, 12 us
-// at the rate of a copy), 64 x 8192 2-bit tokens 111 and 127, 2 x 1000 8.3 and 9.7.
+// read and multiplied a second time. That traffic is what the weights cost. 8 kv heads, 4 query
+// heads each, lengths 0.75 of these on average: 32 sequences x 8192 bf16 tokens 154 us without them and 168
+// with (63 MB, 9 us at the rate of a copy), 64 x 8192 2-bit tokens 114 and 131 (126 MB, partly in L2; blocks of
+// 32 132 and 152), 2 x 1000 8.3 and 9.7.
 #include "attn_common.cuh"
 #include "host_checks.h"
 
