@@ -524,7 +524,8 @@ size_t kvarn_weights_workspace_bytes(const kvarn_config* cfg, int32_t batch, int
  * buffer (weights kept from step to step) or two that do not overlap.
  * weights_in NULL or decay 0: this step's weights alone. decay in 0 .. 1.
  * workspace: at least kvarn_weights_workspace_bytes bytes, 16-byte aligned.
- * Device faults as kvarn_decode_attn; a sequence with one has its weights unspecified.
+ * Device faults as kvarn_decode_attn; a sequence with one has its weights unspecified, and so
+ * has a kv head with a score that is not finite (its out is NaN, or counts finite scores alone).
  */
 int kvarn_decode_attn_weights(const kvarn_config* cfg, const void* q, int32_t q_dtype, const void* pool,
                               int64_t n_pool_blocks, const void* staging, const int32_t* block_table,
